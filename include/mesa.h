@@ -84,7 +84,17 @@ typedef enum {
     MESA_KERNEL_BWD_KV = 6,          /* backward: key and value gradients                */
     MESA_KERNEL_BWD_GATE = 7,        /* backward: gate and regulariser gradients         */
     MESA_KERNEL_HAWK = 8,            /* Hawk layer recurrence (all its kernels)          */
-    MESA_KERNEL_COUNT = 9
+                                     /* 9..15 are not used                               */
+    MESA_KERNEL_DELTA_PREP = 16,     /* delta rule: the chunks' state-free matrices      */
+    MESA_KERNEL_DELTA_SCAN = 17,     /* delta rule: the pass over the chunks             */
+    MESA_KERNEL_DELTA_STEP = 18,     /* delta rule: one token                            */
+    MESA_KERNEL_DELTA_BWD_SCAN = 19, /* delta rule: the backward's pass over the chunks  */
+    MESA_KERNEL_DELTA_GRADS = 20,    /* delta rule: gradients per chunk, sums over heads */
+    MESA_KERNEL_GATE_NORM = 21,      /* norm and gate of a layer's outputs               */
+    MESA_KERNEL_GATE_NORM_BWD = 22,
+    MESA_KERNEL_RESIDUAL_NORM = 23,  /* residual scale, addition and norm                */
+    MESA_KERNEL_RESIDUAL_NORM_BWD = 24,
+    MESA_KERNEL_COUNT = 25
 } mesa_kernel_id;
 
 /* Library ABI version (MESA_ABI_VERSION of the build). */
@@ -319,6 +329,100 @@ size_t mesa_hawk_workspace_bytes(int B, int T, int D);
 mesa_status mesa_hawk_scan(const void *x, const void *ga, const void *gx, int in_dtype, const float *lam,
                            float c, const float *h0, int B, int T, int D, float *y, float *h_final,
                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated delta rule over a whole sequence: the linear-attention layer that
+ * takes, per token, one decayed gradient step on the objective the Mesa layer
+ * solves to the end.  Per batch row and head, with the state S (a map from
+ * keys to values, like the Mesa layer's G):
+ *   S_t = gamma_t S_{t-1} (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,
+ *   out_t = S_t q_t,     S_0 = state0 (zeros when NULL)
+ *
+ *   q, k       [B, Hk, T, dk]   dtype (mesa_dtype)
+ *   v          [B, H, T, dv]    dtype; H a multiple of Hk: value head h uses
+ *                               key and query head h / (H / Hk)
+ *   gamma,beta [B, H, T]        float32.  0 < gamma <= 1; gamma = 0 is taken
+ *                               too and forgets the state (a sequence start in
+ *                               a packed row).  beta is the write strength:
+ *                               0 writes nothing, so a padded token is gamma =
+ *                               1, beta = 0 and leaves the state as it is.
+ *                               The rule is a contraction for beta |k|^2 <= 2;
+ *                               beyond that states may grow without bound.
+ *   state0     [B, H, dv, dk]   float32, or NULL
+ *   out        [B, H, T, dv]    dtype, written (bfloat16 rounds to nearest even)
+ *   final_state [B, H, dv, dk]  float32 S_T, or NULL; may be state0 itself
+ *   workspace                   at least mesa_delta_workspace_bytes(...)
+ * dk in {16, 32, 64, 128}, dv in {16, 32, 64, 128, 256}, T >= 0.  Sums, states
+ * and decays are float32 (prefix sums of ln gamma float64); products run as
+ * fp16 MFMAs on two-part splits (see mesa_dtype).
+ */
+size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype);
+mesa_status mesa_delta_forward(const void *q, const void *k, const void *v, int dtype, const float *gamma,
+                               const float *beta, const float *state0, int B, int Hk, int H, int T, int dk,
+                               int dv, void *out, float *final_state, void *workspace,
+                               size_t workspace_bytes, void *stream);
+
+/*
+ * One token of the gated delta rule for N sequences, states updated in place:
+ *   q, k [N, Hk, dk], v [N, H, dv] dtype; gamma, beta [N, H] float32;
+ *   state [N, H, dv, dk] float32 in/out; out [N, H, dv] dtype.
+ * Sizes and heads as mesa_delta_forward; its final_state is this state.
+ */
+mesa_status mesa_delta_step(const void *q, const void *k, const void *v, int dtype, const float *gamma,
+                            const float *beta, float *state, int N, int Hk, int H, int dk, int dv, void *out,
+                            void *stream);
+
+/*
+ * Norm and gate of a layer's outputs, per token and head:
+ *   y = x / sqrt(mean(x^2) + eps) * w * silu(gate),   silu(g) = g / (1 + e^-g)
+ *   x     [B, H, T, d]   x_dtype: a layer's output (mesa_forward, mesa_delta_forward)
+ *   gate  [B, T, H, d]   dtype, or NULL for no gate: rows of an input projection
+ *   w     [H, d]         float32
+ *   y     [B, T, H, d]   dtype: rows of the output projection's input
+ * d in {16, 32, 64, 128, 256}; eps > 0.  A row of zeros gives zeros.  Squares
+ * are summed in float32: |x| up to about 1e18.
+ *
+ * Backward, for grad_y = dL/dy [B, T, H, d] dtype, from the forward's inputs:
+ *   grad_x [B, H, T, d] x_dtype, grad_gate [B, T, H, d] dtype (NULL exactly
+ *   when gate is), grad_w [H, d] float32; workspace at least
+ *   mesa_gate_norm_backward_workspace_bytes(...).  Sums are taken in a fixed
+ *   order: results do not change from run to run.
+ */
+mesa_status mesa_gate_norm(const void *x, int x_dtype, const void *gate, int dtype, const float *w, float eps,
+                           int B, int H, int T, int d, void *y, void *stream);
+size_t mesa_gate_norm_backward_workspace_bytes(int B, int H, int T, int d);
+mesa_status mesa_gate_norm_backward(const void *x, int x_dtype, const void *gate, int dtype, const float *w,
+                                    float eps, const void *grad_y, int B, int H, int T, int d, void *grad_x,
+                                    void *grad_gate, float *grad_w, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/*
+ * Residual scale, addition and the next block's norm, per row:
+ *   h_out = h + scale * y,   n = h_out / sqrt(mean(h_out^2) + eps) * w
+ *   h      [R, D]  h_dtype: the residual
+ *   y      [R, D]  dtype: the block's output, or NULL (n = the norm of h;
+ *                  h_out must then be NULL too)
+ *   scale  [D]     float32, or NULL for 1
+ *   w      [D]     float32
+ *   h_out  [R, D]  h_dtype; may be h itself
+ *   n      [R, D]  dtype; from h_out before its rounding
+ * 1 <= D <= 16384 (rows of a multiple of 8 elements move in 16-byte pieces),
+ * R >= 0, eps > 0; |h_out| up to about 1e18.
+ *
+ * Backward, for grad_n = dL/dn and grad_h_out = dL/d(h_out) through the rest
+ * of the network (h_dtype, NULL for zeros), from the forward's inputs:
+ *   grad_h [R, D] h_dtype, grad_y [R, D] dtype (NULL exactly when y is),
+ *   grad_w [D] float32, grad_scale [D] float32 (NULL exactly when scale is);
+ *   workspace at least mesa_residual_norm_backward_workspace_bytes(...).
+ */
+mesa_status mesa_residual_norm(const void *h, int h_dtype, const void *y, int dtype, const float *scale,
+                               const float *w, float eps, int R, int D, void *h_out, void *n, void *stream);
+size_t mesa_residual_norm_backward_workspace_bytes(int R, int D);
+mesa_status mesa_residual_norm_backward(const void *h, int h_dtype, const void *y, int dtype, const float *scale,
+                                        const float *w, float eps, const void *grad_n, const void *grad_h_out,
+                                        int R, int D, void *grad_h, void *grad_y, float *grad_w,
+                                        float *grad_scale, void *workspace, size_t workspace_bytes,
+                                        void *stream);
 
 /*
  * Optional per-kernel timing (not part of the method).  While enabled, each

@@ -1,0 +1,422 @@
+// block_norms.hip -- the norms around a layer and their gradients (gfx950).
+//
+// Gate norm, per token and head (x a layer's output row of d features, g its
+// gate row, w the head's weights):
+//   u = x rsqrt(mean(x^2) + eps),   y = u w silu(g),   silu(g) = g sigmoid(g)
+// with x in the layers' [B, H, T, d] order and g, y in the projections'
+// [B, T, H, d] order.  Gradients, with d_u = dy w silu(g):
+//   dx = rsqrt(..) (d_u - u mean(d_u u)),   dw = sum over tokens of dy u silu(g)
+//   dg = dy u w sigmoid(g) (1 + g (1 - sigmoid(g)))
+//
+// Residual norm, per row of D features:
+//   z = h + s y,   n = z rsqrt(mean(z^2) + eps) w
+// Gradients, with u = z rsqrt(..), d_u = dn w and dh' the gradient of z as
+// the residual's next value:
+//   dz = rsqrt(..) (d_u - u mean(d_u u)) + dh',   dh = dz,  dy = s dz
+//   dw = sum over rows of dn u,   ds = sum over rows of dz y
+//
+// All of them are HBM-bound: each input element is read once and each output
+// element written once, and a row stays in registers between its sums and
+// its outputs.  The arithmetic is float32; outputs are rounded once.  The
+// parameter gradients are summed in registers over the rows that a thread
+// sees, then over the workgroup in LDS, then over the workgroups by a second
+// small kernel, all in a fixed order (no atomics).
+#include <algorithm>
+
+#include "io8.h"
+#include "mesa_kernels.h"
+
+namespace mesa {
+
+// Sum over groups of L consecutive lanes (L a power of two up to 64).
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+__device__ __forceinline__ float sigmoid(float g) { return 1.0f / (1.0f + __expf(-g)); }
+
+// ---------------------------------------------------------------- gate norm
+
+constexpr int kGateThreads = 256;
+constexpr int kGateTokens = 8;   // consecutive tokens of a head that neighbouring rows of a workgroup take
+
+// A row takes d / 8 lanes.  Rows go by as [b][block of 8 tokens][h][token]:
+// a workgroup's rows are then runs of 8 tokens in x and runs of heads in the
+// gate, so both sides use whole cache lines.
+template <int d, typename X, typename G>
+__global__ __launch_bounds__(kGateThreads) void gate_norm_kernel(GateNormArgs a) {
+    constexpr int L = d / 8, rows = kGateThreads / L;
+    const int lane = threadIdx.x % L;
+    const long tb = (a.T + kGateTokens - 1) / kGateTokens;
+    const long r = (long)blockIdx.x * rows + threadIdx.x / L;
+    const int ti = (int)(r % kGateTokens);
+    const long r1 = r / kGateTokens;
+    const int h = (int)(r1 % a.H);
+    const long r2 = r1 / a.H;
+    const long t = (r2 % tb) * kGateTokens + ti, b = r2 / tb;
+    const bool live = b < a.B && t < a.T;
+    const size_t xo = (((size_t)b * a.H + h) * a.T + t) * d + 8 * lane;
+    const size_t go = (((size_t)b * a.T + t) * a.H + h) * d + 8 * lane;
+    f32x8 x{}, g{};
+    if (live) {
+        x = load8(static_cast<const X*>(a.x) + xo);
+        if (a.gate) g = load8(static_cast<const G*>(a.gate) + go);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += x.v[e] * x.v[e];
+    const float rs = rsqrtf(lane_sum<L>(ss) * (1.0f / d) + a.eps);
+    if (!live) return;
+    const f32x8 w = load8(a.w + (size_t)h * d + 8 * lane);
+    f32x8 y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float act = a.gate ? g.v[e] * sigmoid(g.v[e]) : 1.0f;
+        y.v[e] = x.v[e] * rs * w.v[e] * act;
+    }
+    store8(static_cast<G*>(a.y) + go, y);
+}
+
+// A workgroup takes one head and a run of its (b, t) rows, so that a thread
+// keeps the same eight columns of dw in registers throughout.
+template <int d, typename X, typename G>
+__global__ __launch_bounds__(kGateThreads) void gate_norm_bwd_kernel(GateNormBwdArgs a) {
+    constexpr int L = d / 8, rows = kGateThreads / L;
+    __shared__ float red[rows][d + 4];
+    const int lane = threadIdx.x % L, slot = threadIdx.x / L;
+    const int h = blockIdx.x % a.H;
+    const int part = blockIdx.x / a.H;
+    const long BT = (long)a.B * a.T;
+    const f32x8 w = load8(a.w + (size_t)h * d + 8 * lane);
+    float dw[8] = {};
+    // every lane of a wave runs the same number of rounds: the row sums cross lanes
+    for (long r0 = (long)part * a.rows_per_part; r0 < min(BT, (long)(part + 1) * a.rows_per_part); r0 += rows) {
+        const long r = r0 + slot;
+        const bool live = r < BT && r < (long)(part + 1) * a.rows_per_part;
+        const long b = live ? r / a.T : 0, t = live ? r % a.T : 0;
+        const size_t xo = (((size_t)b * a.H + h) * a.T + t) * d + 8 * lane;
+        const size_t go = (((size_t)b * a.T + t) * a.H + h) * d + 8 * lane;
+        f32x8 x{}, g{}, dy{};
+        if (live) {
+            x = load8(static_cast<const X*>(a.x) + xo);
+            if (a.gate) g = load8(static_cast<const G*>(a.gate) + go);
+            dy = load8(static_cast<const G*>(a.grad_y) + go);
+        }
+        float ss = 0.f, c = 0.f, act[8], sg[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sg[e] = sigmoid(g.v[e]);
+            act[e] = a.gate ? g.v[e] * sg[e] : 1.0f;
+            ss += x.v[e] * x.v[e];
+            c += dy.v[e] * w.v[e] * act[e] * x.v[e];
+        }
+        const float rs = rsqrtf(lane_sum<L>(ss) * (1.0f / d) + a.eps);
+        const float m = lane_sum<L>(c) * rs * rs * (1.0f / d);   // mean(d_u u) rs
+        f32x8 dx, dg;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float u = x.v[e] * rs;
+            dx.v[e] = rs * (dy.v[e] * w.v[e] * act[e]) - x.v[e] * rs * m;
+            dg.v[e] = dy.v[e] * u * w.v[e] * sg[e] * (1.0f + g.v[e] * (1.0f - sg[e]));
+            dw[e] += dy.v[e] * u * act[e];
+        }
+        if (live) {
+            store8(static_cast<X*>(a.grad_x) + xo, dx);
+            if (a.gate) store8(static_cast<G*>(a.grad_gate) + go, dg);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[slot][8 * lane + e] = dw[e];
+    __syncthreads();
+    for (int f = threadIdx.x; f < d; f += kGateThreads) {
+        float s = 0.f;
+        for (int i = 0; i < rows; ++i) s += red[i][f];
+        a.partial[((size_t)part * a.H + h) * d + f] = s;
+    }
+}
+
+// out[f] = sum over the parts of partial[part][f], f < n: 64 columns a
+// workgroup, its four waves taking every fourth part.
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float* partial, size_t pitch, int parts, long n, float* out) {
+    __shared__ float red[4][64];
+    const long f = (long)blockIdx.x * 64 + threadIdx.x % 64;
+    const int q = threadIdx.x / 64;
+    float s = 0.f;
+    if (f < n)
+        for (int p = q; p < parts; p += 4) s += partial[(size_t)p * pitch + f];
+    red[q][threadIdx.x % 64] = s;
+    __syncthreads();
+    if (q == 0 && f < n) {
+        const int i = threadIdx.x;
+        out[f] = (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
+    }
+}
+
+hipError_t launch_sum_parts(const float* partial, size_t pitch, int parts, long n, float* out, hipStream_t s) {
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)((n + 63) / 64)), dim3(256), 0, s, partial, pitch, parts, n, out);
+    return hipGetLastError();
+}
+
+template <int d, typename X, typename G>
+hipError_t gate_norm_go(const GateNormArgs& a, hipStream_t s) {
+    constexpr int rows = kGateThreads / (d / 8);
+    const long n = (long)a.B * ((a.T + kGateTokens - 1) / kGateTokens) * a.H * kGateTokens;
+    hipLaunchKernelGGL((gate_norm_kernel<d, X, G>), dim3((unsigned)((n + rows - 1) / rows)), dim3(kGateThreads), 0, s, a);
+    return hipGetLastError();
+}
+template <int d, typename X, typename G>
+hipError_t gate_norm_bwd_go(const GateNormBwdArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL((gate_norm_bwd_kernel<d, X, G>), dim3((unsigned)(a.parts * a.H)), dim3(kGateThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+#define MESA_GATE_DISPATCH(go)                                                         \
+    template <int d, typename A>                                                       \
+    hipError_t go##_t(const A& a, hipStream_t s) {                                     \
+        if (a.x_bf16) return a.g_bf16 ? go<d, bf16_t, bf16_t>(a, s) : go<d, bf16_t, float>(a, s); \
+        return a.g_bf16 ? go<d, float, bf16_t>(a, s) : go<d, float, float>(a, s);      \
+    }                                                                                  \
+    template <typename A>                                                              \
+    hipError_t go##_d(const A& a, hipStream_t s) {                                     \
+        switch (a.d) {                                                                 \
+            case 16: return go##_t<16>(a, s);                                          \
+            case 32: return go##_t<32>(a, s);                                          \
+            case 64: return go##_t<64>(a, s);                                          \
+            case 128: return go##_t<128>(a, s);                                        \
+            case 256: return go##_t<256>(a, s);                                        \
+        }                                                                              \
+        return hipErrorInvalidValue;                                                   \
+    }
+MESA_GATE_DISPATCH(gate_norm_go)
+MESA_GATE_DISPATCH(gate_norm_bwd_go)
+
+hipError_t launch_gate_norm(const GateNormArgs& a, hipStream_t s) { return gate_norm_go_d(a, s); }
+hipError_t launch_gate_norm_bwd(const GateNormBwdArgs& a, hipStream_t s) {
+    const hipError_t e = gate_norm_bwd_go_d(a, s);
+    if (e != hipSuccess) return e;
+    const long n = (long)a.H * a.d;
+    return launch_sum_parts(a.partial, (size_t)n, a.parts, n, a.grad_w, s);
+}
+
+// ------------------------------------------------------------ residual norm
+
+// W waves share a row (W = 1: each of a workgroup's four waves has its own);
+// a thread holds N pieces of V elements, piece j of thread t at column
+// V (t + 64 W j).
+template <int W> struct RowGroup {
+    static constexpr int threads = W == 1 ? 256 : 64 * W;
+    static constexpr int rows = W == 1 ? 4 : 1;   // rows of a workgroup at a time
+    static __device__ int tid() { return W == 1 ? threadIdx.x % 64 : threadIdx.x; }
+    // sums of two values over a row's threads; `red` holds 2 W floats a round
+    static __device__ void sum2(float& x, float& y, float (&red)[2][2][16], int& flip) {
+        x = lane_sum<64>(x);
+        y = lane_sum<64>(y);
+        if constexpr (W > 1) {
+            const int w = threadIdx.x / 64;
+            // two buffers in turn: a wave may write its next row's sums
+            // while another still reads this row's
+            if (threadIdx.x % 64 == 0) { red[flip][0][w] = x; red[flip][1][w] = y; }
+            __syncthreads();
+            x = y = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) { x += red[flip][0][i]; y += red[flip][1][i]; }
+            flip ^= 1;
+        }
+    }
+};
+
+template <int W, int V, int N, typename Hh, typename Y>
+__global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_kernel(ResidualNormArgs a) {
+    using RG = RowGroup<W>;
+    __shared__ float red[2][2][16];
+    int flip = 0;
+    const int t = RG::tid();
+    const long r = (long)blockIdx.x * RG::rows + (W == 1 ? threadIdx.x / 64 : 0);
+    if (r >= a.R) return;   // a whole wave (W = 1), or never
+    const size_t ro = (size_t)r * a.D;
+    float z[N][V], ss = 0.f, none = 0.f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int f = V * (t + 64 * W * j);
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[j][e] = 0.f;
+        if (f < a.D) {
+            load_v<V>(static_cast<const Hh*>(a.h) + ro + f, z[j]);
+            if (a.y) {
+                float y[V], s[V];
+                load_v<V>(static_cast<const Y*>(a.y) + ro + f, y);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[e] = 1.0f;
+                if (a.scale) load_v<V>(a.scale + f, s);
+#pragma unroll
+                for (int e = 0; e < V; ++e) z[j][e] += s[e] * y[e];
+                store_v<V>(static_cast<Hh*>(a.h_out) + ro + f, z[j]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) ss += z[j][e] * z[j][e];
+    }
+    RG::sum2(ss, none, red, flip);
+    const float rs = rsqrtf(ss / (float)a.D + a.eps);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const int f = V * (t + 64 * W * j);
+        if (f < a.D) {
+            float w[V];
+            load_v<V>(a.w + f, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) w[e] *= z[j][e] * rs;
+            store_v<V>(static_cast<Y*>(a.n) + ro + f, w);
+        }
+    }
+}
+
+// Workgroup i takes row groups i, i + gridDim.x, ...; its sums of dw and ds go
+// to partial[i][0..D) and partial[i][D..2D).
+template <int W, int V, int N, typename Hh, typename Y>
+__global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel(ResidualNormBwdArgs a) {
+    using RG = RowGroup<W>;
+    __shared__ float red[2][2][16];
+    __shared__ float own[W == 1 ? 4 : 1][W == 1 ? 64 * V * N : 1];
+    int flip = 0;
+    const int t = RG::tid(), wave = threadIdx.x / 64;
+    float dw[N][V] = {}, ds[N][V] = {};
+    const float inv_D = 1.0f / (float)a.D;
+    for (long r = (long)blockIdx.x * RG::rows + (W == 1 ? wave : 0); r < a.R; r += (long)gridDim.x * RG::rows) {
+        const size_t ro = (size_t)r * a.D;
+        float z[N][V], y[N][V], d[N][V], ss = 0.f, c = 0.f;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int f = V * (t + 64 * W * j);
+#pragma unroll
+            for (int e = 0; e < V; ++e) z[j][e] = y[j][e] = d[j][e] = 0.f;
+            if (f < a.D) {
+                load_v<V>(static_cast<const Hh*>(a.h) + ro + f, z[j]);
+                load_v<V>(static_cast<const Y*>(a.grad_n) + ro + f, d[j]);
+                if (a.y) load_v<V>(static_cast<const Y*>(a.y) + ro + f, y[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int f = V * (t + 64 * W * j);
+            if (f < a.D) {
+                float s[V], w[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[e] = 1.0f;
+                if (a.scale) load_v<V>(a.scale + f, s);
+                load_v<V>(a.w + f, w);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    z[j][e] += s[e] * y[j][e];
+                    ss += z[j][e] * z[j][e];
+                    c += d[j][e] * w[e] * z[j][e];
+                }
+            }
+        }
+        RG::sum2(ss, c, red, flip);
+        const float rs = rsqrtf(ss * inv_D + a.eps);
+        const float m = c * rs * rs * inv_D;   // mean(d_u u) rs
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int f = V * (t + 64 * W * j);
+            if (f < a.D) {
+                float s[V], w[V], dh[V], dz[V];
+#pragma unroll
+                for (int e = 0; e < V; ++e) { s[e] = 1.0f; dh[e] = 0.f; }
+                if (a.scale) load_v<V>(a.scale + f, s);
+                load_v<V>(a.w + f, w);
+                if (a.grad_h_out) load_v<V>(static_cast<const Hh*>(a.grad_h_out) + ro + f, dh);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float u = z[j][e] * rs;
+                    dz[e] = rs * (d[j][e] * w[e]) - u * m + dh[e];
+                    dw[j][e] += d[j][e] * u;
+                    ds[j][e] += dz[e] * y[j][e];
+                }
+                store_v<V>(static_cast<Hh*>(a.grad_h) + ro + f, dz);
+                if (a.grad_y) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e) dz[e] *= s[e];
+                    store_v<V>(static_cast<Y*>(a.grad_y) + ro + f, dz);
+                }
+            }
+        }
+    }
+    float* out = a.partial + (size_t)blockIdx.x * 2 * a.D;
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int f = V * (t + 64 * W * j);
+            if (f < a.D)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    out[f + e] = dw[j][e];
+                    if (a.grad_scale) out[a.D + f + e] = ds[j][e];
+                }
+        }
+    } else {
+        for (int k = 0; k < (a.grad_scale ? 2 : 1); ++k) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int e = 0; e < V; ++e) own[wave][V * (t + 64 * j) + e] = k ? ds[j][e] : dw[j][e];
+            __syncthreads();
+            for (int f = threadIdx.x; f < a.D; f += 256)
+                out[(size_t)k * a.D + f] = (own[0][f] + own[1][f]) + (own[2][f] + own[3][f]);
+        }
+    }
+}
+
+// The row layouts built: D up to 512 and 2048 with a wave a row, up to 2048
+// with four waves and one piece a thread (few rows: the row's latency counts),
+// up to 8192 with four waves, up to 32768 with sixteen.
+template <template <int, int, int> class Go, typename A>
+hipError_t residual_shape(const A& a, hipStream_t s) {
+    const bool v8 = a.D % 8 == 0;
+    if (a.D <= 512) return v8 ? Go<1, 8, 1>::go(a, s) : Go<1, 1, 8>::go(a, s);
+    if (a.D <= 2048 && a.R <= 1024) return v8 ? Go<4, 8, 1>::go(a, s) : Go<4, 1, 8>::go(a, s);
+    if (a.D <= 2048) return v8 ? Go<1, 8, 4>::go(a, s) : Go<1, 1, 32>::go(a, s);
+    if (a.D <= 8192) return v8 ? Go<4, 8, 4>::go(a, s) : Go<4, 1, 32>::go(a, s);
+    return v8 ? Go<16, 8, 2>::go(a, s) : Go<16, 1, 16>::go(a, s);
+}
+
+template <int W, int V, int N> struct FwdGo {
+    template <typename Hh, typename Y>
+    static hipError_t one(const ResidualNormArgs& a, hipStream_t s) {
+        using RG = RowGroup<W>;
+        hipLaunchKernelGGL((residual_norm_kernel<W, V, N, Hh, Y>), dim3((unsigned)((a.R + RG::rows - 1) / RG::rows)),
+                           dim3(RG::threads), 0, s, a);
+        return hipGetLastError();
+    }
+    static hipError_t go(const ResidualNormArgs& a, hipStream_t s) {
+        if (a.h_bf16) return a.y_bf16 ? one<bf16_t, bf16_t>(a, s) : one<bf16_t, float>(a, s);
+        return a.y_bf16 ? one<float, bf16_t>(a, s) : one<float, float>(a, s);
+    }
+};
+template <int W, int V, int N> struct BwdGo {
+    template <typename Hh, typename Y>
+    static hipError_t one(const ResidualNormBwdArgs& a, hipStream_t s) {
+        hipLaunchKernelGGL((residual_norm_bwd_kernel<W, V, N, Hh, Y>), dim3((unsigned)a.parts),
+                           dim3(RowGroup<W>::threads), 0, s, a);
+        return hipGetLastError();
+    }
+    static hipError_t go(const ResidualNormBwdArgs& a, hipStream_t s) {
+        if (a.h_bf16) return a.y_bf16 ? one<bf16_t, bf16_t>(a, s) : one<bf16_t, float>(a, s);
+        return a.y_bf16 ? one<float, bf16_t>(a, s) : one<float, float>(a, s);
+    }
+};
+
+hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) { return residual_shape<FwdGo>(a, s); }
+hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a, hipStream_t s) {
+    hipError_t e = residual_shape<BwdGo>(a, s);
+    if (e != hipSuccess) return e;
+    e = launch_sum_parts(a.partial, 2 * (size_t)a.D, a.parts, a.D, a.grad_w, s);
+    if (e != hipSuccess || !a.grad_scale) return e;
+    return launch_sum_parts(a.partial + a.D, 2 * (size_t)a.D, a.parts, a.D, a.grad_scale, s);
+}
+
+}  // namespace mesa

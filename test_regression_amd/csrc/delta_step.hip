@@ -1,0 +1,112 @@
+// delta_step.hip -- one token of the gated delta rule, state updated in place (gfx950).
+//
+// Per sequence and head, with the state S (dv x dk), decay g and strength b:
+//   e = b (v - g S k),   S' = g S + e k^T,   o = S' q = g S q + e (k . q)
+// Row i of S only meets v_i: e_i = b (v_i - g S_i . k) and o_i = g S_i . q +
+// e_i (k . q).  So each row is read once, both of its dot products are taken
+// from the registers, and it is written back.
+//
+// HBM-bound: 8 dk dv bytes of state a head against about 7 flops for each
+// 8 bytes.  Eight lanes take a row (four at dk = 16), 16-byte pieces
+// interleaved over them, so that a wave's accesses are 128-byte runs and the
+// row sums take three lane exchanges.
+#include "io8.h"
+#include "mesa_kernels.h"
+
+namespace mesa {
+
+template <int dk> struct StepShape {
+    static constexpr int lanes = dk >= 32 ? 8 : 4;
+    static constexpr int pieces = dk / (4 * lanes);
+    static constexpr int rows = 64 / lanes;       // rows of a wave at a time; a head's dv is a multiple of them
+};
+
+template <int L>
+__device__ __forceinline__ float step_sum(float v) {
+    v += dpp<0xB1>(v);                 // lanes 1 apart
+    v += dpp<0x4E>(v);                 // lanes 2 apart
+    if constexpr (L == 8) v += dpp<0x141>(v);   // row_half_mirror: the other four of the eight
+    return v;
+}
+
+// A wave takes RG consecutive groups of rows of one head.
+template <int dk, int RG, typename In>
+__global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a) {
+    using Sh = StepShape<dk>;
+    const long g0 = ((long)blockIdx.x * 4 + threadIdx.x / 64) * RG;
+    if (g0 >= a.groups) return;
+    const int lane = threadIdx.x % 64, li = lane % Sh::lanes, lr = lane / Sh::lanes;
+    const long row0 = g0 * Sh::rows;
+    const long nh = row0 / a.dv;
+    const long n = nh / a.H;
+    const int h = (int)(nh % a.H);
+    const size_t ko = ((size_t)n * a.Hk + h / (a.H / a.Hk)) * dk + 4 * li;
+    f32x4 S[RG][Sh::pieces], k[Sh::pieces], q[Sh::pieces];
+    float* p = a.state + (size_t)(row0 + lr) * dk + 4 * li;
+#pragma unroll
+    for (int i = 0; i < RG; ++i)
+#pragma unroll
+        for (int j = 0; j < Sh::pieces; ++j)
+            S[i][j] = load4(p + (size_t)i * Sh::rows * dk + 4 * Sh::lanes * j);
+    const float ga = a.gamma[nh], be = a.beta[nh];
+    float v[RG];
+#pragma unroll
+    for (int i = 0; i < RG; ++i) v[i] = to_f32(static_cast<const In*>(a.v)[row0 + i * Sh::rows + lr]);
+    float kq = 0.f;
+#pragma unroll
+    for (int j = 0; j < Sh::pieces; ++j) {
+        k[j] = load4(static_cast<const In*>(a.k) + ko + 4 * Sh::lanes * j);
+        q[j] = load4(static_cast<const In*>(a.q) + ko + 4 * Sh::lanes * j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kq += k[j][e] * q[j][e];
+    }
+    kq = step_sum<Sh::lanes>(kq);
+#pragma unroll
+    for (int i = 0; i < RG; ++i) {
+        float sk = 0.f, sq = 0.f;
+#pragma unroll
+        for (int j = 0; j < Sh::pieces; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                S[i][j][e] *= ga;
+                sk += S[i][j][e] * k[j][e];
+                sq += S[i][j][e] * q[j][e];
+            }
+        sk = step_sum<Sh::lanes>(sk);
+        sq = step_sum<Sh::lanes>(sq);
+        const float e1 = be * (v[i] - sk);
+#pragma unroll
+        for (int j = 0; j < Sh::pieces; ++j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[i][j][e] += e1 * k[j][e];
+            *reinterpret_cast<f32x4*>(p + (size_t)i * Sh::rows * dk + 4 * Sh::lanes * j) = S[i][j];
+        }
+        if (li == 0) store1(static_cast<In*>(a.out) + row0 + i * Sh::rows + lr, sq + e1 * kq);
+    }
+}
+
+template <int dk, typename In>
+hipError_t step_go(DeltaStepArgs a, hipStream_t s) {
+    constexpr int rows = StepShape<dk>::rows;
+    a.groups = a.NH * (a.dv / rows);
+    // four groups a wave once that still leaves 16 waves a CU, so that a wave
+    // has 64 bytes a lane and more in flight
+    if (a.dv / rows % 4 == 0 && a.groups >= 4L * 16 * 256) {
+        hipLaunchKernelGGL((delta_step_kernel<dk, 4, In>), dim3((unsigned)((a.groups / 4 + 3) / 4)), dim3(256), 0, s, a);
+    } else {
+        hipLaunchKernelGGL((delta_step_kernel<dk, 1, In>), dim3((unsigned)((a.groups + 3) / 4)), dim3(256), 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_delta_step(const DeltaStepArgs& a, hipStream_t s) {
+    switch (a.dk) {
+        case 16: return a.bf16 ? step_go<16, bf16_t>(a, s) : step_go<16, float>(a, s);
+        case 32: return a.bf16 ? step_go<32, bf16_t>(a, s) : step_go<32, float>(a, s);
+        case 64: return a.bf16 ? step_go<64, bf16_t>(a, s) : step_go<64, float>(a, s);
+        case 128: return a.bf16 ? step_go<128, bf16_t>(a, s) : step_go<128, float>(a, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace mesa

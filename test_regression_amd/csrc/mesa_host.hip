@@ -93,6 +93,17 @@ hipError_t zero_fill(void* p, size_t bytes, hipStream_t s) {
     return hipGetLastError();
 }
 
+__global__ void copy_words_kernel(float* out, const float* in, size_t n) {
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
+        out[i] = in[i];
+}
+
+hipError_t copy_words(float* out, const float* in, size_t n, hipStream_t s) {
+    const unsigned blocks = (unsigned)std::min<size_t>((n + 255) / 256, 4096);
+    hipLaunchKernelGGL(copy_words_kernel, dim3(blocks), dim3(256), 0, s, out, in, n);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 extern "C" {
@@ -533,6 +544,264 @@ mesa_status mesa_hawk_scan(const void* x, const void* ga, const void* gx, int in
     return MESA_OK;
 }
 
+// ---- gated delta rule ----
+static bool dtype_ok(int t) { return t == MESA_DTYPE_F32 || t == MESA_DTYPE_BF16; }
+
+// Bytes per head and chunk: the fp16 planes of M (two) and P (one for bf16,
+// two for float32), then the scalars.
+static size_t delta_image_halfs(int dtype) {
+    return (size_t)(dtype == MESA_DTYPE_BF16 ? 3 : 4) * mesa::kDeltaChunk * mesa::kDeltaChunk;
+}
+static long delta_chunks(int T) { return ((long)T + mesa::kDeltaChunk - 1) / mesa::kDeltaChunk; }
+
+size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype) {
+    if (B <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
+    return (size_t)B * H * delta_chunks(T) * (delta_image_halfs(dtype) * 2 + mesa::kDeltaScal * sizeof(float));
+}
+
+// The checks the delta entry points share; `rows` is T or, for the step, 1.
+static mesa_status delta_checks(int dtype, int B, int Hk, int H, int T, int dk, int dv) {
+    if (!dtype_ok(dtype))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "dtype %d is not MESA_DTYPE_F32 or MESA_DTYPE_BF16", dtype);
+    if (B <= 0 || Hk <= 0 || H <= 0 || T < 0 || dk <= 0 || dv <= 0)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "sizes must be positive, T >= 0 (B or N=%d Hk=%d H=%d T=%d dk=%d dv=%d)",
+                    B, Hk, H, T, dk, dv);
+    if (H % Hk != 0) return fail(MESA_ERR_INVALID_ARGUMENT, "H=%d is not a multiple of Hk=%d", H, Hk);
+    if (!supported_d(dk)) return fail(MESA_ERR_UNSUPPORTED, "dk=%d not built (16, 32, 64, 128)", dk);
+    if (!supported_d(dv) && dv != 256) return fail(MESA_ERR_UNSUPPORTED, "dv=%d not built (16, 32, 64, 128, 256)", dv);
+    // launches of one workgroup per head and chunk, and up to 64 row groups a head
+    if ((double)B * H * std::max<long>(delta_chunks(T), 64) > 1e9)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B*H=%ld, chunks=%ld)", (long)B * H, delta_chunks(T));
+    return MESA_OK;
+}
+
+static hipError_t copy_or_zero(float* out, const float* in, size_t n, hipStream_t s) {
+    if (!out || out == in) return hipSuccess;
+    return in ? copy_words(out, in, n, s) : zero_fill(out, n * sizeof(float), s);
+}
+
+mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int dtype, const float* gamma,
+                               const float* beta, const float* state0, int B, int Hk, int H, int T, int dk,
+                               int dv, void* out, float* final_state, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+    g_err.clear();
+    const mesa_status st = delta_checks(dtype, B, Hk, H, T, dk, dv);
+    if (st != MESA_OK) return st;
+    if (T > 0 && (!q || !k || !v || !gamma || !beta || !out || !workspace))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "q, k, v, gamma, beta, out and workspace must be non-null");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(state0, 16) ||
+        !aligned(final_state, 16) || !aligned(workspace, 16) || !aligned(gamma, 4) || !aligned(beta, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for tensors/workspace, 4 B for gamma/beta)");
+    if (out && (out == q || out == k || out == v))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "out must not alias q, k or v");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const long BH = (long)B * H, nc = delta_chunks(T);
+    if (T == 0) {
+        // no token: the final state is the initial one
+        const hipError_t e = copy_or_zero(final_state, state0, (size_t)BH * dv * dk, s);
+        if (e != hipSuccess) return hip_fail(e, "final state for T = 0");
+        return MESA_OK;
+    }
+    if (workspace_bytes < mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype))
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes,
+                    mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype));
+    uint16_t* img = static_cast<uint16_t*>(workspace);
+    float* scal = reinterpret_cast<float*>(img + (size_t)BH * nc * delta_image_halfs(dtype));
+    const mesa::DeltaArgs a{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
+                            out, final_state, img, scal, nullptr, nullptr};
+    hipError_t e = timed_launch(MESA_KERNEL_DELTA_PREP, s, [&] { return mesa::launch_delta_prep(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta chunk-matrix kernel launch");
+    e = timed_launch(MESA_KERNEL_DELTA_SCAN, s, [&] { return mesa::launch_delta_scan(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta scan kernel launch");
+    return MESA_OK;
+}
+
+mesa_status mesa_delta_step(const void* q, const void* k, const void* v, int dtype, const float* gamma,
+                            const float* beta, float* state, int N, int Hk, int H, int dk, int dv, void* out,
+                            void* stream) {
+    g_err.clear();
+    const mesa_status st = delta_checks(dtype, N, Hk, H, 1, dk, dv);
+    if (st != MESA_OK) return st;
+    if (!q || !k || !v || !gamma || !beta || !state || !out)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "q, k, v, gamma, beta, state and out must be non-null");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(state, 16) ||
+        !aligned(gamma, 4) || !aligned(beta, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for tensors, 4 B for gamma/beta)");
+    if (out == q || out == k || out == v) return fail(MESA_ERR_INVALID_ARGUMENT, "out must not alias q, k or v");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const mesa::DeltaStepArgs a{q, k, v, gamma, beta, state, (long)N * H, Hk, H, dk, dv, dtype == MESA_DTYPE_BF16,
+                                out, 0};
+    const hipError_t e = timed_launch(MESA_KERNEL_DELTA_STEP, s, [&] { return mesa::launch_delta_step(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta step kernel launch");
+    return MESA_OK;
+}
+
+// ---- norms around a layer ----
+static mesa_status gate_checks(const void* x, int x_dtype, const void* gate, int dtype, const float* w, float eps,
+                               int B, int H, int T, int d) {
+    if (!dtype_ok(x_dtype) || !dtype_ok(dtype))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "x_dtype %d / dtype %d must be MESA_DTYPE_F32 or MESA_DTYPE_BF16",
+                    x_dtype, dtype);
+    if (B <= 0 || H <= 0 || T < 0 || d <= 0)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "sizes must be positive, T >= 0 (B=%d H=%d T=%d d=%d)", B, H, T, d);
+    if (!(eps > 0.0f) || std::isinf(eps)) return fail(MESA_ERR_INVALID_ARGUMENT, "eps must be finite and > 0");
+    if (!w || (T > 0 && !x)) return fail(MESA_ERR_INVALID_ARGUMENT, "w, and x when T > 0, must be non-null");
+    if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(w, 16))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
+    if (!supported_d(d) && d != 256) return fail(MESA_ERR_UNSUPPORTED, "d=%d not built (16, 32, 64, 128, 256)", d);
+    if ((double)B * H * ((double)T + 8) > 1e9)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B=%d H=%d T=%d)", B, H, T);
+    return MESA_OK;
+}
+
+mesa_status mesa_gate_norm(const void* x, int x_dtype, const void* gate, int dtype, const float* w, float eps, int B,
+                           int H, int T, int d, void* y, void* stream) {
+    g_err.clear();
+    const mesa_status st = gate_checks(x, x_dtype, gate, dtype, w, eps, B, H, T, d);
+    if (st != MESA_OK) return st;
+    if (T > 0 && !y) return fail(MESA_ERR_INVALID_ARGUMENT, "y must be non-null");
+    if (!aligned(y, 16)) return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
+    if (y && (y == x || y == gate)) return fail(MESA_ERR_INVALID_ARGUMENT, "y must not alias x or gate");
+    if (T == 0) return MESA_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const mesa::GateNormArgs a{x, gate, w, eps, B, H, T, d, x_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16, y};
+    const hipError_t e = timed_launch(MESA_KERNEL_GATE_NORM, s, [&] { return mesa::launch_gate_norm(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "gate norm kernel launch");
+    return MESA_OK;
+}
+
+// Workgroups a head of the backward (each keeps one partial sum of grad_w):
+// about 2048 in all, each with whole passes of its 2048 / d rows.
+static void gate_parts(int B, int H, int T, int d, int* parts, long* rows) {
+    const long BT = (long)B * T, pass = 2048 / d;
+    long p = std::min(std::max(2048L / H, 1L), (BT + pass - 1) / pass);
+    const long r = ((BT + p - 1) / p + pass - 1) / pass * pass;
+    *rows = r;
+    *parts = (int)((BT + r - 1) / r);
+}
+
+size_t mesa_gate_norm_backward_workspace_bytes(int B, int H, int T, int d) {
+    if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || d > 2048) return 0;
+    int parts;
+    long rows;
+    gate_parts(B, H, T, d, &parts, &rows);
+    return (size_t)parts * H * d * sizeof(float);
+}
+
+mesa_status mesa_gate_norm_backward(const void* x, int x_dtype, const void* gate, int dtype, const float* w, float eps,
+                                    const void* grad_y, int B, int H, int T, int d, void* grad_x, void* grad_gate,
+                                    float* grad_w, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    const mesa_status st = gate_checks(x, x_dtype, gate, dtype, w, eps, B, H, T, d);
+    if (st != MESA_OK) return st;
+    if (!grad_w || (T > 0 && (!grad_y || !grad_x || !workspace)))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_w, and grad_y, grad_x and workspace when T > 0, must be non-null");
+    if (T > 0 && (gate == nullptr) != (grad_gate == nullptr))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_gate must be given exactly when gate is");
+    if (!aligned(grad_y, 16) || !aligned(grad_x, 16) || !aligned(grad_gate, 16) || !aligned(workspace, 16) ||
+        !aligned(grad_w, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for tensors/workspace, 4 B for grad_w)");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0) {
+        const hipError_t e = zero_fill(grad_w, (size_t)H * d * sizeof(float), s);
+        if (e != hipSuccess) return hip_fail(e, "zero fill of grad_w");
+        return MESA_OK;
+    }
+    for (const void* o : {(const void*)grad_x, (const void*)grad_gate})
+        if (o && (o == x || o == gate || o == grad_y))
+            return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
+    const size_t need = mesa_gate_norm_backward_workspace_bytes(B, H, T, d);
+    if (workspace_bytes < need)
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    mesa::GateNormBwdArgs a{x, gate, w, eps, B, H, T, d, x_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16,
+                            grad_y, grad_x, grad_gate, grad_w, static_cast<float*>(workspace), 0, 0};
+    gate_parts(B, H, T, d, &a.parts, &a.rows_per_part);
+    const hipError_t e = timed_launch(MESA_KERNEL_GATE_NORM_BWD, s, [&] { return mesa::launch_gate_norm_bwd(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "gate norm backward kernel launch");
+    return MESA_OK;
+}
+
+static mesa_status residual_checks(const void* h, int h_dtype, const void* y, int dtype, const float* scale,
+                                   const float* w, float eps, int R, int D) {
+    if (!dtype_ok(h_dtype) || !dtype_ok(dtype))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "h_dtype %d / dtype %d must be MESA_DTYPE_F32 or MESA_DTYPE_BF16",
+                    h_dtype, dtype);
+    if (R < 0 || D <= 0) return fail(MESA_ERR_INVALID_ARGUMENT, "sizes must be positive, R >= 0 (R=%d D=%d)", R, D);
+    if (!(eps > 0.0f) || std::isinf(eps)) return fail(MESA_ERR_INVALID_ARGUMENT, "eps must be finite and > 0");
+    if (!w || (R > 0 && !h)) return fail(MESA_ERR_INVALID_ARGUMENT, "w, and h when R > 0, must be non-null");
+    if (scale && !y && R > 0) return fail(MESA_ERR_INVALID_ARGUMENT, "scale needs y");
+    if (!aligned(h, 16) || !aligned(y, 16) || !aligned(scale, 16) || !aligned(w, 16))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
+    if (D > 16384) return fail(MESA_ERR_UNSUPPORTED, "D=%d not built (at most 16384)", D);
+    return MESA_OK;
+}
+
+mesa_status mesa_residual_norm(const void* h, int h_dtype, const void* y, int dtype, const float* scale, const float* w,
+                               float eps, int R, int D, void* h_out, void* n, void* stream) {
+    g_err.clear();
+    const mesa_status st = residual_checks(h, h_dtype, y, dtype, scale, w, eps, R, D);
+    if (st != MESA_OK) return st;
+    if (R > 0 && !n) return fail(MESA_ERR_INVALID_ARGUMENT, "n must be non-null");
+    if (R > 0 && (y == nullptr) != (h_out == nullptr))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "h_out must be given exactly when y is");
+    if (!aligned(h_out, 16) || !aligned(n, 16))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
+    if (n && (n == h || n == y || n == h_out)) return fail(MESA_ERR_INVALID_ARGUMENT, "n must not alias h, y or h_out");
+    if (h_out && h_out == y) return fail(MESA_ERR_INVALID_ARGUMENT, "h_out must not alias y");
+    if (R == 0) return MESA_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const mesa::ResidualNormArgs a{h, y, w, scale, eps, R, D, h_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16,
+                                   h_out, n};
+    const hipError_t e = timed_launch(MESA_KERNEL_RESIDUAL_NORM, s, [&] { return mesa::launch_residual_norm(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "residual norm kernel launch");
+    return MESA_OK;
+}
+
+// Workgroups of the backward, each with one partial sum of the parameter gradients.
+static int residual_parts(int R) { return (int)std::min<long>(((long)R + 3) / 4, 512); }
+
+size_t mesa_residual_norm_backward_workspace_bytes(int R, int D) {
+    if (R <= 0 || D <= 0) return 0;
+    return (size_t)residual_parts(R) * 2 * D * sizeof(float);
+}
+
+mesa_status mesa_residual_norm_backward(const void* h, int h_dtype, const void* y, int dtype, const float* scale,
+                                        const float* w, float eps, const void* grad_n, const void* grad_h_out, int R,
+                                        int D, void* grad_h, void* grad_y, float* grad_w, float* grad_scale,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    const mesa_status st = residual_checks(h, h_dtype, y, dtype, scale, w, eps, R, D);
+    if (st != MESA_OK) return st;
+    if (!grad_w || (R > 0 && (!grad_n || !grad_h || !workspace)))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_w, and grad_n, grad_h and workspace when R > 0, must be non-null");
+    if ((scale == nullptr) != (grad_scale == nullptr) || (R > 0 && (y == nullptr) != (grad_y == nullptr)))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_y and grad_scale must be given exactly when y and scale are");
+    if (!aligned(grad_n, 16) || !aligned(grad_h_out, 16) || !aligned(grad_h, 16) || !aligned(grad_y, 16) ||
+        !aligned(workspace, 16) || !aligned(grad_w, 4) || !aligned(grad_scale, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT,
+                    "misaligned pointer (16 B for tensors/workspace, 4 B for grad_w/grad_scale)");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (R == 0) {
+        hipError_t e = zero_fill(grad_w, (size_t)D * sizeof(float), s);
+        if (e == hipSuccess) e = zero_fill(grad_scale, (size_t)D * sizeof(float), s);
+        if (e != hipSuccess) return hip_fail(e, "zero fill of the parameter gradients");
+        return MESA_OK;
+    }
+    for (const void* o : {(const void*)grad_h, (const void*)grad_y})
+        if (o && (o == h || o == y || o == grad_n || o == grad_h_out))
+            return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
+    const size_t need = mesa_residual_norm_backward_workspace_bytes(R, D);
+    if (workspace_bytes < need)
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    const mesa::ResidualNormBwdArgs a{h, y, w, scale, eps, R, D, h_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16,
+                                      grad_n, grad_h_out, grad_h, grad_y, grad_w, grad_scale,
+                                      static_cast<float*>(workspace), residual_parts(R)};
+    const hipError_t e =
+        timed_launch(MESA_KERNEL_RESIDUAL_NORM_BWD, s, [&] { return mesa::launch_residual_norm_bwd(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "residual norm backward kernel launch");
+    return MESA_OK;
+}
+
 mesa_status mesa_profile_enable(int on) {
     std::lock_guard<std::mutex> g(g_prof_mu);
     g_prof_on = on != 0;
@@ -553,7 +822,9 @@ mesa_status mesa_profile_reset(void) {
 
 mesa_status mesa_profile_read(int kernel_id, double* total_ms, int64_t* launches) {
     g_err.clear();
-    if (kernel_id < 0 || kernel_id >= MESA_KERNEL_COUNT || !total_ms || !launches)
+    const bool used = (kernel_id >= 0 && kernel_id <= MESA_KERNEL_HAWK) ||
+                      (kernel_id >= MESA_KERNEL_DELTA_PREP && kernel_id < MESA_KERNEL_COUNT);
+    if (!used || !total_ms || !launches)
         return fail(MESA_ERR_INVALID_ARGUMENT, "bad kernel id %d or null output", kernel_id);
     std::lock_guard<std::mutex> g(g_prof_mu);
     mesa_status st = MESA_OK;
@@ -584,6 +855,15 @@ const char* mesa_kernel_name(int kernel_id) {
         case MESA_KERNEL_BWD_KV: return "bwd_kv_kernel";
         case MESA_KERNEL_BWD_GATE: return "bwd_gate_kernel";
         case MESA_KERNEL_HAWK: return "hawk_kernels";
+        case MESA_KERNEL_DELTA_PREP: return "delta_prep_kernel";
+        case MESA_KERNEL_DELTA_SCAN: return "delta_scan_kernel";
+        case MESA_KERNEL_DELTA_STEP: return "delta_step_kernel";
+        case MESA_KERNEL_DELTA_BWD_SCAN: return "delta_bwd_scan_kernel";
+        case MESA_KERNEL_DELTA_GRADS: return "delta_grads_kernels";
+        case MESA_KERNEL_GATE_NORM: return "gate_norm_kernel";
+        case MESA_KERNEL_GATE_NORM_BWD: return "gate_norm_bwd_kernels";
+        case MESA_KERNEL_RESIDUAL_NORM: return "residual_norm_kernel";
+        case MESA_KERNEL_RESIDUAL_NORM_BWD: return "residual_norm_bwd_kernels";
     }
     return "unknown";
 }

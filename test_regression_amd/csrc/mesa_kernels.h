@@ -93,6 +93,55 @@ struct HawkArgs {
 };
 hipError_t launch_hawk(const HawkArgs& a, hipStream_t s);
 
+// Gated delta rule (delta_*.hip).
+constexpr int kDeltaChunk = 64;   // tokens per chunk
+constexpr int kDeltaScal = 576;   // floats of per-chunk scalars in the workspace
+struct DeltaArgs {
+    const void* q; const void* k; const void* v; const float* gamma; const float* beta; const float* state0;
+    long BH; int Hk; int H; int T; int dk; int dv; int nc; int bf16;
+    void* out; float* final_state;
+    uint16_t* img; float* scal;   // workspace: per head and chunk the planes of M and P, the scalars
+    float* S; float* E;           // backward workspace: chunk start states [BH][nc][dv][dk], E [BH][nc][64][dv]
+};
+hipError_t launch_delta_prep(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E
+struct DeltaStepArgs {
+    const void* q; const void* k; const void* v; const float* gamma; const float* beta; float* state;
+    long NH; int Hk; int H; int dk; int dv; int bf16;
+    void* out;
+    long groups;   // set by the launch: row groups of a wave
+};
+hipError_t launch_delta_step(const DeltaStepArgs& a, hipStream_t s);
+
+// Norms around a layer (block_norms.hip).
+struct GateNormArgs {
+    const void* x; const void* gate; const float* w; float eps;
+    int B; int H; int T; int d; int x_bf16; int g_bf16;
+    void* y;
+};
+struct GateNormBwdArgs {
+    const void* x; const void* gate; const float* w; float eps;
+    int B; int H; int T; int d; int x_bf16; int g_bf16;
+    const void* grad_y; void* grad_x; void* grad_gate; float* grad_w;
+    float* partial; int parts; long rows_per_part;   // dw per part: [parts][H][d]
+};
+struct ResidualNormArgs {
+    const void* h; const void* y; const float* w; const float* scale; float eps;
+    long R; int D; int h_bf16; int y_bf16;
+    void* h_out; void* n;
+};
+struct ResidualNormBwdArgs {
+    const void* h; const void* y; const float* w; const float* scale; float eps;
+    long R; int D; int h_bf16; int y_bf16;
+    const void* grad_n; const void* grad_h_out; void* grad_h; void* grad_y; float* grad_w; float* grad_scale;
+    float* partial; int parts;   // dw and ds per part: [parts][2][D]
+};
+hipError_t launch_gate_norm(const GateNormArgs& a, hipStream_t s);
+hipError_t launch_gate_norm_bwd(const GateNormBwdArgs& a, hipStream_t s);
+hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s);
+hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a, hipStream_t s);
+
 hipError_t launch_cg_output(const CgOutputArgs& a, hipStream_t s);
 hipError_t launch_cg_output_bf16(const CgOutputArgs& a, hipStream_t s);   // bf16 q/k/v, d >= 32
 hipError_t launch_qk_preprocess(const QkPreArgs& a, hipStream_t s);

@@ -7,6 +7,7 @@ if libmesa.so is missing or cannot be loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -17,6 +18,8 @@ MESA_OK, MESA_ERR_INVALID_ARGUMENT, MESA_ERR_UNSUPPORTED, MESA_ERR_WORKSPACE_TOO
 MESA_DTYPE_F32, MESA_DTYPE_BF16 = 0, 1
 KERNEL_CHUNK_STATES, KERNEL_CG_OUTPUT, KERNEL_DECODE, KERNEL_QK_PREPROCESS = 0, 1, 2, 3
 KERNEL_BWD_ADJOINT, KERNEL_BWD_STATES, KERNEL_BWD_KV, KERNEL_BWD_GATE, KERNEL_HAWK = 4, 5, 6, 7, 8
+(KERNEL_DELTA_PREP, KERNEL_DELTA_SCAN, KERNEL_DELTA_STEP, KERNEL_DELTA_BWD_SCAN, KERNEL_DELTA_GRADS, KERNEL_GATE_NORM,
+ KERNEL_GATE_NORM_BWD, KERNEL_RESIDUAL_NORM, KERNEL_RESIDUAL_NORM_BWD) = range(16, 25)
 MESA_WARM_COLD, MESA_WARM_PREVIOUS, MESA_WARM_PROJECTED = 0, 1, 2
 
 # Every symbol include/mesa.h declares, with its ctypes signature.
@@ -42,6 +45,15 @@ SIGNATURES = {
     "mesa_qk_preprocess": ([_P, _I, _P, _I, _P, _P, _I, _I, _I, _I, _P, _I, _P], _I),
     "mesa_hawk_workspace_bytes": ([_I, _I, _I], _Z),
     "mesa_hawk_scan": ([_P, _P, _P, _I, _P, _F, _P, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "mesa_delta_workspace_bytes": ([_I, _I, _I, _I, _I, _I], _Z),
+    "mesa_delta_forward": ([_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "mesa_delta_step": ([_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P], _I),
+    "mesa_gate_norm": ([_P, _I, _P, _I, _P, _F, _I, _I, _I, _I, _P, _P], _I),
+    "mesa_gate_norm_backward_workspace_bytes": ([_I, _I, _I, _I], _Z),
+    "mesa_gate_norm_backward": ([_P, _I, _P, _I, _P, _F, _P, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P], _I),
+    "mesa_residual_norm": ([_P, _I, _P, _I, _P, _P, _F, _I, _I, _P, _P, _P], _I),
+    "mesa_residual_norm_backward_workspace_bytes": ([_I, _I], _Z),
+    "mesa_residual_norm_backward": ([_P, _I, _P, _I, _P, _P, _F, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
     "mesa_profile_enable": ([_I], _I),
     "mesa_profile_read": ([_I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)], _I),
     "mesa_profile_reset": ([], _I),
@@ -408,6 +420,203 @@ def mesa_hawk_scan(x, ga, gx, lam, c=8.0, h0=None, *, out=None, return_final=Fal
                               _stream(stream))
     _check(st, "mesa_hawk_scan")
     return (out, hf) if return_final else out
+
+
+def _on(dev, stream):
+    """The context in which a call allocates and enqueues: the tensors' device,
+    and `stream` when one is given (which then owns what is allocated)."""
+    import torch
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, expected {dev}")
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _bytes(workspace, nbytes, dev):
+    """(workspace, its size): the caller's, checked, or a new one."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, dev)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _delta_checks(q, k, v, gamma, beta, state, lead, **more):
+    """Shapes, dtypes and devices of a delta-rule call whose tensors are
+    [lead..., ...]: (B, H) and T tokens, or (N, H) of one token.  Returns (B,
+    Hk, H, T, dk, dv); `more` holds (tensor, shape of its last axes, dtype)."""
+    import torch
+    nd = 4 if lead == "T" else 3
+    B, Hk, *t, dk = _dims(q, "q", nd)
+    H, dv = _dims(v, "v", nd)[1], v.shape[-1]
+    _shapes((k, "k", (B, Hk, *t, dk)), (v, "v", (B, H, *t, dv)), (gamma, "gamma", (B, H, *t)), (beta, "beta", (B, H, *t)),
+            *_given((state, "state", (B, H, dv, dk))), *_given(*((x, n, (B, H, *t, dv) if s == "out" else (B, H, dv, dk))
+                                                             for n, (x, s) in more.items())))
+    if H % Hk:
+        raise ValueError(f"{H} value heads are not a multiple of {Hk} key heads")
+    _qkv_dtype(q)
+    f32 = torch.float32
+    for x, n, dt in ((q, "q", q.dtype), (k, "k", q.dtype), (v, "v", q.dtype), (gamma, "gamma", f32), (beta, "beta", f32),
+                     (state, "state", f32), *((x, n, q.dtype if s == "out" else f32) for n, (x, s) in more.items())):
+        if x is not None:
+            _need(x, n, dt, q.device)
+    return B, Hk, H, t[0] if t else 1, dk, dv
+
+
+def mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype) -> int:
+    return int(lib().mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype))
+
+
+def mesa_delta_forward(q, k, v, gamma, beta, state=None, *, out=None, return_final=False, final_state=None,
+                       workspace=None, stream=None):
+    """Gated delta rule over a sequence (see include/mesa.h, mesa_delta_forward).
+
+    q, k: [B,Hk,T,dk]; v: [B,H,T,dv] (float32 or bfloat16, same dtype; H a
+    multiple of Hk); gamma, beta: [B,H,T] float32; state: [B,H,dv,dk] float32
+    or None.  Returns (out [B,H,T,dv] in q's dtype, final_state [B,H,dv,dk] or
+    None); final_state may be the state passed in.
+    """
+    import torch
+    B, Hk, H, T, dk, dv = _delta_checks(q, k, v, gamma, beta, state, "T", out=(out, "out"),
+                                        final_state=(final_state, "state"))
+    dev, dt = q.device, _qkv_dtype(q)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((B, H, T, dv), dtype=q.dtype, device=dev)
+        if return_final and final_state is None:
+            final_state = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
+        workspace, nbytes = _bytes(workspace, mesa_delta_workspace_bytes(B, H, T, dk, dv, dt), dev)
+        st = lib().mesa_delta_forward(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(gamma), _ptr(beta), _ptr(state), B, Hk, H, T,
+                                      dk, dv, _ptr(out), _ptr(final_state), _ptr(workspace), nbytes, _stream(None))
+    _check(st, "mesa_delta_forward")
+    return out, final_state
+
+
+def mesa_delta_step(q, k, v, gamma, beta, state, *, out=None, stream=None):
+    """One token of the gated delta rule (see include/mesa.h, mesa_delta_step);
+    state [N,H,dv,dk] float32 is updated in place.
+
+    q, k: [N,Hk,dk]; v: [N,H,dv]; gamma, beta: [N,H].  Returns out [N,H,dv].
+    """
+    import torch
+    N, Hk, H, _, dk, dv = _delta_checks(q, k, v, gamma, beta, state, "", out=(out, "out"))
+    with _on(q.device, stream):
+        if out is None:
+            out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        st = lib().mesa_delta_step(_ptr(q), _ptr(k), _ptr(v), _qkv_dtype(q), _ptr(gamma), _ptr(beta), _ptr(state), N, Hk,
+                                   H, dk, dv, _ptr(out), _stream(None))
+    _check(st, "mesa_delta_step")
+    return out
+
+
+def _gate_checks(x, gate, w, grad_y=None, y=None, dtype=None):
+    import torch
+    B, H, T, d = _dims(x, "x", 4)
+    rows = (B, T, H, d)
+    _shapes((w, "w", (H, d)), *_given((gate, "gate", rows), (grad_y, "grad_y", rows), (y, "y", rows)))
+    dtype = next((t.dtype for t in (gate, grad_y, y) if t is not None), x.dtype if dtype is None else dtype)
+    _need(x, "x", None, None)
+    _qkv_dtype(x)
+    for t, n, dt in ((gate, "gate", dtype), (w, "w", torch.float32), (grad_y, "grad_y", dtype), (y, "y", dtype)):
+        if t is not None:
+            _need(t, n, dt, x.device)
+    return B, H, T, d, dtype
+
+
+def mesa_gate_norm(x, gate, w, eps=1e-6, *, out=None, out_dtype=None, stream=None):
+    """Per-head RMS norm of a layer's outputs times silu(gate) (see include/mesa.h, mesa_gate_norm).
+
+    x: [B,H,T,d]; gate: [B,T,H,d] or None; w: [H,d] float32.  Returns y
+    [B,T,H,d] in gate's dtype (without a gate out_dtype, default x's).
+    """
+    import torch
+    B, H, T, d, dtype = _gate_checks(x, gate, w, y=out, dtype=out_dtype)
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty((B, T, H, d), dtype=dtype, device=x.device)
+        st = lib().mesa_gate_norm(_ptr(x), _qkv_dtype(x), _ptr(gate), _qkv_dtype(out), _ptr(w), float(eps), B, H, T, d,
+                                  _ptr(out), _stream(None))
+    _check(st, "mesa_gate_norm")
+    return out
+
+
+def mesa_gate_norm_backward(x, gate, w, grad_y, eps=1e-6, *, workspace=None, stream=None):
+    """Gradients of mesa_gate_norm from its inputs and grad_y [B,T,H,d].
+    Returns a dict of grad_x, grad_gate (None without a gate) and grad_w."""
+    import torch
+    B, H, T, d, dtype = _gate_checks(x, gate, w, grad_y=grad_y)
+    dev = x.device
+    with _on(dev, stream):
+        g = dict(grad_x=torch.empty_like(x), grad_gate=None if gate is None else torch.empty_like(gate),
+                 grad_w=torch.empty((H, d), dtype=torch.float32, device=dev))
+        workspace, nbytes = _bytes(workspace, int(lib().mesa_gate_norm_backward_workspace_bytes(B, H, T, d)), dev)
+        st = lib().mesa_gate_norm_backward(_ptr(x), _qkv_dtype(x), _ptr(gate), _qkv_dtype(grad_y), _ptr(w), float(eps),
+                                           _ptr(grad_y), B, H, T, d, _ptr(g["grad_x"]), _ptr(g["grad_gate"]),
+                                           _ptr(g["grad_w"]), _ptr(workspace), nbytes, _stream(None))
+    _check(st, "mesa_gate_norm_backward")
+    return g
+
+
+def _residual_checks(h, y, w, scale, grad_n=None, grad_h_out=None, n=None, h_out=None, dtype=None):
+    import torch
+    R, D = _dims(h, "h", 2)
+    _shapes((w, "w", (D,)), *_given((y, "y", (R, D)), (scale, "scale", (D,)), (grad_n, "grad_n", (R, D)),
+                                    (grad_h_out, "grad_h_out", (R, D)), (n, "n", (R, D)), (h_out, "h_out", (R, D))))
+    if y is None and (scale is not None or h_out is not None):
+        raise ValueError("scale and h_out need y")
+    dtype = next((t.dtype for t in (y, grad_n, n) if t is not None), h.dtype if dtype is None else dtype)
+    _need(h, "h", None, None)
+    _qkv_dtype(h)
+    f32 = torch.float32
+    for t, name, dt in ((y, "y", dtype), (w, "w", f32), (scale, "scale", f32), (grad_n, "grad_n", dtype),
+                        (grad_h_out, "grad_h_out", h.dtype), (n, "n", dtype), (h_out, "h_out", h.dtype)):
+        if t is not None:
+            _need(t, name, dt, h.device)
+    return R, D, dtype
+
+
+def mesa_residual_norm(h, y, w, scale=None, eps=1e-6, *, h_out=None, n=None, out_dtype=None, stream=None):
+    """Residual addition with its scale, and the next block's RMS norm (see
+    include/mesa.h, mesa_residual_norm).
+
+    h: [R,D] residual; y: [R,D] block output or None; w, scale: [D] float32.
+    Returns (h_out = h + scale y in h's dtype, n in y's dtype); without y, (h,
+    its norm in out_dtype, default h's).  h_out may be h itself.
+    """
+    import torch
+    R, D, dtype = _residual_checks(h, y, w, scale, n=n, h_out=h_out, dtype=out_dtype)
+    dev = h.device
+    with _on(dev, stream):
+        if n is None:
+            n = torch.empty((R, D), dtype=dtype, device=dev)
+        if y is not None and h_out is None:
+            h_out = torch.empty_like(h)
+        st = lib().mesa_residual_norm(_ptr(h), _qkv_dtype(h), _ptr(y), _qkv_dtype(n), _ptr(scale), _ptr(w), float(eps),
+                                      R, D, _ptr(h_out), _ptr(n), _stream(None))
+    _check(st, "mesa_residual_norm")
+    return (h if y is None else h_out), n
+
+
+def mesa_residual_norm_backward(h, y, w, grad_n, scale=None, eps=1e-6, *, grad_h_out=None, workspace=None, stream=None):
+    """Gradients of mesa_residual_norm from its inputs, grad_n and grad_h_out
+    (the residual's gradient from what follows, or None).  Returns a dict of
+    grad_h, grad_y, grad_w and grad_scale (None where the input is)."""
+    import torch
+    R, D, dtype = _residual_checks(h, y, w, scale, grad_n=grad_n, grad_h_out=grad_h_out)
+    dev = h.device
+    with _on(dev, stream):
+        f32 = dict(dtype=torch.float32, device=dev)
+        g = dict(grad_h=torch.empty_like(h), grad_y=None if y is None else torch.empty_like(y),
+                 grad_w=torch.empty((D,), **f32), grad_scale=None if scale is None else torch.empty((D,), **f32))
+        workspace, nbytes = _bytes(workspace, int(lib().mesa_residual_norm_backward_workspace_bytes(R, D)), dev)
+        st = lib().mesa_residual_norm_backward(_ptr(h), _qkv_dtype(h), _ptr(y), _qkv_dtype(grad_n), _ptr(scale), _ptr(w),
+                                               float(eps), _ptr(grad_n), _ptr(grad_h_out), R, D, _ptr(g["grad_h"]),
+                                               _ptr(g["grad_y"]), _ptr(g["grad_w"]), _ptr(g["grad_scale"]),
+                                               _ptr(workspace), nbytes, _stream(None))
+    _check(st, "mesa_residual_norm_backward")
+    return g
 
 
 def profile_enable(on: bool = True):

@@ -1,0 +1,218 @@
+"""The gated delta rule on the GPU (mesa_delta_forward, mesa_delta_step)
+against its token-by-token float64 form, at the sizes where a chunked kernel
+can go wrong.  The bounds are derived in tests/delta_helpers.py."""
+import sys
+
+import numpy as np
+import pytest
+
+from tests.delta_helpers import F32, delta_inputs, delta_ref, rel, tol
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+def dev(t):
+    return {n: None if x is None else x.cuda() for n, x in t.items()}
+
+
+def forward(t, **kw):
+    import torch
+    from test_regression_amd import mesa
+    d = dev(t)
+    out, final = mesa.mesa_delta_forward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], d["state"], return_final=True, **kw)
+    torch.cuda.synchronize()
+    return out.double().cpu().numpy(), final.double().cpu().numpy()
+
+
+def check(t, f, dtype):
+    o, S = forward(t)
+    ro, rS = delta_ref(f)
+    eo, eS = rel(o, ro), rel(S, rS)
+    say(f"  rel_l2 out={eo:.2e} final={eS:.2e}")
+    assert eo <= tol(dtype) and eS <= F32
+    return o, S
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 15, 64, 65, 130, 300])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (32, 64), (64, 32), (128, 128), (64, 256), (128, 16)])
+def test_delta_forward_shapes(dk, dv, T, dtype):
+    seed = 100 + dk + dv + T
+    say("case delta", dict(dk=dk, dv=dv, T=T, dtype=dtype, seed=seed))
+    check(*delta_inputs(seed, 2, 2, 2, T, dk, dv, dtype, start=T % 2 == 0), dtype)
+
+
+@pytest.mark.parametrize("B,Hk,H,T", [(1, 1, 1, 77), (1, 1, 3, 200), (3, 2, 6, 129), (2, 5, 5, 64), (1, 9, 9, 33)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_delta_forward_heads(B, Hk, H, T, dtype):
+    say("case delta heads", (B, Hk, H, T, dtype))
+    check(*delta_inputs(7 + T, B, Hk, H, T, 64, 128, dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_delta_forward_long(dtype):
+    say("case delta long", dtype)
+    check(*delta_inputs(11, 1, 2, 2, 2000, 128, 64, dtype, lo=0.97), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("what", ["strong", "none", "full", "still", "same_keys", "orthogonal", "tiny", "huge", "zeros",
+                                  "reset"])
+def test_delta_forward_hard_inputs(what, dtype):
+    import torch
+    say("case delta hard", what, dtype)
+    t, f = delta_inputs(23, 1, 2, 2, 200, 64, 64, dtype)
+
+    def put(name, fn):
+        x = t[name].clone()
+        fn(x)
+        t[name], f[name] = x, x.double().numpy()
+    if what == "strong":      # decays that underflow over a chunk
+        put("gamma", lambda x: x.copy_(torch.rand_like(x) * 0.1 + 1e-4))
+    elif what == "none":      # no decay, full writes
+        put("gamma", lambda x: x.fill_(1.0))
+        put("beta", lambda x: x.fill_(1.0))
+    elif what == "full":
+        put("beta", lambda x: x.fill_(1.0))
+    elif what == "still":     # nothing is written: the state only decays
+        put("beta", lambda x: x.zero_())
+    elif what == "same_keys":  # every token rewrites the same entry
+        put("beta", lambda x: x.fill_(1.0))
+        put("k", lambda x: x.copy_(x[:, :, :1].expand_as(x).clone()))
+    elif what == "orthogonal":
+        put("k", lambda x: x.copy_(torch.eye(64)[torch.arange(200) % 64].expand_as(x)))
+    elif what == "tiny":
+        for n in ("v", "state"):
+            put(n, lambda x: x.mul_(2.0 ** -60))
+    elif what == "huge":
+        for n in ("v", "state"):
+            put(n, lambda x: x.mul_(2.0 ** 60))
+    elif what == "zeros":     # rows of zeros among the keys and queries
+        put("k", lambda x: x[:, :, ::3].zero_())
+        put("q", lambda x: x[:, :, 1::3].zero_())
+    elif what == "reset":     # a gate of 0 forgets everything before it
+        put("gamma", lambda x: x.index_fill_(2, torch.tensor([0, 70, 71, 128]), 0.0))
+    o, S = check(t, f, dtype)
+    if what == "reset":
+        # what follows the reset at 128 is the rule from nothing
+        t2 = {n: (x[:, :, 128:].contiguous() if x is not None and n != "state" else None) for n, x in t.items()}
+        o2, S2 = forward(t2)
+        assert rel(o[:, :, 128:], o2) <= tol(dtype) and rel(S, S2) <= F32
+
+
+def test_delta_forward_bf16_rounds_the_float_result():
+    """The bf16 call's outputs are the float32 call's on the same values within
+    the documented 11-bit products and one rounding, element by element."""
+    say("case delta bf16 against f32")
+    t, _ = delta_inputs(31, 1, 2, 2, 256, 128, 128, "bf16")
+    o, S = forward(t)
+    o2, S2 = forward({n: None if x is None else x.float() for n, x in t.items()})
+    assert rel(S, S2) <= F32
+    # two products of 11-bit operands, each term off by at most 3 2^-12; a
+    # row's terms sum to at most |q| |S| + ... < 8 times the largest output
+    assert np.abs(o - o2).max() <= (2.0 ** -8 + 8 * 3 * 2.0 ** -12) * np.abs(o2).max()
+
+
+def test_delta_pieces_equal_the_whole_and_padding_is_inert():
+    import torch
+    say("case delta pieces")
+    t, f = delta_inputs(41, 2, 2, 4, 230, 64, 64, "f32")
+    o, S = check(t, f, "f32")
+    cut = lambda a, b: {n: x if n == "state" else x[:, :, a:b].contiguous() for n, x in t.items()}  # noqa: E731
+    o1, S1 = forward(cut(0, 100))
+    rest = cut(100, 230)
+    rest["state"] = torch.from_numpy(S1).float()
+    o2, S2 = forward(rest)
+    assert rel(np.concatenate([o1, o2], 2), o) <= F32 and rel(S2, S) <= F32
+    # padded behind the end with gate 1 and strength 0: the state stays
+    pad = {n: x if n == "state" else torch.cat([x, x[:, :, :37]], 2) for n, x in t.items()}
+    pad["gamma"][:, :, 230:] = 1.0
+    pad["beta"][:, :, 230:] = 0.0
+    op, Sp = forward(pad)
+    assert rel(op[:, :, :230], o) <= F32 and rel(Sp, S) <= F32
+
+
+def test_delta_forward_no_tokens_in_place_state_and_repeat():
+    import torch
+    from test_regression_amd import mesa
+    say("case delta no tokens")
+    t, f = delta_inputs(51, 1, 2, 2, 90, 32, 32, "bf16")
+    d = dev(t)
+    e = {n: x if n == "state" else x[:, :, :0].contiguous() for n, x in d.items()}
+    out, S = mesa.mesa_delta_forward(e["q"], e["k"], e["v"], e["gamma"], e["beta"], d["state"], return_final=True)
+    assert out.shape == (1, 2, 0, 32) and torch.equal(S, d["state"])
+    _, S = mesa.mesa_delta_forward(e["q"], e["k"], e["v"], e["gamma"], e["beta"], return_final=True)
+    assert bool((S == 0).all())
+    # the final state over the initial one; the same call twice gives the same bits
+    a = mesa.mesa_delta_forward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], d["state"], return_final=True)
+    s = d["state"].clone()
+    b = mesa.mesa_delta_forward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], s, final_state=s)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], s)
+
+
+def test_delta_forward_writes_only_its_outputs():
+    import torch
+    from test_regression_amd import mesa
+    say("case delta guards")
+    t, _ = delta_inputs(61, 2, 1, 2, 70, 64, 32, "bf16")
+    d = dev(t)
+    big = torch.full((2 * 2 * 70 * 32 + 256,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = big[128:128 + 2 * 2 * 70 * 32].view(2, 2, 70, 32)
+    nbytes = mesa.mesa_delta_workspace_bytes(2, 2, 70, 64, 32, mesa.MESA_DTYPE_BF16)
+    ws = torch.full((nbytes + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+    r, _ = mesa.mesa_delta_forward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], d["state"], out=out,
+                                   workspace=ws[256:256 + nbytes])
+    torch.cuda.synchronize()
+    ref, _ = mesa.mesa_delta_forward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], d["state"])
+    assert torch.equal(r, ref)
+    assert bool((big[:128] == 7).all()) and bool((big[-128:] == 7).all())
+    assert bool((ws[:256] == 0x5a).all()) and bool((ws[-256:] == 0x5a).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,Hk,H,dk,dv", [(1, 1, 1, 16, 16), (1, 4, 4, 64, 64), (3, 2, 6, 32, 128), (2, 3, 3, 128, 256),
+                                          (5, 1, 2, 16, 32), (130, 16, 16, 128, 128), (7, 1, 1, 64, 16)])
+def test_delta_step(N, Hk, H, dk, dv, dtype):
+    import torch
+    from test_regression_amd import mesa
+    say("case delta step", (N, Hk, H, dk, dv, dtype))
+    t, f = delta_inputs(71 + N, N, Hk, H, 1, dk, dv, dtype)
+    d = dev(t)
+    one = {n: x if n == "state" else x[:, :, 0].contiguous() for n, x in d.items()}
+    out = mesa.mesa_delta_step(one["q"], one["k"], one["v"], one["gamma"], one["beta"], one["state"])
+    torch.cuda.synchronize()
+    ro, rS = delta_ref(f)
+    # sums of at most 128 float terms: 2 log2(128) + 4 roundings of 2^-24 each, twice
+    bound = 36 * 2.0 ** -24
+    assert rel(one["state"].double().cpu(), rS) <= bound
+    assert rel(out.double().cpu(), ro[:, :, 0]) <= bound + (2.0 ** -8 if dtype == "bf16" else 0.0)
+
+
+def test_prompt_then_tokens():
+    """A prompt through the sequence call, then tokens one at a time on its final state."""
+    import torch
+    from test_regression_amd import mesa
+    say("case delta prompt then tokens")
+    t, f = delta_inputs(81, 2, 2, 4, 140, 64, 128, "f32")
+    d = dev(t)
+    p = {n: x if n == "state" else x[:, :, :128].contiguous() for n, x in d.items()}
+    out, S = mesa.mesa_delta_forward(p["q"], p["k"], p["v"], p["gamma"], p["beta"], p["state"], return_final=True)
+    outs = [out]
+    for i in range(128, 140):
+        one = {n: d[n][:, :, i].contiguous() for n in ("q", "k", "v", "gamma", "beta")}
+        outs.append(mesa.mesa_delta_step(one["q"], one["k"], one["v"], one["gamma"], one["beta"], S)[:, :, None])
+    torch.cuda.synchronize()
+    ro, rS = delta_ref(f)
+    assert rel(torch.cat(outs, 2).double().cpu(), ro) <= F32 and rel(S.double().cpu(), rS) <= F32
