@@ -363,6 +363,27 @@ mesa_status mesa_delta_forward(const void *q, const void *k, const void *v, int 
                                size_t workspace_bytes, void *stream);
 
 /*
+ * Gradients of the gated delta rule, from the forward's inputs (the chunk
+ * states are formed again), for L = <out, grad_out> + <final_state, grad_final>:
+ *   grad_out   [B, H, T, dv]    dtype
+ *   grad_final [B, H, dv, dk]   float32, or NULL for zeros
+ *   grad_q, grad_k [B, Hk, T, dk], grad_v [B, H, T, dv]  dtype, written;
+ *                               shared heads' gradients are summed in float32
+ *   grad_gamma, grad_beta [B, H, T]  float32, written (grad_gamma is written 0
+ *                               where gamma is 0)
+ *   grad_state [B, H, dv, dk]   float32 gradient of state0, or NULL; may be
+ *                               grad_final itself
+ *   workspace                   at least mesa_delta_backward_workspace_bytes(...)
+ * Sums are taken in a fixed order: results do not change from run to run.
+ */
+size_t mesa_delta_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype);
+mesa_status mesa_delta_backward(const void *q, const void *k, const void *v, int dtype, const float *gamma,
+                                const float *beta, const float *state0, const void *grad_out,
+                                const float *grad_final, int B, int Hk, int H, int T, int dk, int dv,
+                                void *grad_q, void *grad_k, void *grad_v, float *grad_gamma, float *grad_beta,
+                                float *grad_state, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * One token of the gated delta rule for N sequences, states updated in place:
  *   q, k [N, Hk, dk], v [N, H, dv] dtype; gamma, beta [N, H] float32;
  *   state [N, H, dv, dk] float32 in/out; out [N, H, dv] dtype.

@@ -128,4 +128,38 @@ __device__ __forceinline__ f16x8 col_operand(const uint32_t* P, int pitch, int i
     return f16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
+// 16-byte pieces of `PLANES` 64 x 64 planes on their way into LDS.
+template <int PLANES>
+struct PlaneUnits {
+    static constexpr int n = PLANES * 2;
+    u32x4 raw[n];
+    __device__ __forceinline__ void load(const uint16_t* img) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) raw[i] = reinterpret_cast<const u32x4*>(img)[threadIdx.x + 256 * i];
+    }
+    __device__ __forceinline__ void store(uint32_t (&P)[PLANES][kDC * kDP]) const {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const int u = threadIdx.x + 256 * i;   // plane u / 512, row (u / 8) % 64, piece u % 8
+            *reinterpret_cast<u32x4*>(&P[i / 2][(u / 8 % kDC) * kDP + 4 * (u % 8)]) = raw[i];
+        }
+    }
+};
+
+// The column's operands of a block of NT accumulator tiles: scaled so that
+// the largest magnitude lands in [2^14, 2^15), split in hi and lo; returns
+// the scale's inverse.
+template <int NT>
+__device__ __forceinline__ float column_operands(const f32x4 (&X)[NT], f16x8 (&H)[NT / 2], f16x8 (&L)[NT / 2]) {
+    const int E = h2_exp(kslot_max(absmax(X)));
+    const float s = pow2(E);
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j) h2_split(X[2 * j], X[2 * j + 1], s, H[j], L[j]);
+    return pow2(-E);
+}
+
+__device__ __forceinline__ f32x4 row4(const float* sc, int i, int g) {
+    return *reinterpret_cast<const f32x4*>(sc + 16 * i + 4 * g);
+}
+
 }  // namespace mesa

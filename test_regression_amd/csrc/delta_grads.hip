@@ -1,0 +1,457 @@
+// delta_grads.hip -- the gated delta rule's gradients per chunk (gfx950).
+//
+// With a chunk's start state S, the gradient dS' of its end state, E and dV
+// from the two passes over the chunks (delta_core.h's notation, all 64 x dv,
+// dv x dk or dk x dv as their products need):
+//   Y = dO E^T,  Z = dV E^T            (64 x 64, contracted over dv)
+//   oS = dO S^T, rS = dV S^T, W = E dS'^T   (64 x dk)
+//   dQ = G oS + (D.Y b) K
+//   dK = D_C b W - G rS + (D.Y b)^T Q - (D.Z b) K - (D.Z b)^T K
+//   db_j = D_Cj k_j.W_j + sum_i (P_ij Y_ij - A_ij Z_ij)
+// where D is cut to j <= i with Y and to j < i with Z, and b scales columns.
+// The gate of token t scales every product of a token j < t with one i >= t,
+// and the state that crosses t:
+//   dg_t g_t = sum_{i >= t > j} b_j (P_ij Y_ij - A_ij Z_ij)
+//              + sum_{i >= t} G_i (q_i.oS_i - k_i.rS_i)
+//              + sum_{j < t} b_j D_Cj k_j.W_j + G_C <S, dS'>
+// summed over the pairs that cross t, not as a difference of row and column
+// sums, which would cancel.
+//
+// One workgroup of four waves per chunk and head; wave w owns tokens
+// 16 w .. 16 w + 15 as rows.  First the products over dv, 32 columns of dv at a
+// time through LDS (token rows scaled each, states per block); then, with K, Q
+// and the decayed Y, Z in LDS, the products over the chunk's tokens.  All
+// operands are 22-bit splits (bf16 rows are exact in one part).
+#include "delta_core.h"
+
+namespace mesa {
+
+constexpr int kVW = 24;   // words per LDS row of 32 dv columns
+
+template <int DKP, int NP>
+struct alignas(16) GradsLds {
+    static constexpr int KW = delta_row_words(DKP);
+    union {
+        struct {
+            uint32_t V[3][2][kDC * kVW];   // dO, dV, E rows
+            uint32_t S[2][2][32 * KW];     // S, dS' rows (dv)
+        };
+        struct {
+            uint32_t K[NP][kDC * KW];
+            uint32_t Q[NP][kDC * KW];
+            union {
+                struct {
+                    uint32_t Y[2][kDC * kDP];
+                    uint32_t Z[2][kDC * kDP];
+                };
+                float X[kDC * kDF];
+            };
+        };
+    };
+    double L[kDC];
+    float beta[kDC], G[kDC], end[kDC];
+    float vs[3][kDC];          // 2^-E of the token rows
+    float read[kDC], write[kDC];
+    float col[4][kDC], cross[4][kDC];
+    float red[8][4];           // per-wave maxima and sums
+};
+
+// Eight elements of a 64 x 32 block of rows of pitch dv, scaled by the row's
+// own power of two into fp16 planes.
+__device__ __forceinline__ void stage_row8(const f32x8& x, uint32_t (&P)[2][kDC * kVW], float* inv) {
+    const int row = threadIdx.x / 4, q = threadIdx.x % 4;
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x.v[e]));
+    m = fmaxf(m, __shfl_xor(m, 1, 64));
+    m = fmaxf(m, __shfl_xor(m, 2, 64));
+    const int E = h2_exp(m);
+    if (q == 0) inv[row] = pow2(-E);
+    f16x8 hi, lo;
+    h2_split(f32x4{x.v[0], x.v[1], x.v[2], x.v[3]}, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]}, pow2(E), hi, lo);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int at = row * kVW + perm32(8 * q + 4 * half) / 2;
+        *reinterpret_cast<f16x4*>(&P[0][at]) = f16x4{hi[4 * half], hi[4 * half + 1], hi[4 * half + 2], hi[4 * half + 3]};
+        *reinterpret_cast<f16x4*>(&P[1][at]) = f16x4{lo[4 * half], lo[4 * half + 1], lo[4 * half + 2], lo[4 * half + 3]};
+    }
+}
+
+// hi hi + hi lo + lo hi; AP: whether A has a lo part.
+template <bool AP, bool BP>
+__device__ __forceinline__ f32x4 product(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4 t) {
+    if constexpr (BP) t = mfma_f16x32(ah, bl, t);
+    if constexpr (AP) t = mfma_f16x32(al, bh, t);
+    return mfma_f16x32(ah, bh, t);
+}
+
+template <int DKP, typename In>
+__global__ __launch_bounds__(256) void delta_grads_kernel(DeltaBwdArgs b) {
+    constexpr int NP = delta_planes<In>(), NJ = DKP / 32, NS = DKP / 16, KW = delta_row_words(DKP);
+    constexpr bool F = NP == 2;   // rows stored as float: two parts
+    __shared__ GradsLds<DKP, NP> L;
+    const DeltaArgs& a = b.f;
+    const int lane = threadIdx.x % 64, w = threadIdx.x / 64, n = lane & 15, g = lane >> 4;
+    const int c = (int)(blockIdx.x % a.nc);
+    const long bh = blockIdx.x / a.nc;
+    const long bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
+    const int valid = min(kDC, a.T - c * kDC);
+    const size_t tok = (size_t)bh * a.T + (size_t)c * kDC;
+    const size_t ktok = ((size_t)bk * a.T + (size_t)c * kDC) * a.dk;
+    const size_t vo = (size_t)blockIdx.x * kDC * a.dv, so = (size_t)blockIdx.x * a.dv * a.dk;
+    const f32x4 zero{0.f, 0.f, 0.f, 0.f};
+    float gate = 1.f;
+    if (w == 0) {
+        gate = lane < valid ? a.gamma[tok + lane] : 1.f;
+        double x = fmax(log((double)gate), -200.0);
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double t = __shfl_up(x, o, 64);
+            if (lane >= o) x += t;
+        }
+        L.L[lane] = x;
+        L.beta[lane] = lane < valid ? a.beta[tok + lane] : 0.f;
+        L.G[lane] = expf((float)x);
+        L.end[lane] = expf((float)(__shfl(x, 63, 64) - x));
+    }
+    // ---- products over dv ----
+    f32x4 Y[4], Z[4], oS[NS], rS[NS], W[NS];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) Y[j] = Z[j] = zero;
+#pragma unroll
+    for (int m = 0; m < NS; ++m) oS[m] = rS[m] = W[m] = zero;
+    float carry = 0.f;   // this thread's share of <S, dS'>
+    for (int v0 = 0; v0 < a.dv; v0 += 32) {
+        {
+            const int row = threadIdx.x / 4, vc = v0 + 8 * (threadIdx.x % 4);
+            f32x8 o{}, r{}, e{};
+            if (vc < a.dv) {
+                if (row < valid) o = load8(static_cast<const In*>(b.grad_out) + (tok + row) * a.dv + vc);
+                r = load8(b.dR + vo + (size_t)row * a.dv + vc);
+                e = load8(a.E + vo + (size_t)row * a.dv + vc);
+            }
+            constexpr int per_row = DKP / 8, units = 32 * per_row, SU = (units + 255) / 256;
+            f32x8 s[SU], d[SU];
+            float ms = 0.f, md = 0.f;
+#pragma unroll
+            for (int i = 0; i < SU; ++i) {
+                const int u = threadIdx.x + 256 * i, vr = v0 + u / per_row, kc = 8 * (u % per_row);
+                s[i] = d[i] = f32x8{};
+                if (u < units && vr < a.dv && kc < a.dk) {
+                    s[i] = load8(a.S + so + (size_t)vr * a.dk + kc);
+                    d[i] = load8(b.dS + so + (size_t)vr * a.dk + kc);
+                }
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    ms = fmaxf(ms, fabsf(s[i].v[x]));
+                    md = fmaxf(md, fabsf(d[i].v[x]));
+                    carry += s[i].v[x] * d[i].v[x];
+                }
+            }
+            ms = wave_max(ms);
+            md = wave_max(md);
+            __syncthreads();   // the previous block is read (and the first time L.L.. are written)
+            if (lane == 0) { L.red[0][w] = ms; L.red[1][w] = md; }
+            stage_row8(o, L.V[0], L.vs[0]);
+            stage_row8(r, L.V[1], L.vs[1]);
+            stage_row8(e, L.V[2], L.vs[2]);
+            __syncthreads();
+            ms = fmaxf(fmaxf(L.red[0][0], L.red[0][1]), fmaxf(L.red[0][2], L.red[0][3]));
+            md = fmaxf(fmaxf(L.red[1][0], L.red[1][1]), fmaxf(L.red[1][2], L.red[1][3]));
+            const float ss = pow2(h2_exp(ms)), sd = pow2(h2_exp(md));
+#pragma unroll
+            for (int i = 0; i < SU; ++i) {
+                const int u = threadIdx.x + 256 * i, kc = 8 * (u % per_row);
+                if (u >= units) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const f32x8& x = t ? d[i] : s[i];
+                    f16x8 hi, lo;
+                    h2_split(f32x4{x.v[0], x.v[1], x.v[2], x.v[3]}, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]}, t ? sd : ss, hi, lo);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int at = (u / per_row) * KW + perm32(kc + 4 * half) / 2;
+                        *reinterpret_cast<f16x4*>(&L.S[t][0][at]) = f16x4{hi[4 * half], hi[4 * half + 1], hi[4 * half + 2], hi[4 * half + 3]};
+                        *reinterpret_cast<f16x4*>(&L.S[t][1][at]) = f16x4{lo[4 * half], lo[4 * half + 1], lo[4 * half + 2], lo[4 * half + 3]};
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const float is = pow2(-h2_exp(fmaxf(fmaxf(L.red[0][0], L.red[0][1]), fmaxf(L.red[0][2], L.red[0][3]))));
+        const float id = pow2(-h2_exp(fmaxf(fmaxf(L.red[1][0], L.red[1][1]), fmaxf(L.red[1][2], L.red[1][3]))));
+        const f16x8 oh = row_operand(L.V[0][0], kVW, w, 0, n, g), ol = row_operand(L.V[0][1], kVW, w, 0, n, g);
+        const f16x8 rh = row_operand(L.V[1][0], kVW, w, 0, n, g), rl = row_operand(L.V[1][1], kVW, w, 0, n, g);
+        const f16x8 eh = row_operand(L.V[2][0], kVW, w, 0, n, g), el = row_operand(L.V[2][1], kVW, w, 0, n, g);
+        const f32x4 so4 = row4(L.vs[0], w, g), sr4 = row4(L.vs[1], w, g), se4 = row4(L.vs[2], w, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f16x8 bh_ = row_operand(L.V[2][0], kVW, j, 0, n, g), bl = row_operand(L.V[2][1], kVW, j, 0, n, g);
+            const f32x4 y = product<F, true>(oh, ol, bh_, bl, zero), z = product<true, true>(rh, rl, bh_, bl, zero);
+            const float se = L.vs[2][16 * j + n];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                Y[j][r] += y[r] * (so4[r] * se);
+                Z[j][r] += z[r] * (sr4[r] * se);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < NS; ++m) {
+            const f16x8 sh = col_operand(L.S[0][0], KW, m, 0, n, g), sl = col_operand(L.S[0][1], KW, m, 0, n, g);
+            const f16x8 dh = col_operand(L.S[1][0], KW, m, 0, n, g), dl = col_operand(L.S[1][1], KW, m, 0, n, g);
+            const f32x4 x = product<F, true>(oh, ol, sh, sl, zero), y = product<true, true>(rh, rl, sh, sl, zero);
+            const f32x4 z = product<true, true>(eh, el, dh, dl, zero);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                oS[m][r] += x[r] * (so4[r] * is);
+                rS[m][r] += y[r] * (sr4[r] * is);
+                W[m][r] += z[r] * (se4[r] * id);
+            }
+        }
+    }
+    // ---- K and Q, one scale each for the chunk ----
+    carry = wavesum(carry);
+    float ek, eq;   // 2^-EK, 2^-EQ
+    {
+        using Units = RowUnits<DKP, In>;
+        Units k, q;
+        k.load(static_cast<const In*>(a.k) + ktok, a.dk, valid);
+        q.load(static_cast<const In*>(a.q) + ktok, a.dk, valid);
+        float mk = 0.f, mq = 0.f;
+#pragma unroll
+        for (int i = 0; i < Units::n; ++i) {
+            mk = fmaxf(mk, k.absmax(i));
+            mq = fmaxf(mq, q.absmax(i));
+        }
+        mk = wave_max(mk);
+        mq = wave_max(mq);
+        if (lane == 0) { L.red[2][w] = mk; L.red[3][w] = mq; L.red[4][w] = carry; }
+        __syncthreads();   // maxima written, the dv blocks read
+        mk = fmaxf(fmaxf(L.red[2][0], L.red[2][1]), fmaxf(L.red[2][2], L.red[2][3]));
+        mq = fmaxf(fmaxf(L.red[3][0], L.red[3][1]), fmaxf(L.red[3][2], L.red[3][3]));
+        const int EK = h2_exp(mk), EQ = h2_exp(mq);
+        ek = pow2(-EK);
+        eq = pow2(-EQ);
+#pragma unroll
+        for (int i = 0; i < Units::n; ++i) {
+            k.template store<NP>(L.K, i, pow2(EK));
+            q.template store<NP>(L.Q, i, pow2(EQ));
+        }
+    }
+    __syncthreads();
+    // ---- A and P; what crosses; the decayed Y and Z ----
+    {
+        f16x8 kh[NJ], kl[NJ], qh[NJ], ql[NJ];
+#pragma unroll
+        for (int s = 0; s < NJ; ++s) {
+            kh[s] = row_operand(L.K[0], KW, w, s, n, g);
+            kl[s] = row_operand(L.K[NP - 1], KW, w, s, n, g);
+            qh[s] = row_operand(L.Q[0], KW, w, s, n, g);
+            ql[s] = row_operand(L.Q[NP - 1], KW, w, s, n, g);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f32x4 A = zero, P = zero;
+#pragma unroll
+            for (int s = 0; s < NJ; ++s) {
+                const f16x8 bh_ = row_operand(L.K[0], KW, j, s, n, g), bl = row_operand(L.K[NP - 1], KW, j, s, n, g);
+                A = product<F, F>(kh[s], kl[s], bh_, bl, A);
+                P = product<F, F>(qh[s], ql[s], bh_, bl, P);
+            }
+            const int cj = 16 * j + n;
+            const double Lj = L.L[cj];
+            const float bj = L.beta[cj];
+            float sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * w + 4 * g + r;
+                const float D = row >= cj ? expf((float)(L.L[row] - Lj)) : 0.f;
+                const float Ds = row > cj ? D : 0.f;
+                const float py = P[r] * (ek * eq) * D * Y[j][r], az = A[r] * (ek * ek) * Ds * Z[j][r];
+                sum += py - az;
+                L.X[row * kDF + cj] = row > cj ? bj * (py - az) : 0.f;
+                Y[j][r] *= D * bj;
+                Z[j][r] *= Ds * bj;
+            }
+            sum = kslot_sum(sum);
+            if (g == 0) L.col[w][cj] = sum;
+        }
+    }
+    // row dots with the keys and queries
+    {
+        f32x4 qo = zero, kr = zero, kw = zero;
+        const _Float16* Kh = reinterpret_cast<const _Float16*>(L.K[0]);
+        const _Float16* Qh = reinterpret_cast<const _Float16*>(L.Q[0]);
+        const _Float16* Kl = reinterpret_cast<const _Float16*>(L.K[NP - 1]);
+        const _Float16* Ql = reinterpret_cast<const _Float16*>(L.Q[NP - 1]);
+#pragma unroll
+        for (int m = 0; m < NS; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int at = (16 * w + 4 * g + r) * 2 * KW + perm32(16 * m + n);
+                float k = (float)Kh[at], q = (float)Qh[at];
+                if constexpr (F) { k += (float)Kl[at]; q += (float)Ql[at]; }
+                qo[r] += q * oS[m][r];
+                kr[r] += k * rS[m][r];
+                kw[r] += k * W[m][r];
+            }
+        const f32x4 G = row4(L.G, w, g), end = row4(L.end, w, g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float q1 = rowsum16(qo[r]) * eq, k1 = rowsum16(kr[r]) * ek, k2 = rowsum16(kw[r]) * ek;
+            if (n == 0) {
+                L.read[16 * w + 4 * g + r] = G[r] * (q1 - k1);
+                L.write[16 * w + 4 * g + r] = end[r] * k2;
+            }
+        }
+    }
+    const float my = wave_max(absmax(Y)), mz = wave_max(absmax(Z));
+    if (lane == 0) { L.red[5][w] = my; L.red[6][w] = mz; }
+    __syncthreads();
+    {
+        // lane t: sum over the wave's rows i >= t of the row's sum over j < t
+        float acc = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int row = 16 * w + i;
+            float x = lane ? L.X[row * kDF + lane - 1] : 0.f;
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const float t = __shfl_up(x, o, 64);
+                if (lane >= o) x += t;
+            }
+            if (row >= lane) acc += x;
+        }
+        L.cross[w][lane] = acc;
+    }
+    __syncthreads();   // X is read: Y and Z take its place
+    if (w == 0) {
+        const float wr = L.write[lane];
+        float rd = L.read[lane], before = L.beta[lane] * wr;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const float t = __shfl_down(rd, o, 64), u = __shfl_up(before, o, 64);
+            if (lane + o < 64) rd += t;
+            if (lane >= o) before += u;
+        }
+        before = __shfl_up(before, 1, 64);
+        if (lane == 0) before = 0.f;
+        const float state = L.G[kDC - 1] * ((L.red[4][0] + L.red[4][1]) + (L.red[4][2] + L.red[4][3]));
+        const float cross = (L.cross[0][lane] + L.cross[1][lane]) + (L.cross[2][lane] + L.cross[3][lane]);
+        const float cols = (L.col[0][lane] + L.col[1][lane]) + (L.col[2][lane] + L.col[3][lane]);
+        if (lane < valid) {
+            b.grad_beta[tok + lane] = wr + cols;
+            b.grad_gamma[tok + lane] = gate > 0.f ? (cross + rd + before + state) / gate : 0.f;
+        }
+    }
+    float ey, ez;
+    {
+        const int EY = h2_exp(fmaxf(fmaxf(L.red[5][0], L.red[5][1]), fmaxf(L.red[5][2], L.red[5][3])));
+        const int EZ = h2_exp(fmaxf(fmaxf(L.red[6][0], L.red[6][1]), fmaxf(L.red[6][2], L.red[6][3])));
+        ey = pow2(-EY);
+        ez = pow2(-EZ);
+        const float sy = pow2(EY), sz = pow2(EZ);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int at = (16 * w + 4 * g + r) * 2 * kDP + perm32(16 * j + n);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float x = t ? Z[j][r] * sz : Y[j][r] * sy;
+                    const _Float16 hi = (_Float16)x;
+                    reinterpret_cast<_Float16*>(t ? L.Z[0] : L.Y[0])[at] = hi;
+                    reinterpret_cast<_Float16*>(t ? L.Z[1] : L.Y[1])[at] = (_Float16)(x - (float)hi);
+                }
+            }
+    }
+    __syncthreads();
+    // ---- products over the tokens ----
+    f16x8 yh[2], yl[2], zh[2], zl[2], yth[2], ytl[2], zth[2], ztl[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        yh[j] = row_operand(L.Y[0], kDP, w, j, n, g);
+        yl[j] = row_operand(L.Y[1], kDP, w, j, n, g);
+        zh[j] = row_operand(L.Z[0], kDP, w, j, n, g);
+        zl[j] = row_operand(L.Z[1], kDP, w, j, n, g);
+        yth[j] = col_operand(L.Y[0], kDP, w, j, n, g);
+        ytl[j] = col_operand(L.Y[1], kDP, w, j, n, g);
+        zth[j] = col_operand(L.Z[0], kDP, w, j, n, g);
+        ztl[j] = col_operand(L.Z[1], kDP, w, j, n, g);
+    }
+    const f32x4 G = row4(L.G, w, g), end = row4(L.end, w, g), be = row4(L.beta, w, g);
+    const size_t ho = (tok + 16 * w + 4 * g) * a.dk + n, ko = ktok + (size_t)(16 * w + 4 * g) * a.dk + n;
+#pragma unroll
+    for (int m = 0; m < NS; ++m) {
+        f32x4 tq = zero, tk = zero, tz = zero;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const f16x8 kh = col_operand(L.K[0], KW, m, j, n, g), qh = col_operand(L.Q[0], KW, m, j, n, g);
+            f16x8 kl = kh, ql = qh;
+            if constexpr (F) {
+                kl = col_operand(L.K[1], KW, m, j, n, g);
+                ql = col_operand(L.Q[1], KW, m, j, n, g);
+            }
+            tq = product<true, F>(yh[j], yl[j], kh, kl, tq);
+            tk = product<true, F>(yth[j], ytl[j], qh, ql, tk);
+            tz = product<true, F>(zh[j], zl[j], kh, kl, tz);
+            tz = product<true, F>(zth[j], ztl[j], kh, kl, tz);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (16 * w + 4 * g + r >= valid || 16 * m >= a.dk) continue;
+            const float dq = G[r] * oS[m][r] + tq[r] * (ey * ek);
+            const float dk = end[r] * be[r] * W[m][r] - G[r] * rS[m][r] + tk[r] * (ey * eq) - tz[r] * (ez * ek);
+            if (b.part) {
+                b.part[ho + (size_t)r * a.dk + 16 * m] = dq;
+                b.part[(size_t)a.BH * a.T * a.dk + ho + (size_t)r * a.dk + 16 * m] = dk;
+            } else {
+                store1(static_cast<In*>(b.grad_q) + ko + (size_t)r * a.dk + 16 * m, dq);
+                store1(static_cast<In*>(b.grad_k) + ko + (size_t)r * a.dk + 16 * m, dk);
+            }
+        }
+    }
+}
+
+// grad_q and grad_k of a key head: the sum over its value heads, in order.
+// A thread takes four consecutive features.
+template <typename In>
+__global__ __launch_bounds__(256) void delta_head_sum_kernel(DeltaBwdArgs b, long quads) {
+    const DeltaArgs& a = b.f;
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= quads) return;
+    const long per = (long)a.T * a.dk / 4;   // of a head
+    const long head = i / per, at = i % per;
+    const int rep = a.H / a.Hk;
+    const float* p = b.part + 4 * ((head / a.Hk * a.H + head % a.Hk * rep) * per + at);
+    f32x4 q{0.f, 0.f, 0.f, 0.f}, k = q;
+    for (int r = 0; r < rep; ++r) {
+        q += load4(p + 4 * r * per);
+        k += load4(p + 4 * (r * per + a.BH * per));
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        store1(static_cast<In*>(b.grad_q) + 4 * i + e, q[e]);
+        store1(static_cast<In*>(b.grad_k) + 4 * i + e, k[e]);
+    }
+}
+
+template <int DKP>
+hipError_t grads_go(const DeltaBwdArgs& b, hipStream_t s) {
+    const dim3 grid((unsigned)(b.f.BH * b.f.nc));
+    if (b.f.bf16) hipLaunchKernelGGL((delta_grads_kernel<DKP, bf16_t>), grid, dim3(256), 0, s, b);
+    else hipLaunchKernelGGL((delta_grads_kernel<DKP, float>), grid, dim3(256), 0, s, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_delta_grads(const DeltaBwdArgs& b, hipStream_t s) {
+    hipError_t e = b.f.dk <= 32 ? grads_go<32>(b, s) : b.f.dk == 64 ? grads_go<64>(b, s) : grads_go<128>(b, s);
+    if (e != hipSuccess || !b.part) return e;
+    const long quads = b.f.BH / b.f.H * b.f.Hk * b.f.T * b.f.dk / 4;
+    const dim3 grid((unsigned)((quads + 255) / 256));
+    if (b.f.bf16) hipLaunchKernelGGL(delta_head_sum_kernel<bf16_t>, grid, dim3(256), 0, s, b, quads);
+    else hipLaunchKernelGGL(delta_head_sum_kernel<float>, grid, dim3(256), 0, s, b, quads);
+    return hipGetLastError();
+}
+
+}  // namespace mesa

@@ -12,7 +12,8 @@
 // blocks below by diagonals, M_ij = -M_ii sum_{j<=k<i} (A diag b)_ik M_kj, on
 // float MFMAs whose accumulator order is the next product's operand order.
 // M is kept to 22 bits (its errors reach the state); P to 11 for bf16
-// outputs, whose own rounding is 8 times coarser, and to 22 for float ones.
+// outputs, whose own rounding is 8 times coarser, and to 22 for float ones and
+// for the gradients (those of the gates are float32 sums over P).
 #include "delta_core.h"
 
 namespace mesa {
@@ -53,7 +54,7 @@ __device__ __forceinline__ void planes_out(const float* F, uint16_t* img, float*
     }
 }
 
-template <int DKP, typename In>
+template <int DKP, typename In, int PP>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     constexpr int NP = delta_planes<In>(), NJ = DKP / 32, KW = delta_row_words(DKP);
     __shared__ PrepLds<DKP, NP> L;
@@ -200,10 +201,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int r = 0; r < 4; ++r) L.N[(16 * w + 4 * g + r) * kDF + 16 * j + n] = P[j][r];
-    uint16_t* img = a.img + (size_t)blockIdx.x * ((2 + NP) * kDC * kDC);
+    uint16_t* img = a.img + (size_t)blockIdx.x * ((2 + PP) * kDC * kDC);
     planes_out<2>(L.M, img, L.mi);
     __syncthreads();
-    planes_out<NP>(L.N, img + 2 * kDC * kDC, L.pi);
+    planes_out<PP>(L.N, img + 2 * kDC * kDC, L.pi);
     __syncthreads();
     if (threadIdx.x < kDC) {
         const int t = threadIdx.x;
@@ -225,8 +226,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 template <int DKP>
 hipError_t prep_go(const DeltaArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.BH * a.nc));
-    if (a.bf16) hipLaunchKernelGGL((delta_prep_kernel<DKP, bf16_t>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((delta_prep_kernel<DKP, float>), grid, dim3(256), 0, s, a);
+    if (!a.bf16) hipLaunchKernelGGL((delta_prep_kernel<DKP, float, 2>), grid, dim3(256), 0, s, a);
+    else if (a.p_planes == 2) hipLaunchKernelGGL((delta_prep_kernel<DKP, bf16_t, 2>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((delta_prep_kernel<DKP, bf16_t, 1>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

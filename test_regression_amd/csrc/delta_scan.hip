@@ -28,40 +28,6 @@ struct alignas(16) ScanLds {
     float sc[kScal];
 };
 
-// 16-byte pieces of `PLANES` 64 x 64 planes on their way into LDS.
-template <int PLANES>
-struct PlaneUnits {
-    static constexpr int n = PLANES * 2;
-    u32x4 raw[n];
-    __device__ __forceinline__ void load(const uint16_t* img) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) raw[i] = reinterpret_cast<const u32x4*>(img)[threadIdx.x + 256 * i];
-    }
-    __device__ __forceinline__ void store(uint32_t (&P)[PLANES][kDC * kDP]) const {
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const int u = threadIdx.x + 256 * i;   // plane u / 512, row (u / 8) % 64, piece u % 8
-            *reinterpret_cast<u32x4*>(&P[i / 2][(u / 8 % kDC) * kDP + 4 * (u % 8)]) = raw[i];
-        }
-    }
-};
-
-// The column's operands of a block of NT accumulator tiles: scaled so that
-// the largest magnitude lands in [2^14, 2^15), split in hi and lo; returns
-// the scale's inverse.
-template <int NT>
-__device__ __forceinline__ float column_operands(const f32x4 (&X)[NT], f16x8 (&H)[NT / 2], f16x8 (&L)[NT / 2]) {
-    const int E = h2_exp(kslot_max(absmax(X)));
-    const float s = pow2(E);
-#pragma unroll
-    for (int j = 0; j < NT / 2; ++j) h2_split(X[2 * j], X[2 * j + 1], s, H[j], L[j]);
-    return pow2(-E);
-}
-
-__device__ __forceinline__ f32x4 row4(const float* sc, int i, int g) {
-    return *reinterpret_cast<const f32x4*>(sc + 16 * i + 4 * g);
-}
-
 // OUT: write O.  SAVE: write each chunk's start state and E (the backward's
 // recomputation).
 template <int DKP, typename In, bool OUT, bool SAVE>
@@ -80,7 +46,8 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a) {
     const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
     const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + col;
     In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col : nullptr;
-    const uint16_t* img = a.img + (size_t)bh * a.nc * ((2 + NP) * kDC * kDC);
+    const size_t image = (size_t)(2 + a.p_planes) * kDC * kDC;
+    const uint16_t* img = a.img + (size_t)bh * a.nc * image;
     const float* scal = a.scal + (size_t)bh * a.nc * kScal;
     const size_t so = ((size_t)bh * a.dv + col) * a.dk + 4 * g;   // this lane's row of the (dv x dk) state
     const f32x4 zero{0.f, 0.f, 0.f, 0.f};
@@ -107,8 +74,8 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a) {
             ksr[i] = sc[kKs + Units::row(i)];
             if constexpr (OUT) qsr[i] = sc[kQs + Units::row(i)];
         }
-        mr.load(img + (size_t)c * ((2 + NP) * kDC * kDC));
-        if constexpr (OUT) pr.load(img + (size_t)c * ((2 + NP) * kDC * kDC) + 2 * kDC * kDC);
+        mr.load(img + c * image);
+        if constexpr (OUT) pr.load(img + c * image + 2 * kDC * kDC);
         if (threadIdx.x < kScal / 4) scr = load4(sc + 4 * threadIdx.x);
         const In* vp = Vp + (size_t)c * kDC * a.dv;
 #pragma unroll

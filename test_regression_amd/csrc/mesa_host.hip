@@ -608,11 +608,94 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
     uint16_t* img = static_cast<uint16_t*>(workspace);
     float* scal = reinterpret_cast<float*>(img + (size_t)BH * nc * delta_image_halfs(dtype));
     const mesa::DeltaArgs a{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
-                            out, final_state, img, scal, nullptr, nullptr};
+                            out, final_state, img, scal, dtype == MESA_DTYPE_BF16 ? 1 : 2, nullptr, nullptr};
     hipError_t e = timed_launch(MESA_KERNEL_DELTA_PREP, s, [&] { return mesa::launch_delta_prep(a, s); });
     if (e != hipSuccess) return hip_fail(e, "delta chunk-matrix kernel launch");
     e = timed_launch(MESA_KERNEL_DELTA_SCAN, s, [&] { return mesa::launch_delta_scan(a, s); });
     if (e != hipSuccess) return hip_fail(e, "delta scan kernel launch");
+    return MESA_OK;
+}
+
+// Backward workspace, offsets in bytes (every segment a multiple of 16).
+struct DeltaBwdLayout {
+    size_t scal, S, dS, E, dR, part, total;
+};
+static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int dv) {
+    const size_t n = (size_t)B * H * delta_chunks(T), C = mesa::kDeltaChunk;
+    DeltaBwdLayout l{};
+    size_t o = n * delta_image_halfs(MESA_DTYPE_F32) * 2;   // two planes of M and of P for either type
+    l.scal = o; o += n * mesa::kDeltaScal * sizeof(float);
+    l.S = o;    o += n * dv * dk * sizeof(float);
+    l.dS = o;   o += n * dv * dk * sizeof(float);
+    l.E = o;    o += n * C * dv * sizeof(float);
+    l.dR = o;   o += n * C * dv * sizeof(float);
+    l.part = o; o += H != Hk ? 2 * (size_t)B * H * T * dk * sizeof(float) : 0;
+    l.total = o;
+    return l;
+}
+
+size_t mesa_delta_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype) {
+    if (B <= 0 || Hk <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
+    return delta_bwd_layout(B, Hk, H, T, dk, dv).total;
+}
+
+mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int dtype, const float* gamma,
+                                const float* beta, const float* state0, const void* grad_out,
+                                const float* grad_final, int B, int Hk, int H, int T, int dk, int dv, void* grad_q,
+                                void* grad_k, void* grad_v, float* grad_gamma, float* grad_beta, float* grad_state,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    const mesa_status st = delta_checks(dtype, B, Hk, H, T, dk, dv);
+    if (st != MESA_OK) return st;
+    if (T > 0 && (!q || !k || !v || !gamma || !beta || !grad_out || !grad_q || !grad_k || !grad_v || !grad_gamma ||
+                  !grad_beta || !workspace))
+        return fail(MESA_ERR_INVALID_ARGUMENT,
+                    "q, k, v, gamma, beta, grad_out, their gradients and workspace must be non-null");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(state0, 16) || !aligned(grad_out, 16) ||
+        !aligned(grad_final, 16) || !aligned(grad_q, 16) || !aligned(grad_k, 16) || !aligned(grad_v, 16) ||
+        !aligned(grad_state, 16) || !aligned(workspace, 16) || !aligned(gamma, 4) || !aligned(beta, 4) ||
+        !aligned(grad_gamma, 4) || !aligned(grad_beta, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT,
+                    "misaligned pointer (16 B for tensors/workspace, 4 B for gamma/beta and their gradients)");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const long BH = (long)B * H, nc = delta_chunks(T);
+    if (T == 0) {
+        const hipError_t e = copy_or_zero(grad_state, grad_final, (size_t)BH * dv * dk, s);
+        if (e != hipSuccess) return hip_fail(e, "state gradient for T = 0");
+        return MESA_OK;
+    }
+    const void* ins[] = {q, k, v, grad_out};
+    const void* outs[] = {grad_q, grad_k, grad_v};
+    for (const void* o : outs)
+        for (const void* i : ins)
+            if (o == i) return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
+    const DeltaBwdLayout l = delta_bwd_layout(B, Hk, H, T, dk, dv);
+    if (workspace_bytes < l.total)
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, l.total);
+    char* ws = static_cast<char*>(workspace);
+    auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
+    mesa::DeltaBwdArgs a{};
+    a.f = mesa::DeltaArgs{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
+                          nullptr, nullptr, reinterpret_cast<uint16_t*>(ws), at(l.scal), 2, at(l.S), at(l.E)};
+    a.grad_out = grad_out;
+    a.grad_final = grad_final;
+    a.grad_q = grad_q;
+    a.grad_k = grad_k;
+    a.grad_v = grad_v;
+    a.grad_gamma = grad_gamma;
+    a.grad_beta = grad_beta;
+    a.grad_state = grad_state;
+    a.dS = at(l.dS);
+    a.dR = at(l.dR);
+    a.part = H != Hk ? at(l.part) : nullptr;
+    hipError_t e = timed_launch(MESA_KERNEL_DELTA_PREP, s, [&] { return mesa::launch_delta_prep(a.f, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta chunk-matrix kernel launch");
+    e = timed_launch(MESA_KERNEL_DELTA_SCAN, s, [&] { return mesa::launch_delta_states(a.f, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta scan kernel launch");
+    e = timed_launch(MESA_KERNEL_DELTA_BWD_SCAN, s, [&] { return mesa::launch_delta_bwd_scan(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta backward scan kernel launch");
+    e = timed_launch(MESA_KERNEL_DELTA_GRADS, s, [&] { return mesa::launch_delta_grads(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta gradient kernel launch");
     return MESA_OK;
 }
 

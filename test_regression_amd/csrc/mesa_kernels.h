@@ -101,8 +101,18 @@ struct DeltaArgs {
     long BH; int Hk; int H; int T; int dk; int dv; int nc; int bf16;
     void* out; float* final_state;
     uint16_t* img; float* scal;   // workspace: per head and chunk the planes of M and P, the scalars
+    int p_planes;                 // planes of P in img: 1 (bf16 forward) or 2
     float* S; float* E;           // backward workspace: chunk start states [BH][nc][dv][dk], E [BH][nc][64][dv]
 };
+struct DeltaBwdArgs {
+    DeltaArgs f;                  // q, k, v, gamma, beta, state0, sizes, img, scal, S, E
+    const void* grad_out; const float* grad_final;
+    void* grad_q; void* grad_k; void* grad_v; float* grad_gamma; float* grad_beta; float* grad_state;
+    float* dS; float* dR;         // workspace: gradients of the chunks' end states, of v in float (both as S and E)
+    float* part;                  // workspace: dq, then dk of each value head [2][BH][T][dk] (H != Hk), else nullptr
+};
+hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& a, hipStream_t s);
+hipError_t launch_delta_grads(const DeltaBwdArgs& a, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E

@@ -47,6 +47,9 @@ SIGNATURES = {
     "mesa_hawk_scan": ([_P, _P, _P, _I, _P, _F, _P, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
     "mesa_delta_workspace_bytes": ([_I, _I, _I, _I, _I, _I], _Z),
     "mesa_delta_forward": ([_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "mesa_delta_backward_workspace_bytes": ([_I] * 7, _Z),
+    "mesa_delta_backward": ([_P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
+                             _P, _Z, _P], _I),
     "mesa_delta_step": ([_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P], _I),
     "mesa_gate_norm": ([_P, _I, _P, _I, _P, _F, _I, _I, _I, _I, _P, _P], _I),
     "mesa_gate_norm_backward_workspace_bytes": ([_I, _I, _I, _I], _Z),
@@ -492,6 +495,34 @@ def mesa_delta_forward(q, k, v, gamma, beta, state=None, *, out=None, return_fin
                                       dk, dv, _ptr(out), _ptr(final_state), _ptr(workspace), nbytes, _stream(None))
     _check(st, "mesa_delta_forward")
     return out, final_state
+
+
+def mesa_delta_backward_workspace_bytes(B, Hk, H, T, dk, dv, dtype) -> int:
+    return int(lib().mesa_delta_backward_workspace_bytes(B, Hk, H, T, dk, dv, dtype))
+
+
+def mesa_delta_backward(q, k, v, gamma, beta, grad_out, state=None, *, grad_final=None, workspace=None, stream=None):
+    """Gradients of mesa_delta_forward (see include/mesa.h, mesa_delta_backward).
+
+    grad_out: [B,H,T,dv] in q's dtype; grad_final: [B,H,dv,dk] float32 or
+    None.  Returns a dict of grad_q, grad_k [B,Hk,T,dk], grad_v (q's dtype),
+    grad_gamma, grad_beta and grad_state (float32; None without a state).
+    """
+    import torch
+    B, Hk, H, T, dk, dv = _delta_checks(q, k, v, gamma, beta, state, "T", grad_out=(grad_out, "out"),
+                                        grad_final=(grad_final, "state"))
+    dev, dt = q.device, _qkv_dtype(q)
+    with _on(dev, stream):
+        g = dict(grad_q=torch.empty_like(q), grad_k=torch.empty_like(k), grad_v=torch.empty_like(v),
+                 grad_gamma=torch.empty_like(gamma), grad_beta=torch.empty_like(beta),
+                 grad_state=None if state is None else torch.empty_like(state))
+        workspace, nbytes = _bytes(workspace, mesa_delta_backward_workspace_bytes(B, Hk, H, T, dk, dv, dt), dev)
+        st = lib().mesa_delta_backward(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(gamma), _ptr(beta), _ptr(state),
+                                       _ptr(grad_out), _ptr(grad_final), B, Hk, H, T, dk, dv, _ptr(g["grad_q"]),
+                                       _ptr(g["grad_k"]), _ptr(g["grad_v"]), _ptr(g["grad_gamma"]), _ptr(g["grad_beta"]),
+                                       _ptr(g["grad_state"]), _ptr(workspace), nbytes, _stream(None))
+    _check(st, "mesa_delta_backward")
+    return g
 
 
 def mesa_delta_step(q, k, v, gamma, beta, state, *, out=None, stream=None):

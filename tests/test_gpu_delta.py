@@ -216,3 +216,137 @@ def test_prompt_then_tokens():
     torch.cuda.synchronize()
     ro, rS = delta_ref(f)
     assert rel(torch.cat(outs, 2).double().cpu(), ro) <= F32 and rel(S.double().cpu(), rS) <= F32
+
+
+def backward_errors(t, f, dtype, seed, with_final=True):
+    import torch
+    from test_regression_amd import mesa
+    rng = np.random.default_rng(seed)
+    d = dev(t)
+    go = torch.from_numpy(rng.standard_normal(t["v"].shape)).to(t["v"].dtype)
+    shape = f["state"].shape
+    gf = torch.from_numpy(0.3 * rng.standard_normal(shape)).float() if with_final else None
+    g = mesa.mesa_delta_backward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], go.cuda(), d["state"],
+                                 grad_final=None if gf is None else gf.cuda())
+    torch.cuda.synchronize()
+    _, _, ref = delta_ref(f, go.double().numpy(), None if gf is None else gf.double().numpy())
+    assert (g["grad_state"] is None) == (t["state"] is None)
+    got = {n: x.double().cpu().numpy() for n, x in g.items() if x is not None}
+    return {n: rel(x, ref[n]) for n, x in got.items()}, got, ref
+
+
+# Gradients: the backward's chain is the forward's and its own, twice the
+# products and inverses of the bound in delta_helpers; the roundings of
+# bfloat16 gradients come on top.
+GRAD_F32 = 2 * F32
+
+
+def grad_tol(name, dtype):
+    return GRAD_F32 + (2.0 ** -8 if dtype == "bf16" and name in ("grad_q", "grad_k", "grad_v") else 0.0)
+
+
+def check_grads(t, f, dtype, seed, with_final=True):
+    errs, got, ref = backward_errors(t, f, dtype, seed, with_final)
+    say("  " + " ".join(f"{n[5:]}={e:.1e}" for n, e in errs.items()))
+    for n, e in errs.items():
+        assert e <= grad_tol(n, dtype), n
+    return got, ref
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 15, 64, 65, 130, 300])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (32, 64), (64, 32), (128, 128), (64, 256), (128, 16)])
+def test_delta_backward_shapes(dk, dv, T, dtype):
+    seed = 300 + dk + dv + T
+    say("case delta backward", dict(dk=dk, dv=dv, T=T, dtype=dtype, seed=seed))
+    check_grads(*delta_inputs(seed, 2, 2, 2, T, dk, dv, dtype, start=T % 2 == 0), dtype, seed, T % 3 == 0)
+
+
+@pytest.mark.parametrize("B,Hk,H,T", [(1, 1, 1, 77), (1, 1, 3, 200), (3, 2, 6, 129), (1, 9, 9, 33)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_delta_backward_heads(B, Hk, H, T, dtype):
+    say("case delta backward heads", (B, Hk, H, T, dtype))
+    check_grads(*delta_inputs(17 + T, B, Hk, H, T, 64, 128, dtype), dtype, T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("what", ["strong", "none", "still", "same_keys", "zeros", "reset", "silent"])
+def test_delta_backward_hard_inputs(what, dtype):
+    import torch
+    say("case delta backward hard", what, dtype)
+    t, f = delta_inputs(29, 1, 2, 2, 200, 64, 64, dtype)
+
+    def put(name, fn):
+        x = t[name].clone()
+        fn(x)
+        t[name], f[name] = x, x.double().numpy()
+    if what == "strong":
+        put("gamma", lambda x: x.copy_(torch.rand_like(x) * 0.1 + 1e-2))
+    elif what == "none":
+        put("gamma", lambda x: x.fill_(1.0))
+        put("beta", lambda x: x.fill_(1.0))
+    elif what == "still":     # strength 0: its own gradient does not vanish
+        put("beta", lambda x: x[:, :, ::2].zero_())
+    elif what == "same_keys":
+        put("beta", lambda x: x.fill_(0.9))
+        put("k", lambda x: x.copy_(x[:, :, :1].expand_as(x).clone()))
+    elif what == "zeros":
+        put("k", lambda x: x[:, :, ::3].zero_())
+        put("q", lambda x: x[:, :, 1::3].zero_())
+    elif what == "reset":
+        put("gamma", lambda x: x.index_fill_(2, torch.tensor([70, 128]), 0.0))
+    elif what == "silent":    # values and start of zeros: only the values' gradients remain
+        put("v", lambda x: x.zero_())
+        put("state", lambda x: x.zero_())
+    if what in ("reset", "silent"):
+        errs, got, ref = backward_errors(t, f, dtype, 5)
+        if what == "reset":
+            at = np.array([70, 128])
+            assert (got["grad_gamma"][:, :, at] == 0).all()
+            got["grad_gamma"][:, :, at] = ref["grad_gamma"][:, :, at] = 0
+            assert rel(got["grad_gamma"], ref["grad_gamma"]) <= GRAD_F32
+            assert all(e <= grad_tol(n, dtype) for n, e in errs.items() if n != "grad_gamma"), errs
+        else:
+            for n in ("grad_q", "grad_k", "grad_gamma", "grad_beta"):
+                assert (got[n] == 0).all(), n
+            assert errs["grad_v"] <= grad_tol("grad_v", dtype) and errs["grad_state"] <= GRAD_F32
+    else:
+        check_grads(t, f, dtype, 5)
+
+
+def test_delta_backward_against_differences():
+    """The gradients of the GPU's own float32 forward, by central differences of
+    a projection of it in the float64 definition."""
+    say("case delta backward differences")
+    t, f = delta_inputs(91, 1, 1, 2, 70, 16, 16, "f32")
+    got, ref = check_grads(t, f, "f32", 91)
+    rng = np.random.default_rng(91)
+    go = rng.standard_normal(t["v"].shape).astype(np.float32).astype(np.float64)
+    gf = (0.3 * rng.standard_normal(f["state"].shape)).astype(np.float32).astype(np.float64)
+    for n in ("q", "k", "v", "gamma", "beta", "state"):
+        d = rng.standard_normal(f[n].shape)
+        h = 1e-5
+        vals = []
+        for s in (h, -h):
+            o, S = delta_ref({**f, n: f[n] + s * d})
+            vals.append((o * go).sum() + (S * gf).sum())
+        num, ana = (vals[0] - vals[1]) / (2 * h), float((got["grad_" + n] * d).sum())
+        # truncation h^2 and cancellation 1e-16 / h of sums of some thousand terms
+        assert abs(num - ana) <= 1e-4 * max(1.0, np.linalg.norm(ref["grad_" + n]) * np.linalg.norm(d) / np.sqrt(d.size))
+
+
+def test_delta_backward_no_tokens_repeat_and_in_place():
+    import torch
+    from test_regression_amd import mesa
+    say("case delta backward no tokens, repeat")
+    t, _ = delta_inputs(95, 1, 2, 4, 150, 32, 32, "bf16")
+    d = dev(t)
+    go, gf = torch.randn_like(d["v"]), torch.randn_like(d["state"])
+    args = (d["q"], d["k"], d["v"], d["gamma"], d["beta"], go, d["state"])
+    a = mesa.mesa_delta_backward(*args, grad_final=gf)
+    b = mesa.mesa_delta_backward(*args, grad_final=gf)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    e = [x[:, :, :0].contiguous() for x in args[:6]]
+    g = mesa.mesa_delta_backward(*e, d["state"], grad_final=gf)
+    assert torch.equal(g["grad_state"], gf) and g["grad_q"].shape == (1, 2, 0, 32)
