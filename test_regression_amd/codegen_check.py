@@ -153,6 +153,51 @@ def scan_inline_asm(text: str):
     return out
 
 
+# MFMAs written in asm (accumulator tied to the destination): the compiler
+# makes nothing wait for them either.
+#  - a VALU result needs VALU_TO_MFMA wait states before one reads it;
+#  - its result may only be touched by MFMAs that accumulate onto it for
+#    ASM_MFMA_RESULT wait states (the compiler leaves 8 after the 16x16x32
+#    fp16 MFMA).
+ASM_MFMA_RESULT = 8
+
+
+def scan_asm_mfma(text: str):
+    """Returns [(asm MFMA, offending instruction)] that break either rule above."""
+    ins = _instructions(text)
+    out = []
+    for i, (t, in_asm) in enumerate(ins):
+        if not in_asm or not t.startswith("v_mfma"):
+            continue
+        _, ops = _operand_regs(t)
+        read, dst = set().union(*ops[1:]), ops[0]
+        waits = 0
+        for u, _ in reversed(ins[:i]):
+            if waits >= VALU_TO_MFMA:
+                break
+            m, uops = _operand_regs(u)
+            if m.startswith("v_") and not m.startswith("v_mfma") and uops and uops[0] & read:
+                out.append((t, u))
+                break
+            waits += _wait_states(u)
+        waits = 0
+        for u, _ in ins[i + 1:]:
+            if waits >= ASM_MFMA_RESULT:
+                break
+            m, uops = _operand_regs(u)
+            if m.startswith("v_mfma"):
+                if uops[0] == dst:
+                    break        # accumulates onto it: judged from there
+                touched = set().union(*uops)
+            else:
+                touched = set().union(*uops) if uops else set()
+            if touched & dst:
+                out.append((t, u))
+                break
+            waits += _wait_states(u)
+    return out
+
+
 def loop_lds_waits(text: str, kernel_prefix: str, min_mfma: int = 100, max_mfma: int = 400):
     """The loops of one kernel that issue between min_mfma and max_mfma MFMAs
     per pass (in the CG kernels, each wave's iteration; the persistent loop
@@ -196,7 +241,7 @@ def compile_asm(src: str) -> str:
 
 def check_all(sources=None):
     """Compile each kernel source to gfx950 assembly; return {source: hazards},
-    the SrcC rewrites of scan_asm followed by the inline-asm findings."""
+    the SrcC rewrites of scan_asm followed by the two inline-asm scans' findings."""
     sources = sources or [s for s in B.SOURCES if s != "mesa_host.hip"]
     res = {}
     with tempfile.TemporaryDirectory() as td:
@@ -205,7 +250,7 @@ def check_all(sources=None):
             cmd = [B.HIPCC, *B.flags_for(src), "--cuda-device-only", "-S", os.path.join(B.CSRC, src), "-o", asm]
             subprocess.run(cmd, check=True, capture_output=True)
             text = open(asm).read()
-            res[src] = scan_asm(text) + scan_inline_asm(text)
+            res[src] = scan_asm(text) + scan_inline_asm(text) + scan_asm_mfma(text)
     return res
 
 

@@ -10,7 +10,7 @@
 // D_ij = G_i / G_j (j <= i):
 //   A_ij = D_ij k_i.k_j (j < i),  P_ij = D_ij q_i.k_j (j <= i)
 //   E = M (V - diag(G) K S),   M = (I + A diag(b))^-1  (unit lower triangular)
-//   O = diag(G) Q S + P diag(b) E
+//   O = diag(G) Q S + (P diag(b)) E
 //   S' = G_C S + (diag(D_C.) K)^T diag(b) E
 // M and P do not depend on the state: one kernel forms them for all chunks
 // at once (delta_prep.hip); the pass over the chunks (delta_scan.hip) is a
@@ -24,29 +24,97 @@
 #include "io8.h"
 #include "mesa_kernels.h"
 
+#include <type_traits>
+
 namespace mesa {
 
 constexpr int kDC = kDeltaChunk;   // tokens of a chunk
 constexpr int kDP = 40;     // words per LDS row of a 64 x 64 plane (fp16, columns perm32)
 constexpr int kDF = 68;     // floats per LDS row of a 64 x 64 float matrix
 
-// Per-chunk scalars in the workspace, 64 each: powers of two that scale the
-// key and query rows into fp16's range; the factors that undo row scales and
-// apply the gates.
+// Per-chunk scalars in the workspace: powers of two that scale the key and
+// query rows into fp16's range, and the factors that undo row scales and apply
+// the gates (64 values each, then single ones).
 enum DeltaScal {
     kKs = 0,      // 2^EK_t
     kQs = 64,     // 2^EQ_t
     kGk = 128,    // G_t 2^-EK_t
     kGq = 192,    // G_t 2^-EQ_t
-    kMi = 256,    // 2^-EM_t, the scale of row t of M undone
-    kPi = 320,    // 2^-EP_t, of row t of P
-    kDc = 384,    // D_Ct 2^-EK_t
-    kBe = 448,    // b_t
-    kGc = 512,    // G_C (one value)
+    kQi = 256,    // 2^-EQ_t; row t of P diag(b) is scaled by 2^(EQ_t + EP)
+    kDb = 320,    // D_Ct b_t 2^-EK_t
+    kBe = 384,    // b_t
+    kGc = 448,    // G_C
+    kMi = 449,    // 2^-EM, the scale of M undone
+    kPi = 450,    // 2^-EP
     kScal = kDeltaScal
 };
 
+// A plane of M or P diag(b) in the workspace holds 16-byte units of eight
+// columns (perm32): rows below 32 their first 32 columns, the others all 64;
+// what is above stays out, being zero in blocks that no product reads.
+constexpr int kPlaneUnits = kDeltaPlaneUnits;
+__device__ __forceinline__ int unit_row(int u) { return u < 128 ? u / 4 : 16 + u / 8; }
+__device__ __forceinline__ int unit_col(int u) { return u < 128 ? u % 4 : u % 8; }
+
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// p + a lane's byte offset: a scalar base and a 32-bit lane offset.
+template <typename T>
+__device__ __forceinline__ T* lane_at(T* p, uint32_t bytes) {
+    typedef std::conditional_t<std::is_const_v<T>, const char, char> byte;
+    return reinterpret_cast<T*>(reinterpret_cast<byte*>(p) + bytes);
+}
+
+// A loop counter the compiler cannot see through: addresses formed from it stay
+// a scalar base and a lane's 32-bit offset, where it would otherwise keep and
+// advance a 64-bit lane pointer for each of a chunk's loads and stores.
+__device__ __forceinline__ int opaque(int c) {
+    asm("" : "+s"(c));
+    return c;
+}
+
+// Eight floats, scaled by s (a power of two), rounded to fp16: one instruction each.
+__device__ __forceinline__ f16x8 h2_hi_mix(const f32x4& a, const f32x4& b, float s) {
+    uint32_t h0, h1, h2, h3;
+    asm("v_fma_mixlo_f16 %0, %4, %5, 0\n\t"
+        "v_fma_mixhi_f16 %0, %4, %6, 0\n\t"
+        "v_fma_mixlo_f16 %1, %4, %7, 0\n\t"
+        "v_fma_mixhi_f16 %1, %4, %8, 0\n\t"
+        "v_fma_mixlo_f16 %2, %4, %9, 0\n\t"
+        "v_fma_mixhi_f16 %2, %4, %10, 0\n\t"
+        "v_fma_mixlo_f16 %3, %4, %11, 0\n\t"
+        "v_fma_mixhi_f16 %3, %4, %12, 0\n\t"
+        "s_nop 1"
+        : "=&v"(h0), "=&v"(h1), "=&v"(h2), "=&v"(h3)
+        : "v"(s), "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "v"(b[0]), "v"(b[1]), "v"(b[2]), "v"(b[3]));
+    return __builtin_bit_cast(f16x8, u32x4{h0, h1, h2, h3});
+}
+
+// MFMAs with the accumulator tied to its destination, in vector registers.  The
+// compiler's own choice gives many of them a separate accumulator input, which
+// later instructions then overwrite while it is still read, or keeps the
+// accumulators in the other register file, at a copy for every value read and
+// written.  Inline asm is opaque to its hazard bookkeeping: mfma_ready() stands
+// between VALU writes of the accumulators and the first MFMA on them (two wait
+// states), mfma_done() between the last one and the first use of the results
+// (12; 8 are asked for); codegen_check.py checks the distances in the built
+// code.  Operands come from LDS or from the mix splits, which wait by themselves.
+__device__ __forceinline__ void mfma_acc(f32x4& c, f16x8 a, f16x8 b) {
+    asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+}
+// onto zero
+__device__ __forceinline__ void mfma_first(f32x4& c, f16x8 a, f16x8 b) {
+    asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
+}
+#define MESA_MFMA_FENCE(name, wait)                                                                                   \
+    __device__ __forceinline__ void name(f32x4 (&C)[2]) { asm(wait : "+v"(C[0]), "+v"(C[1])); }                       \
+    __device__ __forceinline__ void name(f32x4 (&C)[4]) { asm(wait : "+v"(C[0]), "+v"(C[1]), "+v"(C[2]), "+v"(C[3])); } \
+    __device__ __forceinline__ void name(f32x4 (&C)[8]) {                                                             \
+        asm(wait : "+v"(C[0]), "+v"(C[1]), "+v"(C[2]), "+v"(C[3]), "+v"(C[4]), "+v"(C[5]), "+v"(C[6]), "+v"(C[7]));   \
+    }
+MESA_MFMA_FENCE(mfma_ready, "s_nop 1")
+MESA_MFMA_FENCE(mfma_done, "s_nop 11")
+#undef MESA_MFMA_FENCE
 
 // Key planes: 1 where keys and queries are stored as bf16, else 2.
 template <typename In> constexpr int delta_planes() { return sizeof(In) == 2 ? 1 : 2; }
@@ -62,16 +130,17 @@ struct RowUnits {
     u32x4 raw[n][words / 4];
     static __device__ __forceinline__ int row(int i) { return (threadIdx.x + THREADS * i) / per_row; }
     static __device__ __forceinline__ int col(int i) { return 8 * ((threadIdx.x + THREADS * i) % per_row); }
-    // rows `valid` and up, and features dk and up, are zeros
+    // Rows `valid` and up repeat the last one: their gates and strengths make
+    // them inert (the strength is 0), so only their finiteness matters.
+    // Features dk and up are zeros.
     __device__ __forceinline__ void load(const In* p, int dk, int valid) {
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const int r = row(i), c = col(i);
+            const In* s = lane_at(p, ((uint32_t)min(row(i), valid - 1) * (DKP == 32 ? dk : DKP) + col(i)) * sizeof(In));
             u32x4 a{0u, 0u, 0u, 0u}, b = a;
-            if (r < valid && c < dk) {
-                const In* s = p + (size_t)r * dk + c;
-                a = *reinterpret_cast<const u32x4*>(s);
-                if constexpr (words == 8) b = *reinterpret_cast<const u32x4*>(s + 4);
+            if (DKP > 32 || col(i) < dk) {
+                a = reinterpret_cast<const u32x4*>(s)[0];
+                if constexpr (words == 8) b = reinterpret_cast<const u32x4*>(s)[1];
             }
             raw[i][0] = a;
             if constexpr (words == 8) raw[i][1] = b;
@@ -82,9 +151,29 @@ struct RowUnits {
         else return e % 2 ? __uint_as_float(raw[i][0][e / 2] & 0xffff0000u) : __uint_as_float(raw[i][0][e / 2] << 16);
     }
     __device__ __forceinline__ float absmax(int i) const {
-        float m = 0.f;
+        if constexpr (words == 4) {
+            // bf16 magnitudes order as their bit patterns
+            uint32_t m = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(get(i, e)));
+            for (int e = 0; e < 4; ++e) {
+                typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+                m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m),
+                                                                           __builtin_bit_cast(u16x2, raw[i][0][e] & 0x7fff7fffu)));
+            }
+            return __uint_as_float(max(m & 0xffff0000u, m << 16));
+        } else {
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(get(i, e)));
+            return m;
+        }
+    }
+    // the largest of a row's units, in every lane that holds one of them
+    static __device__ __forceinline__ float row_max(float m) {
+        m = fmaxf(m, dpp_f32<0xb1>(m));
+        m = fmaxf(m, dpp_f32<0x4e>(m));
+        if constexpr (per_row > 4) m = fmaxf(m, dpp_f32<0x141>(m));
+        if constexpr (per_row > 8) m = fmaxf(m, dpp_f32<0x140>(m));
         return m;
     }
     // into fp16 planes (hi, and lo where there are two), scaled by s
@@ -92,22 +181,17 @@ struct RowUnits {
     __device__ __forceinline__ void store(uint32_t (&P)[NP][kDC * delta_row_words(DKP)], int i, float s) const {
         uint32_t* d = &P[0][row(i) * delta_row_words(DKP)];
         const int c = col(i);
-        _Float16 hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float y = get(i, e) * s;
-            hi[e] = (_Float16)y;
-            lo[e] = (_Float16)(y - (float)hi[e]);
-        }
+        const f32x4 x{get(i, 0), get(i, 1), get(i, 2), get(i, 3)}, y{get(i, 4), get(i, 5), get(i, 6), get(i, 7)};
+        f16x8 hi, lo;
+        if constexpr (NP == 2) h2_split_mix(x, y, s, hi, lo);
+        else hi = h2_hi_mix(x, y, s);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int w = perm32(c + 4 * half) / 2;
-            const _Float16* h = hi + 4 * half;
-            *reinterpret_cast<f16x4*>(d + w) = f16x4{h[0], h[1], h[2], h[3]};
-            if constexpr (NP == 2) {
-                const _Float16* l = lo + 4 * half;
-                *reinterpret_cast<f16x4*>(&P[1][row(i) * delta_row_words(DKP)] + w) = f16x4{l[0], l[1], l[2], l[3]};
-            }
+            *reinterpret_cast<f16x4*>(d + w) = half ? __builtin_shufflevector(hi, hi, 4, 5, 6, 7) : __builtin_shufflevector(hi, hi, 0, 1, 2, 3);
+            if constexpr (NP == 2)
+                *reinterpret_cast<f16x4*>(&P[1][row(i) * delta_row_words(DKP)] + w) =
+                    half ? __builtin_shufflevector(lo, lo, 4, 5, 6, 7) : __builtin_shufflevector(lo, lo, 0, 1, 2, 3);
         }
     }
 };
@@ -128,38 +212,53 @@ __device__ __forceinline__ f16x8 col_operand(const uint32_t* P, int pitch, int i
     return f16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
 }
 
-// 16-byte pieces of `PLANES` 64 x 64 planes on their way into LDS.
-template <int PLANES>
+// The units of N planes on their way into LDS planes that follow each other.
+template <int N>
 struct PlaneUnits {
-    static constexpr int n = PLANES * 2;
+    static constexpr int total = N * kPlaneUnits, n = (total + 255) / 256;
     u32x4 raw[n];
+    static __device__ __forceinline__ bool has(int i) { return 256 * (i + 1) <= total || threadIdx.x + 256 * i < total; }
     __device__ __forceinline__ void load(const uint16_t* img) {
 #pragma unroll
-        for (int i = 0; i < n; ++i) raw[i] = reinterpret_cast<const u32x4*>(img)[threadIdx.x + 256 * i];
+        for (int i = 0; i < n; ++i)
+            if (has(i)) raw[i] = *lane_at(reinterpret_cast<const u32x4*>(img), 16 * (threadIdx.x + 256 * i));
     }
-    __device__ __forceinline__ void store(uint32_t (&P)[PLANES][kDC * kDP]) const {
+    __device__ __forceinline__ void store(uint32_t* P) const {
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const int u = threadIdx.x + 256 * i;   // plane u / 512, row (u / 8) % 64, piece u % 8
-            *reinterpret_cast<u32x4*>(&P[i / 2][(u / 8 % kDC) * kDP + 4 * (u % 8)]) = raw[i];
+            const int u = threadIdx.x + 256 * i, pl = u / kPlaneUnits, v = u % kPlaneUnits;
+            if (has(i)) *reinterpret_cast<u32x4*>(P + (pl * kDC + unit_row(v)) * kDP + 4 * unit_col(v)) = raw[i];
         }
     }
 };
 
-// The column's operands of a block of NT accumulator tiles: scaled so that
-// the largest magnitude lands in [2^14, 2^15), split in hi and lo; returns
-// the scale's inverse.
+// The column's operands of a block of NT accumulator tiles, scaled by 2^E and
+// split in hi and lo (or hi alone).
 template <int NT>
-__device__ __forceinline__ float column_operands(const f32x4 (&X)[NT], f16x8 (&H)[NT / 2], f16x8 (&L)[NT / 2]) {
-    const int E = h2_exp(kslot_max(absmax(X)));
+__device__ __forceinline__ int column_exp(const f32x4 (&X)[NT]) { return h2_exp(kslot_max(absmax(X))); }
+// X holds VALU results, or MFMA results from before the last barrier (h2_split_mix).
+template <int NT>
+__device__ __forceinline__ void column_split(const f32x4 (&X)[NT], int E, f16x8 (&H)[NT / 2], f16x8 (&L)[NT / 2]) {
     const float s = pow2(E);
 #pragma unroll
-    for (int j = 0; j < NT / 2; ++j) h2_split(X[2 * j], X[2 * j + 1], s, H[j], L[j]);
-    return pow2(-E);
+    for (int j = 0; j < NT / 2; ++j) h2_split_mix(X[2 * j], X[2 * j + 1], s, H[j], L[j]);
+}
+template <int NT>
+__device__ __forceinline__ void column_hi(const f32x4 (&X)[NT], int E, f16x8 (&H)[NT / 2]) {
+    const float s = pow2(E);
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j) H[j] = h2_hi_mix(X[2 * j], X[2 * j + 1], s);
 }
 
 __device__ __forceinline__ f32x4 row4(const float* sc, int i, int g) {
     return *reinterpret_cast<const f32x4*>(sc + 16 * i + 4 * g);
+}
+
+// Waves of a scan's workgroup that take columns: four, unless that leaves
+// compute units (256 of them) idle.
+inline int scan_waves(long BH, int dv) {
+    const long tiles = BH * (dv / 16);
+    return tiles <= 256 ? 1 : tiles <= 512 ? 2 : 4;
 }
 
 }  // namespace mesa

@@ -1,13 +1,17 @@
 // delta_prep.hip -- the state-free matrices of every chunk of the gated delta
-// rule (gfx950): M = (I + A diag(b))^-1 and P (delta_core.h), with the scales
-// and gate factors the passes over the chunks use.
+// rule (gfx950): M = (I + A diag(b))^-1 and P diag(b) (delta_core.h), with the
+// scales and gate factors the passes over the chunks use.
 //
-// One workgroup of four waves per chunk and head.  The decays are formed as
-// exp(L_i - L_j) from the chunk's prefix sums L of ln g in double: in float the
-// sums' rounding alone would put 1e-5 on the decays of a strongly gated chunk.
+// One workgroup of four waves per chunk and head.  The decays are
+// 2^(L_i - L_j) from the chunk's prefix sums L of log2 g in double: in float
+// the sums' rounding alone would put 1e-5 on the decays of a strongly gated
+// chunk.  A 16 x 16 block below the diagonal takes them as 2^(L_i - m)
+// 2^(m - L_j) with m at the end of the block's columns (both factors are at
+// most 1), so that a lane evaluates five exponentials and not sixteen.
 // Wave w forms the 16-row block w of K K^T and Q K^T (all four column blocks,
 // those above the diagonal being dropped: an accumulator that only some waves
-// use was kept in registers that the next MFMAs' inputs reuse too early).  M comes block by block in float: the four 16 x 16 diagonal
+// use was kept in registers that the next MFMAs' inputs reuse too early).
+// M comes block by block in float: the four 16 x 16 diagonal
 // blocks by forward substitution, one a wave with a column a lane, then the
 // blocks below by diagonals, M_ij = -M_ii sum_{j<=k<i} (A diag b)_ik M_kj, on
 // float MFMAs whose accumulator order is the next product's operand order.
@@ -26,31 +30,27 @@ struct alignas(16) PrepLds {
         uint32_t Q[NP][kDC * KW];
         float M[kDC * kDF];
     };
-    float N[kDC * kDF];   // A diag(b); after the inverse, P
+    float N[kDC * kDF];   // A diag(b); after the inverse, P diag(b)
     double L[kDC];
-    float beta[kDC], ks[kDC], qs[kDC], mi[kDC], pi[kDC];
+    float beta[kDC], ks[kDC], qs[kDC];
+    float rowf[4][kDC];   // 2^(L_i - L_{16j+15}) for row i below column block j
+    float colf[kDC];      // 2^(L_{16j+15} - L_col) in its own block j
+    float redm[4], redp[4];
 };
 
-// Rows of a float matrix in LDS as fp16 planes of perm32 rows in memory, each
-// row scaled by a power of two whose inverse goes to inv[row].
+// The units of a 64 x 64 float matrix in LDS, scaled by s, as fp16 planes in memory.
 template <int PLANES>
-__device__ __forceinline__ void planes_out(const float* F, uint16_t* img, float* inv) {
+__device__ __forceinline__ void planes_out(const float* F, uint16_t* img, float s) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int unit = threadIdx.x + 256 * h, row = unit / 8, q = unit % 8, b = q / 4, g = q % 4;
-        const f32x4 x = *reinterpret_cast<const f32x4*>(F + row * kDF + 32 * b + 4 * g);
-        const f32x4 y = *reinterpret_cast<const f32x4*>(F + row * kDF + 32 * b + 16 + 4 * g);
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m = fmaxf(m, fmaxf(fabsf(x[e]), fabsf(y[e])));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-        const int E = h2_exp(m);
+    for (int i = 0; i < 2; ++i) {
+        const int u = threadIdx.x + 256 * i;
+        if (i == 1 && u >= kPlaneUnits) break;
+        const int row = unit_row(u), q = unit_col(u);
+        const float* p = F + row * kDF + 32 * (q / 4) + 4 * (q % 4);
         f16x8 hi, lo;
-        h2_split(x, y, pow2(E), hi, lo);
-        *reinterpret_cast<f16x8*>(img + row * kDC + 8 * q) = hi;
-        if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(img + kDC * kDC + row * kDC + 8 * q) = lo;
-        if (q == 0) inv[row] = pow2(-E);
+        h2_split(load4(p), load4(p + 16), s, hi, lo);
+        *reinterpret_cast<f16x8*>(img + 8 * u) = hi;
+        if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(img + 8 * (kPlaneUnits + u)) = lo;
     }
 }
 
@@ -58,10 +58,10 @@ template <int DKP, typename In, int PP>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     constexpr int NP = delta_planes<In>(), NJ = DKP / 32, KW = delta_row_words(DKP);
     __shared__ PrepLds<DKP, NP> L;
-    const int lane = threadIdx.x % 64, w = threadIdx.x / 64, n = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), n = lane & 15, g = lane >> 4;
     const int c = (int)(blockIdx.x % a.nc);
-    const long bh = blockIdx.x / a.nc;
-    const long bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
+    const int bh = blockIdx.x / a.nc;
+    const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
     const int valid = min(kDC, a.T - c * kDC);
     const size_t tok = (size_t)bh * a.T + (size_t)c * kDC;
     const size_t ktok = ((size_t)bk * a.T + (size_t)c * kDC) * a.dk;
@@ -71,25 +71,21 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
         k.load(static_cast<const In*>(a.k) + ktok, a.dk, valid);
         q.load(static_cast<const In*>(a.q) + ktok, a.dk, valid);
         if (w == 0) {
-            // a gate of 0 (a reset) counts as e^-200, which is 0 in float
-            double x = lane < valid ? fmax(log((double)a.gamma[tok + lane]), -200.0) : 0.0;
+            // a gate of 0 (a reset) counts as 2^-200, which is 0 in float
+            const int t = min(lane, valid - 1);
+            const float ga = a.gamma[tok + t], be = a.beta[tok + t];
+            double x = lane < valid ? (double)fmaxf(logf(ga), -140.f) * 1.4426950408889634 : 0.0;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
-                const double t = __shfl_up(x, o, 64);
-                if (lane >= o) x += t;
+                const double t2 = __shfl_up(x, o, 64);
+                if (lane >= o) x += t2;
             }
             L.L[lane] = x;
-            L.beta[lane] = lane < valid ? a.beta[tok + lane] : 0.f;
+            L.beta[lane] = lane < valid ? be : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < Units::n; ++i) {
-            float mk = k.absmax(i), mq = q.absmax(i);
-#pragma unroll
-            for (int o = 1; o < Units::per_row; o <<= 1) {
-                mk = fmaxf(mk, __shfl_xor(mk, o, 64));
-                mq = fmaxf(mq, __shfl_xor(mq, o, 64));
-            }
-            const float sk = pow2(h2_exp(mk)), sq = pow2(h2_exp(mq));
+            const float sk = pow2(h2_exp(Units::row_max(k.absmax(i)))), sq = pow2(h2_exp(Units::row_max(q.absmax(i))));
             k.template store<NP>(L.K, i, sk);
             q.template store<NP>(L.Q, i, sq);
             if (Units::col(i) == 0) {
@@ -99,52 +95,80 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
         }
     }
     __syncthreads();
+    {
+        // lane (n, g) of wave w: row 16 w + n against column block g
+        const double x = L.L[16 * w + n], m = L.L[16 * min(g, w) + 15];
+        const float f = __builtin_amdgcn_exp2f((float)(g < w ? x - m : m - x));
+        if (g < w) L.rowf[g][16 * w + n] = f;
+        else if (g == w) L.colf[16 * w + n] = f;
+    }
     // ---- rows 16 w .. 16 w + 15 of K K^T and Q K^T ----
     const f32x4 zero{0.f, 0.f, 0.f, 0.f};
-    f32x4 P[4];
-    {
-        f32x4 A[4];
+    f32x4 P[4], A[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) A[j] = P[j] = zero;
+    for (int j = 0; j < 4; ++j) A[j] = P[j] = zero;
 #pragma unroll
-        for (int s = 0; s < NJ; ++s) {
-            const f16x8 kh = row_operand(L.K[0], KW, w, s, n, g), qh = row_operand(L.Q[0], KW, w, s, n, g);
-            f16x8 kl = kh, ql = qh;
-            if constexpr (NP == 2) {
-                kl = row_operand(L.K[1], KW, w, s, n, g);
-                ql = row_operand(L.Q[1], KW, w, s, n, g);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f16x8 bh_ = row_operand(L.K[0], KW, j, s, n, g);
-                A[j] = mfma_f16x32(kh, bh_, A[j]);
-                P[j] = mfma_f16x32(qh, bh_, P[j]);
-                if constexpr (NP == 2) {
-                    const f16x8 bl = row_operand(L.K[1], KW, j, s, n, g);
-                    A[j] = mfma_f16x32(kl, bh_, A[j]);
-                    P[j] = mfma_f16x32(ql, bh_, P[j]);
-                    A[j] = mfma_f16x32(kh, bl, A[j]);
-                    P[j] = mfma_f16x32(qh, bl, P[j]);
-                }
-            }
+    for (int s = 0; s < NJ; ++s) {
+        const f16x8 kh = row_operand(L.K[0], KW, w, s, n, g), qh = row_operand(L.Q[0], KW, w, s, n, g);
+        f16x8 kl = kh, ql = qh;
+        if constexpr (NP == 2) {
+            kl = row_operand(L.K[1], KW, w, s, n, g);
+            ql = row_operand(L.Q[1], KW, w, s, n, g);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int col = 16 * j + n;
-            const double Lj = L.L[col];
-            const float kj = 1.0f / L.ks[col], bj = L.beta[col];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * w + 4 * g + r;
-                const float D = row >= col ? expf((float)(L.L[row] - Lj)) : 0.f;
-                const float ki = 1.0f / L.ks[row], qi = 1.0f / L.qs[row];
-                P[j][r] = row >= col ? P[j][r] * kj * qi * D : 0.f;
-                L.N[row * kDF + col] = row > col ? A[j][r] * kj * ki * D * bj : 0.f;
+            const f16x8 bh_ = row_operand(L.K[0], KW, j, s, n, g);
+            A[j] = mfma_f16x32(kh, bh_, A[j]);
+            P[j] = mfma_f16x32(qh, bh_, P[j]);
+            if constexpr (NP == 2) {
+                const f16x8 bl = row_operand(L.K[1], KW, j, s, n, g);
+                A[j] = mfma_f16x32(kl, bh_, A[j]);
+                P[j] = mfma_f16x32(ql, bh_, P[j]);
+                A[j] = mfma_f16x32(kh, bl, A[j]);
+                P[j] = mfma_f16x32(qh, bl, P[j]);
             }
         }
     }
-    __syncthreads();   // Q is read: M takes its place
+    __syncthreads();   // the decay factors are written, Q is read: M takes its place
+    // P keeps the scale 2^EQ of its rows, which bounds it next to the queries
+    {
+        const int r0 = 16 * w + 4 * g;
+        const f32x4 ks = load4(L.ks + r0);
+        f32x4 ki;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) ki[r] = 1.0f / ks[r];
+        float mp = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int col = 16 * j + n;
+            const float f = L.beta[col] / L.ks[col];
+            f32x4 D;
+            if (j < w) {
+                const f32x4 rf = load4(L.rowf[j] + r0);
+                const float cf = L.colf[col] * f;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) D[r] = rf[r] * cf;
+            } else if (j == w) {
+                const double Lc = L.L[col];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    D[r] = r0 + r >= col ? __builtin_amdgcn_exp2f((float)(L.L[r0 + r] - Lc)) * f : 0.f;
+            } else {
+                D = zero;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                P[j][r] *= D[r];
+                mp = fmaxf(mp, fabsf(P[j][r]));
+                L.N[(r0 + r) * kDF + col] = r0 + r > col ? A[j][r] * ki[r] * D[r] : 0.f;
+            }
+        }
+        mp = wave_max(mp);
+        if (lane == 0) L.redp[w] = mp;
+    }
+    __syncthreads();
     // ---- M's diagonal blocks; zeros above the diagonal ----
+    float mm = 0.f;
     {
         const float* Nd = L.N + 16 * w * kDF + 16 * w;
         float x[16];
@@ -153,7 +177,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
             float s0 = i == n ? 1.f : 0.f, s1 = 0.f;
 #pragma unroll
             for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
-                const f32x4 r = *reinterpret_cast<const f32x4*>(Nd + i * kDF + 4 * j4);
+                const f32x4 r = load4(Nd + i * kDF + 4 * j4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int j = 4 * j4 + e;
@@ -162,16 +186,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
                 }
             }
             x[i] = s0 + s1;
+            mm = fmaxf(mm, fabsf(x[i]));
         }
         if (g == 0)
 #pragma unroll
             for (int i = 0; i < 16; ++i) L.M[(16 * w + i) * kDF + 16 * w + n] = x[i];
+        if (w == 0 || w == 2)   // the one block above the diagonal that a stored row reaches
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j <= w) continue;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) L.M[(16 * w + 4 * g + r) * kDF + 16 * j + n] = 0.f;
-        }
+            for (int r = 0; r < 4; ++r) L.M[(16 * w + 4 * g + r) * kDF + 16 * (w + 1) + n] = 0.f;
     }
     __syncthreads();
     // ---- the blocks below, diagonal by diagonal ----
@@ -183,43 +205,53 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
             for (int o = 0; o < d; ++o) {
                 const int kb = j + o;
-                const f32x4 x = *reinterpret_cast<const f32x4*>(L.N + (16 * w + n) * kDF + 16 * kb + 4 * g);
+                const f32x4 x = load4(L.N + (16 * w + n) * kDF + 16 * kb + 4 * g);
 #pragma unroll
                 for (int s = 0; s < 4; ++s) t = mfma4(x[s], L.M[(16 * kb + 4 * g + s) * kDF + 16 * j + n], t);
             }
-            const f32x4 y = *reinterpret_cast<const f32x4*>(L.M + (16 * w + n) * kDF + 16 * w + 4 * g);
+            const f32x4 y = load4(L.M + (16 * w + n) * kDF + 16 * w + 4 * g);
             f32x4 u = zero;
 #pragma unroll
             for (int s = 0; s < 4; ++s) u = mfma4(y[s], t[s], u);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) L.M[(16 * w + 4 * g + r) * kDF + 16 * j + n] = -u[r];
+            for (int r = 0; r < 4; ++r) {
+                L.M[(16 * w + 4 * g + r) * kDF + 16 * j + n] = -u[r];
+                mm = fmaxf(mm, fabsf(u[r]));
+            }
         }
-        __syncthreads();
+        if (d < 3) __syncthreads();
     }
-    // ---- out: planes of M and P, scalars ----
+    mm = wave_max(mm);
+    if (lane == 0) L.redm[w] = mm;
+    __syncthreads();   // M is whole, N is read: P takes its place
 #pragma unroll
     for (int j = 0; j < 4; ++j)
+        if (j / 2 <= w / 2)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) L.N[(16 * w + 4 * g + r) * kDF + 16 * j + n] = P[j][r];
-    uint16_t* img = a.img + (size_t)blockIdx.x * ((2 + PP) * kDC * kDC);
-    planes_out<2>(L.M, img, L.mi);
+            for (int r = 0; r < 4; ++r) L.N[(16 * w + 4 * g + r) * kDF + 16 * j + n] = P[j][r];
+    uint16_t* img = a.img + (size_t)blockIdx.x * ((2 + PP) * kPlaneUnits * 8);
+    const int EM = h2_exp(fmaxf(fmaxf(L.redm[0], L.redm[1]), fmaxf(L.redm[2], L.redm[3])));
+    const int EP = h2_exp(fmaxf(fmaxf(L.redp[0], L.redp[1]), fmaxf(L.redp[2], L.redp[3])));
+    planes_out<2>(L.M, img, pow2(EM));
     __syncthreads();
-    planes_out<PP>(L.N, img + 2 * kDC * kDC, L.pi);
-    __syncthreads();
+    planes_out<PP>(L.N, img + 2 * kPlaneUnits * 8, pow2(EP));
     if (threadIdx.x < kDC) {
         const int t = threadIdx.x;
         float* sc = a.scal + (size_t)blockIdx.x * kScal;
-        const double Lt = L.L[t], Lc = L.L[kDC - 1];
-        const float G = expf((float)Lt), ki = 1.0f / L.ks[t];
+        const double Lt = L.L[t];
+        const float G = __builtin_amdgcn_exp2f((float)Lt), ki = 1.0f / L.ks[t], qi = 1.0f / L.qs[t], be = L.beta[t];
         sc[kKs + t] = L.ks[t];
         sc[kQs + t] = L.qs[t];
         sc[kGk + t] = G * ki;
-        sc[kGq + t] = G / L.qs[t];
-        sc[kMi + t] = L.mi[t];
-        sc[kPi + t] = L.pi[t];
-        sc[kDc + t] = expf((float)(Lc - Lt)) * ki;
-        sc[kBe + t] = L.beta[t];
-        if (t == kDC - 1) sc[kGc] = G;
+        sc[kGq + t] = G * qi;
+        sc[kQi + t] = qi;
+        sc[kDb + t] = __builtin_amdgcn_exp2f((float)(L.L[kDC - 1] - Lt)) * be * ki;
+        sc[kBe + t] = be;
+        if (t == kDC - 1) {
+            sc[kGc] = G;
+            sc[kMi] = pow2(-EM);
+            sc[kPi] = pow2(-EP);
+        }
     }
 }
 

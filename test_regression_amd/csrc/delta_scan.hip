@@ -4,12 +4,18 @@
 // meet the other columns.  Its part of S (dk x 16) stays in registers in MFMA
 // accumulator order, which is also the operand order of the next product
 // (cg_h2.h's perm32), so the chunk's chain
-//   X = K S,  R = V - G X,  E = M R,  O = G Q S + P (b E),
+//   X = K S,  R = V - G X,  E = M R,  O = G Q S + (P diag(b)) E,
 //   S' = G_C S + K^T (D_C b E)
 // runs without exchanging anything between lanes but the column maxima that
-// scale the fp16 operands.  A workgroup of four waves (64 columns) shares the
-// chunk's K, Q, M and P in LDS; the next chunk's rows are in flight in
-// registers meanwhile.
+// scale the fp16 operands.  S is kept scaled by a power of two per column, so
+// that the update's MFMAs add onto it directly.  A workgroup of four waves
+// stages the chunk's K, Q, M and P in LDS for its columns; the next chunk's
+// rows are in flight in registers meanwhile.
+//
+// The pass is bound by the instructions a wave issues for a chunk (4 cycles
+// each, a wave a SIMD) and by the chain's latencies, not by memory.  Few heads
+// leave compute units idle: then a workgroup takes 32 or 16 columns and its
+// other waves only stage.
 //
 // Precision: S, R and b E enter the products that feed the state as hi + lo
 // (22 bits).  For bf16 outputs the two products that only feed O take the hi
@@ -31,61 +37,68 @@ struct alignas(16) ScanLds {
 // OUT: write O.  SAVE: write each chunk's start state and E (the backward's
 // recomputation).
 template <int DKP, typename In, bool OUT, bool SAVE>
-__global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves) {
     constexpr int NP = delta_planes<In>(), NJ = DKP / 32, NS = DKP / 16, KW = delta_row_words(DKP);
     __shared__ ScanLds<DKP, NP> L;
-    const int lane = threadIdx.x % 64, w = threadIdx.x / 64, n = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), n = lane & 15, g = lane >> 4;
     // the column groups of a head on one XCD (workgroups go to the 8 XCDs in turn)
-    const int cgs = (a.dv + 63) / 64;
-    const long bh = (long)(blockIdx.x / (8 * cgs)) * 8 + blockIdx.x % 8;
+    const int cgs = (a.dv + 16 * waves - 1) / (16 * waves);
+    const int bh = (int)(blockIdx.x / (8 * cgs)) * 8 + blockIdx.x % 8;
     if (bh >= a.BH) return;
-    const int col = 64 * (int)(blockIdx.x / 8 % cgs) + 16 * w + n;
-    const bool live = col - n < a.dv;   // a whole wave
-    const long bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
+    const int col0 = 16 * (waves * (int)(blockIdx.x / 8 % cgs) + w);   // the wave's first column
+    const bool live = w < waves && col0 < a.dv;
+    const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
     const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
     const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
-    const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + col;
-    In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col : nullptr;
-    const size_t image = (size_t)(2 + a.p_planes) * kDC * kDC;
+    const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + col0;
+    In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col0 : nullptr;
+    const size_t image = (size_t)(2 + a.p_planes) * kPlaneUnits * 8;
     const uint16_t* img = a.img + (size_t)bh * a.nc * image;
     const float* scal = a.scal + (size_t)bh * a.nc * kScal;
-    const size_t so = ((size_t)bh * a.dv + col) * a.dk + 4 * g;   // this lane's row of the (dv x dk) state
+    const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;   // this lane's row of the (dv x dk) state
+    const uint32_t lv = (4 * g * a.dv + n) * sizeof(In);               // this lane's bytes in a 16-row tile of v
     const f32x4 zero{0.f, 0.f, 0.f, 0.f};
 
-    f32x4 S[NS];
+    f32x4 S[NS];   // the state times 2^cs
+    int cs = 0;
 #pragma unroll
     for (int m = 0; m < NS; ++m)
         S[m] = a.state0 && live && 16 * m < a.dk ? load4(a.state0 + so + 16 * m) : zero;
 
     using Units = RowUnits<DKP, In>;
+    using Planes = PlaneUnits<OUT ? 2 + NP : 2>;
     Units kr, qr;
-    PlaneUnits<2> mr;
-    PlaneUnits<NP> pr;
+    Planes pr;
     In vr[16];
     float ksr[Units::n], qsr[Units::n];
     f32x4 scr = zero;
-    auto fetch = [&](int c) {
+    auto fetch = [&](int chunk) {
+        const int c = opaque(chunk);
         const int valid = min(kDC, a.T - c * kDC);
         kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
         if constexpr (OUT) qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
         const float* sc = scal + (size_t)c * kScal;
 #pragma unroll
         for (int i = 0; i < Units::n; ++i) {
-            ksr[i] = sc[kKs + Units::row(i)];
-            if constexpr (OUT) qsr[i] = sc[kQs + Units::row(i)];
+            ksr[i] = *lane_at(sc + kKs, 4 * Units::row(i));
+            if constexpr (OUT) qsr[i] = *lane_at(sc + kQs, 4 * Units::row(i));
         }
-        mr.load(img + c * image);
-        if constexpr (OUT) pr.load(img + c * image + 2 * kDC * kDC);
-        if (threadIdx.x < kScal / 4) scr = load4(sc + 4 * threadIdx.x);
+        pr.load(img + c * image);
+        if (threadIdx.x < kScal / 4) scr = load4(lane_at(sc, 16 * threadIdx.x));
+        if (!live) return;
         const In* vp = Vp + (size_t)c * kDC * a.dv;
+        if (valid == kDC) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = 16 * (i / 4) + 4 * g + i % 4;
-            vr[i] = live && t < valid ? vp[(size_t)t * a.dv] : In{};
+            for (int i = 0; i < 16; ++i) vr[i] = *lane_at(vp + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                vr[i] = vp[(uint32_t)min(16 * (i / 4) + 4 * g + i % 4, valid - 1) * a.dv + n];
         }
     };
     fetch(0);
-    for (int c = 0; c < a.nc; ++c) {
+    for (int chunk = 0; chunk < a.nc; ++chunk) {
+        const int c = opaque(chunk);
         __syncthreads();   // the previous chunk's tiles are read
         f32x4 V[4];
 #pragma unroll
@@ -93,43 +106,57 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a) {
             kr.template store<NP>(L.K, i, ksr[i]);
             if constexpr (OUT) qr.template store<NP>(L.Q, i, qsr[i]);
         }
-        mr.store(L.M);
-        if constexpr (OUT) pr.store(L.P);
+        pr.store(L.M[0]);   // P's planes follow M's
         if (threadIdx.x < kScal / 4) *reinterpret_cast<f32x4*>(L.sc + 4 * threadIdx.x) = scr;
 #pragma unroll
         for (int i = 0; i < 16; ++i) V[i / 4][i % 4] = to_f32(vr[i]);
         __syncthreads();
-        if (c + 1 < a.nc) fetch(c + 1);
+        if (chunk + 1 < a.nc) fetch(chunk + 1);
         if (!live) continue;
 
         if constexpr (SAVE) {
-            float* sp = a.S + (size_t)c * a.dv * a.dk + ((size_t)bh * a.nc * a.dv + col) * a.dk + 4 * g;
+            const float s = pow2(-cs);
+            float* sp = a.S + ((size_t)bh * a.nc + c) * a.dv * a.dk + (size_t)(col0 + n) * a.dk + 4 * g;
 #pragma unroll
             for (int m = 0; m < NS; ++m)
-                if (16 * m < a.dk) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m];
+                if (16 * m < a.dk) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
         }
         // ---- K S and Q S ----
         f16x8 Sh[NJ], Sl[NJ];
-        const float is = column_operands(S, Sh, Sl);
+        const int es = column_exp(S);
+        column_split(S, es, Sh, Sl);
+        const float is = pow2(-es - cs);
         f32x4 X[4], Y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            X[i] = Y[i] = zero;
+        for (int j = 0; j < NJ; ++j) {
+            f16x8 kh[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) kh[i] = row_operand(L.K[0], KW, i, j, n, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) j ? mfma_acc(X[i], kh[i], Sl[j]) : mfma_first(X[i], kh[i], Sl[j]);
+            if constexpr (NP == 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mfma_acc(X[i], row_operand(L.K[1], KW, i, j, n, g), Sh[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mfma_acc(X[i], kh[i], Sh[j]);
+        }
+        mfma_done(X);
+        if constexpr (OUT) {
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const f16x8 kh = row_operand(L.K[0], KW, i, j, n, g);
-                X[i] = mfma_f16x32(kh, Sl[j], X[i]);
-                if constexpr (NP == 2) X[i] = mfma_f16x32(row_operand(L.K[1], KW, i, j, n, g), Sh[j], X[i]);
-                X[i] = mfma_f16x32(kh, Sh[j], X[i]);
-                if constexpr (OUT) {
-                    const f16x8 qh = row_operand(L.Q[0], KW, i, j, n, g);
-                    if constexpr (NP == 2) {
-                        Y[i] = mfma_f16x32(qh, Sl[j], Y[i]);
-                        Y[i] = mfma_f16x32(row_operand(L.Q[1], KW, i, j, n, g), Sh[j], Y[i]);
-                    }
-                    Y[i] = mfma_f16x32(qh, Sh[j], Y[i]);
+                f16x8 qh[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qh[i] = row_operand(L.Q[0], KW, i, j, n, g);
+                if constexpr (NP == 2) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) j ? mfma_acc(Y[i], qh[i], Sl[j]) : mfma_first(Y[i], qh[i], Sl[j]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mfma_acc(Y[i], row_operand(L.Q[1], KW, i, j, n, g), Sh[j]);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) NP == 2 || j ? mfma_acc(Y[i], qh[i], Sh[j]) : mfma_first(Y[i], qh[i], Sh[j]);
             }
+            mfma_done(Y);
         }
         // ---- E = M (V - G K S) ----
 #pragma unroll
@@ -139,89 +166,115 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a) {
             for (int r = 0; r < 4; ++r) X[i][r] = V[i][r] - (gk[r] * is) * X[i][r];
         }
         f16x8 Bh[2], Bl[2];
-        const float ir = column_operands(X, Bh, Bl);
+        const int er = column_exp(X);
+        column_split(X, er, Bh, Bl);
         f32x4 U[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            U[i] = zero;
+        for (int j = 0; j < 2; ++j) {   // row tiles 2 j and up reach column block j
+            f16x8 mh[4], ml[4];
 #pragma unroll
-            for (int j = 0; j <= i / 2; ++j) {
-                const f16x8 mh = row_operand(L.M[0], kDP, i, j, n, g);
-                U[i] = mfma_f16x32(mh, Bl[j], U[i]);
-                U[i] = mfma_f16x32(row_operand(L.M[1], kDP, i, j, n, g), Bh[j], U[i]);
-                U[i] = mfma_f16x32(mh, Bh[j], U[i]);
-            }
-            const f32x4 mi = row4(L.sc + kMi, i, g), be = row4(L.sc + kBe, i, g);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) U[i][r] *= mi[r] * ir;
-            if constexpr (SAVE) {
-                float* ep = a.E + ((size_t)(bh * a.nc + c) * kDC + 16 * i + 4 * g) * a.dv + col;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) ep[(size_t)r * a.dv] = U[i][r];
+            for (int i = 2 * j; i < 4; ++i) {
+                mh[i] = row_operand(L.M[0], kDP, i, j, n, g);
+                ml[i] = row_operand(L.M[1], kDP, i, j, n, g);
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r) U[i][r] *= be[r];
+            for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(U[i], mh[i], Bl[j]) : mfma_first(U[i], mh[i], Bl[j]);
+#pragma unroll
+            for (int i = 2 * j; i < 4; ++i) mfma_acc(U[i], ml[i], Bh[j]);
+#pragma unroll
+            for (int i = 2 * j; i < 4; ++i) mfma_acc(U[i], mh[i], Bh[j]);
         }
-        // ---- O = G Q S + P b E ----
+        mfma_done(U);
+        const float ir = L.sc[kMi] * pow2(-er);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) U[i] *= ir;
+        if constexpr (SAVE) {
+            float* ep = a.E + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) *lane_at(ep + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv * (4 / sizeof(In))) = U[i / 4][i % 4];
+        }
+        // ---- O = G Q S + P diag(b) E ----
         if constexpr (OUT) {
-            const float iu = column_operands(U, Bh, Bl);
-            const int valid = min(kDC, a.T - c * kDC);
-            In* op = Op + (size_t)c * kDC * a.dv;
+            const int eu = column_exp(U);
+            if constexpr (NP == 2) column_split(U, eu, Bh, Bl);
+            else column_hi(U, eu, Bh);
+            const float iu = L.sc[kPi] * pow2(-eu);
+            f32x4 Z[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                f16x8 ph[4];
+#pragma unroll
+                for (int i = 2 * j; i < 4; ++i) ph[i] = row_operand(L.P[0], kDP, i, j, n, g);
+                if constexpr (NP == 2) {
+#pragma unroll
+                    for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(Z[i], ph[i], Bl[j]) : mfma_first(Z[i], ph[i], Bl[j]);
+#pragma unroll
+                    for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], row_operand(L.P[1], kDP, i, j, n, g), Bh[j]);
+                }
+#pragma unroll
+                for (int i = 2 * j; i < 4; ++i) NP == 2 || j ? mfma_acc(Z[i], ph[i], Bh[j]) : mfma_first(Z[i], ph[i], Bh[j]);
+            }
+            mfma_done(Z);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                f32x4 Z = zero;
+                const f32x4 gq = row4(L.sc + kGq, i, g), qi = row4(L.sc + kQi, i, g);
 #pragma unroll
-                for (int j = 0; j <= i / 2; ++j) {
-                    const f16x8 ph = row_operand(L.P[0], kDP, i, j, n, g);
-                    if constexpr (NP == 2) {
-                        Z = mfma_f16x32(ph, Bl[j], Z);
-                        Z = mfma_f16x32(row_operand(L.P[1], kDP, i, j, n, g), Bh[j], Z);
-                    }
-                    Z = mfma_f16x32(ph, Bh[j], Z);
-                }
-                const f32x4 gq = row4(L.sc + kGq, i, g), pi = row4(L.sc + kPi, i, g);
+                for (int r = 0; r < 4; ++r) Y[i][r] = (gq[r] * is) * Y[i][r] + (qi[r] * iu) * Z[i][r];
+            }
+            const int valid = min(kDC, a.T - c * kDC);
+            In* op = Op + (size_t)c * kDC * a.dv;
+            if (valid == kDC) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 16 * i + 4 * g + r;
-                    const float o = (gq[r] * is) * Y[i][r] + (pi[r] * iu) * Z[r];
-                    if (t < valid) store1(op + (size_t)t * a.dv, o);
+                for (int i = 0; i < 16; ++i) store1(lane_at(op + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv), Y[i / 4][i % 4]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int t = 16 * (i / 4) + 4 * g + i % 4;
+                    if (t < valid) store1(op + (uint32_t)t * a.dv + n, Y[i / 4][i % 4]);
                 }
             }
         }
         // ---- S' = G_C S + K^T (D_C b E) ----
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const f32x4 dc = row4(L.sc + kDc, i, g);
+        for (int i = 0; i < 4; ++i) U[i] *= row4(L.sc + kDb, i, g);
+        // a write that is 2^25 times smaller than the state takes a scale at
+        // which the scaled state stays below 2^40
+        const int ew = min(column_exp(U), es + cs + 25);
+        column_split(U, ew, Bh, Bl);
+        const float gs = __builtin_amdgcn_ldexpf(L.sc[kGc], ew - cs);
+        cs = ew;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) U[i][r] *= dc[r];
+        for (int m = 0; m < NS; ++m) S[m] *= gs;
+        mfma_ready(S);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            f16x8 kh[NS];
+#pragma unroll
+            for (int m = 0; m < NS; ++m) kh[m] = col_operand(L.K[0], KW, m, j, n, g);
+#pragma unroll
+            for (int m = 0; m < NS; ++m) mfma_acc(S[m], kh[m], Bl[j]);
+            if constexpr (NP == 2)
+#pragma unroll
+                for (int m = 0; m < NS; ++m) mfma_acc(S[m], col_operand(L.K[1], KW, m, j, n, g), Bh[j]);
+#pragma unroll
+            for (int m = 0; m < NS; ++m) mfma_acc(S[m], kh[m], Bh[j]);
         }
-        const float iw = column_operands(U, Bh, Bl);
-        const float gc = L.sc[kGc];
-#pragma unroll
-        for (int m = 0; m < NS; ++m) {
-            f32x4 t = zero;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const f16x8 kh = col_operand(L.K[0], KW, m, j, n, g);
-                t = mfma_f16x32(kh, Bl[j], t);
-                if constexpr (NP == 2) t = mfma_f16x32(col_operand(L.K[1], KW, m, j, n, g), Bh[j], t);
-                t = mfma_f16x32(kh, Bh[j], t);
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) S[m][r] = gc * S[m][r] + iw * t[r];
-        }
+        mfma_done(S);
     }
-    if (a.final_state && live)
+    if (a.final_state && live) {
+        const float s = pow2(-cs);
 #pragma unroll
         for (int m = 0; m < NS; ++m)
-            if (16 * m < a.dk) *reinterpret_cast<f32x4*>(a.final_state + so + 16 * m) = S[m];
+            if (16 * m < a.dk) *reinterpret_cast<f32x4*>(a.final_state + so + 16 * m) = S[m] * s;
+    }
 }
 
 template <int DKP, bool OUT, bool SAVE>
 hipError_t scan_go(const DeltaArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((a.BH + 7) / 8 * 8 * ((a.dv + 63) / 64)));
-    if (a.bf16) hipLaunchKernelGGL((delta_scan_kernel<DKP, bf16_t, OUT, SAVE>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((delta_scan_kernel<DKP, float, OUT, SAVE>), grid, dim3(256), 0, s, a);
+    const int waves = scan_waves(a.BH, a.dv);
+    const dim3 grid((unsigned)((a.BH + 7) / 8 * 8 * ((a.dv + 16 * waves - 1) / (16 * waves))));
+    if (a.bf16) hipLaunchKernelGGL((delta_scan_kernel<DKP, bf16_t, OUT, SAVE>), grid, dim3(256), 0, s, a, waves);
+    else hipLaunchKernelGGL((delta_scan_kernel<DKP, float, OUT, SAVE>), grid, dim3(256), 0, s, a, waves);
     return hipGetLastError();
 }
 template <bool OUT, bool SAVE>

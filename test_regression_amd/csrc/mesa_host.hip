@@ -550,7 +550,7 @@ static bool dtype_ok(int t) { return t == MESA_DTYPE_F32 || t == MESA_DTYPE_BF16
 // Bytes per head and chunk: the fp16 planes of M (two) and P (one for bf16,
 // two for float32), then the scalars.
 static size_t delta_image_halfs(int dtype) {
-    return (size_t)(dtype == MESA_DTYPE_BF16 ? 3 : 4) * mesa::kDeltaChunk * mesa::kDeltaChunk;
+    return (size_t)(dtype == MESA_DTYPE_BF16 ? 3 : 4) * mesa::kDeltaPlaneUnits * 8;
 }
 static long delta_chunks(int T) { return ((long)T + mesa::kDeltaChunk - 1) / mesa::kDeltaChunk; }
 

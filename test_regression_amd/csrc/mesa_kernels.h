@@ -95,7 +95,8 @@ hipError_t launch_hawk(const HawkArgs& a, hipStream_t s);
 
 // Gated delta rule (delta_*.hip).
 constexpr int kDeltaChunk = 64;   // tokens per chunk
-constexpr int kDeltaScal = 576;   // floats of per-chunk scalars in the workspace
+constexpr int kDeltaScal = 512;   // floats of per-chunk scalars in the workspace
+constexpr int kDeltaPlaneUnits = 384;   // 16-byte units of a plane of M or P in the workspace
 struct DeltaArgs {
     const void* q; const void* k; const void* v; const float* gamma; const float* beta; const float* state0;
     long BH; int Hk; int H; int T; int dk; int dv; int nc; int bf16;
