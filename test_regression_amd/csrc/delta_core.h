@@ -128,8 +128,9 @@ struct RowUnits {
     static constexpr int n = kDC * per_row / THREADS;
     static constexpr int words = sizeof(In) == 2 ? 4 : 8;
     u32x4 raw[n][words / 4];
-    static __device__ __forceinline__ int row(int i) { return (threadIdx.x + THREADS * i) / per_row; }
-    static __device__ __forceinline__ int col(int i) { return 8 * ((threadIdx.x + THREADS * i) % per_row); }
+    // (a workgroup of 512 threads stages with its second half)
+    static __device__ __forceinline__ int row(int i) { return (threadIdx.x % THREADS + THREADS * i) / per_row; }
+    static __device__ __forceinline__ int col(int i) { return 8 * ((threadIdx.x % THREADS + THREADS * i) % per_row); }
     // Rows `valid` and up repeat the last one: their gates and strengths make
     // them inert (the strength is 0), so only their finiteness matters.
     // Features dk and up are zeros.
@@ -217,16 +218,16 @@ template <int N>
 struct PlaneUnits {
     static constexpr int total = N * kPlaneUnits, n = (total + 255) / 256;
     u32x4 raw[n];
-    static __device__ __forceinline__ bool has(int i) { return 256 * (i + 1) <= total || threadIdx.x + 256 * i < total; }
+    static __device__ __forceinline__ bool has(int i) { return 256 * (i + 1) <= total || threadIdx.x % 256 + 256 * i < total; }
     __device__ __forceinline__ void load(const uint16_t* img) {
 #pragma unroll
         for (int i = 0; i < n; ++i)
-            if (has(i)) raw[i] = *lane_at(reinterpret_cast<const u32x4*>(img), 16 * (threadIdx.x + 256 * i));
+            if (has(i)) raw[i] = *lane_at(reinterpret_cast<const u32x4*>(img), 16 * (threadIdx.x % 256 + 256 * i));
     }
     __device__ __forceinline__ void store(uint32_t* P) const {
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const int u = threadIdx.x + 256 * i, pl = u / kPlaneUnits, v = u % kPlaneUnits;
+            const int u = threadIdx.x % 256 + 256 * i, pl = u / kPlaneUnits, v = u % kPlaneUnits;
             if (has(i)) *reinterpret_cast<u32x4*>(P + (pl * kDC + unit_row(v)) * kDP + 4 * unit_col(v)) = raw[i];
         }
     }
@@ -252,6 +253,21 @@ __device__ __forceinline__ void column_hi(const f32x4 (&X)[NT], int E, f16x8 (&H
 
 __device__ __forceinline__ f32x4 row4(const float* sc, int i, int g) {
     return *reinterpret_cast<const f32x4*>(sc + 16 * i + 4 * g);
+}
+
+// The same planes without the block that is never read: rows below 32 hold 32
+// columns at a pitch of 24 words, the others 64 at kDP.
+constexpr int kCP = 24, kCU = 32 * kCP, kCPlane = kCU + 32 * kDP;
+__device__ __forceinline__ uint32_t* compact_unit(uint32_t* P, int u) {
+    const int v = u % kPlaneUnits;
+    return P + u / kPlaneUnits * kCPlane + (v < 128 ? v / 4 * kCP + 4 * (v % 4) : kCU + (v - 128) / 8 * kDP + 4 * (v % 8));
+}
+__device__ __forceinline__ f16x8 compact_row_operand(const uint32_t* P, int i, int j, int m, int g) {
+    return i < 2 ? lds_f16x8(P + (16 * i + m) * kCP + 4 * g)
+                 : lds_f16x8(P + kCU + (16 * (i - 2) + m) * kDP + 16 * j + 4 * g);
+}
+__device__ __forceinline__ f16x8 compact_col_operand(const uint32_t* P, int i, int j, int m, int g) {
+    return j == 0 ? col_operand(P, kCP, i, 0, m, g) : col_operand(P + kCU, kDP, i, 0, m, g);
 }
 
 // Waves of a scan's workgroup that take columns: four, unless that leaves

@@ -269,21 +269,21 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
     }
 }
 
-template <int DKP, bool OUT, bool SAVE>
+template <bool OUT, bool SAVE>
 hipError_t scan_go(const DeltaArgs& a, hipStream_t s) {
     const int waves = scan_waves(a.BH, a.dv);
     const dim3 grid((unsigned)((a.BH + 7) / 8 * 8 * ((a.dv + 16 * waves - 1) / (16 * waves))));
-    if (a.bf16) hipLaunchKernelGGL((delta_scan_kernel<DKP, bf16_t, OUT, SAVE>), grid, dim3(256), 0, s, a, waves);
-    else hipLaunchKernelGGL((delta_scan_kernel<DKP, float, OUT, SAVE>), grid, dim3(256), 0, s, a, waves);
+    hipLaunchKernelGGL((delta_scan_kernel<128, float, OUT, SAVE>), grid, dim3(256), 0, s, a, waves);
     return hipGetLastError();
 }
-template <bool OUT, bool SAVE>
-hipError_t scan_dk(const DeltaArgs& a, hipStream_t s) {
-    return a.dk <= 32 ? scan_go<32, OUT, SAVE>(a, s)
-                      : a.dk == 64 ? scan_go<64, OUT, SAVE>(a, s) : scan_go<128, OUT, SAVE>(a, s);
-}
 
-hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) { return scan_dk<true, false>(a, s); }
-hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s) { return scan_dk<false, true>(a, s); }
+// Float rows of 128 features need two planes of K twice in the eight-wave
+// kernel's LDS, which does not hold them; everything else takes that kernel.
+hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) {
+    return a.bf16 || a.dk < 128 ? launch_delta_scan8(a, s) : scan_go<true, false>(a, s);
+}
+hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s) {
+    return a.bf16 || a.dk < 128 ? launch_delta_states8(a, s) : scan_go<false, true>(a, s);
+}
 
 }  // namespace mesa

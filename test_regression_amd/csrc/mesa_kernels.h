@@ -116,6 +116,8 @@ hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& a, hipStream_t s);
 hipError_t launch_delta_grads(const DeltaBwdArgs& a, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_scan8(const DeltaArgs& a, hipStream_t s);     // the same on eight waves (not float with dk 128)
+hipError_t launch_delta_states8(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E
 struct DeltaStepArgs {
     const void* q; const void* k; const void* v; const float* gamma; const float* beta; float* state;
