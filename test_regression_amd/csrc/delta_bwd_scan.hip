@@ -76,16 +76,9 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
         if (threadIdx.x < kScal / 4) scr = load4(lane_at(sc, 16 * threadIdx.x));
         const In* op = Op + (size_t)c * kDC * a.dv;
         if (!live) return;
-        if (valid == kDC) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) vr[i] = *lane_at(op + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv);
-        } else {   // zeros behind the end
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int t = 16 * (i / 4) + 4 * g + i % 4;
-                vr[i] = t < valid ? op[(uint32_t)t * a.dv + n] : In{};
-            }
-        }
+        each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {   // zeros behind the end
+            vr[i] = valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid ? *lane_at(op, o) : In{};
+        });
     };
     fetch(a.nc - 1);
     for (int chunk = a.nc - 1; chunk >= 0; --chunk) {
@@ -200,19 +193,10 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
         {
             float* rp = b.dR + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
             In* vp = Vp + (size_t)c * kDC * a.dv;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                *lane_at(rp + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv * (4 / sizeof(In))) = t[i / 4][i % 4];
-            if (valid == kDC) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) store1(lane_at(vp + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv), t[i / 4][i % 4]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int tok = 16 * (i / 4) + 4 * g + i % 4;
-                    if (tok < valid) store1(vp + (uint32_t)tok * a.dv + n, t[i / 4][i % 4]);
-                }
-            }
+            each_value(lv * (4 / sizeof(In)), fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(rp, o) = t[i / 4][i % 4]; });
+            each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {
+                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) store1(lane_at(vp, o), t[i / 4][i % 4]);
+            });
         }
         // ---- dS = G_C dS' + Q^T (G dO) - K^T (G dV), dS kept scaled as the forward's S ----
         const int ew = min(h2_exp(kslot_max(fmaxf(absmax(X), absmax(B)))), es + cs + 25);
@@ -253,17 +237,14 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
     }
 }
 
-template <int DKP>
-hipError_t bwd_scan_go(const DeltaBwdArgs& b, hipStream_t s) {
+// Float rows of 128 features: two planes of K, twice, do not fit the
+// eight-wave kernel's LDS; everything else takes that kernel.
+hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& b, hipStream_t s) {
+    if (b.f.bf16 || b.f.dk < 128) return launch_delta_bwd_scan8(b, s);
     const int waves = scan_waves(b.f.BH, b.f.dv);
     const dim3 grid((unsigned)((b.f.BH + 7) / 8 * 8 * ((b.f.dv + 16 * waves - 1) / (16 * waves))));
-    if (b.f.bf16) hipLaunchKernelGGL((delta_bwd_scan_kernel<DKP, bf16_t>), grid, dim3(256), 0, s, b, waves);
-    else hipLaunchKernelGGL((delta_bwd_scan_kernel<DKP, float>), grid, dim3(256), 0, s, b, waves);
+    hipLaunchKernelGGL((delta_bwd_scan_kernel<128, float>), grid, dim3(256), 0, s, b, waves);
     return hipGetLastError();
-}
-
-hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& b, hipStream_t s) {
-    return b.f.dk <= 32 ? bwd_scan_go<32>(b, s) : b.f.dk == 64 ? bwd_scan_go<64>(b, s) : bwd_scan_go<128>(b, s);
 }
 
 }  // namespace mesa

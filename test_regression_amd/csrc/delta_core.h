@@ -73,6 +73,25 @@ __device__ __forceinline__ int opaque(int c) {
     return c;
 }
 
+// A value that the compiler takes to change with c: what is formed from it is
+// not kept in registers from chunk to chunk.
+__device__ __forceinline__ uint32_t fresh(uint32_t x, int c) {
+    asm("" : "+s"(x) : "s"(c));
+    return x;
+}
+// The 16 values of a wave's 64 x 16 tile of rows of `pitch` bytes that a lane
+// holds in accumulator order, at byte lv of the tile: f(byte offset, i) for
+// value i of row 16 (i / 4) + i % 4 + 4 g.
+template <typename Fn>
+__device__ __forceinline__ void each_value(uint32_t lv, uint32_t pitch, Fn f) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        uint32_t o = lv + 16 * t * pitch;
+#pragma unroll
+        for (int r = 0; r < 4; ++r, o += pitch) f(o, 4 * t + r);
+    }
+}
+
 // Eight floats, scaled by s (a power of two), rounded to fp16: one instruction each.
 __device__ __forceinline__ f16x8 h2_hi_mix(const f32x4& a, const f32x4& b, float s) {
     uint32_t h0, h1, h2, h3;

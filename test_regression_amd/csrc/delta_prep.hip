@@ -25,12 +25,14 @@ namespace mesa {
 template <int DKP, int NP>
 struct alignas(16) PrepLds {
     static constexpr int KW = delta_row_words(DKP);
-    uint32_t K[NP][kDC * KW];
+    union {
+        uint32_t K[NP][kDC * KW];
+        float N[kDC * kDF];   // A diag(b); after the inverse, P diag(b)
+    };
     union {
         uint32_t Q[NP][kDC * KW];
         float M[kDC * kDF];
     };
-    float N[kDC * kDF];   // A diag(b); after the inverse, P diag(b)
     double L[kDC];
     float beta[kDC], ks[kDC], qs[kDC];
     float rowf[4][kDC];   // 2^(L_i - L_{16j+15}) for row i below column block j
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
             }
         }
     }
-    __syncthreads();   // the decay factors are written, Q is read: M takes its place
+    __syncthreads();   // the decay factors are written, K and Q are read: N and M take their places
     // P keeps the scale 2^EQ of its rows, which bounds it next to the queries
     {
         const int r0 = 16 * w + 4 * g;

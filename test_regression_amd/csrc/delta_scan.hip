@@ -87,14 +87,9 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
         if (threadIdx.x < kScal / 4) scr = load4(lane_at(sc, 16 * threadIdx.x));
         if (!live) return;
         const In* vp = Vp + (size_t)c * kDC * a.dv;
-        if (valid == kDC) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) vr[i] = *lane_at(vp + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                vr[i] = vp[(uint32_t)min(16 * (i / 4) + 4 * g + i % 4, valid - 1) * a.dv + n];
-        }
+        each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {   // zeros behind the end
+            vr[i] = valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid ? *lane_at(vp, o) : In{};
+        });
     };
     fetch(0);
     for (int chunk = 0; chunk < a.nc; ++chunk) {
@@ -190,8 +185,7 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
         for (int i = 0; i < 4; ++i) U[i] *= ir;
         if constexpr (SAVE) {
             float* ep = a.E + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) *lane_at(ep + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv * (4 / sizeof(In))) = U[i / 4][i % 4];
+            each_value(lv * (4 / sizeof(In)), fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(ep, o) = U[i / 4][i % 4]; });
         }
         // ---- O = G Q S + P diag(b) E ----
         if constexpr (OUT) {
@@ -223,16 +217,9 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
             }
             const int valid = min(kDC, a.T - c * kDC);
             In* op = Op + (size_t)c * kDC * a.dv;
-            if (valid == kDC) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) store1(lane_at(op + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv), Y[i / 4][i % 4]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = 16 * (i / 4) + 4 * g + i % 4;
-                    if (t < valid) store1(op + (uint32_t)t * a.dv + n, Y[i / 4][i % 4]);
-                }
-            }
+            each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {
+                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) store1(lane_at(op, o), Y[i / 4][i % 4]);
+            });
         }
         // ---- S' = G_C S + K^T (D_C b E) ----
 #pragma unroll

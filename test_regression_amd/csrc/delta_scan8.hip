@@ -170,8 +170,7 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
             if constexpr (SAVE) {
                 const uint32_t le = (4 * g * a.dv + n) * 4;
                 float* ep = a.E + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) *lane_at(ep + (size_t)(16 * (i / 4) + i % 4) * a.dv, le) = U[i / 4][i % 4];
+                each_value(le, fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(ep, o) = U[i / 4][i % 4]; });
             }
             if constexpr (OUT) {
                 const int eu = column_exp(U);
@@ -320,16 +319,9 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
             }
             const int valid = min(kDC, a.T - c * kDC);
             In* op = Op + (size_t)c * kDC * a.dv;
-            if (valid == kDC) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) store1(lane_at(op + (size_t)(16 * (i / 4) + i % 4) * a.dv, lv), Y[i / 4][i % 4]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int t = 16 * (i / 4) + 4 * g + i % 4;
-                    if (t < valid) store1(op + (uint32_t)t * a.dv + n, Y[i / 4][i % 4]);
-                }
-            }
+            each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {
+                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) store1(lane_at(op, o), Y[i / 4][i % 4]);
+            });
         };
         // every fetch is a whole chunk ahead of its store
         fetch_k(0);

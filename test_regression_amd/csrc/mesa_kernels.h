@@ -113,6 +113,7 @@ struct DeltaBwdArgs {
     float* part;                  // workspace: dq, then dk of each value head [2][BH][T][dk] (H != Hk), else nullptr
 };
 hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& a, hipStream_t s);
+hipError_t launch_delta_bwd_scan8(const DeltaBwdArgs& a, hipStream_t s);   // on eight waves (not float with dk 128)
 hipError_t launch_delta_grads(const DeltaBwdArgs& a, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);
