@@ -238,9 +238,9 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
 }
 
 // Float rows of 128 features: two planes of K, twice, do not fit the
-// eight-wave kernel's LDS; everything else takes that kernel.
+// split kernel's LDS; everything else takes that kernel.
 hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& b, hipStream_t s) {
-    if (b.f.bf16 || b.f.dk < 128) return launch_delta_bwd_scan8(b, s);
+    if (b.f.bf16 || b.f.dk < 128) return launch_delta_bwd_split(b, s);
     const int waves = scan_waves(b.f.BH, b.f.dv);
     const dim3 grid((unsigned)((b.f.BH + 7) / 8 * 8 * ((b.f.dv + 16 * waves - 1) / (16 * waves))));
     hipLaunchKernelGGL((delta_bwd_scan_kernel<128, float>), grid, dim3(256), 0, s, b, waves);

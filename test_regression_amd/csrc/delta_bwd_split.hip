@@ -1,40 +1,39 @@
-// delta_bwd_scan8.hip -- the gated delta rule's backward pass over the chunks
+// delta_bwd_split.hip -- the gated delta rule's backward pass over the chunks
 // with the state's chain and everything beside it on different waves (gfx950).
 //
-// delta_bwd_scan.hip's pass, split as delta_scan8.hip splits the forward's.
-// Waves 0..3 run, for 16 dv columns each and from the last chunk to the first,
-// what the next chunk waits for:
+// delta_bwd_scan.hip's pass, split over twelve waves as delta_scan_split.hip
+// splits the forward's.  Waves 0..3 run, for 16 dv columns each and from the
+// last chunk to the first, what the next chunk waits for:
 //   dE = D_C b K dS' + T,  dV = M^T dE,  dS = G_C dS' + N - K^T (G dV)
-// Waves 4..7 stage the chunks, form T = (P diag(b))^T dO and N = Q^T (G dO),
-// which need no state, ahead of them, and write dV out.  Two barriers a chunk:
-//   first half of c    state: split, K dS', dE     others: M of c and P of c - 1
-//                                                   in, N of c, dV of c + 1 out
-//   second half of c   state: dV, update            others: T of c - 1; K, Q of
-//                                                   c - 1 in
+// Waves 4..7 form T = (P diag(b))^T dO and N = Q^T (G dO), which need no state,
+// ahead of them, and write dV out.  Waves 8..11 stage the chunks.  Two barriers
+// a chunk; between them:
+//   first half of c    split, K dS', dE    N of c, dV of c + 1 out    M of c, P of c - 1 in
+//   second half of c   dV, update          T of c - 1                 K, Q of c - 1 in
 // K is held twice in LDS.
 #include "delta_core.h"
 
 namespace mesa {
 
 template <int DKP, typename In>
-struct alignas(16) BwdScan8Lds {
+struct alignas(16) BwdSplitLds {
     static constexpr int NP = delta_planes<In>(), KW = delta_row_words(DKP), NS = DKP / 16;
     uint32_t K[2][NP][kDC * KW];
     uint32_t M[2 * kCPlane];
     uint32_t Q[NP][kDC * KW];
     uint32_t P[2 * kCPlane];
-    f32x4 T[4][4][64], N[4][NS][64], dV[4][4][64];
+    f32x4 T[4][4][64], N[4][NS][64], dV[4][4 * kTileSlots];
     int ne[4][64];   // the exponent that brings N's column to [2^14, 2^15)
     float sc[2][kScal];
 };
 
 template <int DKP, typename In>
-__global__ __launch_bounds__(512) void delta_bwd_scan8_kernel(DeltaBwdArgs b, int waves) {
-    using Lds = BwdScan8Lds<DKP, In>;
+__global__ __launch_bounds__(768) void delta_bwd_split_kernel(DeltaBwdArgs b, int waves) {
+    using Lds = BwdSplitLds<DKP, In>;
     constexpr int NP = Lds::NP, NJ = DKP / 32, NS = Lds::NS, KW = Lds::KW;
     __shared__ Lds L;
     const DeltaArgs& a = b.f;
-    const int lane = threadIdx.x % 64, w8 = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = w8 % 4;
+    const int lane = threadIdx.x % 64, w12 = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = w12 % 4;
     const int n = lane & 15, g = lane >> 4;
     const int cols = 16 * waves, cgs = (a.dv + cols - 1) / cols;
     const int bh = (int)(blockIdx.x / (8 * cgs)) * 8 + blockIdx.x % 8;
@@ -43,7 +42,7 @@ __global__ __launch_bounds__(512) void delta_bwd_scan8_kernel(DeltaBwdArgs b, in
     const bool live = w < waves && col0 < a.dv;
     const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;
 
-    if (w8 < 4) {
+    if (w12 < 4) {
         // ---------------- the state's chain ----------------
         f32x4 S[NS];   // the gradient of the state times 2^cs
         int cs = 0;
@@ -119,7 +118,7 @@ __global__ __launch_bounds__(512) void delta_bwd_scan8_kernel(DeltaBwdArgs b, in
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 U[i] *= ix;
-                L.dV[w][i][lane] = U[i];
+                L.dV[w][tile_slot(i, n, g)] = U[i];
                 const f32x4 gk = row4(sc + kGk, i, g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) U[i][r] *= -gk[r];
@@ -158,44 +157,13 @@ __global__ __launch_bounds__(512) void delta_bwd_scan8_kernel(DeltaBwdArgs b, in
             for (int m = 0; m < NS; ++m)
                 if (16 * m < a.dk) *reinterpret_cast<f32x4*>(b.grad_state + so + 16 * m) = S[m] * s;
         }
-    } else {
-        // ---------------- staging, T and N, dV out ----------------
-        const int tid = threadIdx.x - 256;
-        const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
-        const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
-        const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
+    } else if (w12 < 8) {
+        // ---------------- T and N; dV out ----------------
         const In* Op = static_cast<const In*>(b.grad_out) + (size_t)bh * a.T * a.dv + col0;
         In* Vp = static_cast<In*>(b.grad_v) + (size_t)bh * a.T * a.dv + col0;
-        constexpr size_t image = (size_t)4 * kPlaneUnits * 8;
-        const uint16_t* img = a.img + (size_t)bh * a.nc * image;
-        const float* scal = a.scal + (size_t)bh * a.nc * kScal;
         const uint32_t lv = (4 * g * a.dv + n) * sizeof(In);   // this lane's bytes in a 16-row tile of v
-        using Units = RowUnits<DKP, In>;
-        using Planes = PlaneUnits<2>;
-        Units kr, qr;
-        Planes mr, pr;
-        float ksr[Units::n], qsr[Units::n];
-        f32x4 scr{0.f, 0.f, 0.f, 0.f};
-        In nr[16];             // dO of the next chunk
-        f32x4 dO[4];           // dO of this one
-        auto fetch_kq = [&](int chunk) {
-            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
-            kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
-            qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
-            const float* sc = scal + (size_t)c * kScal;
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) {
-                ksr[i] = *lane_at(sc + kKs, 4 * Units::row(i));
-                qsr[i] = *lane_at(sc + kQs, 4 * Units::row(i));
-            }
-        };
-        auto put_kq = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) {
-                kr.template store<NP>(L.K[c & 1], i, ksr[i]);
-                qr.template store<NP>(L.Q, i, qsr[i]);
-            }
-        };
+        In nr[16];     // dO of the next chunk
+        f32x4 dO[4];   // and of this one
         auto fetch_o = [&](int chunk) {
             if (!live) return;
             const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
@@ -203,21 +171,6 @@ __global__ __launch_bounds__(512) void delta_bwd_scan8_kernel(DeltaBwdArgs b, in
             each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {   // zeros behind the end
                 nr[i] = valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid ? *lane_at(op, o) : In{};
             });
-        };
-        auto fetch_m = [&](int chunk) { mr.load(img + opaque(chunk) * image); };
-        auto fetch_p = [&](int chunk) {
-            const int c = opaque(chunk);
-            pr.load(img + c * image + 2 * kPlaneUnits * 8);
-            if (tid < kScal / 4) scr = load4(lane_at(scal + (size_t)c * kScal, 16 * tid));
-        };
-        auto put = [&](uint32_t* D, const Planes& u) {
-#pragma unroll
-            for (int i = 0; i < Planes::n; ++i)
-                if (Planes::has(i)) *reinterpret_cast<u32x4*>(compact_unit(D, tid + 256 * i)) = u.raw[i];
-        };
-        auto put_p = [&](int c) {
-            put(L.P, pr);
-            if (tid < kScal / 4) *reinterpret_cast<f32x4*>(L.sc[c & 1] + 4 * tid) = scr;
         };
         // T of chunk c, whose P and scalars are in LDS; its dO becomes the current one
         auto form_t = [&](int c) {
@@ -295,67 +248,122 @@ __global__ __launch_bounds__(512) void delta_bwd_scan8_kernel(DeltaBwdArgs b, in
         };
         auto values_out = [&](int c) {
             if (!live) return;
-            f32x4 t[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) t[i] = L.dV[w][i][lane];
             const int valid = min(kDC, a.T - c * kDC);
             float* rp = b.dR + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
             In* vp = Vp + (size_t)c * kDC * a.dv;
-            each_value(lv * (4 / sizeof(In)), fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(rp, o) = t[i / 4][i % 4]; });
-            each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {
-                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) store1(lane_at(vp, o), t[i / 4][i % 4]);
-            });
+            const uint32_t lo = lane / 4 * a.dv + lane % 4 * 4, pitch = fresh(16 * a.dv, c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 v = tile_row(L.dV[w], i, lane);
+                store4(lane_at(rp, 4 * (lo + i * pitch)), v);
+                if (16 * i + lane / 4 < valid) store4(lane_at(vp, (uint32_t)sizeof(In) * (lo + i * pitch)), v);
+            }
         };
-        // the last chunk: P, then T over it, K and Q; what a half puts in LDS was
-        // fetched in the half before
-        fetch_p(a.nc - 1);
         fetch_o(a.nc - 1);
-        fetch_kq(a.nc - 1);
-        put_p(a.nc - 1);
         __syncthreads();
         form_t(a.nc - 1);
-        put_kq(a.nc - 1);
-        fetch_m(a.nc - 1);
-        if (a.nc > 1) {
-            fetch_p(a.nc - 2);
-            fetch_o(a.nc - 2);
-        }
+        if (a.nc > 1) fetch_o(a.nc - 2);
         for (int chunk = a.nc - 1; chunk >= 0; --chunk) {
             const int c = opaque(chunk);
             __syncthreads();
-            put(L.M, mr);
-            if (chunk > 0) {
-                put_p(c - 1);
-                fetch_kq(chunk - 1);
-            }
             form_n(c);
             if (chunk + 1 < a.nc) values_out(c + 1);
             __syncthreads();
             if (chunk > 0) {
-                put_kq(c - 1);
-                fetch_m(chunk - 1);
-                if (chunk > 1) fetch_p(chunk - 2);
                 form_t(c - 1);
                 if (chunk > 1) fetch_o(chunk - 2);
             }
         }
         __syncthreads();
         values_out(0);
+    } else {
+        // ---------------- staging ----------------
+        const int tid = threadIdx.x - 512;
+        const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
+        const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
+        const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
+        constexpr size_t image = (size_t)4 * kPlaneUnits * 8;
+        const uint16_t* img = a.img + (size_t)bh * a.nc * image;
+        const float* scal = a.scal + (size_t)bh * a.nc * kScal;
+        using Units = RowUnits<DKP, In>;
+        using Planes = PlaneUnits<2>;
+        Units kr, qr;
+        Planes mr, pr;
+        float ksr[Units::n], qsr[Units::n];
+        f32x4 scr{0.f, 0.f, 0.f, 0.f};
+        auto fetch_kq = [&](int chunk) {
+            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
+            kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
+            qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
+            const float* sc = scal + (size_t)c * kScal;
+#pragma unroll
+            for (int i = 0; i < Units::n; ++i) {
+                ksr[i] = *lane_at(sc + kKs, 4 * Units::row(i));
+                qsr[i] = *lane_at(sc + kQs, 4 * Units::row(i));
+            }
+        };
+        auto put_kq = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < Units::n; ++i) {
+                kr.template store<NP>(L.K[c & 1], i, ksr[i]);
+                qr.template store<NP>(L.Q, i, qsr[i]);
+            }
+        };
+        auto fetch_m = [&](int chunk) { mr.load(img + opaque(chunk) * image); };
+        auto fetch_p = [&](int chunk) {
+            const int c = opaque(chunk);
+            pr.load(img + c * image + 2 * kPlaneUnits * 8);
+            if (tid < kScal / 4) scr = load4(lane_at(scal + (size_t)c * kScal, 16 * tid));
+        };
+        auto put = [&](uint32_t* D, const Planes& u) {
+#pragma unroll
+            for (int i = 0; i < Planes::n; ++i)
+                if (Planes::has(i)) *reinterpret_cast<u32x4*>(compact_unit(D, tid + 256 * i)) = u.raw[i];
+        };
+        auto put_p = [&](int c) {
+            put(L.P, pr);
+            if (tid < kScal / 4) *reinterpret_cast<f32x4*>(L.sc[c & 1] + 4 * tid) = scr;
+        };
+        // a chunk's rows are fetched a chunk ahead of their store
+        fetch_p(a.nc - 1);
+        fetch_kq(a.nc - 1);
+        fetch_m(a.nc - 1);
+        put_p(a.nc - 1);
+        if (a.nc > 1) fetch_p(a.nc - 2);
+        __syncthreads();
+        put_kq(a.nc - 1);
+        if (a.nc > 1) fetch_kq(a.nc - 2);
+        for (int chunk = a.nc - 1; chunk >= 0; --chunk) {
+            const int c = opaque(chunk);
+            __syncthreads();
+            put(L.M, mr);
+            if (chunk > 0) {
+                put_p(c - 1);
+                fetch_m(chunk - 1);
+                if (chunk > 1) fetch_p(chunk - 2);
+            }
+            __syncthreads();
+            if (chunk > 0) {
+                put_kq(c - 1);
+                if (chunk > 1) fetch_kq(chunk - 2);
+            }
+        }
+        __syncthreads();
     }
 }
 
 template <int DKP, typename In>
-hipError_t bwd_scan8_go(const DeltaBwdArgs& b, hipStream_t s) {
+hipError_t bwd_split_go(const DeltaBwdArgs& b, hipStream_t s) {
     const int waves = scan_waves(b.f.BH, b.f.dv);
     const dim3 grid((unsigned)((b.f.BH + 7) / 8 * 8 * ((b.f.dv + 16 * waves - 1) / (16 * waves))));
-    hipLaunchKernelGGL((delta_bwd_scan8_kernel<DKP, In>), grid, dim3(512), 0, s, b, waves);
+    hipLaunchKernelGGL((delta_bwd_split_kernel<DKP, In>), grid, dim3(768), 0, s, b, waves);
     return hipGetLastError();
 }
 
-hipError_t launch_delta_bwd_scan8(const DeltaBwdArgs& b, hipStream_t s) {
-    if (!b.f.bf16) return b.f.dk <= 32 ? bwd_scan8_go<32, float>(b, s) : bwd_scan8_go<64, float>(b, s);
-    return b.f.dk <= 32 ? bwd_scan8_go<32, bf16_t>(b, s)
-                        : b.f.dk == 64 ? bwd_scan8_go<64, bf16_t>(b, s) : bwd_scan8_go<128, bf16_t>(b, s);
+hipError_t launch_delta_bwd_split(const DeltaBwdArgs& b, hipStream_t s) {
+    if (!b.f.bf16) return b.f.dk <= 32 ? bwd_split_go<32, float>(b, s) : bwd_split_go<64, float>(b, s);
+    return b.f.dk <= 32 ? bwd_split_go<32, bf16_t>(b, s)
+                        : b.f.dk == 64 ? bwd_split_go<64, bf16_t>(b, s) : bwd_split_go<128, bf16_t>(b, s);
 }
 
 }  // namespace mesa

@@ -289,6 +289,21 @@ __device__ __forceinline__ f16x8 compact_col_operand(const uint32_t* P, int i, i
     return j == 0 ? col_operand(P, kCP, i, 0, m, g) : col_operand(P + kCU, kDP, i, 0, m, g);
 }
 
+// A wave's 64 x 16 tile in accumulator order, through LDS, as row pieces: lane l
+// gets columns 4 (l % 4) .. + 3 of row 16 i + l / 4.  A tile's 16 columns of a
+// lane group take 17 slots, so that both sides touch every bank once.
+constexpr int kTileSlots = 4 * 17;
+__device__ __forceinline__ int tile_slot(int i, int n, int g) { return i * kTileSlots + g * 17 + n; }
+__device__ __forceinline__ f32x4 tile_row(const f32x4* T, int i, int lane) {
+    const int row = lane / 4;
+    const float* p = reinterpret_cast<const float*>(T + tile_slot(i, 4 * (lane % 4), row / 4)) + row % 4;
+    return f32x4{p[0], p[4], p[8], p[12]};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 v) { *reinterpret_cast<f32x4*>(p) = v; }
+__device__ __forceinline__ void store4(bf16_t* p, f32x4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+}
+
 // Waves of a scan's workgroup that take columns: four, unless that leaves
 // compute units (256 of them) idle.
 inline int scan_waves(long BH, int dv) {

@@ -1,36 +1,40 @@
-// delta_scan8.hip -- the gated delta rule's pass over the chunks with the
+// delta_scan_split.hip -- the gated delta rule's pass over the chunks with the
 // state's chain and everything beside it on different waves (gfx950).
 //
-// The chain of delta_scan.hip, split over the eight waves of a workgroup, two
+// The chain of delta_scan.hip, split over the twelve waves of a workgroup, three
 // a SIMD.  Waves 0..3 each own 16 dv columns of the state and run what the
 // next chunk waits for:
 //   X = K S,  E = M (V - G X),  S' = G_C S + K^T (D_C b E)
-// Waves 4..7 stage the chunks in LDS and form the outputs of the chunk before,
-// O = G Q S + (P diag(b)) E, from the fp16 parts of S and E that the state
-// waves leave in LDS.  Two barriers a chunk; between them:
-//   first half   state: splits S, X, R      others: M in, O of chunk c - 1
-//   second half  state: E, update           others: Q, P of c and K, V of c + 1 in
+// Waves 4..7 form the outputs of the chunk before, O = G Q S + (P diag(b)) E,
+// from the fp16 parts of S and E that the state waves leave in LDS (in the
+// backward's recomputation they write E out).  Waves 8..11 stage the chunks.
+// Two barriers a chunk; between them:
+//   first half    split S, X, R    O of chunk c - 1    M of c in
+//   second half   E, update        --                  Q, P of c; K, V of c + 1 in
 // so K is held twice in LDS and everything else once.
 //
 // A wave alone on its SIMD issues one vector instruction in 5 cycles (9 for
 // the mixed-precision ones of the splits) while the SIMD could take one in
-// 1.3 from several waves; the pass is bound by the state waves' own
+// 1.3 from several waves (measured); the pass is bound by the state waves' own
 // instructions and latencies, which is why nothing else is left to them.
 #include "delta_core.h"
 
 namespace mesa {
 
-template <int DKP, typename In>
-struct alignas(16) Scan8Lds {
+template <int DKP, typename In, bool OUT>
+struct alignas(16) ScanSplitLds {
     static constexpr int NP = delta_planes<In>(), KW = delta_row_words(DKP), NJ = DKP / 32;
     static constexpr int VW = sizeof(In) == 2 ? 8 : 20;   // words of a row of 16 values
     static constexpr int parts = NP * (NJ + 2);           // operands of S and of E that the outputs take
     uint32_t K[2][NP][kDC * KW];
     uint32_t M[2 * kCPlane];
     uint32_t V[4][kDC * VW];
-    uint32_t Q[NP][kDC * KW];
-    uint32_t P[NP * kCPlane];
-    f16x8 ex[4][parts][64];
+    uint32_t Q[OUT ? NP : 1][OUT ? kDC * KW : 4];
+    uint32_t P[OUT ? NP * kCPlane : 4];
+    union {
+        f16x8 ex[4][parts][64];             // for the outputs, whose waves then turn O around here
+        f32x4 E[4][4 * kTileSlots];         // for the recomputation
+    };
     float is[4][64], iu[4][64];
     float sc[2][kScal];
 };
@@ -61,11 +65,11 @@ struct ValueUnits {
 };
 
 template <int DKP, typename In, bool OUT, bool SAVE>
-__global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves) {
-    using Lds = Scan8Lds<DKP, In>;
+__global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int waves) {
+    using Lds = ScanSplitLds<DKP, In, OUT>;
     constexpr int NP = Lds::NP, NJ = Lds::NJ, NS = DKP / 16, KW = Lds::KW;
     __shared__ Lds L;
-    const int lane = threadIdx.x % 64, w8 = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = w8 % 4;
+    const int lane = threadIdx.x % 64, w12 = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = w12 % 4;
     const int n = lane & 15, g = lane >> 4;
     // the column groups of a head on one XCD (workgroups go to the 8 XCDs in turn)
     const int cols = 16 * waves, cgs = (a.dv + cols - 1) / cols;
@@ -75,7 +79,7 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
     const bool live = w < waves && col0 < a.dv;
     const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;   // this lane's row of the (dv x dk) state
 
-    if (w8 < 4) {
+    if (w12 < 4) {
         // ---------------- the state's chain ----------------
         f32x4 S[NS];   // the state times 2^cs
         int cs = 0;
@@ -167,11 +171,9 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
             const float ir = sc[kMi] * pow2(-er);
 #pragma unroll
             for (int i = 0; i < 4; ++i) U[i] *= ir;
-            if constexpr (SAVE) {
-                const uint32_t le = (4 * g * a.dv + n) * 4;
-                float* ep = a.E + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
-                each_value(le, fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(ep, o) = U[i / 4][i % 4]; });
-            }
+            if constexpr (SAVE)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) L.E[w][tile_slot(i, n, g)] = U[i];
             if constexpr (OUT) {
                 const int eu = column_exp(U);
                 f16x8 Eh[2], El[2];
@@ -218,53 +220,10 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
             for (int m = 0; m < NS; ++m)
                 if (16 * m < a.dk) *reinterpret_cast<f32x4*>(a.final_state + so + 16 * m) = S[m] * s;
         }
-        if constexpr (OUT) __syncthreads();
-    } else {
-        // ---------------- staging, and the outputs of the chunk before ----------------
-        const int tid = threadIdx.x - 256;
-        const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
-        const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
-        const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
-        const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + colg;
+        __syncthreads();
+    } else if (w12 < 8) {
+        // ---------------- outputs of the chunk before, or E out ----------------
         In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col0 : nullptr;
-        const size_t image = (size_t)(2 + a.p_planes) * kPlaneUnits * 8;
-        const uint16_t* img = a.img + (size_t)bh * a.nc * image;
-        const float* scal = a.scal + (size_t)bh * a.nc * kScal;
-        const uint32_t lv = (4 * g * a.dv + n) * sizeof(In);   // this lane's bytes in a 16-row tile of o
-        using Units = RowUnits<DKP, In>;
-        using MUnits = PlaneUnits<2>;
-        using PUnits = PlaneUnits<NP>;
-        Units kr, qr;
-        MUnits mr;
-        PUnits pr;
-        ValueUnits<In> vr;
-        float ksr[Units::n], qsr[Units::n];
-        f32x4 scr{0.f, 0.f, 0.f, 0.f};
-        // K, V and scalars; M; Q and P of a chunk
-        auto fetch_k = [&](int chunk) {
-            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
-            kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
-            vr.load(Vp + (size_t)c * kDC * a.dv, a.dv, cols, a.dv - colg, valid, tid);
-            const float* sc = scal + (size_t)c * kScal;
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) ksr[i] = *lane_at(sc + kKs, 4 * Units::row(i));
-            if (tid < kScal / 4) scr = load4(lane_at(sc, 16 * tid));
-        };
-        auto fetch_m = [&](int chunk) { mr.load(img + opaque(chunk) * image); };
-        auto fetch_q = [&](int chunk) {
-            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
-            qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
-            const float* sc = scal + (size_t)c * kScal;
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) qsr[i] = *lane_at(sc + kQs, 4 * Units::row(i));
-            pr.load(img + c * image + 2 * kPlaneUnits * 8);
-        };
-        auto put_k = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) kr.template store<NP>(L.K[c & 1], i, ksr[i]);
-            vr.template store<Lds::VW>(L.V, cols, tid);
-            if (tid < kScal / 4) *reinterpret_cast<f32x4*>(L.sc[c & 1] + 4 * tid) = scr;
-        };
         auto output = [&](int c) {
             if (!live) return;
             const float* sc = L.sc[c & 1];
@@ -319,9 +278,96 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
             }
             const int valid = min(kDC, a.T - c * kDC);
             In* op = Op + (size_t)c * kDC * a.dv;
-            each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {
-                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) store1(lane_at(op, o), Y[i / 4][i % 4]);
-            });
+            // turned around in this wave's own part of ex, which is read
+            const uint32_t lo = (lane / 4 * a.dv + lane % 4 * 4) * sizeof(In), pitch = fresh(16 * a.dv * sizeof(In), c);
+            wave_lds_sync();
+            if constexpr (sizeof(In) == 2) {
+                uint2* T = reinterpret_cast<uint2*>(L.ex[w]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    T[tile_slot(i, n, g)] = make_uint2(bf16_pair(Y[i][0], Y[i][1]), bf16_pair(Y[i][2], Y[i][3]));
+                wave_lds_sync();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = lane / 4;
+                    const uint16_t* p = reinterpret_cast<const uint16_t*>(T + tile_slot(i, 4 * (lane % 4), row / 4)) + row % 4;
+                    const uint2 v = make_uint2(p[0] | (uint32_t)p[4] << 16, p[8] | (uint32_t)p[12] << 16);
+                    if (16 * i + row < valid) *reinterpret_cast<uint2*>(lane_at(op, lo + i * pitch)) = v;
+                }
+            } else {
+                f32x4* T = reinterpret_cast<f32x4*>(L.ex[w]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) T[tile_slot(i, n, g)] = Y[i];
+                wave_lds_sync();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f32x4 v = tile_row(T, i, lane);
+                    if (16 * i + lane / 4 < valid) store4(lane_at(op, lo + i * pitch), v);
+                }
+            }
+        };
+        auto e_out = [&](int c) {
+            if (!live) return;
+            float* ep = a.E + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
+            const uint32_t lo = (lane / 4 * a.dv + lane % 4 * 4) * 4, pitch = fresh(16 * a.dv * 4, c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) store4(lane_at(ep, lo + i * pitch), tile_row(L.E[w], i, lane));
+        };
+        for (int chunk = 0; chunk < a.nc; ++chunk) {
+            const int c = opaque(chunk);
+            __syncthreads();
+            if (chunk > 0) {
+                if constexpr (OUT) output(c - 1);
+                else e_out(c - 1);
+            }
+            __syncthreads();
+        }
+        __syncthreads();
+        if constexpr (OUT) output(a.nc - 1);
+        else e_out(a.nc - 1);
+    } else {
+        // ---------------- staging ----------------
+        const int tid = threadIdx.x - 512;
+        const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
+        const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
+        const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
+        const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + colg;
+        const size_t image = (size_t)(2 + a.p_planes) * kPlaneUnits * 8;
+        const uint16_t* img = a.img + (size_t)bh * a.nc * image;
+        const float* scal = a.scal + (size_t)bh * a.nc * kScal;
+        using Units = RowUnits<DKP, In>;
+        using MUnits = PlaneUnits<2>;
+        using PUnits = PlaneUnits<NP>;
+        Units kr, qr;
+        MUnits mr;
+        PUnits pr;
+        ValueUnits<In> vr;
+        float ksr[Units::n], qsr[Units::n];
+        f32x4 scr{0.f, 0.f, 0.f, 0.f};
+        // K, V and scalars; M; Q and P of a chunk
+        auto fetch_k = [&](int chunk) {
+            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
+            kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
+            vr.load(Vp + (size_t)c * kDC * a.dv, a.dv, cols, a.dv - colg, valid, tid);
+            const float* sc = scal + (size_t)c * kScal;
+#pragma unroll
+            for (int i = 0; i < Units::n; ++i) ksr[i] = *lane_at(sc + kKs, 4 * Units::row(i));
+            if (tid < kScal / 4) scr = load4(lane_at(sc, 16 * tid));
+        };
+        auto fetch_m = [&](int chunk) { mr.load(img + opaque(chunk) * image); };
+        auto fetch_q = [&](int chunk) {
+            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
+            qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
+            const float* sc = scal + (size_t)c * kScal;
+#pragma unroll
+            for (int i = 0; i < Units::n; ++i) qsr[i] = *lane_at(sc + kQs, 4 * Units::row(i));
+            pr.load(img + c * image + 2 * kPlaneUnits * 8);
+        };
+        auto put_k = [&](int c) {
+#pragma unroll
+            for (int i = 0; i < Units::n; ++i) kr.template store<NP>(L.K[c & 1], i, ksr[i]);
+            vr.template store<Lds::VW>(L.V, cols, tid);
+            if (tid < kScal / 4) *reinterpret_cast<f32x4*>(L.sc[c & 1] + 4 * tid) = scr;
         };
         // every fetch is a whole chunk ahead of its store
         fetch_k(0);
@@ -336,8 +382,6 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
             for (int i = 0; i < MUnits::n; ++i)
                 if (MUnits::has(i)) *reinterpret_cast<u32x4*>(compact_unit(L.M, tid + 256 * i)) = mr.raw[i];
             if (chunk + 1 < a.nc) fetch_m(chunk + 1);
-            if constexpr (OUT)
-                if (chunk > 0) output(c - 1);
             __syncthreads();
             if constexpr (OUT) {
 #pragma unroll
@@ -352,28 +396,25 @@ __global__ __launch_bounds__(512) void delta_scan8_kernel(DeltaArgs a, int waves
                 if (chunk + 2 < a.nc) fetch_k(chunk + 2);
             }
         }
-        if constexpr (OUT) {
-            __syncthreads();
-            output(a.nc - 1);
-        }
+        __syncthreads();
     }
 }
 
 template <int DKP, typename In, bool OUT, bool SAVE>
-hipError_t scan8_go(const DeltaArgs& a, hipStream_t s) {
+hipError_t scan_split_go(const DeltaArgs& a, hipStream_t s) {
     const int waves = scan_waves(a.BH, a.dv);
     const dim3 grid((unsigned)((a.BH + 7) / 8 * 8 * ((a.dv + 16 * waves - 1) / (16 * waves))));
-    hipLaunchKernelGGL((delta_scan8_kernel<DKP, In, OUT, SAVE>), grid, dim3(512), 0, s, a, waves);
+    hipLaunchKernelGGL((delta_scan_split_kernel<DKP, In, OUT, SAVE>), grid, dim3(768), 0, s, a, waves);
     return hipGetLastError();
 }
 template <bool OUT, bool SAVE>
-hipError_t scan8_dk(const DeltaArgs& a, hipStream_t s) {
-    if (!a.bf16) return a.dk <= 32 ? scan8_go<32, float, OUT, SAVE>(a, s) : scan8_go<64, float, OUT, SAVE>(a, s);
-    return a.dk <= 32 ? scan8_go<32, bf16_t, OUT, SAVE>(a, s)
-                      : a.dk == 64 ? scan8_go<64, bf16_t, OUT, SAVE>(a, s) : scan8_go<128, bf16_t, OUT, SAVE>(a, s);
+hipError_t scan_split_dk(const DeltaArgs& a, hipStream_t s) {
+    if (!a.bf16) return a.dk <= 32 ? scan_split_go<32, float, OUT, SAVE>(a, s) : scan_split_go<64, float, OUT, SAVE>(a, s);
+    return a.dk <= 32 ? scan_split_go<32, bf16_t, OUT, SAVE>(a, s)
+                      : a.dk == 64 ? scan_split_go<64, bf16_t, OUT, SAVE>(a, s) : scan_split_go<128, bf16_t, OUT, SAVE>(a, s);
 }
 
-hipError_t launch_delta_scan8(const DeltaArgs& a, hipStream_t s) { return scan8_dk<true, false>(a, s); }
-hipError_t launch_delta_states8(const DeltaArgs& a, hipStream_t s) { return scan8_dk<false, true>(a, s); }
+hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<true, false>(a, s); }
+hipError_t launch_delta_states_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<false, true>(a, s); }
 
 }  // namespace mesa

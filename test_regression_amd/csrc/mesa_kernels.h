@@ -113,12 +113,12 @@ struct DeltaBwdArgs {
     float* part;                  // workspace: dq, then dk of each value head [2][BH][T][dk] (H != Hk), else nullptr
 };
 hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& a, hipStream_t s);
-hipError_t launch_delta_bwd_scan8(const DeltaBwdArgs& a, hipStream_t s);   // on eight waves (not float with dk 128)
+hipError_t launch_delta_bwd_split(const DeltaBwdArgs& a, hipStream_t s);   // with its chain on waves of its own (not float with dk 128)
 hipError_t launch_delta_grads(const DeltaBwdArgs& a, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);
-hipError_t launch_delta_scan8(const DeltaArgs& a, hipStream_t s);     // the same on eight waves (not float with dk 128)
-hipError_t launch_delta_states8(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s);     // the same with its chain on waves of its own (not float with dk 128)
+hipError_t launch_delta_states_split(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E
 struct DeltaStepArgs {
     const void* q; const void* k; const void* v; const float* gamma; const float* beta; float* state;
