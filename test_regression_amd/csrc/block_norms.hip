@@ -138,25 +138,38 @@ __global__ __launch_bounds__(kGateThreads) void gate_norm_bwd_kernel(GateNormBwd
     }
 }
 
-// out[f] = sum over the parts of partial[part][f], f < n: 64 columns a
-// workgroup, its four waves taking every fourth part.
-__global__ __launch_bounds__(256) void sum_parts_kernel(const float* partial, size_t pitch, int parts, long n, float* out) {
-    __shared__ float red[4][64];
+// out[f] = sum over the parts of partial[part][f] for f < n, and out2[f - n2] from
+// column n2 on where out2 is given: 64 columns a workgroup, its sixteen waves
+// taking every sixteenth part.
+__global__ __launch_bounds__(1024) void sum_parts_kernel(const float* partial, size_t pitch, int parts, long n, float* out,
+                                                         long n2, float* out2) {
+    __shared__ float red[16][64];
     const long f = (long)blockIdx.x * 64 + threadIdx.x % 64;
     const int q = threadIdx.x / 64;
-    float s = 0.f;
-    if (f < n)
-        for (int p = q; p < parts; p += 4) s += partial[(size_t)p * pitch + f];
-    red[q][threadIdx.x % 64] = s;
+    float s[4] = {};
+    if (f < n) {
+        const float* p = partial + f;
+        int i = q;
+        for (; i + 48 < parts; i += 64)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[k] += p[(size_t)(i + 16 * k) * pitch];
+        for (; i < parts; i += 16) s[0] += p[(size_t)i * pitch];
+    }
+    red[q][threadIdx.x % 64] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
     if (q == 0 && f < n) {
-        const int i = threadIdx.x;
-        out[f] = (red[0][i] + red[1][i]) + (red[2][i] + red[3][i]);
+        float t = 0.f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) t += red[k][threadIdx.x];
+        if (out2 && f >= n2) out2[f - n2] = t;
+        else out[f] = t;
     }
 }
 
-hipError_t launch_sum_parts(const float* partial, size_t pitch, int parts, long n, float* out, hipStream_t s) {
-    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)((n + 63) / 64)), dim3(256), 0, s, partial, pitch, parts, n, out);
+hipError_t launch_sum_parts(const float* partial, size_t pitch, int parts, long n, float* out, long n2, float* out2,
+                            hipStream_t s) {
+    hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)((n + 63) / 64)), dim3(1024), 0, s, partial, pitch, parts, n, out,
+                       n2, out2);
     return hipGetLastError();
 }
 
@@ -198,7 +211,7 @@ hipError_t launch_gate_norm_bwd(const GateNormBwdArgs& a, hipStream_t s) {
     const hipError_t e = gate_norm_bwd_go_d(a, s);
     if (e != hipSuccess) return e;
     const long n = (long)a.H * a.d;
-    return launch_sum_parts(a.partial, (size_t)n, a.parts, n, a.grad_w, s);
+    return launch_sum_parts(a.partial, (size_t)n, a.parts, n, a.grad_w, n, nullptr, s);
 }
 
 // ------------------------------------------------------------ residual norm
@@ -412,11 +425,10 @@ template <int W, int V, int N> struct BwdGo {
 
 hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) { return residual_shape<FwdGo>(a, s); }
 hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a, hipStream_t s) {
-    hipError_t e = residual_shape<BwdGo>(a, s);
+    const hipError_t e = residual_shape<BwdGo>(a, s);
     if (e != hipSuccess) return e;
-    e = launch_sum_parts(a.partial, 2 * (size_t)a.D, a.parts, a.D, a.grad_w, s);
-    if (e != hipSuccess || !a.grad_scale) return e;
-    return launch_sum_parts(a.partial + a.D, 2 * (size_t)a.D, a.parts, a.D, a.grad_scale, s);
+    return launch_sum_parts(a.partial, 2 * (size_t)a.D, a.parts, a.grad_scale ? 2L * a.D : a.D, a.grad_w, a.D, a.grad_scale,
+                            s);
 }
 
 }  // namespace mesa

@@ -127,6 +127,7 @@ __device__ __forceinline__ void mfma_first(f32x4& c, f16x8 a, f16x8 b) {
 }
 #define MESA_MFMA_FENCE(name, wait)                                                                                   \
     __device__ __forceinline__ void name(f32x4 (&C)[2]) { asm(wait : "+v"(C[0]), "+v"(C[1])); }                       \
+    __device__ __forceinline__ void name(f32x4 (&C)[3]) { asm(wait : "+v"(C[0]), "+v"(C[1]), "+v"(C[2])); }           \
     __device__ __forceinline__ void name(f32x4 (&C)[4]) { asm(wait : "+v"(C[0]), "+v"(C[1]), "+v"(C[2]), "+v"(C[3])); } \
     __device__ __forceinline__ void name(f32x4 (&C)[8]) {                                                             \
         asm(wait : "+v"(C[0]), "+v"(C[1]), "+v"(C[2]), "+v"(C[3]), "+v"(C[4]), "+v"(C[5]), "+v"(C[6]), "+v"(C[7]));   \

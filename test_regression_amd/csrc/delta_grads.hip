@@ -41,8 +41,8 @@ struct alignas(16) GradsLds {
             uint32_t Q[NP][kDC * KW];
             union {
                 struct {
-                    uint32_t Y[2][kDC * kDP];
-                    uint32_t Z[2][kDC * kDP];
+                    uint32_t Y[2 * kCPlane];
+                    uint32_t Z[2 * kCPlane];
                 };
                 float X[kDC * kDF];
             };
@@ -77,21 +77,28 @@ __device__ __forceinline__ void stage_row8(const f32x8& x, uint32_t (&P)[2][kDC 
     }
 }
 
-// hi hi + hi lo + lo hi; AP: whether A has a lo part.
-template <bool AP, bool BP>
-__device__ __forceinline__ f32x4 product(f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl, f32x4 t) {
-    if constexpr (BP) t = mfma_f16x32(ah, bl, t);
-    if constexpr (AP) t = mfma_f16x32(al, bh, t);
-    return mfma_f16x32(ah, bh, t);
+// t (+)= A B as hi lo + lo hi + hi hi; AP, BP: whether A, B have a lo part.
+template <bool FIRST, bool AP, bool BP>
+__device__ __forceinline__ void product(f32x4& t, f16x8 ah, f16x8 al, f16x8 bh, f16x8 bl) {
+    if constexpr (BP) {
+        if constexpr (FIRST) mfma_first(t, ah, bl);
+        else mfma_acc(t, ah, bl);
+    }
+    if constexpr (AP) {
+        if constexpr (FIRST && !BP) mfma_first(t, al, bh);
+        else mfma_acc(t, al, bh);
+    }
+    if constexpr (FIRST && !AP && !BP) mfma_first(t, ah, bh);
+    else mfma_acc(t, ah, bh);
 }
 
 template <int DKP, typename In>
-__global__ __launch_bounds__(256) void delta_grads_kernel(DeltaBwdArgs b) {
+__global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void delta_grads_kernel(DeltaBwdArgs b) {
     constexpr int NP = delta_planes<In>(), NJ = DKP / 32, NS = DKP / 16, KW = delta_row_words(DKP);
     constexpr bool F = NP == 2;   // rows stored as float: two parts
     __shared__ GradsLds<DKP, NP> L;
     const DeltaArgs& a = b.f;
-    const int lane = threadIdx.x % 64, w = threadIdx.x / 64, n = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), n = lane & 15, g = lane >> 4;
     const int c = (int)(blockIdx.x % a.nc);
     const long bh = blockIdx.x / a.nc;
     const long bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
@@ -184,28 +191,47 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaBwdArgs b) {
         const f16x8 rh = row_operand(L.V[1][0], kVW, w, 0, n, g), rl = row_operand(L.V[1][1], kVW, w, 0, n, g);
         const f16x8 eh = row_operand(L.V[2][0], kVW, w, 0, n, g), el = row_operand(L.V[2][1], kVW, w, 0, n, g);
         const f32x4 so4 = row4(L.vs[0], w, g), sr4 = row4(L.vs[1], w, g), se4 = row4(L.vs[2], w, g);
+        {
+            f32x4 y[4], z[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f16x8 bh_ = row_operand(L.V[2][0], kVW, j, 0, n, g), bl = row_operand(L.V[2][1], kVW, j, 0, n, g);
-            const f32x4 y = product<F, true>(oh, ol, bh_, bl, zero), z = product<true, true>(rh, rl, bh_, bl, zero);
-            const float se = L.vs[2][16 * j + n];
+            for (int j = 0; j < 4; ++j) {
+                const f16x8 bh_ = row_operand(L.V[2][0], kVW, j, 0, n, g), bl = row_operand(L.V[2][1], kVW, j, 0, n, g);
+                product<true, F, true>(y[j], oh, ol, bh_, bl);
+                product<true, true, true>(z[j], rh, rl, bh_, bl);
+            }
+            mfma_done(y);
+            mfma_done(z);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                Y[j][r] += y[r] * (so4[r] * se);
-                Z[j][r] += z[r] * (sr4[r] * se);
+            for (int j = 0; j < 4; ++j) {
+                const float se = L.vs[2][16 * j + n];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    Y[j][r] += y[j][r] * (so4[r] * se);
+                    Z[j][r] += z[j][r] * (sr4[r] * se);
+                }
             }
         }
+        const f32x4 os4 = so4 * is, rs4 = sr4 * is, es4 = se4 * id;
 #pragma unroll
-        for (int m = 0; m < NS; ++m) {
-            const f16x8 sh = col_operand(L.S[0][0], KW, m, 0, n, g), sl = col_operand(L.S[0][1], KW, m, 0, n, g);
-            const f16x8 dh = col_operand(L.S[1][0], KW, m, 0, n, g), dl = col_operand(L.S[1][1], KW, m, 0, n, g);
-            const f32x4 x = product<F, true>(oh, ol, sh, sl, zero), y = product<true, true>(rh, rl, sh, sl, zero);
-            const f32x4 z = product<true, true>(eh, el, dh, dl, zero);
+        for (int m0 = 0; m0 < NS; m0 += 2) {
+            f32x4 x[2], y[2], z[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                oS[m][r] += x[r] * (so4[r] * is);
-                rS[m][r] += y[r] * (sr4[r] * is);
-                W[m][r] += z[r] * (se4[r] * id);
+            for (int k = 0; k < 2; ++k) {
+                const int m = m0 + k;
+                const f16x8 sh = col_operand(L.S[0][0], KW, m, 0, n, g), sl = col_operand(L.S[0][1], KW, m, 0, n, g);
+                const f16x8 dh = col_operand(L.S[1][0], KW, m, 0, n, g), dl = col_operand(L.S[1][1], KW, m, 0, n, g);
+                product<true, F, true>(x[k], oh, ol, sh, sl);
+                product<true, true, true>(y[k], rh, rl, sh, sl);
+                product<true, true, true>(z[k], eh, el, dh, dl);
+            }
+            mfma_done(x);
+            mfma_done(y);
+            mfma_done(z);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                oS[m0 + k] += x[k] * os4;
+                rS[m0 + k] += y[k] * rs4;
+                W[m0 + k] += z[k] * es4;
             }
         }
     }
@@ -251,13 +277,20 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaBwdArgs b) {
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f32x4 A = zero, P = zero;
+            f32x4 AP[2];   // the blocks of A and P
 #pragma unroll
             for (int s = 0; s < NJ; ++s) {
                 const f16x8 bh_ = row_operand(L.K[0], KW, j, s, n, g), bl = row_operand(L.K[NP - 1], KW, j, s, n, g);
-                A = product<F, F>(kh[s], kl[s], bh_, bl, A);
-                P = product<F, F>(qh[s], ql[s], bh_, bl, P);
+                if (s == 0) {
+                    product<true, F, F>(AP[0], kh[s], kl[s], bh_, bl);
+                    product<true, F, F>(AP[1], qh[s], ql[s], bh_, bl);
+                } else {
+                    product<false, F, F>(AP[0], kh[s], kl[s], bh_, bl);
+                    product<false, F, F>(AP[1], qh[s], ql[s], bh_, bl);
+                }
             }
+            mfma_done(AP);
+            const f32x4 A = AP[0], P = AP[1];
             const int cj = 16 * j + n;
             const double Lj = L.L[cj];
             const float bj = L.beta[cj];
@@ -351,39 +384,50 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaBwdArgs b) {
         ey = pow2(-EY);
         ez = pow2(-EZ);
         const float sy = pow2(EY), sz = pow2(EZ);
+        // compact planes (delta_core.h): rows below 32 have no columns from 32 on
+        const int r0 = 16 * w + 4 * g, base = w < 2 ? r0 * 2 * kCP : 2 * kCU + (r0 - 32) * 2 * kDP, pitch = 2 * (w < 2 ? kCP : kDP);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j) {
+            if (j / 2 > w / 2) continue;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int at = (16 * w + 4 * g + r) * 2 * kDP + perm32(16 * j + n);
+                const int at = base + r * pitch + perm32(16 * j + n);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const float x = t ? Z[j][r] * sz : Y[j][r] * sy;
                     const _Float16 hi = (_Float16)x;
-                    reinterpret_cast<_Float16*>(t ? L.Z[0] : L.Y[0])[at] = hi;
-                    reinterpret_cast<_Float16*>(t ? L.Z[1] : L.Y[1])[at] = (_Float16)(x - (float)hi);
+                    _Float16* D = reinterpret_cast<_Float16*>(t ? L.Z : L.Y) + at;
+                    D[0] = hi;
+                    D[2 * kCPlane] = (_Float16)(x - (float)hi);
                 }
             }
+        }
     }
     __syncthreads();
     // ---- products over the tokens ----
     f16x8 yh[2], yl[2], zh[2], zl[2], yth[2], ytl[2], zth[2], ztl[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-        yh[j] = row_operand(L.Y[0], kDP, w, j, n, g);
-        yl[j] = row_operand(L.Y[1], kDP, w, j, n, g);
-        zh[j] = row_operand(L.Z[0], kDP, w, j, n, g);
-        zl[j] = row_operand(L.Z[1], kDP, w, j, n, g);
-        yth[j] = col_operand(L.Y[0], kDP, w, j, n, g);
-        ytl[j] = col_operand(L.Y[1], kDP, w, j, n, g);
-        zth[j] = col_operand(L.Z[0], kDP, w, j, n, g);
-        ztl[j] = col_operand(L.Z[1], kDP, w, j, n, g);
+        // blocks above the diagonal are not there
+        yh[j] = yl[j] = zh[j] = zl[j] = yth[j] = ytl[j] = zth[j] = ztl[j] = f16x8{};
+        if (j <= w / 2) {
+            yh[j] = compact_row_operand(L.Y, w, j, n, g);
+            yl[j] = compact_row_operand(L.Y + kCPlane, w, j, n, g);
+            zh[j] = compact_row_operand(L.Z, w, j, n, g);
+            zl[j] = compact_row_operand(L.Z + kCPlane, w, j, n, g);
+        }
+        if (j >= w / 2) {
+            yth[j] = compact_col_operand(L.Y, w, j, n, g);
+            ytl[j] = compact_col_operand(L.Y + kCPlane, w, j, n, g);
+            zth[j] = compact_col_operand(L.Z, w, j, n, g);
+            ztl[j] = compact_col_operand(L.Z + kCPlane, w, j, n, g);
+        }
     }
     const f32x4 G = row4(L.G, w, g), end = row4(L.end, w, g), be = row4(L.beta, w, g);
     const size_t ho = (tok + 16 * w + 4 * g) * a.dk + n, ko = ktok + (size_t)(16 * w + 4 * g) * a.dk + n;
 #pragma unroll
     for (int m = 0; m < NS; ++m) {
-        f32x4 tq = zero, tk = zero, tz = zero;
+        f32x4 t[3];   // (D.Y b) K, (D.Y b)^T Q, (D.Z b) K + (D.Z b)^T K
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const f16x8 kh = col_operand(L.K[0], KW, m, j, n, g), qh = col_operand(L.Q[0], KW, m, j, n, g);
@@ -392,11 +436,19 @@ __global__ __launch_bounds__(256) void delta_grads_kernel(DeltaBwdArgs b) {
                 kl = col_operand(L.K[1], KW, m, j, n, g);
                 ql = col_operand(L.Q[1], KW, m, j, n, g);
             }
-            tq = product<true, F>(yh[j], yl[j], kh, kl, tq);
-            tk = product<true, F>(yth[j], ytl[j], qh, ql, tk);
-            tz = product<true, F>(zh[j], zl[j], kh, kl, tz);
-            tz = product<true, F>(zth[j], ztl[j], kh, kl, tz);
+            if (j == 0) {
+                product<true, true, F>(t[0], yh[j], yl[j], kh, kl);
+                product<true, true, F>(t[1], yth[j], ytl[j], qh, ql);
+                product<true, true, F>(t[2], zh[j], zl[j], kh, kl);
+            } else {
+                product<false, true, F>(t[0], yh[j], yl[j], kh, kl);
+                product<false, true, F>(t[1], yth[j], ytl[j], qh, ql);
+                product<false, true, F>(t[2], zh[j], zl[j], kh, kl);
+            }
+            product<false, true, F>(t[2], zth[j], ztl[j], kh, kl);
         }
+        mfma_done(t);
+        const f32x4 tq = t[0], tk = t[1], tz = t[2];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             if (16 * w + 4 * g + r >= valid || 16 * m >= a.dk) continue;
