@@ -217,8 +217,8 @@ hipError_t launch_gate_norm_bwd(const GateNormBwdArgs& a, hipStream_t s) {
 // ------------------------------------------------------------ residual norm
 
 // W waves share a row (W = 1: each of a workgroup's four waves has its own);
-// a thread holds N pieces of V elements, piece j of thread t at column
-// V (t + 64 W j).
+// a thread holds N pieces of 8 elements, piece j of thread t at column
+// 8 (t + 64 W j).  Rows need no more than their elements' alignment.
 template <int W> struct RowGroup {
     static constexpr int threads = W == 1 ? 256 : 64 * W;
     static constexpr int rows = W == 1 ? 4 : 1;   // rows of a workgroup at a time
@@ -241,7 +241,7 @@ template <int W> struct RowGroup {
     }
 };
 
-template <int W, int V, int N, typename Hh, typename Y>
+template <int W, int N, bool WHOLE, typename Hh, typename Y>
 __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_kernel(ResidualNormArgs a) {
     using RG = RowGroup<W>;
     __shared__ float red[2][2][16];
@@ -250,82 +250,81 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_kernel(Res
     const long r = (long)blockIdx.x * RG::rows + (W == 1 ? threadIdx.x / 64 : 0);
     if (r >= a.R) return;   // a whole wave (W = 1), or never
     const size_t ro = (size_t)r * a.D;
-    float z[N][V], ss = 0.f, none = 0.f;
+    f32x8 z[N];
+    float ss = 0.f, none = 0.f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int f = V * (t + 64 * W * j);
-#pragma unroll
-        for (int e = 0; e < V; ++e) z[j][e] = 0.f;
-        if (f < a.D) {
-            load_v<V>(static_cast<const Hh*>(a.h) + ro + f, z[j]);
+        const int f = 8 * (t + 64 * W * j), left = a.D - f;
+        z[j] = f32x8{};
+        if (left > 0) {
+            z[j] = load8_upto<WHOLE>(static_cast<const Hh*>(a.h) + ro + f, left);
             if (a.y) {
-                float y[V], s[V];
-                load_v<V>(static_cast<const Y*>(a.y) + ro + f, y);
+                const f32x8 y = load8_upto<WHOLE>(static_cast<const Y*>(a.y) + ro + f, left);
+                if (a.scale) {
+                    const f32x8 s = load8_upto<WHOLE>(a.scale + f, left);
 #pragma unroll
-                for (int e = 0; e < V; ++e) s[e] = 1.0f;
-                if (a.scale) load_v<V>(a.scale + f, s);
+                    for (int e = 0; e < 8; ++e) z[j].v[e] += s.v[e] * y.v[e];
+                } else {
 #pragma unroll
-                for (int e = 0; e < V; ++e) z[j][e] += s[e] * y[e];
-                store_v<V>(static_cast<Hh*>(a.h_out) + ro + f, z[j]);
+                    for (int e = 0; e < 8; ++e) z[j].v[e] += y.v[e];
+                }
+                store8_upto<WHOLE>(static_cast<Hh*>(a.h_out) + ro + f, z[j], left);
             }
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) ss += z[j][e] * z[j][e];
+        for (int e = 0; e < 8; ++e) ss += z[j].v[e] * z[j].v[e];
     }
     RG::sum2(ss, none, red, flip);
     const float rs = rsqrtf(ss / (float)a.D + a.eps);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-        const int f = V * (t + 64 * W * j);
-        if (f < a.D) {
-            float w[V];
-            load_v<V>(a.w + f, w);
+        const int f = 8 * (t + 64 * W * j), left = a.D - f;
+        if (left > 0) {
+            f32x8 w = load8_upto<WHOLE>(a.w + f, left);
 #pragma unroll
-            for (int e = 0; e < V; ++e) w[e] *= z[j][e] * rs;
-            store_v<V>(static_cast<Y*>(a.n) + ro + f, w);
+            for (int e = 0; e < 8; ++e) w.v[e] *= z[j].v[e] * rs;
+            store8_upto<WHOLE>(static_cast<Y*>(a.n) + ro + f, w, left);
         }
     }
 }
 
 // Workgroup i takes row groups i, i + gridDim.x, ...; its sums of dw and ds go
 // to partial[i][0..D) and partial[i][D..2D).
-template <int W, int V, int N, typename Hh, typename Y>
+template <int W, int N, bool WHOLE, typename Hh, typename Y>
 __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel(ResidualNormBwdArgs a) {
     using RG = RowGroup<W>;
     __shared__ float red[2][2][16];
-    __shared__ float own[W == 1 ? 4 : 1][W == 1 ? 64 * V * N : 1];
+    __shared__ float own[W == 1 ? 4 : 1][W == 1 ? 64 * 8 * N : 1];
     int flip = 0;
     const int t = RG::tid(), wave = threadIdx.x / 64;
-    float dw[N][V] = {}, ds[N][V] = {};
+    float dw[N][8] = {}, ds[N][8] = {};
     const float inv_D = 1.0f / (float)a.D;
     for (long r = (long)blockIdx.x * RG::rows + (W == 1 ? wave : 0); r < a.R; r += (long)gridDim.x * RG::rows) {
         const size_t ro = (size_t)r * a.D;
-        float z[N][V], y[N][V], d[N][V], ss = 0.f, c = 0.f;
+        f32x8 z[N], y[N], d[N];
+        float ss = 0.f, c = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int f = V * (t + 64 * W * j);
-#pragma unroll
-            for (int e = 0; e < V; ++e) z[j][e] = y[j][e] = d[j][e] = 0.f;
-            if (f < a.D) {
-                load_v<V>(static_cast<const Hh*>(a.h) + ro + f, z[j]);
-                load_v<V>(static_cast<const Y*>(a.grad_n) + ro + f, d[j]);
-                if (a.y) load_v<V>(static_cast<const Y*>(a.y) + ro + f, y[j]);
+            const int f = 8 * (t + 64 * W * j), left = a.D - f;
+            z[j] = y[j] = d[j] = f32x8{};
+            if (left > 0) {
+                z[j] = load8_upto<WHOLE>(static_cast<const Hh*>(a.h) + ro + f, left);
+                d[j] = load8_upto<WHOLE>(static_cast<const Y*>(a.grad_n) + ro + f, left);
+                if (a.y) y[j] = load8_upto<WHOLE>(static_cast<const Y*>(a.y) + ro + f, left);
             }
         }
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int f = V * (t + 64 * W * j);
-            if (f < a.D) {
-                float s[V], w[V];
+            const int f = 8 * (t + 64 * W * j), left = a.D - f;
+            if (left > 0) {
+                const f32x8 w = load8_upto<WHOLE>(a.w + f, left);
+                f32x8 s{};
+                if (a.scale) s = load8_upto<WHOLE>(a.scale + f, left);
 #pragma unroll
-                for (int e = 0; e < V; ++e) s[e] = 1.0f;
-                if (a.scale) load_v<V>(a.scale + f, s);
-                load_v<V>(a.w + f, w);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    z[j][e] += s[e] * y[j][e];
-                    ss += z[j][e] * z[j][e];
-                    c += d[j][e] * w[e] * z[j][e];
+                for (int e = 0; e < 8; ++e) {
+                    z[j].v[e] += a.scale ? s.v[e] * y[j].v[e] : y[j].v[e];
+                    ss += z[j].v[e] * z[j].v[e];
+                    c += d[j].v[e] * w.v[e] * z[j].v[e];
                 }
             }
         }
@@ -334,26 +333,26 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel
         const float m = c * rs * rs * inv_D;   // mean(d_u u) rs
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int f = V * (t + 64 * W * j);
-            if (f < a.D) {
-                float s[V], w[V], dh[V], dz[V];
+            const int f = 8 * (t + 64 * W * j), left = a.D - f;
+            if (left > 0) {
+                const f32x8 w = load8_upto<WHOLE>(a.w + f, left);
+                f32x8 dz{};
+                if (a.grad_h_out) dz = load8_upto<WHOLE>(static_cast<const Hh*>(a.grad_h_out) + ro + f, left);
 #pragma unroll
-                for (int e = 0; e < V; ++e) { s[e] = 1.0f; dh[e] = 0.f; }
-                if (a.scale) load_v<V>(a.scale + f, s);
-                load_v<V>(a.w + f, w);
-                if (a.grad_h_out) load_v<V>(static_cast<const Hh*>(a.grad_h_out) + ro + f, dh);
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float u = z[j][e] * rs;
-                    dz[e] = rs * (d[j][e] * w[e]) - u * m + dh[e];
-                    dw[j][e] += d[j][e] * u;
-                    ds[j][e] += dz[e] * y[j][e];
+                for (int e = 0; e < 8; ++e) {
+                    const float u = z[j].v[e] * rs;
+                    dz.v[e] = rs * (d[j].v[e] * w.v[e]) - u * m + dz.v[e];
+                    dw[j][e] += d[j].v[e] * u;
+                    ds[j][e] += dz.v[e] * y[j].v[e];
                 }
-                store_v<V>(static_cast<Hh*>(a.grad_h) + ro + f, dz);
+                store8_upto<WHOLE>(static_cast<Hh*>(a.grad_h) + ro + f, dz, left);
                 if (a.grad_y) {
+                    if (a.scale) {
+                        const f32x8 s = load8_upto<WHOLE>(a.scale + f, left);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) dz[e] *= s[e];
-                    store_v<V>(static_cast<Y*>(a.grad_y) + ro + f, dz);
+                        for (int e = 0; e < 8; ++e) dz.v[e] *= s.v[e];
+                    }
+                    store8_upto<WHOLE>(static_cast<Y*>(a.grad_y) + ro + f, dz, left);
                 }
             }
         }
@@ -362,10 +361,10 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel
     if constexpr (W > 1) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int f = V * (t + 64 * W * j);
-            if (f < a.D)
+            const int f = 8 * (t + 64 * W * j);
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
+            for (int e = 0; e < 8; ++e)
+                if (f + e < a.D) {
                     out[f + e] = dw[j][e];
                     if (a.grad_scale) out[a.D + f + e] = ds[j][e];
                 }
@@ -376,7 +375,7 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel
 #pragma unroll
             for (int j = 0; j < N; ++j)
 #pragma unroll
-                for (int e = 0; e < V; ++e) own[wave][V * (t + 64 * j) + e] = k ? ds[j][e] : dw[j][e];
+                for (int e = 0; e < 8; ++e) own[wave][8 * (t + 64 * j) + e] = k ? ds[j][e] : dw[j][e];
             __syncthreads();
             for (int f = threadIdx.x; f < a.D; f += 256)
                 out[(size_t)k * a.D + f] = (own[0][f] + own[1][f]) + (own[2][f] + own[3][f]);
@@ -387,21 +386,22 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel
 // The row layouts built: D up to 512 and 2048 with a wave a row, up to 2048
 // with four waves and one piece a thread (few rows: the row's latency counts),
 // up to 8192 with four waves, up to 32768 with sixteen.
-template <template <int, int, int> class Go, typename A>
+template <template <int, int, bool> class Go, bool WHOLE, typename A>
+hipError_t residual_rows(const A& a, hipStream_t s) {
+    if (a.D <= 512) return Go<1, 1, WHOLE>::go(a, s);
+    if (a.D <= 2048) return a.R <= 1024 ? Go<4, 1, WHOLE>::go(a, s) : Go<1, 4, WHOLE>::go(a, s);
+    return a.D <= 8192 ? Go<4, 4, WHOLE>::go(a, s) : Go<16, 2, WHOLE>::go(a, s);
+}
+template <template <int, int, bool> class Go, typename A>
 hipError_t residual_shape(const A& a, hipStream_t s) {
-    const bool v8 = a.D % 8 == 0;
-    if (a.D <= 512) return v8 ? Go<1, 8, 1>::go(a, s) : Go<1, 1, 8>::go(a, s);
-    if (a.D <= 2048 && a.R <= 1024) return v8 ? Go<4, 8, 1>::go(a, s) : Go<4, 1, 8>::go(a, s);
-    if (a.D <= 2048) return v8 ? Go<1, 8, 4>::go(a, s) : Go<1, 1, 32>::go(a, s);
-    if (a.D <= 8192) return v8 ? Go<4, 8, 4>::go(a, s) : Go<4, 1, 32>::go(a, s);
-    return v8 ? Go<16, 8, 2>::go(a, s) : Go<16, 1, 16>::go(a, s);
+    return a.D % 8 == 0 ? residual_rows<Go, true>(a, s) : residual_rows<Go, false>(a, s);
 }
 
-template <int W, int V, int N> struct FwdGo {
+template <int W, int N, bool WHOLE> struct FwdGo {
     template <typename Hh, typename Y>
     static hipError_t one(const ResidualNormArgs& a, hipStream_t s) {
         using RG = RowGroup<W>;
-        hipLaunchKernelGGL((residual_norm_kernel<W, V, N, Hh, Y>), dim3((unsigned)((a.R + RG::rows - 1) / RG::rows)),
+        hipLaunchKernelGGL((residual_norm_kernel<W, N, WHOLE, Hh, Y>), dim3((unsigned)((a.R + RG::rows - 1) / RG::rows)),
                            dim3(RG::threads), 0, s, a);
         return hipGetLastError();
     }
@@ -410,10 +410,10 @@ template <int W, int V, int N> struct FwdGo {
         return a.y_bf16 ? one<float, bf16_t>(a, s) : one<float, float>(a, s);
     }
 };
-template <int W, int V, int N> struct BwdGo {
+template <int W, int N, bool WHOLE> struct BwdGo {
     template <typename Hh, typename Y>
     static hipError_t one(const ResidualNormBwdArgs& a, hipStream_t s) {
-        hipLaunchKernelGGL((residual_norm_bwd_kernel<W, V, N, Hh, Y>), dim3((unsigned)a.parts),
+        hipLaunchKernelGGL((residual_norm_bwd_kernel<W, N, WHOLE, Hh, Y>), dim3((unsigned)a.parts),
                            dim3(RowGroup<W>::threads), 0, s, a);
         return hipGetLastError();
     }

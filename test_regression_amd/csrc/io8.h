@@ -40,27 +40,65 @@ __device__ __forceinline__ void store8(bf16_t* p, const f32x8& r) {
                                               bf16_pair(r.v[4], r.v[5]), bf16_pair(r.v[6], r.v[7]));
 }
 
-// V = 8: one vector access; V = 1: a single element (rows that are not a
-// multiple of eight elements, so only element-aligned).
-template <int V, typename T>
-__device__ __forceinline__ void load_v(const T* p, float (&r)[V]) {
-    if constexpr (V == 8) {
-        const f32x8 x = load8(p);
+// The same at any element alignment, of the first `left` of the eight elements
+// (the others read as zeros and are not written).  With WHOLE, left is 8 or
+// more; without it a row's last, ragged piece goes element by element, which
+// costs a branch at every access.  The stores are streaming ones: the outputs
+// are larger than the caches, or too small for it to matter.
+typedef float f32x4_el __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_el __attribute__((ext_vector_type(4), aligned(2)));
+template <bool WHOLE>
+__device__ __forceinline__ f32x8 load8_upto(const float* p, int left) {
+    f32x8 r{};
+    if (WHOLE || left >= 8) {
+        const f32x4_el a = reinterpret_cast<const f32x4_el*>(p)[0], b = reinterpret_cast<const f32x4_el*>(p)[1];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[e] = x.v[e];
+        for (int e = 0; e < 4; ++e) { r.v[e] = a[e]; r.v[4 + e] = b[e]; }
     } else {
-        r[0] = to_f32(*p);
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) r.v[e] = p[e];
+    }
+    return r;
+}
+template <bool WHOLE>
+__device__ __forceinline__ f32x8 load8_upto(const bf16_t* p, int left) {
+    f32x8 r{};
+    if (WHOLE || left >= 8) {
+        const u32x4_el w = *reinterpret_cast<const u32x4_el*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r.v[2 * i] = __uint_as_float(w[i] << 16);
+            r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) r.v[e] = to_f32(p[e]);
+    }
+    return r;
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store8_upto(float* p, const f32x8& r, int left) {
+    if (WHOLE || left >= 8) {
+        __builtin_nontemporal_store(f32x4_el{r.v[0], r.v[1], r.v[2], r.v[3]}, reinterpret_cast<f32x4_el*>(p));
+        __builtin_nontemporal_store(f32x4_el{r.v[4], r.v[5], r.v[6], r.v[7]}, reinterpret_cast<f32x4_el*>(p) + 1);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) p[e] = r.v[e];
     }
 }
-template <int V, typename T>
-__device__ __forceinline__ void store_v(T* p, const float (&r)[V]) {
-    if constexpr (V == 8) {
-        f32x8 x;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x.v[e] = r[e];
-        store8(p, x);
+template <bool WHOLE>
+__device__ __forceinline__ void store8_upto(bf16_t* p, const f32x8& r, int left) {
+    if (WHOLE || left >= 8) {
+        __builtin_nontemporal_store(u32x4_el{bf16_pair(r.v[0], r.v[1]), bf16_pair(r.v[2], r.v[3]),
+                                             bf16_pair(r.v[4], r.v[5]), bf16_pair(r.v[6], r.v[7])},
+                                    reinterpret_cast<u32x4_el*>(p));
     } else {
-        store1(p, r[0]);
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < left) store1(p + e, r.v[e]);
     }
 }
 
