@@ -425,6 +425,20 @@ def mesa_hawk_scan(x, ga, gx, lam, c=8.0, h0=None, *, out=None, return_final=Fal
     return (out, hf) if return_final else out
 
 
+def _tensors(dev, *specs):
+    """Checks (tensor, name, shape, dtype) specs, tensors that are None left
+    out: every shape before any device, dtype or layout."""
+    for t, name, shape, _ in specs:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    for t, name, _, dtype in specs:
+        if t is not None and not (t.dtype is dtype and t.is_cuda and t.is_contiguous() and t.device == dev):
+            _need(t, name, dtype, dev)
+
+
+_HERE = contextlib.nullcontext()
+
+
 def _on(dev, stream):
     """The context in which a call allocates and enqueues: the tensors' device,
     and `stream` when one is given (which then owns what is allocated)."""
@@ -433,39 +447,35 @@ def _on(dev, stream):
         if stream.device != dev:
             raise ValueError(f"stream is on {stream.device}, expected {dev}")
         return torch.cuda.stream(stream)
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
-def _bytes(workspace, nbytes, dev):
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _here(dev):
+    """The raw handle of dev's current stream."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _scratch(workspace, nbytes, dev):
     """(workspace, its size): the caller's, checked, or a new one."""
     import torch
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    else:
-        _need(workspace, "workspace", None, dev)
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev), max(nbytes, 16)
+    _need(workspace, "workspace", None, dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
-def _delta_checks(q, k, v, gamma, beta, state, lead, **more):
-    """Shapes, dtypes and devices of a delta-rule call whose tensors are
-    [lead..., ...]: (B, H) and T tokens, or (N, H) of one token.  Returns (B,
-    Hk, H, T, dk, dv); `more` holds (tensor, shape of its last axes, dtype)."""
-    import torch
-    nd = 4 if lead == "T" else 3
-    B, Hk, *t, dk = _dims(q, "q", nd)
-    H, dv = _dims(v, "v", nd)[1], v.shape[-1]
-    _shapes((k, "k", (B, Hk, *t, dk)), (v, "v", (B, H, *t, dv)), (gamma, "gamma", (B, H, *t)), (beta, "beta", (B, H, *t)),
-            *_given((state, "state", (B, H, dv, dk))), *_given(*((x, n, (B, H, *t, dv) if s == "out" else (B, H, dv, dk))
-                                                             for n, (x, s) in more.items())))
-    if H % Hk:
+def _delta_sizes(q, v, ndim):
+    """(B or N, Hk, H, the token axis, dk, dv) of a delta-rule call."""
+    B, Hk, *t, dk = _dims(q, "q", ndim)
+    _, H, *_, dv = _dims(v, "v", ndim)
+    if H % Hk if Hk else H:
         raise ValueError(f"{H} value heads are not a multiple of {Hk} key heads")
-    _qkv_dtype(q)
-    f32 = torch.float32
-    for x, n, dt in ((q, "q", q.dtype), (k, "k", q.dtype), (v, "v", q.dtype), (gamma, "gamma", f32), (beta, "beta", f32),
-                     (state, "state", f32), *((x, n, q.dtype if s == "out" else f32) for n, (x, s) in more.items())):
-        if x is not None:
-            _need(x, n, dt, q.device)
-    return B, Hk, H, t[0] if t else 1, dk, dv
+    return B, Hk, H, t, dk, dv
 
 
 def mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype) -> int:
@@ -482,17 +492,22 @@ def mesa_delta_forward(q, k, v, gamma, beta, state=None, *, out=None, return_fin
     None); final_state may be the state passed in.
     """
     import torch
-    B, Hk, H, T, dk, dv = _delta_checks(q, k, v, gamma, beta, state, "T", out=(out, "out"),
-                                        final_state=(final_state, "state"))
-    dev, dt = q.device, _qkv_dtype(q)
+    B, Hk, H, (T,), dk, dv = _delta_sizes(q, v, 4)
+    dev, dt, code, f32 = q.device, q.dtype, _qkv_dtype(q), torch.float32
+    gates, states = (B, H, T), (B, H, dv, dk)
+    _tensors(dev, (q, "q", (B, Hk, T, dk), dt), (k, "k", (B, Hk, T, dk), dt), (v, "v", (B, H, T, dv), dt),
+             (gamma, "gamma", gates, f32), (beta, "beta", gates, f32), (state, "state", states, f32),
+             (out, "out", (B, H, T, dv), dt), (final_state, "final_state", states, f32))
     with _on(dev, stream):
         if out is None:
-            out = torch.empty((B, H, T, dv), dtype=q.dtype, device=dev)
+            out = torch.empty((B, H, T, dv), dtype=dt, device=dev)
         if return_final and final_state is None:
-            final_state = torch.empty((B, H, dv, dk), dtype=torch.float32, device=dev)
-        workspace, nbytes = _bytes(workspace, mesa_delta_workspace_bytes(B, H, T, dk, dv, dt), dev)
-        st = lib().mesa_delta_forward(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(gamma), _ptr(beta), _ptr(state), B, Hk, H, T,
-                                      dk, dv, _ptr(out), _ptr(final_state), _ptr(workspace), nbytes, _stream(None))
+            final_state = torch.empty(states, dtype=f32, device=dev)
+        L = lib()
+        workspace, nbytes = _scratch(workspace, L.mesa_delta_workspace_bytes(B, H, T, dk, dv, code), dev)
+        st = L.mesa_delta_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, gamma.data_ptr(), beta.data_ptr(),
+                                  _at(state), B, Hk, H, T, dk, dv, out.data_ptr(), _at(final_state),
+                                  workspace.data_ptr(), nbytes, _here(dev))
     _check(st, "mesa_delta_forward")
     return out, final_state
 
@@ -509,18 +524,23 @@ def mesa_delta_backward(q, k, v, gamma, beta, grad_out, state=None, *, grad_fina
     grad_gamma, grad_beta and grad_state (float32; None without a state).
     """
     import torch
-    B, Hk, H, T, dk, dv = _delta_checks(q, k, v, gamma, beta, state, "T", grad_out=(grad_out, "out"),
-                                        grad_final=(grad_final, "state"))
-    dev, dt = q.device, _qkv_dtype(q)
+    B, Hk, H, (T,), dk, dv = _delta_sizes(q, v, 4)
+    dev, dt, code, f32 = q.device, q.dtype, _qkv_dtype(q), torch.float32
+    gates, states = (B, H, T), (B, H, dv, dk)
+    _tensors(dev, (q, "q", (B, Hk, T, dk), dt), (k, "k", (B, Hk, T, dk), dt), (v, "v", (B, H, T, dv), dt),
+             (gamma, "gamma", gates, f32), (beta, "beta", gates, f32), (state, "state", states, f32),
+             (grad_out, "grad_out", (B, H, T, dv), dt), (grad_final, "grad_final", states, f32))
     with _on(dev, stream):
         g = dict(grad_q=torch.empty_like(q), grad_k=torch.empty_like(k), grad_v=torch.empty_like(v),
                  grad_gamma=torch.empty_like(gamma), grad_beta=torch.empty_like(beta),
                  grad_state=None if state is None else torch.empty_like(state))
-        workspace, nbytes = _bytes(workspace, mesa_delta_backward_workspace_bytes(B, Hk, H, T, dk, dv, dt), dev)
-        st = lib().mesa_delta_backward(_ptr(q), _ptr(k), _ptr(v), dt, _ptr(gamma), _ptr(beta), _ptr(state),
-                                       _ptr(grad_out), _ptr(grad_final), B, Hk, H, T, dk, dv, _ptr(g["grad_q"]),
-                                       _ptr(g["grad_k"]), _ptr(g["grad_v"]), _ptr(g["grad_gamma"]), _ptr(g["grad_beta"]),
-                                       _ptr(g["grad_state"]), _ptr(workspace), nbytes, _stream(None))
+        L = lib()
+        workspace, nbytes = _scratch(workspace, L.mesa_delta_backward_workspace_bytes(B, Hk, H, T, dk, dv, code), dev)
+        st = L.mesa_delta_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, gamma.data_ptr(), beta.data_ptr(),
+                                   _at(state), grad_out.data_ptr(), _at(grad_final), B, Hk, H, T, dk, dv,
+                                   g["grad_q"].data_ptr(), g["grad_k"].data_ptr(), g["grad_v"].data_ptr(),
+                                   g["grad_gamma"].data_ptr(), g["grad_beta"].data_ptr(), _at(g["grad_state"]),
+                                   workspace.data_ptr(), nbytes, _here(dev))
     _check(st, "mesa_delta_backward")
     return g
 
@@ -532,27 +552,33 @@ def mesa_delta_step(q, k, v, gamma, beta, state, *, out=None, stream=None):
     q, k: [N,Hk,dk]; v: [N,H,dv]; gamma, beta: [N,H].  Returns out [N,H,dv].
     """
     import torch
-    N, Hk, H, _, dk, dv = _delta_checks(q, k, v, gamma, beta, state, "", out=(out, "out"))
-    with _on(q.device, stream):
+    N, Hk, H, _, dk, dv = _delta_sizes(q, v, 3)
+    dev, dt, code, f32 = q.device, q.dtype, _qkv_dtype(q), torch.float32
+    _tensors(dev, (q, "q", (N, Hk, dk), dt), (k, "k", (N, Hk, dk), dt), (v, "v", (N, H, dv), dt),
+             (gamma, "gamma", (N, H), f32), (beta, "beta", (N, H), f32), (state, "state", (N, H, dv, dk), f32),
+             (out, "out", (N, H, dv), dt))
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
-        st = lib().mesa_delta_step(_ptr(q), _ptr(k), _ptr(v), _qkv_dtype(q), _ptr(gamma), _ptr(beta), _ptr(state), N, Hk,
-                                   H, dk, dv, _ptr(out), _stream(None))
+            out = torch.empty((N, H, dv), dtype=dt, device=dev)
+        st = lib().mesa_delta_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), code, gamma.data_ptr(), beta.data_ptr(),
+                                   state.data_ptr(), N, Hk, H, dk, dv, out.data_ptr(), _here(dev))
     _check(st, "mesa_delta_step")
     return out
 
 
 def _gate_checks(x, gate, w, grad_y=None, y=None, dtype=None):
+    """Checks a gate norm's tensors; returns (B, H, T, d, dtype of y)."""
     import torch
     B, H, T, d = _dims(x, "x", 4)
     rows = (B, T, H, d)
-    _shapes((w, "w", (H, d)), *_given((gate, "gate", rows), (grad_y, "grad_y", rows), (y, "y", rows)))
-    dtype = next((t.dtype for t in (gate, grad_y, y) if t is not None), x.dtype if dtype is None else dtype)
-    _need(x, "x", None, None)
-    _qkv_dtype(x)
-    for t, n, dt in ((gate, "gate", dtype), (w, "w", torch.float32), (grad_y, "grad_y", dtype), (y, "y", dtype)):
+    for t in (gate, grad_y, y):
         if t is not None:
-            _need(t, n, dt, x.device)
+            dtype = t.dtype
+            break
+    else:
+        dtype = x.dtype if dtype is None else dtype
+    _tensors(x.device, (x, "x", (B, H, T, d), x.dtype), (w, "w", (H, d), torch.float32), (gate, "gate", rows, dtype),
+             (grad_y, "grad_y", rows, dtype), (y, "out", rows, dtype))
     return B, H, T, d, dtype
 
 
@@ -564,11 +590,12 @@ def mesa_gate_norm(x, gate, w, eps=1e-6, *, out=None, out_dtype=None, stream=Non
     """
     import torch
     B, H, T, d, dtype = _gate_checks(x, gate, w, y=out, dtype=out_dtype)
-    with _on(x.device, stream):
+    dev = x.device
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty((B, T, H, d), dtype=dtype, device=x.device)
-        st = lib().mesa_gate_norm(_ptr(x), _qkv_dtype(x), _ptr(gate), _qkv_dtype(out), _ptr(w), float(eps), B, H, T, d,
-                                  _ptr(out), _stream(None))
+            out = torch.empty((B, T, H, d), dtype=dtype, device=dev)
+        st = lib().mesa_gate_norm(x.data_ptr(), _qkv_dtype(x), _at(gate), _qkv_dtype(out), w.data_ptr(), eps, B, H, T, d,
+                                  out.data_ptr(), _here(dev))
     _check(st, "mesa_gate_norm")
     return out
 
@@ -582,29 +609,31 @@ def mesa_gate_norm_backward(x, gate, w, grad_y, eps=1e-6, *, workspace=None, str
     with _on(dev, stream):
         g = dict(grad_x=torch.empty_like(x), grad_gate=None if gate is None else torch.empty_like(gate),
                  grad_w=torch.empty((H, d), dtype=torch.float32, device=dev))
-        workspace, nbytes = _bytes(workspace, int(lib().mesa_gate_norm_backward_workspace_bytes(B, H, T, d)), dev)
-        st = lib().mesa_gate_norm_backward(_ptr(x), _qkv_dtype(x), _ptr(gate), _qkv_dtype(grad_y), _ptr(w), float(eps),
-                                           _ptr(grad_y), B, H, T, d, _ptr(g["grad_x"]), _ptr(g["grad_gate"]),
-                                           _ptr(g["grad_w"]), _ptr(workspace), nbytes, _stream(None))
+        L = lib()
+        workspace, nbytes = _scratch(workspace, L.mesa_gate_norm_backward_workspace_bytes(B, H, T, d), dev)
+        st = L.mesa_gate_norm_backward(x.data_ptr(), _qkv_dtype(x), _at(gate), _qkv_dtype(grad_y), w.data_ptr(), eps,
+                                       grad_y.data_ptr(), B, H, T, d, g["grad_x"].data_ptr(), _at(g["grad_gate"]),
+                                       g["grad_w"].data_ptr(), workspace.data_ptr(), nbytes, _here(dev))
     _check(st, "mesa_gate_norm_backward")
     return g
 
 
 def _residual_checks(h, y, w, scale, grad_n=None, grad_h_out=None, n=None, h_out=None, dtype=None):
+    """Checks a residual norm's tensors; returns (R, D, dtype of n)."""
     import torch
     R, D = _dims(h, "h", 2)
-    _shapes((w, "w", (D,)), *_given((y, "y", (R, D)), (scale, "scale", (D,)), (grad_n, "grad_n", (R, D)),
-                                    (grad_h_out, "grad_h_out", (R, D)), (n, "n", (R, D)), (h_out, "h_out", (R, D))))
     if y is None and (scale is not None or h_out is not None):
         raise ValueError("scale and h_out need y")
-    dtype = next((t.dtype for t in (y, grad_n, n) if t is not None), h.dtype if dtype is None else dtype)
-    _need(h, "h", None, None)
-    _qkv_dtype(h)
-    f32 = torch.float32
-    for t, name, dt in ((y, "y", dtype), (w, "w", f32), (scale, "scale", f32), (grad_n, "grad_n", dtype),
-                        (grad_h_out, "grad_h_out", h.dtype), (n, "n", dtype), (h_out, "h_out", h.dtype)):
+    for t in (y, grad_n, n):
         if t is not None:
-            _need(t, name, dt, h.device)
+            dtype = t.dtype
+            break
+    else:
+        dtype = h.dtype if dtype is None else dtype
+    rows, ht, f32 = (R, D), h.dtype, torch.float32
+    _tensors(h.device, (h, "h", rows, ht), (y, "y", rows, dtype), (w, "w", (D,), f32), (scale, "scale", (D,), f32),
+             (grad_n, "grad_n", rows, dtype), (grad_h_out, "grad_h_out", rows, ht), (n, "n", rows, dtype),
+             (h_out, "h_out", rows, ht))
     return R, D, dtype
 
 
@@ -624,8 +653,8 @@ def mesa_residual_norm(h, y, w, scale=None, eps=1e-6, *, h_out=None, n=None, out
             n = torch.empty((R, D), dtype=dtype, device=dev)
         if y is not None and h_out is None:
             h_out = torch.empty_like(h)
-        st = lib().mesa_residual_norm(_ptr(h), _qkv_dtype(h), _ptr(y), _qkv_dtype(n), _ptr(scale), _ptr(w), float(eps),
-                                      R, D, _ptr(h_out), _ptr(n), _stream(None))
+        st = lib().mesa_residual_norm(h.data_ptr(), _qkv_dtype(h), _at(y), _qkv_dtype(n), _at(scale), w.data_ptr(), eps,
+                                      R, D, _at(h_out), n.data_ptr(), _here(dev))
     _check(st, "mesa_residual_norm")
     return (h if y is None else h_out), n
 
@@ -641,11 +670,12 @@ def mesa_residual_norm_backward(h, y, w, grad_n, scale=None, eps=1e-6, *, grad_h
         f32 = dict(dtype=torch.float32, device=dev)
         g = dict(grad_h=torch.empty_like(h), grad_y=None if y is None else torch.empty_like(y),
                  grad_w=torch.empty((D,), **f32), grad_scale=None if scale is None else torch.empty((D,), **f32))
-        workspace, nbytes = _bytes(workspace, int(lib().mesa_residual_norm_backward_workspace_bytes(R, D)), dev)
-        st = lib().mesa_residual_norm_backward(_ptr(h), _qkv_dtype(h), _ptr(y), _qkv_dtype(grad_n), _ptr(scale), _ptr(w),
-                                               float(eps), _ptr(grad_n), _ptr(grad_h_out), R, D, _ptr(g["grad_h"]),
-                                               _ptr(g["grad_y"]), _ptr(g["grad_w"]), _ptr(g["grad_scale"]),
-                                               _ptr(workspace), nbytes, _stream(None))
+        L = lib()
+        workspace, nbytes = _scratch(workspace, L.mesa_residual_norm_backward_workspace_bytes(R, D), dev)
+        st = L.mesa_residual_norm_backward(h.data_ptr(), _qkv_dtype(h), _at(y), _qkv_dtype(grad_n), _at(scale),
+                                           w.data_ptr(), eps, grad_n.data_ptr(), _at(grad_h_out), R, D,
+                                           g["grad_h"].data_ptr(), _at(g["grad_y"]), g["grad_w"].data_ptr(),
+                                           _at(g["grad_scale"]), workspace.data_ptr(), nbytes, _here(dev))
     _check(st, "mesa_residual_norm_backward")
     return g
 
