@@ -16,7 +16,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmesa.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 SOURCES = ["mesa_host.hip", "chunk_states.hip", "cg_output.hip", "cg_output_bf16.hip", "decode.hip", "qk_preprocess.hip",
-           "bwd_adjoint.hip", "bwd_states.hip", "bwd_kv.hip", "bwd_gate.hip", "hawk.hip", "delta_prep.hip", "delta_scan.hip", "delta_scan_split.hip",
+           "bwd_adjoint.hip", "bwd_states.hip", "bwd_kv.hip", "bwd_gate.hip", "hawk.hip", "delta_prep.hip", "delta_scan.hip", "delta_scan_split.hip", "delta_segments.hip",
            "delta_bwd_scan.hip", "delta_bwd_split.hip", "delta_grads.hip", "delta_step.hip", "block_norms.hip", "probes.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -158,8 +158,9 @@ def scan_inline_asm(text: str):
 #  - a VALU result needs VALU_TO_MFMA wait states before one reads it;
 #  - its result may only be touched by MFMAs that accumulate onto it for
 #    ASM_MFMA_RESULT wait states (the compiler leaves 8 after the 16x16x32
-#    fp16 MFMA).
+#    fp16 MFMA; the 16x16x4 float one takes twice its passes).
 ASM_MFMA_RESULT = 8
+ASM_MFMA_F32_RESULT = 11
 
 
 def scan_asm_mfma(text: str):
@@ -182,7 +183,7 @@ def scan_asm_mfma(text: str):
             waits += _wait_states(u)
         waits = 0
         for u, _ in ins[i + 1:]:
-            if waits >= ASM_MFMA_RESULT:
+            if waits >= (ASM_MFMA_F32_RESULT if "16x16x4_f32" in t else ASM_MFMA_RESULT):
                 break
             m, uops = _operand_regs(u)
             if m.startswith("v_mfma"):

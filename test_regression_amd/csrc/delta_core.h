@@ -116,10 +116,14 @@ __device__ __forceinline__ f16x8 h2_hi_mix(const f32x4& a, const f32x4& b, float
 // written.  Inline asm is opaque to its hazard bookkeeping: mfma_ready() stands
 // between VALU writes of the accumulators and the first MFMA on them (two wait
 // states), mfma_done() between the last one and the first use of the results
-// (12; 8 are asked for); codegen_check.py checks the distances in the built
+// (12; 8 are asked for, 11 after the float one); codegen_check.py checks the distances in the built
 // code.  Operands come from LDS or from the mix splits, which wait by themselves.
 __device__ __forceinline__ void mfma_acc(f32x4& c, f16x8 a, f16x8 b) {
     asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+}
+// four k-slots of float
+__device__ __forceinline__ void mfma4_acc(f32x4& c, float a, float b) {
+    asm("v_mfma_f32_16x16x4_f32 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
 // onto zero
 __device__ __forceinline__ void mfma_first(f32x4& c, f16x8 a, f16x8 b) {

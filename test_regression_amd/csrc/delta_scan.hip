@@ -267,10 +267,14 @@ hipError_t scan_go(const DeltaArgs& a, hipStream_t s) {
 // Float rows of 128 features need two planes of K twice in the split
 // kernel's LDS, which does not hold them; everything else takes that kernel.
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) {
-    return a.bf16 || a.dk < 128 ? launch_delta_scan_split(a, s) : scan_go<true, false>(a, s);
+    if (!a.bf16 && a.dk == 128) return scan_go<true, false>(a, s);
+    const hipError_t e = launch_delta_segments(a, s);
+    return e != hipSuccess ? e : launch_delta_scan_split(a, s);
 }
 hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s) {
-    return a.bf16 || a.dk < 128 ? launch_delta_states_split(a, s) : scan_go<false, true>(a, s);
+    if (!a.bf16 && a.dk == 128) return scan_go<false, true>(a, s);
+    const hipError_t e = launch_delta_segments(a, s);
+    return e != hipSuccess ? e : launch_delta_states_split(a, s);
 }
 
 }  // namespace mesa

@@ -13,6 +13,11 @@
 //   second half   E, update        --                  Q, P of c; K, V of c + 1 in
 // so K is held twice in LDS and everything else once.
 //
+// With few heads the sequence is cut into segments that are passed over at once
+// (delta_segments.hip): first each segment but the last from a zero state (ENDS:
+// nothing but the end state is written) and, for its transition, from the dk
+// unit states with no values; then all from their joined start states.
+//
 // A wave alone on its SIMD issues one vector instruction in 5 cycles (9 for
 // the mixed-precision ones of the splits) while the SIMD could take one in
 // 1.3 from several waves (measured); the pass is bound by the state waves' own
@@ -64,29 +69,38 @@ struct ValueUnits {
     }
 };
 
-template <int DKP, typename In, bool OUT, bool SAVE>
+template <int DKP, typename In, bool OUT, bool SAVE, bool ENDS = !OUT && !SAVE>
 __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int waves) {
     using Lds = ScanSplitLds<DKP, In, OUT>;
     constexpr int NP = Lds::NP, NJ = Lds::NJ, NS = DKP / 16, KW = Lds::KW;
     __shared__ Lds L;
     const int lane = threadIdx.x % 64, w12 = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = w12 % 4;
     const int n = lane & 15, g = lane >> 4;
-    // the column groups of a head on one XCD (workgroups go to the 8 XCDs in turn)
-    const int cols = 16 * waves, cgs = (a.dv + cols - 1) / cols;
-    const int bh = (int)(blockIdx.x / (8 * cgs)) * 8 + blockIdx.x % 8;
-    if (bh >= a.BH) return;
+    // the column groups of a head's segment on one XCD (workgroups go to the 8 XCDs in turn)
+    const int nseg = ENDS ? a.nseg - 1 : a.nseg, all_cols = ENDS ? a.dv + a.dk : a.dv;
+    const int cols = 16 * waves, cgs = (all_cols + cols - 1) / cols;
+    const int vh = (int)(blockIdx.x / (8 * cgs)) * 8 + blockIdx.x % 8;
+    if (vh >= a.BH * nseg) return;
+    const int bh = vh / nseg, seg = vh % nseg;
+    const int c0 = seg * a.seg_chunks, c1 = min(a.nc, c0 + a.seg_chunks);   // its chunks
     const int colg = cols * (int)(blockIdx.x / 8 % cgs), col0 = colg + 16 * w;
-    const bool live = w < waves && col0 < a.dv;
-    const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;   // this lane's row of the (dv x dk) state
-
+    const bool live = w < waves && col0 < (ENDS && seg > 0 ? all_cols : a.dv);
+    const size_t so = (size_t)(col0 + n) * a.dk + 4 * g;   // this lane's row of a (dv x dk) state
+    if (ENDS && seg == 0 && colg >= a.dv) return;          // the first segment needs no transition
     if (w12 < 4) {
         // ---------------- the state's chain ----------------
         f32x4 S[NS];   // the state times 2^cs
         int cs = 0;
+        const float* from = seg == 0 ? (a.state0 ? a.state0 + (size_t)bh * a.dv * a.dk : nullptr)
+                                     : ENDS ? nullptr : a.seg_start + (size_t)vh * a.dv * a.dk;
 #pragma unroll
-        for (int m = 0; m < NS; ++m)
-            S[m] = a.state0 && live && 16 * m < a.dk ? load4(a.state0 + so + 16 * m) : f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int chunk = 0; chunk < a.nc; ++chunk) {
+        for (int m = 0; m < NS; ++m) {
+            S[m] = from && live && 16 * m < a.dk ? load4(from + so + 16 * m) : f32x4{0.f, 0.f, 0.f, 0.f};
+            if (ENDS && col0 >= a.dv)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[m][r] = 16 * m + 4 * g + r == col0 - a.dv + n ? 1.f : 0.f;
+        }
+        for (int chunk = c0; chunk < c1; ++chunk) {
             const int c = opaque(chunk);
             __syncthreads();
             const float* sc = L.sc[c & 1];
@@ -95,7 +109,7 @@ __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int 
             if (live) {
                 if constexpr (SAVE) {
                     const float s = pow2(-cs);
-                    float* sp = a.S + ((size_t)bh * a.nc + c) * a.dv * a.dk + (size_t)(col0 + n) * a.dk + 4 * g;
+                    float* sp = a.S + ((size_t)bh * a.nc + c) * a.dv * a.dk + so;
 #pragma unroll
                     for (int m = 0; m < NS; ++m)
                         if (16 * m < a.dk) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
@@ -214,11 +228,13 @@ __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int 
             }
             mfma_done(S);
         }
-        if (a.final_state && live) {
+        float* to = ENDS ? a.seg_end + (size_t)vh * all_cols * a.dk
+                         : a.final_state && seg == nseg - 1 ? a.final_state + (size_t)bh * a.dv * a.dk : nullptr;
+        if (to && live) {
             const float s = pow2(-cs);
 #pragma unroll
             for (int m = 0; m < NS; ++m)
-                if (16 * m < a.dk) *reinterpret_cast<f32x4*>(a.final_state + so + 16 * m) = S[m] * s;
+                if (16 * m < a.dk) *reinterpret_cast<f32x4*>(to + so + 16 * m) = S[m] * s;
         }
         __syncthreads();
     } else if (w12 < 8) {
@@ -313,18 +329,18 @@ __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int 
 #pragma unroll
             for (int i = 0; i < 4; ++i) store4(lane_at(ep, lo + i * pitch), tile_row(L.E[w], i, lane));
         };
-        for (int chunk = 0; chunk < a.nc; ++chunk) {
+        for (int chunk = c0; chunk < c1; ++chunk) {
             const int c = opaque(chunk);
             __syncthreads();
-            if (chunk > 0) {
+            if (chunk > c0) {
                 if constexpr (OUT) output(c - 1);
-                else e_out(c - 1);
+                if constexpr (SAVE) e_out(c - 1);
             }
             __syncthreads();
         }
         __syncthreads();
-        if constexpr (OUT) output(a.nc - 1);
-        else e_out(a.nc - 1);
+        if constexpr (OUT) output(c1 - 1);
+        if constexpr (SAVE) e_out(c1 - 1);
     } else {
         // ---------------- staging ----------------
         const int tid = threadIdx.x - 512;
@@ -370,18 +386,18 @@ __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int 
             if (tid < kScal / 4) *reinterpret_cast<f32x4*>(L.sc[c & 1] + 4 * tid) = scr;
         };
         // every fetch is a whole chunk ahead of its store
-        fetch_k(0);
-        fetch_m(0);
-        if constexpr (OUT) fetch_q(0);
-        put_k(0);
-        if (a.nc > 1) fetch_k(1);
-        for (int chunk = 0; chunk < a.nc; ++chunk) {
+        fetch_k(c0);
+        fetch_m(c0);
+        if constexpr (OUT) fetch_q(c0);
+        put_k(c0);
+        if (c0 + 1 < c1) fetch_k(c0 + 1);
+        for (int chunk = c0; chunk < c1; ++chunk) {
             const int c = opaque(chunk);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < MUnits::n; ++i)
                 if (MUnits::has(i)) *reinterpret_cast<u32x4*>(compact_unit(L.M, tid + 256 * i)) = mr.raw[i];
-            if (chunk + 1 < a.nc) fetch_m(chunk + 1);
+            if (chunk + 1 < c1) fetch_m(chunk + 1);
             __syncthreads();
             if constexpr (OUT) {
 #pragma unroll
@@ -389,11 +405,11 @@ __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int 
 #pragma unroll
                 for (int i = 0; i < PUnits::n; ++i)
                     if (PUnits::has(i)) *reinterpret_cast<u32x4*>(compact_unit(L.P, tid + 256 * i)) = pr.raw[i];
-                if (chunk + 1 < a.nc) fetch_q(chunk + 1);
+                if (chunk + 1 < c1) fetch_q(chunk + 1);
             }
-            if (chunk + 1 < a.nc) {
+            if (chunk + 1 < c1) {
                 put_k(c + 1);
-                if (chunk + 2 < a.nc) fetch_k(chunk + 2);
+                if (chunk + 2 < c1) fetch_k(chunk + 2);
             }
         }
         __syncthreads();
@@ -402,8 +418,10 @@ __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int 
 
 template <int DKP, typename In, bool OUT, bool SAVE>
 hipError_t scan_split_go(const DeltaArgs& a, hipStream_t s) {
-    const int waves = scan_waves(a.BH, a.dv);
-    const dim3 grid((unsigned)((a.BH + 7) / 8 * 8 * ((a.dv + 16 * waves - 1) / (16 * waves))));
+    constexpr bool ENDS = !OUT && !SAVE;
+    const long heads = a.BH * (ENDS ? a.nseg - 1 : a.nseg);
+    const int all_cols = ENDS ? a.dv + a.dk : a.dv, waves = scan_waves(heads, all_cols);
+    const dim3 grid((unsigned)((heads + 7) / 8 * 8 * ((all_cols + 16 * waves - 1) / (16 * waves))));
     hipLaunchKernelGGL((delta_scan_split_kernel<DKP, In, OUT, SAVE>), grid, dim3(768), 0, s, a, waves);
     return hipGetLastError();
 }
@@ -416,5 +434,6 @@ hipError_t scan_split_dk(const DeltaArgs& a, hipStream_t s) {
 
 hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<true, false>(a, s); }
 hipError_t launch_delta_states_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<false, true>(a, s); }
+hipError_t launch_delta_ends_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<false, false>(a, s); }
 
 }  // namespace mesa

@@ -554,9 +554,22 @@ static size_t delta_image_halfs(int dtype) {
 }
 static long delta_chunks(int T) { return ((long)T + mesa::kDeltaChunk - 1) / mesa::kDeltaChunk; }
 
+// Bytes of the segments' end and start states (0 with one segment).
+static size_t delta_segment_bytes(long BH, int nseg, int dk, int dv) {
+    return nseg > 1 ? (size_t)BH * ((size_t)(nseg - 1) * (dv + dk) + (size_t)nseg * dv) * dk * sizeof(float) : 0;
+}
+static void delta_use_segments(mesa::DeltaArgs* a, int nseg, float* ws) {
+    a->nseg = nseg;
+    a->seg_chunks = (a->nc + nseg - 1) / nseg;
+    a->seg_end = ws;
+    a->seg_start = ws + (size_t)a->BH * (nseg - 1) * (a->dv + a->dk) * a->dk;
+}
+
 size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype) {
     if (B <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
-    return (size_t)B * H * delta_chunks(T) * (delta_image_halfs(dtype) * 2 + mesa::kDeltaScal * sizeof(float));
+    const long BH = (long)B * H, nc = delta_chunks(T);
+    return (size_t)BH * nc * (delta_image_halfs(dtype) * 2 + mesa::kDeltaScal * sizeof(float)) +
+           delta_segment_bytes(BH, mesa::delta_segments(BH, (int)nc, dk, dv, dtype == MESA_DTYPE_BF16), dk, dv);
 }
 
 // The checks the delta entry points share; `rows` is T or, for the step, 1.
@@ -607,8 +620,9 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
                     mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype));
     uint16_t* img = static_cast<uint16_t*>(workspace);
     float* scal = reinterpret_cast<float*>(img + (size_t)BH * nc * delta_image_halfs(dtype));
-    const mesa::DeltaArgs a{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
-                            out, final_state, img, scal, dtype == MESA_DTYPE_BF16 ? 1 : 2, nullptr, nullptr};
+    mesa::DeltaArgs a{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
+                      out, final_state, img, scal, dtype == MESA_DTYPE_BF16 ? 1 : 2};
+    delta_use_segments(&a, mesa::delta_segments(BH, (int)nc, dk, dv, a.bf16), scal + (size_t)BH * nc * mesa::kDeltaScal);
     hipError_t e = timed_launch(MESA_KERNEL_DELTA_PREP, s, [&] { return mesa::launch_delta_prep(a, s); });
     if (e != hipSuccess) return hip_fail(e, "delta chunk-matrix kernel launch");
     e = timed_launch(MESA_KERNEL_DELTA_SCAN, s, [&] { return mesa::launch_delta_scan(a, s); });
@@ -618,9 +632,10 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
 
 // Backward workspace, offsets in bytes (every segment a multiple of 16).
 struct DeltaBwdLayout {
-    size_t scal, S, dS, E, dR, part, total;
+    size_t scal, S, dS, E, dR, seg, part, total;
+    int nseg;
 };
-static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int dv) {
+static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int dv, int dtype) {
     const size_t n = (size_t)B * H * delta_chunks(T), C = mesa::kDeltaChunk;
     DeltaBwdLayout l{};
     size_t o = n * delta_image_halfs(MESA_DTYPE_F32) * 2;   // two planes of M and of P for either type
@@ -629,6 +644,8 @@ static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int 
     l.dS = o;   o += n * dv * dk * sizeof(float);
     l.E = o;    o += n * C * dv * sizeof(float);
     l.dR = o;   o += n * C * dv * sizeof(float);
+    l.nseg = mesa::delta_segments((long)B * H, (int)delta_chunks(T), dk, dv, dtype == MESA_DTYPE_BF16);
+    l.seg = o;  o += delta_segment_bytes((long)B * H, l.nseg, dk, dv);
     l.part = o; o += H != Hk ? 2 * (size_t)B * H * T * dk * sizeof(float) : 0;
     l.total = o;
     return l;
@@ -636,7 +653,7 @@ static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int 
 
 size_t mesa_delta_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype) {
     if (B <= 0 || Hk <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
-    return delta_bwd_layout(B, Hk, H, T, dk, dv).total;
+    return delta_bwd_layout(B, Hk, H, T, dk, dv, dtype).total;
 }
 
 mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int dtype, const float* gamma,
@@ -669,7 +686,7 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
     for (const void* o : outs)
         for (const void* i : ins)
             if (o == i) return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
-    const DeltaBwdLayout l = delta_bwd_layout(B, Hk, H, T, dk, dv);
+    const DeltaBwdLayout l = delta_bwd_layout(B, Hk, H, T, dk, dv, dtype);
     if (workspace_bytes < l.total)
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, l.total);
     char* ws = static_cast<char*>(workspace);
@@ -677,6 +694,7 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
     mesa::DeltaBwdArgs a{};
     a.f = mesa::DeltaArgs{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
                           nullptr, nullptr, reinterpret_cast<uint16_t*>(ws), at(l.scal), 2, at(l.S), at(l.E)};
+    delta_use_segments(&a.f, l.nseg, at(l.seg));
     a.grad_out = grad_out;
     a.grad_final = grad_final;
     a.grad_q = grad_q;

@@ -104,6 +104,9 @@ struct DeltaArgs {
     uint16_t* img; float* scal;   // workspace: per head and chunk the planes of M and P, the scalars
     int p_planes;                 // planes of P in img: 1 (bf16 forward) or 2
     float* S; float* E;           // backward workspace: chunk start states [BH][nc][dv][dk], E [BH][nc][64][dv]
+    int nseg; int seg_chunks;     // segments of a sequence that are passed over at once, chunks of one
+    float* seg_end;               // nseg > 1, workspace: [BH][nseg - 1][dv + dk][dk] (delta_segments.hip)
+    float* seg_start;             // and [BH][nseg][dv][dk], the segments' start states from the second on
 };
 struct DeltaBwdArgs {
     DeltaArgs f;                  // q, k, v, gamma, beta, state0, sizes, img, scal, S, E
@@ -119,6 +122,9 @@ hipError_t launch_delta_prep(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s);     // the same with its chain on waves of its own (not float with dk 128)
 hipError_t launch_delta_states_split(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_ends_split(const DeltaArgs& a, hipStream_t s);    // the segments' end states and transitions
+hipError_t launch_delta_segments(const DeltaArgs& a, hipStream_t s);      // and from them the segments' start states
+int delta_segments(long BH, int nc, int dk, int dv, int bf16);            // the number of segments
 hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E
 struct DeltaStepArgs {
     const void* q; const void* k; const void* v; const float* gamma; const float* beta; float* state;

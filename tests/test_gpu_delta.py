@@ -67,6 +67,19 @@ def test_delta_forward_long(dtype):
     check(*delta_inputs(11, 1, 2, 2, 2000, 128, 64, dtype, lo=0.97), dtype)
 
 
+# Long sequences of few heads are passed over in segments at once (from about
+# 30 chunks on): ragged last segments, odd head counts, every width.
+LONG = [(1, 1, 1, 2100, 16, 16), (1, 1, 3, 2500, 32, 64), (1, 2, 2, 4160, 64, 128), (1, 1, 1, 2300, 128, 256),
+        (2, 1, 1, 8229, 16, 32), (1, 3, 3, 3000, 128, 16)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hk,H,T,dk,dv", LONG)
+def test_delta_forward_segments(B, Hk, H, T, dk, dv, dtype):
+    say("case delta segments", (B, Hk, H, T, dk, dv, dtype))
+    check(*delta_inputs(13 + T, B, Hk, H, T, dk, dv, dtype, start=T % 2 == 0, lo=0.97), dtype)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("what", ["strong", "none", "full", "still", "same_keys", "orthogonal", "tiny", "huge", "zeros",
                                   "reset"])
@@ -267,6 +280,13 @@ def test_delta_backward_shapes(dk, dv, T, dtype):
 def test_delta_backward_heads(B, Hk, H, T, dtype):
     say("case delta backward heads", (B, Hk, H, T, dtype))
     check_grads(*delta_inputs(17 + T, B, Hk, H, T, 64, 128, dtype), dtype, T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,Hk,H,T,dk,dv", LONG)
+def test_delta_backward_segments(B, Hk, H, T, dk, dv, dtype):
+    say("case delta backward segments", (B, Hk, H, T, dk, dv, dtype))
+    check_grads(*delta_inputs(19 + T, B, Hk, H, T, dk, dv, dtype, start=T % 2 == 0, lo=0.97), dtype, T, T % 2 == 0)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
