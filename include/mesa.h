@@ -88,7 +88,7 @@ typedef enum {
     MESA_KERNEL_DELTA_PREP = 16,     /* delta rule: the chunks' state-free matrices      */
     MESA_KERNEL_DELTA_SCAN = 17,     /* delta rule: the pass over the chunks             */
     MESA_KERNEL_DELTA_STEP = 18,     /* delta rule: one token                            */
-    MESA_KERNEL_DELTA_BWD_SCAN = 19, /* delta rule: the backward's pass over the chunks  */
+    MESA_KERNEL_DELTA_BWD_SCAN = 19, /* delta rule: the backward's passes over the chunks */
     MESA_KERNEL_DELTA_GRADS = 20,    /* delta rule: gradients per chunk, sums over heads */
     MESA_KERNEL_GATE_NORM = 21,      /* norm and gate of a layer's outputs               */
     MESA_KERNEL_GATE_NORM_BWD = 22,

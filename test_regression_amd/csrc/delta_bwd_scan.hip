@@ -237,13 +237,14 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
     }
 }
 
-// Float rows of 128 features: two planes of K, twice, do not fit the
-// split kernel's LDS; everything else takes that kernel.
-hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& b, hipStream_t s) {
-    if (b.f.bf16 || b.f.dk < 128) return launch_delta_bwd_split(b, s);
+// Float rows of 128 features: two planes of K, twice, do not fit the split
+// kernels' LDS; everything else takes those.
+hipError_t launch_delta_passes(const DeltaBwdArgs& b, hipStream_t s) {
+    if (b.f.bf16 || b.f.dk < 128) return launch_delta_passes_split(b, s);
+    const hipError_t e = launch_delta_states(b.f, s);
+    if (e != hipSuccess) return e;
     const int waves = scan_waves(b.f.BH, b.f.dv);
-    const dim3 grid((unsigned)((b.f.BH + 7) / 8 * 8 * ((b.f.dv + 16 * waves - 1) / (16 * waves))));
-    hipLaunchKernelGGL((delta_bwd_scan_kernel<128, float>), grid, dim3(256), 0, s, b, waves);
+    hipLaunchKernelGGL((delta_bwd_scan_kernel<128, float>), dim3(scan_blocks(b.f.BH, b.f.dv, waves)), dim3(256), 0, s, b, waves);
     return hipGetLastError();
 }
 

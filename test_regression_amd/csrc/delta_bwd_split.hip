@@ -11,7 +11,11 @@
 //   first half of c    split, K dS', dE    N of c, dV of c + 1 out    M of c, P of c - 1 in
 //   second half of c   dV, update          T of c - 1                 K, Q of c - 1 in
 // K is held twice in LDS.
-#include "delta_core.h"
+//
+// The pass needs nothing of the forward's recomputation (the chunks' start
+// states and E, delta_scan_split.h), nor that of it, so one launch holds the
+// workgroups of both: with few heads they fill the GPU together.
+#include "delta_scan_split.h"
 
 namespace mesa {
 
@@ -28,17 +32,16 @@ struct alignas(16) BwdSplitLds {
 };
 
 template <int DKP, typename In>
-__global__ __launch_bounds__(768) void delta_bwd_split_kernel(DeltaBwdArgs b, int waves) {
+__device__ __forceinline__ void bwd_split(BwdSplitLds<DKP, In>& L, const DeltaBwdArgs& b, int waves, unsigned block) {
     using Lds = BwdSplitLds<DKP, In>;
     constexpr int NP = Lds::NP, NJ = DKP / 32, NS = Lds::NS, KW = Lds::KW;
-    __shared__ Lds L;
     const DeltaArgs& a = b.f;
     const int lane = threadIdx.x % 64, w12 = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = w12 % 4;
     const int n = lane & 15, g = lane >> 4;
     const int cols = 16 * waves, cgs = (a.dv + cols - 1) / cols;
-    const int bh = (int)(blockIdx.x / (8 * cgs)) * 8 + blockIdx.x % 8;
+    const int bh = (int)(block / (8 * cgs)) * 8 + block % 8;
     if (bh >= a.BH) return;
-    const int col0 = cols * (int)(blockIdx.x / 8 % cgs) + 16 * w;
+    const int col0 = cols * (int)(block / 8 % cgs) + 16 * w;
     const bool live = w < waves && col0 < a.dv;
     const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;
 
@@ -353,17 +356,29 @@ __global__ __launch_bounds__(768) void delta_bwd_split_kernel(DeltaBwdArgs b, in
 }
 
 template <int DKP, typename In>
-hipError_t bwd_split_go(const DeltaBwdArgs& b, hipStream_t s) {
-    const int waves = scan_waves(b.f.BH, b.f.dv);
-    const dim3 grid((unsigned)((b.f.BH + 7) / 8 * 8 * ((b.f.dv + 16 * waves - 1) / (16 * waves))));
-    hipLaunchKernelGGL((delta_bwd_split_kernel<DKP, In>), grid, dim3(768), 0, s, b, waves);
+__global__ __launch_bounds__(768) void delta_passes_kernel(DeltaBwdArgs b, int waves, unsigned bwd_blocks) {
+    __shared__ union {
+        BwdSplitLds<DKP, In> b;
+        ScanSplitLds<DKP, In, false> f;
+    } L;
+    // the longer pass first
+    if (blockIdx.x < bwd_blocks) bwd_split<DKP, In>(L.b, b, waves, blockIdx.x);
+    else scan_split<DKP, In, false, true>(L.f, b.f, waves, blockIdx.x - bwd_blocks);
+}
+
+template <int DKP, typename In>
+hipError_t passes_go(const DeltaBwdArgs& b, hipStream_t s) {
+    const DeltaArgs& a = b.f;
+    const int waves = scan_waves(a.BH * (1 + a.nseg), a.dv);
+    const unsigned bwd = scan_blocks(a.BH, a.dv, waves), fwd = scan_blocks(a.BH * a.nseg, a.dv, waves);
+    hipLaunchKernelGGL((delta_passes_kernel<DKP, In>), dim3(bwd + fwd), dim3(768), 0, s, b, waves, bwd);
     return hipGetLastError();
 }
 
-hipError_t launch_delta_bwd_split(const DeltaBwdArgs& b, hipStream_t s) {
-    if (!b.f.bf16) return b.f.dk <= 32 ? bwd_split_go<32, float>(b, s) : bwd_split_go<64, float>(b, s);
-    return b.f.dk <= 32 ? bwd_split_go<32, bf16_t>(b, s)
-                        : b.f.dk == 64 ? bwd_split_go<64, bf16_t>(b, s) : bwd_split_go<128, bf16_t>(b, s);
+hipError_t launch_delta_passes_split(const DeltaBwdArgs& b, hipStream_t s) {
+    if (!b.f.bf16) return b.f.dk <= 32 ? passes_go<32, float>(b, s) : passes_go<64, float>(b, s);
+    return b.f.dk <= 32 ? passes_go<32, bf16_t>(b, s)
+                        : b.f.dk == 64 ? passes_go<64, bf16_t>(b, s) : passes_go<128, bf16_t>(b, s);
 }
 
 }  // namespace mesa

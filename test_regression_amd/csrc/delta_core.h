@@ -315,5 +315,9 @@ inline int scan_waves(long BH, int dv) {
     const long tiles = BH * (dv / 16);
     return tiles <= 256 ? 1 : tiles <= 512 ? 2 : 4;
 }
+// Its workgroups: heads in eights, one a XCD, and their column groups.
+inline unsigned scan_blocks(long heads, int cols, int waves) {
+    return (unsigned)((heads + 7) / 8 * 8 * ((cols + 16 * waves - 1) / (16 * waves)));
+}
 
 }  // namespace mesa

@@ -259,22 +259,18 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
 template <bool OUT, bool SAVE>
 hipError_t scan_go(const DeltaArgs& a, hipStream_t s) {
     const int waves = scan_waves(a.BH, a.dv);
-    const dim3 grid((unsigned)((a.BH + 7) / 8 * 8 * ((a.dv + 16 * waves - 1) / (16 * waves))));
-    hipLaunchKernelGGL((delta_scan_kernel<128, float, OUT, SAVE>), grid, dim3(256), 0, s, a, waves);
+    hipLaunchKernelGGL((delta_scan_kernel<128, float, OUT, SAVE>), dim3(scan_blocks(a.BH, a.dv, waves)), dim3(256), 0, s, a,
+                       waves);
     return hipGetLastError();
 }
 
-// Float rows of 128 features need two planes of K twice in the split
-// kernel's LDS, which does not hold them; everything else takes that kernel.
+// Float rows of 128 features need two planes of K twice in the split kernel's
+// LDS, which does not hold them; everything else takes that kernel.
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) {
     if (!a.bf16 && a.dk == 128) return scan_go<true, false>(a, s);
     const hipError_t e = launch_delta_segments(a, s);
     return e != hipSuccess ? e : launch_delta_scan_split(a, s);
 }
-hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s) {
-    if (!a.bf16 && a.dk == 128) return scan_go<false, true>(a, s);
-    const hipError_t e = launch_delta_segments(a, s);
-    return e != hipSuccess ? e : launch_delta_states_split(a, s);
-}
+hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s) { return scan_go<false, true>(a, s); }
 
 }  // namespace mesa

@@ -1,439 +1,30 @@
-// delta_scan_split.hip -- the gated delta rule's pass over the chunks with the
-// state's chain and everything beside it on different waves (gfx950).
-//
-// The chain of delta_scan.hip, split over the twelve waves of a workgroup, three
-// a SIMD.  Waves 0..3 each own 16 dv columns of the state and run what the
-// next chunk waits for:
-//   X = K S,  E = M (V - G X),  S' = G_C S + K^T (D_C b E)
-// Waves 4..7 form the outputs of the chunk before, O = G Q S + (P diag(b)) E,
-// from the fp16 parts of S and E that the state waves leave in LDS (in the
-// backward's recomputation they write E out).  Waves 8..11 stage the chunks.
-// Two barriers a chunk; between them:
-//   first half    split S, X, R    O of chunk c - 1    M of c in
-//   second half   E, update        --                  Q, P of c; K, V of c + 1 in
-// so K is held twice in LDS and everything else once.
-//
-// With few heads the sequence is cut into segments that are passed over at once
-// (delta_segments.hip): first each segment but the last from a zero state (ENDS:
-// nothing but the end state is written) and, for its transition, from the dk
-// unit states with no values; then all from their joined start states.
-//
-// A wave alone on its SIMD issues one vector instruction in 5 cycles (9 for
-// the mixed-precision ones of the splits) while the SIMD could take one in
-// 1.3 from several waves (measured); the pass is bound by the state waves' own
-// instructions and latencies, which is why nothing else is left to them.
-#include "delta_core.h"
+// delta_scan_split.hip -- launches of the gated delta rule's pass over the chunks
+// (delta_scan_split.h): the forward's, and the segments' ends.
+#include "delta_scan_split.h"
 
 namespace mesa {
 
 template <int DKP, typename In, bool OUT>
-struct alignas(16) ScanSplitLds {
-    static constexpr int NP = delta_planes<In>(), KW = delta_row_words(DKP), NJ = DKP / 32;
-    static constexpr int VW = sizeof(In) == 2 ? 8 : 20;   // words of a row of 16 values
-    static constexpr int parts = NP * (NJ + 2);           // operands of S and of E that the outputs take
-    uint32_t K[2][NP][kDC * KW];
-    uint32_t M[2 * kCPlane];
-    uint32_t V[4][kDC * VW];
-    uint32_t Q[OUT ? NP : 1][OUT ? kDC * KW : 4];
-    uint32_t P[OUT ? NP * kCPlane : 4];
-    union {
-        f16x8 ex[4][parts][64];             // for the outputs, whose waves then turn O around here
-        f32x4 E[4][4 * kTileSlots];         // for the recomputation
-    };
-    float is[4][64], iu[4][64];
-    float sc[2][kScal];
-};
-
-// The units of a chunk's rows of v (16 `waves` columns) on their way into LDS.
-template <typename In>
-struct ValueUnits {
-    static constexpr int per = 16 / sizeof(In), n = 64 * 64 / per / 256;   // values of a unit; units a thread at most
-    u32x4 raw[n];
-    __device__ __forceinline__ void load(const In* p, int dv, int cols, int left, int valid, int tid) {
-        const int row_units = cols / per;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const int u = tid + 256 * i, row = u / row_units, c = u % row_units * per;
-            raw[i] = u32x4{0u, 0u, 0u, 0u};
-            if (row < kDC && c < left) raw[i] = *reinterpret_cast<const u32x4*>(lane_at(p, ((uint32_t)min(row, valid - 1) * dv + c) * sizeof(In)));
-        }
-    }
-    template <int W>
-    __device__ __forceinline__ void store(uint32_t (&V)[4][kDC * W], int cols, int tid) const {
-        const int row_units = cols / per;
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const int u = tid + 256 * i, row = u / row_units, c = u % row_units * per;
-            if (row < kDC) *reinterpret_cast<u32x4*>(&V[c / 16][row * W + c % 16 * sizeof(In) / 4]) = raw[i];
-        }
-    }
-};
-
-template <int DKP, typename In, bool OUT, bool SAVE, bool ENDS = !OUT && !SAVE>
 __global__ __launch_bounds__(768) void delta_scan_split_kernel(DeltaArgs a, int waves) {
-    using Lds = ScanSplitLds<DKP, In, OUT>;
-    constexpr int NP = Lds::NP, NJ = Lds::NJ, NS = DKP / 16, KW = Lds::KW;
-    __shared__ Lds L;
-    const int lane = threadIdx.x % 64, w12 = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), w = w12 % 4;
-    const int n = lane & 15, g = lane >> 4;
-    // the column groups of a head's segment on one XCD (workgroups go to the 8 XCDs in turn)
-    const int nseg = ENDS ? a.nseg - 1 : a.nseg, all_cols = ENDS ? a.dv + a.dk : a.dv;
-    const int cols = 16 * waves, cgs = (all_cols + cols - 1) / cols;
-    const int vh = (int)(blockIdx.x / (8 * cgs)) * 8 + blockIdx.x % 8;
-    if (vh >= a.BH * nseg) return;
-    const int bh = vh / nseg, seg = vh % nseg;
-    const int c0 = seg * a.seg_chunks, c1 = min(a.nc, c0 + a.seg_chunks);   // its chunks
-    const int colg = cols * (int)(blockIdx.x / 8 % cgs), col0 = colg + 16 * w;
-    const bool live = w < waves && col0 < (ENDS && seg > 0 ? all_cols : a.dv);
-    const size_t so = (size_t)(col0 + n) * a.dk + 4 * g;   // this lane's row of a (dv x dk) state
-    if (ENDS && seg == 0 && colg >= a.dv) return;          // the first segment needs no transition
-    if (w12 < 4) {
-        // ---------------- the state's chain ----------------
-        f32x4 S[NS];   // the state times 2^cs
-        int cs = 0;
-        const float* from = seg == 0 ? (a.state0 ? a.state0 + (size_t)bh * a.dv * a.dk : nullptr)
-                                     : ENDS ? nullptr : a.seg_start + (size_t)vh * a.dv * a.dk;
-#pragma unroll
-        for (int m = 0; m < NS; ++m) {
-            S[m] = from && live && 16 * m < a.dk ? load4(from + so + 16 * m) : f32x4{0.f, 0.f, 0.f, 0.f};
-            if (ENDS && col0 >= a.dv)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[m][r] = 16 * m + 4 * g + r == col0 - a.dv + n ? 1.f : 0.f;
-        }
-        for (int chunk = c0; chunk < c1; ++chunk) {
-            const int c = opaque(chunk);
-            __syncthreads();
-            const float* sc = L.sc[c & 1];
-            f16x8 Sh[NJ], Sl[NJ], Bh[2], Bl[2];
-            int es = 0, er = 0;
-            if (live) {
-                if constexpr (SAVE) {
-                    const float s = pow2(-cs);
-                    float* sp = a.S + ((size_t)bh * a.nc + c) * a.dv * a.dk + so;
-#pragma unroll
-                    for (int m = 0; m < NS; ++m)
-                        if (16 * m < a.dk) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
-                }
-                // ---- X = K S ----
-                es = column_exp(S);
-                column_split(S, es, Sh, Sl);
-                f32x4 X[4];
-                const auto& K = L.K[c & 1];
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    f16x8 kh[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kh[i] = row_operand(K[0], KW, i, j, n, g);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) j ? mfma_acc(X[i], kh[i], Sl[j]) : mfma_first(X[i], kh[i], Sl[j]);
-                    if constexpr (NP == 2)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) mfma_acc(X[i], row_operand(K[NP - 1], KW, i, j, n, g), Sh[j]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mfma_acc(X[i], kh[i], Sh[j]);
-                }
-                mfma_done(X);
-                // ---- R = V - G X ----
-                const float is = pow2(-es - cs);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 gk = row4(sc + kGk, i, g);
-                    f32x4 v;
-                    if constexpr (sizeof(In) == 2) {
-                        const f16x4 t = lds_tr_f16x4(&L.V[w][(16 * i + 4 * g + (n >> 2)) * Lds::VW + 2 * (n & 3)]);
-                        const uint2 u = __builtin_bit_cast(uint2, t);
-                        v = f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                  __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)};
-                    } else {
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] = __uint_as_float(L.V[w][(16 * i + 4 * g + r) * Lds::VW + n]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) X[i][r] = v[r] - (gk[r] * is) * X[i][r];
-                }
-                er = column_exp(X);
-                column_split(X, er, Bh, Bl);
-            }
-            __syncthreads();
-            if (!live) continue;
-            if constexpr (OUT) {
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    L.ex[w][j][lane] = Sh[j];
-                    if constexpr (NP == 2) L.ex[w][NJ + 2 + j][lane] = Sl[j];
-                }
-                L.is[w][lane] = pow2(-es - cs);
-            }
-            // ---- E = M R ----
-            f32x4 U[4];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {   // row tiles 2 j and up reach column block j
-                f16x8 mh[4], ml[4];
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) {
-                    mh[i] = compact_row_operand(L.M, i, j, n, g);
-                    ml[i] = compact_row_operand(L.M + kCPlane, i, j, n, g);
-                }
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(U[i], mh[i], Bl[j]) : mfma_first(U[i], mh[i], Bl[j]);
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) mfma_acc(U[i], ml[i], Bh[j]);
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) mfma_acc(U[i], mh[i], Bh[j]);
-            }
-            mfma_done(U);
-            const float ir = sc[kMi] * pow2(-er);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) U[i] *= ir;
-            if constexpr (SAVE)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) L.E[w][tile_slot(i, n, g)] = U[i];
-            if constexpr (OUT) {
-                const int eu = column_exp(U);
-                f16x8 Eh[2], El[2];
-                if constexpr (NP == 2) column_split(U, eu, Eh, El);
-                else column_hi(U, eu, Eh);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    L.ex[w][NJ + j][lane] = Eh[j];
-                    if constexpr (NP == 2) L.ex[w][2 * NJ + 2 + j][lane] = El[j];
-                }
-                L.iu[w][lane] = sc[kPi] * pow2(-eu);
-            }
-            // ---- S' = G_C S + K^T (D_C b E) ----
-#pragma unroll
-            for (int i = 0; i < 4; ++i) U[i] *= row4(sc + kDb, i, g);
-            // a write that is 2^25 times smaller than the state takes a scale at
-            // which the scaled state stays below 2^40
-            const int ew = min(column_exp(U), es + cs + 25);
-            column_split(U, ew, Bh, Bl);
-            const float gs = __builtin_amdgcn_ldexpf(sc[kGc], ew - cs);
-            cs = ew;
-#pragma unroll
-            for (int m = 0; m < NS; ++m) S[m] *= gs;
-            mfma_ready(S);
-            const auto& K = L.K[c & 1];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f16x8 kh[NS];
-#pragma unroll
-                for (int m = 0; m < NS; ++m) kh[m] = col_operand(K[0], KW, m, j, n, g);
-#pragma unroll
-                for (int m = 0; m < NS; ++m) mfma_acc(S[m], kh[m], Bl[j]);
-                if constexpr (NP == 2)
-#pragma unroll
-                    for (int m = 0; m < NS; ++m) mfma_acc(S[m], col_operand(K[NP - 1], KW, m, j, n, g), Bh[j]);
-#pragma unroll
-                for (int m = 0; m < NS; ++m) mfma_acc(S[m], kh[m], Bh[j]);
-            }
-            mfma_done(S);
-        }
-        float* to = ENDS ? a.seg_end + (size_t)vh * all_cols * a.dk
-                         : a.final_state && seg == nseg - 1 ? a.final_state + (size_t)bh * a.dv * a.dk : nullptr;
-        if (to && live) {
-            const float s = pow2(-cs);
-#pragma unroll
-            for (int m = 0; m < NS; ++m)
-                if (16 * m < a.dk) *reinterpret_cast<f32x4*>(to + so + 16 * m) = S[m] * s;
-        }
-        __syncthreads();
-    } else if (w12 < 8) {
-        // ---------------- outputs of the chunk before, or E out ----------------
-        In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col0 : nullptr;
-        auto output = [&](int c) {
-            if (!live) return;
-            const float* sc = L.sc[c & 1];
-            f16x8 Sh[NJ], Sl[NJ], Eh[2], El[2];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                Sh[j] = L.ex[w][j][lane];
-                if constexpr (NP == 2) Sl[j] = L.ex[w][NJ + 2 + j][lane];
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                Eh[j] = L.ex[w][NJ + j][lane];
-                if constexpr (NP == 2) El[j] = L.ex[w][2 * NJ + 2 + j][lane];
-            }
-            f32x4 Y[4], Z[4];
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                f16x8 qh[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qh[i] = row_operand(L.Q[0], KW, i, j, n, g);
-                if constexpr (NP == 2) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) j ? mfma_acc(Y[i], qh[i], Sl[j]) : mfma_first(Y[i], qh[i], Sl[j]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) mfma_acc(Y[i], row_operand(L.Q[NP - 1], KW, i, j, n, g), Sh[j]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) NP == 2 || j ? mfma_acc(Y[i], qh[i], Sh[j]) : mfma_first(Y[i], qh[i], Sh[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f16x8 ph[4];
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) ph[i] = compact_row_operand(L.P, i, j, n, g);
-                if constexpr (NP == 2) {
-#pragma unroll
-                    for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(Z[i], ph[i], El[j]) : mfma_first(Z[i], ph[i], El[j]);
-#pragma unroll
-                    for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], compact_row_operand(L.P + (NP - 1) * kCPlane, i, j, n, g), Eh[j]);
-                }
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) NP == 2 || j ? mfma_acc(Z[i], ph[i], Eh[j]) : mfma_first(Z[i], ph[i], Eh[j]);
-            }
-            mfma_done(Y);
-            mfma_done(Z);
-            const float is = L.is[w][lane], iu = L.iu[w][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 gq = row4(sc + kGq, i, g), qi = row4(sc + kQi, i, g);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) Y[i][r] = (gq[r] * is) * Y[i][r] + (qi[r] * iu) * Z[i][r];
-            }
-            const int valid = min(kDC, a.T - c * kDC);
-            In* op = Op + (size_t)c * kDC * a.dv;
-            // turned around in this wave's own part of ex, which is read
-            const uint32_t lo = (lane / 4 * a.dv + lane % 4 * 4) * sizeof(In), pitch = fresh(16 * a.dv * sizeof(In), c);
-            wave_lds_sync();
-            if constexpr (sizeof(In) == 2) {
-                uint2* T = reinterpret_cast<uint2*>(L.ex[w]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    T[tile_slot(i, n, g)] = make_uint2(bf16_pair(Y[i][0], Y[i][1]), bf16_pair(Y[i][2], Y[i][3]));
-                wave_lds_sync();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = lane / 4;
-                    const uint16_t* p = reinterpret_cast<const uint16_t*>(T + tile_slot(i, 4 * (lane % 4), row / 4)) + row % 4;
-                    const uint2 v = make_uint2(p[0] | (uint32_t)p[4] << 16, p[8] | (uint32_t)p[12] << 16);
-                    if (16 * i + row < valid) *reinterpret_cast<uint2*>(lane_at(op, lo + i * pitch)) = v;
-                }
-            } else {
-                f32x4* T = reinterpret_cast<f32x4*>(L.ex[w]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) T[tile_slot(i, n, g)] = Y[i];
-                wave_lds_sync();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 v = tile_row(T, i, lane);
-                    if (16 * i + lane / 4 < valid) store4(lane_at(op, lo + i * pitch), v);
-                }
-            }
-        };
-        auto e_out = [&](int c) {
-            if (!live) return;
-            float* ep = a.E + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
-            const uint32_t lo = (lane / 4 * a.dv + lane % 4 * 4) * 4, pitch = fresh(16 * a.dv * 4, c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) store4(lane_at(ep, lo + i * pitch), tile_row(L.E[w], i, lane));
-        };
-        for (int chunk = c0; chunk < c1; ++chunk) {
-            const int c = opaque(chunk);
-            __syncthreads();
-            if (chunk > c0) {
-                if constexpr (OUT) output(c - 1);
-                if constexpr (SAVE) e_out(c - 1);
-            }
-            __syncthreads();
-        }
-        __syncthreads();
-        if constexpr (OUT) output(c1 - 1);
-        if constexpr (SAVE) e_out(c1 - 1);
-    } else {
-        // ---------------- staging ----------------
-        const int tid = threadIdx.x - 512;
-        const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
-        const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
-        const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
-        const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + colg;
-        const size_t image = (size_t)(2 + a.p_planes) * kPlaneUnits * 8;
-        const uint16_t* img = a.img + (size_t)bh * a.nc * image;
-        const float* scal = a.scal + (size_t)bh * a.nc * kScal;
-        using Units = RowUnits<DKP, In>;
-        using MUnits = PlaneUnits<2>;
-        using PUnits = PlaneUnits<NP>;
-        Units kr, qr;
-        MUnits mr;
-        PUnits pr;
-        ValueUnits<In> vr;
-        float ksr[Units::n], qsr[Units::n];
-        f32x4 scr{0.f, 0.f, 0.f, 0.f};
-        // K, V and scalars; M; Q and P of a chunk
-        auto fetch_k = [&](int chunk) {
-            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
-            kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
-            vr.load(Vp + (size_t)c * kDC * a.dv, a.dv, cols, a.dv - colg, valid, tid);
-            const float* sc = scal + (size_t)c * kScal;
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) ksr[i] = *lane_at(sc + kKs, 4 * Units::row(i));
-            if (tid < kScal / 4) scr = load4(lane_at(sc, 16 * tid));
-        };
-        auto fetch_m = [&](int chunk) { mr.load(img + opaque(chunk) * image); };
-        auto fetch_q = [&](int chunk) {
-            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
-            qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
-            const float* sc = scal + (size_t)c * kScal;
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) qsr[i] = *lane_at(sc + kQs, 4 * Units::row(i));
-            pr.load(img + c * image + 2 * kPlaneUnits * 8);
-        };
-        auto put_k = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < Units::n; ++i) kr.template store<NP>(L.K[c & 1], i, ksr[i]);
-            vr.template store<Lds::VW>(L.V, cols, tid);
-            if (tid < kScal / 4) *reinterpret_cast<f32x4*>(L.sc[c & 1] + 4 * tid) = scr;
-        };
-        // every fetch is a whole chunk ahead of its store
-        fetch_k(c0);
-        fetch_m(c0);
-        if constexpr (OUT) fetch_q(c0);
-        put_k(c0);
-        if (c0 + 1 < c1) fetch_k(c0 + 1);
-        for (int chunk = c0; chunk < c1; ++chunk) {
-            const int c = opaque(chunk);
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < MUnits::n; ++i)
-                if (MUnits::has(i)) *reinterpret_cast<u32x4*>(compact_unit(L.M, tid + 256 * i)) = mr.raw[i];
-            if (chunk + 1 < c1) fetch_m(chunk + 1);
-            __syncthreads();
-            if constexpr (OUT) {
-#pragma unroll
-                for (int i = 0; i < Units::n; ++i) qr.template store<NP>(L.Q, i, qsr[i]);
-#pragma unroll
-                for (int i = 0; i < PUnits::n; ++i)
-                    if (PUnits::has(i)) *reinterpret_cast<u32x4*>(compact_unit(L.P, tid + 256 * i)) = pr.raw[i];
-                if (chunk + 1 < c1) fetch_q(chunk + 1);
-            }
-            if (chunk + 1 < c1) {
-                put_k(c + 1);
-                if (chunk + 2 < c1) fetch_k(chunk + 2);
-            }
-        }
-        __syncthreads();
-    }
+    __shared__ ScanSplitLds<DKP, In, OUT> L;
+    scan_split<DKP, In, OUT, false>(L, a, waves, blockIdx.x);
 }
 
-template <int DKP, typename In, bool OUT, bool SAVE>
+template <int DKP, typename In, bool OUT>
 hipError_t scan_split_go(const DeltaArgs& a, hipStream_t s) {
-    constexpr bool ENDS = !OUT && !SAVE;
-    const long heads = a.BH * (ENDS ? a.nseg - 1 : a.nseg);
-    const int all_cols = ENDS ? a.dv + a.dk : a.dv, waves = scan_waves(heads, all_cols);
-    const dim3 grid((unsigned)((heads + 7) / 8 * 8 * ((all_cols + 16 * waves - 1) / (16 * waves))));
-    hipLaunchKernelGGL((delta_scan_split_kernel<DKP, In, OUT, SAVE>), grid, dim3(768), 0, s, a, waves);
+    const long heads = a.BH * (OUT ? a.nseg : a.nseg - 1);
+    const int cols = OUT ? a.dv : a.dv + a.dk, waves = scan_waves(heads, cols);
+    hipLaunchKernelGGL((delta_scan_split_kernel<DKP, In, OUT>), dim3(scan_blocks(heads, cols, waves)), dim3(768), 0, s, a, waves);
     return hipGetLastError();
 }
-template <bool OUT, bool SAVE>
+template <bool OUT>
 hipError_t scan_split_dk(const DeltaArgs& a, hipStream_t s) {
-    if (!a.bf16) return a.dk <= 32 ? scan_split_go<32, float, OUT, SAVE>(a, s) : scan_split_go<64, float, OUT, SAVE>(a, s);
-    return a.dk <= 32 ? scan_split_go<32, bf16_t, OUT, SAVE>(a, s)
-                      : a.dk == 64 ? scan_split_go<64, bf16_t, OUT, SAVE>(a, s) : scan_split_go<128, bf16_t, OUT, SAVE>(a, s);
+    if (!a.bf16) return a.dk <= 32 ? scan_split_go<32, float, OUT>(a, s) : scan_split_go<64, float, OUT>(a, s);
+    return a.dk <= 32 ? scan_split_go<32, bf16_t, OUT>(a, s)
+                      : a.dk == 64 ? scan_split_go<64, bf16_t, OUT>(a, s) : scan_split_go<128, bf16_t, OUT>(a, s);
 }
 
-hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<true, false>(a, s); }
-hipError_t launch_delta_states_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<false, true>(a, s); }
-hipError_t launch_delta_ends_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<false, false>(a, s); }
+hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<true>(a, s); }
+hipError_t launch_delta_ends_split(const DeltaArgs& a, hipStream_t s) { return scan_split_dk<false>(a, s); }
 
 }  // namespace mesa

@@ -561,6 +561,7 @@ static size_t delta_segment_bytes(long BH, int nseg, int dk, int dv) {
 static void delta_use_segments(mesa::DeltaArgs* a, int nseg, float* ws) {
     a->nseg = nseg;
     a->seg_chunks = (a->nc + nseg - 1) / nseg;
+    if (nseg == 1) return;
     a->seg_end = ws;
     a->seg_start = ws + (size_t)a->BH * (nseg - 1) * (a->dv + a->dk) * a->dk;
 }
@@ -632,10 +633,9 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
 
 // Backward workspace, offsets in bytes (every segment a multiple of 16).
 struct DeltaBwdLayout {
-    size_t scal, S, dS, E, dR, seg, part, total;
-    int nseg;
+    size_t scal, S, dS, E, dR, part, total;
 };
-static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int dv, int dtype) {
+static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int dv) {
     const size_t n = (size_t)B * H * delta_chunks(T), C = mesa::kDeltaChunk;
     DeltaBwdLayout l{};
     size_t o = n * delta_image_halfs(MESA_DTYPE_F32) * 2;   // two planes of M and of P for either type
@@ -644,8 +644,6 @@ static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int 
     l.dS = o;   o += n * dv * dk * sizeof(float);
     l.E = o;    o += n * C * dv * sizeof(float);
     l.dR = o;   o += n * C * dv * sizeof(float);
-    l.nseg = mesa::delta_segments((long)B * H, (int)delta_chunks(T), dk, dv, dtype == MESA_DTYPE_BF16);
-    l.seg = o;  o += delta_segment_bytes((long)B * H, l.nseg, dk, dv);
     l.part = o; o += H != Hk ? 2 * (size_t)B * H * T * dk * sizeof(float) : 0;
     l.total = o;
     return l;
@@ -653,7 +651,7 @@ static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int 
 
 size_t mesa_delta_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype) {
     if (B <= 0 || Hk <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
-    return delta_bwd_layout(B, Hk, H, T, dk, dv, dtype).total;
+    return delta_bwd_layout(B, Hk, H, T, dk, dv).total;
 }
 
 mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int dtype, const float* gamma,
@@ -686,7 +684,7 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
     for (const void* o : outs)
         for (const void* i : ins)
             if (o == i) return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
-    const DeltaBwdLayout l = delta_bwd_layout(B, Hk, H, T, dk, dv, dtype);
+    const DeltaBwdLayout l = delta_bwd_layout(B, Hk, H, T, dk, dv);
     if (workspace_bytes < l.total)
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, l.total);
     char* ws = static_cast<char*>(workspace);
@@ -694,7 +692,7 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
     mesa::DeltaBwdArgs a{};
     a.f = mesa::DeltaArgs{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
                           nullptr, nullptr, reinterpret_cast<uint16_t*>(ws), at(l.scal), 2, at(l.S), at(l.E)};
-    delta_use_segments(&a.f, l.nseg, at(l.seg));
+    delta_use_segments(&a.f, 1, nullptr);
     a.grad_out = grad_out;
     a.grad_final = grad_final;
     a.grad_q = grad_q;
@@ -708,10 +706,8 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
     a.part = H != Hk ? at(l.part) : nullptr;
     hipError_t e = timed_launch(MESA_KERNEL_DELTA_PREP, s, [&] { return mesa::launch_delta_prep(a.f, s); });
     if (e != hipSuccess) return hip_fail(e, "delta chunk-matrix kernel launch");
-    e = timed_launch(MESA_KERNEL_DELTA_SCAN, s, [&] { return mesa::launch_delta_states(a.f, s); });
-    if (e != hipSuccess) return hip_fail(e, "delta scan kernel launch");
-    e = timed_launch(MESA_KERNEL_DELTA_BWD_SCAN, s, [&] { return mesa::launch_delta_bwd_scan(a, s); });
-    if (e != hipSuccess) return hip_fail(e, "delta backward scan kernel launch");
+    e = timed_launch(MESA_KERNEL_DELTA_BWD_SCAN, s, [&] { return mesa::launch_delta_passes(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "delta backward pass kernel launch");
     e = timed_launch(MESA_KERNEL_DELTA_GRADS, s, [&] { return mesa::launch_delta_grads(a, s); });
     if (e != hipSuccess) return hip_fail(e, "delta gradient kernel launch");
     return MESA_OK;
@@ -957,9 +953,9 @@ const char* mesa_kernel_name(int kernel_id) {
         case MESA_KERNEL_BWD_GATE: return "bwd_gate_kernel";
         case MESA_KERNEL_HAWK: return "hawk_kernels";
         case MESA_KERNEL_DELTA_PREP: return "delta_prep_kernel";
-        case MESA_KERNEL_DELTA_SCAN: return "delta_scan_kernel";
+        case MESA_KERNEL_DELTA_SCAN: return "delta_scan_kernels";
         case MESA_KERNEL_DELTA_STEP: return "delta_step_kernel";
-        case MESA_KERNEL_DELTA_BWD_SCAN: return "delta_bwd_scan_kernel";
+        case MESA_KERNEL_DELTA_BWD_SCAN: return "delta_bwd_passes";
         case MESA_KERNEL_DELTA_GRADS: return "delta_grads_kernels";
         case MESA_KERNEL_GATE_NORM: return "gate_norm_kernel";
         case MESA_KERNEL_GATE_NORM_BWD: return "gate_norm_bwd_kernels";

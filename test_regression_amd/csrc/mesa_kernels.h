@@ -115,17 +115,16 @@ struct DeltaBwdArgs {
     float* dS; float* dR;         // workspace: gradients of the chunks' end states, of v in float (both as S and E)
     float* part;                  // workspace: dq, then dk of each value head [2][BH][T][dk] (H != Hk), else nullptr
 };
-hipError_t launch_delta_bwd_scan(const DeltaBwdArgs& a, hipStream_t s);
-hipError_t launch_delta_bwd_split(const DeltaBwdArgs& a, hipStream_t s);   // with its chain on waves of its own (not float with dk 128)
+hipError_t launch_delta_passes(const DeltaBwdArgs& a, hipStream_t s);        // the forward's pass again, writing S and E, and the backward's
+hipError_t launch_delta_passes_split(const DeltaBwdArgs& a, hipStream_t s);
 hipError_t launch_delta_grads(const DeltaBwdArgs& a, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s);
-hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s);     // the same with its chain on waves of its own (not float with dk 128)
-hipError_t launch_delta_states_split(const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s);   // with its chain on waves of its own (not float, dk 128)
 hipError_t launch_delta_ends_split(const DeltaArgs& a, hipStream_t s);    // the segments' end states and transitions
 hipError_t launch_delta_segments(const DeltaArgs& a, hipStream_t s);      // and from them the segments' start states
 int delta_segments(long BH, int nc, int dk, int dv, int bf16);            // the number of segments
-hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E
+hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E (float, dk 128)
 struct DeltaStepArgs {
     const void* q; const void* k; const void* v; const float* gamma; const float* beta; float* state;
     long NH; int Hk; int H; int dk; int dv; int bf16;
