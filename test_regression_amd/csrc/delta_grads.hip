@@ -63,12 +63,12 @@ __device__ __forceinline__ void stage_row8(const f32x8& x, uint32_t (&P)[2][kDC 
     float m = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x.v[e]));
-    m = fmaxf(m, __shfl_xor(m, 1, 64));
-    m = fmaxf(m, __shfl_xor(m, 2, 64));
+    m = fmaxf(m, dpp_f32<0xb1>(m));
+    m = fmaxf(m, dpp_f32<0x4e>(m));
     const int E = h2_exp(m);
     if (q == 0) inv[row] = pow2(-E);
     f16x8 hi, lo;
-    h2_split(f32x4{x.v[0], x.v[1], x.v[2], x.v[3]}, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]}, pow2(E), hi, lo);
+    h2_split_mix(f32x4{x.v[0], x.v[1], x.v[2], x.v[3]}, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]}, pow2(E), hi, lo);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         const int at = row * kVW + perm32(8 * q + 4 * half) / 2;
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
                 for (int t = 0; t < 2; ++t) {
                     const f32x8& x = t ? d[i] : s[i];
                     f16x8 hi, lo;
-                    h2_split(f32x4{x.v[0], x.v[1], x.v[2], x.v[3]}, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]}, t ? sd : ss, hi, lo);
+                    h2_split_mix(f32x4{x.v[0], x.v[1], x.v[2], x.v[3]}, f32x4{x.v[4], x.v[5], x.v[6], x.v[7]}, t ? sd : ss, hi, lo);
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int at = (u / per_row) * KW + perm32(kc + 4 * half) / 2;
