@@ -384,8 +384,9 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel
 }
 
 // The row layouts built: D up to 512 and 2048 with a wave a row, up to 2048
-// with four waves and one piece a thread (few rows: the row's latency counts),
-// up to 8192 with four waves, up to 32768 with sixteen.
+// with four waves and one piece a thread (few rows: the row's latency counts;
+// four waves a row lose at 32768 x 2048, where a wave a row needs no barrier),
+// up to 8192 with four waves, up to 16384 with sixteen.
 template <template <int, int, bool> class Go, bool WHOLE, typename A>
 hipError_t residual_rows(const A& a, hipStream_t s) {
     if (a.D <= 512) return Go<1, 1, WHOLE>::go(a, s);

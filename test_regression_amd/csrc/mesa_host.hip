@@ -573,6 +573,9 @@ size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype
            delta_segment_bytes(BH, mesa::delta_segments(BH, (int)nc, dk, dv, dtype == MESA_DTYPE_BF16), dk, dv);
 }
 
+// A launch holds fewer than 2^32 threads.
+constexpr double kMaxThreads = 4.0e9;
+
 // The checks the delta entry points share; `rows` is T or, for the step, 1.
 static mesa_status delta_checks(int dtype, int B, int Hk, int H, int T, int dk, int dv) {
     if (!dtype_ok(dtype))
@@ -583,8 +586,12 @@ static mesa_status delta_checks(int dtype, int B, int Hk, int H, int T, int dk, 
     if (H % Hk != 0) return fail(MESA_ERR_INVALID_ARGUMENT, "H=%d is not a multiple of Hk=%d", H, Hk);
     if (!supported_d(dk)) return fail(MESA_ERR_UNSUPPORTED, "dk=%d not built (16, 32, 64, 128)", dk);
     if (!supported_d(dv) && dv != 256) return fail(MESA_ERR_UNSUPPORTED, "dv=%d not built (16, 32, 64, 128, 256)", dv);
-    // launches of one workgroup per head and chunk, and up to 64 row groups a head
-    if ((double)B * H * std::max<long>(delta_chunks(T), 64) > 1e9)
+    // the launches' threads: 256 a head and chunk, two passes of 768 a head and
+    // 64 columns of dv, the step's at most 8 a row of the state, and
+    // one for four features where the gradients of shared heads are summed
+    const double BH = (double)B * H;
+    const double threads = std::max({BH * delta_chunks(T) * 256, BH * std::max(dv, 32) * 64, (double)B * Hk * T * dk / 4});
+    if (threads > kMaxThreads)
         return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B*H=%ld, chunks=%ld)", (long)B * H, delta_chunks(T));
     return MESA_OK;
 }
@@ -746,7 +753,7 @@ static mesa_status gate_checks(const void* x, int x_dtype, const void* gate, int
     if (!aligned(x, 16) || !aligned(gate, 16) || !aligned(w, 16))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
     if (!supported_d(d) && d != 256) return fail(MESA_ERR_UNSUPPORTED, "d=%d not built (16, 32, 64, 128, 256)", d);
-    if ((double)B * H * ((double)T + 8) > 1e9)
+    if ((double)B * H * ((double)T + 8) * (d / 8) > kMaxThreads)
         return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B=%d H=%d T=%d)", B, H, T);
     return MESA_OK;
 }
@@ -830,6 +837,8 @@ static mesa_status residual_checks(const void* h, int h_dtype, const void* y, in
     if (!aligned(h, 16) || !aligned(y, 16) || !aligned(scale, 16) || !aligned(w, 16))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
     if (D > 16384) return fail(MESA_ERR_UNSUPPORTED, "D=%d not built (at most 16384)", D);
+    if ((double)R * (D <= 2048 ? 64 : D <= 8192 ? 256 : 1024) > kMaxThreads)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (R=%d)", R);
     return MESA_OK;
 }
 

@@ -566,17 +566,23 @@ def mesa_delta_step(q, k, v, gamma, beta, state, *, out=None, stream=None):
     return out
 
 
+def _rows_dtype(dtype, x, *rows):
+    """The dtype of a norm's rows: the first given tensor's, which an explicit
+    out_dtype must agree with, else out_dtype, else x's."""
+    for t in rows:
+        if t is not None:
+            if dtype is not None and dtype is not t.dtype:
+                raise ValueError(f"out_dtype is {dtype}, expected {t.dtype}")
+            return t.dtype
+    return x.dtype if dtype is None else dtype
+
+
 def _gate_checks(x, gate, w, grad_y=None, y=None, dtype=None):
     """Checks a gate norm's tensors; returns (B, H, T, d, dtype of y)."""
     import torch
     B, H, T, d = _dims(x, "x", 4)
     rows = (B, T, H, d)
-    for t in (gate, grad_y, y):
-        if t is not None:
-            dtype = t.dtype
-            break
-    else:
-        dtype = x.dtype if dtype is None else dtype
+    dtype = _rows_dtype(dtype, x, gate, grad_y, y)
     _tensors(x.device, (x, "x", (B, H, T, d), x.dtype), (w, "w", (H, d), torch.float32), (gate, "gate", rows, dtype),
              (grad_y, "grad_y", rows, dtype), (y, "out", rows, dtype))
     return B, H, T, d, dtype
@@ -624,12 +630,7 @@ def _residual_checks(h, y, w, scale, grad_n=None, grad_h_out=None, n=None, h_out
     R, D = _dims(h, "h", 2)
     if y is None and (scale is not None or h_out is not None):
         raise ValueError("scale and h_out need y")
-    for t in (y, grad_n, n):
-        if t is not None:
-            dtype = t.dtype
-            break
-    else:
-        dtype = h.dtype if dtype is None else dtype
+    dtype = _rows_dtype(dtype, h, y, grad_n, n)
     rows, ht, f32 = (R, D), h.dtype, torch.float32
     _tensors(h.device, (h, "h", rows, ht), (y, "y", rows, dtype), (w, "w", (D,), f32), (scale, "scale", (D,), f32),
              (grad_n, "grad_n", rows, dtype), (grad_h_out, "grad_h_out", rows, ht), (n, "n", rows, dtype),
