@@ -94,8 +94,9 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
         // ---------------- the state's chain ----------------
         f32x4 S[NS];   // the state times 2^cs
         int cs = 0;
-        const float* from = seg == 0 ? (a.state0 ? a.state0 + (size_t)bh * a.dv * a.dk : nullptr)
-                                     : ENDS ? nullptr : a.seg_start + (size_t)vh * a.dv * a.dk;
+        // all segments start from their copies: the last one's end may go over state0
+        const float* from = !ENDS && nseg > 1 ? a.seg_start + (size_t)vh * a.dv * a.dk
+                            : seg == 0 && a.state0 ? a.state0 + (size_t)bh * a.dv * a.dk : nullptr;
 #pragma unroll
         for (int m = 0; m < NS; ++m) {
             S[m] = from && live && 16 * m < a.dk ? load4(from + so + 16 * m) : f32x4{0.f, 0.f, 0.f, 0.f};

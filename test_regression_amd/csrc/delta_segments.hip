@@ -41,6 +41,12 @@ __global__ __launch_bounds__(DK * 4) void delta_segments_kernel(DeltaArgs a) {
             for (int e = 0; e < 4; ++e) phi[k][e] = end[(s * end_rows + a.dv + 16 * k + 4 * g + e) * DK + j + n];
     };
     load_b(0);
+    // the first start is state0 or zeros
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const size_t at = (size_t)(v0 + 4 * g + r) * DK + j + n;
+        to[at] = a.state0 ? a.state0[(size_t)bh * a.dv * DK + at] : 0.f;
+    }
     for (int s = 0; s + 1 < a.nseg; ++s) {
         f32x4 xy[2] = {t, f32x4{0.f, 0.f, 0.f, 0.f}};
         if (s > 0) {

@@ -106,7 +106,7 @@ struct DeltaArgs {
     float* S; float* E;           // backward workspace: chunk start states [BH][nc][dv][dk], E [BH][nc][64][dv]
     int nseg; int seg_chunks;     // segments of a sequence that are passed over at once, chunks of one
     float* seg_end;               // nseg > 1, workspace: [BH][nseg - 1][dv + dk][dk] (delta_segments.hip)
-    float* seg_start;             // and [BH][nseg][dv][dk], the segments' start states from the second on
+    float* seg_start;             // and [BH][nseg][dv][dk], the segments' start states
 };
 struct DeltaBwdArgs {
     DeltaArgs f;                  // q, k, v, gamma, beta, state0, sizes, img, scal, S, E
