@@ -354,7 +354,9 @@ mesa_status mesa_hawk_scan(const void *x, const void *ga, const void *gx, int in
  *   workspace                   at least mesa_delta_workspace_bytes(...)
  * dk in {16, 32, 64, 128}, dv in {16, 32, 64, 128, 256}, T >= 0.  Sums, states
  * and decays are float32 (prefix sums of ln gamma float64); products run as
- * fp16 MFMAs on two-part splits (see mesa_dtype).
+ * fp16 MFMAs on two-part splits (see mesa_dtype).  Values are taken as finite:
+ * a NaN or infinity reaches its chunk of 64 tokens and what follows in its head
+ * (other heads and rows never), also from a token with beta = 0.
  */
 size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype);
 mesa_status mesa_delta_forward(const void *q, const void *k, const void *v, int dtype, const float *gamma,

@@ -32,6 +32,13 @@ constexpr int kDC = kDeltaChunk;   // tokens of a chunk
 constexpr int kDP = 40;     // words per LDS row of a 64 x 64 plane (fp16, columns perm32)
 constexpr int kDF = 68;     // floats per LDS row of a 64 x 64 float matrix
 
+// log2 of a gate for the chunk's double prefix sums.  A gate of 0 (a reset)
+// counts as 2^-202, which is 0 in float; a NaN stays one.
+__device__ __forceinline__ double log2_gate(float gate) {
+    const float x = logf(gate);
+    return (double)(x < -140.f ? -140.f : x) * 1.4426950408889634;
+}
+
 // Per-chunk scalars in the workspace: powers of two that scale the key and
 // query rows into fp16's range, and the factors that undo row scales and apply
 // the gates (64 values each, then single ones).

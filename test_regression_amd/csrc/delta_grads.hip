@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
     float gate = 1.f;
     if (w == 0) {
         gate = lane < valid ? a.gamma[tok + lane] : 1.f;
-        double x = fmax(log((double)gate), -200.0);
+        double x = log2_gate(gate);
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const double t = __shfl_up(x, o, 64);
@@ -118,8 +118,8 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         }
         L.L[lane] = x;
         L.beta[lane] = lane < valid ? a.beta[tok + lane] : 0.f;
-        L.G[lane] = expf((float)x);
-        L.end[lane] = expf((float)(__shfl(x, 63, 64) - x));
+        L.G[lane] = __builtin_amdgcn_exp2f((float)x);
+        L.end[lane] = __builtin_amdgcn_exp2f((float)(__shfl(x, 63, 64) - x));
     }
     // ---- products over dv ----
     f32x4 Y[4], Z[4], oS[NS], rS[NS], W[NS];
@@ -298,7 +298,7 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = 16 * w + 4 * g + r;
-                const float D = row >= cj ? expf((float)(L.L[row] - Lj)) : 0.f;
+                const float D = row >= cj ? __builtin_amdgcn_exp2f((float)(L.L[row] - Lj)) : 0.f;
                 const float Ds = row > cj ? D : 0.f;
                 const float py = P[r] * (ek * eq) * D * Y[j][r], az = A[r] * (ek * ek) * Ds * Z[j][r];
                 sum += py - az;
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         const float cols = (L.col[0][lane] + L.col[1][lane]) + (L.col[2][lane] + L.col[3][lane]);
         if (lane < valid) {
             b.grad_beta[tok + lane] = wr + cols;
-            b.grad_gamma[tok + lane] = gate > 0.f ? (cross + rd + before + state) / gate : 0.f;
+            b.grad_gamma[tok + lane] = gate == 0.f ? 0.f : (cross + rd + before + state) / gate;
         }
     }
     float ey, ez;

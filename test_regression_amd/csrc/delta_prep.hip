@@ -73,10 +73,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
         k.load(static_cast<const In*>(a.k) + ktok, a.dk, valid);
         q.load(static_cast<const In*>(a.q) + ktok, a.dk, valid);
         if (w == 0) {
-            // a gate of 0 (a reset) counts as 2^-200, which is 0 in float
             const int t = min(lane, valid - 1);
             const float ga = a.gamma[tok + t], be = a.beta[tok + t];
-            double x = lane < valid ? (double)fmaxf(logf(ga), -140.f) * 1.4426950408889634 : 0.0;
+            double x = lane < valid ? log2_gate(ga) : 0.0;
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) {
                 const double t2 = __shfl_up(x, o, 64);

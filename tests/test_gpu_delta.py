@@ -370,3 +370,112 @@ def test_delta_backward_no_tokens_repeat_and_in_place():
     e = [x[:, :, :0].contiguous() for x in args[:6]]
     g = mesa.mesa_delta_backward(*e, d["state"], grad_final=gf)
     assert torch.equal(g["grad_state"], gf) and g["grad_q"].shape == (1, 2, 0, 32)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_delta_keys_of_mixed_sizes(dtype):
+    """Keys and queries of very different lengths in a chunk, and padded tokens
+    whose keys are longer than any that write."""
+    import torch
+    say("case delta mixed sizes", dtype)
+    t, f = delta_inputs(97, 1, 2, 2, 200, 64, 64, dtype)
+    size = 2.0 ** -(torch.arange(200) % 9).float()[:, None]
+    idle = torch.arange(200) % 7 == 3
+    size[idle] = 2.0 ** 8
+    for n in ("q", "k"):
+        t[n] = (t[n].float() * size).to(t[n].dtype)      # powers of two: exact
+    t["beta"][:, :, idle] = 0.0
+    f.update({n: t[n].double().numpy() for n in ("q", "k", "beta")})
+    # q of 2^8 would drown the others' outputs: those tokens are read apart
+    o, S = forward(t)
+    ro, rS = delta_ref(f)
+    on = ~idle.numpy()
+    assert rel(S, rS) <= F32 and rel(o[:, :, on], ro[:, :, on]) <= tol(dtype) and rel(o[:, :, ~on], ro[:, :, ~on]) <= tol(dtype)
+    t["q"][:, :, idle] = 0.0
+    f["q"] = t["q"].double().numpy()
+    errs, got, ref = backward_errors(t, f, dtype, 97)
+    # the gradients of the idle tokens' strengths come from keys 2^8 long, and
+    # theirs and the others' are off in proportion to their own
+    for n in ("grad_q", "grad_k", "grad_v", "grad_gamma", "grad_state"):
+        assert errs[n] <= grad_tol(n, dtype), (n, errs)
+    for m in (on, ~on):
+        assert rel(got["grad_beta"][:, :, m], ref["grad_beta"][:, :, m]) <= GRAD_F32
+
+
+@pytest.mark.parametrize("what", ["q", "k", "v", "gamma", "beta"])
+def test_delta_nan_stays_in_its_head(what):
+    import torch
+    from test_regression_amd import mesa
+    say("case delta nan", what)
+    t, _ = delta_inputs(101, 2, 2, 2, 200, 64, 64, "f32")
+    d = dev(t)
+    go, gf = torch.randn_like(d["v"]), torch.randn_like(d["state"])
+    run = lambda: (mesa.mesa_delta_forward(*d.values(), return_final=True),  # noqa: E731
+                   mesa.mesa_delta_backward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], go, d["state"], grad_final=gf))
+    (o, S), g = run()
+    d[what][1, 0, 100] = float("nan")
+    (o2, S2), g2 = run()
+    torch.cuda.synchronize()
+    pick = lambda x: torch.cat([x[0], x[1, 1:]])  # noqa: E731
+    assert torch.equal(pick(o), pick(o2)) and torch.equal(pick(S), pick(S2))
+    for n in g:
+        assert torch.equal(pick(g[n]), pick(g2[n])), n
+    # chunks before the token's keep their outputs, and it does not go unseen
+    assert torch.equal(o[1, 0, :64], o2[1, 0, :64])
+    assert bool(o2[1, 0, 100].isnan().all())
+    if what != "q":
+        assert bool(o2[1, 0, 128:].isnan().all()) and bool(S2[1, 0].isnan().all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_delta_segments_state_in_place(dtype):
+    """The final state over the initial one where segments run at once."""
+    import torch
+    from test_regression_amd import mesa
+    say("case delta segments in place", dtype)
+    t, _ = delta_inputs(103, 1, 1, 2, 4100, 64, 64, dtype, lo=0.97)
+    d = dev(t)
+    a = mesa.mesa_delta_forward(*d.values(), return_final=True)
+    s = d["state"].clone()
+    b = mesa.mesa_delta_forward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], s, final_state=s)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], s)
+
+
+def test_delta_more_than_2_31_elements():
+    """The last row of a batch whose tensors pass 2^31 elements and 2^32 bytes."""
+    import torch
+    from test_regression_amd import mesa
+    B, H, T, d = 258, 16, 4096, 128
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GiB of free memory")
+    say("case delta large", (B, H, T, d))
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    new = lambda: torch.randn(B, H, T, d, dtype=torch.bfloat16, device="cuda", generator=gen)  # noqa: E731
+    q, k, v = new().mul_(0.088), new().mul_(0.088), new()
+    gamma = torch.rand(B, H, T, device="cuda", generator=gen).mul_(0.2).add_(0.8)
+    beta = torch.rand(B, H, T, device="cuda", generator=gen)
+    last = [x[-1:].contiguous() for x in (q, k, v, gamma, beta)]
+    out, S = mesa.mesa_delta_forward(q, k, v, gamma, beta, return_final=True)
+    o1, S1 = mesa.mesa_delta_forward(*last, return_final=True)
+    say("  forward")
+    assert torch.equal(out[-1:], o1) or rel(out[-1:].double().cpu(), o1.double().cpu()) <= 2 * tol("bf16")
+    assert rel(S[-1:].double().cpu(), S1.double().cpu()) <= 2 * F32
+    g = mesa.mesa_delta_backward(q, k, v, gamma, beta, out)
+    g1 = mesa.mesa_delta_backward(*last, out[-1:].contiguous())
+    torch.cuda.synchronize()
+    say("  backward")
+    for n in g:
+        if g[n] is not None:
+            assert torch.equal(g[n][-1:], g1[n]), n
+    del g, g1, out, q, k, v
+    torch.cuda.empty_cache()
+    # the step over states of more than 2^32 bytes
+    N = 4200
+    S = torch.randn(N, H, d, d, device="cuda", generator=gen)
+    one = lambda: torch.randn(N, H, d, dtype=torch.bfloat16, device="cuda", generator=gen).mul_(0.088)  # noqa: E731
+    q, k, v, ga = one(), one(), one(), torch.rand(N, H, device="cuda", generator=gen)
+    S1 = S[-2:].clone()
+    o = mesa.mesa_delta_step(q, k, v, ga, ga, S)
+    o1 = mesa.mesa_delta_step(*(x[-2:].contiguous() for x in (q, k, v, ga, ga)), S1)
+    torch.cuda.synchronize()
+    assert torch.equal(o[-2:], o1) and torch.equal(S[-2:], S1)
