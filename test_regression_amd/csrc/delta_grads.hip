@@ -39,20 +39,15 @@ struct alignas(16) GradsLds {
         struct {
             uint32_t K[NP][kDC * KW];
             uint32_t Q[NP][kDC * KW];
-            union {
-                struct {
-                    uint32_t Y[2 * kCPlane];
-                    uint32_t Z[2 * kCPlane];
-                };
-                float X[kDC * kDF];
-            };
+            uint32_t Y[2 * kCPlane];
+            uint32_t Z[2 * kCPlane];
         };
     };
     double L[kDC];
     float beta[kDC], G[kDC], end[kDC];
     float vs[3][kDC];          // 2^-E of the token rows
     float read[kDC], write[kDC];
-    float col[4][kDC], cross[4][kDC];
+    float col[4][kDC], cross[4][kDC + 1];
     float red[8][4];           // per-wave maxima and sums
 };
 
@@ -90,6 +85,17 @@ __device__ __forceinline__ void product(f32x4& t, f16x8 ah, f16x8 al, f16x8 bh, 
     }
     if constexpr (FIRST && !AP && !BP) mfma_first(t, ah, bh);
     else mfma_acc(t, ah, bh);
+}
+
+// A buffer of n elements: stores past its end are dropped.
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(T* p, int n) {
+    return __builtin_amdgcn_make_buffer_rsrc(p, (short)0, n * (int)sizeof(T), 0x00020000);
+}
+template <typename T>
+__device__ __forceinline__ void put1(__amdgpu_buffer_rsrc_t r, uint32_t i, float x) {
+    if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, x), r, i * 4, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)x), r, i * 2, 0, 0);
 }
 
 template <int DKP, typename In>
@@ -267,6 +273,11 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
     __syncthreads();
     // ---- A and P; what crosses; the decayed Y and Z ----
     {
+        // X_ij = b_j (P_ij Y_ij - A_ij Z_ij) crosses the gates j + 1 .. i: along a
+        // row its sums up to column j, taken within 16 lanes and on top of the
+        // blocks before, are summed over the rows below
+        float before[4] = {};
+        if (lane == 0) L.cross[w][0] = 0.f;
         f16x8 kh[NJ], kl[NJ], qh[NJ], ql[NJ];
 #pragma unroll
         for (int s = 0; s < NJ; ++s) {
@@ -294,7 +305,7 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
             const int cj = 16 * j + n;
             const double Lj = L.L[cj];
             const float bj = L.beta[cj];
-            float sum = 0.f;
+            float sum = 0.f, cross = 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int row = 16 * w + 4 * g + r;
@@ -302,12 +313,23 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
                 const float Ds = row > cj ? D : 0.f;
                 const float py = P[r] * (ek * eq) * D * Y[j][r], az = A[r] * (ek * ek) * Ds * Z[j][r];
                 sum += py - az;
-                L.X[row * kDF + cj] = row > cj ? bj * (py - az) : 0.f;
+                float x = row > cj ? bj * (py - az) : 0.f;
+                x += dpp_f32<0x111>(x);   // row_shr:1, 2, 4, 8
+                x += dpp_f32<0x112>(x);
+                x += dpp_f32<0x114>(x);
+                x += dpp_f32<0x118>(x);
+                x += before[r];
+                before[r] = dpp_f32<0x15f>(x);   // the last lane's
+                cross += row > cj ? x : 0.f;
                 Y[j][r] *= D * bj;
                 Z[j][r] *= Ds * bj;
             }
             sum = kslot_sum(sum);
-            if (g == 0) L.col[w][cj] = sum;
+            cross = kslot_sum(cross);
+            if (g == 0) {
+                L.col[w][cj] = sum;
+                L.cross[w][cj + 1] = cross;
+            }
         }
     }
     // row dots with the keys and queries
@@ -341,23 +363,6 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
     const float my = wave_max(absmax(Y)), mz = wave_max(absmax(Z));
     if (lane == 0) { L.red[5][w] = my; L.red[6][w] = mz; }
     __syncthreads();
-    {
-        // lane t: sum over the wave's rows i >= t of the row's sum over j < t
-        float acc = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int row = 16 * w + i;
-            float x = lane ? L.X[row * kDF + lane - 1] : 0.f;
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const float t = __shfl_up(x, o, 64);
-                if (lane >= o) x += t;
-            }
-            if (row >= lane) acc += x;
-        }
-        L.cross[w][lane] = acc;
-    }
-    __syncthreads();   // X is read: Y and Z take its place
     if (w == 0) {
         const float wr = L.write[lane];
         float rd = L.read[lane], before = L.beta[lane] * wr;
@@ -424,7 +429,12 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         }
     }
     const f32x4 G = row4(L.G, w, g), end = row4(L.end, w, g), be = row4(L.beta, w, g);
-    const size_t ho = (tok + 16 * w + 4 * g) * a.dk + n, ko = ktok + (size_t)(16 * w + 4 * g) * a.dk + n;
+    // rows behind the last token fall off the end of the buffers
+    const uint32_t ro = (uint32_t)(16 * w + 4 * g) * a.dk + n;
+    const int elems = valid * a.dk;
+    const auto rq = b.part ? row_buffer(b.part + tok * a.dk, elems) : row_buffer(static_cast<In*>(b.grad_q) + ktok, elems);
+    const auto rk = b.part ? row_buffer(b.part + ((size_t)a.BH * a.T + tok) * a.dk, elems)
+                           : row_buffer(static_cast<In*>(b.grad_k) + ktok, elems);
 #pragma unroll
     for (int m = 0; m < NS; ++m) {
         f32x4 t[3];   // (D.Y b) K, (D.Y b)^T Q, (D.Z b) K + (D.Z b)^T K
@@ -449,17 +459,17 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         }
         mfma_done(t);
         const f32x4 tq = t[0], tk = t[1], tz = t[2];
+        if (DKP == 32 && 16 * m >= a.dk) continue;
+        const f32x4 dq = G * oS[m] + tq * (ey * ek), dk = end * be * W[m] - G * rS[m] + tk * (ey * eq) - tz * (ez * ek);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (16 * w + 4 * g + r >= valid || 16 * m >= a.dk) continue;
-            const float dq = G[r] * oS[m][r] + tq[r] * (ey * ek);
-            const float dk = end[r] * be[r] * W[m][r] - G[r] * rS[m][r] + tk[r] * (ey * eq) - tz[r] * (ez * ek);
+            const uint32_t at = ro + r * a.dk + 16 * m;
             if (b.part) {
-                b.part[ho + (size_t)r * a.dk + 16 * m] = dq;
-                b.part[(size_t)a.BH * a.T * a.dk + ho + (size_t)r * a.dk + 16 * m] = dk;
+                put1<float>(rq, at, dq[r]);
+                put1<float>(rk, at, dk[r]);
             } else {
-                store1(static_cast<In*>(b.grad_q) + ko + (size_t)r * a.dk + 16 * m, dq);
-                store1(static_cast<In*>(b.grad_k) + ko + (size_t)r * a.dk + 16 * m, dk);
+                put1<In>(rq, at, dq[r]);
+                put1<In>(rk, at, dk[r]);
             }
         }
     }
