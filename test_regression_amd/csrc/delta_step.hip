@@ -29,29 +29,24 @@ __device__ __forceinline__ float step_sum(float v) {
     return v;
 }
 
-// A wave takes RG consecutive groups of rows of one head.
-template <int dk, int RG, typename In>
+// A wave takes one group of rows of a head.
+template <int dk, typename In>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a) {
     using Sh = StepShape<dk>;
-    const long g0 = ((long)blockIdx.x * 4 + threadIdx.x / 64) * RG;
-    if (g0 >= a.groups) return;
+    const long grp = (long)blockIdx.x * 4 + threadIdx.x / 64;
+    if (grp >= a.groups) return;
     const int lane = threadIdx.x % 64, li = lane % Sh::lanes, lr = lane / Sh::lanes;
-    const long row0 = g0 * Sh::rows;
+    const long row0 = grp * Sh::rows;
     const long nh = row0 / a.dv;
     const long n = nh / a.H;
     const int h = (int)(nh % a.H);
     const size_t ko = ((size_t)n * a.Hk + h / (a.H / a.Hk)) * dk + 4 * li;
-    f32x4 S[RG][Sh::pieces], k[Sh::pieces], q[Sh::pieces];
+    f32x4 S[Sh::pieces], k[Sh::pieces], q[Sh::pieces];
     float* p = a.state + (size_t)(row0 + lr) * dk + 4 * li;
 #pragma unroll
-    for (int i = 0; i < RG; ++i)
-#pragma unroll
-        for (int j = 0; j < Sh::pieces; ++j)
-            S[i][j] = load4(p + (size_t)i * Sh::rows * dk + 4 * Sh::lanes * j);
+    for (int j = 0; j < Sh::pieces; ++j) S[j] = load4(p + 4 * Sh::lanes * j);
     const float ga = a.gamma[nh], be = a.beta[nh];
-    float v[RG];
-#pragma unroll
-    for (int i = 0; i < RG; ++i) v[i] = to_f32(static_cast<const In*>(a.v)[row0 + i * Sh::rows + lr]);
+    const float v = to_f32(static_cast<const In*>(a.v)[row0 + lr]);
     float kq = 0.f;
 #pragma unroll
     for (int j = 0; j < Sh::pieces; ++j) {
@@ -61,41 +56,32 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaStepArgs a) {
         for (int e = 0; e < 4; ++e) kq += k[j][e] * q[j][e];
     }
     kq = step_sum<Sh::lanes>(kq);
+    float sk = 0.f, sq = 0.f;
 #pragma unroll
-    for (int i = 0; i < RG; ++i) {
-        float sk = 0.f, sq = 0.f;
+    for (int j = 0; j < Sh::pieces; ++j)
 #pragma unroll
-        for (int j = 0; j < Sh::pieces; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                S[i][j][e] *= ga;
-                sk += S[i][j][e] * k[j][e];
-                sq += S[i][j][e] * q[j][e];
-            }
-        sk = step_sum<Sh::lanes>(sk);
-        sq = step_sum<Sh::lanes>(sq);
-        const float e1 = be * (v[i] - sk);
-#pragma unroll
-        for (int j = 0; j < Sh::pieces; ++j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[i][j][e] += e1 * k[j][e];
-            *reinterpret_cast<f32x4*>(p + (size_t)i * Sh::rows * dk + 4 * Sh::lanes * j) = S[i][j];
+        for (int e = 0; e < 4; ++e) {
+            S[j][e] *= ga;
+            sk += S[j][e] * k[j][e];
+            sq += S[j][e] * q[j][e];
         }
-        if (li == 0) store1(static_cast<In*>(a.out) + row0 + i * Sh::rows + lr, sq + e1 * kq);
+    sk = step_sum<Sh::lanes>(sk);
+    sq = step_sum<Sh::lanes>(sq);
+    const float e1 = be * (v - sk);
+#pragma unroll
+    for (int j = 0; j < Sh::pieces; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[j][e] += e1 * k[j][e];
+        *reinterpret_cast<f32x4*>(p + 4 * Sh::lanes * j) = S[j];
     }
+    if (li == 0) store1(static_cast<In*>(a.out) + row0 + lr, sq + e1 * kq);
 }
 
 template <int dk, typename In>
 hipError_t step_go(DeltaStepArgs a, hipStream_t s) {
     constexpr int rows = StepShape<dk>::rows;
     a.groups = a.NH * (a.dv / rows);
-    // four groups a wave once that still leaves 16 waves a CU, so that a wave
-    // has 64 bytes a lane and more in flight
-    if (a.dv / rows % 4 == 0 && a.groups >= 4L * 16 * 256) {
-        hipLaunchKernelGGL((delta_step_kernel<dk, 4, In>), dim3((unsigned)((a.groups / 4 + 3) / 4)), dim3(256), 0, s, a);
-    } else {
-        hipLaunchKernelGGL((delta_step_kernel<dk, 1, In>), dim3((unsigned)((a.groups + 3) / 4)), dim3(256), 0, s, a);
-    }
+    hipLaunchKernelGGL((delta_step_kernel<dk, In>), dim3((unsigned)((a.groups + 3) / 4)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
