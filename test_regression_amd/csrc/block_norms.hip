@@ -289,43 +289,73 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_kernel(Res
 }
 
 // Workgroup i takes row groups i, i + gridDim.x, ...; its sums of dw and ds go
-// to partial[i][0..D) and partial[i][D..2D).
+// to partial[i][0..D) and partial[i][D..2D).  With one piece a thread the next
+// row is in flight while a row's sums are joined.
 template <int W, int N, bool WHOLE, typename Hh, typename Y>
 __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel(ResidualNormBwdArgs a) {
     using RG = RowGroup<W>;
+    // the next row on its way; w, scale and dh' kept from the sums to the outputs
+    // (a thread of sixteen waves has half the registers)
+    constexpr bool AHEAD = N == 1, KEEP = W < 16;
     __shared__ float red[2][2][16];
     __shared__ float own[W == 1 ? 4 : 1][W == 1 ? 64 * 8 * N : 1];
     int flip = 0;
     const int t = RG::tid(), wave = threadIdx.x / 64;
     float dw[N][8] = {}, ds[N][8] = {};
     const float inv_D = 1.0f / (float)a.D;
-    for (long r = (long)blockIdx.x * RG::rows + (W == 1 ? wave : 0); r < a.R; r += (long)gridDim.x * RG::rows) {
+    struct Row { f32x8 z[N], y[N], d[N], g[N]; };
+    auto load = [&](Row& x, long r) {
         const size_t ro = (size_t)r * a.D;
-        f32x8 z[N], y[N], d[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int f = 8 * (t + 64 * W * j), left = a.D - f;
+            x.z[j] = x.y[j] = x.d[j] = x.g[j] = f32x8{};
+            if (left > 0) {
+                x.z[j] = load8_upto<WHOLE>(static_cast<const Hh*>(a.h) + ro + f, left);
+                x.d[j] = load8_upto<WHOLE>(static_cast<const Y*>(a.grad_n) + ro + f, left);
+                if (a.y) x.y[j] = load8_upto<WHOLE>(static_cast<const Y*>(a.y) + ro + f, left);
+                if (KEEP && a.grad_h_out) x.g[j] = load8_upto<WHOLE>(static_cast<const Hh*>(a.grad_h_out) + ro + f, left);
+            }
+        }
+    };
+    struct Weights { f32x8 w, s; };
+    auto weights = [&](int j) {
+        const int f = 8 * (t + 64 * W * j), left = a.D - f;
+        Weights x{};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x.s.v[e] = 1.f;
+        if (left > 0) {
+            x.w = load8_upto<WHOLE>(a.w + f, left);
+            if (a.scale) x.s = load8_upto<WHOLE>(a.scale + f, left);
+        }
+        return x;
+    };
+    Weights kept[KEEP ? N : 1];
+    if constexpr (KEEP)
+#pragma unroll
+        for (int j = 0; j < N; ++j) kept[j] = weights(j);
+    Row next;
+    const long step = (long)gridDim.x * RG::rows;
+    long r = (long)blockIdx.x * RG::rows + (W == 1 ? wave : 0);
+    if (AHEAD && r < a.R) load(next, r);
+    for (; r < a.R; r += step) {
+        const size_t ro = (size_t)r * a.D;
+        Row x;
+        if constexpr (AHEAD) {
+            x = next;
+            if (r + step < a.R) load(next, r + step);
+        } else {
+            load(x, r);
+        }
         float ss = 0.f, c = 0.f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int f = 8 * (t + 64 * W * j), left = a.D - f;
-            z[j] = y[j] = d[j] = f32x8{};
-            if (left > 0) {
-                z[j] = load8_upto<WHOLE>(static_cast<const Hh*>(a.h) + ro + f, left);
-                d[j] = load8_upto<WHOLE>(static_cast<const Y*>(a.grad_n) + ro + f, left);
-                if (a.y) y[j] = load8_upto<WHOLE>(static_cast<const Y*>(a.y) + ro + f, left);
-            }
-        }
+            const Weights p = KEEP ? kept[KEEP ? j : 0] : weights(j);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int f = 8 * (t + 64 * W * j), left = a.D - f;
-            if (left > 0) {
-                const f32x8 w = load8_upto<WHOLE>(a.w + f, left);
-                f32x8 s{};
-                if (a.scale) s = load8_upto<WHOLE>(a.scale + f, left);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    z[j].v[e] += a.scale ? s.v[e] * y[j].v[e] : y[j].v[e];
-                    ss += z[j].v[e] * z[j].v[e];
-                    c += d[j].v[e] * w.v[e] * z[j].v[e];
-                }
+            for (int e = 0; e < 8; ++e) {
+                x.z[j].v[e] += p.s.v[e] * x.y[j].v[e];
+                ss += x.z[j].v[e] * x.z[j].v[e];
+                c += x.d[j].v[e] * p.w.v[e] * x.z[j].v[e];
             }
         }
         RG::sum2(ss, c, red, flip);
@@ -335,23 +365,20 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel
         for (int j = 0; j < N; ++j) {
             const int f = 8 * (t + 64 * W * j), left = a.D - f;
             if (left > 0) {
-                const f32x8 w = load8_upto<WHOLE>(a.w + f, left);
-                f32x8 dz{};
-                if (a.grad_h_out) dz = load8_upto<WHOLE>(static_cast<const Hh*>(a.grad_h_out) + ro + f, left);
+                const Weights p = KEEP ? kept[KEEP ? j : 0] : weights(j);
+                if (!KEEP && a.grad_h_out) x.g[j] = load8_upto<WHOLE>(static_cast<const Hh*>(a.grad_h_out) + ro + f, left);
+                f32x8 dz;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float u = z[j].v[e] * rs;
-                    dz.v[e] = rs * (d[j].v[e] * w.v[e]) - u * m + dz.v[e];
-                    dw[j][e] += d[j].v[e] * u;
-                    ds[j][e] += dz.v[e] * y[j].v[e];
+                    const float u = x.z[j].v[e] * rs;
+                    dz.v[e] = rs * (x.d[j].v[e] * p.w.v[e]) - u * m + x.g[j].v[e];
+                    dw[j][e] += x.d[j].v[e] * u;
+                    ds[j][e] += dz.v[e] * x.y[j].v[e];
                 }
                 store8_upto<WHOLE>(static_cast<Hh*>(a.grad_h) + ro + f, dz, left);
                 if (a.grad_y) {
-                    if (a.scale) {
-                        const f32x8 s = load8_upto<WHOLE>(a.scale + f, left);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) dz.v[e] *= s.v[e];
-                    }
+                    for (int e = 0; e < 8; ++e) dz.v[e] *= p.s.v[e];
                     store8_upto<WHOLE>(static_cast<Y*>(a.grad_y) + ro + f, dz, left);
                 }
             }
@@ -383,21 +410,6 @@ __global__ __launch_bounds__(RowGroup<W>::threads) void residual_norm_bwd_kernel
     }
 }
 
-// The row layouts built: D up to 512 and 2048 with a wave a row, up to 2048
-// with four waves and one piece a thread (few rows: the row's latency counts;
-// four waves a row lose at 32768 x 2048, where a wave a row needs no barrier),
-// up to 8192 with four waves, up to 16384 with sixteen.
-template <template <int, int, bool> class Go, bool WHOLE, typename A>
-hipError_t residual_rows(const A& a, hipStream_t s) {
-    if (a.D <= 512) return Go<1, 1, WHOLE>::go(a, s);
-    if (a.D <= 2048) return a.R <= 1024 ? Go<4, 1, WHOLE>::go(a, s) : Go<1, 4, WHOLE>::go(a, s);
-    return a.D <= 8192 ? Go<4, 4, WHOLE>::go(a, s) : Go<16, 2, WHOLE>::go(a, s);
-}
-template <template <int, int, bool> class Go, typename A>
-hipError_t residual_shape(const A& a, hipStream_t s) {
-    return a.D % 8 == 0 ? residual_rows<Go, true>(a, s) : residual_rows<Go, false>(a, s);
-}
-
 template <int W, int N, bool WHOLE> struct FwdGo {
     template <typename Hh, typename Y>
     static hipError_t one(const ResidualNormArgs& a, hipStream_t s) {
@@ -424,9 +436,28 @@ template <int W, int N, bool WHOLE> struct BwdGo {
     }
 };
 
-hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) { return residual_shape<FwdGo>(a, s); }
+template <bool WHOLE>
+hipError_t residual_fwd(const ResidualNormArgs& a, hipStream_t s) {
+    if (a.D <= 512) return FwdGo<1, 1, WHOLE>::go(a, s);
+    if (a.D <= 1024) return FwdGo<2, 1, WHOLE>::go(a, s);
+    if (a.D <= 2048) return FwdGo<4, 1, WHOLE>::go(a, s);
+    if (a.D <= 4096) return FwdGo<8, 1, WHOLE>::go(a, s);
+    return a.D <= 8192 ? FwdGo<16, 1, WHOLE>::go(a, s) : FwdGo<16, 2, WHOLE>::go(a, s);
+}
+template <bool WHOLE>
+hipError_t residual_bwd(const ResidualNormBwdArgs& a, hipStream_t s) {
+    if (a.D <= 512) return BwdGo<1, 1, WHOLE>::go(a, s);
+    if (a.D <= 1024) return BwdGo<1, 2, WHOLE>::go(a, s);
+    if (a.D <= 2048) return BwdGo<4, 1, WHOLE>::go(a, s);
+    if (a.D <= 4096) return BwdGo<8, 1, WHOLE>::go(a, s);
+    return a.D <= 8192 ? BwdGo<8, 2, WHOLE>::go(a, s) : BwdGo<16, 2, WHOLE>::go(a, s);
+}
+
+hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s) {
+    return a.D % 8 == 0 ? residual_fwd<true>(a, s) : residual_fwd<false>(a, s);
+}
 hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a, hipStream_t s) {
-    const hipError_t e = residual_shape<BwdGo>(a, s);
+    const hipError_t e = a.D % 8 == 0 ? residual_bwd<true>(a, s) : residual_bwd<false>(a, s);
     if (e != hipSuccess) return e;
     return launch_sum_parts(a.partial, 2 * (size_t)a.D, a.parts, a.grad_scale ? 2L * a.D : a.D, a.grad_w, a.D, a.grad_scale,
                             s);
