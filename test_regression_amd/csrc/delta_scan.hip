@@ -15,7 +15,9 @@
 // The pass is bound by the instructions a wave issues for a chunk (4 cycles
 // each, a wave a SIMD) and by the chain's latencies, not by memory.  Few heads
 // leave compute units idle: then a workgroup takes 32 or 16 columns and its
-// other waves only stage.
+// other waves only stage.  Only float rows of 128 features come here, whose
+// planes delta_scan_split.h's kernel has no LDS for: a forward of 8x16x4096, dv =
+// 128, takes 690 us of which this is 80 %, one of 2x16x4096 493 us.
 //
 // Precision: S, R and b E enter the products that feed the state as hi + lo
 // (22 bits).  For bf16 outputs the two products that only feed O take the hi

@@ -133,7 +133,7 @@ def residual_ref(h, y, s, w, eps, dn=None, dh=None):
 
 
 @pytest.mark.parametrize("ht,yt", [("f32", "bf16"), ("bf16", "bf16"), ("f32", "f32"), ("bf16", "f32")])
-@pytest.mark.parametrize("R,D", [(1, 1), (3, 7), (5, 512), (1, 513), (257, 520), (1025, 1237), (1030, 2048), (2, 2056),
+@pytest.mark.parametrize("R,D", [(1, 1), (3, 7), (5, 512), (1, 513), (257, 520), (1025, 1237), (1030, 2048), (2, 2056), (9, 1000), (2100, 640), (300, 8191), (260, 8200),
                                  (9, 4099), (3, 8192), (2, 9001), (1, 16384)])
 def test_residual_norm(R, D, ht, yt):
     import torch
