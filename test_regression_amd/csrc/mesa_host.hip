@@ -838,7 +838,7 @@ static mesa_status residual_checks(const void* h, int h_dtype, const void* y, in
     if (!aligned(h, 16) || !aligned(y, 16) || !aligned(scale, 16) || !aligned(w, 16))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
     if (D > 16384) return fail(MESA_ERR_UNSUPPORTED, "D=%d not built (at most 16384)", D);
-    if ((double)R * (D <= 2048 ? 64 : D <= 8192 ? 256 : 1024) > kMaxThreads)
+    if ((double)R * (D <= 512 ? 64 : D <= 1024 ? 128 : D <= 2048 ? 256 : D <= 4096 ? 512 : 1024) > kMaxThreads)
         return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (R=%d)", R);
     return MESA_OK;
 }
