@@ -139,3 +139,53 @@ def test_calls_on_a_given_stream():
     for i, (o, S) in enumerate(got):
         assert torch.equal(o, ref[i % 2][0]) and torch.equal(S, ref[i % 2][1])
     assert len(junk) == 16
+
+
+def test_captured_long_prompt_carries_its_state():
+    """A sequence long enough for segments, captured with its final state over
+    its initial one: each replay takes the state on, as eager calls do."""
+    import torch
+    from test_regression_amd import mesa
+    say("case graph, segments")
+    t, _ = delta_inputs(7, 1, 1, 2, 4100, 64, 64, "bf16", lo=0.97)
+    d = {n: x.cuda() for n, x in t.items()}
+    args = [d[n] for n in ("q", "k", "v", "gamma", "beta")]
+    ws = torch.empty(mesa.mesa_delta_workspace_bytes(1, 2, 4100, 64, 64, 1), dtype=torch.uint8, device="cuda")
+    out, state = torch.empty_like(d["v"]), d["state"].clone()
+    call = lambda: mesa.mesa_delta_forward(*args, state, out=out, final_state=state, workspace=ws)  # noqa: E731
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    state.copy_(d["state"])
+    eager = d["state"].clone()
+    for i in range(3):
+        graph.replay()
+        o, eager = mesa.mesa_delta_forward(*args, eager, return_final=True)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o) and torch.equal(state, eager), i
+
+
+def test_calls_on_two_streams_at_once():
+    import torch
+    from test_regression_amd import mesa
+    say("case two streams")
+    d = [{n: x.cuda() for n, x in delta_inputs(s, 1, 2, 2, 1000, 64, 64, "bf16")[0].items()} for s in (8, 9)]
+    go = [torch.randn_like(x["v"]) for x in d]
+    fwd = lambda x, s: mesa.mesa_delta_forward(*x.values(), return_final=True, stream=s)  # noqa: E731
+    bwd = lambda x, g, s: mesa.mesa_delta_backward(x["q"], x["k"], x["v"], x["gamma"], x["beta"], g, x["state"], stream=s)  # noqa: E731
+    ref = [(fwd(x, None), bwd(x, g, None)) for x, g in zip(d, go)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            got[i].append((fwd(d[i], s), bwd(d[i], go[i], s)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for f, b in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(f, ref[i][0]))
+            assert all(torch.equal(b[n], ref[i][1][n]) for n in b)
