@@ -43,6 +43,9 @@ struct alignas(16) PrepLds {
     float redm[4], redp[4];
 };
 
+// 1 / x for a power of two from 2^-126 to 2^126.
+__device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
+
 // The units of a 64 x 64 float matrix in LDS, scaled by s, as fp16 planes in memory.
 template <int PLANES>
 __device__ __forceinline__ void planes_out(const float* F, uint16_t* img, float s) {
@@ -53,7 +56,7 @@ __device__ __forceinline__ void planes_out(const float* F, uint16_t* img, float 
         const int row = unit_row(u), q = unit_col(u);
         const float* p = F + row * kDF + 32 * (q / 4) + 4 * (q % 4);
         f16x8 hi, lo;
-        h2_split(load4(p), load4(p + 16), s, hi, lo);
+        h2_split_mix(load4(p), load4(p + 16), s, hi, lo);
         *reinterpret_cast<f16x8*>(img + 8 * u) = hi;
         if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(img + 8 * (kPlaneUnits + u)) = lo;
     }
@@ -140,12 +143,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
         const f32x4 ks = load4(L.ks + r0);
         f32x4 ki;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) ki[r] = 1.0f / ks[r];
+        for (int r = 0; r < 4; ++r) ki[r] = inverse_pow2(ks[r]);
         float mp = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = 16 * j + n;
-            const float f = L.beta[col] / L.ks[col];
+            const float f = L.beta[col] * inverse_pow2(L.ks[col]);
             f32x4 D;
             if (j < w) {
                 const f32x4 rf = load4(L.rowf[j] + r0);
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
         const int t = threadIdx.x;
         float* sc = a.scal + (size_t)blockIdx.x * kScal;
         const double Lt = L.L[t];
-        const float G = __builtin_amdgcn_exp2f((float)Lt), ki = 1.0f / L.ks[t], qi = 1.0f / L.qs[t], be = L.beta[t];
+        const float G = __builtin_amdgcn_exp2f((float)Lt), ki = inverse_pow2(L.ks[t]), qi = inverse_pow2(L.qs[t]), be = L.beta[t];
         sc[kKs + t] = L.ks[t];
         sc[kQs + t] = L.qs[t];
         sc[kGk + t] = G * ki;
