@@ -111,7 +111,8 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
         }
         // ---- dE = D_C b K dS' + (P diag(b))^T dO ----
         f16x8 Sh[NJ], Sl[NJ];
-        const int es = column_exp(S);
+        const float smax = column_max(S);
+        const int es = h2_exp(smax);
         column_split(S, es, Sh, Sl);
         const float is = pow2(-es - cs);
         f32x4 X[4], B[4];
@@ -203,7 +204,7 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
             });
         }
         // ---- dS = G_C dS' + Q^T (G dO) - K^T (G dV), dS kept scaled as the forward's S ----
-        const int ew = min(h2_exp(kslot_max(fmaxf(absmax(X), absmax(B)))), es + cs + 25);
+        const int ew = min(h2_exp(kslot_max(fmaxf(absmax(X), absmax(B)))), add_exp_cap(smax, es, cs, L.sc[kGc]));
         const float gs = __builtin_amdgcn_ldexpf(L.sc[kGc], ew - cs);
         cs = ew;
         f16x8 Xh[2], Xl[2];

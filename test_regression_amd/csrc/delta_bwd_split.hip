@@ -32,7 +32,7 @@ struct alignas(16) BwdSplitLds {
     uint32_t Q[NP][kDC * KW];
     uint32_t P[2 * kCPlane];
     f32x4 T[4][4][64], N[4][NS][64], dV[4][4 * kTileSlots];
-    int ne[4][64];   // the exponent that brings N's column to [2^14, 2^15)
+    int ne[4][64];   // the cap that N's column sets to the scale of what it is added to
     float sc[2][kScal];
 };
 
@@ -64,6 +64,7 @@ __device__ __forceinline__ void bwd_split(BwdSplitLds<DKP, In>& L, const DeltaBw
             const float* sc = L.sc[c & 1];
             const auto& K = L.K[c & 1];
             f16x8 Bh[2], Bl[2];
+            float smax = 0.f;
             int es = 0, ex = 0;
             if (live) {
                 {
@@ -75,7 +76,8 @@ __device__ __forceinline__ void bwd_split(BwdSplitLds<DKP, In>& L, const DeltaBw
                 }
                 // ---- dE = D_C b K dS' + T ----
                 f16x8 Sh[NJ], Sl[NJ];
-                es = column_exp(S);
+                smax = column_max(S);
+                es = h2_exp(smax);
                 column_split(S, es, Sh, Sl);
                 const float is = pow2(-es - cs);
                 f32x4 X[4];
@@ -132,7 +134,7 @@ __device__ __forceinline__ void bwd_split(BwdSplitLds<DKP, In>& L, const DeltaBw
                 for (int r = 0; r < 4; ++r) U[i][r] *= -gk[r];
             }
             // ---- dS = G_C dS' + N - K^T (G dV) ----
-            const int ew = min(column_exp(U), min(es + cs, L.ne[w][lane]) + 25);
+            const int ew = min(column_exp(U), min(add_exp_cap(smax, es, cs, sc[kGc]), L.ne[w][lane]));
             column_split(U, ew, Bh, Bl);
             const float gs = __builtin_amdgcn_ldexpf(sc[kGc], ew - cs), ns = pow2(ew);
             cs = ew;
@@ -252,7 +254,8 @@ __device__ __forceinline__ void bwd_split(BwdSplitLds<DKP, In>& L, const DeltaBw
                 t[m] *= ib;
                 L.N[w][m][lane] = t[m];
             }
-            L.ne[w][lane] = column_exp(t);
+            const float nmax = column_max(t);
+            L.ne[w][lane] = add_exp_cap(nmax, h2_exp(nmax), 0, 1.f);
         };
         auto values_out = [&](int c) {
             if (!live) return;

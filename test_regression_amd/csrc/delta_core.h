@@ -267,7 +267,20 @@ struct PlaneUnits {
 // The column's operands of a block of NT accumulator tiles, scaled by 2^E and
 // split in hi and lo (or hi alone).
 template <int NT>
-__device__ __forceinline__ int column_exp(const f32x4 (&X)[NT]) { return h2_exp(kslot_max(absmax(X))); }
+__device__ __forceinline__ float column_max(const f32x4 (&X)[NT]) { return kslot_max(absmax(X)); }
+template <int NT>
+__device__ __forceinline__ int column_exp(const f32x4 (&X)[NT]) { return h2_exp(column_max(X)); }
+
+// The largest scale 2^E for what a chunk adds to a column of the state, whose
+// largest magnitude is smax 2^-cs (scaled 2^es into fp16's range) before the
+// chunk's gates decay it by gc: the state goes to the same scale and stays
+// below 2^41 there.  Where no state is left the additions choose freely: a cap
+// from an empty or a forgotten column would push small ones into fp16's
+// subnormals.
+constexpr int kNoCap = 1 << 16;
+__device__ __forceinline__ int add_exp_cap(float smax, int es, int cs, float gc) {
+    return smax > 0.f && gc > 0.f ? es + cs + 26 - __builtin_amdgcn_frexp_expf(gc) : kNoCap;
+}
 // X holds VALU results, or MFMA results from before the last barrier (h2_split_mix).
 template <int NT>
 __device__ __forceinline__ void column_split(const f32x4 (&X)[NT], int E, f16x8 (&H)[NT / 2], f16x8 (&L)[NT / 2]) {

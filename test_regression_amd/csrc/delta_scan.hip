@@ -120,7 +120,8 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
         }
         // ---- K S and Q S ----
         f16x8 Sh[NJ], Sl[NJ];
-        const int es = column_exp(S);
+        const float smax = column_max(S);
+        const int es = h2_exp(smax);
         column_split(S, es, Sh, Sl);
         const float is = pow2(-es - cs);
         f32x4 X[4], Y[4];
@@ -226,9 +227,7 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
         // ---- S' = G_C S + K^T (D_C b E) ----
 #pragma unroll
         for (int i = 0; i < 4; ++i) U[i] *= row4(L.sc + kDb, i, g);
-        // a write that is 2^25 times smaller than the state takes a scale at
-        // which the scaled state stays below 2^40
-        const int ew = min(column_exp(U), es + cs + 25);
+        const int ew = min(column_exp(U), add_exp_cap(smax, es, cs, L.sc[kGc]));
         column_split(U, ew, Bh, Bl);
         const float gs = __builtin_amdgcn_ldexpf(L.sc[kGc], ew - cs);
         cs = ew;

@@ -113,6 +113,7 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
             __syncthreads();
             const float* sc = L.sc[c & 1];
             f16x8 Sh[NJ], Sl[NJ], Bh[2], Bl[2];
+            float smax = 0.f;
             int es = 0, er = 0;
             if (live) {
                 if constexpr (SAVE) {
@@ -123,7 +124,8 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
                         if (16 * m < a.dk) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
                 }
                 // ---- X = K S ----
-                es = column_exp(S);
+                smax = column_max(S);
+                es = h2_exp(smax);
                 column_split(S, es, Sh, Sl);
                 f32x4 X[4];
                 const auto& K = L.K[c & 1];
@@ -211,9 +213,7 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
             // ---- S' = G_C S + K^T (D_C b E) ----
 #pragma unroll
             for (int i = 0; i < 4; ++i) U[i] *= row4(sc + kDb, i, g);
-            // a write that is 2^25 times smaller than the state takes a scale at
-            // which the scaled state stays below 2^40
-            const int ew = min(column_exp(U), es + cs + 25);
+            const int ew = min(column_exp(U), add_exp_cap(smax, es, cs, sc[kGc]));
             column_split(U, ew, Bh, Bl);
             const float gs = __builtin_amdgcn_ldexpf(sc[kGc], ew - cs);
             cs = ew;
