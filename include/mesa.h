@@ -354,7 +354,12 @@ mesa_status mesa_hawk_scan(const void *x, const void *ga, const void *gx, int in
  *   workspace                   at least mesa_delta_workspace_bytes(...)
  * dk in {16, 32, 64, 128}, dv in {16, 32, 64, 128, 256}, T >= 0.  Sums, states
  * and decays are float32 (prefix sums of ln gamma float64); products run as
- * fp16 MFMAs on two-part splits (see mesa_dtype).  Values are taken as finite:
+ * fp16 MFMAs on two-part splits (see mesa_dtype; of a bfloat16 output's decayed
+ * scores the second part is a byte, which leaves them 2^-14).  A split shares
+ * its scale among a chunk of 64 tokens and keeps 2^-39 of its largest element,
+ * so that a value 2^-17 and more below the largest of its chunk and column (also
+ * one of a token with beta = 0) is met with fewer bits.  The sizes of v, states
+ * and gradients are otherwise free, from 2^-60 to 2^60.  Values are taken as finite:
  * a NaN or infinity reaches its chunk of 64 tokens and what follows in its head
  * (other heads and rows never), also from a token with beta = 0.
  */

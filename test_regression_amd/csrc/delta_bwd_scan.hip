@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
     const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
     const In* Op = static_cast<const In*>(b.grad_out) + (size_t)bh * a.T * a.dv + col0;
     In* Vp = static_cast<In*>(b.grad_v) + (size_t)bh * a.T * a.dv + col0;
-    constexpr size_t image = (size_t)4 * kPlaneUnits * 8;
+    constexpr size_t image = delta_image_words(false);
     const uint16_t* img = a.img + (size_t)bh * a.nc * image;
     const float* scal = a.scal + (size_t)bh * a.nc * kScal;
     const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;

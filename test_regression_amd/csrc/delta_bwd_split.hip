@@ -293,7 +293,7 @@ __device__ __forceinline__ void bwd_split(BwdSplitLds<DKP, In>& L, const DeltaBw
         const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
         const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
         const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
-        constexpr size_t image = (size_t)4 * kPlaneUnits * 8;
+        constexpr size_t image = delta_image_words(false);
         const uint16_t* img = a.img + (size_t)bh * a.nc * image;
         const float* scal = a.scal + (size_t)bh * a.nc * kScal;
         using Units = RowUnits<DKP, In>;

@@ -255,6 +255,21 @@ struct PlaneUnits {
         for (int i = 0; i < n; ++i)
             if (has(i)) raw[i] = *lane_at(reinterpret_cast<const u32x4*>(img), 16 * (threadIdx.x % 256 + 256 * i));
     }
+    // units that hold a byte an element, the upper byte of its fp16 pattern
+    __device__ __forceinline__ void load_bytes(const uint16_t* img) {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            if (has(i)) {
+                const uint2 b = *lane_at(reinterpret_cast<const uint2*>(img), 8 * (threadIdx.x % 256 + 256 * i));
+                raw[i][0] = b.x;
+                raw[i][1] = b.y;
+            }
+    }
+    __device__ __forceinline__ u32x4 from_bytes(int i) const {
+        const uint32_t x = raw[i][0], y = raw[i][1];
+        return u32x4{__builtin_amdgcn_perm(x, x, 0x010c000c), __builtin_amdgcn_perm(x, x, 0x030c020c),
+                     __builtin_amdgcn_perm(y, y, 0x010c000c), __builtin_amdgcn_perm(y, y, 0x030c020c)};
+    }
     __device__ __forceinline__ void store(uint32_t* P) const {
 #pragma unroll
         for (int i = 0; i < n; ++i) {

@@ -15,9 +15,11 @@
 // blocks by forward substitution, one a wave with a column a lane, then the
 // blocks below by diagonals, M_ij = -M_ii sum_{j<=k<i} (A diag b)_ik M_kj, on
 // float MFMAs whose accumulator order is the next product's operand order.
-// M is kept to 22 bits (its errors reach the state); P to 11 for bf16
-// outputs, whose own rounding is 8 times coarser, and to 22 for float ones and
-// for the gradients (those of the gates are float32 sums over P).
+// M is kept to 22 bits (its errors reach the state), and so is P for float
+// outputs and for the gradients (those of the gates are float32 sums over P).
+// For bf16 outputs P's second part is rounded to a byte, the upper half of its
+// fp16 pattern: P is then off by at most 2^-11 2^-3 = 2^-14 of an element, a
+// 32nd of the outputs' own smallest half step, for three quarters of the memory.
 //
 // 8x16x4096, dk = 128, bf16: 103-124 us for 266 MB of keys and queries in and 166
 // MB of planes out, 3.5-4.2 TB/s; vector instructions take 60 % of the cycles.
@@ -47,7 +49,7 @@ struct alignas(16) PrepLds {
 __device__ __forceinline__ float inverse_pow2(float x) { return __uint_as_float(0x7f000000u - __float_as_uint(x)); }
 
 // The units of a 64 x 64 float matrix in LDS, scaled by s, as fp16 planes in memory.
-template <int PLANES>
+template <bool BYTES>
 __device__ __forceinline__ void planes_out(const float* F, uint16_t* img, float s) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -58,11 +60,18 @@ __device__ __forceinline__ void planes_out(const float* F, uint16_t* img, float 
         f16x8 hi, lo;
         h2_split_mix(load4(p), load4(p + 16), s, hi, lo);
         *reinterpret_cast<f16x8*>(img + 8 * u) = hi;
-        if constexpr (PLANES == 2) *reinterpret_cast<f16x8*>(img + 8 * (kPlaneUnits + u)) = lo;
+        if constexpr (BYTES) {
+            // each half's upper byte, rounded to nearest
+            u32x4 w = __builtin_bit_cast(u32x4, lo) + 0x00800080u;
+            *reinterpret_cast<uint2*>(img + 8 * kPlaneUnits + 4 * u) =
+                make_uint2(__builtin_amdgcn_perm(w[1], w[0], 0x07050301), __builtin_amdgcn_perm(w[3], w[2], 0x07050301));
+        } else {
+            *reinterpret_cast<f16x8*>(img + 8 * (kPlaneUnits + u)) = lo;
+        }
     }
 }
 
-template <int DKP, typename In, int PP>
+template <int DKP, typename In, bool PBYTES>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
     constexpr int NP = delta_planes<In>(), NJ = DKP / 32, KW = delta_row_words(DKP);
     __shared__ PrepLds<DKP, NP> L;
@@ -236,12 +245,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
         if (j / 2 <= w / 2)
 #pragma unroll
             for (int r = 0; r < 4; ++r) L.N[(16 * w + 4 * g + r) * kDF + 16 * j + n] = P[j][r];
-    uint16_t* img = a.img + (size_t)blockIdx.x * ((2 + PP) * kPlaneUnits * 8);
+    uint16_t* img = a.img + (size_t)blockIdx.x * delta_image_words(PBYTES);
     const int EM = h2_exp(fmaxf(fmaxf(L.redm[0], L.redm[1]), fmaxf(L.redm[2], L.redm[3])));
     const int EP = h2_exp(fmaxf(fmaxf(L.redp[0], L.redp[1]), fmaxf(L.redp[2], L.redp[3])));
-    planes_out<2>(L.M, img, pow2(EM));
+    planes_out<false>(L.M, img, pow2(EM));
     __syncthreads();
-    planes_out<PP>(L.N, img + 2 * kPlaneUnits * 8, pow2(EP));
+    planes_out<PBYTES>(L.N, img + 2 * kPlaneUnits * 8, pow2(EP));
     if (threadIdx.x < kDC) {
         const int t = threadIdx.x;
         float* sc = a.scal + (size_t)blockIdx.x * kScal;
@@ -265,9 +274,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 template <int DKP>
 hipError_t prep_go(const DeltaArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.BH * a.nc));
-    if (!a.bf16) hipLaunchKernelGGL((delta_prep_kernel<DKP, float, 2>), grid, dim3(256), 0, s, a);
-    else if (a.p_planes == 2) hipLaunchKernelGGL((delta_prep_kernel<DKP, bf16_t, 2>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((delta_prep_kernel<DKP, bf16_t, 1>), grid, dim3(256), 0, s, a);
+    if (!a.bf16) hipLaunchKernelGGL((delta_prep_kernel<DKP, float, false>), grid, dim3(256), 0, s, a);
+    else if (!a.p_bytes) hipLaunchKernelGGL((delta_prep_kernel<DKP, bf16_t, false>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((delta_prep_kernel<DKP, bf16_t, true>), grid, dim3(256), 0, s, a);
     return hipGetLastError();
 }
 

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
     const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
     const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + col0;
     In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col0 : nullptr;
-    const size_t image = (size_t)(2 + a.p_planes) * kPlaneUnits * 8;
+    constexpr size_t image = delta_image_words(false);
     const uint16_t* img = a.img + (size_t)bh * a.nc * image;
     const float* scal = a.scal + (size_t)bh * a.nc * kScal;
     const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;   // this lane's row of the (dv x dk) state

@@ -9,9 +9,17 @@
 // from the fp16 parts of S and E that the state waves leave in LDS (in the
 // backward's recomputation they write E out).  Waves 8..11 stage the chunks.
 // Two barriers a chunk; between them:
-//   first half    split S, X, R    O of chunk c - 1    M of c in
-//   second half   E, update        --                  Q, P of c; K, V of c + 1 in
-// so K is held twice in LDS and everything else once.
+//   first half    split S, X, R    Q S of chunk c - 1    M of c in
+//   second half   E, update        P E, O out            Q, P of c; K, V of c + 1 in
+// so K is held twice in LDS and everything else once.  What the output waves
+// need of P and E is in their registers by the second half; O is turned around
+// in LDS of its own, for which float rows leave no room (these finish O in the
+// first half, in S's and E's place).
+//
+// S and E enter the outputs as hi + lo too, bf16 outputs among them.  With their
+// hi parts and P's alone (11 bits), a bf16 output in which the terms cancel is
+// off by up to 2^-11 of the terms; that took 314-326 us a layer of 8x16x4096 and
+// 303 us for 1x16x16384, against 336-348 and 309.
 //
 // With few heads the sequence is cut into segments that are passed over at once
 // (delta_segments.hip): first each segment but the last from a zero state (ENDS:
@@ -35,18 +43,22 @@ template <int DKP, typename In, bool OUT>
 struct alignas(16) ScanSplitLds {
     static constexpr int NP = delta_planes<In>(), KW = delta_row_words(DKP), NJ = DKP / 32;
     static constexpr int VW = sizeof(In) == 2 ? 8 : 20;   // words of a row of 16 values
-    static constexpr int parts = NP * (NJ + 2);           // operands of S and of E that the outputs take
+    static constexpr int parts = 2 * (NJ + 2);            // operands of S and of E that the outputs take
     uint32_t K[2][NP][kDC * KW];
     uint32_t M[2 * kCPlane];
     uint32_t V[4][kDC * VW];
     uint32_t Q[OUT ? NP : 1][OUT ? kDC * KW : 4];
-    uint32_t P[OUT ? NP * kCPlane : 4];
+    uint32_t P[OUT ? 2 * kCPlane : 4];
     union {
-        f16x8 ex[4][parts][64];             // for the outputs, whose waves then turn O around here
+        f16x8 ex[4][parts][64];             // for the outputs (hi parts of S, then E; the same, lo)
         f32x4 E[4][4 * kTileSlots];         // for the recomputation
     };
     float is[4][64], iu[4][64];
     float sc[2][kScal];
+    // where the output waves turn O around: apart for bf16 rows, so that it can
+    // wait for a chunk's second half, else in their part of ex
+    static constexpr bool APART = OUT && NP == 1;
+    uint2 O[APART ? 4 : 1][APART ? 4 * kTileSlots : 1];
 };
 
 // The units of a chunk's rows of v (16 `waves` columns) on their way into LDS.
@@ -166,14 +178,6 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
             }
             __syncthreads();
             if (!live) continue;
-            if constexpr (OUT) {
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    L.ex[w][j][lane] = Sh[j];
-                    if constexpr (NP == 2) L.ex[w][NJ + 2 + j][lane] = Sl[j];
-                }
-                L.is[w][lane] = pow2(-es - cs);
-            }
             // ---- E = M R ----
             f32x4 U[4];
 #pragma unroll
@@ -191,6 +195,14 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
 #pragma unroll
                 for (int i = 2 * j; i < 4; ++i) mfma_acc(U[i], mh[i], Bh[j]);
             }
+            if constexpr (OUT) {   // while E is on its way
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    L.ex[w][j][lane] = Sh[j];
+                    L.ex[w][NJ + 2 + j][lane] = Sl[j];
+                }
+                L.is[w][lane] = pow2(-es - cs);
+            }
             mfma_done(U);
             const float ir = sc[kMi] * pow2(-er);
 #pragma unroll
@@ -201,12 +213,11 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
             if constexpr (OUT) {
                 const int eu = column_exp(U);
                 f16x8 Eh[2], El[2];
-                if constexpr (NP == 2) column_split(U, eu, Eh, El);
-                else column_hi(U, eu, Eh);
+                column_split(U, eu, Eh, El);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     L.ex[w][NJ + j][lane] = Eh[j];
-                    if constexpr (NP == 2) L.ex[w][2 * NJ + 2 + j][lane] = El[j];
+                    L.ex[w][2 * NJ + 2 + j][lane] = El[j];
                 }
                 L.iu[w][lane] = sc[kPi] * pow2(-eu);
             }
@@ -248,65 +259,71 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
     } else if (w12 < 8) {
         // ---------------- outputs of the chunk before, or E out ----------------
         In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col0 : nullptr;
-        auto output = [&](int c) {
+        f32x4 Y[4], zs[4];   // G Q S, and the factors of P diag(b) E's rows
+        f16x8 Eh[2], El[2], ph[2][4], pl[2][4];
+        auto form_output = [&](int c) {
             if (!live) return;
             const float* sc = L.sc[c & 1];
-            f16x8 Sh[NJ], Sl[NJ], Eh[2], El[2];
+            f16x8 Sh[NJ], Sl[NJ];
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 Sh[j] = L.ex[w][j][lane];
-                if constexpr (NP == 2) Sl[j] = L.ex[w][NJ + 2 + j][lane];
+                Sl[j] = L.ex[w][NJ + 2 + j][lane];
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 Eh[j] = L.ex[w][NJ + j][lane];
-                if constexpr (NP == 2) El[j] = L.ex[w][2 * NJ + 2 + j][lane];
+                El[j] = L.ex[w][2 * NJ + 2 + j][lane];
             }
-            f32x4 Y[4], Z[4];
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 f16x8 qh[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) qh[i] = row_operand(L.Q[0], KW, i, j, n, g);
-                if constexpr (NP == 2) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) j ? mfma_acc(Y[i], qh[i], Sl[j]) : mfma_first(Y[i], qh[i], Sl[j]);
+                for (int i = 0; i < 4; ++i) j ? mfma_acc(Y[i], qh[i], Sl[j]) : mfma_first(Y[i], qh[i], Sl[j]);
+                if constexpr (NP == 2)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mfma_acc(Y[i], row_operand(L.Q[NP - 1], KW, i, j, n, g), Sh[j]);
-                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) NP == 2 || j ? mfma_acc(Y[i], qh[i], Sh[j]) : mfma_first(Y[i], qh[i], Sh[j]);
+                for (int i = 0; i < 4; ++i) mfma_acc(Y[i], qh[i], Sh[j]);
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                f16x8 ph[4];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int i = 2 * j; i < 4; ++i) ph[i] = compact_row_operand(L.P, i, j, n, g);
-                if constexpr (NP == 2) {
-#pragma unroll
-                    for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(Z[i], ph[i], El[j]) : mfma_first(Z[i], ph[i], El[j]);
-#pragma unroll
-                    for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], compact_row_operand(L.P + (NP - 1) * kCPlane, i, j, n, g), Eh[j]);
+                for (int i = 2 * j; i < 4; ++i) {
+                    ph[j][i] = compact_row_operand(L.P, i, j, n, g);
+                    pl[j][i] = compact_row_operand(L.P + kCPlane, i, j, n, g);
                 }
-#pragma unroll
-                for (int i = 2 * j; i < 4; ++i) NP == 2 || j ? mfma_acc(Z[i], ph[i], Eh[j]) : mfma_first(Z[i], ph[i], Eh[j]);
-            }
             mfma_done(Y);
-            mfma_done(Z);
             const float is = L.is[w][lane], iu = L.iu[w][lane];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const f32x4 gq = row4(sc + kGq, i, g), qi = row4(sc + kQi, i, g);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) Y[i][r] = (gq[r] * is) * Y[i][r] + (qi[r] * iu) * Z[i][r];
+                Y[i] *= row4(sc + kGq, i, g) * is;
+                zs[i] = row4(sc + kQi, i, g) * iu;
             }
+        };
+        auto finish_output = [&](int c) {
+            if (!live) return;
+            f32x4 Z[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(Z[i], ph[j][i], El[j]) : mfma_first(Z[i], ph[j][i], El[j]);
+#pragma unroll
+                for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], pl[j][i], Eh[j]);
+#pragma unroll
+                for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], ph[j][i], Eh[j]);
+            }
+            mfma_done(Z);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Y[i] += zs[i] * Z[i];
             const int valid = min(kDC, a.T - c * kDC);
             In* op = Op + (size_t)c * kDC * a.dv;
-            // turned around in this wave's own part of ex, which is read
             const uint32_t lo = (lane / 4 * a.dv + lane % 4 * 4) * sizeof(In), pitch = fresh(16 * a.dv * sizeof(In), c);
             wave_lds_sync();
             if constexpr (sizeof(In) == 2) {
-                uint2* T = reinterpret_cast<uint2*>(L.ex[w]);
+                uint2* T = L.O[w];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     T[tile_slot(i, n, g)] = make_uint2(bf16_pair(Y[i][0], Y[i][1]), bf16_pair(Y[i][2], Y[i][3]));
@@ -319,7 +336,7 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
                     if (16 * i + row < valid) *reinterpret_cast<uint2*>(lane_at(op, lo + i * pitch)) = v;
                 }
             } else {
-                f32x4* T = reinterpret_cast<f32x4*>(L.ex[w]);
+                f32x4* T = reinterpret_cast<f32x4*>(L.ex[w]);   // which is read
 #pragma unroll
                 for (int i = 0; i < 4; ++i) T[tile_slot(i, n, g)] = Y[i];
                 wave_lds_sync();
@@ -341,13 +358,19 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
             const int c = opaque(chunk);
             __syncthreads();
             if (chunk > c0) {
-                if constexpr (OUT) output(c - 1);
+                if constexpr (OUT) form_output(c - 1);
+                if constexpr (OUT && !Lds::APART) finish_output(c - 1);
                 if constexpr (SAVE) e_out(c - 1);
             }
             __syncthreads();
+            if constexpr (Lds::APART)
+                if (chunk > c0) finish_output(c - 1);
         }
         __syncthreads();
-        if constexpr (OUT) output(c1 - 1);
+        if constexpr (OUT) {
+            form_output(c1 - 1);
+            finish_output(c1 - 1);
+        }
         if constexpr (SAVE) e_out(c1 - 1);
     } else {
         // ---------------- staging ----------------
@@ -356,15 +379,16 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
         const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
         const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
         const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + colg;
-        const size_t image = (size_t)(2 + a.p_planes) * kPlaneUnits * 8;
+        constexpr bool PBYTES = !SAVE && NP == 1;   // as delta_prep.hip leaves P for the forward
+        constexpr size_t image = delta_image_words(PBYTES);
         const uint16_t* img = a.img + (size_t)bh * a.nc * image;
         const float* scal = a.scal + (size_t)bh * a.nc * kScal;
         using Units = RowUnits<DKP, In>;
         using MUnits = PlaneUnits<2>;
-        using PUnits = PlaneUnits<NP>;
+        using PUnits = PlaneUnits<1>;
         Units kr, qr;
         MUnits mr;
-        PUnits pr;
+        PUnits pr[2];
         ValueUnits<In> vr;
         float ksr[Units::n], qsr[Units::n];
         f32x4 scr{0.f, 0.f, 0.f, 0.f};
@@ -385,7 +409,10 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
             const float* sc = scal + (size_t)c * kScal;
 #pragma unroll
             for (int i = 0; i < Units::n; ++i) qsr[i] = *lane_at(sc + kQs, 4 * Units::row(i));
-            pr.load(img + c * image + 2 * kPlaneUnits * 8);
+            const uint16_t* p = img + c * image + 2 * kPlaneUnits * 8;
+            pr[0].load(p);
+            if constexpr (PBYTES) pr[1].load_bytes(p + kPlaneUnits * 8);
+            else pr[1].load(p + kPlaneUnits * 8);
         };
         auto put_k = [&](int c) {
 #pragma unroll
@@ -412,7 +439,10 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
                 for (int i = 0; i < Units::n; ++i) qr.template store<NP>(L.Q, i, qsr[i]);
 #pragma unroll
                 for (int i = 0; i < PUnits::n; ++i)
-                    if (PUnits::has(i)) *reinterpret_cast<u32x4*>(compact_unit(L.P, tid + 256 * i)) = pr.raw[i];
+                    if (PUnits::has(i)) {
+                        *reinterpret_cast<u32x4*>(compact_unit(L.P, tid + 256 * i)) = pr[0].raw[i];
+                        *reinterpret_cast<u32x4*>(compact_unit(L.P, kPlaneUnits + tid + 256 * i)) = PBYTES ? pr[1].from_bytes(i) : pr[1].raw[i];
+                    }
                 if (chunk + 1 < c1) fetch_q(chunk + 1);
             }
             if (chunk + 1 < c1) {

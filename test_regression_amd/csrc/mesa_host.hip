@@ -547,11 +547,6 @@ mesa_status mesa_hawk_scan(const void* x, const void* ga, const void* gx, int in
 // ---- gated delta rule ----
 static bool dtype_ok(int t) { return t == MESA_DTYPE_F32 || t == MESA_DTYPE_BF16; }
 
-// Bytes per head and chunk: the fp16 planes of M (two) and P (one for bf16,
-// two for float32), then the scalars.
-static size_t delta_image_halfs(int dtype) {
-    return (size_t)(dtype == MESA_DTYPE_BF16 ? 3 : 4) * mesa::kDeltaPlaneUnits * 8;
-}
 static long delta_chunks(int T) { return ((long)T + mesa::kDeltaChunk - 1) / mesa::kDeltaChunk; }
 
 // Bytes of the segments' end and start states (0 with one segment).
@@ -569,7 +564,7 @@ static void delta_use_segments(mesa::DeltaArgs* a, int nseg, float* ws) {
 size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype) {
     if (B <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
     const long BH = (long)B * H, nc = delta_chunks(T);
-    return (size_t)BH * nc * (delta_image_halfs(dtype) * 2 + mesa::kDeltaScal * sizeof(float)) +
+    return (size_t)BH * nc * (mesa::delta_image_words(dtype == MESA_DTYPE_BF16) * 2 + mesa::kDeltaScal * sizeof(float)) +
            delta_segment_bytes(BH, mesa::delta_segments(BH, (int)nc, dk, dv, dtype == MESA_DTYPE_BF16), dk, dv);
 }
 
@@ -627,9 +622,9 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes,
                     mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype));
     uint16_t* img = static_cast<uint16_t*>(workspace);
-    float* scal = reinterpret_cast<float*>(img + (size_t)BH * nc * delta_image_halfs(dtype));
+    float* scal = reinterpret_cast<float*>(img + (size_t)BH * nc * mesa::delta_image_words(dtype == MESA_DTYPE_BF16));
     mesa::DeltaArgs a{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
-                      out, final_state, img, scal, dtype == MESA_DTYPE_BF16 ? 1 : 2};
+                      out, final_state, img, scal, dtype == MESA_DTYPE_BF16};
     delta_use_segments(&a, mesa::delta_segments(BH, (int)nc, dk, dv, a.bf16), scal + (size_t)BH * nc * mesa::kDeltaScal);
     hipError_t e = timed_launch(MESA_KERNEL_DELTA_PREP, s, [&] { return mesa::launch_delta_prep(a, s); });
     if (e != hipSuccess) return hip_fail(e, "delta chunk-matrix kernel launch");
@@ -645,7 +640,7 @@ struct DeltaBwdLayout {
 static DeltaBwdLayout delta_bwd_layout(int B, int Hk, int H, int T, int dk, int dv) {
     const size_t n = (size_t)B * H * delta_chunks(T), C = mesa::kDeltaChunk;
     DeltaBwdLayout l{};
-    size_t o = n * delta_image_halfs(MESA_DTYPE_F32) * 2;   // two planes of M and of P for either type
+    size_t o = n * mesa::delta_image_words(false) * 2;
     l.scal = o; o += n * mesa::kDeltaScal * sizeof(float);
     l.S = o;    o += n * dv * dk * sizeof(float);
     l.dS = o;   o += n * dv * dk * sizeof(float);
@@ -698,7 +693,7 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
     auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
     mesa::DeltaBwdArgs a{};
     a.f = mesa::DeltaArgs{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
-                          nullptr, nullptr, reinterpret_cast<uint16_t*>(ws), at(l.scal), 2, at(l.S), at(l.E)};
+                          nullptr, nullptr, reinterpret_cast<uint16_t*>(ws), at(l.scal), false, at(l.S), at(l.E)};
     delta_use_segments(&a.f, 1, nullptr);
     a.grad_out = grad_out;
     a.grad_final = grad_final;

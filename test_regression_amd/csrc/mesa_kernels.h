@@ -97,12 +97,15 @@ hipError_t launch_hawk(const HawkArgs& a, hipStream_t s);
 constexpr int kDeltaChunk = 64;   // tokens per chunk
 constexpr int kDeltaScal = 512;   // floats of per-chunk scalars in the workspace
 constexpr int kDeltaPlaneUnits = 384;   // 16-byte units of a plane of M or P in the workspace
+// A chunk's planes in the workspace, in 2-byte words: two of M, then P's first
+// part and its second, which is a plane too or (p_bytes) a byte an element.
+constexpr size_t delta_image_words(bool p_bytes) { return (size_t)(p_bytes ? 7 : 8) * kDeltaPlaneUnits * 4; }
 struct DeltaArgs {
     const void* q; const void* k; const void* v; const float* gamma; const float* beta; const float* state0;
     long BH; int Hk; int H; int T; int dk; int dv; int nc; int bf16;
     void* out; float* final_state;
     uint16_t* img; float* scal;   // workspace: per head and chunk the planes of M and P, the scalars
-    int p_planes;                 // planes of P in img: 1 (bf16 forward) or 2
+    bool p_bytes;                 // how img holds P (delta_image_words): in bytes for the bf16 forward
     float* S; float* E;           // backward workspace: chunk start states [BH][nc][dv][dk], E [BH][nc][64][dv]
     int nseg; int seg_chunks;     // segments of a sequence that are passed over at once, chunks of one
     float* seg_end;               // nseg > 1, workspace: [BH][nseg - 1][dv + dk][dk] (delta_segments.hip)
