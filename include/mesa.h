@@ -362,6 +362,9 @@ mesa_status mesa_hawk_scan(const void *x, const void *ga, const void *gx, int in
  * and gradients are otherwise free, from 2^-60 to 2^60.  Values are taken as finite:
  * a NaN or infinity reaches its chunk of 64 tokens and what follows in its head
  * (other heads and rows never), also from a token with beta = 0.
+ *
+ * Here and in the calls below, outputs and workspace share no memory with an
+ * input or with one another but where it says "may be"; others are refused.
  */
 size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype);
 mesa_status mesa_delta_forward(const void *q, const void *k, const void *v, int dtype, const float *gamma,

@@ -10,6 +10,8 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -544,6 +546,32 @@ mesa_status mesa_hawk_scan(const void* x, const void* ga, const void* gx, int in
     return MESA_OK;
 }
 
+// A tensor of a call: its address (NULL when absent), size and name, and for an
+// output the input that it may be written over, address for address.
+struct Span {
+    const void* p;
+    size_t bytes;
+    const char* name;
+    const char* over = nullptr;
+};
+// Refuses outputs that share memory with an input or with one another: the
+// kernels of a call read and write in an order of their own.
+static mesa_status no_alias(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    auto shared = [](const Span& a, const Span& b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p && b.p && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            if (shared(*o, i) && !(o->p == i.p && o->over && !strcmp(o->over, i.name)))
+                return fail(MESA_ERR_INVALID_ARGUMENT, "%s must not alias %s", o->name, i.name);
+        for (auto q = outs.begin(); q != o; ++q)
+            if (shared(*o, *q)) return fail(MESA_ERR_INVALID_ARGUMENT, "%s must not alias %s", o->name, q->name);
+    }
+    return MESA_OK;
+}
+static size_t bytes_of(int dtype, double n) { return (size_t)(n * (dtype == MESA_DTYPE_BF16 ? 2 : 4)); }
+
 // ---- gated delta rule ----
 static bool dtype_ok(int t) { return t == MESA_DTYPE_F32 || t == MESA_DTYPE_BF16; }
 
@@ -608,19 +636,23 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(state0, 16) ||
         !aligned(final_state, 16) || !aligned(workspace, 16) || !aligned(gamma, 4) || !aligned(beta, 4))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for tensors/workspace, 4 B for gamma/beta)");
-    if (out && (out == q || out == k || out == v))
-        return fail(MESA_ERR_INVALID_ARGUMENT, "out must not alias q, k or v");
-    hipStream_t s = static_cast<hipStream_t>(stream);
     const long BH = (long)B * H, nc = delta_chunks(T);
+    const size_t need = mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype);
+    if (workspace_bytes < need)
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    const size_t kb = bytes_of(dtype, (double)B * Hk * T * dk), vb = bytes_of(dtype, (double)BH * T * dv),
+                 gb = (size_t)BH * T * sizeof(float), sb = (size_t)BH * dv * dk * sizeof(float);
+    const mesa_status al = no_alias(
+        {{out, vb, "out"}, {final_state, sb, "final_state", "state0"}, {workspace, need, "workspace"}},
+        {{q, kb, "q"}, {k, kb, "k"}, {v, vb, "v"}, {gamma, gb, "gamma"}, {beta, gb, "beta"}, {state0, sb, "state0"}});
+    if (al != MESA_OK) return al;
+    hipStream_t s = static_cast<hipStream_t>(stream);
     if (T == 0) {
         // no token: the final state is the initial one
         const hipError_t e = copy_or_zero(final_state, state0, (size_t)BH * dv * dk, s);
         if (e != hipSuccess) return hip_fail(e, "final state for T = 0");
         return MESA_OK;
     }
-    if (workspace_bytes < mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype))
-        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes,
-                    mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype));
     uint16_t* img = static_cast<uint16_t*>(workspace);
     float* scal = reinterpret_cast<float*>(img + (size_t)BH * nc * mesa::delta_image_words(dtype == MESA_DTYPE_BF16));
     mesa::DeltaArgs a{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
@@ -674,21 +706,24 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
         !aligned(grad_gamma, 4) || !aligned(grad_beta, 4))
         return fail(MESA_ERR_INVALID_ARGUMENT,
                     "misaligned pointer (16 B for tensors/workspace, 4 B for gamma/beta and their gradients)");
-    hipStream_t s = static_cast<hipStream_t>(stream);
     const long BH = (long)B * H, nc = delta_chunks(T);
+    const DeltaBwdLayout l = delta_bwd_layout(B, Hk, H, T, dk, dv);
+    if (workspace_bytes < l.total)
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, l.total);
+    const size_t kb = bytes_of(dtype, (double)B * Hk * T * dk), vb = bytes_of(dtype, (double)BH * T * dv),
+                 gb = (size_t)BH * T * sizeof(float), sb = (size_t)BH * dv * dk * sizeof(float);
+    const mesa_status al = no_alias(
+        {{grad_q, kb, "grad_q"}, {grad_k, kb, "grad_k"}, {grad_v, vb, "grad_v"}, {grad_gamma, gb, "grad_gamma"},
+         {grad_beta, gb, "grad_beta"}, {grad_state, sb, "grad_state", "grad_final"}, {workspace, l.total, "workspace"}},
+        {{q, kb, "q"}, {k, kb, "k"}, {v, vb, "v"}, {gamma, gb, "gamma"}, {beta, gb, "beta"}, {state0, sb, "state0"},
+         {grad_out, vb, "grad_out"}, {grad_final, sb, "grad_final"}});
+    if (al != MESA_OK) return al;
+    hipStream_t s = static_cast<hipStream_t>(stream);
     if (T == 0) {
         const hipError_t e = copy_or_zero(grad_state, grad_final, (size_t)BH * dv * dk, s);
         if (e != hipSuccess) return hip_fail(e, "state gradient for T = 0");
         return MESA_OK;
     }
-    const void* ins[] = {q, k, v, grad_out};
-    const void* outs[] = {grad_q, grad_k, grad_v};
-    for (const void* o : outs)
-        for (const void* i : ins)
-            if (o == i) return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
-    const DeltaBwdLayout l = delta_bwd_layout(B, Hk, H, T, dk, dv);
-    if (workspace_bytes < l.total)
-        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, l.total);
     char* ws = static_cast<char*>(workspace);
     auto at = [&](size_t o) { return reinterpret_cast<float*>(ws + o); };
     mesa::DeltaBwdArgs a{};
@@ -726,7 +761,11 @@ mesa_status mesa_delta_step(const void* q, const void* k, const void* v, int dty
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(state, 16) ||
         !aligned(gamma, 4) || !aligned(beta, 4))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for tensors, 4 B for gamma/beta)");
-    if (out == q || out == k || out == v) return fail(MESA_ERR_INVALID_ARGUMENT, "out must not alias q, k or v");
+    const size_t kb = bytes_of(dtype, (double)N * Hk * dk), vb = bytes_of(dtype, (double)N * H * dv),
+                 gb = (size_t)N * H * sizeof(float), sb = (size_t)N * H * dv * dk * sizeof(float);
+    const mesa_status al = no_alias({{out, vb, "out"}, {state, sb, "state"}},
+                                    {{q, kb, "q"}, {k, kb, "k"}, {v, vb, "v"}, {gamma, gb, "gamma"}, {beta, gb, "beta"}});
+    if (al != MESA_OK) return al;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const mesa::DeltaStepArgs a{q, k, v, gamma, beta, state, (long)N * H, Hk, H, dk, dv, dtype == MESA_DTYPE_BF16,
                                 out, 0};
@@ -760,7 +799,10 @@ mesa_status mesa_gate_norm(const void* x, int x_dtype, const void* gate, int dty
     if (st != MESA_OK) return st;
     if (T > 0 && !y) return fail(MESA_ERR_INVALID_ARGUMENT, "y must be non-null");
     if (!aligned(y, 16)) return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
-    if (y && (y == x || y == gate)) return fail(MESA_ERR_INVALID_ARGUMENT, "y must not alias x or gate");
+    const double rows = (double)B * H * T * d;
+    const size_t xb = bytes_of(x_dtype, rows), yb = bytes_of(dtype, rows);
+    const mesa_status al = no_alias({{y, yb, "y"}}, {{x, xb, "x"}, {gate, yb, "gate"}, {w, (size_t)H * d * sizeof(float), "w"}});
+    if (al != MESA_OK) return al;
     if (T == 0) return MESA_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const mesa::GateNormArgs a{x, gate, w, eps, B, H, T, d, x_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16, y};
@@ -807,12 +849,15 @@ mesa_status mesa_gate_norm_backward(const void* x, int x_dtype, const void* gate
         if (e != hipSuccess) return hip_fail(e, "zero fill of grad_w");
         return MESA_OK;
     }
-    for (const void* o : {(const void*)grad_x, (const void*)grad_gate})
-        if (o && (o == x || o == gate || o == grad_y))
-            return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
     const size_t need = mesa_gate_norm_backward_workspace_bytes(B, H, T, d);
     if (workspace_bytes < need)
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    const double n = (double)B * H * T * d;
+    const size_t xb = bytes_of(x_dtype, n), yb = bytes_of(dtype, n), wb = (size_t)H * d * sizeof(float);
+    const mesa_status al = no_alias(
+        {{grad_x, xb, "grad_x"}, {grad_gate, yb, "grad_gate"}, {grad_w, wb, "grad_w"}, {workspace, need, "workspace"}},
+        {{x, xb, "x"}, {gate, yb, "gate"}, {w, wb, "w"}, {grad_y, yb, "grad_y"}});
+    if (al != MESA_OK) return al;
     mesa::GateNormBwdArgs a{x, gate, w, eps, B, H, T, d, x_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16,
                             grad_y, grad_x, grad_gate, grad_w, static_cast<float*>(workspace), 0, 0};
     gate_parts(B, H, T, d, &a.parts, &a.rows_per_part);
@@ -848,8 +893,10 @@ mesa_status mesa_residual_norm(const void* h, int h_dtype, const void* y, int dt
         return fail(MESA_ERR_INVALID_ARGUMENT, "h_out must be given exactly when y is");
     if (!aligned(h_out, 16) || !aligned(n, 16))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for every tensor)");
-    if (n && (n == h || n == y || n == h_out)) return fail(MESA_ERR_INVALID_ARGUMENT, "n must not alias h, y or h_out");
-    if (h_out && h_out == y) return fail(MESA_ERR_INVALID_ARGUMENT, "h_out must not alias y");
+    const size_t hb = bytes_of(h_dtype, (double)R * D), yb = bytes_of(dtype, (double)R * D), wb = (size_t)D * sizeof(float);
+    const mesa_status al = no_alias({{h_out, hb, "h_out", "h"}, {n, yb, "n"}},
+                                    {{h, hb, "h"}, {y, yb, "y"}, {scale, wb, "scale"}, {w, wb, "w"}});
+    if (al != MESA_OK) return al;
     if (R == 0) return MESA_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const mesa::ResidualNormArgs a{h, y, w, scale, eps, R, D, h_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16,
@@ -891,12 +938,15 @@ mesa_status mesa_residual_norm_backward(const void* h, int h_dtype, const void* 
         if (e != hipSuccess) return hip_fail(e, "zero fill of the parameter gradients");
         return MESA_OK;
     }
-    for (const void* o : {(const void*)grad_h, (const void*)grad_y})
-        if (o && (o == h || o == y || o == grad_n || o == grad_h_out))
-            return fail(MESA_ERR_INVALID_ARGUMENT, "the gradients must not alias the inputs");
     const size_t need = mesa_residual_norm_backward_workspace_bytes(R, D);
     if (workspace_bytes < need)
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    const size_t hb = bytes_of(h_dtype, (double)R * D), yb = bytes_of(dtype, (double)R * D), wb = (size_t)D * sizeof(float);
+    const mesa_status al = no_alias(
+        {{grad_h, hb, "grad_h"}, {grad_y, yb, "grad_y"}, {grad_w, wb, "grad_w"}, {grad_scale, wb, "grad_scale"},
+         {workspace, need, "workspace"}},
+        {{h, hb, "h"}, {y, yb, "y"}, {scale, wb, "scale"}, {w, wb, "w"}, {grad_n, yb, "grad_n"}, {grad_h_out, hb, "grad_h_out"}});
+    if (al != MESA_OK) return al;
     const mesa::ResidualNormBwdArgs a{h, y, w, scale, eps, R, D, h_dtype == MESA_DTYPE_BF16, dtype == MESA_DTYPE_BF16,
                                       grad_n, grad_h_out, grad_h, grad_y, grad_w, grad_scale,
                                       static_cast<float*>(workspace), residual_parts(R, D)};
