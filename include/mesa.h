@@ -351,7 +351,9 @@ mesa_status mesa_hawk_scan(const void *x, const void *ga, const void *gx, int in
  *   state0     [B, H, dv, dk]   float32, or NULL
  *   out        [B, H, T, dv]    dtype, written (bfloat16 rounds to nearest even)
  *   final_state [B, H, dv, dk]  float32 S_T, or NULL; may be state0 itself
- *   workspace                   at least mesa_delta_workspace_bytes(...)
+ *   workspace                   at least mesa_delta_workspace_bytes(...), which
+ *                               never decreases with B, H or T: one for the
+ *                               largest batch and longest sequence serves all
  * dk in {16, 32, 64, 128}, dv in {16, 32, 64, 128, 256}, T >= 0.  Sums, states
  * and decays are float32 (prefix sums of ln gamma float64); products run as
  * fp16 MFMAs on two-part splits (see mesa_dtype; of a bfloat16 output's decayed

@@ -78,22 +78,38 @@ __global__ __launch_bounds__(DK * 4) void delta_segments_kernel(DeltaArgs a) {
 // with one, two or four column tiles a workgroup (up to 256, 512, 1024 tiles at
 // once; measured with bf16 and dk = 128), the two more launches about 20 us.
 // 1x16x16384 takes 307 us in all in the eight segments this gives, 690 in one.
+struct SegmentModel {
+    double whole, ends, real;   // us a chunk: the sequence in one piece; the segments' ends, the pass from their starts
+};
+static SegmentModel segment_model(long BH, int dk, int dv, int n) {
+    auto chunk_us = [](long tiles) { return tiles <= 256 ? 2.5 : tiles <= 512 ? 2.9 : 3.5 * ((tiles + 1023) / 1024); };
+    const long tiles = BH * (dv / 16);
+    return {chunk_us(tiles), chunk_us(tiles + (n - 2) * BH * ((dv + dk) / 16)), chunk_us(tiles * n)};
+}
 int delta_segments(long BH, int nc, int dk, int dv, int bf16) {
     if (!bf16 && dk == 128) return 1;
-    auto pass = [](long tiles, int chunks) {
-        const long rounds = (tiles + 1023) / 1024;
-        return chunks * (tiles <= 256 ? 2.5 : tiles <= 512 ? 2.9 : 3.5 * rounds);
-    };
-    const long tiles = BH * (dv / 16);
     int best = 1;
-    double t1 = pass(tiles, nc);
+    double t1 = segment_model(BH, dk, dv, 4).whole * nc;
     for (int n : {4, 8, 16}) {
         const int chunks = (nc + n - 1) / n;
         if (chunks < 4 || (n - 1) * chunks >= nc) continue;   // the last segment is not empty
-        const double t = 20.0 + pass(tiles + (n - 2) * BH * ((dv + dk) / 16), chunks) + pass(tiles * n, chunks);
+        const SegmentModel m = segment_model(BH, dk, dv, n);
+        const double t = 20.0 + chunks * m.ends + chunks * m.real;
         if (t < 0.9 * t1) { best = n; t1 = t; }
     }
     return best;
+}
+
+// The most segments that any sequence of up to nc chunks takes: n is taken for
+// nc' chunks only with nc' > 3 n and 20 + (ends + real) nc' / n < 0.9 whole nc',
+// and both then hold for nc >= nc' too.
+int delta_segments_most(long BH, int nc, int dk, int dv, int bf16) {
+    if (!bf16 && dk == 128) return 1;
+    for (int n : {16, 8, 4}) {
+        const SegmentModel m = segment_model(BH, dk, dv, n);
+        if (nc > 3 * n && (0.9 * m.whole - (m.ends + m.real) / n) * nc > 20.0) return n;
+    }
+    return 1;
 }
 
 hipError_t launch_delta_segments(const DeltaArgs& a, hipStream_t s) {

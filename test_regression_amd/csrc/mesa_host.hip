@@ -589,11 +589,28 @@ static void delta_use_segments(mesa::DeltaArgs* a, int nseg, float* ws) {
     a->seg_start = ws + (size_t)a->BH * (nseg - 1) * (a->dv + a->dk) * a->dk;
 }
 
+// Bytes of a head's chunk: its planes of M and P, its scalars.
+static size_t delta_chunk_bytes(int dtype) {
+    return mesa::delta_image_words(dtype == MESA_DTYPE_BF16) * 2 + mesa::kDeltaScal * sizeof(float);
+}
+
 size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype) {
     if (B <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
+    // enough for every smaller batch and shorter sequence too: the states of the
+    // segments, which only few heads have, may be more than those of the heads
+    // and chunks that come on top.  From 1280 column tiles on there are none
+    // (delta_segments_most: ends + real >= 3.5 (2 n - 1) a round of tiles, whole
+    // at most 3.5 a started round, and n >= 4).
     const long BH = (long)B * H, nc = delta_chunks(T);
-    return (size_t)BH * nc * (mesa::delta_image_words(dtype == MESA_DTYPE_BF16) * 2 + mesa::kDeltaScal * sizeof(float)) +
-           delta_segment_bytes(BH, mesa::delta_segments(BH, (int)nc, dk, dv, dtype == MESA_DTYPE_BF16), dk, dv);
+    size_t most = delta_chunk_bytes(dtype) * BH * nc;
+    const int bf16 = dtype == MESA_DTYPE_BF16;
+    int found = 1;   // segments of the head counts seen so far: fewer heads matter only with more of them
+    if (nc > 12)
+        for (long b = std::min(BH, 1280L * 16 / std::max(dv, 16)); b > 0 && found < 16; --b) {
+            const int n = mesa::delta_segments_most(b, (int)nc, dk, dv, bf16);
+            if (n > found) most = std::max(most, delta_chunk_bytes(dtype) * b * nc + delta_segment_bytes(b, found = n, dk, dv));
+        }
+    return most;
 }
 
 // A launch holds fewer than 2^32 threads.
@@ -637,7 +654,8 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
         !aligned(final_state, 16) || !aligned(workspace, 16) || !aligned(gamma, 4) || !aligned(beta, 4))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for tensors/workspace, 4 B for gamma/beta)");
     const long BH = (long)B * H, nc = delta_chunks(T);
-    const size_t need = mesa_delta_workspace_bytes(B, H, T, dk, dv, dtype);
+    const int nseg = T > 0 ? mesa::delta_segments(BH, (int)nc, dk, dv, dtype == MESA_DTYPE_BF16) : 1;
+    const size_t need = delta_chunk_bytes(dtype) * BH * nc + delta_segment_bytes(BH, nseg, dk, dv);
     if (workspace_bytes < need)
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
     const size_t kb = bytes_of(dtype, (double)B * Hk * T * dk), vb = bytes_of(dtype, (double)BH * T * dv),
@@ -657,7 +675,7 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
     float* scal = reinterpret_cast<float*>(img + (size_t)BH * nc * mesa::delta_image_words(dtype == MESA_DTYPE_BF16));
     mesa::DeltaArgs a{q, k, v, gamma, beta, state0, BH, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16,
                       out, final_state, img, scal, dtype == MESA_DTYPE_BF16};
-    delta_use_segments(&a, mesa::delta_segments(BH, (int)nc, dk, dv, a.bf16), scal + (size_t)BH * nc * mesa::kDeltaScal);
+    delta_use_segments(&a, nseg, scal + (size_t)BH * nc * mesa::kDeltaScal);
     hipError_t e = timed_launch(MESA_KERNEL_DELTA_PREP, s, [&] { return mesa::launch_delta_prep(a, s); });
     if (e != hipSuccess) return hip_fail(e, "delta chunk-matrix kernel launch");
     e = timed_launch(MESA_KERNEL_DELTA_SCAN, s, [&] { return mesa::launch_delta_scan(a, s); });
@@ -824,10 +842,9 @@ static void gate_parts(int B, int H, int T, int d, int* parts, long* rows) {
 
 size_t mesa_gate_norm_backward_workspace_bytes(int B, int H, int T, int d) {
     if (B <= 0 || H <= 0 || T <= 0 || d <= 0 || d > 2048) return 0;
-    int parts;
-    long rows;
-    gate_parts(B, H, T, d, &parts, &rows);
-    return (size_t)parts * H * d * sizeof(float);
+    // before gate_parts rounds them, so that fewer rows or heads never need more
+    const long passes = ((long)B * T + 2048 / d - 1) / (2048 / d);
+    return (size_t)std::min(passes * H, std::max(1024L, (long)H)) * d * sizeof(float);
 }
 
 mesa_status mesa_gate_norm_backward(const void* x, int x_dtype, const void* gate, int dtype, const float* w, float eps,
@@ -913,7 +930,8 @@ static int residual_parts(int R, int D) { return (int)std::min<long>(((long)R + 
 
 size_t mesa_residual_norm_backward_workspace_bytes(int R, int D) {
     if (R <= 0 || D <= 0) return 0;
-    return (size_t)residual_parts(R, D) * 2 * D * sizeof(float);
+    // up to 2048 columns there may be twice the parts
+    return (size_t)std::max((long)residual_parts(R, D) * D, (long)residual_parts(R, 2048) * std::min(D, 2048)) * 2 * sizeof(float);
 }
 
 mesa_status mesa_residual_norm_backward(const void* h, int h_dtype, const void* y, int dtype, const float* scale,

@@ -127,6 +127,7 @@ hipError_t launch_delta_scan_split(const DeltaArgs& a, hipStream_t s);   // with
 hipError_t launch_delta_ends_split(const DeltaArgs& a, hipStream_t s);    // the segments' end states and transitions
 hipError_t launch_delta_segments(const DeltaArgs& a, hipStream_t s);      // and from them the segments' start states
 int delta_segments(long BH, int nc, int dk, int dv, int bf16);            // the number of segments
+int delta_segments_most(long BH, int nc, int dk, int dv, int bf16);       // the largest of any length up to nc
 hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s);   // the scan without out, writing S and E (float, dk 128)
 struct DeltaStepArgs {
     const void* q; const void* k; const void* v; const float* gamma; const float* beta; float* state;
