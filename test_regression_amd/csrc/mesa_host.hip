@@ -616,8 +616,8 @@ size_t mesa_delta_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype
 // A launch holds fewer than 2^32 threads.
 constexpr double kMaxThreads = 4.0e9;
 
-// The checks the delta entry points share; `rows` is T or, for the step, 1.
-static mesa_status delta_checks(int dtype, int B, int Hk, int H, int T, int dk, int dv) {
+// The checks the delta entry points share; T is 1 for the step.
+static mesa_status delta_checks(int dtype, int B, int Hk, int H, int T, int dk, int dv, bool step) {
     if (!dtype_ok(dtype))
         return fail(MESA_ERR_INVALID_ARGUMENT, "dtype %d is not MESA_DTYPE_F32 or MESA_DTYPE_BF16", dtype);
     if (B <= 0 || Hk <= 0 || H <= 0 || T < 0 || dk <= 0 || dv <= 0)
@@ -626,11 +626,13 @@ static mesa_status delta_checks(int dtype, int B, int Hk, int H, int T, int dk, 
     if (H % Hk != 0) return fail(MESA_ERR_INVALID_ARGUMENT, "H=%d is not a multiple of Hk=%d", H, Hk);
     if (!supported_d(dk)) return fail(MESA_ERR_UNSUPPORTED, "dk=%d not built (16, 32, 64, 128)", dk);
     if (!supported_d(dv) && dv != 256) return fail(MESA_ERR_UNSUPPORTED, "dv=%d not built (16, 32, 64, 128, 256)", dv);
-    // the launches' threads: 256 a head and chunk, two passes of 768 a head and
-    // 64 columns of dv, the step's at most 8 a row of the state, and
-    // one for four features where the gradients of shared heads are summed
+    // the launches' threads: the step's at most 8 a row of the state; else 256 a
+    // head and chunk, two passes of 768 a head (in eights) and 64 columns of dv,
+    // and one for four features where the gradients of shared heads are summed
     const double BH = (double)B * H;
-    const double threads = std::max({BH * delta_chunks(T) * 256, BH * std::max(dv, 32) * 64, (double)B * Hk * T * dk / 4});
+    const double threads = step ? BH * dv * 8
+                                : std::max({BH * delta_chunks(T) * 256, (BH + 7) * ((dv + 63) / 64) * 2 * 768,
+                                            (double)B * Hk * T * dk / 4});
     if (threads > kMaxThreads)
         return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B*H=%ld, chunks=%ld)", (long)B * H, delta_chunks(T));
     return MESA_OK;
@@ -646,7 +648,7 @@ mesa_status mesa_delta_forward(const void* q, const void* k, const void* v, int 
                                int dv, void* out, float* final_state, void* workspace, size_t workspace_bytes,
                                void* stream) {
     g_err.clear();
-    const mesa_status st = delta_checks(dtype, B, Hk, H, T, dk, dv);
+    const mesa_status st = delta_checks(dtype, B, Hk, H, T, dk, dv, false);
     if (st != MESA_OK) return st;
     if (T > 0 && (!q || !k || !v || !gamma || !beta || !out || !workspace))
         return fail(MESA_ERR_INVALID_ARGUMENT, "q, k, v, gamma, beta, out and workspace must be non-null");
@@ -712,7 +714,7 @@ mesa_status mesa_delta_backward(const void* q, const void* k, const void* v, int
                                 void* grad_k, void* grad_v, float* grad_gamma, float* grad_beta, float* grad_state,
                                 void* workspace, size_t workspace_bytes, void* stream) {
     g_err.clear();
-    const mesa_status st = delta_checks(dtype, B, Hk, H, T, dk, dv);
+    const mesa_status st = delta_checks(dtype, B, Hk, H, T, dk, dv, false);
     if (st != MESA_OK) return st;
     if (T > 0 && (!q || !k || !v || !gamma || !beta || !grad_out || !grad_q || !grad_k || !grad_v || !grad_gamma ||
                   !grad_beta || !workspace))
@@ -772,7 +774,7 @@ mesa_status mesa_delta_step(const void* q, const void* k, const void* v, int dty
                             const float* beta, float* state, int N, int Hk, int H, int dk, int dv, void* out,
                             void* stream) {
     g_err.clear();
-    const mesa_status st = delta_checks(dtype, N, Hk, H, 1, dk, dv);
+    const mesa_status st = delta_checks(dtype, N, Hk, H, 1, dk, dv, true);
     if (st != MESA_OK) return st;
     if (!q || !k || !v || !gamma || !beta || !state || !out)
         return fail(MESA_ERR_INVALID_ARGUMENT, "q, k, v, gamma, beta, state and out must be non-null");
