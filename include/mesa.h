@@ -381,8 +381,9 @@ mesa_status mesa_delta_forward(const void *q, const void *k, const void *v, int 
  *   grad_final [B, H, dv, dk]   float32, or NULL for zeros
  *   grad_q, grad_k [B, Hk, T, dk], grad_v [B, H, T, dv]  dtype, written;
  *                               shared heads' gradients are summed in float32
- *   grad_gamma, grad_beta [B, H, T]  float32, written (grad_gamma is written 0
- *                               where gamma is 0)
+ *   grad_gamma, grad_beta [B, H, T]  float32, written.  Where gamma is 0, a
+ *                               sequence start and not a decay, grad_gamma is
+ *                               written 0 (the derivative there need not be)
  *   grad_state [B, H, dv, dk]   float32 gradient of state0, or NULL; may be
  *                               grad_final itself
  *   workspace                   at least mesa_delta_backward_workspace_bytes(...)

@@ -15,7 +15,9 @@
 //              + sum_{i >= t} G_i (q_i.oS_i - k_i.rS_i)
 //              + sum_{j < t} b_j D_Cj k_j.W_j + G_C <S, dS'>
 // summed over the pairs that cross t, not as a difference of row and column
-// sums, which would cancel.
+// sums, which would cancel.  Below kTinyGate the products that hold g_t leave
+// float's range: there the same sums are taken of products without it, g_t in
+// D_ij, G_i, D_Cj and G_C being left out (a wave-wide sum for each such gate).
 //
 // One workgroup of four waves per chunk and head; wave w owns tokens
 // 16 w .. 16 w + 15 as rows.  First the products over dv, 32 columns of dv at a
@@ -33,6 +35,7 @@
 namespace mesa {
 
 constexpr int kVW = 24;   // words per LDS row of 32 dv columns
+constexpr float kTinyGate = 0x1p-64f;
 
 template <int DKP, int NP>
 struct alignas(16) GradsLds {
@@ -51,9 +54,13 @@ struct alignas(16) GradsLds {
     };
     double L[kDC];
     float beta[kDC], G[kDC], end[kDC];
-    float vs[3][kDC];          // 2^-E of the token rows
-    float read[kDC], write[kDC];
+    union {
+        float vs[3][kDC];      // 2^-E of the token rows
+        float tcross[4][kDC];  // per wave the pairs' sums across the tiny gates
+    };
+    float read[kDC], write[kDC];   // rows' dots, without their decays
     float col[4][kDC], cross[4][kDC + 1];
+    unsigned long long tiny;   // tokens with a gate below kTinyGate
     float red[8][4];           // per-wave maxima and sums
 };
 
@@ -132,6 +139,8 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         L.beta[lane] = lane < valid ? a.beta[tok + lane] : 0.f;
         L.G[lane] = __builtin_amdgcn_exp2f((float)x);
         L.end[lane] = __builtin_amdgcn_exp2f((float)(__shfl(x, 63, 64) - x));
+        const unsigned long long tiny = __ballot(gate > 0.f && gate < kTinyGate);
+        if (lane == 0) L.tiny = tiny;
     }
     // ---- products over dv ----
     f32x4 Y[4], Z[4], oS[NS], rS[NS], W[NS];
@@ -267,6 +276,7 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         __syncthreads();   // maxima written, the dv blocks read
         mk = fmaxf(fmaxf(L.red[2][0], L.red[2][1]), fmaxf(L.red[2][2], L.red[2][3]));
         mq = fmaxf(fmaxf(L.red[3][0], L.red[3][1]), fmaxf(L.red[3][2], L.red[3][3]));
+        L.tcross[w][lane] = 0.f;
         const int EK = h2_exp(mk), EQ = h2_exp(mq);
         ek = pow2(-EK);
         eq = pow2(-EQ);
@@ -284,16 +294,27 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         // blocks before, are summed over the rows below
         float before[4] = {};
         if (lane == 0) L.cross[w][0] = 0.f;
+        const unsigned long long tiny = L.tiny;
         f16x8 kh[NJ], kl[NJ], qh[NJ], ql[NJ];
+        auto rows = [&] {
 #pragma unroll
-        for (int s = 0; s < NJ; ++s) {
-            kh[s] = row_operand(L.K[0], KW, w, s, n, g);
-            kl[s] = row_operand(L.K[NP - 1], KW, w, s, n, g);
-            qh[s] = row_operand(L.Q[0], KW, w, s, n, g);
-            ql[s] = row_operand(L.Q[NP - 1], KW, w, s, n, g);
-        }
+            for (int s = 0; s < NJ; ++s) {
+                kh[s] = row_operand(L.K[0], KW, w, s, n, g);
+                kl[s] = row_operand(L.K[NP - 1], KW, w, s, n, g);
+                qh[s] = row_operand(L.Q[0], KW, w, s, n, g);
+                ql[s] = row_operand(L.Q[NP - 1], KW, w, s, n, g);
+            }
+        };
+        // read again for each block where they would be kept in accumulator
+        // registers, from which they would come too late for the MFMAs in asm
+        constexpr bool KEEP = !(F && DKP == 128);
+        if constexpr (KEEP) rows();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            if constexpr (!KEEP) {
+                rows();
+                __builtin_amdgcn_sched_barrier(0);
+            }
             f32x4 AP[2];   // the blocks of A and P
 #pragma unroll
             for (int s = 0; s < NJ; ++s) {
@@ -311,6 +332,22 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
             const int cj = 16 * j + n;
             const double Lj = L.L[cj];
             const float bj = L.beta[cj];
+            for (unsigned long long left = tiny; left; left &= left - 1) {
+                const int t = __builtin_ctzll(left);
+                float s = 0.f;
+                if (t > cj) {
+                    const float before = __builtin_amdgcn_exp2f((float)(L.L[t - 1] - Lj)) * bj;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = 16 * w + 4 * g + r;
+                        if (row >= t)
+                            s += __builtin_amdgcn_exp2f((float)(L.L[row] - L.L[t])) * before *
+                                 (P[r] * (ek * eq) * Y[j][r] - A[r] * (ek * ek) * Z[j][r]);
+                    }
+                }
+                s = wavesum(s);
+                if (lane == 0) L.tcross[w][t] += s;
+            }
             float sum = 0.f, cross = 0.f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -356,13 +393,12 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
                 kr[r] += k * rS[m][r];
                 kw[r] += k * W[m][r];
             }
-        const f32x4 G = row4(L.G, w, g), end = row4(L.end, w, g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const float q1 = rowsum16(qo[r]) * eq, k1 = rowsum16(kr[r]) * ek, k2 = rowsum16(kw[r]) * ek;
             if (n == 0) {
-                L.read[16 * w + 4 * g + r] = G[r] * (q1 - k1);
-                L.write[16 * w + 4 * g + r] = end[r] * k2;
+                L.read[16 * w + 4 * g + r] = q1 - k1;
+                L.write[16 * w + 4 * g + r] = k2;
             }
         }
     }
@@ -370,8 +406,8 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
     if (lane == 0) { L.red[5][w] = my; L.red[6][w] = mz; }
     __syncthreads();
     if (w == 0) {
-        const float wr = L.write[lane];
-        float rd = L.read[lane], before = L.beta[lane] * wr;
+        const float wr = L.end[lane] * L.write[lane];
+        float rd = L.G[lane] * L.read[lane], before = L.beta[lane] * wr;
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
             const float t = __shfl_down(rd, o, 64), u = __shfl_up(before, o, 64);
@@ -380,12 +416,23 @@ __global__ __launch_bounds__(256, DKP == 128 && sizeof(In) == 4 ? 1 : 2) void de
         }
         before = __shfl_up(before, 1, 64);
         if (lane == 0) before = 0.f;
-        const float state = L.G[kDC - 1] * ((L.red[4][0] + L.red[4][1]) + (L.red[4][2] + L.red[4][3]));
+        const float carried = (L.red[4][0] + L.red[4][1]) + (L.red[4][2] + L.red[4][3]);
+        const float state = L.G[kDC - 1] * carried;
         const float cross = (L.cross[0][lane] + L.cross[1][lane]) + (L.cross[2][lane] + L.cross[3][lane]);
         const float cols = (L.col[0][lane] + L.col[1][lane]) + (L.col[2][lane] + L.col[3][lane]);
+        float dg = gate == 0.f ? 0.f : (cross + rd + before + state) / gate;
+        for (unsigned long long left = L.tiny; left; left &= left - 1) {
+            const int t = __builtin_ctzll(left);
+            const double Lb = t ? L.L[t - 1] : 0.0, Lt = L.L[t], Li = L.L[lane];
+            const float G = __builtin_amdgcn_exp2f((float)Lb), D = __builtin_amdgcn_exp2f((float)(L.L[kDC - 1] - Lt));
+            float s = lane >= t ? __builtin_amdgcn_exp2f((float)(Li - Lt)) * G * L.read[lane]
+                                : __builtin_amdgcn_exp2f((float)(Lb - Li)) * D * L.beta[lane] * L.write[lane];
+            s = wavesum(s) + G * D * carried + ((L.tcross[0][t] + L.tcross[1][t]) + (L.tcross[2][t] + L.tcross[3][t]));
+            if (lane == t) dg = s;
+        }
         if (lane < valid) {
             b.grad_beta[tok + lane] = wr + cols;
-            b.grad_gamma[tok + lane] = gate == 0.f ? 0.f : (cross + rd + before + state) / gate;
+            b.grad_gamma[tok + lane] = dg;
         }
     }
     float ey, ez;

@@ -522,6 +522,8 @@ def mesa_delta_backward(q, k, v, gamma, beta, grad_out, state=None, *, grad_fina
     grad_out: [B,H,T,dv] in q's dtype; grad_final: [B,H,dv,dk] float32 or
     None.  Returns a dict of grad_q, grad_k [B,Hk,T,dk], grad_v (q's dtype),
     grad_gamma, grad_beta and grad_state (float32; None without a state).
+    grad_gamma is 0 where gamma is: a gate of 0 marks a sequence's start in a
+    packed row and is not differentiated.
     """
     import torch
     B, Hk, H, (T,), dk, dv = _delta_sizes(q, v, 4)
