@@ -20,20 +20,18 @@
 
 namespace mesa {
 
-template <int DKP, int NP>
 struct alignas(16) BwdScanLds {
-    static constexpr int KW = delta_row_words(DKP);
-    uint32_t K[NP][kDC * KW];
-    uint32_t Q[NP][kDC * KW];
+    static constexpr int KW = delta_row_words(128);
+    uint32_t K[2][kDC * KW];
+    uint32_t Q[2][kDC * KW];
     uint32_t M[2][kDC * kDP];
     uint32_t P[2][kDC * kDP];
     float sc[kScal];
 };
 
-template <int DKP, typename In>
 __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int waves) {
-    constexpr int NP = delta_planes<In>(), NJ = DKP / 32, NS = DKP / 16, KW = delta_row_words(DKP);
-    __shared__ BwdScanLds<DKP, NP> L;
+    constexpr int DK = 128, NJ = DK / 32, NS = DK / 16, KW = BwdScanLds::KW;
+    __shared__ BwdScanLds L;
     const DeltaArgs& a = b.f;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), n = lane & 15, g = lane >> 4;
     const int cgs = (a.dv + 16 * waves - 1) / (16 * waves);
@@ -42,34 +40,34 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
     const int col0 = 16 * (waves * (int)(blockIdx.x / 8 % cgs) + w);   // the wave's first column
     const bool live = w < waves && col0 < a.dv;
     const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
-    const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
-    const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
-    const In* Op = static_cast<const In*>(b.grad_out) + (size_t)bh * a.T * a.dv + col0;
-    In* Vp = static_cast<In*>(b.grad_v) + (size_t)bh * a.T * a.dv + col0;
+    const float* Kp = static_cast<const float*>(a.k) + (size_t)bk * a.T * DK;
+    const float* Qp = static_cast<const float*>(a.q) + (size_t)bk * a.T * DK;
+    const float* Op = static_cast<const float*>(b.grad_out) + (size_t)bh * a.T * a.dv + col0;
+    float* Vp = static_cast<float*>(b.grad_v) + (size_t)bh * a.T * a.dv + col0;
     constexpr size_t image = delta_image_words(false);
     const uint16_t* img = a.img + (size_t)bh * a.nc * image;
     const float* scal = a.scal + (size_t)bh * a.nc * kScal;
-    const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;
-    const uint32_t lv = (4 * g * a.dv + n) * sizeof(In);   // this lane's bytes in a 16-row tile of v
+    const size_t so = ((size_t)bh * a.dv + col0 + n) * DK + 4 * g;
+    const uint32_t lv = (4 * g * a.dv + n) * 4;   // this lane's bytes in a 16-row tile of v
     const f32x4 zero{0.f, 0.f, 0.f, 0.f};
 
     f32x4 S[NS];   // the gradient of the state times 2^cs
     int cs = 0;
 #pragma unroll
     for (int m = 0; m < NS; ++m)
-        S[m] = b.grad_final && live && 16 * m < a.dk ? load4(b.grad_final + so + 16 * m) : zero;
+        S[m] = b.grad_final && live ? load4(b.grad_final + so + 16 * m) : zero;
 
-    using Units = RowUnits<DKP, In>;
+    using Units = RowUnits<DK, float>;
     Units kr, qr;
     PlaneUnits<4> pr;
-    In vr[16];
+    float vr[16];
     float ksr[Units::n], qsr[Units::n];
     f32x4 scr = zero;
     auto fetch = [&](int chunk) {
         const int c = opaque(chunk);
         const int valid = min(kDC, a.T - c * kDC);
-        kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
-        qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
+        kr.load(Kp + (size_t)c * kDC * DK, DK, valid);
+        qr.load(Qp + (size_t)c * kDC * DK, DK, valid);
         const float* sc = scal + (size_t)c * kScal;
 #pragma unroll
         for (int i = 0; i < Units::n; ++i) {
@@ -78,10 +76,10 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
         }
         pr.load(img + c * image);
         if (threadIdx.x < kScal / 4) scr = load4(lane_at(sc, 16 * threadIdx.x));
-        const In* op = Op + (size_t)c * kDC * a.dv;
+        const float* op = Op + (size_t)c * kDC * a.dv;
         if (!live) return;
-        each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {   // zeros behind the end
-            vr[i] = valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid ? *lane_at(op, o) : In{};
+        each_value(lv, fresh(a.dv * 4, c), [&](uint32_t o, int i) {   // zeros behind the end
+            vr[i] = valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid ? *lane_at(op, o) : 0.f;
         });
     };
     fetch(a.nc - 1);
@@ -91,23 +89,22 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
         f32x4 dO[4];
 #pragma unroll
         for (int i = 0; i < Units::n; ++i) {
-            kr.template store<NP>(L.K, i, ksr[i]);
-            qr.template store<NP>(L.Q, i, qsr[i]);
+            kr.template store<2>(L.K, i, ksr[i]);
+            qr.template store<2>(L.Q, i, qsr[i]);
         }
         pr.store(L.M[0]);   // P's planes follow M's
         if (threadIdx.x < kScal / 4) *reinterpret_cast<f32x4*>(L.sc + 4 * threadIdx.x) = scr;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dO[i / 4][i % 4] = to_f32(vr[i]);
+        for (int i = 0; i < 16; ++i) dO[i / 4][i % 4] = vr[i];
         __syncthreads();
         if (chunk > 0) fetch(chunk - 1);
         if (!live) continue;
 
         {
             const float s = pow2(-cs);
-            float* sp = b.dS + ((size_t)bh * a.nc + c) * a.dv * a.dk + (size_t)(col0 + n) * a.dk + 4 * g;
+            float* sp = b.dS + ((size_t)bh * a.nc + c) * a.dv * DK + (size_t)(col0 + n) * DK + 4 * g;
 #pragma unroll
-            for (int m = 0; m < NS; ++m)
-                if (16 * m < a.dk) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
+            for (int m = 0; m < NS; ++m) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
         }
         // ---- dE = D_C b K dS' + (P diag(b))^T dO ----
         f16x8 Sh[NJ], Sl[NJ];
@@ -129,16 +126,15 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
             for (int i = 0; i < 4; ++i) kh[i] = row_operand(L.K[0], KW, i, j, n, g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) j ? mfma_acc(X[i], kh[i], Sl[j]) : mfma_first(X[i], kh[i], Sl[j]);
-            if constexpr (NP == 2)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mfma_acc(X[i], row_operand(L.K[1], KW, i, j, n, g), Sh[j]);
+            for (int i = 0; i < 4; ++i) mfma_acc(X[i], row_operand(L.K[1], KW, i, j, n, g), Sh[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) mfma_acc(X[i], kh[i], Sh[j]);
         }
         mfma_done(X);
         f16x8 Bh[2], Bl[2];
         const int eb = column_exp(B);
-        column_split(B, eb, Bh, Bl);   // bf16 gradients are exact in the hi part
+        column_split(B, eb, Bh, Bl);
         const float ip = L.sc[kPi] * pow2(-eb);
         f32x4 t[4];
 #pragma unroll
@@ -149,11 +145,10 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
                 ph[i] = col_operand(L.P[0], kDP, i, j, n, g);
                 pl[i] = col_operand(L.P[1], kDP, i, j, n, g);
             }
-            if constexpr (NP == 2)
 #pragma unroll
-                for (int i = 0; i < 2 * j + 2; ++i) i / 2 < j ? mfma_acc(t[i], ph[i], Bl[j]) : mfma_first(t[i], ph[i], Bl[j]);
+            for (int i = 0; i < 2 * j + 2; ++i) i / 2 < j ? mfma_acc(t[i], ph[i], Bl[j]) : mfma_first(t[i], ph[i], Bl[j]);
 #pragma unroll
-            for (int i = 0; i < 2 * j + 2; ++i) NP == 2 || i / 2 < j ? mfma_acc(t[i], pl[i], Bh[j]) : mfma_first(t[i], pl[i], Bh[j]);
+            for (int i = 0; i < 2 * j + 2; ++i) mfma_acc(t[i], pl[i], Bh[j]);
 #pragma unroll
             for (int i = 0; i < 2 * j + 2; ++i) mfma_acc(t[i], ph[i], Bh[j]);
         }
@@ -197,10 +192,10 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
         }
         {
             float* rp = b.dR + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
-            In* vp = Vp + (size_t)c * kDC * a.dv;
-            each_value(lv * (4 / sizeof(In)), fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(rp, o) = t[i / 4][i % 4]; });
-            each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {
-                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) store1(lane_at(vp, o), t[i / 4][i % 4]);
+            float* vp = Vp + (size_t)c * kDC * a.dv;
+            each_value(lv, fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(rp, o) = t[i / 4][i % 4]; });
+            each_value(lv, fresh(a.dv * 4, c), [&](uint32_t o, int i) {
+                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) *lane_at(vp, o) = t[i / 4][i % 4];
             });
         }
         // ---- dS = G_C dS' + Q^T (G dO) - K^T (G dV), dS kept scaled as the forward's S ----
@@ -218,16 +213,15 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
 #pragma unroll
             for (int t2 = 0; t2 < 2; ++t2) {   // K with the values' gradients, Q with the outputs'
                 const uint32_t* hi = t2 ? L.Q[0] : L.K[0];
-                const uint32_t* lo = t2 ? L.Q[NP - 1] : L.K[NP - 1];
+                const uint32_t* lo = t2 ? L.Q[1] : L.K[1];
                 const f16x8 h = t2 ? Bh[j] : Xh[j], l = t2 ? Bl[j] : Xl[j];
                 f16x8 rows[NS];
 #pragma unroll
                 for (int m = 0; m < NS; ++m) rows[m] = col_operand(hi, KW, m, j, n, g);
 #pragma unroll
                 for (int m = 0; m < NS; ++m) mfma_acc(S[m], rows[m], l);
-                if constexpr (NP == 2)
 #pragma unroll
-                    for (int m = 0; m < NS; ++m) mfma_acc(S[m], col_operand(lo, KW, m, j, n, g), h);
+                for (int m = 0; m < NS; ++m) mfma_acc(S[m], col_operand(lo, KW, m, j, n, g), h);
 #pragma unroll
                 for (int m = 0; m < NS; ++m) mfma_acc(S[m], rows[m], h);
             }
@@ -237,8 +231,7 @@ __global__ __launch_bounds__(256) void delta_bwd_scan_kernel(DeltaBwdArgs b, int
     if (b.grad_state && live) {
         const float s = pow2(-cs);
 #pragma unroll
-        for (int m = 0; m < NS; ++m)
-            if (16 * m < a.dk) *reinterpret_cast<f32x4*>(b.grad_state + so + 16 * m) = S[m] * s;
+        for (int m = 0; m < NS; ++m) *reinterpret_cast<f32x4*>(b.grad_state + so + 16 * m) = S[m] * s;
     }
 }
 
@@ -249,7 +242,7 @@ hipError_t launch_delta_passes(const DeltaBwdArgs& b, hipStream_t s) {
     const hipError_t e = launch_delta_states(b.f, s);
     if (e != hipSuccess) return e;
     const int waves = scan_waves(b.f.BH, b.f.dv);
-    hipLaunchKernelGGL((delta_bwd_scan_kernel<128, float>), dim3(scan_blocks(b.f.BH, b.f.dv, waves)), dim3(256), 0, s, b, waves);
+    hipLaunchKernelGGL(delta_bwd_scan_kernel, dim3(scan_blocks(b.f.BH, b.f.dv, waves)), dim3(256), 0, s, b, waves);
     return hipGetLastError();
 }
 

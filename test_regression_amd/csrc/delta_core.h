@@ -49,10 +49,9 @@ enum DeltaScal {
     kGq = 192,    // G_t 2^-EQ_t
     kQi = 256,    // 2^-EQ_t; row t of P diag(b) is scaled by 2^(EQ_t + EP)
     kDb = 320,    // D_Ct b_t 2^-EK_t
-    kBe = 384,    // b_t
-    kGc = 448,    // G_C
-    kMi = 449,    // 2^-EM, the scale of M undone
-    kPi = 450,    // 2^-EP
+    kGc = 384,    // G_C
+    kMi = 385,    // 2^-EM, the scale of M undone
+    kPi = 386,    // 2^-EP
     kScal = kDeltaScal
 };
 

@@ -262,7 +262,6 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
         sc[kGq + t] = G * qi;
         sc[kQi + t] = qi;
         sc[kDb + t] = __builtin_amdgcn_exp2f((float)(L.L[kDC - 1] - Lt)) * be * ki;
-        sc[kBe + t] = be;
         if (t == kDC - 1) {
             sc[kGc] = G;
             sc[kMi] = pow2(-EM);

@@ -19,29 +19,26 @@
 // planes delta_scan_split.h's kernel has no LDS for: a forward of 8x16x4096, dv =
 // 128, takes 690 us of which this is 80 %, one of 2x16x4096 493 us.
 //
-// Precision: S, R and b E enter the products that feed the state as hi + lo
-// (22 bits).  For bf16 outputs the two products that only feed O take the hi
-// parts alone (11 bits: 2^-12 a term against the output's own 2^-8).
+// Precision: every operand is hi + lo (22 bits).
 #include "delta_core.h"
 
 namespace mesa {
 
-template <int DKP, int NP>
 struct alignas(16) ScanLds {
-    static constexpr int KW = delta_row_words(DKP);
-    uint32_t K[NP][kDC * KW];
-    uint32_t Q[NP][kDC * KW];
+    static constexpr int KW = delta_row_words(128);
+    uint32_t K[2][kDC * KW];
+    uint32_t Q[2][kDC * KW];
     uint32_t M[2][kDC * kDP];
-    uint32_t P[NP][kDC * kDP];
+    uint32_t P[2][kDC * kDP];
     float sc[kScal];
 };
 
-// OUT: write O.  SAVE: write each chunk's start state and E (the backward's
-// recomputation).
-template <int DKP, typename In, bool OUT, bool SAVE>
+// OUT: write O.  Else the backward's recomputation: write each chunk's start
+// state and E.
+template <bool OUT>
 __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves) {
-    constexpr int NP = delta_planes<In>(), NJ = DKP / 32, NS = DKP / 16, KW = delta_row_words(DKP);
-    __shared__ ScanLds<DKP, NP> L;
+    constexpr int DK = 128, NJ = DK / 32, NS = DK / 16, KW = ScanLds::KW;
+    __shared__ ScanLds L;
     const int lane = threadIdx.x % 64, w = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), n = lane & 15, g = lane >> 4;
     // the column groups of a head on one XCD (workgroups go to the 8 XCDs in turn)
     const int cgs = (a.dv + 16 * waves - 1) / (16 * waves);
@@ -50,35 +47,35 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
     const int col0 = 16 * (waves * (int)(blockIdx.x / 8 % cgs) + w);   // the wave's first column
     const bool live = w < waves && col0 < a.dv;
     const int bk = (bh / a.H) * a.Hk + (bh % a.H) / (a.H / a.Hk);
-    const In* Kp = static_cast<const In*>(a.k) + (size_t)bk * a.T * a.dk;
-    const In* Qp = static_cast<const In*>(a.q) + (size_t)bk * a.T * a.dk;
-    const In* Vp = static_cast<const In*>(a.v) + (size_t)bh * a.T * a.dv + col0;
-    In* Op = OUT ? static_cast<In*>(a.out) + (size_t)bh * a.T * a.dv + col0 : nullptr;
+    const float* Kp = static_cast<const float*>(a.k) + (size_t)bk * a.T * DK;
+    const float* Qp = static_cast<const float*>(a.q) + (size_t)bk * a.T * DK;
+    const float* Vp = static_cast<const float*>(a.v) + (size_t)bh * a.T * a.dv + col0;
+    float* Op = OUT ? static_cast<float*>(a.out) + (size_t)bh * a.T * a.dv + col0 : nullptr;
     constexpr size_t image = delta_image_words(false);
     const uint16_t* img = a.img + (size_t)bh * a.nc * image;
     const float* scal = a.scal + (size_t)bh * a.nc * kScal;
-    const size_t so = ((size_t)bh * a.dv + col0 + n) * a.dk + 4 * g;   // this lane's row of the (dv x dk) state
-    const uint32_t lv = (4 * g * a.dv + n) * sizeof(In);               // this lane's bytes in a 16-row tile of v
+    const size_t so = ((size_t)bh * a.dv + col0 + n) * DK + 4 * g;   // this lane's row of the (dv x dk) state
+    const uint32_t lv = (4 * g * a.dv + n) * 4;               // this lane's bytes in a 16-row tile of v
     const f32x4 zero{0.f, 0.f, 0.f, 0.f};
 
     f32x4 S[NS];   // the state times 2^cs
     int cs = 0;
 #pragma unroll
     for (int m = 0; m < NS; ++m)
-        S[m] = a.state0 && live && 16 * m < a.dk ? load4(a.state0 + so + 16 * m) : zero;
+        S[m] = a.state0 && live ? load4(a.state0 + so + 16 * m) : zero;
 
-    using Units = RowUnits<DKP, In>;
-    using Planes = PlaneUnits<OUT ? 2 + NP : 2>;
+    using Units = RowUnits<DK, float>;
+    using Planes = PlaneUnits<OUT ? 4 : 2>;
     Units kr, qr;
     Planes pr;
-    In vr[16];
+    float vr[16];
     float ksr[Units::n], qsr[Units::n];
     f32x4 scr = zero;
     auto fetch = [&](int chunk) {
         const int c = opaque(chunk);
         const int valid = min(kDC, a.T - c * kDC);
-        kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
-        if constexpr (OUT) qr.load(Qp + (size_t)c * kDC * a.dk, a.dk, valid);
+        kr.load(Kp + (size_t)c * kDC * DK, DK, valid);
+        if constexpr (OUT) qr.load(Qp + (size_t)c * kDC * DK, DK, valid);
         const float* sc = scal + (size_t)c * kScal;
 #pragma unroll
         for (int i = 0; i < Units::n; ++i) {
@@ -88,9 +85,9 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
         pr.load(img + c * image);
         if (threadIdx.x < kScal / 4) scr = load4(lane_at(sc, 16 * threadIdx.x));
         if (!live) return;
-        const In* vp = Vp + (size_t)c * kDC * a.dv;
-        each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {   // zeros behind the end
-            vr[i] = valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid ? *lane_at(vp, o) : In{};
+        const float* vp = Vp + (size_t)c * kDC * a.dv;
+        each_value(lv, fresh(a.dv * 4, c), [&](uint32_t o, int i) {   // zeros behind the end
+            vr[i] = valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid ? *lane_at(vp, o) : 0.f;
         });
     };
     fetch(0);
@@ -100,23 +97,22 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
         f32x4 V[4];
 #pragma unroll
         for (int i = 0; i < Units::n; ++i) {
-            kr.template store<NP>(L.K, i, ksr[i]);
-            if constexpr (OUT) qr.template store<NP>(L.Q, i, qsr[i]);
+            kr.template store<2>(L.K, i, ksr[i]);
+            if constexpr (OUT) qr.template store<2>(L.Q, i, qsr[i]);
         }
         pr.store(L.M[0]);   // P's planes follow M's
         if (threadIdx.x < kScal / 4) *reinterpret_cast<f32x4*>(L.sc + 4 * threadIdx.x) = scr;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) V[i / 4][i % 4] = to_f32(vr[i]);
+        for (int i = 0; i < 16; ++i) V[i / 4][i % 4] = vr[i];
         __syncthreads();
         if (chunk + 1 < a.nc) fetch(chunk + 1);
         if (!live) continue;
 
-        if constexpr (SAVE) {
+        if constexpr (!OUT) {
             const float s = pow2(-cs);
-            float* sp = a.S + ((size_t)bh * a.nc + c) * a.dv * a.dk + (size_t)(col0 + n) * a.dk + 4 * g;
+            float* sp = a.S + ((size_t)bh * a.nc + c) * a.dv * DK + (size_t)(col0 + n) * DK + 4 * g;
 #pragma unroll
-            for (int m = 0; m < NS; ++m)
-                if (16 * m < a.dk) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
+            for (int m = 0; m < NS; ++m) *reinterpret_cast<f32x4*>(sp + 16 * m) = S[m] * s;
         }
         // ---- K S and Q S ----
         f16x8 Sh[NJ], Sl[NJ];
@@ -132,9 +128,8 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
             for (int i = 0; i < 4; ++i) kh[i] = row_operand(L.K[0], KW, i, j, n, g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) j ? mfma_acc(X[i], kh[i], Sl[j]) : mfma_first(X[i], kh[i], Sl[j]);
-            if constexpr (NP == 2)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mfma_acc(X[i], row_operand(L.K[1], KW, i, j, n, g), Sh[j]);
+            for (int i = 0; i < 4; ++i) mfma_acc(X[i], row_operand(L.K[1], KW, i, j, n, g), Sh[j]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) mfma_acc(X[i], kh[i], Sh[j]);
         }
@@ -145,14 +140,12 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
                 f16x8 qh[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) qh[i] = row_operand(L.Q[0], KW, i, j, n, g);
-                if constexpr (NP == 2) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) j ? mfma_acc(Y[i], qh[i], Sl[j]) : mfma_first(Y[i], qh[i], Sl[j]);
+                for (int i = 0; i < 4; ++i) j ? mfma_acc(Y[i], qh[i], Sl[j]) : mfma_first(Y[i], qh[i], Sl[j]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mfma_acc(Y[i], row_operand(L.Q[1], KW, i, j, n, g), Sh[j]);
-                }
+                for (int i = 0; i < 4; ++i) mfma_acc(Y[i], row_operand(L.Q[1], KW, i, j, n, g), Sh[j]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) NP == 2 || j ? mfma_acc(Y[i], qh[i], Sh[j]) : mfma_first(Y[i], qh[i], Sh[j]);
+                for (int i = 0; i < 4; ++i) mfma_acc(Y[i], qh[i], Sh[j]);
             }
             mfma_done(Y);
         }
@@ -186,15 +179,14 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
         const float ir = L.sc[kMi] * pow2(-er);
 #pragma unroll
         for (int i = 0; i < 4; ++i) U[i] *= ir;
-        if constexpr (SAVE) {
+        if constexpr (!OUT) {
             float* ep = a.E + ((size_t)bh * a.nc + c) * kDC * a.dv + col0;
-            each_value(lv * (4 / sizeof(In)), fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(ep, o) = U[i / 4][i % 4]; });
+            each_value(lv, fresh(a.dv * 4, c), [&](uint32_t o, int i) { *lane_at(ep, o) = U[i / 4][i % 4]; });
         }
         // ---- O = G Q S + P diag(b) E ----
         if constexpr (OUT) {
             const int eu = column_exp(U);
-            if constexpr (NP == 2) column_split(U, eu, Bh, Bl);
-            else column_hi(U, eu, Bh);
+            column_split(U, eu, Bh, Bl);
             const float iu = L.sc[kPi] * pow2(-eu);
             f32x4 Z[4];
 #pragma unroll
@@ -202,14 +194,12 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
                 f16x8 ph[4];
 #pragma unroll
                 for (int i = 2 * j; i < 4; ++i) ph[i] = row_operand(L.P[0], kDP, i, j, n, g);
-                if constexpr (NP == 2) {
 #pragma unroll
-                    for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(Z[i], ph[i], Bl[j]) : mfma_first(Z[i], ph[i], Bl[j]);
+                for (int i = 2 * j; i < 4; ++i) j ? mfma_acc(Z[i], ph[i], Bl[j]) : mfma_first(Z[i], ph[i], Bl[j]);
 #pragma unroll
-                    for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], row_operand(L.P[1], kDP, i, j, n, g), Bh[j]);
-                }
+                for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], row_operand(L.P[1], kDP, i, j, n, g), Bh[j]);
 #pragma unroll
-                for (int i = 2 * j; i < 4; ++i) NP == 2 || j ? mfma_acc(Z[i], ph[i], Bh[j]) : mfma_first(Z[i], ph[i], Bh[j]);
+                for (int i = 2 * j; i < 4; ++i) mfma_acc(Z[i], ph[i], Bh[j]);
             }
             mfma_done(Z);
 #pragma unroll
@@ -219,9 +209,9 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
                 for (int r = 0; r < 4; ++r) Y[i][r] = (gq[r] * is) * Y[i][r] + (qi[r] * iu) * Z[i][r];
             }
             const int valid = min(kDC, a.T - c * kDC);
-            In* op = Op + (size_t)c * kDC * a.dv;
-            each_value(lv, fresh(a.dv * sizeof(In), c), [&](uint32_t o, int i) {
-                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) store1(lane_at(op, o), Y[i / 4][i % 4]);
+            float* op = Op + (size_t)c * kDC * a.dv;
+            each_value(lv, fresh(a.dv * 4, c), [&](uint32_t o, int i) {
+                if (valid == kDC || 16 * (i / 4) + 4 * g + i % 4 < valid) *lane_at(op, o) = Y[i / 4][i % 4];
             });
         }
         // ---- S' = G_C S + K^T (D_C b E) ----
@@ -241,9 +231,8 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
             for (int m = 0; m < NS; ++m) kh[m] = col_operand(L.K[0], KW, m, j, n, g);
 #pragma unroll
             for (int m = 0; m < NS; ++m) mfma_acc(S[m], kh[m], Bl[j]);
-            if constexpr (NP == 2)
 #pragma unroll
-                for (int m = 0; m < NS; ++m) mfma_acc(S[m], col_operand(L.K[1], KW, m, j, n, g), Bh[j]);
+            for (int m = 0; m < NS; ++m) mfma_acc(S[m], col_operand(L.K[1], KW, m, j, n, g), Bh[j]);
 #pragma unroll
             for (int m = 0; m < NS; ++m) mfma_acc(S[m], kh[m], Bh[j]);
         }
@@ -252,26 +241,24 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, int waves)
     if (a.final_state && live) {
         const float s = pow2(-cs);
 #pragma unroll
-        for (int m = 0; m < NS; ++m)
-            if (16 * m < a.dk) *reinterpret_cast<f32x4*>(a.final_state + so + 16 * m) = S[m] * s;
+        for (int m = 0; m < NS; ++m) *reinterpret_cast<f32x4*>(a.final_state + so + 16 * m) = S[m] * s;
     }
 }
 
-template <bool OUT, bool SAVE>
+template <bool OUT>
 hipError_t scan_go(const DeltaArgs& a, hipStream_t s) {
     const int waves = scan_waves(a.BH, a.dv);
-    hipLaunchKernelGGL((delta_scan_kernel<128, float, OUT, SAVE>), dim3(scan_blocks(a.BH, a.dv, waves)), dim3(256), 0, s, a,
-                       waves);
+    hipLaunchKernelGGL((delta_scan_kernel<OUT>), dim3(scan_blocks(a.BH, a.dv, waves)), dim3(256), 0, s, a, waves);
     return hipGetLastError();
 }
 
 // Float rows of 128 features need two planes of K twice in the split kernel's
 // LDS, which does not hold them; everything else takes that kernel.
 hipError_t launch_delta_scan(const DeltaArgs& a, hipStream_t s) {
-    if (!a.bf16 && a.dk == 128) return scan_go<true, false>(a, s);
+    if (!a.bf16 && a.dk == 128) return scan_go<true>(a, s);
     const hipError_t e = launch_delta_segments(a, s);
     return e != hipSuccess ? e : launch_delta_scan_split(a, s);
 }
-hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s) { return scan_go<false, true>(a, s); }
+hipError_t launch_delta_states(const DeltaArgs& a, hipStream_t s) { return scan_go<false>(a, s); }
 
 }  // namespace mesa

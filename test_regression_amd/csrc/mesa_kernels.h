@@ -95,7 +95,7 @@ hipError_t launch_hawk(const HawkArgs& a, hipStream_t s);
 
 // Gated delta rule (delta_*.hip).
 constexpr int kDeltaChunk = 64;   // tokens per chunk
-constexpr int kDeltaScal = 512;   // floats of per-chunk scalars in the workspace
+constexpr int kDeltaScal = 400;   // floats of per-chunk scalars in the workspace
 constexpr int kDeltaPlaneUnits = 384;   // 16-byte units of a plane of M or P in the workspace
 // A chunk's planes in the workspace, in 2-byte words: two of M, then P's first
 // part and its second, which is a plane too or (p_bytes) a byte an element.
