@@ -9,8 +9,8 @@
 // from the fp16 parts of S and E that the state waves leave in LDS (in the
 // backward's recomputation they write E out).  Waves 8..11 stage the chunks.
 // Two barriers a chunk; between them:
-//   first half    split S, X, R    Q S of chunk c - 1    M of c in
-//   second half   E, update        P E, O out            Q, P of c; K, V of c + 1 in
+//   first half    split S, X, R    Q S of chunk c - 1    M of c, K of c + 1 in
+//   second half   E, update        P E, O out            Q, P of c, V of c + 1 in
 // so K is held twice in LDS and everything else once.  What the output waves
 // need of P and E is in their registers by the second half; O is turned around
 // in LDS of its own, for which float rows leave no room (these finish O in the
@@ -18,8 +18,8 @@
 //
 // S and E enter the outputs as hi + lo too, bf16 outputs among them.  With their
 // hi parts and P's alone (11 bits), a bf16 output in which the terms cancel is
-// off by up to 2^-11 of the terms; that took 314-326 us a layer of 8x16x4096 and
-// 303 us for 1x16x16384, against 336-348 and 309.
+// off by up to 2^-11 of the terms; the second parts make the pass 234 us and not
+// 215 for 8x16x4096 (dk = dv = 128), 28 and not 26 for 4x8x4096 (dk = dv = 64).
 //
 // With few heads the sequence is cut into segments that are passed over at once
 // (delta_segments.hip): first each segment but the last from a zero state (ENDS:
@@ -43,7 +43,7 @@ template <int DKP, typename In, bool OUT>
 struct alignas(16) ScanSplitLds {
     static constexpr int NP = delta_planes<In>(), KW = delta_row_words(DKP), NJ = DKP / 32;
     static constexpr int VW = sizeof(In) == 2 ? 8 : 20;   // words of a row of 16 values
-    static constexpr int parts = 2 * (NJ + 2);            // operands of S and of E that the outputs take
+    static constexpr int parts = OUT ? 2 * (NJ + 2) : 1;  // operands of S and of E that the outputs take
     uint32_t K[2][NP][kDC * KW];
     uint32_t M[2 * kCPlane];
     uint32_t V[4][kDC * VW];
@@ -392,15 +392,18 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
         ValueUnits<In> vr;
         float ksr[Units::n], qsr[Units::n];
         f32x4 scr{0.f, 0.f, 0.f, 0.f};
-        // K, V and scalars; M; Q and P of a chunk
+        // K; V and scalars; M; Q and P of a chunk
         auto fetch_k = [&](int chunk) {
             const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
             kr.load(Kp + (size_t)c * kDC * a.dk, a.dk, valid);
-            vr.load(Vp + (size_t)c * kDC * a.dv, a.dv, cols, a.dv - colg, valid, tid);
             const float* sc = scal + (size_t)c * kScal;
 #pragma unroll
             for (int i = 0; i < Units::n; ++i) ksr[i] = *lane_at(sc + kKs, 4 * Units::row(i));
-            if (tid < kScal / 4) scr = load4(lane_at(sc, 16 * tid));
+        };
+        auto fetch_v = [&](int chunk) {
+            const int c = opaque(chunk), valid = min(kDC, a.T - c * kDC);
+            vr.load(Vp + (size_t)c * kDC * a.dv, a.dv, cols, a.dv - colg, valid, tid);
+            if (tid < kScal / 4) scr = load4(lane_at(scal + (size_t)c * kScal, 16 * tid));
         };
         auto fetch_m = [&](int chunk) { mr.load(img + opaque(chunk) * image); };
         auto fetch_q = [&](int chunk) {
@@ -417,22 +420,33 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
         auto put_k = [&](int c) {
 #pragma unroll
             for (int i = 0; i < Units::n; ++i) kr.template store<NP>(L.K[c & 1], i, ksr[i]);
+        };
+        auto put_v = [&](int c) {
             vr.template store<Lds::VW>(L.V, cols, tid);
             if (tid < kScal / 4) *reinterpret_cast<f32x4*>(L.sc[c & 1] + 4 * tid) = scr;
         };
         // every fetch is a whole chunk ahead of its store
         fetch_k(c0);
+        fetch_v(c0);
         fetch_m(c0);
         if constexpr (OUT) fetch_q(c0);
         put_k(c0);
-        if (c0 + 1 < c1) fetch_k(c0 + 1);
+        put_v(c0);
+        if (c0 + 1 < c1) {
+            fetch_k(c0 + 1);
+            fetch_v(c0 + 1);
+        }
         for (int chunk = c0; chunk < c1; ++chunk) {
             const int c = opaque(chunk);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < MUnits::n; ++i)
                 if (MUnits::has(i)) *reinterpret_cast<u32x4*>(compact_unit(L.M, tid + 256 * i)) = mr.raw[i];
-            if (chunk + 1 < c1) fetch_m(chunk + 1);
+            if (chunk + 1 < c1) {
+                fetch_m(chunk + 1);
+                put_k(c + 1);   // over the chunk before's
+                if (chunk + 2 < c1) fetch_k(chunk + 2);
+            }
             __syncthreads();
             if constexpr (OUT) {
 #pragma unroll
@@ -446,8 +460,8 @@ __device__ __forceinline__ void scan_split(ScanSplitLds<DKP, In, OUT>& L, const 
                 if (chunk + 1 < c1) fetch_q(chunk + 1);
             }
             if (chunk + 1 < c1) {
-                put_k(c + 1);
-                if (chunk + 2 < c1) fetch_k(chunk + 2);
+                put_v(c + 1);
+                if (chunk + 2 < c1) fetch_v(chunk + 2);
             }
         }
         __syncthreads();
