@@ -84,7 +84,8 @@ typedef enum {
     MESA_KERNEL_BWD_KV = 6,          /* backward: key and value gradients                */
     MESA_KERNEL_BWD_GATE = 7,        /* backward: gate and regulariser gradients         */
     MESA_KERNEL_HAWK = 8,            /* Hawk layer recurrence (all its kernels)          */
-                                     /* 9..15 are not used                               */
+                                     /* 9..15 are not used: 9 was the first id that was  */
+                                     /* refused, and callers may count on it             */
     MESA_KERNEL_DELTA_PREP = 16,     /* delta rule: the chunks' state-free matrices      */
     MESA_KERNEL_DELTA_SCAN = 17,     /* delta rule: the pass over the chunks             */
     MESA_KERNEL_DELTA_STEP = 18,     /* delta rule: one token                            */
@@ -387,6 +388,7 @@ mesa_status mesa_delta_forward(const void *q, const void *k, const void *v, int 
  *   grad_state [B, H, dv, dk]   float32 gradient of state0, or NULL; may be
  *                               grad_final itself
  *   workspace                   at least mesa_delta_backward_workspace_bytes(...)
+ * Products of a gradient with a value or a state keep their bits down to 2^-110.
  * Sums are taken in a fixed order: results do not change from run to run.
  */
 size_t mesa_delta_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype);

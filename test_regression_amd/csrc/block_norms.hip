@@ -23,10 +23,11 @@
 // small kernel (4-5 us), all in a fixed order (no atomics).
 //
 // Measured (times of whole calls; a large copy reaches 5.5 TB/s):
-//   gate norm 8x16x4096x128 bf16         78 us  5.2 TB/s; gradients 134 us  5.0 TB/s
-//   residual norm 32768x2048 f32 + bf16 145 us  5.6 TB/s; gradients with the
-//     residual's 213 us 5.7 TB/s, without 177 us 5.3 TB/s
-//   4099x1237 f32: 16 us, gradients 26 us; a row or 256: 3 to 5 us in the kernel
+//   gate norm 8x16x4096x128 bf16         79 us  5.1 TB/s; gradients 136 us  4.9 TB/s
+//   residual norm 32768x2048 f32 + bf16 144 us  5.6 TB/s; gradients with the
+//     residual's 216 us 5.6 TB/s, without 178 us 5.3 TB/s
+//   4099x1237 f32: 16 us, gradients with the residual's 32 us, without 28; a row
+//     or 256: 3 to 5 us in the kernel
 #include <algorithm>
 
 #include "io8.h"

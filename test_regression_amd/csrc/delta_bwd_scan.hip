@@ -14,7 +14,7 @@
 // to 22 bits: the gate gradients are float32 sums of these results.
 //
 // For float rows of 128 features (the others take delta_bwd_split.hip): the
-// gradients of 2x16x4096, dv = 128, take 1114 us in all, bound by this chain and
+// gradients of 2x16x4096, dv = 128, take 1098 us in all, bound by this chain and
 // the forward's.
 #include "delta_core.h"
 

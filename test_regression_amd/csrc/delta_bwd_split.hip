@@ -17,9 +17,9 @@
 // workgroups of both: with few heads they fill the GPU together.
 //
 // Bound, like the forward's pass, by the chain: 2x16x4096, dk = dv = 128, bf16
-// (256 column tiles each way) takes 242-254 us, 3.8-4.0 us a chunk, for 0.67 GB of
+// (256 column tiles each way) takes 244-255 us, 3.8-4.0 us a chunk, for 0.67 GB of
 // traffic; all of the gradients took 590 us with a launch for each pass and 447
-// with one.  2x8x1023 float with dk = 64, dv = 128: 52 us.
+// with one (428 today).  2x8x1023 float with dk = 64, dv = 128: 51-52 us.
 #include "delta_scan_split.h"
 
 namespace mesa {

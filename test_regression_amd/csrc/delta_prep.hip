@@ -21,8 +21,8 @@
 // fp16 pattern: P is then off by at most 2^-11 2^-3 = 2^-14 of an element, a
 // 32nd of the outputs' own smallest half step, for three quarters of the memory.
 //
-// 8x16x4096, dk = 128, bf16: 103-124 us for 266 MB of keys and queries in and 166
-// MB of planes out, 3.5-4.2 TB/s; vector instructions take 60 % of the cycles.
+// 8x16x4096, dk = 128, bf16: 102-125 us for 273 MB of keys, queries and gates in
+// and 189 MB of planes out, 3.7-4.5 TB/s; vector instructions take 59 % of the cycles.
 #include "delta_core.h"
 
 namespace mesa {

@@ -17,7 +17,7 @@
 // leave compute units idle: then a workgroup takes 32 or 16 columns and its
 // other waves only stage.  Only float rows of 128 features come here, whose
 // planes delta_scan_split.h's kernel has no LDS for: a forward of 8x16x4096, dv =
-// 128, takes 690 us of which this is 80 %, one of 2x16x4096 493 us.
+// 128, takes 691 us of which this is 80 %, one of 2x16x4096 497 us.
 //
 // Precision: every operand is hi + lo (22 bits).
 #include "delta_core.h"

@@ -29,11 +29,13 @@
 // A wave alone on its SIMD issues one vector instruction in 5 cycles (9 for
 // the mixed-precision ones of the splits) while the SIMD could take one in
 // 1.3 from several waves (measured); the pass is bound by the state waves' own
-// instructions and latencies, which is why nothing else is left to them: matrix
-// instructions take 23 % of the cycles and LDS 45 %.  8x16x4096, dk = dv = 128,
-// bf16: 217-265 us, 3.4-4.1 us a chunk (with all of a column's work on one wave,
-// delta_scan.hip's way, 358 us).  1x16x16384 in eight segments: 158 us for the ends, 16
-// to join them and 113 for the pass, 690 us in one piece.
+// instructions and latencies, which is why nothing else is left to them (2500 and
+// 3600 cycles in a chunk's halves; matrix instructions take 28 %), and where every
+// compute unit has a workgroup by the staging waves' wait for memory as well (2900
+// and 3800).  8x16x4096, dk = dv = 128, bf16: 230-285 us, 3.6-4.5 us a chunk (with
+// all of a column's work on one wave, delta_scan.hip's way, 358 us); with all loads
+// from the caches 205.  1x16x16384 in eight segments: 151-158 us for the ends, 16 to
+// join them and 118-123 for the pass; 302 us in all, 690 in one piece.
 #pragma once
 #include "delta_core.h"
 

@@ -77,7 +77,14 @@ __global__ __launch_bounds__(DK * 4) void delta_segments_kernel(DeltaArgs a) {
 // Segments by the passes' modelled time: a chunk takes about 2.5, 2.9 or 3.5 us
 // with one, two or four column tiles a workgroup (up to 256, 512, 1024 tiles at
 // once; measured with bf16 and dk = 128), the two more launches about 20 us.
-// 1x16x16384 takes 307 us in all in the eight segments this gives, 690 in one.
+// Whole forward calls with 1, 4, 8 and 16 segments, in us, * the model's choice:
+//   1x16x16384 128x128 bf16  690 361 305* 339    4x8x4096 64x64 float   183 111 106* 123
+//   1x16x4096  128x128 bf16  182 109 104* 131    8x8x8192 16x32 float   343 222 230 242*
+//   1x8x2048   128x256 bf16   96  65*  69  95    1x4x16384 16x16 float  516 229 129 82*
+//   4x8x4096   64x64   bf16  149  97  84*  97    1x4x16384 32x64 bf16   430 203 118 78*
+//   1x1x1024   128x128 bf16   53*  41   -   -    2x16x2048 32x32 bf16    73  50  43* -
+// The launches cost less than 20 us for one head, and the chunks of narrow float
+// rows less than the model's: at worst a tenth and a quarter are left there.
 struct SegmentModel {
     double whole, ends, real;   // us a chunk: the sequence in one piece; the segments' ends, the pass from their starts
 };

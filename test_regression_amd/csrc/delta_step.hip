@@ -10,7 +10,7 @@
 // 8 bytes.  Eight lanes take a row (four at dk = 16), 16-byte pieces
 // interleaved over them, so that a wave's accesses are 128-byte runs and the
 // row sums take three lane exchanges.  A wave takes one group of 8 or 16 rows:
-// 256 sequences x 16 heads of 128 x 128 take 94 us, 5.8 TB/s; with four groups
+// 256 sequences x 16 heads of 128 x 128 take 95 us, 5.6 TB/s; with four groups
 // a wave 102 us.  One sequence of 4 heads of 64 x 64: 3 us in the kernel.
 #include "io8.h"
 #include "mesa_kernels.h"

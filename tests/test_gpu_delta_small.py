@@ -129,6 +129,23 @@ def test_gradients_of_small_values_from_no_state(dtype, dk, dv):
 
 
 @pytest.mark.parametrize("dtype,dk,dv", WIDTHS)
+def test_small_values_with_small_gradients(dtype, dk, dv):
+    """Products of 2^-110."""
+    import torch
+    from test_regression_amd import mesa
+    say("case delta small values, small gradients", (dtype, dk, dv))
+    t, f = delta_inputs(255, 1, 2, 2, 200, dk, dv, dtype)
+    for n in ("v", "state"):
+        scaled(t, f, n, 2.0 ** -55)
+    go = (torch.from_numpy(np.random.default_rng(255).standard_normal(t["v"].shape)) * 2.0 ** -55).to(t["v"].dtype)
+    d = dev(t)
+    g = mesa.mesa_delta_backward(d["q"], d["k"], d["v"], d["gamma"], d["beta"], go.cuda(), d["state"])
+    _, _, ref = delta_ref(f, go.double().numpy())
+    for n, x in g.items():
+        assert rel(x.double().cpu().numpy(), ref[n]) <= grad_tol(n, dtype), (n, rel(x.double().cpu().numpy(), ref[n]))
+
+
+@pytest.mark.parametrize("dtype,dk,dv", WIDTHS)
 def test_small_gradients_before_a_reset(dtype, dk, dv):
     """Gradients of unit size behind a gate of 0, of 2^-40 before it."""
     import torch
