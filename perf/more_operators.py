@@ -206,11 +206,11 @@ def _conv(s):
     W = w.shape[0]
     if own:
         from test_regression_amd import mesa
-        y, h = mesa.mesa_causal_conv(x, w, bias, hist, lens=lens, hist_out=hist if dy is None else None,
-                                     return_hist=hist is not None)
-        r = dict(y=y)
-        if hist is not None:
-            r["hist"] = h
+        if hist is None:
+            r = dict(y=mesa.mesa_causal_conv(x, w, bias, lens=lens))
+        else:
+            y, h = mesa.mesa_causal_conv(x, w, bias, hist, lens=lens, hist_out=hist if dy is None else None, return_hist=True)
+            r = dict(y=y, hist=h)
         if dy is not None:
             g = mesa.mesa_causal_conv_backward(x, w, dy, bias, hist, lens=lens)
             r.update({k: v for k, v in g.items() if v is not None})
