@@ -95,7 +95,16 @@ typedef enum {
     MESA_KERNEL_GATE_NORM_BWD = 22,
     MESA_KERNEL_RESIDUAL_NORM = 23,  /* residual scale, addition and norm                */
     MESA_KERNEL_RESIDUAL_NORM_BWD = 24,
-    MESA_KERNEL_COUNT = 25
+                                     /* 25..31 are not used, as 9..15                    */
+    MESA_KERNEL_CAUSAL_CONV = 32,    /* causal convolution over rows                     */
+    MESA_KERNEL_CAUSAL_CONV_BWD = 33,
+    MESA_KERNEL_SSM_SCAN = 34,       /* state space scan: the passes over the chunks     */
+    MESA_KERNEL_SSM_STATES = 35,     /* state space scan: the backward's chunk states    */
+    MESA_KERNEL_SSM_GRADS = 36,      /* state space scan: gradients per chunk, their sums */
+    MESA_KERNEL_SSM_STEP = 37,       /* state space scan: one token                      */
+    MESA_KERNEL_QK_ROTATE = 38,      /* norm and rotation of queries and keys            */
+    MESA_KERNEL_QK_ROTATE_BWD = 39,
+    MESA_KERNEL_COUNT = 40
 } mesa_kernel_id;
 
 /* Library ABI version (MESA_ABI_VERSION of the build). */
@@ -459,6 +468,197 @@ mesa_status mesa_residual_norm_backward(const void *h, int h_dtype, const void *
                                         int R, int D, void *grad_h, void *grad_y, float *grad_w,
                                         float *grad_scale, void *workspace, size_t workspace_bytes,
                                         void *stream);
+
+/*
+ * Strided tensors.  In the calls below some tensors may be views: slices of the
+ * rows of a projection, of a convolution's output, of one buffer of gradients.
+ * `*_strides` then holds their element strides {batch, head, token} (of a
+ * [B, T, D] tensor {batch, token}), NULL says contiguous in the order given.
+ * The last dimension is always contiguous; a view needs the alignment of an
+ * element only.  Strides are not negative; an input's may be 0 (the same rows for
+ * several), an output's rows may not share memory.  Outputs that lie between one
+ * another in the same rows are told apart where they have a stride in common.
+ * All other pointers, and contiguous tensors, are 16-byte aligned as everywhere.
+ *
+ * Lengths.  `lens` [B] int32, or NULL: the tokens that each row of a padded batch
+ * has (taken as 0 below 0 and as T above T).  What is behind them is not read;
+ * outputs and gradients there are written as zeros, and states and histories are
+ * those after the row's own last token.
+ */
+
+/*
+ * Short causal convolution over the rows of an input projection, with its
+ * activation, as it stands before the state space scan.  Per channel,
+ *   z_t = bias + sum_{j<W} w[j] x_{t-j},   y_t = silu(z_t), or z_t when silu is 0
+ *
+ *   x         [B, T, D]       dtype, x_strides
+ *   w         [W, D]          float32; j = 0 weighs the current token
+ *   width     W, 1 <= W <= 4
+ *   bias      [D]             float32, or NULL
+ *   hist      [B, W-1, D]     dtype, the W-1 rows before t = 0 (oldest first), or
+ *                             NULL for zeros
+ *   hist_out  [B, W-1, D]     dtype, or NULL: the last W-1 rows of hist followed by
+ *                             x, the hist of the next piece (prefill, then one
+ *                             token per decode step); may be hist itself
+ *   y         [B, T, D]       dtype
+ * Any D >= 1 and T >= 0.
+ */
+mesa_status mesa_causal_conv(const void *x, const int64_t *x_strides, int dtype, const float *w, int width,
+                             const float *bias, int silu, const void *hist, void *hist_out, const int32_t *lens,
+                             int B, int T, int D, void *y, void *stream);
+
+/*
+ * Gradients of mesa_causal_conv from its inputs and grad_y = dL/dy [B, T, D]:
+ *   grad_x [B, T, D] dtype, grad_x_strides; grad_hist [B, W-1, D] dtype, or NULL;
+ *   grad_w [W, D] float32; grad_bias [D] float32 (NULL exactly when bias is).
+ * hist_out is not differentiated.  Sums are taken in a fixed order.
+ */
+size_t mesa_causal_conv_backward_workspace_bytes(int B, int T, int D, int width);
+mesa_status mesa_causal_conv_backward(const void *x, const int64_t *x_strides, int dtype, const float *w, int width,
+                                      const float *bias, int silu, const void *hist, const int32_t *lens,
+                                      const void *grad_y, int B, int T, int D, void *grad_x,
+                                      const int64_t *grad_x_strides, float *grad_w, float *grad_bias,
+                                      void *grad_hist, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Selective state space scan over whole sequences: the gated linear layer whose
+ * state decays by what each token says, one number a head, and takes the token's
+ * outer product without looking at what it holds (the delta rule looks).  Per batch
+ * row and head, with the state S (a map from keys to values, like the delta rule's),
+ *   step_t = softplus(dt_t + dt_bias), or dt_t + dt_bias when softplus is 0
+ *   S_t = exp(A step_t) S_{t-1} + step_t x_t b_t^T,   S_0 = state0 (zeros when NULL)
+ *   out_t = S_t c_t + D x_t
+ *
+ *   x          [B, H, T, dv]    dtype, x_strides: the values
+ *   b, c       [B, Hk, T, dk]   dtype, b_strides, c_strides: the key's and the
+ *                               query's part; H a multiple of Hk, head h uses
+ *                               b and c of h / (H / Hk)
+ *   dt         [B, H, T]        dt_dtype, dt_strides; steps are >= 0.  A token of
+ *                               step 0 (raw -infinity, or the storage type's
+ *                               lowest value) leaves the state as it is
+ *   A          [H]              float32, A <= 0
+ *   D, dt_bias [H]              float32, or NULL
+ *   state0     [B, H, dv, dk]   float32, or NULL
+ *   out        [B, H, T, dv]    dtype, written (bfloat16 rounds to nearest even)
+ *   final_state [B, H, dv, dk]  float32, or NULL; may be state0 itself
+ *   workspace                   at least mesa_ssm_workspace_bytes(...) (0 where
+ *                               none is needed), which never decreases with B, H
+ *                               or T
+ * dk and dv in {16, 32, 64, 128}, T >= 0, token strides of x, b and c below 2^24.
+ * Sums and states are float32, prefix sums of the decays float64.  Rows stored as bfloat16 enter the products exactly; what
+ * is formed in float32 enters as two bfloat16 parts where only bfloat16 outputs
+ * follow (2^-18 of a term) and as three (2^-27) where the state does.  Values are
+ * taken as finite: a NaN or infinity reaches its chunk of 64 tokens and what
+ * follows in its head, other heads never (of b and c: of the heads that share them).
+ */
+size_t mesa_ssm_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype);
+mesa_status mesa_ssm_forward(const void *x, const int64_t *x_strides, const void *b, const int64_t *b_strides,
+                             const void *c, const int64_t *c_strides, int dtype, const void *dt,
+                             const int64_t *dt_strides, int dt_dtype, const float *A, const float *D,
+                             const float *dt_bias, int softplus, const float *state0, const int32_t *lens, int B,
+                             int Hk, int H, int T, int dk, int dv, void *out, float *final_state, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of the scan, from the forward's inputs (the chunk states are formed
+ * again), for L = <out, grad_out> + <final_state, grad_final>:
+ *   grad_out   [B, H, T, dv]    dtype
+ *   grad_final [B, H, dv, dk]   float32, or NULL for zeros
+ *   grad_x [B, H, T, dv], grad_b, grad_c [B, Hk, T, dk] dtype, with strides; shared
+ *                               heads' gradients are summed in float32
+ *   grad_dt    [B, H, T]        dt_dtype, strides: of the raw dt
+ *   grad_A, grad_D, grad_dt_bias [H]  float32; grad_D and grad_dt_bias NULL exactly
+ *                               when D and dt_bias are
+ *   grad_state [B, H, dv, dk]   float32 gradient of state0, or NULL; may be
+ *                               grad_final itself
+ * Sums are taken in a fixed order: results do not change from run to run.
+ */
+size_t mesa_ssm_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype);
+mesa_status mesa_ssm_backward(const void *x, const int64_t *x_strides, const void *b, const int64_t *b_strides,
+                              const void *c, const int64_t *c_strides, int dtype, const void *dt,
+                              const int64_t *dt_strides, int dt_dtype, const float *A, const float *D,
+                              const float *dt_bias, int softplus, const float *state0, const int32_t *lens,
+                              const void *grad_out, const float *grad_final, int B, int Hk, int H, int T, int dk,
+                              int dv, void *grad_x, const int64_t *grad_x_strides, void *grad_b,
+                              const int64_t *grad_b_strides, void *grad_c, const int64_t *grad_c_strides,
+                              void *grad_dt, const int64_t *grad_dt_strides, float *grad_A, float *grad_D,
+                              float *grad_dt_bias, float *grad_state, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
+/*
+ * One token of the scan for N sequences, states updated in place: x [N, H, dv],
+ * b, c [N, Hk, dk], dt [N, H] with strides {batch, head} (NULL for contiguous);
+ * state [N, H, dv, dk] float32 in/out; out [N, H, dv] dtype.  The rest as
+ * mesa_ssm_forward, whose final_state is this state.
+ */
+mesa_status mesa_ssm_step(const void *x, const int64_t *x_strides, const void *b, const int64_t *b_strides,
+                          const void *c, const int64_t *c_strides, int dtype, const void *dt,
+                          const int64_t *dt_strides, int dt_dtype, const float *A, const float *D,
+                          const float *dt_bias, int softplus, float *state, int N, int Hk, int H, int dk, int dv,
+                          void *out, void *stream);
+
+/*
+ * Angles per token of the rot / 2 pairs of features that mesa_qk_rotate turns, into
+ * HOST memory: freqs[i] = base^(-2 i / rot), and *amplitude, the factor on the
+ * rotated features (1 unless said).  For contexts longer than the one trained on,
+ * stretched `factor` >= 1 times:
+ *   MESA_ROTARY_PLAIN    as above (factor must be 1)
+ *   MESA_ROTARY_LINEAR   all angles divided by factor
+ *   MESA_ROTARY_BASE     base times factor^(rot / (rot - 2)): the fastest pair keeps
+ *                        its angle, the slowest is divided by factor
+ *   MESA_ROTARY_PARTS    pairs that turn more than `fast` times over `context` tokens
+ *                        keep their angle, those that turn less than `slow` times
+ *                        are divided by factor, in between the angles are mixed
+ *                        linearly in the turns; amplitude 1 + 0.1 ln(factor)
+ * `fast` > `slow` >= 0 and `context` > 0 are read by the last only.
+ */
+typedef enum {
+    MESA_ROTARY_PLAIN = 0,
+    MESA_ROTARY_LINEAR = 1,
+    MESA_ROTARY_BASE = 2,
+    MESA_ROTARY_PARTS = 3
+} mesa_rotary_scaling;
+mesa_status mesa_rotary_frequencies(int rot, double base, int scaling, double factor, double context, double fast,
+                                    double slow, double *freqs, float *amplitude);
+
+/*
+ * Per-head RMS norm of queries and keys and the rotation by their positions, in one
+ * pass; also of the state space scan's c and b.  Per token at position p and head:
+ *   n = x / sqrt(mean(x^2) + eps) * w   (norm 1),   n = x   (norm 0)
+ *   (y_a, y_b) = amplitude (n_a cos - n_b sin, n_b cos + n_a sin),  angle p freqs[i]
+ * for the pairs i < rot / 2 of features (a, b) = (i, i + rot / 2), or (2 i, 2 i + 1)
+ * when interleaved; features rot and up are n.
+ *
+ *   q, k      [B, Hq, T, d], [B, Hk, T, d]  dtype, with strides; k NULL with Hk = 0
+ *   freqs     [rot / 2]       float64, on the device (mesa_rotary_frequencies)
+ *   rot       a multiple of 16, 16 <= rot <= d
+ *   positions [B, T] int64 (or [T], positions_stride 0), batch stride
+ *             positions_stride; NULL: token t is at position0 + t.  Angles are
+ *             formed in float64: positions up to 2^40 keep their place in the turn
+ *   wq, wk    [d]             float32 weights of the norm, or NULL for 1
+ *   yq, yk    [B, Hq, T, d], [B, Hk, T, d]  dtype
+ * d in {16, 32, 64, 128, 256}; eps > 0.  A row of zeros gives zeros.  Squares are
+ * summed in float32: |x| up to about 1e18.
+ *
+ * Backward, for grad_yq, grad_yk (contiguous), from the forward's inputs: grad_q,
+ * grad_k dtype, with strides; grad_wq, grad_wk [d] float32 (NULL exactly when wq, wk
+ * are).  q and k are not read without the norm, but must be given.  Sums are taken
+ * in a fixed order.
+ */
+mesa_status mesa_qk_rotate(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                           int dtype, const double *freqs, int rot, int interleaved, float amplitude,
+                           const int64_t *positions, int64_t positions_stride, int64_t position0, const float *wq,
+                           const float *wk, int norm, float eps, int B, int Hq, int Hk, int T, int d, void *yq,
+                           void *yk, void *stream);
+size_t mesa_qk_rotate_backward_workspace_bytes(int d);
+mesa_status mesa_qk_rotate_backward(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                                    int dtype, const double *freqs, int rot, int interleaved, float amplitude,
+                                    const int64_t *positions, int64_t positions_stride, int64_t position0,
+                                    const float *wq, const float *wk, int norm, float eps, const void *grad_yq,
+                                    const void *grad_yk, int B, int Hq, int Hk, int T, int d, void *grad_q,
+                                    const int64_t *grad_q_strides, void *grad_k, const int64_t *grad_k_strides,
+                                    float *grad_wq, float *grad_wk, void *workspace, size_t workspace_bytes,
+                                    void *stream);
 
 /*
  * Optional per-kernel timing (not part of the method).  While enabled, each

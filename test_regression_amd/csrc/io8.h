@@ -47,6 +47,22 @@ __device__ __forceinline__ void store8(bf16_t* p, const f32x8& r) {
 // are larger than the caches, or too small for it to matter.
 typedef float f32x4_el __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4_el __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_el __attribute__((ext_vector_type(2), aligned(2)));
+__device__ __forceinline__ f32x4 load4_el(const float* p) {
+    const f32x4_el a = *reinterpret_cast<const f32x4_el*>(p);
+    return f32x4{a[0], a[1], a[2], a[3]};
+}
+__device__ __forceinline__ f32x4 load4_el(const bf16_t* p) {
+    const u32x2_el w = *reinterpret_cast<const u32x2_el*>(p);
+    return f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                 __uint_as_float(w[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ void store4_el(float* p, f32x4 v) {
+    *reinterpret_cast<f32x4_el*>(p) = f32x4_el{v[0], v[1], v[2], v[3]};
+}
+__device__ __forceinline__ void store4_el(bf16_t* p, f32x4 v) {
+    *reinterpret_cast<u32x2_el*>(p) = u32x2_el{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+}
 template <bool WHOLE>
 __device__ __forceinline__ f32x8 load8_upto(const float* p, int left) {
     f32x8 r{};

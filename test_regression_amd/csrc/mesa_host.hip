@@ -95,6 +95,16 @@ hipError_t zero_fill(void* p, size_t bytes, hipStream_t s) {
     return hipGetLastError();
 }
 
+__global__ void zero_halves_kernel(uint16_t* p, size_t n) {
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x) p[i] = 0u;
+}
+hipError_t zero_halves(void* p, size_t n, hipStream_t s) {
+    if (!p || n == 0) return hipSuccess;
+    const unsigned blocks = (unsigned)std::min<size_t>((n + 255) / 256, 4096);
+    hipLaunchKernelGGL(zero_halves_kernel, dim3(blocks), dim3(256), 0, s, static_cast<uint16_t*>(p), n);
+    return hipGetLastError();
+}
+
 __global__ void copy_words_kernel(float* out, const float* in, size_t n) {
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
         out[i] = in[i];
@@ -976,6 +986,514 @@ mesa_status mesa_residual_norm_backward(const void* h, int h_dtype, const void* 
     return MESA_OK;
 }
 
+// ---- strided tensors ----
+// A tensor [B, heads, T, d] of a call, or with bytes set a plain buffer.
+struct View {
+    const void* p;
+    mesa::RowStrides s;
+    long B, H, T, d;
+    int size;            // bytes of an element
+    const char* name;
+    size_t bytes = 0;
+    const char* over = nullptr;
+};
+static View plain(const void* p, size_t bytes, const char* name, const char* over = nullptr) {
+    return {p, {0, 0, 0}, 1, 1, 1, 1, 1, name, bytes, over};
+}
+static View strided(const void* p, const int64_t* st, long B, long H, long T, long d, int dtype, const char* name) {
+    View v{p, {}, B, H, T, d, dtype == MESA_DTYPE_BF16 ? 2 : 4, name};
+    v.s = st ? mesa::RowStrides{(long)st[0], (long)st[1], (long)st[2]} : mesa::RowStrides{H * T * d, T * d, d};
+    return v;
+}
+static bool empty(const View& v) { return !v.p || (v.bytes == 0 && (v.B <= 0 || v.H <= 0 || v.T <= 0 || v.d <= 0)); }
+static double extent(const View& v) {
+    if (v.bytes) return (double)v.bytes;
+    if (empty(v)) return 0.0;
+    return ((double)(v.B - 1) * v.s.batch + (double)(v.H - 1) * v.s.head + (double)(v.T - 1) * v.s.token + v.d) * v.size;
+}
+// Elements of one row of pitch P, when all strides are multiples of P or stay below it (else 0).
+static long width_in(const View& v, long P) {
+    long w = v.d;
+    const long n[3] = {v.B, v.H, v.T}, s[3] = {v.s.batch, v.s.head, v.s.token};
+    for (int i = 0; i < 3; ++i)
+        if (n[i] > 1 && s[i] % P != 0) w += (n[i] - 1) * s[i];
+    return w <= P ? w : 0;
+}
+// Whether two views whose memory overlaps lie between one another in rows of a pitch they share.
+static bool interleaved(const View& a, const View& b) {
+    if (a.bytes || b.bytes || a.size != b.size) return false;
+    const intptr_t delta = (intptr_t)((uintptr_t)b.p - (uintptr_t)a.p);
+    if (delta % a.size) return false;
+    const long of_a[3] = {a.s.batch, a.s.head, a.s.token}, of_b[3] = {b.s.batch, b.s.head, b.s.token};
+    for (long P : of_a)
+        for (long Q : of_b) {
+            if (P != Q || P <= 0) continue;
+            const long wa = width_in(a, P), wb = width_in(b, P), x = ((delta / a.size) % P + P) % P;
+            if (wa && wb && x >= wa && P - x >= wb) return true;
+        }
+    return false;
+}
+static bool share_memory(const View& a, const View& b) {
+    if (empty(a) || empty(b)) return false;
+    const double d = a.p < b.p ? (double)((uintptr_t)b.p - (uintptr_t)a.p) : -(double)((uintptr_t)a.p - (uintptr_t)b.p);
+    return d < extent(a) && -d < extent(b) && !interleaved(a, b);
+}
+// As no_alias, for views; also refuses strides that are negative, address more than
+// 2^62 bytes, or let an output's rows overlap.
+static mesa_status check_views(std::initializer_list<View> outs, std::initializer_list<View> ins) {
+    for (const auto* list : {&outs, &ins})
+        for (const View& v : *list) {
+            if (empty(v) || v.bytes) continue;
+            if ((v.B > 1 && v.s.batch < 0) || (v.H > 1 && v.s.head < 0) || (v.T > 1 && v.s.token < 0))
+                return fail(MESA_ERR_INVALID_ARGUMENT, "strides of %s must not be negative", v.name);
+            if (extent(v) > 4.0e18) return fail(MESA_ERR_INVALID_ARGUMENT, "strides of %s are too large", v.name);
+            if (!aligned(v.p, v.size)) return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (%s: an element's size)", v.name);
+        }
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (!empty(*o) && !o->bytes) {
+            long n[3] = {o->B, o->H, o->T}, s[3] = {o->s.batch, o->s.head, o->s.token};
+            double reach = (double)o->d;
+            for (int k = 0; k < 3; ++k) {   // by growing stride
+                int at = -1;
+                for (int i = 0; i < 3; ++i)
+                    if (n[i] > 1 && (at < 0 || s[i] < s[at])) at = i;
+                if (at < 0) break;
+                if (s[at] < reach) return fail(MESA_ERR_INVALID_ARGUMENT, "rows of %s must not share memory", o->name);
+                reach += (double)(n[at] - 1) * s[at];
+                n[at] = 1;
+            }
+        }
+        for (const View& i : ins)
+            if (share_memory(*o, i) && !(o->p == i.p && o->over && !strcmp(o->over, i.name)))
+                return fail(MESA_ERR_INVALID_ARGUMENT, "%s must not alias %s", o->name, i.name);
+        for (auto q = outs.begin(); q != o; ++q)
+            if (share_memory(*o, *q)) return fail(MESA_ERR_INVALID_ARGUMENT, "%s must not alias %s", o->name, q->name);
+    }
+    return MESA_OK;
+}
+
+// ---- causal convolution ----
+static mesa_status conv_checks(const void* x, int dtype, const float* w, int width, const float* bias, const void* hist,
+                               const int32_t* lens, int B, int T, int D) {
+    if (!dtype_ok(dtype))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "dtype %d is not MESA_DTYPE_F32 or MESA_DTYPE_BF16", dtype);
+    if (B <= 0 || T < 0 || D <= 0 || width <= 0)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "sizes must be positive, T >= 0 (B=%d T=%d D=%d width=%d)", B, T, D, width);
+    if (width > mesa::kConvMaxWidth) return fail(MESA_ERR_UNSUPPORTED, "width %d not built (at most %d)", width, mesa::kConvMaxWidth);
+    if (!w || (T > 0 && !x)) return fail(MESA_ERR_INVALID_ARGUMENT, "w, and x when T > 0, must be non-null");
+    if (!aligned(w, 16) || !aligned(bias, 16) || !aligned(hist, 16) || !aligned(lens, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for w, bias and hist, 4 B for lens)");
+    // threads: one for eight channels of a run of tokens, in the backward 256 for 256 channels of eight runs
+    const double pieces = ((double)D + 255) / 8, runs = (double)T / mesa::kConvRun + mesa::kConvRun;
+    if (B * pieces * runs > kMaxThreads) return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B=%d T=%d D=%d)", B, T, D);
+    return MESA_OK;
+}
+static View rows_view(const void* p, const int64_t* st, int B, int T, int D, int dtype, const char* name) {
+    const int64_t s[3] = {st ? st[0] : (int64_t)T * D, 0, st ? st[1] : D};
+    return strided(p, s, B, 1, T, D, dtype, name);
+}
+
+mesa_status mesa_causal_conv(const void* x, const int64_t* x_strides, int dtype, const float* w, int width, const float* bias,
+                             int silu, const void* hist, void* hist_out, const int32_t* lens, int B, int T, int D, void* y,
+                             void* stream) {
+    g_err.clear();
+    mesa_status st = conv_checks(x, dtype, w, width, bias, hist, lens, B, T, D);
+    if (st != MESA_OK) return st;
+    if (T > 0 && !y) return fail(MESA_ERR_INVALID_ARGUMENT, "y must be non-null");
+    if (!aligned(y, 16) || !aligned(hist_out, 16))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for y and hist_out)");
+    const View vx = rows_view(x, x_strides, B, T, D, dtype, "x");
+    const size_t hb = bytes_of(dtype, (double)B * (width - 1) * D), wb = (size_t)width * D * sizeof(float);
+    st = check_views({plain(y, bytes_of(dtype, (double)B * T * D), "y"), plain(hist_out, hb, "hist_out", "hist")},
+                     {vx, plain(w, wb, "w"), plain(bias, (size_t)D * 4, "bias"), plain(hist, hb, "hist"), plain(lens, (size_t)B * 4, "lens")});
+    if (st != MESA_OK) return st;
+    if (T == 0 && (!hist_out || hist_out == hist || width == 1)) return MESA_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const mesa::ConvArgs a{x, vx.s.batch, vx.s.token, w, width, bias, silu, hist, hist_out, lens, B, T, D,
+                           dtype == MESA_DTYPE_BF16, y, 0, 0};
+    const hipError_t e = timed_launch(MESA_KERNEL_CAUSAL_CONV, s, [&] { return mesa::launch_causal_conv(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "causal convolution kernel launch");
+    return MESA_OK;
+}
+
+size_t mesa_causal_conv_backward_workspace_bytes(int B, int T, int D, int width) {
+    if (B <= 0 || T <= 0 || D <= 0 || width <= 0) return 0;
+    return (size_t)mesa::conv_bwd_parts(B, T) * (width + 1) * D * sizeof(float);
+}
+
+mesa_status mesa_causal_conv_backward(const void* x, const int64_t* x_strides, int dtype, const float* w, int width,
+                                      const float* bias, int silu, const void* hist, const int32_t* lens,
+                                      const void* grad_y, int B, int T, int D, void* grad_x, const int64_t* grad_x_strides,
+                                      float* grad_w, float* grad_bias, void* grad_hist, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    mesa_status st = conv_checks(x, dtype, w, width, bias, hist, lens, B, T, D);
+    if (st != MESA_OK) return st;
+    if (!grad_w || (T > 0 && (!grad_y || !grad_x || !workspace)))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_w, and grad_y, grad_x and workspace when T > 0, must be non-null");
+    if ((bias == nullptr) != (grad_bias == nullptr))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_bias must be given exactly when bias is");
+    if (!aligned(grad_y, 16) || !aligned(grad_hist, 16) || !aligned(workspace, 16) || !aligned(grad_w, 4) || !aligned(grad_bias, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT,
+                    "misaligned pointer (16 B for grad_y, grad_hist and workspace, 4 B for grad_w and grad_bias)");
+    const size_t need = mesa_causal_conv_backward_workspace_bytes(B, T, D, width);
+    if (workspace_bytes < need)
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, need);
+    const View vx = rows_view(x, x_strides, B, T, D, dtype, "x"), vg = rows_view(grad_x, grad_x_strides, B, T, D, dtype, "grad_x");
+    const size_t hb = bytes_of(dtype, (double)B * (width - 1) * D), wb = (size_t)width * D * 4, db = (size_t)D * 4;
+    st = check_views({vg, plain(grad_hist, hb, "grad_hist"), plain(grad_w, wb, "grad_w"), plain(grad_bias, db, "grad_bias"),
+                      plain(workspace, need, "workspace")},
+                     {vx, plain(w, wb, "w"), plain(bias, db, "bias"), plain(hist, hb, "hist"), plain(lens, (size_t)B * 4, "lens"),
+                      plain(grad_y, bytes_of(dtype, (double)B * T * D), "grad_y")});
+    if (st != MESA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0) {
+        hipError_t e = zero_fill(grad_w, wb, s);
+        if (e == hipSuccess) e = zero_fill(grad_bias, db, s);
+        if (e == hipSuccess) e = zero_halves(grad_hist, hb / 2, s);
+        if (e != hipSuccess) return hip_fail(e, "zero fill of the gradients for T = 0");
+        return MESA_OK;
+    }
+    const mesa::ConvBwdArgs a{{x, vx.s.batch, vx.s.token, w, width, bias, silu, hist, nullptr, lens, B, T, D,
+                               dtype == MESA_DTYPE_BF16, nullptr, 0, 0},
+                              grad_y, grad_x, vg.s.batch, vg.s.token, grad_hist, grad_w, grad_bias,
+                              static_cast<float*>(workspace)};
+    const hipError_t e = timed_launch(MESA_KERNEL_CAUSAL_CONV_BWD, s, [&] { return mesa::launch_causal_conv_bwd(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "causal convolution gradient kernel launch");
+    return MESA_OK;
+}
+
+// ---- state space scan ----
+static long ssm_chunks(int T) { return ((long)T + mesa::kSsmChunk - 1) / mesa::kSsmChunk; }
+// Bytes of n segments' states and decays.
+static size_t ssm_slot_bytes(size_t n, int dk, int dv) { return (n * ((size_t)dv * dk + 1) * sizeof(float) + 15) / 16 * 16; }
+
+size_t mesa_ssm_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype) {
+    if (B <= 0 || H <= 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
+    return ssm_slot_bytes(mesa::ssm_segment_slots((long)B * H, (int)ssm_chunks(T), dv, 1), dk, dv);
+}
+
+// The checks the scan's entry points share; T is 1 for the step.
+static mesa_status ssm_checks(int dtype, int dt_dtype, const float* A, const float* D, const float* dt_bias,
+                              const float* state0, const int32_t* lens, int B, int Hk, int H, int T, int dk, int dv, bool step) {
+    if (!dtype_ok(dtype) || !dtype_ok(dt_dtype))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "dtype %d / dt_dtype %d must be MESA_DTYPE_F32 or MESA_DTYPE_BF16", dtype, dt_dtype);
+    if (B <= 0 || Hk <= 0 || H <= 0 || T < 0 || dk <= 0 || dv <= 0)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "sizes must be positive, T >= 0 (B or N=%d Hk=%d H=%d T=%d dk=%d dv=%d)", B, Hk, H,
+                    T, dk, dv);
+    if (H % Hk != 0) return fail(MESA_ERR_INVALID_ARGUMENT, "H=%d is not a multiple of Hk=%d", H, Hk);
+    if (!A) return fail(MESA_ERR_INVALID_ARGUMENT, "A must be non-null");
+    if (!aligned(A, 4) || !aligned(D, 4) || !aligned(dt_bias, 4) || !aligned(lens, 4) || !aligned(state0, 16))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (4 B for A, D, dt_bias and lens, 16 B for states)");
+    if (!supported_d(dk)) return fail(MESA_ERR_UNSUPPORTED, "dk=%d not built (16, 32, 64, 128)", dk);
+    if (!supported_d(dv)) return fail(MESA_ERR_UNSUPPORTED, "dv=%d not built (16, 32, 64, 128)", dv);
+    // the launches' threads: the step's at most 8 a row of the state; else 512 for 64
+    // columns of dv of a head and segment or chunk, and one for four features of dB and dC
+    const double BH = (double)B * H, nc = (double)ssm_chunks(T);
+    const double threads = step ? BH * dv * 8 : std::max(BH * std::max(nc, 1.0) * ((dv + 63) / 64) * 512, (double)B * Hk * T * dk / 2);
+    if (threads > kMaxThreads) return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B*H=%ld, chunks=%ld)", (long)B * H, ssm_chunks(T));
+    return MESA_OK;
+}
+
+// The kernels address a chunk's rows by 32-bit offsets.
+static mesa_status ssm_pitches(std::initializer_list<View> views) {
+    for (const View& v : views)
+        if (v.T > 1 && v.s.token >= mesa::kSsmPitch)
+            return fail(MESA_ERR_UNSUPPORTED, "token stride of %s not built (2^24 elements or more)", v.name);
+    return MESA_OK;
+}
+
+mesa_status mesa_ssm_forward(const void* x, const int64_t* x_strides, const void* b, const int64_t* b_strides, const void* c,
+                             const int64_t* c_strides, int dtype, const void* dt, const int64_t* dt_strides, int dt_dtype,
+                             const float* A, const float* D, const float* dt_bias, int softplus, const float* state0,
+                             const int32_t* lens, int B, int Hk, int H, int T, int dk, int dv, void* out, float* final_state,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    mesa_status st = ssm_checks(dtype, dt_dtype, A, D, dt_bias, state0, lens, B, Hk, H, T, dk, dv, false);
+    if (st != MESA_OK) return st;
+    if (T > 0 && (!x || !b || !c || !dt || !out))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "x, b, c, dt and out must be non-null");
+    if (!aligned(out, 16) || !aligned(final_state, 16) || !aligned(workspace, 16))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for out, final_state and workspace)");
+    const long BH = (long)B * H, nc = ssm_chunks(T);
+    const int nseg = T > 0 ? mesa::ssm_segments(BH, (int)nc, dv, 1) : 1;
+    const size_t need = ssm_slot_bytes((size_t)BH * (nseg - 1), dk, dv);
+    if (workspace_bytes < need || (need && !workspace))
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace ? workspace_bytes : 0, need);
+    const size_t sb = (size_t)BH * dv * dk * sizeof(float), hb = (size_t)H * 4;
+    const View vx = strided(x, x_strides, B, H, T, dv, dtype, "x"), vb = strided(b, b_strides, B, Hk, T, dk, dtype, "b"),
+               vc = strided(c, c_strides, B, Hk, T, dk, dtype, "c"), vd = strided(dt, dt_strides, B, H, T, 1, dt_dtype, "dt");
+    st = check_views({plain(out, bytes_of(dtype, (double)BH * T * dv), "out"), plain(final_state, sb, "final_state", "state0"),
+                      plain(workspace, need, "workspace")},
+                     {vx, vb, vc, vd, plain(A, hb, "A"), plain(D, hb, "D"), plain(dt_bias, hb, "dt_bias"),
+                      plain(state0, sb, "state0"), plain(lens, (size_t)B * 4, "lens")});
+    if (st != MESA_OK) return st;
+    if ((st = ssm_pitches({vx, vb, vc})) != MESA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0) {
+        const hipError_t e = copy_or_zero(final_state, state0, (size_t)BH * dv * dk, s);
+        if (e != hipSuccess) return hip_fail(e, "final state for T = 0");
+        return MESA_OK;
+    }
+    mesa::SsmArgs a{x, vx.s, b, vb.s, c, vc.s, dt, vd.s, dt_dtype == MESA_DTYPE_BF16, A, D, dt_bias, softplus, state0, lens,
+                    BH, B, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16, out, final_state};
+    a.nseg = nseg;
+    a.seg_chunks = (int)((nc + nseg - 1) / nseg);
+    a.seg_start = static_cast<float*>(workspace);
+    a.seg_decay = a.seg_start + (size_t)BH * (nseg - 1) * dv * dk;
+    const hipError_t e = timed_launch(MESA_KERNEL_SSM_SCAN, s, [&] { return mesa::launch_ssm_scan(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "state space scan kernel launch");
+    return MESA_OK;
+}
+
+// Backward workspace, offsets in bytes (every piece a multiple of 16): the chunk
+// states S and R, the heads' sums, the segments' `slots`, `parts` of dB and dC for a
+// chunk's group of heads.
+struct SsmBwdLayout { size_t R, sums, seg, part, total; };
+static SsmBwdLayout ssm_bwd_layout(int B, int H, int T, int dk, int dv, size_t slots, size_t parts) {
+    const size_t nc = ssm_chunks(T), states = (size_t)B * H * nc * dk * dv * sizeof(float);
+    SsmBwdLayout l{};
+    l.R = states;
+    l.sums = 2 * states;
+    l.seg = l.sums + ((size_t)H * 3 * B * nc * sizeof(double) + 15) / 16 * 16;
+    l.part = l.seg + ssm_slot_bytes(slots, dk, dv);
+    l.total = l.part + parts * 2 * mesa::kSsmChunk * dk * sizeof(float);
+    return l;
+}
+
+size_t mesa_ssm_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype) {
+    if (B <= 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
+    // enough for every smaller batch and shorter sequence too: those may split the heads further, but
+    // into at most kSsmGradGroups workgroups (of a part, row, group and chunk) where there is more than one part
+    const size_t parts = H > Hk ? std::min((size_t)mesa::kSsmGradGroups, (size_t)B * H * ssm_chunks(T)) : 0;
+    return ssm_bwd_layout(B, H, T, dk, dv, mesa::ssm_segment_slots((long)B * H, (int)ssm_chunks(T), dv, 2), parts).total;
+}
+
+mesa_status mesa_ssm_backward(const void* x, const int64_t* x_strides, const void* b, const int64_t* b_strides, const void* c,
+                              const int64_t* c_strides, int dtype, const void* dt, const int64_t* dt_strides, int dt_dtype,
+                              const float* A, const float* D, const float* dt_bias, int softplus, const float* state0,
+                              const int32_t* lens, const void* grad_out, const float* grad_final, int B, int Hk, int H, int T,
+                              int dk, int dv, void* grad_x, const int64_t* grad_x_strides, void* grad_b,
+                              const int64_t* grad_b_strides, void* grad_c, const int64_t* grad_c_strides, void* grad_dt,
+                              const int64_t* grad_dt_strides, float* grad_A, float* grad_D, float* grad_dt_bias,
+                              float* grad_state, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    mesa_status st = ssm_checks(dtype, dt_dtype, A, D, dt_bias, state0, lens, B, Hk, H, T, dk, dv, false);
+    if (st != MESA_OK) return st;
+    if (!grad_A || (T > 0 && (!x || !b || !c || !dt || !grad_out || !grad_x || !grad_b || !grad_c || !grad_dt || !workspace)))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "x, b, c, dt, grad_out, their gradients, grad_A and workspace must be non-null");
+    if ((D == nullptr) != (grad_D == nullptr) || (dt_bias == nullptr) != (grad_dt_bias == nullptr))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_D and grad_dt_bias must be given exactly when D and dt_bias are");
+    if (!aligned(grad_out, 16) || !aligned(grad_final, 16) || !aligned(grad_state, 16) || !aligned(workspace, 16) ||
+        !aligned(grad_A, 4) || !aligned(grad_D, 4) || !aligned(grad_dt_bias, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT,
+                    "misaligned pointer (16 B for grad_out, states and workspace, 4 B for the heads' gradients)");
+    const long BH = (long)B * H, nc = ssm_chunks(T);
+    const int parts = T > 0 ? mesa::ssm_grad_parts(B, Hk, H, (int)nc) : 1;
+    const int nseg = T > 0 ? mesa::ssm_segments(BH, (int)nc, dv, 2) : 1;
+    const SsmBwdLayout l = ssm_bwd_layout(B, H, T, dk, dv, 2 * (size_t)BH * (nseg - 1), parts > 1 ? (size_t)parts * B * Hk * nc : 0);
+    if (T > 0 && workspace_bytes < l.total)
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, l.total);
+    const size_t sb = (size_t)BH * dv * dk * sizeof(float), hb = (size_t)H * 4;
+    const View vx = strided(x, x_strides, B, H, T, dv, dtype, "x"), vb = strided(b, b_strides, B, Hk, T, dk, dtype, "b"),
+               vc = strided(c, c_strides, B, Hk, T, dk, dtype, "c"), vd = strided(dt, dt_strides, B, H, T, 1, dt_dtype, "dt"),
+               gx = strided(grad_x, grad_x_strides, B, H, T, dv, dtype, "grad_x"),
+               gb = strided(grad_b, grad_b_strides, B, Hk, T, dk, dtype, "grad_b"),
+               gc = strided(grad_c, grad_c_strides, B, Hk, T, dk, dtype, "grad_c"),
+               gd = strided(grad_dt, grad_dt_strides, B, H, T, 1, dt_dtype, "grad_dt");
+    st = check_views({gx, gb, gc, gd, plain(grad_A, hb, "grad_A"), plain(grad_D, hb, "grad_D"),
+                      plain(grad_dt_bias, hb, "grad_dt_bias"), plain(grad_state, sb, "grad_state", "grad_final"),
+                      plain(workspace, l.total, "workspace")},
+                     {vx, vb, vc, vd, plain(A, hb, "A"), plain(D, hb, "D"), plain(dt_bias, hb, "dt_bias"),
+                      plain(state0, sb, "state0"), plain(lens, (size_t)B * 4, "lens"),
+                      plain(grad_out, bytes_of(dtype, (double)BH * T * dv), "grad_out"), plain(grad_final, sb, "grad_final")});
+    if (st != MESA_OK) return st;
+    if ((st = ssm_pitches({vx, vb, vc})) != MESA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0) {
+        hipError_t e = copy_or_zero(grad_state, grad_final, (size_t)BH * dv * dk, s);
+        for (float* p : {grad_A, grad_D, grad_dt_bias})
+            if (e == hipSuccess) e = zero_fill(p, hb, s);
+        if (e != hipSuccess) return hip_fail(e, "gradients for T = 0");
+        return MESA_OK;
+    }
+    char* ws = static_cast<char*>(workspace);
+    mesa::SsmGradArgs a{};
+    a.f = mesa::SsmArgs{x, vx.s, b, vb.s, c, vc.s, dt, vd.s, dt_dtype == MESA_DTYPE_BF16, A, D, dt_bias, softplus, state0, lens,
+                        BH, B, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16, nullptr, nullptr, nseg,
+                        (int)((nc + nseg - 1) / nseg), reinterpret_cast<float*>(ws + l.seg),
+                        reinterpret_cast<float*>(ws + l.seg) + 2 * (size_t)BH * (nseg - 1) * dv * dk, grad_out, grad_final, grad_state, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.R)};
+    a.grad_x = grad_x;
+    a.gxs = gx.s;
+    a.grad_b = grad_b;
+    a.gbs = gb.s;
+    a.grad_c = grad_c;
+    a.gcs = gc.s;
+    a.grad_dt = grad_dt;
+    a.gdts = gd.s;
+    a.grad_A = grad_A;
+    a.grad_D = grad_D;
+    a.grad_dt_bias = grad_dt_bias;
+    a.parts = parts;
+    a.part = parts > 1 ? reinterpret_cast<float*>(ws + l.part) : nullptr;
+    a.sums = reinterpret_cast<double*>(ws + l.sums);
+    hipError_t e = timed_launch(MESA_KERNEL_SSM_STATES, s, [&] { return mesa::launch_ssm_states(a.f, s); });
+    if (e != hipSuccess) return hip_fail(e, "state space states kernel launch");
+    e = timed_launch(MESA_KERNEL_SSM_GRADS, s, [&] { return mesa::launch_ssm_grads(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "state space gradient kernel launch");
+    return MESA_OK;
+}
+
+mesa_status mesa_ssm_step(const void* x, const int64_t* x_strides, const void* b, const int64_t* b_strides, const void* c,
+                          const int64_t* c_strides, int dtype, const void* dt, const int64_t* dt_strides, int dt_dtype,
+                          const float* A, const float* D, const float* dt_bias, int softplus, float* state, int N, int Hk,
+                          int H, int dk, int dv, void* out, void* stream) {
+    g_err.clear();
+    mesa_status st = ssm_checks(dtype, dt_dtype, A, D, dt_bias, state, nullptr, N, Hk, H, 1, dk, dv, true);
+    if (st != MESA_OK) return st;
+    if (!x || !b || !c || !dt || !state || !out) return fail(MESA_ERR_INVALID_ARGUMENT, "x, b, c, dt, state and out must be non-null");
+    if (!aligned(out, 16)) return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for out)");
+    auto token = [&](const void* p, const int64_t* t, int heads, int d, int type, const char* name) {
+        const int64_t s[3] = {t ? t[0] : (int64_t)heads * d, t ? t[1] : d, 0};
+        return strided(p, s, N, heads, 1, d, type, name);
+    };
+    const View vx = token(x, x_strides, H, dv, dtype, "x"), vb = token(b, b_strides, Hk, dk, dtype, "b"),
+               vc = token(c, c_strides, Hk, dk, dtype, "c"), vd = token(dt, dt_strides, H, 1, dt_dtype, "dt");
+    const long BH = (long)N * H;
+    const size_t hb = (size_t)H * 4;
+    st = check_views({plain(out, bytes_of(dtype, (double)BH * dv), "out"), plain(state, (size_t)BH * dv * dk * sizeof(float), "state")},
+                     {vx, vb, vc, vd, plain(A, hb, "A"), plain(D, hb, "D"), plain(dt_bias, hb, "dt_bias")});
+    if (st != MESA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const mesa::SsmArgs a{x, vx.s, b, vb.s, c, vc.s, dt, vd.s, dt_dtype == MESA_DTYPE_BF16, A, D, dt_bias, softplus, nullptr,
+                          nullptr, BH, N, Hk, H, 1, dk, dv, 1, dtype == MESA_DTYPE_BF16, out, state};
+    const hipError_t e = timed_launch(MESA_KERNEL_SSM_STEP, s, [&] { return mesa::launch_ssm_step(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "state space step kernel launch");
+    return MESA_OK;
+}
+
+// ---- rotation of queries and keys ----
+mesa_status mesa_rotary_frequencies(int rot, double base, int scaling, double factor, double context, double fast, double slow,
+                                    double* freqs, float* amplitude) {
+    g_err.clear();
+    if (rot < 2 || rot % 2) return fail(MESA_ERR_INVALID_ARGUMENT, "rot=%d must be even and positive", rot);
+    if (!freqs || !amplitude) return fail(MESA_ERR_INVALID_ARGUMENT, "freqs and amplitude must be non-null");
+    if (!(base > 1.0) || std::isinf(base)) return fail(MESA_ERR_INVALID_ARGUMENT, "base must be finite and above 1");
+    if (!(factor >= 1.0) || std::isinf(factor)) return fail(MESA_ERR_INVALID_ARGUMENT, "factor must be finite and at least 1");
+    if (scaling < MESA_ROTARY_PLAIN || scaling > MESA_ROTARY_PARTS) return fail(MESA_ERR_INVALID_ARGUMENT, "scaling %d is not a mesa_rotary_scaling", scaling);
+    if (scaling == MESA_ROTARY_PLAIN && factor != 1.0) return fail(MESA_ERR_INVALID_ARGUMENT, "factor must be 1 without scaling");
+    if (scaling == MESA_ROTARY_BASE && rot < 4) return fail(MESA_ERR_INVALID_ARGUMENT, "rot=%d has no slowest pair to scale", rot);
+    if (scaling == MESA_ROTARY_PARTS && (!(context > 0.0) || std::isinf(context) || !(slow >= 0.0) || !(fast > slow) || std::isinf(fast)))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "context must be finite and > 0, fast finite and > slow >= 0");
+    if (scaling == MESA_ROTARY_BASE) base *= std::pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        const double f = std::pow(base, -2.0 * i / rot);
+        freqs[i] = f;
+        if (scaling == MESA_ROTARY_LINEAR) freqs[i] = f / factor;
+        if (scaling == MESA_ROTARY_PARTS) {
+            const double turns = context * f / 6.283185307179586477;
+            const double keep = std::min(1.0, std::max(0.0, (turns - slow) / (fast - slow)));
+            freqs[i] = f * keep + f / factor * (1.0 - keep);
+        }
+    }
+    *amplitude = scaling == MESA_ROTARY_PARTS ? (float)(1.0 + 0.1 * std::log(factor)) : 1.0f;
+    return MESA_OK;
+}
+
+static mesa_status rotate_checks(const void* q, const void* k, int dtype, const double* freqs, int rot, float amplitude,
+                                 const int64_t* positions, int64_t positions_stride, const float* wq, const float* wk, int norm,
+                                 float eps, int B, int Hq, int Hk, int T, int d) {
+    if (!dtype_ok(dtype))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "dtype %d is not MESA_DTYPE_F32 or MESA_DTYPE_BF16", dtype);
+    if (B <= 0 || Hq <= 0 || Hk < 0 || T < 0 || d <= 0)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "sizes must be positive, Hk and T >= 0 (B=%d Hq=%d Hk=%d T=%d d=%d)", B, Hq, Hk, T, d);
+    if (!freqs || (T > 0 && (!q || (Hk > 0 && !k))))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "freqs, and q and k when T > 0, must be non-null");
+    if (Hk == 0 && k) return fail(MESA_ERR_INVALID_ARGUMENT, "k is given with Hk = 0");
+    if (norm && (!(eps > 0.0f) || std::isinf(eps))) return fail(MESA_ERR_INVALID_ARGUMENT, "eps must be finite and > 0");
+    if (!norm && (wq || wk)) return fail(MESA_ERR_INVALID_ARGUMENT, "wq and wk need the norm");
+    if (wk && Hk == 0) return fail(MESA_ERR_INVALID_ARGUMENT, "wk is given with Hk = 0");
+    if (!(amplitude > 0.0f) || std::isinf(amplitude)) return fail(MESA_ERR_INVALID_ARGUMENT, "amplitude must be finite and > 0");
+    if (!aligned(freqs, 8) || !aligned(positions, 8) || !aligned(wq, 16) || !aligned(wk, 16))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (8 B for freqs and positions, 16 B for weights)");
+    if (positions && positions_stride < 0) return fail(MESA_ERR_INVALID_ARGUMENT, "positions_stride must not be negative");
+    if (!supported_d(d) && d != 256) return fail(MESA_ERR_UNSUPPORTED, "d=%d not built (16, 32, 64, 128, 256)", d);
+    if (rot < 16 || rot > d || rot % 16) return fail(MESA_ERR_UNSUPPORTED, "rot=%d not built (multiples of 16 up to d=%d)", rot, d);
+    if ((double)B * T * (d / 8) * (Hq + Hk) + 256.0 * 32 > kMaxThreads)
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B=%d T=%d heads=%d)", B, T, Hq + Hk);
+    return MESA_OK;
+}
+
+mesa_status mesa_qk_rotate(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides, int dtype,
+                           const double* freqs, int rot, int interleaved, float amplitude, const int64_t* positions,
+                           int64_t positions_stride, int64_t position0, const float* wq, const float* wk, int norm, float eps,
+                           int B, int Hq, int Hk, int T, int d, void* yq, void* yk, void* stream) {
+    g_err.clear();
+    mesa_status st = rotate_checks(q, k, dtype, freqs, rot, amplitude, positions, positions_stride, wq, wk, norm, eps, B, Hq, Hk, T, d);
+    if (st != MESA_OK) return st;
+    if (T > 0 && (!yq || (Hk > 0 && !yk))) return fail(MESA_ERR_INVALID_ARGUMENT, "yq and yk must be non-null");
+    if (!aligned(yq, 16) || !aligned(yk, 16)) return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for yq and yk)");
+    const View vq = strided(q, q_strides, B, Hq, T, d, dtype, "q"), vk = strided(k, k_strides, B, Hk, T, d, dtype, "k");
+    st = check_views({plain(yq, bytes_of(dtype, (double)B * Hq * T * d), "yq"), plain(Hk ? yk : nullptr, bytes_of(dtype, (double)B * Hk * T * d), "yk")},
+                     {vq, vk, plain(freqs, (size_t)rot * 4, "freqs"), plain(wq, (size_t)d * 4, "wq"), plain(wk, (size_t)d * 4, "wk"),
+                      plain(positions, T > 0 ? ((size_t)positions_stride * (B - 1) + T) * 8 : 0, "positions")});
+    if (st != MESA_OK) return st;
+    if (T == 0) return MESA_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const mesa::RotateArgs a{q, vq.s, k, vk.s, freqs, rot, interleaved, amplitude, positions, (long)positions_stride, (long)position0,
+                             wq, wk, norm, eps, B, Hq, Hk, T, d, dtype == MESA_DTYPE_BF16, yq, yk, 1};
+    const hipError_t e = timed_launch(MESA_KERNEL_QK_ROTATE, s, [&] { return mesa::launch_qk_rotate(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "query and key rotation kernel launch");
+    return MESA_OK;
+}
+
+size_t mesa_qk_rotate_backward_workspace_bytes(int d) {
+    return d > 0 ? (size_t)mesa::kRotateParts * 2 * d * sizeof(float) : 0;
+}
+
+mesa_status mesa_qk_rotate_backward(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides, int dtype,
+                                    const double* freqs, int rot, int interleaved, float amplitude, const int64_t* positions,
+                                    int64_t positions_stride, int64_t position0, const float* wq, const float* wk, int norm,
+                                    float eps, const void* grad_yq, const void* grad_yk, int B, int Hq, int Hk, int T, int d,
+                                    void* grad_q, const int64_t* grad_q_strides, void* grad_k, const int64_t* grad_k_strides,
+                                    float* grad_wq, float* grad_wk, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err.clear();
+    mesa_status st = rotate_checks(q, k, dtype, freqs, rot, amplitude, positions, positions_stride, wq, wk, norm, eps, B, Hq, Hk, T, d);
+    if (st != MESA_OK) return st;
+    if (T > 0 && (!grad_yq || !grad_q || (Hk > 0 && (!grad_yk || !grad_k))))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_yq, grad_yk, grad_q and grad_k must be non-null");
+    if ((wq == nullptr) != (grad_wq == nullptr) || (wk == nullptr) != (grad_wk == nullptr))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "grad_wq and grad_wk must be given exactly when wq and wk are");
+    if (!aligned(grad_yq, 16) || !aligned(grad_yk, 16) || !aligned(workspace, 16) || !aligned(grad_wq, 4) || !aligned(grad_wk, 4))
+        return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for grad_yq, grad_yk and workspace, 4 B for grad_wq and grad_wk)");
+    const size_t need = wq || wk ? mesa_qk_rotate_backward_workspace_bytes(d) : 0;
+    if (workspace_bytes < need || (need && !workspace))
+        return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace ? workspace_bytes : 0, need);
+    const View vq = strided(q, q_strides, B, Hq, T, d, dtype, "q"), vk = strided(k, k_strides, B, Hk, T, d, dtype, "k"),
+               gq = strided(grad_q, grad_q_strides, B, Hq, T, d, dtype, "grad_q"),
+               gk = strided(grad_k, grad_k_strides, B, Hk, T, d, dtype, "grad_k");
+    const size_t db = (size_t)d * 4;
+    st = check_views({gq, gk, plain(grad_wq, db, "grad_wq"), plain(grad_wk, db, "grad_wk"), plain(workspace, need, "workspace")},
+                     {vq, vk, plain(freqs, (size_t)rot * 4, "freqs"), plain(wq, db, "wq"), plain(wk, db, "wk"),
+                      plain(positions, T > 0 ? ((size_t)positions_stride * (B - 1) + T) * 8 : 0, "positions"),
+                      plain(grad_yq, bytes_of(dtype, (double)B * Hq * T * d), "grad_yq"),
+                      plain(Hk ? grad_yk : nullptr, bytes_of(dtype, (double)B * Hk * T * d), "grad_yk")});
+    if (st != MESA_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (T == 0) {
+        hipError_t e = zero_fill(grad_wq, db, s);
+        if (e == hipSuccess) e = zero_fill(grad_wk, db, s);
+        if (e != hipSuccess) return hip_fail(e, "zero fill of the weights' gradients");
+        return MESA_OK;
+    }
+    const mesa::RotateBwdArgs a{{q, vq.s, k, vk.s, freqs, rot, interleaved, amplitude, positions, (long)positions_stride,
+                                 (long)position0, wq, wk, norm, eps, B, Hq, Hk, T, d, dtype == MESA_DTYPE_BF16, nullptr, nullptr, 1},
+                                grad_yq, grad_yk, grad_q, gq.s, grad_k, gk.s, grad_wq, grad_wk, static_cast<float*>(workspace)};
+    const hipError_t e = timed_launch(MESA_KERNEL_QK_ROTATE_BWD, s, [&] { return mesa::launch_qk_rotate_bwd(a, s); });
+    if (e != hipSuccess) return hip_fail(e, "query and key rotation gradient kernel launch");
+    return MESA_OK;
+}
+
 mesa_status mesa_profile_enable(int on) {
     std::lock_guard<std::mutex> g(g_prof_mu);
     g_prof_on = on != 0;
@@ -997,7 +1515,8 @@ mesa_status mesa_profile_reset(void) {
 mesa_status mesa_profile_read(int kernel_id, double* total_ms, int64_t* launches) {
     g_err.clear();
     const bool used = (kernel_id >= 0 && kernel_id <= MESA_KERNEL_HAWK) ||
-                      (kernel_id >= MESA_KERNEL_DELTA_PREP && kernel_id < MESA_KERNEL_COUNT);
+                      (kernel_id >= MESA_KERNEL_DELTA_PREP && kernel_id <= MESA_KERNEL_RESIDUAL_NORM_BWD) ||
+                      (kernel_id >= MESA_KERNEL_CAUSAL_CONV && kernel_id < MESA_KERNEL_COUNT);
     if (!used || !total_ms || !launches)
         return fail(MESA_ERR_INVALID_ARGUMENT, "bad kernel id %d or null output", kernel_id);
     std::lock_guard<std::mutex> g(g_prof_mu);
@@ -1038,6 +1557,14 @@ const char* mesa_kernel_name(int kernel_id) {
         case MESA_KERNEL_GATE_NORM_BWD: return "gate_norm_bwd_kernels";
         case MESA_KERNEL_RESIDUAL_NORM: return "residual_norm_kernel";
         case MESA_KERNEL_RESIDUAL_NORM_BWD: return "residual_norm_bwd_kernels";
+        case MESA_KERNEL_CAUSAL_CONV: return "causal_conv_kernel";
+        case MESA_KERNEL_CAUSAL_CONV_BWD: return "causal_conv_bwd_kernels";
+        case MESA_KERNEL_SSM_SCAN: return "ssm_scan_kernels";
+        case MESA_KERNEL_SSM_STATES: return "ssm_state_passes";
+        case MESA_KERNEL_SSM_GRADS: return "ssm_grads_kernels";
+        case MESA_KERNEL_SSM_STEP: return "ssm_step_kernel";
+        case MESA_KERNEL_QK_ROTATE: return "qk_rotate_kernel";
+        case MESA_KERNEL_QK_ROTATE_BWD: return "qk_rotate_bwd_kernels";
     }
     return "unknown";
 }

@@ -165,6 +165,84 @@ hipError_t launch_gate_norm_bwd(const GateNormBwdArgs& a, hipStream_t s);
 hipError_t launch_residual_norm(const ResidualNormArgs& a, hipStream_t s);
 hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a, hipStream_t s);
 
+// Element strides of a tensor [B, heads, T, d] whose rows of d are contiguous.
+struct RowStrides { long batch, head, token; };
+
+// Short causal convolution over rows [B, T, D] (causal_conv.hip).
+constexpr int kConvRun = 32;        // tokens a thread
+constexpr int kConvMaxWidth = 4;    // widest window the kernels are built for
+struct ConvArgs {
+    const void* x; long xb; long xt;   // batch and token strides
+    const float* w; int W; const float* bias; int silu;
+    const void* hist; void* hist_out; const int32_t* lens;
+    int B; int T; int D; int bf16;
+    void* y;
+    int run; int segs;                 // set by the launch
+};
+struct ConvBwdArgs {
+    ConvArgs f;
+    const void* grad_y; void* grad_x; long gxb; long gxt; void* grad_hist;
+    float* grad_w; float* grad_bias;
+    float* partial;                    // workspace: [conv_bwd_parts][W + 1][D]
+};
+long conv_bwd_parts(long B, int T);
+hipError_t launch_causal_conv(ConvArgs a, hipStream_t s);
+hipError_t launch_causal_conv_bwd(ConvBwdArgs a, hipStream_t s);
+
+// State space scan (ssm_*.hip).
+constexpr int kSsmChunk = 64;       // tokens per chunk
+constexpr long kSsmPitch = 1L << 24;   // token strides stay below: a chunk's offsets fit 32 bits
+struct SsmArgs {
+    const void* x; RowStrides xs; const void* bm; RowStrides bs; const void* cm; RowStrides cs;
+    const void* dt; RowStrides dts; int dt_bf16;
+    const float* A; const float* D; const float* dt_bias; int softplus;
+    const float* state0; const int32_t* lens;
+    long BH; int B; int Hk; int H; int T; int dk; int dv; int nc; int bf16;
+    void* out; float* final_state;     // the step: its state
+    int nseg; int seg_chunks;          // segments of a sequence that are passed over at once, chunks of one
+    float* seg_start;                  // nseg > 1, workspace: [sides][BH][nseg - 1] states, the ends, then the next starts
+    float* seg_decay;                  // [sides][BH][nseg - 1]
+    const void* grad_out; const float* grad_final; float* grad_state;   // backward
+    float* S; float* R;                // backward workspace [BH][nc][dk][dv]: states at the chunks' starts, gradients at their ends
+};
+struct SsmGradArgs {
+    SsmArgs f;
+    void* grad_x; RowStrides gxs; void* grad_b; RowStrides gbs; void* grad_c; RowStrides gcs; void* grad_dt; RowStrides gdts;
+    float* grad_A; float* grad_D; float* grad_dt_bias;
+    int parts;       // workgroups that share the heads of one b and c
+    float* part;     // parts > 1: [parts][B Hk][2][T][dk], dC and dB
+    double* sums;    // [H][3][B nc]
+};
+constexpr int kSsmGradGroups = 512;   // workgroups of the gradients, where splitting the heads gives more
+int ssm_segments(long BH, int nc, int dv, int sides);         // the number of segments; the backward has two sides
+long ssm_segment_slots(long BH, int nc, int dv, int sides);   // the most sides BH (segments - 1) of any smaller batch and length
+int ssm_grad_parts(long B, int Hk, int H, int nc);
+hipError_t launch_ssm_scan(const SsmArgs& a, hipStream_t s);
+hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s);   // S and R
+hipError_t launch_ssm_grads(const SsmGradArgs& a, hipStream_t s);
+hipError_t launch_ssm_step(const SsmArgs& a, hipStream_t s);
+
+// Per-head norm of queries and keys and their rotation (qk_rotate.hip).
+constexpr int kRotateParts = 1024;  // workgroups of the backward, each with one partial sum of the weights' gradients
+struct RotateArgs {
+    const void* q; RowStrides qs; const void* k; RowStrides ks;
+    const double* freqs; int rot; int interleaved; float amplitude;
+    const int64_t* positions; long pos_stride; long position0;
+    const float* wq; const float* wk; int norm; float eps;
+    int B; int Hq; int Hk; int T; int d; int bf16;
+    void* yq; void* yk;
+    int slots;                         // set by the launch: rows of a token side by side
+};
+struct RotateBwdArgs {
+    RotateArgs f;
+    const void* grad_yq; const void* grad_yk;
+    void* grad_q; RowStrides gqs; void* grad_k; RowStrides gks;
+    float* grad_wq; float* grad_wk;
+    float* partial;                    // workspace: [kRotateParts][2][d]
+};
+hipError_t launch_qk_rotate(RotateArgs a, hipStream_t s);
+hipError_t launch_qk_rotate_bwd(RotateBwdArgs a, hipStream_t s);
+
 hipError_t launch_cg_output(const CgOutputArgs& a, hipStream_t s);
 hipError_t launch_cg_output_bf16(const CgOutputArgs& a, hipStream_t s);   // bf16 q/k/v, d >= 32
 hipError_t launch_qk_preprocess(const QkPreArgs& a, hipStream_t s);

@@ -1,0 +1,439 @@
+// ssm_grads.hip -- gradients of the state space scan, per chunk (gfx950).
+//
+// With a chunk's start state S (dk x dv), the gradient R of its end state, the
+// prefix sums l, L_ij = e^{l_i - l_j} (j <= i), D the step sizes and g the outputs'
+// gradients:
+//   M = g X^T,  Z = L o M diag(D),  P = L o (C B^T)
+//   dC = Z B + diag(e^l) g S^T        dB = Z^T C + diag(D e^{l_63 - l}) X R^T
+//   V = P^T g + diag(e^{l_63 - l}) B R,  dX = diag(D) V + skip g
+// A token's log decay scales every pair (i >= t > j) of E = Z o (C B^T), what is read
+// of the start state after it, what is written before it and stays to the end, and
+// the start state's way to the end:
+//   da_t = sum_{i >= t > j} E_ij + sum_{i >= t} rd_i + sum_{j < t} wr_j + e^{l_63} <S, R>
+//   rd_i = e^{l_i} c_i . S g_i,   wr_j = D_j e^{l_63 - l_j} b_j . R x_j
+// the pairs taken as prefix sums of E's column sums less its row sums, in float64.
+// Then dD_t = x_t . V_t + A da_t, and the raw step size's gradient through softplus.
+//
+// A workgroup takes one chunk and some of the heads that share b and c, so that their
+// dB and dC are summed in registers; heads of more workgroups are summed in order
+// from float32 parts.  dv goes by in pieces of 64 columns, in all of which the
+// formulas are sums.
+#include <algorithm>
+
+#include "ssm_core.h"
+
+namespace mesa {
+
+constexpr int kGradThreads = 512;
+template <int N, typename In>
+struct GradLds {
+    Plane<In, N> b, c;
+    Plane<In, 64> x, g;
+    Square<In> p;           // rows: the pairs' earlier token
+    Scalars s;
+    float decay;
+    double row[4][kSC], col[4][kSC];    // sums of E over j and of L o (C B^T) o M over i, by the other's block, without the diagonal
+    float diag[kSC], dx[kSC];           // L o (C B^T) o M on the diagonal, M there
+    float rd[N / 16][kSC], wr[N / 16][kSC];   // by 16 rows of dk
+    double carry[N / 16];
+};
+
+template <typename In>
+__device__ __forceinline__ void zero_rows(In* p, long pitch, int cols, int from, int to) {
+    for (int u = threadIdx.x; u < (to - from) * (cols / 4); u += kGradThreads)
+        store4_el(p + (from + u / (cols / 4)) * pitch + 4 * (u % (cols / 4)), f32x4{0.f, 0.f, 0.f, 0.f});
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xf, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// The sums of four values over 16 neighbouring lanes: lane m gets that of value m % 4,
+// by exchanges that halve what is left to sum.
+__device__ __forceinline__ double row_sums(const double (&v)[4], int m) {
+    const bool odd = m & 1, two = m & 2;
+    double a = odd ? v[1] : v[0], b = odd ? v[3] : v[2];
+    a += dpp_f64<0xB1>(odd ? v[0] : v[1]);      // quad_perm [1,0,3,2]
+    b += dpp_f64<0xB1>(odd ? v[2] : v[3]);
+    double c = two ? b : a;
+    c += dpp_f64<0x4E>(two ? a : b);            // quad_perm [2,3,0,1]
+    c += dpp_f64<0x124>(c);                     // row_ror 4
+    return c + dpp_f64<0x128>(c);               // row_ror 8
+}
+__device__ __forceinline__ double kslot_sum(double v) {
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+__device__ __forceinline__ float dot4(const f32x4& a, const f32x4& b) {
+    return (a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3]);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// Two pieces of a row of the chunk states as eight k-slots.
+template <typename PV>
+__device__ __forceinline__ typename PV::Three three8(const f32x4& a, const f32x4& b) {
+    float f[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return PV::three(f);
+}
+
+// Eight waves.  The pairs' ten tiles go round; then a wave takes 16 columns of dv and
+// two tiles of tokens for dX, and 16 rows of dk and N / 32 tiles of tokens for dB, dC.
+template <int N, typename In>
+__global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga) {
+    typedef Plane<In, N> PN;
+    typedef Plane<In, 64> PV;
+    constexpr int TT = N / 32;
+    __shared__ GradLds<N, In> S;
+    const SsmArgs& a = ga.f;
+    const int dk = N > 32 ? N : a.dk;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16;
+    long i0 = blockIdx.x;
+    const int part = (int)(i0 % ga.parts);
+    i0 /= ga.parts;
+    const int chunk = (int)(i0 % a.nc);
+    i0 /= a.nc;
+    const int hk = (int)(i0 % a.Hk);
+    const long b = i0 / a.Hk;
+    const int rep = a.H / a.Hk, h_first = hk * rep + (int)((long)rep * part / ga.parts),
+              h_last = hk * rep + (int)((long)rep * (part + 1) / ga.parts);
+    const long t0 = (long)chunk * kSC;
+    const int rows = (int)min((long)kSC, a.T - t0);
+    const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    const int n = (int)min((long)rows, max(0L, len - t0));   // the chunk's tokens
+    const int nt = wave % (N / 16), first = wave / (N / 16) * TT;   // the wave's rows of dk, its first tile of tokens
+    const int vt = wave % 4, half = wave / 4;                       // its columns of dv, its half of the tokens
+
+    Stage<In, 64, kGradThreads> sx, sg;
+    auto fetch = [&](int h, int v0) {
+        sx.load(static_cast<const In*>(a.x) + b * a.xs.batch + h * a.xs.head + t0 * a.xs.token + v0, a.xs.token, min(64, a.dv - v0), n);
+        sg.load(static_cast<const In*>(a.grad_out) + ((b * a.H + h) * a.T + t0) * a.dv + v0, a.dv, min(64, a.dv - v0), n);
+    };
+    f32x4 cb[2], zsum[2] = {}, dc[TT] = {}, db[TT] = {};
+    if (n > 0) {
+        {
+            Stage<In, N, kGradThreads> sb, sc;
+            sb.load(static_cast<const In*>(a.bm) + b * a.bs.batch + hk * a.bs.head + t0 * a.bs.token, a.bs.token, dk, n);
+            sc.load(static_cast<const In*>(a.cm) + b * a.cs.batch + hk * a.cs.head + t0 * a.cs.token, a.cs.token, dk, n);
+            sb.store(S.b);
+            sc.store(S.c);
+        }
+        // what is above the pairs, where products read it: six tiles
+        if (wave < 6) {
+            const int j = wave < 1 ? 1 : wave < 3 ? 2 : 3, i = wave - j * (j - 1) / 2;
+            S.p.put4(16 * j + m, 16 * i + 4 * g, f32x4{0.f, 0.f, 0.f, 0.f});
+        }
+        fetch(h_first, 0);
+        __syncthreads();
+        // C B^T: rows of tokens 16 i + 4 g + r, columns 16 j + m
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int k = min(wave + 8 * q, 9), i = tile_i(k), j = tile_j(k);
+            mma<true>(cb[q], S.c.row(i, 0, m, g), S.b.row(j, 0, m, g));
+#pragma unroll
+            for (int e = 1; e < N / 32; ++e) mma(cb[q], S.c.row(i, e, m, g), S.b.row(j, e, m, g));
+            mfma_done(cb[q]);
+        }
+    }
+    for (int h = h_first; h < h_last; ++h) {
+        const long bh = b * a.H + h;
+        In* gx = static_cast<In*>(ga.grad_x) + b * ga.gxs.batch + h * ga.gxs.head + t0 * ga.gxs.token;
+        zero_rows(gx, ga.gxs.token, a.dv, n, rows);
+        if (n == 0) {
+            if (threadIdx.x < rows) {
+                const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + threadIdx.x) * ga.gdts.token;
+                if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, 0.f);
+                else static_cast<float*>(ga.grad_dt)[o] = 0.f;
+            }
+            if (threadIdx.x < 3) ga.sums[((long)h * 3 + threadIdx.x) * a.B * a.nc + b * a.nc + chunk] = 0.0;
+            continue;
+        }
+        const float A = a.A[h], skip = a.D ? a.D[h] : 0.0f;
+        double direct = 0.0, da = 0.0, dskip = 0.0;   // wave 7: of token t's step size and log decay, of skip
+        float raw = 0.f, step = 0.f;
+        for (int v0 = 0; v0 < a.dv; v0 += 64) {
+            const int cols = min(64, a.dv - v0), v = v0 + 16 * vt;
+            const float* Rm = a.R + (bh * a.nc + chunk) * dk * a.dv;
+            const float* Sm = a.S + (bh * a.nc + chunk) * dk * a.dv;
+            sx.store(S.x);
+            sg.store(S.g);
+            if (v0 == 0 && wave == 7) {
+                raw = lane < n ? raw_step(a, b, h, t0 + lane) : 0.f;
+                step = lane < n ? step_of(raw, a.softplus) : 0.f;
+                const float d = chunk_scalars(S.s, step, A);
+                if (lane == 0) S.decay = d;
+            }
+            __syncthreads();
+            if (v0 + 64 < a.dv) fetch(h, v0 + 64);
+            else if (h + 1 < h_last) fetch(h + 1, 0);
+            // the pairs
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int lane = lane_again(), m = lane % 16, g = lane / 16, k = wave + 8 * q;
+                if (k >= 10) continue;
+                const int i = tile_i(k), j = tile_j(k), s = 16 * j + m;
+                f32x4 M;
+                mma<true>(M, S.g.row(i, 0, m, g), S.x.row(j, 0, m, g));
+                mma(M, S.g.row(i, 1, m, g), S.x.row(j, 1, m, g));
+                const float D = S.s.step[s];
+                f32x4 L;   // the pairs' decays, one exponential each
+                const double ls = S.s.l[s];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * i + 4 * g + r;
+                    L[r] = i != j || s <= t ? exp2_small(S.s.l[t] - ls) : 0.0f;
+                }
+                mfma_done(M);
+                const f32x4 P = L * cb[q];
+                S.p.put4(s, 16 * i + 4 * g, P);
+                zsum[q] += L * M * D;
+                f32x4 F = P * M;
+                if (i == j) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (s == 16 * i + 4 * g + r) {
+                            S.diag[s] = F[r];
+                            S.dx[s] = M[r];
+                            F[r] = 0.f;
+                        }
+                }
+                const double e[4] = {F[0] * D, F[1] * D, F[2] * D, F[3] * D};
+                const double col = kslot_sum(((double)F[0] + F[1]) + ((double)F[2] + F[3])), row = row_sums(e, m);
+                if (g == 0) S.col[i][s] = col;
+                if (m < 4) S.row[j][16 * i + 4 * g + m] = row;
+            }
+            __syncthreads();
+            // dX, transposed: rows of dv, columns of tokens
+            if (16 * vt < cols) {
+                const int lane = lane_again(), m = lane % 16, g = lane / 16;
+                f32x4 o[2];
+#pragma unroll
+                for (int k = 0; k < N / 32; ++k) {
+                    float f[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int row = 32 * k + 16 * (e / 4);   // and 4 g + e % 4
+                        f[e] = row < dk ? *lane_at(Rm + (row + e % 4) * a.dv + v, (4 * g * a.dv + m) * 4) : 0.f;
+                    }
+                    const typename PN::Two r2 = PN::two(f);
+                    const typename PN::One br[2] = {S.b.row(2 * half, k, m, g), S.b.row(2 * half + 1, k, m, g)};
+                    if (k == 0) mma<true>(o, r2, br);
+                    else mma(o, r2, br);
+                }
+                mfma_done(o);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) o[j] *= S.s.out[16 * (2 * half + j) + m];
+                mfma_ready(o);
+                mma(o, S.g.col(vt, 1, m, g), {S.p.row(2 * half, 1, m, g), S.p.row(2 * half + 1, 1, m, g)});
+                mma(o, S.g.col(vt, 0, m, g), {S.p.row(2 * half, 0, m, g), S.p.row(2 * half + 1, 0, m, g)});
+                mfma_done(o);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int s = 16 * (2 * half + j) + m;
+                    if (s < n) store4_el(gx + s * ga.gxs.token + v + 4 * g, o[j] * S.s.step[s] + skip * S.g.get4(s, 16 * vt + 4 * g));
+                }
+            }
+            // dC and dB of the states, transposed: rows of dk, columns of tokens
+            if (16 * nt < dk) {
+                const int lane = lane_again(), m = lane % 16, g = lane / 16;
+                f32x4 oc[TT], ob[TT], s4[4] = {}, r4[4] = {};
+                double carry = 0.0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // dv = 16, 32: zeros where nothing is
+                    if (cols <= 16 * k) continue;
+                    const int at = 16 * nt * a.dv + v0 + 16 * k, lo = (m * a.dv + 4 * g) * 4;
+                    s4[k] = load4(lane_at(Sm + at, lo));
+                    r4[k] = load4(lane_at(Rm + at, lo));
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    carry += dot4(s4[k], r4[k]);
+                }
+                typename PV::One x0[TT], x1[TT];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    x0[t] = S.g.row(first + t, 0, m, g);
+                    x1[t] = S.g.row(first + t, 1, m, g);
+                }
+                mma_pair(oc, three8<PV>(s4[0], s4[1]), x0, three8<PV>(s4[2], s4[3]), x1);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    x0[t] = S.x.row(first + t, 0, m, g);
+                    x1[t] = S.x.row(first + t, 1, m, g);
+                }
+                mma_pair(ob, three8<PV>(r4[0], r4[1]), x0, three8<PV>(r4[2], r4[3]), x1);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) {
+                    const int s = 16 * (first + t) + m;
+                    oc[t] *= S.s.in[s];
+                    ob[t] *= S.s.out[s];
+                    const float rd = kslot_sum(dot4(oc[t], S.c.get4(s, 16 * nt + 4 * g)));
+                    const float wr = kslot_sum(dot4(ob[t], S.b.get4(s, 16 * nt + 4 * g)));
+                    if (g == 0) {
+                        S.rd[nt][s] = rd;
+                        S.wr[nt][s] = wr;
+                    }
+                    dc[t] += oc[t];
+                    db[t] += ob[t] * S.s.step[s];
+                }
+                if (first == 0) {
+                    carry = wave_sum(carry);
+                    if (lane == 0) S.carry[nt] = carry;
+                }
+            }
+            __syncthreads();
+            if (wave == 7) {
+                const int bi = lane / 16;
+                double row = 0.0, col = 0.0, rdt = 0.0, wrt = 0.0, cr = 0.0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k <= bi) row += S.row[k][lane];
+                    if (k >= bi) col += S.col[k][lane];
+                }
+                for (int k = 0; k < dk / 16; ++k) {
+                    rdt += S.rd[k][lane];
+                    wrt += S.wr[k][lane];
+                    cr += S.carry[k];
+                }
+                direct += col + S.diag[lane] + wrt;
+                // before: of the tokens before t; after: of t and those that follow
+                double before = step * (col + wrt) - row, after = rdt;
+                const double own = before;
+#pragma unroll
+                for (int o = 1; o < 64; o <<= 1) {
+                    const double x = __shfl_up(before, o, 64), y = __shfl_down(after, o, 64);
+                    if (lane >= o) before += x;
+                    if (lane + o < 64) after += y;
+                }
+                da += (before - own) + after + (double)S.decay * cr;
+                dskip += lane < n ? S.dx[lane] : 0.f;
+            }
+        }
+        if (wave == 7) {
+            double draw = 0.0, dA = 0.0;
+            if (lane < n) {
+                const double dstep = direct + (double)A * da;
+                draw = a.softplus ? dstep / (1.0 + (double)expf(-raw)) : dstep;
+                dA = step * da;
+            }
+            if (lane < rows) {
+                const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + lane) * ga.gdts.token;
+                if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, (float)draw);
+                else static_cast<float*>(ga.grad_dt)[o] = (float)draw;
+            }
+            dA = wave_sum(dA);
+            dskip = wave_sum(dskip);
+            draw = wave_sum(draw);
+            if (lane < 3) ga.sums[((long)h * 3 + lane) * a.B * a.nc + b * a.nc + chunk] = lane == 0 ? dA : lane == 1 ? dskip : draw;
+        }
+    }
+    // the pairs' dC and dB over the heads' sum of Z
+    if (n > 0) {
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            if (wave + 8 * q < 10) S.p.put4(16 * tile_j(wave + 8 * q) + m, 16 * tile_i(wave + 8 * q) + 4 * g, zsum[q]);
+        __syncthreads();
+    }
+    if (16 * nt >= dk) return;
+    if (n > 0) {
+        const typename PN::One b0 = S.b.col(nt, 0, m, g), b1 = S.b.col(nt, 1, m, g);
+        const typename PN::One c0 = S.c.col(nt, 0, m, g), c1 = S.c.col(nt, 1, m, g);
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const int at = first + t;
+            mfma_ready(dc[t]);
+            mfma_ready(db[t]);
+            mma(dc[t], b0, S.p.col(at, 0, m, g));
+            mma(db[t], c1, S.p.row(at, 1, m, g));
+            mma(dc[t], b1, S.p.col(at, 1, m, g));
+            mma(db[t], c0, S.p.row(at, 0, m, g));
+            mfma_done(dc[t]);
+            mfma_done(db[t]);
+        }
+    }
+    float* pc = ga.part ? ga.part + ((long)part * a.B * a.Hk + b * a.Hk + hk) * 2 * a.T * dk : nullptr;
+    In* gc = static_cast<In*>(ga.grad_c) + b * ga.gcs.batch + hk * ga.gcs.head;
+    In* gb = static_cast<In*>(ga.grad_b) + b * ga.gbs.batch + hk * ga.gbs.head;
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int s = 16 * (first + t) + m;
+        if (s >= rows) continue;
+        const f32x4 zero{0.f, 0.f, 0.f, 0.f}, vc = s < n ? dc[t] : zero, vb = s < n ? db[t] : zero;
+        if (pc) {
+            store4(pc + (t0 + s) * dk + 16 * nt + 4 * g, vc);
+            store4(pc + (a.T + t0 + s) * dk + 16 * nt + 4 * g, vb);
+        } else {
+            store4_el(gc + (t0 + s) * ga.gcs.token + 16 * nt + 4 * g, vc);
+            store4_el(gb + (t0 + s) * ga.gbs.token + 16 * nt + 4 * g, vb);
+        }
+    }
+}
+
+// dC and dB over the parts of a group's heads, four features a thread.
+template <typename In>
+__global__ __launch_bounds__(256) void ssm_head_sums_kernel(SsmGradArgs ga) {
+    const SsmArgs& a = ga.f;
+    const long per = (long)a.T * a.dk / 4, groups = (long)a.B * a.Hk, i = (long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= groups * 2 * per) return;
+    f32x4 s{};
+    for (int p = 0; p < ga.parts; ++p) s += load4(ga.part + (p * groups * 2 * per + i) * 4);
+    const long grp = i / (2 * per), r = i % (2 * per), e = r % per;
+    const long b = grp / a.Hk, hk = grp % a.Hk, t = e / (a.dk / 4), d = e % (a.dk / 4) * 4;
+    const RowStrides& st = r < per ? ga.gcs : ga.gbs;
+    store4_el(static_cast<In*>(r < per ? ga.grad_c : ga.grad_b) + b * st.batch + hk * st.head + t * st.token + d, s);
+}
+
+// grad_A, grad_D and grad_dt_bias: a workgroup sums one of them for one head over the
+// rows and chunks.
+__global__ __launch_bounds__(256) void ssm_sums_kernel(const double* sums, long n, float* gA, float* gD, float* gbias) {
+    __shared__ double red[4];
+    const double* p = sums + (long)blockIdx.x * n;
+    double s = 0.0;
+    for (long i = threadIdx.x; i < n; i += 256) s += p[i];
+#pragma unroll
+    for (int o = 32; o; o >>= 1) s += __shfl_xor(s, o, 64);
+    if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    float* to = blockIdx.x % 3 == 0 ? gA : blockIdx.x % 3 == 1 ? gD : gbias;
+    if (to) to[blockIdx.x / 3] = (float)((red[0] + red[1]) + (red[2] + red[3]));
+}
+
+template <int N>
+static void grads_go(const SsmGradArgs& a, unsigned blocks, hipStream_t s) {
+    if (a.f.bf16) hipLaunchKernelGGL((ssm_grads_kernel<N, bf16_t>), dim3(blocks), dim3(kGradThreads), 0, s, a);
+    else hipLaunchKernelGGL((ssm_grads_kernel<N, float>), dim3(blocks), dim3(kGradThreads), 0, s, a);
+}
+
+// Workgroups that share the heads of one b and c: as many as fill the card.
+int ssm_grad_parts(long B, int Hk, int H, int nc) {
+    const long groups = B * Hk * nc;
+    return (int)std::min<long>(H / Hk, std::max(1L, kSsmGradGroups / std::max(groups, 1L)));
+}
+
+hipError_t launch_ssm_grads(const SsmGradArgs& a, hipStream_t s) {
+    const unsigned blocks = (unsigned)((long)a.f.B * a.f.Hk * a.f.nc * a.parts);
+    if (a.f.dk <= 32) grads_go<32>(a, blocks, s);
+    else if (a.f.dk <= 64) grads_go<64>(a, blocks, s);
+    else grads_go<128>(a, blocks, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.part) {
+        const long n = (long)a.f.B * a.f.Hk * 2 * a.f.T * a.f.dk / 4;
+        if (a.f.bf16) hipLaunchKernelGGL((ssm_head_sums_kernel<bf16_t>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((ssm_head_sums_kernel<float>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(ssm_sums_kernel, dim3((unsigned)(3 * a.f.H)), dim3(256), 0, s, a.sums, (long)a.f.B * a.f.nc, a.grad_A,
+                       a.grad_D, a.grad_dt_bias);
+    return hipGetLastError();
+}
+
+}  // namespace mesa

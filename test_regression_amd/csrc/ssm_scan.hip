@@ -1,0 +1,393 @@
+// ssm_scan.hip -- the state space scan over whole sequences (gfx950): the pass over
+// the chunks that writes the outputs, and the passes that only carry the state.
+//
+// A workgroup takes up to 64 columns of one head's dv and goes over the chunks of its
+// part of the sequence; a wave keeps 16 columns of the state in accumulators.  Per
+// chunk the four waves form the 64 x 64 matrix L o (C B^T) diag(D) together, through
+// LDS, while the next chunk's rows are on their way.
+#include <algorithm>
+
+#include "ssm_core.h"
+
+namespace mesa {
+
+template <int N, typename In>
+struct ScanLds {
+    Plane<In, N> b, c;
+    Plane<In, 64> x;
+    Square<In> m;
+    Scalars s;
+    float decay;
+};
+template <int N, typename In>
+struct CarryLds {
+    Plane<In, N> b;
+    Plane<In, 64> x;
+    Scalars s;
+    float decay;
+};
+
+// Where a workgroup works.
+struct SsmPlace {
+    long bh, b;
+    int h, v0, cols, seg, valid;   // first column of dv, columns, tokens of the row
+};
+__device__ __forceinline__ SsmPlace ssm_place(const SsmArgs& a, long i, int nseg) {
+    SsmPlace p;
+    const int groups = (a.dv + 63) / 64;
+    p.v0 = 64 * (int)(i % groups);
+    i /= groups;
+    p.seg = (int)(i % nseg);
+    p.bh = i / nseg;
+    p.b = p.bh / a.H;
+    p.h = (int)(p.bh % a.H);
+    p.cols = min(64, a.dv - p.v0);
+    p.valid = a.lens ? min(max(a.lens[p.b], 0), a.T) : a.T;
+    return p;
+}
+
+// Columns of rows times weights by row, in three parts: rows 32 j .. + 31.
+template <typename PV>
+__device__ __forceinline__ typename PV::Three weighted(const typename PV::One& x, const float* w, int j, int g) {
+    float f[8];
+    PV::floats(x, f);
+    const f32x4 a = row4(w, 2 * j, g), b = row4(w, 2 * j + 1, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= e < 4 ? a[e] : b[e - 4];
+    return PV::three(f);
+}
+
+// st = decay st + the rows' columns (transposed) times w, two tiles at a time.
+template <int N, bool FLIP, typename PN, typename W>
+__device__ __forceinline__ void add_outer(f32x4 (&st)[N / 16], float decay, const PN& rows, const W& w0, const W& w1, int m, int g) {
+    constexpr int H = 2;
+#pragma unroll
+    for (int h = 0; h < N / 16; h += H) {
+        typename PN::One k0[H], k1[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            k0[i] = rows.col(h + i, 0, m, g);
+            k1[i] = rows.col(h + i, 1, m, g);
+        }
+        f32x4 u[H];
+        if constexpr (FLIP) mma_pair(u, w0, k0, w1, k1);
+        else mma_pair(u, k0, w0, k1, w1);
+#pragma unroll
+        for (int i = 0; i < H; ++i) st[h + i] = st[h + i] * decay + u[i];
+    }
+}
+
+template <int N, typename In>
+__global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(SsmArgs a) {
+    const int dk = N > 32 ? N : a.dk;
+    typedef Plane<In, N> PN;
+    typedef Plane<In, 64> PV;
+    __shared__ ScanLds<N, In> S;
+    const SsmPlace p = ssm_place(a, blockIdx.x, a.nseg);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16, hk = p.h / (a.H / a.Hk);
+    const long first = (long)p.seg * a.seg_chunks * kSC;
+    const long last = min((long)a.T, first + (long)a.seg_chunks * kSC);   // the segment's tokens
+    const int chunks = first < p.valid ? (int)((min((long)p.valid, last) - first + kSC - 1) / kSC) : 0;
+    const bool mine = 16 * wave < p.cols;
+    const int v = p.v0 + 16 * wave;   // the wave's columns of dv
+    const In* xr = static_cast<const In*>(a.x) + p.b * a.xs.batch + p.h * a.xs.head + p.v0;
+    const In* br = static_cast<const In*>(a.bm) + p.b * a.bs.batch + hk * a.bs.head;
+    const In* cr = static_cast<const In*>(a.cm) + p.b * a.cs.batch + hk * a.cs.head;
+    const float A = a.A[p.h], skip = a.D ? a.D[p.h] : 0.0f;
+    In* out = static_cast<In*>(a.out) + p.bh * a.T * a.dv + v;
+
+    // the state's columns v + m, rows 16 i + 4 g + r
+    f32x4 st[N / 16] = {};
+    const float* from = p.seg == 0 ? a.state0 ? a.state0 + p.bh * a.dv * dk : nullptr
+                                   : a.seg_start + (p.bh * (a.nseg - 1) + p.seg - 1) * a.dv * dk;
+    if (from && mine)
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            if (16 * i < dk) st[i] = load4(from + (long)(v + m) * dk + 16 * i + 4 * g);
+
+    Stage<In, N> sb, sc;
+    Stage<In, 64> sx;
+    float step = 0.f;
+    auto fetch = [&](int c) {
+        const long t0 = first + (long)c * kSC;
+        const int n = (int)min((long)kSC, p.valid - t0);
+        sb.load(br + t0 * a.bs.token, a.bs.token, dk, n);
+        sc.load(cr + t0 * a.cs.token, a.cs.token, dk, n);
+        sx.load(xr + t0 * a.xs.token, a.xs.token, p.cols, n);
+        if (wave == 3) step = lane < n ? step_of(raw_step(a, p.b, p.h, t0 + lane), a.softplus) : 0.0f;
+    };
+    if (chunks > 0) {
+        fetch(0);
+        // above the diagonal blocks, where 32 columns are read
+        if (wave < 2) S.m.put4(32 * wave + m, 32 * wave + 16 + 4 * g, f32x4{0.f, 0.f, 0.f, 0.f});
+    }
+    for (int c = 0; c < chunks; ++c) {
+        const long t0 = first + (long)c * kSC;
+        sb.store(S.b);
+        sc.store(S.c);
+        sx.store(S.x);
+        if (wave == 3) {
+            const float d = chunk_scalars(S.s, step, A);
+            if (lane == 0) S.decay = d;
+        }
+        __syncthreads();
+        if (c + 1 < chunks) fetch(c + 1);
+        const Scalars& sl = S.s;
+        // L o (C B^T) diag(D), tile (i, j): lane's token i-block m, its columns 4 g ..
+        for (int k = wave; k < 10; k += 4) {
+            const int i = tile_i(k), j = tile_j(k);
+            f32x4 acc;
+            mma<true>(acc, S.b.row(j, 0, m, g), S.c.row(i, 0, m, g));
+#pragma unroll
+            for (int q = 1; q < N / 32; ++q) mma(acc, S.b.row(j, q, m, g), S.c.row(i, q, m, g));
+            mfma_done(acc);
+            const int t = 16 * i + m;
+            if (i == j) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int s = 16 * j + 4 * g + r;
+                    acc[r] = s <= t ? acc[r] * sl.step[s] * exp2_small(sl.l[t] - sl.l[s]) : 0.0f;
+                }
+            } else {
+                const float e = sl.e1[t] * block_decay(sl, i, j);
+                const f32x4 e2 = row4(sl.e2, j, g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[r] *= e * e2[r];
+            }
+            S.m.put4(t, 16 * j + 4 * g, acc);
+        }
+        // diag(e^l) C S, transposed: rows of dv, columns of tokens
+        f32x4 o[4];
+        if (mine) {
+#pragma unroll
+            for (int q = 0; q < N / 32; ++q) {
+                float f[8] = {st[2 * q][0], st[2 * q][1], st[2 * q][2], st[2 * q][3],
+                              st[2 * q + 1][0], st[2 * q + 1][1], st[2 * q + 1][2], st[2 * q + 1][3]};
+                const typename PN::Two s2 = PN::two(f);
+                const typename PN::One cr4[4] = {S.c.row(0, q, m, g), S.c.row(1, q, m, g), S.c.row(2, q, m, g), S.c.row(3, q, m, g)};
+                if (q == 0) mma<true>(o, s2, cr4);
+                else mma(o, s2, cr4);
+            }
+            mfma_done(o);
+        }
+        __syncthreads();
+        if (mine) {
+            const typename PV::One x0 = S.x.col(wave, 0, m, g), x1 = S.x.col(wave, 1, m, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] *= sl.in[16 * i + m];
+            mfma_ready(o);
+            mma(o, x0, {S.m.row(0, 0, m, g), S.m.row(1, 0, m, g), S.m.row(2, 0, m, g), S.m.row(3, 0, m, g)});
+            mma(o[2], x1, S.m.row(2, 1, m, g));
+            mma(o[3], x1, S.m.row(3, 1, m, g));
+            mfma_done(o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = 16 * i + m;
+                const f32x4 y = o[i] + skip * S.x.get4(t, 16 * wave + 4 * g);
+                if (t0 + t < p.valid) store4(out + (t0 + t) * a.dv + 4 * g, y);
+                else if (t0 + t < last) store4(out + (t0 + t) * a.dv + 4 * g, f32x4{0.f, 0.f, 0.f, 0.f});
+            }
+            // S' = e^{l_63} S + B^T diag(e^{l_63 - l} D) X
+            const auto w0 = weighted<PV>(x0, sl.write, 0, g), w1 = weighted<PV>(x1, sl.write, 1, g);
+            add_outer<N, false>(st, S.decay, S.b, w0, w1, m, g);
+        }
+        __syncthreads();
+    }
+    if (!mine) return;
+    // rows past the length (whole chunks of them)
+    for (long t = first + (long)chunks * kSC + lane / 4; t < last; t += 16)
+        store4(out + t * a.dv + 4 * (lane % 4), f32x4{0.f, 0.f, 0.f, 0.f});
+    if (a.final_state && p.seg == a.nseg - 1)
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            if (16 * i < dk) store4(a.final_state + (p.bh * a.dv + v + m) * dk + 16 * i + 4 * g, st[i]);
+}
+
+// Passes that only carry a state: S' = e^{l_63} S + a sum of weighted outer products,
+// of b and x from the front, or (BACK) of c and the outputs' gradients from the back:
+// R' = e^{l_63} R + C^T diag(e^l) g.  ENDS: the end states of all segments but the
+// last, from zero but for the first's; otherwise the states at every chunk's start
+// (BACK: the gradients of its end) for the gradients, from the segments' real starts.
+// FLIP: states as [dk][dv], a lane's rows v + 4 g + r and columns 16 i + m of dk, as
+// the gradients take them; else rows 16 i + 4 g + r of dk, column v + m.
+template <int N, typename In, bool ENDS, bool FLIP, bool BACK>
+__device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, const SsmPlace& p) {
+    const int dk = N > 32 ? N : a.dk;
+    typedef Plane<In, 64> PV;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16;
+    const int hk = p.h / (a.H / a.Hk), segs = a.nseg - 1;
+    // chunks of the segment, counted from where the pass starts
+    const int begin = p.seg * a.seg_chunks, end = min(a.nc, begin + a.seg_chunks), real = (p.valid + kSC - 1) / kSC;
+    const bool mine = 16 * wave < p.cols;
+    const int v = p.v0 + 16 * wave;
+    const RowStrides& ks = BACK ? a.cs : a.bs;
+    const In* kr = static_cast<const In*>(BACK ? a.cm : a.bm) + p.b * ks.batch + hk * ks.head;
+    const In* xr = BACK ? static_cast<const In*>(a.grad_out) + p.bh * a.T * a.dv + p.v0
+                        : static_cast<const In*>(a.x) + p.b * a.xs.batch + p.h * a.xs.head + p.v0;
+    const long xt = BACK ? a.dv : a.xs.token;
+    const float A = a.A[p.h];
+    float* seg = a.seg_start + (BACK ? a.BH * segs * a.dv * dk : 0);
+
+    f32x4 st[N / 16] = {};
+    const float* from = p.seg == 0 ? (BACK ? a.grad_final : a.state0) : nullptr;
+    if (from && mine) {
+        from += p.bh * a.dv * dk;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            if (16 * i >= dk) continue;
+            if constexpr (!FLIP) st[i] = load4(from + (long)(v + m) * dk + 16 * i + 4 * g);
+            else
+#pragma unroll
+                for (int r = 0; r < 4; ++r) st[i][r] = from[(long)(v + 4 * g + r) * dk + 16 * i + m];
+        }
+    }
+    if (!ENDS && p.seg > 0 && mine)
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            if (16 * i < dk) st[i] = load4(seg + (p.bh * segs + p.seg - 1) * a.dv * dk + (long)(16 * i + m) * a.dv + v + 4 * g);
+    Stage<In, N> sb;
+    Stage<In, 64> sx;
+    float step = 0.f;
+    // chunk of step k; from the back the row's empty chunks come first
+    auto chunk_of = [&](int k) { return BACK ? a.nc - 1 - k : k; };
+    auto fetch = [&](int k) {
+        const long t0 = (long)chunk_of(k) * kSC;
+        const int n = (int)min((long)kSC, p.valid - t0);
+        sb.load(kr + t0 * ks.token, ks.token, dk, n);
+        sx.load(xr + t0 * xt, xt, p.cols, n);
+        if (wave == 3) step = lane < n ? step_of(raw_step(a, p.b, p.h, t0 + lane), a.softplus) : 0.0f;
+    };
+    const int k0 = BACK ? max(begin, a.nc - real) : begin, k1 = BACK ? end : min(end, real);
+    if (k0 < k1) fetch(k0);
+    double total = 0.0;
+    for (int k = k0; k < k1; ++k) {
+        if (!ENDS && mine) {
+            float* to = (BACK ? a.R : a.S) + (p.bh * a.nc + chunk_of(k)) * dk * a.dv + v + 4 * g;
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i)
+                if (16 * i < dk) store4(to + (long)(16 * i + m) * a.dv, st[i]);
+        }
+        sb.store(S.b);
+        sx.store(S.x);
+        if (wave == 3) {
+            const float d = chunk_scalars(S.s, step, A);
+            if (lane == 0) S.decay = d;
+        }
+        __syncthreads();
+        if (k + 1 < k1) fetch(k + 1);
+        if (ENDS) total += S.s.l[63];
+        if (mine) {
+            const auto w0 = weighted<PV>(S.x.col(wave, 0, m, g), BACK ? S.s.in : S.s.write, 0, g);
+            const auto w1 = weighted<PV>(S.x.col(wave, 1, m, g), BACK ? S.s.in : S.s.write, 1, g);
+            add_outer<N, FLIP>(st, S.decay, S.b, w0, w1, m, g);
+        }
+        __syncthreads();
+    }
+    if (!mine) return;
+    if constexpr (ENDS) {
+        const long at = p.bh * segs + p.seg;
+        if (p.v0 == 0 && threadIdx.x == 0) a.seg_decay[(BACK ? a.BH * segs : 0) + at] = exp2_small(total);
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i) {
+            if (16 * i >= dk) continue;
+            if constexpr (FLIP) store4(seg + at * a.dv * dk + (long)(16 * i + m) * a.dv + v + 4 * g, st[i]);
+            else store4(seg + (at * a.dv + v + m) * dk + 16 * i + 4 * g, st[i]);
+        }
+    } else if (BACK && a.grad_state && p.seg == a.nseg - 1) {
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            if (16 * i < dk)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) a.grad_state[(p.bh * a.dv + v + 4 * g + r) * dk + 16 * i + m] = st[i][r];
+    }
+}
+
+template <int N, typename In>
+__global__ __launch_bounds__(256) void ssm_ends_kernel(SsmArgs a) {
+    __shared__ CarryLds<N, In> S;
+    ssm_carry<N, In, true, false, false>(a, S, ssm_place(a, blockIdx.x, a.nseg - 1));
+}
+// Both directions of the gradients side by side.
+template <int N, typename In, bool ENDS>
+__global__ __launch_bounds__(256) void ssm_states_kernel(SsmArgs a) {
+    __shared__ CarryLds<N, In> S;
+    const SsmPlace p = ssm_place(a, blockIdx.x / 2, ENDS ? a.nseg - 1 : a.nseg);
+    if (blockIdx.x % 2) ssm_carry<N, In, ENDS, true, true>(a, S, p);
+    else ssm_carry<N, In, ENDS, true, false>(a, S, p);
+}
+
+// Segments' ends, from the first's real one on, into the next segments' starts:
+// start_{s+1} = decay_s start_s + end_s, in place.
+__global__ __launch_bounds__(256) void ssm_join_kernel(float* seg, const float* decay, long n, int per, int ends) {
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;   // one of BH * per elements
+    if (i >= n) return;
+    const long bh = i / per;
+    float* p = seg + bh * ends * per + i % per;
+    float s = p[0];
+    for (int e = 1; e < ends; ++e) {
+        s = decay[bh * ends + e] * s + p[(long)e * per];
+        p[(long)e * per] = s;
+    }
+}
+
+enum SsmPass { kOut, kOutEnds, kStates, kStatesEnds };
+template <int N, typename In>
+static void scan_go(const SsmArgs& a, SsmPass pass, unsigned blocks, hipStream_t s) {
+    const dim3 grid(blocks), block(256);
+    switch (pass) {
+        case kOut: hipLaunchKernelGGL((ssm_out_kernel<N, In>), grid, block, 0, s, a); break;
+        case kOutEnds: hipLaunchKernelGGL((ssm_ends_kernel<N, In>), grid, block, 0, s, a); break;
+        case kStates: hipLaunchKernelGGL((ssm_states_kernel<N, In, false>), grid, block, 0, s, a); break;
+        case kStatesEnds: hipLaunchKernelGGL((ssm_states_kernel<N, In, true>), grid, block, 0, s, a); break;
+    }
+}
+template <int N>
+static void scan_type(const SsmArgs& a, SsmPass pass, unsigned blocks, hipStream_t s) {
+    if (a.bf16) scan_go<N, bf16_t>(a, pass, blocks, s);
+    else scan_go<N, float>(a, pass, blocks, s);
+}
+static hipError_t scan_pass(const SsmArgs& a, SsmPass pass, hipStream_t s) {
+    const long segs = pass == kOutEnds || pass == kStatesEnds ? a.nseg - 1 : a.nseg;
+    const unsigned blocks = (unsigned)(a.BH * segs * ((a.dv + 63) / 64) * (pass >= kStates ? 2 : 1));
+    if (a.dk <= 32) scan_type<32>(a, pass, blocks, s);
+    else if (a.dk <= 64) scan_type<64>(a, pass, blocks, s);
+    else scan_type<128>(a, pass, blocks, s);
+    return hipGetLastError();
+}
+// The segments' ends and from them their starts, then the pass; `sides` directions.
+static hipError_t segments(const SsmArgs& a, SsmPass ends, SsmPass pass, int sides, hipStream_t s) {
+    if (a.nseg > 1) {
+        hipError_t e = scan_pass(a, ends, s);
+        if (e != hipSuccess) return e;
+        if (a.nseg > 2) {
+            const long n = sides * a.BH * a.dv * a.dk;
+            hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.seg_start, a.seg_decay, n,
+                               a.dv * a.dk, a.nseg - 1);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+    }
+    return scan_pass(a, pass, s);
+}
+hipError_t launch_ssm_scan(const SsmArgs& a, hipStream_t s) { return segments(a, kOutEnds, kOut, 1, s); }
+hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s) { return segments(a, kStatesEnds, kStates, 2, s); }
+
+// Segments of a sequence that are passed over at once: twice as many while the
+// workgroups (of `sides` directions) stay below kSsmFill and a segment keeps
+// kSsmLeast chunks.
+constexpr long kSsmFill = 512;
+constexpr int kSsmLeast = 8, kSsmMost = 32;
+int ssm_segments(long BH, int nc, int dv, int sides) {
+    const long groups = BH * ((dv + 63) / 64) * sides;
+    int n = 1;
+    while (n < kSsmMost && groups * n < kSsmFill && nc >= 2 * kSsmLeast * n) n *= 2;
+    return n;
+}
+// n segments or more are taken by up to (kSsmFill - 1) / (n / 2) groups.
+long ssm_segment_slots(long BH, int nc, int dv, int sides) {
+    long most = 0;
+    for (int n = 2; n <= kSsmMost && nc >= kSsmLeast * n; n *= 2)
+        most = std::max(most, std::min(BH, (kSsmFill - 1) / (n / 2) / ((dv + 63) / 64 * sides)) * (n - 1));
+    return most * sides;
+}
+
+}  // namespace mesa

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,10 +21,14 @@ KERNEL_CHUNK_STATES, KERNEL_CG_OUTPUT, KERNEL_DECODE, KERNEL_QK_PREPROCESS = 0, 
 KERNEL_BWD_ADJOINT, KERNEL_BWD_STATES, KERNEL_BWD_KV, KERNEL_BWD_GATE, KERNEL_HAWK = 4, 5, 6, 7, 8
 (KERNEL_DELTA_PREP, KERNEL_DELTA_SCAN, KERNEL_DELTA_STEP, KERNEL_DELTA_BWD_SCAN, KERNEL_DELTA_GRADS, KERNEL_GATE_NORM,
  KERNEL_GATE_NORM_BWD, KERNEL_RESIDUAL_NORM, KERNEL_RESIDUAL_NORM_BWD) = range(16, 25)
+(KERNEL_CAUSAL_CONV, KERNEL_CAUSAL_CONV_BWD, KERNEL_SSM_SCAN, KERNEL_SSM_STATES, KERNEL_SSM_GRADS, KERNEL_SSM_STEP,
+ KERNEL_QK_ROTATE, KERNEL_QK_ROTATE_BWD) = range(32, 40)
+MESA_ROTARY_PLAIN, MESA_ROTARY_LINEAR, MESA_ROTARY_BASE, MESA_ROTARY_PARTS = range(4)
 MESA_WARM_COLD, MESA_WARM_PREVIOUS, MESA_WARM_PROJECTED = 0, 1, 2
 
 # Every symbol include/mesa.h declares, with its ctypes signature.
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_L, _D, _S = ctypes.c_int64, ctypes.c_double, ctypes.POINTER(ctypes.c_int64)   # _S: strides
 SIGNATURES = {
     "mesa_abi_version": ([], _I),
     "mesa_status_string": ([_I], ctypes.c_char_p),
@@ -57,6 +62,21 @@ SIGNATURES = {
     "mesa_residual_norm": ([_P, _I, _P, _I, _P, _P, _F, _I, _I, _P, _P, _P], _I),
     "mesa_residual_norm_backward_workspace_bytes": ([_I, _I], _Z),
     "mesa_residual_norm_backward": ([_P, _I, _P, _I, _P, _P, _F, _P, _P, _I, _I, _P, _P, _P, _P, _P, _Z, _P], _I),
+    "mesa_causal_conv": ([_P, _S, _I, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _P, _P], _I),
+    "mesa_causal_conv_backward_workspace_bytes": ([_I] * 4, _Z),
+    "mesa_causal_conv_backward": ([_P, _S, _I, _P, _I, _P, _I, _P, _P, _P, _I, _I, _I, _P, _S, _P, _P, _P, _P, _Z, _P], _I),
+    "mesa_ssm_workspace_bytes": ([_I] * 6, _Z),
+    "mesa_ssm_forward": ([_P, _S, _P, _S, _P, _S, _I, _P, _S, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P,
+                          _P, _Z, _P], _I),
+    "mesa_ssm_backward_workspace_bytes": ([_I] * 7, _Z),
+    "mesa_ssm_backward": ([_P, _S, _P, _S, _P, _S, _I, _P, _S, _I, _P, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                           _P, _S, _P, _S, _P, _S, _P, _S, _P, _P, _P, _P, _P, _Z, _P], _I),
+    "mesa_ssm_step": ([_P, _S, _P, _S, _P, _S, _I, _P, _S, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P], _I),
+    "mesa_rotary_frequencies": ([_I, _D, _I, _D, _D, _D, _D, ctypes.POINTER(_D), ctypes.POINTER(_F)], _I),
+    "mesa_qk_rotate": ([_P, _S, _P, _S, _I, _P, _I, _I, _F, _P, _L, _L, _P, _P, _I, _F, _I, _I, _I, _I, _I, _P, _P, _P], _I),
+    "mesa_qk_rotate_backward_workspace_bytes": ([_I], _Z),
+    "mesa_qk_rotate_backward": ([_P, _S, _P, _S, _I, _P, _I, _I, _F, _P, _L, _L, _P, _P, _I, _F, _P, _P, _I, _I, _I, _I, _I,
+                                 _P, _S, _P, _S, _P, _P, _P, _Z, _P], _I),
     "mesa_profile_enable": ([_I], _I),
     "mesa_profile_read": ([_I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int64)], _I),
     "mesa_profile_reset": ([], _I),
@@ -680,6 +700,309 @@ def mesa_residual_norm_backward(h, y, w, grad_n, scale=None, eps=1e-6, *, grad_h
                                            g["grad_h"].data_ptr(), _at(g["grad_y"]), g["grad_w"].data_ptr(),
                                            _at(g["grad_scale"]), workspace.data_ptr(), nbytes, _here(dev))
     _check(st, "mesa_residual_norm_backward")
+    return g
+
+
+@functools.lru_cache(maxsize=1024)
+def _stride_array(strides):
+    return (ctypes.c_int64 * len(strides))(*strides)
+
+
+def _strides(t):
+    """The strides of a view's leading dimensions, None for a contiguous (or absent) tensor."""
+    return None if t is None or t.is_contiguous() else _stride_array(t.stride()[:-1])
+
+
+def _views(dev, views, plain):
+    """As _tensors for the plain specs; the views' last dimension must be contiguous."""
+    for t, name, shape, _ in (*views, *plain):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    for t, name, shape, dtype in views:
+        if t is None or (t.is_cuda and t.dtype is dtype and t.device == dev and t.stride(-1) == 1):
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"the last dimension of {name} must be contiguous")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    _tensors(dev, *plain)
+
+
+def mesa_causal_conv(x, w, bias=None, hist=None, *, silu=True, lens=None, out=None, return_hist=False, hist_out=None,
+                     stream=None):
+    """Causal convolution over rows with its activation (see include/mesa.h, mesa_causal_conv).
+
+    x: [B,T,D] float32 or bfloat16, may be a slice of wider rows; w: [W,D],
+    bias: [D] float32; hist: [B,W-1,D] in x's dtype or None; lens: [B] int32 or
+    None.  Returns y, and with return_hist also hist_out, the rows for the next
+    piece; hist_out may be hist.
+    """
+    import torch
+    B, T, D = _dims(x, "x", 3)
+    W = _dims(w, "w", 2)[0]
+    dev, dt, f32, rows = x.device, x.dtype, torch.float32, (B, W - 1, D)
+    code = _qkv_dtype(x)
+    _views(dev, [(x, "x", (B, T, D), dt)],
+           [(w, "w", (W, D), f32), (bias, "bias", (D,), f32), (hist, "hist", rows, dt), (lens, "lens", (B,), torch.int32),
+            (out, "out", (B, T, D), dt), (hist_out, "hist_out", rows, dt)])
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((B, T, D), dtype=dt, device=dev)
+        if return_hist and hist_out is None:
+            hist_out = torch.empty(rows, dtype=dt, device=dev)
+        st = lib().mesa_causal_conv(x.data_ptr(), _strides(x), code, w.data_ptr(), W, _at(bias), int(silu), _at(hist),
+                                    _at(hist_out), _at(lens), B, T, D, out.data_ptr(), _here(dev))
+    _check(st, "mesa_causal_conv")
+    return (out, hist_out) if return_hist else out
+
+
+def mesa_causal_conv_backward(x, w, grad_y, bias=None, hist=None, *, silu=True, lens=None, grad_x=None, workspace=None,
+                              stream=None):
+    """Gradients of mesa_causal_conv from its inputs and grad_y [B,T,D].  Returns a
+    dict of grad_x (into the view passed in, if any), grad_w, grad_bias and
+    grad_hist (None without a bias, a history)."""
+    import torch
+    B, T, D = _dims(x, "x", 3)
+    W = _dims(w, "w", 2)[0]
+    dev, dt, f32, rows = x.device, x.dtype, torch.float32, (B, W - 1, D)
+    code = _qkv_dtype(x)
+    _views(dev, [(x, "x", (B, T, D), dt), (grad_x, "grad_x", (B, T, D), dt)],
+           [(w, "w", (W, D), f32), (bias, "bias", (D,), f32), (hist, "hist", rows, dt), (lens, "lens", (B,), torch.int32),
+            (grad_y, "grad_y", (B, T, D), dt)])
+    with _on(dev, stream):
+        g = dict(grad_x=torch.empty((B, T, D), dtype=dt, device=dev) if grad_x is None else grad_x, grad_w=torch.empty_like(w),
+                 grad_bias=None if bias is None else torch.empty_like(bias),
+                 grad_hist=None if hist is None else torch.empty_like(hist))
+        L = lib()
+        workspace, nbytes = _scratch(workspace, L.mesa_causal_conv_backward_workspace_bytes(B, T, D, W), dev)
+        st = L.mesa_causal_conv_backward(x.data_ptr(), _strides(x), code, w.data_ptr(), W, _at(bias), int(silu), _at(hist),
+                                         _at(lens), grad_y.data_ptr(), B, T, D, g["grad_x"].data_ptr(), _strides(g["grad_x"]),
+                                         g["grad_w"].data_ptr(), _at(g["grad_bias"]), _at(g["grad_hist"]),
+                                         workspace.data_ptr(), nbytes, _here(dev))
+    _check(st, "mesa_causal_conv_backward")
+    return g
+
+
+def _gate(t, name, shape, dtype):
+    """The spec of a tensor with one element a head and token, of any strides, as a view."""
+    return None if t is None else t.unsqueeze(-1), name, (*shape, 1), dtype
+
+
+def _ssm_sizes(x, b, ndim):
+    """(B or N, Hk, H, the token axis, dk, dv) of a state space call."""
+    B, H, *t, dv = _dims(x, "x", ndim)
+    _, Hk, *_, dk = _dims(b, "b", ndim)
+    if H % Hk if Hk else H:
+        raise ValueError(f"{H} heads are not a multiple of the {Hk} of b and c")
+    return B, Hk, H, t, dk, dv
+
+
+def _ssm_checks(x, b, c, dt, A, D, dt_bias, state, tokens, Hk, H, dk, dv, views=(), plain=()):
+    """Checks the tensors of a state space call, of `tokens` (B, T) or (N,); returns
+    (device, dtype, its code, dt's code)."""
+    import torch
+    dev, ty, f32 = x.device, x.dtype, torch.float32
+    codes = _qkv_dtype(x), _qkv_dtype(dt)
+    B, *T = tokens
+    shared, gates = (B, Hk, *T, dk), (B, H, *T)
+    if dt.dim() != len(gates):
+        raise ValueError(f"dt must have {len(gates)} dimensions, got shape {list(dt.shape)}")
+    _views(dev, [(x, "x", (B, H, *T, dv), ty), (b, "b", shared, ty), (c, "c", shared, ty), _gate(dt, "dt", gates, dt.dtype), *views],
+           [(A, "A", (H,), f32), (D, "D", (H,), f32), (dt_bias, "dt_bias", (H,), f32), (state, "state", (B, H, dv, dk), f32),
+            *plain])
+    return (dev, ty, *codes)
+
+
+def _gate_strides(t):
+    """All strides of a tensor whose rows are single elements."""
+    return None if t.is_contiguous() else _stride_array(t.stride())
+
+
+def mesa_ssm_workspace_bytes(B, H, T, dk, dv, dtype) -> int:
+    return int(lib().mesa_ssm_workspace_bytes(B, H, T, dk, dv, dtype))
+
+
+def mesa_ssm_forward(x, b, c, dt, A, D=None, dt_bias=None, state=None, *, softplus=True, lens=None, out=None,
+                     return_final=False, final_state=None, workspace=None, stream=None):
+    """Selective state space scan over a sequence (see include/mesa.h, mesa_ssm_forward).
+
+    x: [B,H,T,dv]; b, c: [B,Hk,T,dk] (float32 or bfloat16, same dtype; H a
+    multiple of Hk); dt: [B,H,T] float32 or bfloat16; all of them may be views,
+    such as slices of a convolution's rows [B,T,..] transposed to heads.  A, D,
+    dt_bias: [H] float32; state: [B,H,dv,dk] float32 or None; lens: [B] int32 or
+    None.  Returns (out [B,H,T,dv] in x's dtype, final_state [B,H,dv,dk] or
+    None); final_state may be the state passed in.
+    """
+    import torch
+    B, Hk, H, (T,), dk, dv = _ssm_sizes(x, b, 4)
+    f32, states = torch.float32, (B, H, dv, dk)
+    dev, ty, code, dt_code = _ssm_checks(
+        x, b, c, dt, A, D, dt_bias, state, (B, T), Hk, H, dk, dv,
+        plain=[(lens, "lens", (B,), torch.int32), (out, "out", (B, H, T, dv), x.dtype), (final_state, "final_state", states, f32)])
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((B, H, T, dv), dtype=ty, device=dev)
+        if return_final and final_state is None:
+            final_state = torch.empty(states, dtype=f32, device=dev)
+        L = lib()
+        need = L.mesa_ssm_workspace_bytes(B, H, T, dk, dv, code)
+        ws, nbytes = (None, 0) if workspace is None and not need else _scratch(workspace, need, dev)
+        st = L.mesa_ssm_forward(x.data_ptr(), _strides(x), b.data_ptr(), _strides(b), c.data_ptr(), _strides(c), code,
+                                dt.data_ptr(), _gate_strides(dt), dt_code, A.data_ptr(), _at(D), _at(dt_bias), int(softplus),
+                                _at(state), _at(lens), B, Hk, H, T, dk, dv, out.data_ptr(), _at(final_state), _at(ws), nbytes,
+                                _here(dev))
+    _check(st, "mesa_ssm_forward")
+    return out, final_state
+
+
+def mesa_ssm_backward_workspace_bytes(B, Hk, H, T, dk, dv, dtype) -> int:
+    return int(lib().mesa_ssm_backward_workspace_bytes(B, Hk, H, T, dk, dv, dtype))
+
+
+def mesa_ssm_backward(x, b, c, dt, A, grad_out, D=None, dt_bias=None, state=None, *, softplus=True, lens=None,
+                      grad_final=None, grad_x=None, grad_b=None, grad_c=None, grad_dt=None, workspace=None, stream=None):
+    """Gradients of mesa_ssm_forward (see include/mesa.h, mesa_ssm_backward).
+
+    grad_out: [B,H,T,dv] in x's dtype; grad_final: [B,H,dv,dk] float32 or None.
+    grad_x, grad_b, grad_c and grad_dt may be views to write into, such as slices
+    of the gradient of a convolution's rows.  Returns a dict of them and of
+    grad_A, grad_D, grad_dt_bias [H] and grad_state (None without D, dt_bias, a
+    state).
+    """
+    import torch
+    B, Hk, H, (T,), dk, dv = _ssm_sizes(x, b, 4)
+    f32, states, rows, shared, gates = torch.float32, (B, H, dv, dk), (B, H, T, dv), (B, Hk, T, dk), (B, H, T)
+    ty = x.dtype
+    dev, ty, code, dt_code = _ssm_checks(
+        x, b, c, dt, A, D, dt_bias, state, (B, T), Hk, H, dk, dv,
+        [(grad_x, "grad_x", rows, ty), (grad_b, "grad_b", shared, ty), (grad_c, "grad_c", shared, ty),
+         _gate(grad_dt, "grad_dt", gates, dt.dtype)],
+        [(lens, "lens", (B,), torch.int32), (grad_out, "grad_out", rows, ty), (grad_final, "grad_final", states, f32)])
+    with _on(dev, stream):
+        def out(t, shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=dev) if t is None else t
+        g = dict(grad_x=out(grad_x, rows, ty), grad_b=out(grad_b, shared, ty), grad_c=out(grad_c, shared, ty),
+                 grad_dt=out(grad_dt, gates, dt.dtype), grad_A=torch.empty_like(A), grad_D=None if D is None else torch.empty_like(D),
+                 grad_dt_bias=None if dt_bias is None else torch.empty_like(dt_bias),
+                 grad_state=None if state is None else torch.empty_like(state))
+        L = lib()
+        workspace, nbytes = _scratch(workspace, L.mesa_ssm_backward_workspace_bytes(B, Hk, H, T, dk, dv, code), dev)
+        st = L.mesa_ssm_backward(x.data_ptr(), _strides(x), b.data_ptr(), _strides(b), c.data_ptr(), _strides(c), code,
+                                 dt.data_ptr(), _gate_strides(dt), dt_code, A.data_ptr(), _at(D), _at(dt_bias), int(softplus),
+                                 _at(state), _at(lens), grad_out.data_ptr(), _at(grad_final), B, Hk, H, T, dk, dv,
+                                 g["grad_x"].data_ptr(), _strides(g["grad_x"]), g["grad_b"].data_ptr(), _strides(g["grad_b"]),
+                                 g["grad_c"].data_ptr(), _strides(g["grad_c"]), g["grad_dt"].data_ptr(),
+                                 _gate_strides(g["grad_dt"]), g["grad_A"].data_ptr(), _at(g["grad_D"]), _at(g["grad_dt_bias"]),
+                                 _at(g["grad_state"]), workspace.data_ptr(), nbytes, _here(dev))
+    _check(st, "mesa_ssm_backward")
+    return g
+
+
+def mesa_ssm_step(x, b, c, dt, A, state, D=None, dt_bias=None, *, softplus=True, out=None, stream=None):
+    """One token of the state space scan (see include/mesa.h, mesa_ssm_step); state
+    [N,H,dv,dk] float32 is updated in place.
+
+    x: [N,H,dv]; b, c: [N,Hk,dk]; dt: [N,H]; views as in mesa_ssm_forward.
+    Returns out [N,H,dv].
+    """
+    import torch
+    N, Hk, H, _, dk, dv = _ssm_sizes(x, b, 3)
+    dev, ty, code, dt_code = _ssm_checks(x, b, c, dt, A, D, dt_bias, state, (N,), Hk, H, dk, dv,
+                                         plain=[(out, "out", (N, H, dv), x.dtype)])
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((N, H, dv), dtype=ty, device=dev)
+        st = lib().mesa_ssm_step(x.data_ptr(), _strides(x), b.data_ptr(), _strides(b), c.data_ptr(), _strides(c), code,
+                                 dt.data_ptr(), _gate_strides(dt), dt_code, A.data_ptr(), _at(D), _at(dt_bias), int(softplus),
+                                 state.data_ptr(), N, Hk, H, dk, dv, out.data_ptr(), _here(dev))
+    _check(st, "mesa_ssm_step")
+    return out
+
+
+def mesa_rotary_frequencies(rot, base=10000.0, scaling=MESA_ROTARY_PLAIN, factor=1.0, context=0.0, fast=32.0, slow=1.0, *,
+                            device="cuda"):
+    """(freqs [rot/2] float64 on `device`, amplitude) for mesa_qk_rotate (see
+    include/mesa.h, mesa_rotary_frequencies); the scalings are MESA_ROTARY_*."""
+    import torch
+    freqs, amplitude = (ctypes.c_double * max(int(rot) // 2, 1))(), ctypes.c_float()
+    _check(lib().mesa_rotary_frequencies(int(rot), base, scaling, factor, context, fast, slow, freqs, ctypes.byref(amplitude)),
+           "mesa_rotary_frequencies")
+    return torch.tensor(list(freqs), dtype=torch.float64).to(device), amplitude.value
+
+
+def _rotate_checks(q, k, freqs, positions, wq, wk, views=lambda *heads: (), plain=lambda *heads: ()):
+    """Checks a rotation's tensors; `views` and `plain` give more specs from the rows'
+    shapes.  Returns (B, Hq, Hk, T, d, rot, device, dtype, its code, positions' batch stride)."""
+    import torch
+    B, Hq, T, d = _dims(q, "q", 4)
+    Hk = 0 if k is None else _dims(k, "k", 4)[1]
+    rot = 2 * _dims(freqs, "freqs", 1)[0]
+    dev, ty, f32 = q.device, q.dtype, torch.float32
+    code = _qkv_dtype(q)
+    shared = positions is not None and positions.dim() == 1
+    rows = (B, Hq, T, d), (B, Hk, T, d)
+    _views(dev, [(q, "q", rows[0], ty), (k, "k", rows[1], ty), *views(*rows)],
+           [(freqs, "freqs", (rot // 2,), torch.float64), (wq, "wq", (d,), f32), (wk, "wk", (d,), f32),
+            (positions, "positions", (T,) if shared else (B, T), torch.int64), *plain(*rows)])
+    return B, Hq, Hk, T, d, rot, dev, ty, code, 0 if shared or positions is None else T
+
+
+def mesa_qk_rotate(q, k, freqs, positions=None, wq=None, wk=None, *, norm=True, eps=1e-6, interleaved=False, amplitude=1.0,
+                   position0=0, out_q=None, out_k=None, stream=None):
+    """Per-head RMS norm of queries and keys and their rotation (see include/mesa.h, mesa_qk_rotate).
+
+    q: [B,Hq,T,d], k: [B,Hk,T,d] or None (float32 or bfloat16; may be views);
+    freqs: [rot/2] float64 (mesa_rotary_frequencies); positions: [B,T] or [T]
+    int64, or None for position0 + t; wq, wk: [d] float32 or None.  Returns
+    (yq, yk), contiguous; yk is None without k.
+    """
+    import torch
+    B, Hq, Hk, T, d, rot, dev, ty, code, ps = _rotate_checks(
+        q, k, freqs, positions, wq, wk, plain=lambda hq, hk: ((out_q, "out_q", hq, q.dtype), (out_k, "out_k", hk, q.dtype)))
+    with _on(dev, stream):
+        if out_q is None:
+            out_q = torch.empty((B, Hq, T, d), dtype=ty, device=dev)
+        if k is not None and out_k is None:
+            out_k = torch.empty((B, Hk, T, d), dtype=ty, device=dev)
+        st = lib().mesa_qk_rotate(q.data_ptr(), _strides(q), _at(k), _strides(k), code, freqs.data_ptr(), rot, int(interleaved),
+                                  amplitude, _at(positions), ps, position0, _at(wq), _at(wk), int(norm), eps, B, Hq, Hk, T, d,
+                                  out_q.data_ptr(), _at(out_k), _here(dev))
+    _check(st, "mesa_qk_rotate")
+    return out_q, out_k
+
+
+def mesa_qk_rotate_backward(q, k, grad_yq, grad_yk, freqs, positions=None, wq=None, wk=None, *, norm=True, eps=1e-6,
+                            interleaved=False, amplitude=1.0, position0=0, grad_q=None, grad_k=None, workspace=None,
+                            stream=None):
+    """Gradients of mesa_qk_rotate from its inputs and grad_yq, grad_yk.  grad_q and
+    grad_k may be views to write into.  Returns a dict of them and of grad_wq,
+    grad_wk (None where the weights are)."""
+    import torch
+    B, Hq, Hk, T, d, rot, dev, ty, code, ps = _rotate_checks(
+        q, k, freqs, positions, wq, wk, lambda hq, hk: ((grad_q, "grad_q", hq, q.dtype), (grad_k, "grad_k", hk, q.dtype)),
+        lambda hq, hk: ((grad_yq, "grad_yq", hq, q.dtype), (grad_yk, "grad_yk", hk, q.dtype)))
+    if (k is None) != (grad_yk is None):
+        raise ValueError("grad_yk must be given exactly when k is")
+    with _on(dev, stream):
+        if grad_q is None:
+            grad_q = torch.empty((B, Hq, T, d), dtype=ty, device=dev)
+        if k is not None and grad_k is None:
+            grad_k = torch.empty((B, Hk, T, d), dtype=ty, device=dev)
+        g = dict(grad_q=grad_q, grad_k=grad_k, grad_wq=None if wq is None else torch.empty_like(wq),
+                 grad_wk=None if wk is None else torch.empty_like(wk))
+        L = lib()
+        need = L.mesa_qk_rotate_backward_workspace_bytes(d) if wq is not None or wk is not None else 0
+        ws, nbytes = (None, 0) if workspace is None and not need else _scratch(workspace, need, dev)
+        st = L.mesa_qk_rotate_backward(q.data_ptr(), _strides(q), _at(k), _strides(k), code, freqs.data_ptr(), rot,
+                                       int(interleaved), amplitude, _at(positions), ps, position0, _at(wq), _at(wk), int(norm),
+                                       eps, grad_yq.data_ptr(), _at(grad_yk), B, Hq, Hk, T, d, grad_q.data_ptr(),
+                                       _strides(grad_q), _at(grad_k), _strides(grad_k), _at(g["grad_wq"]), _at(g["grad_wk"]),
+                                       _at(ws), nbytes, _here(dev))
+    _check(st, "mesa_qk_rotate_backward")
     return g
 
 
