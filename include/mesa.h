@@ -544,7 +544,7 @@ mesa_status mesa_causal_conv_backward(const void *x, const int64_t *x_strides, i
  *   workspace                   at least mesa_ssm_workspace_bytes(...) (0 where
  *                               none is needed), which never decreases with B, H
  *                               or T
- * dk and dv in {16, 32, 64, 128}, T >= 0, token strides of x, b and c below 2^24.
+ * dk and dv in {16, 32, 64, 128}, T >= 0, token strides of x, b and c below 2^23.
  * Sums and states are float32, prefix sums of the decays float64.  Rows stored as bfloat16 enter the products exactly; what
  * is formed in float32 enters as two bfloat16 parts where only bfloat16 outputs
  * follow (2^-18 of a term) and as three (2^-27) where the state does.  Values are

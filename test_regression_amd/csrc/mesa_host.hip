@@ -1199,7 +1199,7 @@ static mesa_status ssm_checks(int dtype, int dt_dtype, const float* A, const flo
 static mesa_status ssm_pitches(std::initializer_list<View> views) {
     for (const View& v : views)
         if (v.T > 1 && v.s.token >= mesa::kSsmPitch)
-            return fail(MESA_ERR_UNSUPPORTED, "token stride of %s not built (2^24 elements or more)", v.name);
+            return fail(MESA_ERR_UNSUPPORTED, "token stride of %s not built (2^23 elements or more)", v.name);
     return MESA_OK;
 }
 

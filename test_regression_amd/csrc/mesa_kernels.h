@@ -191,7 +191,7 @@ hipError_t launch_causal_conv_bwd(ConvBwdArgs a, hipStream_t s);
 
 // State space scan (ssm_*.hip).
 constexpr int kSsmChunk = 64;       // tokens per chunk
-constexpr long kSsmPitch = 1L << 24;   // token strides stay below: a chunk's offsets fit 32 bits
+constexpr long kSsmPitch = 1L << 23;   // token strides stay below: a chunk's offsets fit 32 bits
 struct SsmArgs {
     const void* x; RowStrides xs; const void* bm; RowStrides bs; const void* cm; RowStrides cs;
     const void* dt; RowStrides dts; int dt_bf16;

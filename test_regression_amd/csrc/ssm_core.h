@@ -287,25 +287,28 @@ template <> struct Square<float> {
 };
 
 // 64 rows of W columns on their way into a plane, by the workgroup's threads: units of
-// eight columns.  Columns `cols` and up and rows `valid` and up are zeros.
+// eight columns.  The loads' bounds make zeros of rows `valid` and up and of columns
+// `cols` and up, without instructions for it.
 template <typename In, int W, int THREADS = 256>
 struct Stage {
     static constexpr int per_row = W / 8, n = (kSC * per_row + THREADS - 1) / THREADS, parts = sizeof(In) / 2;
+    uint32_t at[n];
     u32x4 raw[n][parts];
     static __device__ __forceinline__ int row(int i) { return ((int)threadIdx.x + THREADS * i) / per_row; }
     static __device__ __forceinline__ int col(int i) { return 8 * (((int)threadIdx.x + THREADS * i) % per_row); }
+    // `pitch` (below kSsmPitch) between the rows
+    __device__ __forceinline__ Stage(long pitch, int cols) {
+#pragma unroll
+        for (int i = 0; i < n; ++i)
+            at[i] = row(i) < kSC && col(i) < cols ? ((uint32_t)row(i) * (uint32_t)pitch + col(i)) * (uint32_t)sizeof(In) : 1u << 31;
+    }
     __device__ __forceinline__ void load(const In* p, long pitch, int cols, int valid) {
+        const int bytes = ((valid - 1) * (int)pitch + cols) * (int)sizeof(In);
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<In*>(p), (short)0, bytes, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-            const int r = row(i), c = col(i);
-            const bool on = r < valid && c < cols;
-            const In* s = lane_at(p, ((uint32_t)r * (uint32_t)pitch + c) * sizeof(In));   // pitch below kSsmPitch
+        for (int i = 0; i < n; ++i)
 #pragma unroll
-            for (int q = 0; q < parts; ++q) {
-                raw[i][q] = u32x4{0u, 0u, 0u, 0u};
-                if (on) raw[i][q] = __builtin_bit_cast(u32x4, reinterpret_cast<const u32x4_el*>(s)[q]);
-            }
-        }
+            for (int q = 0; q < parts; ++q) raw[i][q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at[i] + 16 * q, 0, 0));
     }
     __device__ __forceinline__ void store(Plane<In, W>& P) const {
 #pragma unroll
@@ -325,6 +328,7 @@ struct Scalars {
     float in[kSC];        // 2^(l_t): from the chunk's start
     float out[kSC];       // 2^(l_63 - l_t): to its end
     float write[kSC];     // that times D_t
+    float decay;          // 2^(l_63)
 };
 
 // 2^x for x <= 0, to the instruction's rounding: what is left after the nearest whole
@@ -344,18 +348,30 @@ __device__ __forceinline__ float raw_step(const SsmArgs& a, long b, int h, long 
     return a.dt_bias ? x + a.dt_bias[h] : x;
 }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, true);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over the lanes up to one's own.
+__device__ __forceinline__ double prefix_sum(double x) {
+    x = dpp_add<0x111, 0xf>(x);   // row_shr 1, 2, 4, 8
+    x = dpp_add<0x112, 0xf>(x);
+    x = dpp_add<0x114, 0xf>(x);
+    x = dpp_add<0x118, 0xf>(x);
+    x = dpp_add<0x142, 0xa>(x);   // row_bcast15: rows 0 and 2 into 1 and 3
+    return dpp_add<0x143, 0xc>(x);   // row_bcast31: the lower half into the upper
+}
+
 // By a whole wave, lane t for token t of the chunk (step 0 past the row's end).  The
 // log decay of one token counts as at least -2^14 powers of two, which float32 has
-// as 0; a NaN stays one.  Returns 2^(l_63).
-__device__ __forceinline__ float chunk_scalars(Scalars& s, float step, float A) {
+// as 0; a NaN stays one.
+__device__ __forceinline__ void chunk_scalars(Scalars& s, float step, float A) {
     const int t = threadIdx.x % 64;
     double x = (double)step * (double)A * 1.4426950408889634;
-    x = x < -16384.0 ? -16384.0 : x;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_up(x, o, 64);
-        if (t >= o) x += y;
-    }
+    x = prefix_sum(x < -16384.0 ? -16384.0 : x);
     const double before = __shfl(x, t < 16 ? 0 : (t & 48) - 1, 64), after = __shfl(x, t | 15, 64), end = __shfl(x, 63, 64);
     s.l[t] = x;
     s.e1[t] = exp2_small(x - (t < 16 ? 0.0 : before));
@@ -365,7 +381,7 @@ __device__ __forceinline__ float chunk_scalars(Scalars& s, float step, float A) 
     const float out = exp2_small(end - x);
     s.out[t] = out;
     s.write[t] = out * step;
-    return exp2_small(end);
+    if (t == 63) s.decay = exp2_small(x);
 }
 
 // 2^(l before row block i - l at the end of row block j), j < i

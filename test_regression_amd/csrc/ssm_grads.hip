@@ -25,13 +25,49 @@
 namespace mesa {
 
 constexpr int kGradThreads = 512;
+// Whether the next head's values, gradients and scalars have their own place to go to
+// while those of this one are read: all but the widest float32 rows, which fill the LDS.
+template <int N, typename In> constexpr int kGradBuffers = sizeof(In) == 4 && N == 128 ? 1 : 2;
+
+// A state's rows of dk by 64 columns of dv: two parts, or float32.
+template <typename In, int N> struct StatePlane;
+template <int N> struct StatePlane<bf16_t, N> {
+    static constexpr int pitch = Plane<bf16_t, 64>::pitch;
+    uint32_t w[2][N * pitch];
+    __device__ __forceinline__ void put(int n, int g, int k, const B3 (&s)[2]) {   // columns 16 k + 4 g ..
+        const u32x4 h = __builtin_bit_cast(u32x4, s[k / 2].h), l = __builtin_bit_cast(u32x4, s[k / 2].m);
+        const int at = n * pitch + perm32(16 * k + 4 * g) / 2, o = 2 * (k % 2);
+        *reinterpret_cast<uint2*>(&w[0][at]) = make_uint2(h[o], h[o + 1]);
+        *reinterpret_cast<uint2*>(&w[1][at]) = make_uint2(l[o], l[o + 1]);
+    }
+    // columns 16 i + m as rows, over rows 32 j ..
+    __device__ __forceinline__ B2 col(int i, int j, int m, int g) const {
+        return B2{__builtin_bit_cast(bf16x8, col_operand(w[0], pitch, i, j, m, g)),
+                  __builtin_bit_cast(bf16x8, col_operand(w[1], pitch, i, j, m, g))};
+    }
+};
+template <int N> struct StatePlane<float, N> {
+    static constexpr int pitch = N == 128 ? 64 : 68;   // 68 spreads the reads over the banks, and does not fit
+    float w[N * pitch];
+    __device__ __forceinline__ void put(int n, int g, int k, const F8 (&s)[2]) {
+        const float* v = s[k / 2].v + 4 * (k % 2);
+        *reinterpret_cast<f32x4*>(w + n * pitch + 16 * k + 4 * g) = f32x4{v[0], v[1], v[2], v[3]};
+    }
+    __device__ __forceinline__ F8 col(int i, int j, int m, int g) const {
+        F8 r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.v[e] = w[(32 * j + 4 * g + e % 4 + 16 * (e / 4)) * pitch + 16 * i + m];
+        return r;
+    }
+};
+
 template <int N, typename In>
 struct GradLds {
     Plane<In, N> b, c;
-    Plane<In, 64> x, g;
+    Plane<In, 64> x[kGradBuffers<N, In>], g[kGradBuffers<N, In>];
     Square<In> p;           // rows: the pairs' earlier token
-    Scalars s;
-    float decay;
+    StatePlane<In, N> r;
+    Scalars s[kGradBuffers<N, In>];     // of this head and the next
     double row[4][kSC], col[4][kSC];    // sums of E over j and of L o (C B^T) o M over i, by the other's block, without the diagonal
     float diag[kSC], dx[kSC];           // L o (C B^T) o M on the diagonal, M there
     float rd[N / 16][kSC], wr[N / 16][kSC];   // by 16 rows of dk
@@ -83,13 +119,16 @@ __device__ __forceinline__ typename PV::Three three8(const f32x4& a, const f32x4
     return PV::three(f);
 }
 
-// Eight waves.  The pairs' ten tiles go round; then a wave takes 16 columns of dv and
-// two tiles of tokens for dX, and 16 rows of dk and N / 32 tiles of tokens for dB, dC.
+// Eight waves.  The pairs' ten tiles go round; a wave takes 16 rows of dk and N / 32
+// tiles of tokens for dB and dC, and leaves the rows of R in LDS; then it takes 16
+// columns of dv and two tiles of tokens for dX, while wave 7 sums up the tokens' decays
+// and forms the next head's scalars.  The next piece's rows and states are on their way
+// from the middle of a piece to the middle of the next.
 template <int N, typename In>
 __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga) {
     typedef Plane<In, N> PN;
     typedef Plane<In, 64> PV;
-    constexpr int TT = N / 32;
+    constexpr int TT = N / 32, buffers = kGradBuffers<N, In>;
     __shared__ GradLds<N, In> S;
     const SsmArgs& a = ga.f;
     const int dk = N > 32 ? N : a.dk;
@@ -109,27 +148,58 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
     const int n = (int)min((long)rows, max(0L, len - t0));   // the chunk's tokens
     const int nt = wave % (N / 16), first = wave / (N / 16) * TT;   // the wave's rows of dk, its first tile of tokens
     const int vt = wave % 4, half = wave / 4;                       // its columns of dv, its half of the tokens
+    const int cols = min(64, a.dv), pieces = (a.dv + 63) / 64;      // a piece: 64 columns of a head's dv, or all
+    const int all = (h_last - h_first) * pieces;
+    auto head = [&](int k) { return h_first + k / pieces; };
+    auto column = [&](int k) { return 64 * (k % pieces); };
 
-    Stage<In, 64, kGradThreads> sx, sg;
-    auto fetch = [&](int h, int v0) {
-        sx.load(static_cast<const In*>(a.x) + b * a.xs.batch + h * a.xs.head + t0 * a.xs.token + v0, a.xs.token, min(64, a.dv - v0), n);
-        sg.load(static_cast<const In*>(a.grad_out) + ((b * a.H + h) * a.T + t0) * a.dv + v0, a.dv, min(64, a.dv - v0), n);
+    Stage<In, 64, kGradThreads> sx(a.xs.token, cols), sg(a.dv, cols);
+    f32x4 s4[4] = {}, r4[4] = {};   // the wave's rows of S and R: row m, columns 16 k + 4 g ..
+    auto fetch = [&](int k) {
+        const int h = head(k), v0 = column(k);
+        sx.load(static_cast<const In*>(a.x) + b * a.xs.batch + h * a.xs.head + t0 * a.xs.token + v0, a.xs.token, cols, n);
+        sg.load(static_cast<const In*>(a.grad_out) + ((b * a.H + h) * a.T + t0) * a.dv + v0, a.dv, cols, n);
+    };
+    auto fetch_states = [&](int k) {
+        if (16 * nt >= dk) return;
+        const long at = (((b * a.H + head(k)) * a.nc + chunk) * dk + 16 * nt) * a.dv + column(k);
+        const int lo = (m * a.dv + 4 * g) * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // dv = 16, 32: zeros where nothing is
+            if (cols <= 16 * q) continue;
+            s4[q] = load4(lane_at(a.S + at + 16 * q, lo));
+            r4[q] = load4(lane_at(a.R + at + 16 * q, lo));
+        }
+    };
+    float raw = 0.f, next_raw = 0.f;   // wave 7: the raw step sizes
+    auto fetch_raw = [&](int h) {
+        if (h < h_last && lane < n) next_raw = raw_step(a, b, h, t0 + lane);
+    };
+    auto scalars = [&](int h) {
+        raw = next_raw;
+        if (h < h_last) chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw, a.softplus) : 0.f, a.A[h]);
+        fetch_raw(h + 1);
     };
     f32x4 cb[2], zsum[2] = {}, dc[TT] = {}, db[TT] = {};
     if (n > 0) {
+        fetch(0);
+        fetch_states(0);
         {
-            Stage<In, N, kGradThreads> sb, sc;
+            Stage<In, N, kGradThreads> sb(a.bs.token, dk), sc(a.cs.token, dk);
             sb.load(static_cast<const In*>(a.bm) + b * a.bs.batch + hk * a.bs.head + t0 * a.bs.token, a.bs.token, dk, n);
             sc.load(static_cast<const In*>(a.cm) + b * a.cs.batch + hk * a.cs.head + t0 * a.cs.token, a.cs.token, dk, n);
             sb.store(S.b);
             sc.store(S.c);
+        }
+        if (wave == 7) {
+            fetch_raw(h_first);
+            scalars(h_first);
         }
         // what is above the pairs, where products read it: six tiles
         if (wave < 6) {
             const int j = wave < 1 ? 1 : wave < 3 ? 2 : 3, i = wave - j * (j - 1) / 2;
             S.p.put4(16 * j + m, 16 * i + 4 * g, f32x4{0.f, 0.f, 0.f, 0.f});
         }
-        fetch(h_first, 0);
         __syncthreads();
         // C B^T: rows of tokens 16 i + 4 g + r, columns 16 j + m
 #pragma unroll
@@ -142,195 +212,179 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         }
     }
     for (int h = h_first; h < h_last; ++h) {
-        const long bh = b * a.H + h;
-        In* gx = static_cast<In*>(ga.grad_x) + b * ga.gxs.batch + h * ga.gxs.head + t0 * ga.gxs.token;
-        zero_rows(gx, ga.gxs.token, a.dv, n, rows);
-        if (n == 0) {
-            if (threadIdx.x < rows) {
-                const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + threadIdx.x) * ga.gdts.token;
-                if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, 0.f);
-                else static_cast<float*>(ga.grad_dt)[o] = 0.f;
-            }
-            if (threadIdx.x < 3) ga.sums[((long)h * 3 + threadIdx.x) * a.B * a.nc + b * a.nc + chunk] = 0.0;
-            continue;
+        zero_rows(static_cast<In*>(ga.grad_x) + b * ga.gxs.batch + h * ga.gxs.head + t0 * ga.gxs.token, ga.gxs.token, a.dv, n, rows);
+        if (n > 0) continue;
+        if (threadIdx.x < rows) {
+            const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + threadIdx.x) * ga.gdts.token;
+            if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, 0.f);
+            else static_cast<float*>(ga.grad_dt)[o] = 0.f;
         }
-        const float A = a.A[h], skip = a.D ? a.D[h] : 0.0f;
-        double direct = 0.0, da = 0.0, dskip = 0.0;   // wave 7: of token t's step size and log decay, of skip
-        float raw = 0.f, step = 0.f;
-        for (int v0 = 0; v0 < a.dv; v0 += 64) {
-            const int cols = min(64, a.dv - v0), v = v0 + 16 * vt;
-            const float* Rm = a.R + (bh * a.nc + chunk) * dk * a.dv;
-            const float* Sm = a.S + (bh * a.nc + chunk) * dk * a.dv;
-            sx.store(S.x);
-            sg.store(S.g);
-            if (v0 == 0 && wave == 7) {
-                raw = lane < n ? raw_step(a, b, h, t0 + lane) : 0.f;
-                step = lane < n ? step_of(raw, a.softplus) : 0.f;
-                const float d = chunk_scalars(S.s, step, A);
-                if (lane == 0) S.decay = d;
+        if (threadIdx.x < 3) ga.sums[((long)h * 3 + threadIdx.x) * a.B * a.nc + b * a.nc + chunk] = 0.0;
+    }
+    double direct = 0.0, da = 0.0, dskip = 0.0;   // wave 7: of token t's step size and log decay, of skip
+    for (int k = 0; k < (n > 0 ? all : 0); ++k) {
+        const int h = head(k), v0 = column(k);
+        Plane<In, 64>& X = S.x[k % buffers];
+        Plane<In, 64>& G = S.g[k % buffers];
+        const Scalars& sl = S.s[h % buffers];
+        sx.store(X);
+        sg.store(G);
+        __syncthreads();
+        if (k + 1 < all) fetch(k + 1);
+        // the pairs
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int lane = lane_again(), m = lane % 16, g = lane / 16, tile = wave + 8 * q;
+            if (tile >= 10) continue;
+            const int i = tile_i(tile), j = tile_j(tile), s = 16 * j + m;
+            f32x4 M;
+            mma<true>(M, G.row(i, 0, m, g), X.row(j, 0, m, g));
+            mma(M, G.row(i, 1, m, g), X.row(j, 1, m, g));
+            const float D = sl.step[s];
+            f32x4 L;   // the pairs' decays, one exponential each
+            const double ls = sl.l[s];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * i + 4 * g + r;
+                L[r] = i != j || s <= t ? exp2_small(sl.l[t] - ls) : 0.0f;
             }
-            __syncthreads();
-            if (v0 + 64 < a.dv) fetch(h, v0 + 64);
-            else if (h + 1 < h_last) fetch(h + 1, 0);
-            // the pairs
+            mfma_done(M);
+            const f32x4 P = L * cb[q];
+            S.p.put4(s, 16 * i + 4 * g, P);
+            zsum[q] += L * M * D;
+            f32x4 F = P * M;
+            if (i == j) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int lane = lane_again(), m = lane % 16, g = lane / 16, k = wave + 8 * q;
-                if (k >= 10) continue;
-                const int i = tile_i(k), j = tile_j(k), s = 16 * j + m;
-                f32x4 M;
-                mma<true>(M, S.g.row(i, 0, m, g), S.x.row(j, 0, m, g));
-                mma(M, S.g.row(i, 1, m, g), S.x.row(j, 1, m, g));
-                const float D = S.s.step[s];
-                f32x4 L;   // the pairs' decays, one exponential each
-                const double ls = S.s.l[s];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 16 * i + 4 * g + r;
-                    L[r] = i != j || s <= t ? exp2_small(S.s.l[t] - ls) : 0.0f;
-                }
-                mfma_done(M);
-                const f32x4 P = L * cb[q];
-                S.p.put4(s, 16 * i + 4 * g, P);
-                zsum[q] += L * M * D;
-                f32x4 F = P * M;
-                if (i == j) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (s == 16 * i + 4 * g + r) {
-                            S.diag[s] = F[r];
-                            S.dx[s] = M[r];
-                            F[r] = 0.f;
-                        }
-                }
-                const double e[4] = {F[0] * D, F[1] * D, F[2] * D, F[3] * D};
-                const double col = kslot_sum(((double)F[0] + F[1]) + ((double)F[2] + F[3])), row = row_sums(e, m);
-                if (g == 0) S.col[i][s] = col;
-                if (m < 4) S.row[j][16 * i + 4 * g + m] = row;
-            }
-            __syncthreads();
-            // dX, transposed: rows of dv, columns of tokens
-            if (16 * vt < cols) {
-                const int lane = lane_again(), m = lane % 16, g = lane / 16;
-                f32x4 o[2];
-#pragma unroll
-                for (int k = 0; k < N / 32; ++k) {
-                    float f[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int row = 32 * k + 16 * (e / 4);   // and 4 g + e % 4
-                        f[e] = row < dk ? *lane_at(Rm + (row + e % 4) * a.dv + v, (4 * g * a.dv + m) * 4) : 0.f;
+                for (int r = 0; r < 4; ++r)
+                    if (s == 16 * i + 4 * g + r) {
+                        S.diag[s] = F[r];
+                        S.dx[s] = M[r];
+                        F[r] = 0.f;
                     }
-                    const typename PN::Two r2 = PN::two(f);
-                    const typename PN::One br[2] = {S.b.row(2 * half, k, m, g), S.b.row(2 * half + 1, k, m, g)};
-                    if (k == 0) mma<true>(o, r2, br);
-                    else mma(o, r2, br);
-                }
-                mfma_done(o);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) o[j] *= S.s.out[16 * (2 * half + j) + m];
-                mfma_ready(o);
-                mma(o, S.g.col(vt, 1, m, g), {S.p.row(2 * half, 1, m, g), S.p.row(2 * half + 1, 1, m, g)});
-                mma(o, S.g.col(vt, 0, m, g), {S.p.row(2 * half, 0, m, g), S.p.row(2 * half + 1, 0, m, g)});
-                mfma_done(o);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int s = 16 * (2 * half + j) + m;
-                    if (s < n) store4_el(gx + s * ga.gxs.token + v + 4 * g, o[j] * S.s.step[s] + skip * S.g.get4(s, 16 * vt + 4 * g));
-                }
             }
-            // dC and dB of the states, transposed: rows of dk, columns of tokens
-            if (16 * nt < dk) {
-                const int lane = lane_again(), m = lane % 16, g = lane / 16;
-                f32x4 oc[TT], ob[TT], s4[4] = {}, r4[4] = {};
-                double carry = 0.0;
+            const double e[4] = {F[0] * D, F[1] * D, F[2] * D, F[3] * D};
+            const double col = kslot_sum(((double)F[0] + F[1]) + ((double)F[2] + F[3])), row = row_sums(e, m);
+            if (g == 0) S.col[i][s] = col;
+            if (m < 4) S.row[j][16 * i + 4 * g + m] = row;
+        }
+        // dC and dB of the states, transposed: rows of dk, columns of tokens
+        if (16 * nt < dk) {
+            const int lane = lane_again(), m = lane % 16, g = lane / 16;
+            double carry = 0.0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {   // dv = 16, 32: zeros where nothing is
-                    if (cols <= 16 * k) continue;
-                    const int at = 16 * nt * a.dv + v0 + 16 * k, lo = (m * a.dv + 4 * g) * 4;
-                    s4[k] = load4(lane_at(Sm + at, lo));
-                    r4[k] = load4(lane_at(Rm + at, lo));
-                }
+            for (int q = 0; q < 4; ++q) carry += dot4(s4[q], r4[q]);
+            f32x4 o[TT];
+            typename PV::One x0[TT], x1[TT];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    carry += dot4(s4[k], r4[k]);
-                }
-                typename PV::One x0[TT], x1[TT];
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    x0[t] = S.g.row(first + t, 0, m, g);
-                    x1[t] = S.g.row(first + t, 1, m, g);
-                }
-                mma_pair(oc, three8<PV>(s4[0], s4[1]), x0, three8<PV>(s4[2], s4[3]), x1);
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    x0[t] = S.x.row(first + t, 0, m, g);
-                    x1[t] = S.x.row(first + t, 1, m, g);
-                }
-                mma_pair(ob, three8<PV>(r4[0], r4[1]), x0, three8<PV>(r4[2], r4[3]), x1);
-#pragma unroll
-                for (int t = 0; t < TT; ++t) {
-                    const int s = 16 * (first + t) + m;
-                    oc[t] *= S.s.in[s];
-                    ob[t] *= S.s.out[s];
-                    const float rd = kslot_sum(dot4(oc[t], S.c.get4(s, 16 * nt + 4 * g)));
-                    const float wr = kslot_sum(dot4(ob[t], S.b.get4(s, 16 * nt + 4 * g)));
-                    if (g == 0) {
-                        S.rd[nt][s] = rd;
-                        S.wr[nt][s] = wr;
-                    }
-                    dc[t] += oc[t];
-                    db[t] += ob[t] * S.s.step[s];
-                }
-                if (first == 0) {
-                    carry = wave_sum(carry);
-                    if (lane == 0) S.carry[nt] = carry;
-                }
+            for (int t = 0; t < TT; ++t) {
+                x0[t] = G.row(first + t, 0, m, g);
+                x1[t] = G.row(first + t, 1, m, g);
             }
-            __syncthreads();
-            if (wave == 7) {
-                const int bi = lane / 16;
-                double row = 0.0, col = 0.0, rdt = 0.0, wrt = 0.0, cr = 0.0;
+            mma_pair(o, three8<PV>(s4[0], s4[1]), x0, three8<PV>(s4[2], s4[3]), x1);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (k <= bi) row += S.row[k][lane];
-                    if (k >= bi) col += S.col[k][lane];
-                }
-                for (int k = 0; k < dk / 16; ++k) {
-                    rdt += S.rd[k][lane];
-                    wrt += S.wr[k][lane];
-                    cr += S.carry[k];
-                }
-                direct += col + S.diag[lane] + wrt;
-                // before: of the tokens before t; after: of t and those that follow
-                double before = step * (col + wrt) - row, after = rdt;
-                const double own = before;
+            for (int t = 0; t < TT; ++t) {
+                const int s = 16 * (first + t) + m;
+                o[t] *= sl.in[s];
+                const float rd = kslot_sum(dot4(o[t], S.c.get4(s, 16 * nt + 4 * g)));
+                if (g == 0) S.rd[nt][s] = rd;
+                dc[t] += o[t];
+                x0[t] = X.row(first + t, 0, m, g);
+                x1[t] = X.row(first + t, 1, m, g);
+            }
+            const typename PV::Three r3[2] = {three8<PV>(r4[0], r4[1]), three8<PV>(r4[2], r4[3])};
+            mma_pair(o, r3[0], x0, r3[1], x1);
 #pragma unroll
-                for (int o = 1; o < 64; o <<= 1) {
-                    const double x = __shfl_up(before, o, 64), y = __shfl_down(after, o, 64);
-                    if (lane >= o) before += x;
-                    if (lane + o < 64) after += y;
-                }
-                da += (before - own) + after + (double)S.decay * cr;
-                dskip += lane < n ? S.dx[lane] : 0.f;
+            for (int t = 0; t < TT; ++t) {
+                const int s = 16 * (first + t) + m;
+                o[t] *= sl.out[s];
+                const float wr = kslot_sum(dot4(o[t], S.b.get4(s, 16 * nt + 4 * g)));
+                if (g == 0) S.wr[nt][s] = wr;
+                db[t] += o[t] * sl.step[s];
+            }
+            if (first == 0) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) S.r.put(16 * nt + m, g, q, r3);
+                carry = wave_sum(carry);
+                if (lane == 0) S.carry[nt] = carry;
+            }
+        } else if (first == 0) {
+            // dk = 16: zeros for the rows that are not there
+            const typename PV::Three zero[2] = {};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) S.r.put(16 * nt + m, g, q, zero);
+        }
+        if (k + 1 < all) fetch_states(k + 1);
+        __syncthreads();
+        // dX, transposed: rows of dv, columns of tokens
+        if (16 * vt < cols) {
+            const int lane = lane_again(), m = lane % 16, g = lane / 16;
+            f32x4 o[2];
+#pragma unroll
+            for (int q = 0; q < N / 32; ++q) {
+                const typename PN::One br[2] = {S.b.row(2 * half, q, m, g), S.b.row(2 * half + 1, q, m, g)};
+                if (q == 0) mma<true>(o, S.r.col(vt, q, m, g), br);
+                else mma(o, S.r.col(vt, q, m, g), br);
+            }
+            mfma_done(o);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) o[j] *= sl.out[16 * (2 * half + j) + m];
+            mfma_ready(o);
+            mma(o, G.col(vt, 1, m, g), {S.p.row(2 * half, 1, m, g), S.p.row(2 * half + 1, 1, m, g)});
+            mma(o, G.col(vt, 0, m, g), {S.p.row(2 * half, 0, m, g), S.p.row(2 * half + 1, 0, m, g)});
+            mfma_done(o);
+            const float skip = a.D ? a.D[h] : 0.0f;
+            In* gx = static_cast<In*>(ga.grad_x) + b * ga.gxs.batch + h * ga.gxs.head + t0 * ga.gxs.token + v0 + 16 * vt + 4 * g;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int s = 16 * (2 * half + j) + m;
+                if (s < n) store4_el(gx + s * ga.gxs.token, o[j] * sl.step[s] + skip * G.get4(s, 16 * vt + 4 * g));
             }
         }
         if (wave == 7) {
-            double draw = 0.0, dA = 0.0;
-            if (lane < n) {
-                const double dstep = direct + (double)A * da;
-                draw = a.softplus ? dstep / (1.0 + (double)expf(-raw)) : dstep;
-                dA = step * da;
+            const int bi = lane / 16;
+            double row = 0.0, col = 0.0, rdt = 0.0, wrt = 0.0, cr = 0.0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (q <= bi) row += S.row[q][lane];
+                if (q >= bi) col += S.col[q][lane];
             }
-            if (lane < rows) {
-                const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + lane) * ga.gdts.token;
-                if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, (float)draw);
-                else static_cast<float*>(ga.grad_dt)[o] = (float)draw;
+#pragma unroll
+            for (int q = 0; q < N / 16; ++q) {
+                if (16 * q >= dk) continue;
+                rdt += S.rd[q][lane];
+                wrt += S.wr[q][lane];
+                cr += S.carry[q];
             }
-            dA = wave_sum(dA);
-            dskip = wave_sum(dskip);
-            draw = wave_sum(draw);
-            if (lane < 3) ga.sums[((long)h * 3 + lane) * a.B * a.nc + b * a.nc + chunk] = lane == 0 ? dA : lane == 1 ? dskip : draw;
+            const float step = sl.step[lane];
+            direct += col + S.diag[lane] + wrt;
+            dskip += lane < n ? S.dx[lane] : 0.f;
+            // before: of the tokens before t; after: of t and those that follow
+            const double own = step * (col + wrt) - row, before = prefix_sum(own) - own;
+            const double upto = prefix_sum(rdt), after = __shfl(upto, 63, 64) - upto + rdt;
+            da += before + after + (double)sl.decay * cr;
+            if ((k + 1) % pieces == 0) {
+                double draw = 0.0, dA = 0.0;
+                if (lane < n) {
+                    const double dstep = direct + (double)a.A[h] * da;
+                    draw = a.softplus ? dstep / (1.0 + (double)expf(-raw)) : dstep;
+                    dA = step * da;
+                }
+                if (lane < rows) {
+                    const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + lane) * ga.gdts.token;
+                    if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, (float)draw);
+                    else static_cast<float*>(ga.grad_dt)[o] = (float)draw;
+                }
+                dA = wave_sum(dA);
+                dskip = wave_sum(dskip);
+                draw = wave_sum(draw);
+                if (lane < 3) ga.sums[((long)h * 3 + lane) * a.B * a.nc + b * a.nc + chunk] = lane == 0 ? dA : lane == 1 ? dskip : draw;
+                direct = da = dskip = 0.0;
+                if (buffers == 2) scalars(h + 1);
+            }
+        }
+        if (buffers == 1) {
+            __syncthreads();
+            if (wave == 7 && (k + 1) % pieces == 0) scalars(h + 1);
         }
     }
     // the pairs' dC and dB over the heads' sum of Z

@@ -16,15 +16,13 @@ struct ScanLds {
     Plane<In, N> b, c;
     Plane<In, 64> x;
     Square<In> m;
-    Scalars s;
-    float decay;
+    Scalars s[2];   // of this chunk and the next
 };
 template <int N, typename In>
 struct CarryLds {
     Plane<In, N> b;
     Plane<In, 64> x;
-    Scalars s;
-    float decay;
+    Scalars s[2];   // of this chunk and the next
 };
 
 // Where a workgroup works.
@@ -105,19 +103,30 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
         for (int i = 0; i < N / 16; ++i)
             if (16 * i < dk) st[i] = load4(from + (long)(v + m) * dk + 16 * i + 4 * g);
 
-    Stage<In, N> sb, sc;
-    Stage<In, 64> sx;
-    float step = 0.f;
+    Stage<In, N> sb(a.bs.token, dk), sc(a.cs.token, dk);
+    Stage<In, 64> sx(a.xs.token, p.cols);
+    float raw = 0.f;   // wave 3: the step sizes to come
+    auto tokens = [&](int c) { return (int)min((long)kSC, p.valid - first - (long)c * kSC); };
     auto fetch = [&](int c) {
         const long t0 = first + (long)c * kSC;
-        const int n = (int)min((long)kSC, p.valid - t0);
+        const int n = tokens(c);
         sb.load(br + t0 * a.bs.token, a.bs.token, dk, n);
         sc.load(cr + t0 * a.cs.token, a.cs.token, dk, n);
         sx.load(xr + t0 * a.xs.token, a.xs.token, p.cols, n);
-        if (wave == 3) step = lane < n ? step_of(raw_step(a, p.b, p.h, t0 + lane), a.softplus) : 0.0f;
+    };
+    auto fetch_raw = [&](int c) {
+        if (c < chunks && lane < tokens(c)) raw = raw_step(a, p.b, p.h, first + (long)c * kSC + lane);
+    };
+    auto scalars = [&](int c) {
+        if (c < chunks) chunk_scalars(S.s[c % 2], lane < tokens(c) ? step_of(raw, a.softplus) : 0.0f, A);
+        fetch_raw(c + 1);
     };
     if (chunks > 0) {
         fetch(0);
+        if (wave == 3) {
+            fetch_raw(0);
+            scalars(0);
+        }
         // above the diagonal blocks, where 32 columns are read
         if (wave < 2) S.m.put4(32 * wave + m, 32 * wave + 16 + 4 * g, f32x4{0.f, 0.f, 0.f, 0.f});
     }
@@ -126,15 +135,12 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
         sb.store(S.b);
         sc.store(S.c);
         sx.store(S.x);
-        if (wave == 3) {
-            const float d = chunk_scalars(S.s, step, A);
-            if (lane == 0) S.decay = d;
-        }
         __syncthreads();
         if (c + 1 < chunks) fetch(c + 1);
-        const Scalars& sl = S.s;
+        const Scalars& sl = S.s[c % 2];
         // L o (C B^T) diag(D), tile (i, j): lane's token i-block m, its columns 4 g ..
-        for (int k = wave; k < 10; k += 4) {
+        // Wave 3 takes one tile and the next chunk's scalars, the others three.
+        for (int k = wave < 3 ? wave : 9; k < (wave < 3 ? 9 : 10); k += 3) {
             const int i = tile_i(k), j = tile_j(k);
             f32x4 acc;
             mma<true>(acc, S.b.row(j, 0, m, g), S.c.row(i, 0, m, g));
@@ -156,6 +162,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
             }
             S.m.put4(t, 16 * j + 4 * g, acc);
         }
+        if (wave == 3) scalars(c + 1);
         // diag(e^l) C S, transposed: rows of dv, columns of tokens
         f32x4 o[4];
         if (mine) {
@@ -189,7 +196,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
             }
             // S' = e^{l_63} S + B^T diag(e^{l_63 - l} D) X
             const auto w0 = weighted<PV>(x0, sl.write, 0, g), w1 = weighted<PV>(x1, sl.write, 1, g);
-            add_outer<N, false>(st, S.decay, S.b, w0, w1, m, g);
+            add_outer<N, false>(st, sl.decay, S.b, w0, w1, m, g);
         }
         __syncthreads();
     }
@@ -245,20 +252,32 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
 #pragma unroll
         for (int i = 0; i < N / 16; ++i)
             if (16 * i < dk) st[i] = load4(seg + (p.bh * segs + p.seg - 1) * a.dv * dk + (long)(16 * i + m) * a.dv + v + 4 * g);
-    Stage<In, N> sb;
-    Stage<In, 64> sx;
-    float step = 0.f;
+    Stage<In, N> sb(ks.token, dk);
+    Stage<In, 64> sx(xt, p.cols);
+    float raw = 0.f;   // wave 3: the step sizes to come
+    const int k0 = BACK ? max(begin, a.nc - real) : begin, k1 = BACK ? end : min(end, real);
     // chunk of step k; from the back the row's empty chunks come first
     auto chunk_of = [&](int k) { return BACK ? a.nc - 1 - k : k; };
+    auto tokens = [&](int k) { return (int)min((long)kSC, p.valid - (long)chunk_of(k) * kSC); };
     auto fetch = [&](int k) {
         const long t0 = (long)chunk_of(k) * kSC;
-        const int n = (int)min((long)kSC, p.valid - t0);
-        sb.load(kr + t0 * ks.token, ks.token, dk, n);
-        sx.load(xr + t0 * xt, xt, p.cols, n);
-        if (wave == 3) step = lane < n ? step_of(raw_step(a, p.b, p.h, t0 + lane), a.softplus) : 0.0f;
+        sb.load(kr + t0 * ks.token, ks.token, dk, tokens(k));
+        sx.load(xr + t0 * xt, xt, p.cols, tokens(k));
     };
-    const int k0 = BACK ? max(begin, a.nc - real) : begin, k1 = BACK ? end : min(end, real);
-    if (k0 < k1) fetch(k0);
+    auto fetch_raw = [&](int k) {
+        if (k < k1 && lane < tokens(k)) raw = raw_step(a, p.b, p.h, (long)chunk_of(k) * kSC + lane);
+    };
+    auto scalars = [&](int k) {
+        if (k < k1) chunk_scalars(S.s[k % 2], lane < tokens(k) ? step_of(raw, a.softplus) : 0.0f, A);
+        fetch_raw(k + 1);
+    };
+    if (k0 < k1) {
+        fetch(k0);
+        if (wave == 3) {
+            fetch_raw(k0);
+            scalars(k0);
+        }
+    }
     double total = 0.0;
     for (int k = k0; k < k1; ++k) {
         if (!ENDS && mine) {
@@ -269,17 +288,15 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
         }
         sb.store(S.b);
         sx.store(S.x);
-        if (wave == 3) {
-            const float d = chunk_scalars(S.s, step, A);
-            if (lane == 0) S.decay = d;
-        }
         __syncthreads();
         if (k + 1 < k1) fetch(k + 1);
-        if (ENDS) total += S.s.l[63];
+        const Scalars& sl = S.s[k % 2];
+        if (ENDS) total += sl.l[63];
+        if (wave == 3) scalars(k + 1);
         if (mine) {
-            const auto w0 = weighted<PV>(S.x.col(wave, 0, m, g), BACK ? S.s.in : S.s.write, 0, g);
-            const auto w1 = weighted<PV>(S.x.col(wave, 1, m, g), BACK ? S.s.in : S.s.write, 1, g);
-            add_outer<N, FLIP>(st, S.decay, S.b, w0, w1, m, g);
+            const auto w0 = weighted<PV>(S.x.col(wave, 0, m, g), BACK ? sl.in : sl.write, 0, g);
+            const auto w1 = weighted<PV>(S.x.col(wave, 1, m, g), BACK ? sl.in : sl.write, 1, g);
+            add_outer<N, FLIP>(st, sl.decay, S.b, w0, w1, m, g);
         }
         __syncthreads();
     }
@@ -303,13 +320,13 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
 }
 
 template <int N, typename In>
-__global__ __launch_bounds__(256) void ssm_ends_kernel(SsmArgs a) {
+__global__ __launch_bounds__(256, 2) void ssm_ends_kernel(SsmArgs a) {
     __shared__ CarryLds<N, In> S;
     ssm_carry<N, In, true, false, false>(a, S, ssm_place(a, blockIdx.x, a.nseg - 1));
 }
 // Both directions of the gradients side by side.
 template <int N, typename In, bool ENDS>
-__global__ __launch_bounds__(256) void ssm_states_kernel(SsmArgs a) {
+__global__ __launch_bounds__(256, 2) void ssm_states_kernel(SsmArgs a) {
     __shared__ CarryLds<N, In> S;
     const SsmPlace p = ssm_place(a, blockIdx.x / 2, ENDS ? a.nseg - 1 : a.nseg);
     if (blockIdx.x % 2) ssm_carry<N, In, ENDS, true, true>(a, S, p);

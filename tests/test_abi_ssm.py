@@ -127,8 +127,8 @@ def test_ssm_sizes(name, kw, status, needle):
 
 def test_token_strides_past_what_the_kernels_address():
     for name in ("mesa_ssm_forward", "mesa_ssm_backward"):
-        refused(name, UNSUPPORTED, "token stride of x", x=1 << 44, xs=S(0, 64, 1 << 24))
-        refused(name, UNSUPPORTED, "token stride of b", b=1 << 44, bs=S(0, 64, 1 << 24))
+        refused(name, UNSUPPORTED, "token stride of x", x=1 << 44, xs=S(0, 64, 1 << 23))
+        refused(name, UNSUPPORTED, "token stride of b", b=1 << 44, bs=S(0, 64, 1 << 23))
 
 
 @pytest.mark.parametrize("name", ["mesa_causal_conv", "mesa_causal_conv_backward"])
