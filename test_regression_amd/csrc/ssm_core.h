@@ -26,6 +26,13 @@ namespace mesa {
 constexpr int kSC = kSsmChunk;
 static_assert(kSC == 64, "a wave's lanes are a chunk's tokens");
 
+// The workgroup's place in an order in which neighbours share a XCD and its cache:
+// workgroups go to the eight XCDs in turn.
+__device__ __forceinline__ long xcd_order() {
+    const unsigned n = gridDim.x, x = blockIdx.x % 8, q = n / 8, r = n % 8;
+    return (long)x * q + min(x, r) + blockIdx.x / 8;
+}
+
 // The lane's number again, in a way that the compiler cannot see through: addresses
 // formed from it are formed where they are used, not kept in registers over a loop.
 __device__ __forceinline__ int lane_again() {
@@ -76,6 +83,13 @@ __device__ __forceinline__ B3 split3(float (&v)[8]) {
 __device__ __forceinline__ void mfma_ready(f32x4& c) { asm("s_nop 1" : "+v"(c)); }
 __device__ __forceinline__ void mfma_done(f32x4& c) { asm("s_nop 11" : "+v"(c)); }
 __device__ __forceinline__ void mfma_done(f32x4 (&c)[1]) { mfma_done(c[0]); }
+__device__ __forceinline__ void mfma_done(f32x4 (&a)[1], f32x4 (&b)[1]) { asm("s_nop 11" : "+v"(a[0]), "+v"(b[0])); }
+__device__ __forceinline__ void mfma_done(f32x4 (&a)[2], f32x4 (&b)[2]) {
+    asm("s_nop 11" : "+v"(a[0]), "+v"(a[1]), "+v"(b[0]), "+v"(b[1]));
+}
+__device__ __forceinline__ void mfma_done(f32x4 (&a)[4], f32x4 (&b)[4]) {
+    asm("s_nop 11" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]), "+v"(b[0]), "+v"(b[1]), "+v"(b[2]), "+v"(b[3]));
+}
 __device__ __forceinline__ void settle(B2& x) { asm("s_nop 1" : "+v"(x.h), "+v"(x.l)); }
 __device__ __forceinline__ void settle(B3& x) { asm("s_nop 1" : "+v"(x.h), "+v"(x.m), "+v"(x.l)); }
 __device__ __forceinline__ void settle(F8& x) {
@@ -145,12 +159,9 @@ __device__ __forceinline__ void mma_apart(f32x4 (&C)[N], int steps, Step step) {
             if (s < 2) step(C[i], i, s, s == 0);
             else step(low[i], i, s, s == 2);
         }
+    mfma_done(C, low);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        mfma_done(C[i]);
-        mfma_done(low[i]);
-        C[i] += low[i];
-    }
+    for (int i = 0; i < N; ++i) C[i] += low[i];
 }
 template <int N, typename A, typename B>
 __device__ __forceinline__ void mma_pair(f32x4 (&C)[N], const A& a0, const B (&b0)[N], const A& a1, const B (&b1)[N]) {
@@ -342,11 +353,16 @@ __device__ __forceinline__ float exp2_small(double x) {
 __device__ __forceinline__ float step_of(float raw, int softplus) {
     return softplus ? fmaxf(raw, 0.0f) + log1pf(expf(-fabsf(raw))) : raw;
 }
-__device__ __forceinline__ float raw_step(const SsmArgs& a, long b, int h, long t) {
+// The raw value of token t, bits as stored: converted where it is used, so that the
+// load is not waited for where it is issued.
+__device__ __forceinline__ uint32_t step_bits(const SsmArgs& a, long b, int h, long t) {
     const long o = b * a.dts.batch + h * a.dts.head + t * a.dts.token;
-    const float x = a.dt_bf16 ? to_f32(static_cast<const bf16_t*>(a.dt)[o]) : static_cast<const float*>(a.dt)[o];
-    return a.dt_bias ? x + a.dt_bias[h] : x;
+    return a.dt_bf16 ? static_cast<const bf16_t*>(a.dt)[o].bits : static_cast<const uint32_t*>(a.dt)[o];
 }
+__device__ __forceinline__ float raw_step(const SsmArgs& a, uint32_t bits, float bias) {
+    return __uint_as_float(a.dt_bf16 ? bits << 16 : bits) + bias;
+}
+__device__ __forceinline__ float step_bias(const SsmArgs& a, int h) { return a.dt_bias ? a.dt_bias[h] : 0.0f; }
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp_add(double v) {

@@ -133,7 +133,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
     const SsmArgs& a = ga.f;
     const int dk = N > 32 ? N : a.dk;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16;
-    long i0 = blockIdx.x;
+    long i0 = xcd_order();
     const int part = (int)(i0 % ga.parts);
     i0 /= ga.parts;
     const int chunk = (int)(i0 % a.nc);
@@ -171,13 +171,15 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             r4[q] = load4(lane_at(a.R + at + 16 * q, lo));
         }
     };
-    float raw = 0.f, next_raw = 0.f;   // wave 7: the raw step sizes
+    float raw = 0.f;   // wave 7: the raw step sizes, and the next head's
+    uint32_t next_raw = 0u;
     auto fetch_raw = [&](int h) {
-        if (h < h_last && lane < n) next_raw = raw_step(a, b, h, t0 + lane);
+        if (h < h_last && lane < n) next_raw = step_bits(a, b, h, t0 + lane);
     };
     auto scalars = [&](int h) {
-        raw = next_raw;
-        if (h < h_last) chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw, a.softplus) : 0.f, a.A[h]);
+        if (h >= h_last) return;
+        raw = raw_step(a, next_raw, step_bias(a, h));
+        chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw, a.softplus) : 0.f, a.A[h]);
         fetch_raw(h + 1);
     };
     f32x4 cb[2], zsum[2] = {}, dc[TT] = {}, db[TT] = {};

@@ -55,10 +55,10 @@ __device__ __forceinline__ typename PV::Three weighted(const typename PV::One& x
     return PV::three(f);
 }
 
-// st = decay st + the rows' columns (transposed) times w, two tiles at a time.
+// st = decay st + the rows' columns (transposed) times w, four tiles at a time.
 template <int N, bool FLIP, typename PN, typename W>
 __device__ __forceinline__ void add_outer(f32x4 (&st)[N / 16], float decay, const PN& rows, const W& w0, const W& w1, int m, int g) {
-    constexpr int H = 2;
+    constexpr int H = N / 16 < 4 ? N / 16 : 4;
 #pragma unroll
     for (int h = 0; h < N / 16; h += H) {
         typename PN::One k0[H], k1[H];
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
     typedef Plane<In, N> PN;
     typedef Plane<In, 64> PV;
     __shared__ ScanLds<N, In> S;
-    const SsmPlace p = ssm_place(a, blockIdx.x, a.nseg);
+    const SsmPlace p = ssm_place(a, xcd_order(), a.nseg);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16, hk = p.h / (a.H / a.Hk);
     const long first = (long)p.seg * a.seg_chunks * kSC;
     const long last = min((long)a.T, first + (long)a.seg_chunks * kSC);   // the segment's tokens
@@ -105,7 +105,8 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
 
     Stage<In, N> sb(a.bs.token, dk), sc(a.cs.token, dk);
     Stage<In, 64> sx(a.xs.token, p.cols);
-    float raw = 0.f;   // wave 3: the step sizes to come
+    uint32_t raw = 0u;   // wave 3: the step sizes to come
+    const float bias = step_bias(a, p.h);
     auto tokens = [&](int c) { return (int)min((long)kSC, p.valid - first - (long)c * kSC); };
     auto fetch = [&](int c) {
         const long t0 = first + (long)c * kSC;
@@ -115,10 +116,10 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
         sx.load(xr + t0 * a.xs.token, a.xs.token, p.cols, n);
     };
     auto fetch_raw = [&](int c) {
-        if (c < chunks && lane < tokens(c)) raw = raw_step(a, p.b, p.h, first + (long)c * kSC + lane);
+        if (c < chunks && lane < tokens(c)) raw = step_bits(a, p.b, p.h, first + (long)c * kSC + lane);
     };
     auto scalars = [&](int c) {
-        if (c < chunks) chunk_scalars(S.s[c % 2], lane < tokens(c) ? step_of(raw, a.softplus) : 0.0f, A);
+        if (c < chunks) chunk_scalars(S.s[c % 2], lane < tokens(c) ? step_of(raw_step(a, raw, bias), a.softplus) : 0.0f, A);
         fetch_raw(c + 1);
     };
     if (chunks > 0) {
@@ -254,7 +255,8 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
             if (16 * i < dk) st[i] = load4(seg + (p.bh * segs + p.seg - 1) * a.dv * dk + (long)(16 * i + m) * a.dv + v + 4 * g);
     Stage<In, N> sb(ks.token, dk);
     Stage<In, 64> sx(xt, p.cols);
-    float raw = 0.f;   // wave 3: the step sizes to come
+    uint32_t raw = 0u;   // wave 3: the step sizes to come
+    const float bias = step_bias(a, p.h);
     const int k0 = BACK ? max(begin, a.nc - real) : begin, k1 = BACK ? end : min(end, real);
     // chunk of step k; from the back the row's empty chunks come first
     auto chunk_of = [&](int k) { return BACK ? a.nc - 1 - k : k; };
@@ -265,10 +267,10 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
         sx.load(xr + t0 * xt, xt, p.cols, tokens(k));
     };
     auto fetch_raw = [&](int k) {
-        if (k < k1 && lane < tokens(k)) raw = raw_step(a, p.b, p.h, (long)chunk_of(k) * kSC + lane);
+        if (k < k1 && lane < tokens(k)) raw = step_bits(a, p.b, p.h, (long)chunk_of(k) * kSC + lane);
     };
     auto scalars = [&](int k) {
-        if (k < k1) chunk_scalars(S.s[k % 2], lane < tokens(k) ? step_of(raw, a.softplus) : 0.0f, A);
+        if (k < k1) chunk_scalars(S.s[k % 2], lane < tokens(k) ? step_of(raw_step(a, raw, bias), a.softplus) : 0.0f, A);
         fetch_raw(k + 1);
     };
     if (k0 < k1) {
@@ -322,14 +324,14 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
 template <int N, typename In>
 __global__ __launch_bounds__(256, 2) void ssm_ends_kernel(SsmArgs a) {
     __shared__ CarryLds<N, In> S;
-    ssm_carry<N, In, true, false, false>(a, S, ssm_place(a, blockIdx.x, a.nseg - 1));
+    ssm_carry<N, In, true, false, false>(a, S, ssm_place(a, xcd_order(), a.nseg - 1));
 }
 // Both directions of the gradients side by side.
 template <int N, typename In, bool ENDS>
 __global__ __launch_bounds__(256, 2) void ssm_states_kernel(SsmArgs a) {
     __shared__ CarryLds<N, In> S;
-    const SsmPlace p = ssm_place(a, blockIdx.x / 2, ENDS ? a.nseg - 1 : a.nseg);
-    if (blockIdx.x % 2) ssm_carry<N, In, ENDS, true, true>(a, S, p);
+    const SsmPlace p = ssm_place(a, xcd_order() / 2, ENDS ? a.nseg - 1 : a.nseg);
+    if (xcd_order() % 2) ssm_carry<N, In, ENDS, true, true>(a, S, p);
     else ssm_carry<N, In, ENDS, true, false>(a, S, p);
 }
 

@@ -24,7 +24,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, long groups) {
     f32x4 S[pieces];
 #pragma unroll
     for (int j = 0; j < pieces; ++j) S[j] = load4(p + 4 * lanes * j);
-    const float step = step_of(raw_step(a, n, h, 0), a.softplus);
+    const float step = step_of(raw_step(a, step_bits(a, n, h, 0), step_bias(a, h)), a.softplus);
     const float decay = expf(step * a.A[h]);
     const float x = to_f32(static_cast<const In*>(a.x)[n * a.xs.batch + h * a.xs.head + row % a.dv]);
     const In* br = static_cast<const In*>(a.bm) + n * a.bs.batch + hk * a.bs.head + 4 * li;
