@@ -147,8 +147,8 @@ __device__ __forceinline__ void mma(f32x4 (&C)[N], const A& a, const B (&b)[N]) 
             else mma_step<false>(C[i], a, b[i], s);
         }
 }
-// C[i] = a0 b0[i] + a1 b1[i] (or a0[i] b0 + a1[i] b1), ready for use: the largest parts
-// and the others in accumulators of their own.
+// C[i] = a0 b0[i] + a1 b1[i] (or a0[i] b0 + a1[i] b1), ready for use; EXACT: the largest
+// parts and the others in accumulators of their own.
 template <int N, typename Step>
 __device__ __forceinline__ void mma_apart(f32x4 (&C)[N], int steps, Step step) {
     f32x4 low[N];
@@ -163,9 +163,9 @@ __device__ __forceinline__ void mma_apart(f32x4 (&C)[N], int steps, Step step) {
 #pragma unroll
     for (int i = 0; i < N; ++i) C[i] += low[i];
 }
-template <int N, typename A, typename B>
+template <bool EXACT = true, int N, typename A, typename B>
 __device__ __forceinline__ void mma_pair(f32x4 (&C)[N], const A& a0, const B (&b0)[N], const A& a1, const B (&b1)[N]) {
-    if constexpr (sizeof(A) == sizeof(F8)) {
+    if constexpr (!EXACT || std::is_same_v<A, F8>) {
         mma<true>(C, a0, b0);
         mma(C, a1, b1);
         mfma_done(C);
@@ -176,9 +176,9 @@ __device__ __forceinline__ void mma_pair(f32x4 (&C)[N], const A& a0, const B (&b
         });
     }
 }
-template <int N, typename A, typename B>
+template <bool EXACT = true, int N, typename A, typename B>
 __device__ __forceinline__ void mma_pair(f32x4 (&C)[N], const A (&a0)[N], const B& b0, const A (&a1)[N], const B& b1) {
-    if constexpr (sizeof(A) == sizeof(F8)) {
+    if constexpr (!EXACT || std::is_same_v<A, F8>) {
         mma<true>(C, a0, b0);
         mma(C, a1, b1);
         mfma_done(C);
