@@ -90,6 +90,8 @@ __device__ __forceinline__ void mfma_done(f32x4 (&a)[2], f32x4 (&b)[2]) {
 __device__ __forceinline__ void mfma_done(f32x4 (&a)[4], f32x4 (&b)[4]) {
     asm("s_nop 11" : "+v"(a[0]), "+v"(a[1]), "+v"(a[2]), "+v"(a[3]), "+v"(b[0]), "+v"(b[1]), "+v"(b[2]), "+v"(b[3]));
 }
+// mfma_done once x is there too: what leads to x is issued while the products run.
+__device__ __forceinline__ void mfma_done_with(f32x4& c, f32x4& x) { asm("s_nop 11" : "+v"(c), "+v"(x)); }
 __device__ __forceinline__ void settle(B2& x) { asm("s_nop 1" : "+v"(x.h), "+v"(x.l)); }
 __device__ __forceinline__ void settle(B3& x) { asm("s_nop 1" : "+v"(x.h), "+v"(x.m), "+v"(x.l)); }
 __device__ __forceinline__ void settle(F8& x) {
@@ -297,16 +299,16 @@ template <> struct Square<float> {
     __device__ __forceinline__ F8 col(int i, int j, int m, int g) const { return p.col(i, j, m, g); }
 };
 
-// 64 rows of W columns on their way into a plane, by the workgroup's threads: units of
-// eight columns.  The loads' bounds make zeros of rows `valid` and up and of columns
+// 64 rows of W columns on their way into a plane, by THREADS threads: units of eight
+// columns.  The loads' bounds make zeros of rows `valid` and up and of columns
 // `cols` and up, without instructions for it.
 template <typename In, int W, int THREADS = 256>
 struct Stage {
     static constexpr int per_row = W / 8, n = (kSC * per_row + THREADS - 1) / THREADS, parts = sizeof(In) / 2;
     uint32_t at[n];
     u32x4 raw[n][parts];
-    static __device__ __forceinline__ int row(int i) { return ((int)threadIdx.x + THREADS * i) / per_row; }
-    static __device__ __forceinline__ int col(int i) { return 8 * (((int)threadIdx.x + THREADS * i) % per_row); }
+    static __device__ __forceinline__ int row(int i) { return ((int)threadIdx.x % THREADS + THREADS * i) / per_row; }
+    static __device__ __forceinline__ int col(int i) { return 8 * (((int)threadIdx.x % THREADS + THREADS * i) % per_row); }
     // `pitch` (below kSsmPitch) between the rows
     __device__ __forceinline__ Stage(long pitch, int cols) {
 #pragma unroll

@@ -231,6 +231,206 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
             if (16 * i < dk) store4(a.final_state + (p.bh * a.dv + v + m) * dk + 16 * i + 4 * g, st[i]);
 }
 
+// Whole sequences, where one workgroup a CU is what there is: eight waves.  Waves 0 to 3
+// keep 16 columns of the state each and take the chunk's products with it; waves 4 to
+// 7, on the same SIMDs, prepare the next chunk meanwhile: they bring its rows into LDS
+// (and have those after it on their way) and form L o (C B^T) diag(D) + skip I.  The
+// two halves of the LDS change places from chunk to chunk.  A chunk takes 3.7 us on a CU
+// against 3.3 us with two workgroups of ssm_out_kernel there, but no pass for segments'
+// ends comes first: 8 x 32 heads of 4096 tokens, dk 128, dv 64, bfloat16: 237 us, where
+// two segments each take 67 + 208 us.  LDS works 40 % of that, the VALU 33 %, the matrix
+// units 20 %: what is left are waits of the state waves' chain, product by product.
+template <int N, typename In>
+struct WalkLds {
+    Plane<In, N> b, c;
+    Plane<In, 64> x;
+    Square<In> m;
+};
+template <int N, typename In> constexpr bool kWalks = 2 * sizeof(WalkLds<N, In>) + 8192 <= 160 * 1024;
+
+// K tiles (ti, tj) of L o (C B^T) diag(D) + skip I at once, so that their operands'
+// reads and their chains of products overlap: a lane's token m of block ti, columns
+// 4 g .. of block tj.
+template <int K, int N, typename In>
+__device__ __forceinline__ void pair_tiles(WalkLds<N, In>& S, const Scalars& sl, const int (&ti)[K], const int (&tj)[K], float skip,
+                                           int m, int g) {
+    f32x4 acc[K];
+#pragma unroll
+    for (int q = 0; q < N / 32; ++q)
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            if (q == 0) mma<true>(acc[k], S.b.row(tj[k], q, m, g), S.c.row(ti[k], q, m, g));
+            else mma(acc[k], S.b.row(tj[k], q, m, g), S.c.row(ti[k], q, m, g));
+        }
+    f32x4 f[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int t = 16 * ti[k] + m;
+        if (ti[k] == tj[k]) {
+            const double lt = sl.l[t];
+            const f32x4 d = row4(sl.step, tj[k], g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f[k][r] = 4 * g + r <= m ? d[r] * exp2_small(lt - sl.l[16 * tj[k] + 4 * g + r]) : 0.0f;
+        } else {
+            f[k] = row4(sl.e2, tj[k], g) * (sl.e1[t] * block_decay(sl, ti[k], tj[k]));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        mfma_done_with(acc[k], f[k]);
+        f32x4 v = acc[k] * f[k];
+        if (ti[k] == tj[k])
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = 4 * g + r < m ? v[r] : 4 * g + r == m ? v[r] + skip : 0.0f;
+        S.m.put4(16 * ti[k] + m, 16 * tj[k] + 4 * g, v);
+    }
+}
+
+template <int N, typename In>
+__global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
+    typedef Plane<In, N> PN;
+    typedef Plane<In, 64> PV;
+    __shared__ WalkLds<N, In> lds[2];
+    __shared__ Scalars scal[4];   // of the chunk passed over, the one prepared, the one after
+    const int dk = N > 32 ? N : a.dk;
+    const SsmPlace p = ssm_place(a, xcd_order(), a.nseg);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16;
+    const int hk = p.h / (a.H / a.Hk);
+    const long first = (long)p.seg * a.seg_chunks * kSC;
+    const long last = min((long)a.T, first + (long)a.seg_chunks * kSC);   // the segment's tokens
+    const int chunks = first < p.valid ? (int)((min((long)p.valid, last) - first + kSC - 1) / kSC) : 0;
+    const bool carries = wave < 4, mine = carries && 16 * wave < p.cols;
+    const int v = p.v0 + 16 * (wave % 4);   // the wave's columns of dv
+    const In* xr = static_cast<const In*>(a.x) + p.b * a.xs.batch + p.h * a.xs.head + p.v0;
+    const In* br = static_cast<const In*>(a.bm) + p.b * a.bs.batch + hk * a.bs.head;
+    const In* cr = static_cast<const In*>(a.cm) + p.b * a.cs.batch + hk * a.cs.head;
+    const float A = a.A[p.h], skip = a.D ? a.D[p.h] : 0.0f, bias = step_bias(a, p.h);
+    In* out = static_cast<In*>(a.out) + p.bh * a.T * a.dv + v;
+
+    // the state's columns v + m, rows 16 i + 4 g + r
+    f32x4 st[N / 16] = {}, o[4];
+    const float* from = p.seg == 0 ? a.state0 ? a.state0 + p.bh * a.dv * dk : nullptr
+                                   : a.seg_start + (p.bh * (a.nseg - 1) + p.seg - 1) * a.dv * dk;
+    if (from && mine)
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            if (16 * i < dk) st[i] = load4(from + (long)(v + m) * dk + 16 * i + 4 * g);
+
+    Stage<In, N> sb(a.bs.token, dk), sc(a.cs.token, dk);
+    Stage<In, 64> sx(a.xs.token, p.cols);
+    uint32_t raw = 0u;   // wave 7: the step sizes to come
+    auto tokens = [&](int c) { return (int)min((long)kSC, p.valid - first - (long)c * kSC); };
+    auto fetch = [&](int c) {
+        if (c >= chunks) return;
+        const long t0 = first + (long)c * kSC;
+        const int n = tokens(c);
+        sb.load(br + t0 * a.bs.token, a.bs.token, dk, n);
+        sc.load(cr + t0 * a.cs.token, a.cs.token, dk, n);
+        sx.load(xr + t0 * a.xs.token, a.xs.token, p.cols, n);
+    };
+    // diag(e^l) C S, transposed: rows of dv, columns of tokens
+    auto read_state = [&](const WalkLds<N, In>& S, const Scalars& sl) {
+#pragma unroll
+        for (int q = 0; q < N / 32; ++q) {
+            float f[8] = {st[2 * q][0], st[2 * q][1], st[2 * q][2], st[2 * q][3],
+                          st[2 * q + 1][0], st[2 * q + 1][1], st[2 * q + 1][2], st[2 * q + 1][3]};
+            const typename PN::Two s2 = PN::two(f);
+            const typename PN::One c4[4] = {S.c.row(0, q, m, g), S.c.row(1, q, m, g), S.c.row(2, q, m, g), S.c.row(3, q, m, g)};
+            if (q == 0) mma<true>(o, s2, c4);
+            else mma(o, s2, c4);
+        }
+        mfma_done(o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= sl.in[16 * i + m];
+    };
+    auto finish = [&](const WalkLds<N, In>& S, const Scalars& sl, int c) {
+        const typename PV::One x0 = S.x.col(wave, 0, m, g), x1 = S.x.col(wave, 1, m, g);
+        mfma_ready(o);
+        mma(o, x0, {S.m.row(0, 0, m, g), S.m.row(1, 0, m, g), S.m.row(2, 0, m, g), S.m.row(3, 0, m, g)});
+        mma(o[2], x1, S.m.row(2, 1, m, g));
+        mma(o[3], x1, S.m.row(3, 1, m, g));
+        mfma_done(o);
+        const long t0 = first + (long)c * kSC;
+        In* to = out + t0 * a.dv;
+        const int n = tokens(c), rows = (int)min((long)kSC, last - t0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 16 * i + m;
+            if (n < kSC) {
+                if (t >= n) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (t >= rows) continue;
+            }
+            store4(lane_at(to, (t * a.dv + 4 * g) * sizeof(In)), o[i]);
+        }
+        // S' = e^{l_63} S + B^T diag(e^{l_63 - l} D) X
+        const auto w0 = weighted<PV>(x0, sl.write, 0, g), w1 = weighted<PV>(x1, sl.write, 1, g);
+        add_outer<N, false, false>(st, sl.decay, S.b, w0, w1, m, g);
+    };
+    // waves 4 to 6 take the tiles below the diagonal of one column block and one
+    // diagonal tile, wave 7 the last one and the scalars of the chunk after
+    auto pairs = [&](WalkLds<N, In>& S, int c) {
+        const int w = wave - 4;
+        if (w < 3) {
+            const int ti[3] = {max(w, 1), w == 2 ? 3 : 2, w == 2 ? 0 : 3}, tj[3] = {w, w, w == 2 ? 0 : w};
+            pair_tiles<3, N, In>(S, scal[c & 3], ti, tj, skip, m, g);
+        } else {
+            const int last_tile[1] = {3};
+            pair_tiles<1, N, In>(S, scal[c & 3], last_tile, last_tile, skip, m, g);
+        }
+    };
+    auto scalars = [&](int c) {
+        if (c < chunks) chunk_scalars(scal[c & 3], lane < tokens(c) ? step_of(raw_step(a, raw, bias), a.softplus) : 0.0f, A);
+    };
+    auto fetch_raw = [&](int c) {
+        if (c < chunks && lane < tokens(c)) raw = step_bits(a, p.b, p.h, first + (long)c * kSC + lane);
+    };
+    if (!carries) {
+        fetch(0);
+        if (wave == 7 && chunks > 0) {
+            fetch_raw(0);
+            scalars(0);
+            fetch_raw(1);
+        }
+        // above the diagonal blocks, where 32 columns are read
+        lds[(wave - 4) / 2].m.put4(32 * (wave % 2) + m, 32 * (wave % 2) + 16 + 4 * g, f32x4{0.f, 0.f, 0.f, 0.f});
+    }
+    for (int c = chunks > 0 ? -1 : 0; c < chunks; ++c) {
+        WalkLds<N, In>& S = lds[(c + 1) & 1];          // being prepared: chunk c + 1
+        const WalkLds<N, In>& R = lds[c & 1];          // ready: chunk c
+        if (!carries) {
+            if (c + 1 < chunks) {
+                sb.store(S.b);
+                sc.store(S.c);
+                sx.store(S.x);
+            }
+        } else if (mine && c >= 0) {
+            read_state(R, scal[c & 3]);
+        }
+        __syncthreads();
+        if (!carries) {
+            if (c + 1 < chunks) {
+                fetch(c + 2);
+                pairs(S, c + 1);
+                if (wave == 7) {
+                    scalars(c + 2);
+                    fetch_raw(c + 3);
+                }
+            }
+        } else if (mine && c >= 0) {
+            finish(R, scal[c & 3], c);
+        }
+        __syncthreads();
+    }
+    if (!mine) return;
+    // rows past the length (whole chunks of them)
+    for (long t = first + (long)chunks * kSC + lane / 4; t < last; t += 16)
+        store4(out + t * a.dv + 4 * (lane % 4), f32x4{0.f, 0.f, 0.f, 0.f});
+    if (a.final_state && p.seg == a.nseg - 1)
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            if (16 * i < dk) store4(a.final_state + (p.bh * a.dv + v + m) * dk + 16 * i + 4 * g, st[i]);
+}
+
 // Passes that only carry a state: S' = e^{l_63} S + a sum of weighted outer products,
 // of b and x from the front, or (BACK) of c and the outputs' gradients from the back:
 // R' = e^{l_63} R + C^T diag(e^l) g.  ENDS: the end states of all segments but the
@@ -369,12 +569,22 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(float* seg, const float* 
     }
 }
 
+// Workgroups from which on ssm_walk_kernel leaves too few CUs idle for segments to pay
+// (measured per chunk and CU: 3.7 us against 3.3 us and 1.05 us for the ends).
+constexpr long kSsmCUs = 256, kSsmWalk = 216;
 enum SsmPass { kOut, kOutEnds, kStates, kStatesEnds };
 template <int N, typename In>
 static void scan_go(const SsmArgs& a, SsmPass pass, unsigned blocks, hipStream_t s) {
     const dim3 grid(blocks), block(256);
     switch (pass) {
-        case kOut: hipLaunchKernelGGL((ssm_out_kernel<N, In>), grid, block, 0, s, a); break;
+        case kOut:
+            if constexpr (kWalks<N, In>)
+                if (a.nseg == 1 && blocks <= kSsmCUs) {
+                    hipLaunchKernelGGL((ssm_walk_kernel<N, In>), grid, dim3(512), 0, s, a);
+                    break;
+                }
+            hipLaunchKernelGGL((ssm_out_kernel<N, In>), grid, block, 0, s, a);
+            break;
         case kOutEnds: hipLaunchKernelGGL((ssm_ends_kernel<N, In>), grid, block, 0, s, a); break;
         case kStates: hipLaunchKernelGGL((ssm_states_kernel<N, In, false>), grid, block, 0, s, a); break;
         case kStatesEnds: hipLaunchKernelGGL((ssm_states_kernel<N, In, true>), grid, block, 0, s, a); break;
@@ -412,12 +622,14 @@ hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s) { return segments(
 
 // Segments of a sequence that are passed over at once: twice as many while the
 // workgroups (of `sides` directions) stay below kSsmFill and a segment keeps
-// kSsmLeast chunks.
+// kSsmLeast chunks.  16 heads of 16384 tokens, dk and dv 128, bfloat16: 166 us in 16
+// segments (two workgroups a CU), 204 us in 8.
 constexpr long kSsmFill = 512;
 constexpr int kSsmLeast = 8, kSsmMost = 32;
 int ssm_segments(long BH, int nc, int dv, int sides) {
     const long groups = BH * ((dv + 63) / 64) * sides;
     int n = 1;
+    if (sides == 1 && groups >= kSsmWalk && groups <= kSsmCUs) return n;
     while (n < kSsmMost && groups * n < kSsmFill && nc >= 2 * kSsmLeast * n) n *= 2;
     return n;
 }
