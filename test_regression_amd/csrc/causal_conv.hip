@@ -30,17 +30,19 @@ __device__ __forceinline__ int conv_length(const int32_t* lens, long b, int T) {
 
 // Token t of the history followed by x (t >= -(W - 1)); zeros where there is none.
 template <int W, bool WHOLE, typename In>
-__device__ __forceinline__ f32x8 conv_row(const In* x, long ts, const In* hist, int t, int n, int D, int left) {
-    if (t >= 0) return t < n ? load8_upto<WHOLE>(x + t * ts, left) : f32x8{};
-    return hist ? load8_upto<WHOLE>(hist + (long)(t + W - 1) * D, left) : f32x8{};
+__device__ __forceinline__ f32x4 conv_row(const In* x, long ts, const In* hist, int t, int n, int D, int left) {
+    if (t >= 0) return t < n ? load4_upto<WHOLE>(x + t * ts, left) : f32x4{};
+    return hist ? load4_upto<WHOLE>(hist + (long)(t + W - 1) * D, left) : f32x4{};
 }
 
-// A thread's place: eight channels, a run of tokens, a batch row.
+constexpr int kConvChannels = 4;   // of a thread
+
+// A thread's place: kConvChannels channels, a run of tokens, a batch row.
 struct ConvPlace { int d0, left, t0; long b; };
 __device__ __forceinline__ bool conv_place(long i, int D, int segs, int run, long B, ConvPlace* p) {
-    const int pieces = (D + 7) / 8;
+    const int pieces = (D + kConvChannels - 1) / kConvChannels;
     const long r = i / pieces;
-    p->d0 = 8 * (int)(i - r * pieces);
+    p->d0 = kConvChannels * (int)(i - r * pieces);
     p->left = D - p->d0;
     p->b = r / segs;
     p->t0 = (int)(r - p->b * segs) * run;
@@ -55,40 +57,40 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvArgs a) {
     const In* x = static_cast<const In*>(a.x) + p.b * a.xb + p.d0;
     const In* hist = a.hist ? static_cast<const In*>(a.hist) + p.b * (W - 1) * D + p.d0 : nullptr;
     In* y = static_cast<In*>(a.y) + p.b * (long)a.T * D + p.d0;
-    f32x8 w[W], bias{}, last[W];   // last[j]: the row j tokens back
+    f32x4 w[W], bias{}, last[W];   // last[j]: the row j tokens back
 #pragma unroll
-    for (int j = 0; j < W; ++j) w[j] = load8_upto<WHOLE>(a.w + (long)j * D + p.d0, p.left);
-    if (a.bias) bias = load8_upto<WHOLE>(a.bias + p.d0, p.left);
+    for (int j = 0; j < W; ++j) w[j] = load4_upto<WHOLE>(a.w + (long)j * D + p.d0, p.left);
+    if (a.bias) bias = load4_upto<WHOLE>(a.bias + p.d0, p.left);
 #pragma unroll
     for (int j = 1; j < W; ++j) last[j - 1] = conv_row<W, WHOLE>(x, a.xt, hist, p.t0 - j, n, D, p.left);
     const int end = min(p.t0 + a.run, a.T);
     // the rows after this piece's last token, by the one thread that has read the
     // history: hist_out may be hist itself
     if (W > 1 && a.hist_out && p.t0 == 0) {
-        f32x8 keep[W];
+        f32x4 keep[W];
 #pragma unroll
         for (int j = 1; j < W; ++j) keep[j - 1] = conv_row<W, WHOLE>(x, a.xt, hist, n - j, n, D, p.left);
         In* ho = static_cast<In*>(a.hist_out) + p.b * (W - 1) * D + p.d0;
 #pragma unroll
-        for (int j = 1; j < W; ++j) store8_upto<WHOLE>(ho + (long)(W - 1 - j) * D, keep[j - 1], p.left);
+        for (int j = 1; j < W; ++j) store4_upto<WHOLE>(ho + (long)(W - 1 - j) * D, keep[j - 1], p.left);
     }
     for (int t = p.t0; t < end; t += 4) {
-        f32x8 in[4];
+        f32x4 in[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) in[i] = t + i < min(n, end) ? load8_upto<WHOLE>(x + (long)(t + i) * a.xt, p.left) : f32x8{};
+        for (int i = 0; i < 4; ++i) in[i] = t + i < min(n, end) ? load4_upto<WHOLE>(x + (long)(t + i) * a.xt, p.left) : f32x4{};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (t + i >= end) break;
-            f32x8 o{};
+            f32x4 o{};
             if (t + i < n)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float z = bias.v[e] + w[0].v[e] * in[i].v[e];
+                for (int e = 0; e < 4; ++e) {
+                    float z = bias[e] + w[0][e] * in[i][e];
 #pragma unroll
-                    for (int j = 1; j < W; ++j) z += w[j].v[e] * last[j - 1].v[e];
-                    o.v[e] = a.silu ? z * conv_act<In>(z) : z;
+                    for (int j = 1; j < W; ++j) z += w[j][e] * last[j - 1][e];
+                    o[e] = a.silu ? z * conv_act<In>(z) : z;
                 }
-            store8_upto<WHOLE>(y + (long)(t + i) * D, o, p.left);
+            store4_upto<WHOLE>(y + (long)(t + i) * D, o, p.left);
 #pragma unroll
             for (int j = W - 1; j > 1; --j) last[j - 1] = last[j - 2];
             if (W > 1) last[0] = in[i];
@@ -99,86 +101,87 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvArgs a) {
 // A workgroup takes 32 pieces of eight channels and eight runs of tokens of one
 // batch row, so that the weights' gradients are summed in LDS over the runs and
 // written once a workgroup: partial[part][W + 1][D].
-constexpr int kConvPieces = 32, kConvRuns = 8;
+constexpr int kConvPieces = 64, kConvRuns = 8, kConvThreads = kConvPieces * kConvRuns, kConvColumns = kConvPieces * kConvChannels;
 template <int W, bool WHOLE, typename In>
-__global__ __launch_bounds__(256) void causal_conv_bwd_kernel(ConvBwdArgs a) {
-    __shared__ float red[kConvRuns][kConvPieces * 8 + 4];
-    const int piece = threadIdx.x % kConvPieces, slot = threadIdx.x / kConvPieces, D = a.f.D;
-    const int groups = (D + 8 * kConvPieces - 1) / (8 * kConvPieces);
+__global__ __launch_bounds__(kConvThreads) void causal_conv_bwd_kernel(ConvBwdArgs a) {
+    __shared__ float red[kConvRuns][kConvPieces * kConvChannels + 4];
+    // a wave's lanes are the pieces of one run
+    const int piece = threadIdx.x % kConvPieces, slot = __builtin_amdgcn_readfirstlane(threadIdx.x / kConvPieces), D = a.f.D;
+    const int groups = (D + kConvColumns - 1) / kConvColumns;
     const long part = blockIdx.x / groups;
-    const int d0 = 8 * ((int)(blockIdx.x - part * groups) * kConvPieces + piece), left = D - d0;
+    const int d0 = kConvChannels * ((int)(blockIdx.x - part * groups) * kConvPieces + piece), left = D - d0;
     const long b = part / a.f.segs;
     const int run = a.f.run, t0 = ((int)(part - b * a.f.segs) * kConvRuns + slot) * run;
     const bool live = left > 0 && t0 < a.f.T;
-    f32x8 dw[W + 1] = {};   // the weights', then the bias's
+    f32x4 dw[W + 1] = {};   // the weights', then the bias's
     if (live) {
         const int n = conv_length(a.f.lens, b, a.f.T), end = min(t0 + run, a.f.T);
         const In* x = static_cast<const In*>(a.f.x) + b * a.f.xb + d0;
         const In* dy = static_cast<const In*>(a.grad_y) + b * (long)a.f.T * D + d0;
         const In* hist = a.f.hist ? static_cast<const In*>(a.f.hist) + b * (W - 1) * D + d0 : nullptr;
         In* dx = static_cast<In*>(a.grad_x) + b * a.gxb + d0;
-        f32x8 w[W], bias{}, last[W], dz[W];   // last[j]: x of j + 1 tokens back; dz[j]: of j tokens back
+        f32x4 w[W], bias{}, last[W], dz[W];   // last[j]: x of j + 1 tokens back; dz[j]: of j tokens back
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j] = load8_upto<WHOLE>(a.f.w + (long)j * D + d0, left);
-        if (a.f.bias) bias = load8_upto<WHOLE>(a.f.bias + d0, left);
+        for (int j = 0; j < W; ++j) w[j] = load4_upto<WHOLE>(a.f.w + (long)j * D + d0, left);
+        if (a.f.bias) bias = load4_upto<WHOLE>(a.f.bias + d0, left);
 #pragma unroll
         for (int j = 1; j < W; ++j) last[j - 1] = conv_row<W, WHOLE>(x, a.f.xt, hist, t0 - j, n, D, left);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dz[j] = f32x8{};
+        for (int j = 0; j < W; ++j) dz[j] = f32x4{};
         // dx of a token is complete W - 1 tokens later; the last of them are the next run's
         const int stop = end + W - 1;
         for (int t = t0; t < stop; t += 4) {
-            f32x8 in[4], g[4];
+            f32x4 in[4], g[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool on = t + i < min(n, stop);
-                in[i] = on ? load8_upto<WHOLE>(x + (long)(t + i) * a.f.xt, left) : f32x8{};
-                g[i] = on ? load8_upto<WHOLE>(dy + (long)(t + i) * D, left) : f32x8{};
+                in[i] = on ? load4_upto<WHOLE>(x + (long)(t + i) * a.f.xt, left) : f32x4{};
+                g[i] = on ? load4_upto<WHOLE>(dy + (long)(t + i) * D, left) : f32x4{};
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int at = t + i;
                 if (at >= stop) break;
-                f32x8 cur{};
+                f32x4 cur{};
                 if (at < n)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float z = bias.v[e] + w[0].v[e] * in[i].v[e];
+                    for (int e = 0; e < 4; ++e) {
+                        float z = bias[e] + w[0][e] * in[i][e];
 #pragma unroll
-                        for (int j = 1; j < W; ++j) z += w[j].v[e] * last[j - 1].v[e];
+                        for (int j = 1; j < W; ++j) z += w[j][e] * last[j - 1][e];
                         const float s = a.f.silu ? conv_act<In>(z) : 1.0f;
-                        cur.v[e] = a.f.silu ? g[i].v[e] * s * (1.0f + z * (1.0f - s)) : g[i].v[e];
+                        cur[e] = a.f.silu ? g[i][e] * s * (1.0f + z * (1.0f - s)) : g[i][e];
                     }
                 if (at < end)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        dw[0].v[e] += cur.v[e] * in[i].v[e];
+                    for (int e = 0; e < 4; ++e) {
+                        dw[0][e] += cur[e] * in[i][e];
 #pragma unroll
-                        for (int j = 1; j < W; ++j) dw[j].v[e] += cur.v[e] * last[j - 1].v[e];
-                        dw[W].v[e] += cur.v[e];
+                        for (int j = 1; j < W; ++j) dw[j][e] += cur[e] * last[j - 1][e];
+                        dw[W][e] += cur[e];
                     }
 #pragma unroll
                 for (int j = W - 1; j > 0; --j) dz[j] = dz[j - 1];
                 dz[0] = cur;
                 const int to = at - (W - 1);
                 if (to >= t0 && to < end) {
-                    f32x8 o{};
+                    f32x4 o{};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int j = 0; j < W; ++j) o.v[e] += w[j].v[e] * dz[W - 1 - j].v[e];
-                    store8_upto<WHOLE>(dx + (long)to * a.gxt, o, left);
+                        for (int j = 0; j < W; ++j) o[e] += w[j][e] * dz[W - 1 - j][e];
+                    store4_upto<WHOLE>(dx + (long)to * a.gxt, o, left);
                 }
                 // the history's rows see the first W - 1 tokens only: row i (token i - (W - 1))
                 // takes w_j dz_{i - (W - 1) + j}, all of which are known after token i
                 if (W > 1 && t0 == 0 && a.grad_hist && at < W - 1) {
-                    f32x8 o{};
+                    f32x4 o{};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 4; ++e)
 #pragma unroll
                         for (int j = 1; j < W; ++j)
-                            if (W - 1 - j <= at) o.v[e] += w[j].v[e] * dz[W - 1 - j].v[e];
-                    store8_upto<WHOLE>(static_cast<In*>(a.grad_hist) + (b * (W - 1) + at) * D + d0, o, left);
+                            if (W - 1 - j <= at) o[e] += w[j][e] * dz[W - 1 - j][e];
+                    store4_upto<WHOLE>(static_cast<In*>(a.grad_hist) + (b * (W - 1) + at) * D + d0, o, left);
                 }
 #pragma unroll
                 for (int j = W - 1; j > 1; --j) last[j - 1] = last[j - 2];
@@ -189,38 +192,37 @@ __global__ __launch_bounds__(256) void causal_conv_bwd_kernel(ConvBwdArgs a) {
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         __syncthreads();
-        *reinterpret_cast<f32x4*>(&red[slot][8 * piece]) = f32x4{dw[j].v[0], dw[j].v[1], dw[j].v[2], dw[j].v[3]};
-        *reinterpret_cast<f32x4*>(&red[slot][8 * piece + 4]) = f32x4{dw[j].v[4], dw[j].v[5], dw[j].v[6], dw[j].v[7]};
+        *reinterpret_cast<f32x4*>(&red[slot][kConvChannels * piece]) = dw[j];
         __syncthreads();
+        if (threadIdx.x >= kConvColumns) continue;
         float sum = 0.f;
 #pragma unroll
         for (int r = 0; r < kConvRuns; ++r) sum += red[r][threadIdx.x];
-        const int d = d0 - 8 * piece + (int)threadIdx.x;
+        const int d = d0 - kConvChannels * piece + (int)threadIdx.x;
         if (d < D) a.partial[(part * (W + 1) + j) * D + d] = sum;
     }
 }
 
-// grad_w [W][D] and grad_bias [D] over the parts: 64 columns of the partial rows a
-// workgroup, four runs of parts side by side.
+// grad_w [W][D] and grad_bias [D] over the parts: 32 columns of the partial rows a
+// workgroup, eight runs of parts side by side.
 __global__ __launch_bounds__(256) void conv_sums_kernel(const float* partial, long parts, int W, int D, float* grad_w,
                                                         float* grad_bias) {
-    __shared__ float red[4][64];
-    const long col = (long)blockIdx.x * 64 + threadIdx.x % 64, cols = (long)(W + 1) * D;
-    const int slot = threadIdx.x / 64;
-    float s = 0.f;
-    if (col < cols)
-        for (long p = slot; p < parts; p += 4) s += partial[p * cols + col];
-    red[slot][threadIdx.x % 64] = s;
+    __shared__ float red[8][32];
+    const long col = (long)blockIdx.x * 32 + threadIdx.x % 32, cols = (long)(W + 1) * D;
+    const int slot = threadIdx.x / 32;
+    red[slot][threadIdx.x % 32] = col < cols ? strided_sum(partial + col, slot, parts, 8, cols) : 0.f;
     __syncthreads();
     if (slot != 0 || col >= cols) return;
-    s = (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
     if (col < (long)W * D) grad_w[col] = s;
     else if (grad_bias) grad_bias[col - (long)W * D] = s;
 }
 
 template <int W, typename In>
 static void conv_go(const ConvArgs& a, unsigned blocks, hipStream_t s) {
-    if (a.D % 8 == 0) hipLaunchKernelGGL((causal_conv_kernel<W, true, In>), dim3(blocks), dim3(256), 0, s, a);
+    if (a.D % kConvChannels == 0) hipLaunchKernelGGL((causal_conv_kernel<W, true, In>), dim3(blocks), dim3(256), 0, s, a);
     else hipLaunchKernelGGL((causal_conv_kernel<W, false, In>), dim3(blocks), dim3(256), 0, s, a);
 }
 template <int W>
@@ -229,10 +231,32 @@ static void conv_dtype(const ConvArgs& a, unsigned blocks, hipStream_t s) {
     else conv_go<W, float>(a, blocks, s);
 }
 
+// Tokens a thread.  Workgroups that one more round over the card would be needed for
+// cost as much as a full round, and the rows around a run are read again: of the runs
+// that make one to six rounds the one with the fewest rows to go over, if a run of
+// `side` threads over T tokens makes `blocks` workgroups and `slots` of them fit.
+static int conv_run(int T, double blocks, int slots, int side, int W) {
+    int best = 1;
+    double least = 0.0;
+    for (int k = 1; k <= 6; ++k) {
+        const long splits = std::max(1L, (long)(k * slots / blocks));
+        const int run = std::max<long>(std::min(T, kConvLeast), (T + splits * side - 1) / (splits * side));
+        if (run < 1) return 1;   // no tokens
+        const double groups = (T + (long)run * side - 1) / ((long)run * side) * blocks;
+        const double rows = (double)(long)((groups + slots - 1) / slots) * (run + 2 * (W - 1));
+        if (k == 1 || rows < least) {
+            best = run;
+            least = rows;
+        }
+    }
+    return best;
+}
+
 hipError_t launch_causal_conv(ConvArgs a, hipStream_t s) {
-    a.run = kConvRun;
+    const long pieces = (a.D + kConvChannels - 1) / kConvChannels;
+    a.run = conv_run(a.T, (double)a.B * pieces / 256, 256 * 7, 1, a.W);
     a.segs = std::max(1, (a.T + a.run - 1) / a.run);   // without a token the history still moves on
-    const unsigned blocks = (unsigned)(((long)a.B * a.segs * ((a.D + 7) / 8) + 255) / 256);
+    const unsigned blocks = (unsigned)(((long)a.B * a.segs * pieces + 255) / 256);
     switch (a.W) {
         case 1: conv_dtype<1>(a, blocks, s); break;
         case 2: conv_dtype<2>(a, blocks, s); break;
@@ -245,8 +269,8 @@ hipError_t launch_causal_conv(ConvArgs a, hipStream_t s) {
 
 template <int W, typename In>
 static void conv_bwd_go(const ConvBwdArgs& a, unsigned blocks, hipStream_t s) {
-    if (a.f.D % 8 == 0) hipLaunchKernelGGL((causal_conv_bwd_kernel<W, true, In>), dim3(blocks), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((causal_conv_bwd_kernel<W, false, In>), dim3(blocks), dim3(256), 0, s, a);
+    if (a.f.D % kConvChannels == 0) hipLaunchKernelGGL((causal_conv_bwd_kernel<W, true, In>), dim3(blocks), dim3(kConvThreads), 0, s, a);
+    else hipLaunchKernelGGL((causal_conv_bwd_kernel<W, false, In>), dim3(blocks), dim3(kConvThreads), 0, s, a);
 }
 template <int W>
 static void conv_bwd_dtype(const ConvBwdArgs& a, unsigned blocks, hipStream_t s) {
@@ -254,13 +278,14 @@ static void conv_bwd_dtype(const ConvBwdArgs& a, unsigned blocks, hipStream_t s)
     else conv_bwd_go<W, float>(a, blocks, s);
 }
 
-long conv_bwd_parts(long B, int T) { return B * ((T + (long)kConvRun * kConvRuns - 1) / ((long)kConvRun * kConvRuns)); }
+long conv_bwd_parts(long B, int T) { return B * ((T + (long)kConvLeast * kConvRuns - 1) / ((long)kConvLeast * kConvRuns)); }
 
 hipError_t launch_causal_conv_bwd(ConvBwdArgs a, hipStream_t s) {
-    a.f.run = kConvRun;
-    a.f.segs = (int)((a.f.T + (long)kConvRun * kConvRuns - 1) / ((long)kConvRun * kConvRuns));
-    const long parts = conv_bwd_parts(a.f.B, a.f.T);
-    const unsigned blocks = (unsigned)(parts * ((a.f.D + 8 * kConvPieces - 1) / (8 * kConvPieces)));
+    const long groups = (a.f.D + kConvColumns - 1) / kConvColumns;
+    a.f.run = conv_run(a.f.T, (double)a.f.B * groups, 256 * 2, kConvRuns, a.f.W);
+    a.f.segs = (int)((a.f.T + (long)a.f.run * kConvRuns - 1) / ((long)a.f.run * kConvRuns));
+    const long parts = (long)a.f.B * a.f.segs;
+    const unsigned blocks = (unsigned)(parts * groups);
     switch (a.f.W) {
         case 1: conv_bwd_dtype<1>(a, blocks, s); break;
         case 2: conv_bwd_dtype<2>(a, blocks, s); break;
@@ -271,7 +296,7 @@ hipError_t launch_causal_conv_bwd(ConvBwdArgs a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const long cols = (long)(a.f.W + 1) * a.f.D;
-    hipLaunchKernelGGL(conv_sums_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, s, a.partial, parts, a.f.W, a.f.D,
+    hipLaunchKernelGGL(conv_sums_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, s, a.partial, parts, a.f.W, a.f.D,
                        a.grad_w, a.grad_bias);
     return hipGetLastError();
 }

@@ -118,4 +118,46 @@ __device__ __forceinline__ void store8_upto(bf16_t* p, const f32x8& r, int left)
     }
 }
 
+// The same of four elements.
+template <bool WHOLE, typename In>
+__device__ __forceinline__ f32x4 load4_upto(const In* p, int left) {
+    if (WHOLE || left >= 4) return load4_el(p);
+    f32x4 r{};
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+        if (e < left) r[e] = to_f32(p[e]);
+    return r;
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store4_upto(float* p, const f32x4& r, int left) {
+    if (WHOLE || left >= 4) __builtin_nontemporal_store(f32x4_el{r[0], r[1], r[2], r[3]}, reinterpret_cast<f32x4_el*>(p));
+    else
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) p[e] = r[e];
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store4_upto(bf16_t* p, const f32x4& r, int left) {
+    if (WHOLE || left >= 4)
+        __builtin_nontemporal_store(u32x2_el{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])}, reinterpret_cast<u32x2_el*>(p));
+    else
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < left) store1(p + e, r[e]);
+}
+
+// p[i pitch] summed over i = first, first + step, .. below n, in that order, eight
+// loads on their way at a time.
+__device__ __forceinline__ float strided_sum(const float* p, long first, long n, long step, long pitch) {
+    float s = 0.f;
+    for (long i = first; i < n; i += 8 * step) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = i + e * step < n ? p[(i + e * step) * pitch] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += v[e];
+    }
+    return s;
+}
+
 }  // namespace mesa

@@ -1083,8 +1083,8 @@ static mesa_status conv_checks(const void* x, int dtype, const float* w, int wid
     if (!w || (T > 0 && !x)) return fail(MESA_ERR_INVALID_ARGUMENT, "w, and x when T > 0, must be non-null");
     if (!aligned(w, 16) || !aligned(bias, 16) || !aligned(hist, 16) || !aligned(lens, 4))
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for w, bias and hist, 4 B for lens)");
-    // threads: one for eight channels of a run of tokens, in the backward 256 for 256 channels of eight runs
-    const double pieces = ((double)D + 255) / 8, runs = (double)T / mesa::kConvRun + mesa::kConvRun;
+    // threads: one for four channels of a run of tokens, in the backward 512 for 256 channels of eight runs
+    const double pieces = ((double)D + 255) / 4, runs = (double)T / mesa::kConvLeast + mesa::kConvLeast;
     if (B * pieces * runs > kMaxThreads) return fail(MESA_ERR_INVALID_ARGUMENT, "grid too large (B=%d T=%d D=%d)", B, T, D);
     return MESA_OK;
 }

@@ -169,7 +169,7 @@ hipError_t launch_residual_norm_bwd(const ResidualNormBwdArgs& a, hipStream_t s)
 struct RowStrides { long batch, head, token; };
 
 // Short causal convolution over rows [B, T, D] (causal_conv.hip).
-constexpr int kConvRun = 32;        // tokens a thread
+constexpr int kConvLeast = 16;      // the fewest tokens a thread takes, if there are as many
 constexpr int kConvMaxWidth = 4;    // widest window the kernels are built for
 struct ConvArgs {
     const void* x; long xb; long xt;   // batch and token strides
@@ -185,7 +185,7 @@ struct ConvBwdArgs {
     float* grad_w; float* grad_bias;
     float* partial;                    // workspace: [conv_bwd_parts][W + 1][D]
 };
-long conv_bwd_parts(long B, int T);
+long conv_bwd_parts(long B, int T);   // at most
 hipError_t launch_causal_conv(ConvArgs a, hipStream_t s);
 hipError_t launch_causal_conv_bwd(ConvBwdArgs a, hipStream_t s);
 

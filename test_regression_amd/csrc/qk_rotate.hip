@@ -211,18 +211,17 @@ __global__ __launch_bounds__(256) void qk_rotate_bwd_kernel(RotateBwdArgs g) {
     }
 }
 
-// grad_wq and grad_wk over the workgroups' parts: 16 columns a workgroup, 16 runs of
+// grad_wq and grad_wk over the workgroups' parts: eight columns a workgroup, 32 runs of
 // parts side by side.
 __global__ __launch_bounds__(256) void rotate_sums_kernel(const float* partial, long parts, int d, float* gq, float* gk) {
-    __shared__ float red[16][17];
-    const int col = blockIdx.x * 16 + threadIdx.x % 16, slot = threadIdx.x / 16;
-    float s = 0.f;
-    for (long p = slot; p < parts; p += 16) s += partial[p * 2 * d + col];
-    red[slot][threadIdx.x % 16] = s;
+    __shared__ float red[32][8];
+    const int col = blockIdx.x * 8 + threadIdx.x % 8, slot = threadIdx.x / 8;
+    red[slot][threadIdx.x % 8] = strided_sum(partial + col, slot, parts, 32, 2L * d);
     __syncthreads();
     if (slot != 0) return;
-    s = 0.f;
-    for (int i = 0; i < 16; ++i) s += red[i][threadIdx.x];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
     float* to = col < d ? gq : gk;
     if (to) to[col % d] = s;
 }
@@ -273,7 +272,7 @@ hipError_t launch_qk_rotate_bwd(RotateBwdArgs a, hipStream_t s) {
     if (!a.f.norm || (!a.grad_wq && !a.grad_wk)) a.partial = nullptr;
     const hipError_t e = rotate_sized(a, a.f.d, a.f.bf16, blocks, s);
     if (e != hipSuccess || !a.partial) return e;
-    hipLaunchKernelGGL(rotate_sums_kernel, dim3((unsigned)(2 * a.f.d / 16)), dim3(256), 0, s, a.partial, (long)blocks, a.f.d,
+    hipLaunchKernelGGL(rotate_sums_kernel, dim3((unsigned)(2 * a.f.d / 8)), dim3(256), 0, s, a.partial, (long)blocks, a.f.d,
                        a.grad_wq, a.grad_wk);
     return hipGetLastError();
 }
