@@ -146,6 +146,44 @@ __device__ __forceinline__ void store4_upto(bf16_t* p, const f32x4& r, int left)
             if (e < left) store1(p + e, r[e]);
 }
 
+// Four elements on their way: as stored, so that nothing waits for them before get().
+template <bool WHOLE, typename In> struct Held4 {
+    f32x4 v;
+    __device__ __forceinline__ void load(const In* p, int left) { v = load4_upto<WHOLE>(p, left); }
+    __device__ __forceinline__ void clear() { v = f32x4{}; }
+    __device__ __forceinline__ f32x4 get() const { return v; }
+};
+template <> struct Held4<true, bf16_t> {
+    u32x2_el w;
+    __device__ __forceinline__ void load(const bf16_t* p, int) { w = *reinterpret_cast<const u32x2_el*>(p); }
+    __device__ __forceinline__ void clear() { w = u32x2_el{}; }
+    __device__ __forceinline__ f32x4 get() const {
+        return f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                     __uint_as_float(w[1] & 0xffff0000u)};
+    }
+};
+
+// Eight elements of a whole piece on their way.
+template <typename In> struct Held8;
+template <> struct Held8<bf16_t> {
+    u32x4_el w;
+    __device__ __forceinline__ void load(const bf16_t* p) { w = *reinterpret_cast<const u32x4_el*>(p); }
+    __device__ __forceinline__ f32x8 get() const {
+        f32x8 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            r.v[2 * i] = __uint_as_float(w[i] << 16);
+            r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+        return r;
+    }
+};
+template <> struct Held8<float> {
+    f32x8 r;
+    __device__ __forceinline__ void load(const float* p) { r = load8_upto<true>(p, 8); }
+    __device__ __forceinline__ f32x8 get() const { return r; }
+};
+
 // p[i pitch] summed over i = first, first + step, .. below n, in that order, eight
 // loads on their way at a time.
 __device__ __forceinline__ float strided_sum(const float* p, long first, long n, long step, long pitch) {

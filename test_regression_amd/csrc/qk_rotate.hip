@@ -118,8 +118,12 @@ __device__ __forceinline__ void rotate_heads(const RotateArgs& a, const Turns<IN
 #pragma unroll
     for (int e = 0; e < 8; ++e) wv.v[e] = 1.0f;
     if (w) wv = load8_upto<true>(w + d0, 8);
-    for (int h = slot; h < (KEY ? a.Hk : a.Hq); h += a.slots) {
-        f32x8 x = load8_upto<true>(row_in<KEY, In>(a, h, b, t) + d0, 8);
+    const int heads = KEY ? a.Hk : a.Hq;
+    Held8<In> held;   // the next head's row, on its way
+    if (slot < heads) held.load(row_in<KEY, In>(a, slot, b, t) + d0);
+    for (int h = slot; h < heads; h += a.slots) {
+        f32x8 x = held.get();
+        if (h + a.slots < heads) held.load(row_in<KEY, In>(a, h + a.slots, b, t) + d0);
         if (a.norm) {
             float ss = 0.f;
 #pragma unroll
