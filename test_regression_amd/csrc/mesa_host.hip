@@ -1217,7 +1217,7 @@ mesa_status mesa_ssm_forward(const void* x, const int64_t* x_strides, const void
         return fail(MESA_ERR_INVALID_ARGUMENT, "misaligned pointer (16 B for out, final_state and workspace)");
     const long BH = (long)B * H, nc = ssm_chunks(T);
     const int nseg = T > 0 ? mesa::ssm_segments(BH, (int)nc, dv, 1) : 1;
-    const size_t need = ssm_slot_bytes((size_t)BH * (nseg - 1), dk, dv);
+    const size_t need = ssm_slot_bytes((size_t)BH * mesa::ssm_slots(nseg, 1), dk, dv);
     if (workspace_bytes < need || (need && !workspace))
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace ? workspace_bytes : 0, need);
     const size_t sb = (size_t)BH * dv * dk * sizeof(float), hb = (size_t)H * 4;
@@ -1249,13 +1249,14 @@ mesa_status mesa_ssm_forward(const void* x, const int64_t* x_strides, const void
 // Backward workspace, offsets in bytes (every piece a multiple of 16): the chunk
 // states S and R, the heads' sums, the segments' `slots`, `parts` of dB and dC for a
 // chunk's group of heads.
-struct SsmBwdLayout { size_t R, sums, seg, part, total; };
+struct SsmBwdLayout { size_t R, sums, decay, seg, part, total; };
 static SsmBwdLayout ssm_bwd_layout(int B, int H, int T, int dk, int dv, size_t slots, size_t parts) {
     const size_t nc = ssm_chunks(T), states = (size_t)B * H * nc * dk * dv * sizeof(float);
     SsmBwdLayout l{};
     l.R = states;
     l.sums = 2 * states;
-    l.seg = l.sums + ((size_t)H * 3 * B * nc * sizeof(double) + 15) / 16 * 16;
+    l.decay = l.sums + (size_t)H * 3 * B * nc * sizeof(double);
+    l.seg = (l.decay + (size_t)H * 2 * B * nc * sizeof(float) + 15) / 16 * 16;
     l.part = l.seg + ssm_slot_bytes(slots, dk, dv);
     l.total = l.part + parts * 2 * mesa::kSsmChunk * dk * sizeof(float);
     return l;
@@ -1291,7 +1292,7 @@ mesa_status mesa_ssm_backward(const void* x, const int64_t* x_strides, const voi
     const long BH = (long)B * H, nc = ssm_chunks(T);
     const int parts = T > 0 ? mesa::ssm_grad_parts(B, Hk, H, (int)nc) : 1;
     const int nseg = T > 0 ? mesa::ssm_segments(BH, (int)nc, dv, 2) : 1;
-    const SsmBwdLayout l = ssm_bwd_layout(B, H, T, dk, dv, 2 * (size_t)BH * (nseg - 1), parts > 1 ? (size_t)parts * B * Hk * nc : 0);
+    const SsmBwdLayout l = ssm_bwd_layout(B, H, T, dk, dv, (size_t)BH * mesa::ssm_slots(nseg, 2), parts > 1 ? (size_t)parts * B * Hk * nc : 0);
     if (T > 0 && workspace_bytes < l.total)
         return fail(MESA_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", workspace_bytes, l.total);
     const size_t sb = (size_t)BH * dv * dk * sizeof(float), hb = (size_t)H * 4;
@@ -1322,7 +1323,8 @@ mesa_status mesa_ssm_backward(const void* x, const int64_t* x_strides, const voi
     a.f = mesa::SsmArgs{x, vx.s, b, vb.s, c, vc.s, dt, vd.s, dt_dtype == MESA_DTYPE_BF16, A, D, dt_bias, softplus, state0, lens,
                         BH, B, Hk, H, T, dk, dv, (int)nc, dtype == MESA_DTYPE_BF16, nullptr, nullptr, nseg,
                         (int)((nc + nseg - 1) / nseg), reinterpret_cast<float*>(ws + l.seg),
-                        reinterpret_cast<float*>(ws + l.seg) + 2 * (size_t)BH * (nseg - 1) * dv * dk, grad_out, grad_final, grad_state, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.R)};
+                        reinterpret_cast<float*>(ws + l.seg) + (size_t)BH * mesa::ssm_slots(nseg, 2) * dv * dk, grad_out, grad_final,
+                        grad_state, reinterpret_cast<float*>(ws), reinterpret_cast<float*>(ws + l.R), reinterpret_cast<float*>(ws + l.decay)};
     a.grad_x = grad_x;
     a.gxs = gx.s;
     a.grad_b = grad_b;

@@ -200,10 +200,12 @@ struct SsmArgs {
     long BH; int B; int Hk; int H; int T; int dk; int dv; int nc; int bf16;
     void* out; float* final_state;     // the step: its state
     int nseg; int seg_chunks;          // segments of a sequence that are passed over at once, chunks of one
-    float* seg_start;                  // nseg > 1, workspace: [sides][BH][nseg - 1] states, the ends, then the next starts
-    float* seg_decay;                  // [sides][BH][nseg - 1]
+    float* seg_start;                  // nseg > 1, workspace: ssm_slots states, segments' ends, then the next ones' starts
+    float* seg_decay;                  // one a state
     const void* grad_out; const float* grad_final; float* grad_state;   // backward
-    float* S; float* R;                // backward workspace [BH][nc][dk][dv]: states at the chunks' starts, gradients at their ends
+    // backward workspace [BH][nc][dk][dv]: states at the chunks' starts, gradients at their ends, both as they come
+    // from their segment; [2][BH][nc]: the decay from the segment's start to there
+    float* S; float* R; float* chunk_decay;
 };
 struct SsmGradArgs {
     SsmArgs f;
@@ -215,7 +217,9 @@ struct SsmGradArgs {
 };
 constexpr int kSsmGradGroups = 512;   // workgroups of the gradients, where splitting the heads gives more
 int ssm_segments(long BH, int nc, int dv, int sides);         // the number of segments; the backward has two sides
-long ssm_segment_slots(long BH, int nc, int dv, int sides);   // the most sides BH (segments - 1) of any smaller batch and length
+// Segments' ends that are kept for a head: of all but the last, and for the gradients of both directions with it.
+constexpr int ssm_slots(int nseg, int sides) { return nseg == 1 ? 0 : sides == 1 ? nseg - 1 : 2 * nseg; }
+long ssm_segment_slots(long BH, int nc, int dv, int sides);   // the most BH ssm_slots of any smaller batch and length
 int ssm_grad_parts(long B, int Hk, int H, int nc);
 hipError_t launch_ssm_scan(const SsmArgs& a, hipStream_t s);
 hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s);   // S and R

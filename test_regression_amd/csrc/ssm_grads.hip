@@ -171,6 +171,30 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             r4[q] = load4(lane_at(a.R + at + 16 * q, lo));
         }
     };
+    // what the states take from their segments' starts, whose rows are read here (they
+    // stay in the caches) while the pairs are formed
+    const int seg[2] = {chunk / a.seg_chunks, (a.nc - 1 - chunk) / a.seg_chunks};
+    auto fetch_starts = [&](int k, f32x4 (&start)[2][4]) {
+        if (16 * nt >= dk) return;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            if (seg[side] == 0) continue;
+            const long bh = (long)side * a.BH + b * a.H + head(k);
+            const float* from = a.seg_start + ((bh * a.nseg + seg[side] - 1) * dk + 16 * nt) * a.dv + column(k);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (16 * q < cols) start[side][q] = load4(lane_at(from + 16 * q, (m * a.dv + 4 * g) * 4));
+        }
+    };
+    auto add_starts = [&](int k, const f32x4 (&start)[2][4]) {
+        const float* by = a.chunk_decay + (b * a.H + head(k)) * a.nc + chunk;
+        const float ds = by[0], dr = by[a.BH * a.nc];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (seg[0] != 0) s4[q] += ds * start[0][q];
+            if (seg[1] != 0) r4[q] += dr * start[1][q];
+        }
+    };
     float raw = 0.f;   // wave 7: the raw step sizes, and the next head's
     uint32_t next_raw = 0u;
     auto fetch_raw = [&](int h) {
@@ -233,6 +257,8 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         sg.store(G);
         __syncthreads();
         if (k + 1 < all) fetch(k + 1);
+        f32x4 start[2][4] = {};
+        fetch_starts(k, start);
         // the pairs
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -272,6 +298,8 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         // dC and dB of the states, transposed: rows of dk, columns of tokens
         if (16 * nt < dk) {
             const int lane = lane_again(), m = lane % 16, g = lane / 16;
+            add_starts(k, start);
+            __builtin_amdgcn_sched_barrier(0);   // the starts' registers are free from here on
             double carry = 0.0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) carry += dot4(s4[q], r4[q]);

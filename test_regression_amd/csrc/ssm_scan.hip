@@ -433,17 +433,19 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
 
 // Passes that only carry a state: S' = e^{l_63} S + a sum of weighted outer products,
 // of b and x from the front, or (BACK) of c and the outputs' gradients from the back:
-// R' = e^{l_63} R + C^T diag(e^l) g.  ENDS: the end states of all segments but the
-// last, from zero but for the first's; otherwise the states at every chunk's start
-// (BACK: the gradients of its end) for the gradients, from the segments' real starts.
-// FLIP: states as [dk][dv], a lane's rows v + 4 g + r and columns 16 i + m of dk, as
-// the gradients take them; else rows 16 i + 4 g + r of dk, column v + m.
-template <int N, typename In, bool ENDS, bool FLIP, bool BACK>
+// R' = e^{l_63} R + C^T diag(e^l) g.  A segment starts from zero (the first from the
+// state or gradient that is given) and leaves its end and its decay.  STATES, for the
+// gradients: also the states at every chunk's start (BACK: the gradients of its end),
+// as far as they come from their segment, and the decay from the segment's start to
+// there, with which the gradients add the segments' starts; these states are [dk][dv],
+// a lane's rows v + 4 g + r and columns 16 i + m of dk.  Without STATES a lane holds rows
+// 16 i + 4 g + r of dk, column v + m.
+template <int N, typename In, bool STATES, bool BACK>
 __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, const SsmPlace& p) {
     const int dk = N > 32 ? N : a.dk;
     typedef Plane<In, 64> PV;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16;
-    const int hk = p.h / (a.H / a.Hk), segs = a.nseg - 1;
+    const int hk = p.h / (a.H / a.Hk), slots = STATES ? a.nseg : a.nseg - 1;
     // chunks of the segment, counted from where the pass starts
     const int begin = p.seg * a.seg_chunks, end = min(a.nc, begin + a.seg_chunks), real = (p.valid + kSC - 1) / kSC;
     const bool mine = 16 * wave < p.cols;
@@ -454,7 +456,7 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
                         : static_cast<const In*>(a.x) + p.b * a.xs.batch + p.h * a.xs.head + p.v0;
     const long xt = BACK ? a.dv : a.xs.token;
     const float A = a.A[p.h];
-    float* seg = a.seg_start + (BACK ? a.BH * segs * a.dv * dk : 0);
+    const long slot = (BACK ? a.BH + p.bh : p.bh) * slots + p.seg;
 
     f32x4 st[N / 16] = {};
     const float* from = p.seg == 0 ? (BACK ? a.grad_final : a.state0) : nullptr;
@@ -463,16 +465,12 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
 #pragma unroll
         for (int i = 0; i < N / 16; ++i) {
             if (16 * i >= dk) continue;
-            if constexpr (!FLIP) st[i] = load4(from + (long)(v + m) * dk + 16 * i + 4 * g);
+            if constexpr (!STATES) st[i] = load4(from + (long)(v + m) * dk + 16 * i + 4 * g);
             else
 #pragma unroll
                 for (int r = 0; r < 4; ++r) st[i][r] = from[(long)(v + 4 * g + r) * dk + 16 * i + m];
         }
     }
-    if (!ENDS && p.seg > 0 && mine)
-#pragma unroll
-        for (int i = 0; i < N / 16; ++i)
-            if (16 * i < dk) st[i] = load4(seg + (p.bh * segs + p.seg - 1) * a.dv * dk + (long)(16 * i + m) * a.dv + v + 4 * g);
     Stage<In, N> sb(ks.token, dk);
     Stage<In, 64> sx(xt, p.cols);
     uint32_t raw = 0u;   // wave 3: the step sizes to come
@@ -502,7 +500,9 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
     }
     double total = 0.0;
     for (int k = k0; k < k1; ++k) {
-        if (!ENDS && mine) {
+        if (STATES && p.v0 == 0 && threadIdx.x == 0)
+            a.chunk_decay[(BACK ? a.BH + p.bh : p.bh) * a.nc + chunk_of(k)] = exp2_small(total);
+        if (STATES && mine) {
             float* to = (BACK ? a.R : a.S) + (p.bh * a.nc + chunk_of(k)) * dk * a.dv + v + 4 * g;
 #pragma unroll
             for (int i = 0; i < N / 16; ++i)
@@ -513,66 +513,73 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
         __syncthreads();
         if (k + 1 < k1) fetch(k + 1);
         const Scalars& sl = S.s[k % 2];
-        if (ENDS) total += sl.l[63];
+        total += sl.l[63];
         if (wave == 3) scalars(k + 1);
         if (mine) {
             const auto w0 = weighted<PV>(S.x.col(wave, 0, m, g), BACK ? sl.in : sl.write, 0, g);
             const auto w1 = weighted<PV>(S.x.col(wave, 1, m, g), BACK ? sl.in : sl.write, 1, g);
-            add_outer<N, FLIP, FLIP>(st, sl.decay, S.b, w0, w1, m, g);
+            add_outer<N, STATES, STATES>(st, sl.decay, S.b, w0, w1, m, g);
         }
         __syncthreads();
     }
     if (!mine) return;
-    if constexpr (ENDS) {
-        const long at = p.bh * segs + p.seg;
-        if (p.v0 == 0 && threadIdx.x == 0) a.seg_decay[(BACK ? a.BH * segs : 0) + at] = exp2_small(total);
-#pragma unroll
-        for (int i = 0; i < N / 16; ++i) {
-            if (16 * i >= dk) continue;
-            if constexpr (FLIP) store4(seg + at * a.dv * dk + (long)(16 * i + m) * a.dv + v + 4 * g, st[i]);
-            else store4(seg + (at * a.dv + v + m) * dk + 16 * i + 4 * g, st[i]);
-        }
-    } else if (BACK && a.grad_state && p.seg == a.nseg - 1) {
+    if (STATES && a.nseg == 1) {
+        if (!BACK || !a.grad_state) return;
 #pragma unroll
         for (int i = 0; i < N / 16; ++i)
             if (16 * i < dk)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) a.grad_state[(p.bh * a.dv + v + 4 * g + r) * dk + 16 * i + m] = st[i][r];
+        return;
+    }
+    if (p.v0 == 0 && threadIdx.x == 0) a.seg_decay[slot] = exp2_small(total);
+    float* to = a.seg_start + slot * a.dv * dk;
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+        if (16 * i >= dk) continue;
+        if constexpr (STATES) store4(to + (long)(16 * i + m) * a.dv + v + 4 * g, st[i]);
+        else store4(to + (long)(v + m) * dk + 16 * i + 4 * g, st[i]);
     }
 }
 
 template <int N, typename In>
 __global__ __launch_bounds__(256, 2) void ssm_ends_kernel(SsmArgs a) {
     __shared__ CarryLds<N, In> S;
-    ssm_carry<N, In, true, false, false>(a, S, ssm_place(a, xcd_order(), a.nseg - 1));
+    ssm_carry<N, In, false, false>(a, S, ssm_place(a, xcd_order(), a.nseg - 1));
 }
 // Both directions of the gradients side by side.
-template <int N, typename In, bool ENDS>
+template <int N, typename In>
 __global__ __launch_bounds__(256, 2) void ssm_states_kernel(SsmArgs a) {
     __shared__ CarryLds<N, In> S;
-    const SsmPlace p = ssm_place(a, xcd_order() / 2, ENDS ? a.nseg - 1 : a.nseg);
-    if (xcd_order() % 2) ssm_carry<N, In, ENDS, true, true>(a, S, p);
-    else ssm_carry<N, In, ENDS, true, false>(a, S, p);
+    const SsmPlace p = ssm_place(a, xcd_order() / 2, a.nseg);
+    if (xcd_order() % 2) ssm_carry<N, In, true, true>(a, S, p);
+    else ssm_carry<N, In, true, false>(a, S, p);
 }
 
-// Segments' ends, from the first's real one on, into the next segments' starts:
-// start_{s+1} = decay_s start_s + end_s, in place.
-__global__ __launch_bounds__(256) void ssm_join_kernel(float* seg, const float* decay, long n, int per, int ends) {
-    const long i = (long)blockIdx.x * 256 + threadIdx.x;   // one of BH * per elements
+// Segments' ends, the first's being the real one, into the next segments' starts, in
+// place: start_{s+1} = decay_s start_s + end_s.  Of the gradients' second direction
+// (rows bh from `back` on) the last segment's end too, as the start state's gradient,
+// transposed.
+__global__ __launch_bounds__(256) void ssm_join_kernel(float* seg, const float* decay, long n, int dk, int dv, int slots, int starts,
+                                                       long back, float* grad_state) {
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
+    const int per = dk * dv, at = (int)(i % per);
     const long bh = i / per;
-    float* p = seg + bh * ends * per + i % per;
+    float* p = seg + bh * slots * per + at;
     float s = p[0];
-    for (int e = 1; e < ends; ++e) {
-        s = decay[bh * ends + e] * s + p[(long)e * per];
+    for (int e = 1; e < starts; ++e) {
+        s = decay[bh * slots + e] * s + p[(long)e * per];
         p[(long)e * per] = s;
     }
+    if (grad_state && bh >= back)
+        grad_state[(bh - back) * per + (long)(at % dv) * dk + at / dv] = decay[bh * slots + starts] * s + p[(long)starts * per];
 }
 
 // Workgroups from which on ssm_walk_kernel leaves too few CUs idle for segments to pay
 // (measured per chunk and CU: 3.7 us against 3.3 us and 1.05 us for the ends).
 constexpr long kSsmCUs = 256, kSsmWalk = 216;
-enum SsmPass { kOut, kOutEnds, kStates, kStatesEnds };
+enum SsmPass { kOut, kEnds, kStates };
 template <int N, typename In>
 static void scan_go(const SsmArgs& a, SsmPass pass, unsigned blocks, hipStream_t s) {
     const dim3 grid(blocks), block(256);
@@ -585,9 +592,8 @@ static void scan_go(const SsmArgs& a, SsmPass pass, unsigned blocks, hipStream_t
                 }
             hipLaunchKernelGGL((ssm_out_kernel<N, In>), grid, block, 0, s, a);
             break;
-        case kOutEnds: hipLaunchKernelGGL((ssm_ends_kernel<N, In>), grid, block, 0, s, a); break;
-        case kStates: hipLaunchKernelGGL((ssm_states_kernel<N, In, false>), grid, block, 0, s, a); break;
-        case kStatesEnds: hipLaunchKernelGGL((ssm_states_kernel<N, In, true>), grid, block, 0, s, a); break;
+        case kEnds: hipLaunchKernelGGL((ssm_ends_kernel<N, In>), grid, block, 0, s, a); break;
+        case kStates: hipLaunchKernelGGL((ssm_states_kernel<N, In>), grid, block, 0, s, a); break;
     }
 }
 template <int N>
@@ -596,29 +602,27 @@ static void scan_type(const SsmArgs& a, SsmPass pass, unsigned blocks, hipStream
     else scan_go<N, float>(a, pass, blocks, s);
 }
 static hipError_t scan_pass(const SsmArgs& a, SsmPass pass, hipStream_t s) {
-    const long segs = pass == kOutEnds || pass == kStatesEnds ? a.nseg - 1 : a.nseg;
-    const unsigned blocks = (unsigned)(a.BH * segs * ((a.dv + 63) / 64) * (pass >= kStates ? 2 : 1));
+    const unsigned blocks = (unsigned)(a.BH * (pass == kEnds ? a.nseg - 1 : a.nseg) * ((a.dv + 63) / 64) * (pass == kStates ? 2 : 1));
     if (a.dk <= 32) scan_type<32>(a, pass, blocks, s);
     else if (a.dk <= 64) scan_type<64>(a, pass, blocks, s);
     else scan_type<128>(a, pass, blocks, s);
     return hipGetLastError();
 }
-// The segments' ends and from them their starts, then the pass; `sides` directions.
-static hipError_t segments(const SsmArgs& a, SsmPass ends, SsmPass pass, int sides, hipStream_t s) {
-    if (a.nseg > 1) {
-        hipError_t e = scan_pass(a, ends, s);
-        if (e != hipSuccess) return e;
-        if (a.nseg > 2) {
-            const long n = sides * a.BH * a.dv * a.dk;
-            hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.seg_start, a.seg_decay, n,
-                               a.dv * a.dk, a.nseg - 1);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
-    }
-    return scan_pass(a, pass, s);
+static hipError_t join(const SsmArgs& a, int sides, int slots, float* grad_state, hipStream_t s) {
+    const long n = sides * a.BH * a.dv * a.dk;
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.seg_start, a.seg_decay, n, a.dk, a.dv,
+                       slots, a.nseg - 1, a.BH, grad_state);
+    return hipGetLastError();
 }
-hipError_t launch_ssm_scan(const SsmArgs& a, hipStream_t s) { return segments(a, kOutEnds, kOut, 1, s); }
-hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s) { return segments(a, kStatesEnds, kStates, 2, s); }
+hipError_t launch_ssm_scan(const SsmArgs& a, hipStream_t s) {
+    hipError_t e = a.nseg > 1 ? scan_pass(a, kEnds, s) : hipSuccess;
+    if (e == hipSuccess && a.nseg > 2) e = join(a, 1, a.nseg - 1, nullptr, s);
+    return e == hipSuccess ? scan_pass(a, kOut, s) : e;
+}
+hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s) {
+    const hipError_t e = scan_pass(a, kStates, s);
+    return e == hipSuccess && (a.nseg > 2 || (a.nseg > 1 && a.grad_state)) ? join(a, 2, a.nseg, a.grad_state, s) : e;
+}
 
 // Segments of a sequence that are passed over at once: twice as many while the
 // workgroups (of `sides` directions) stay below kSsmFill and a segment keeps
@@ -637,8 +641,8 @@ int ssm_segments(long BH, int nc, int dv, int sides) {
 long ssm_segment_slots(long BH, int nc, int dv, int sides) {
     long most = 0;
     for (int n = 2; n <= kSsmMost && nc >= kSsmLeast * n; n *= 2)
-        most = std::max(most, std::min(BH, (kSsmFill - 1) / (n / 2) / ((dv + 63) / 64 * sides)) * (n - 1));
-    return most * sides;
+        most = std::max(most, std::min(BH, (kSsmFill - 1) / (n / 2) / ((dv + 63) / 64 * sides)) * ssm_slots(n, sides));
+    return most;
 }
 
 }  // namespace mesa
