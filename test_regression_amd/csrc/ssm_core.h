@@ -364,7 +364,13 @@ __device__ __forceinline__ uint32_t step_bits(const SsmArgs& a, long b, int h, l
 __device__ __forceinline__ float raw_step(const SsmArgs& a, uint32_t bits, float bias) {
     return __uint_as_float(a.dt_bf16 ? bits << 16 : bits) + bias;
 }
-__device__ __forceinline__ float step_bias(const SsmArgs& a, int h) { return a.dt_bias ? a.dt_bias[h] : 0.0f; }
+// An element of an array that no kernel writes while this one runs, at an index that
+// the wave shares: through the scalar cache, so that it does not wait behind the
+// vector loads that are on their way.
+__device__ __forceinline__ float shared_load(const float* p, long i) {
+    return reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(p))[i];
+}
+__device__ __forceinline__ float step_bias(const SsmArgs& a, int h) { return a.dt_bias ? shared_load(a.dt_bias, h) : 0.0f; }
 
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp_add(double v) {

@@ -106,12 +106,6 @@ __device__ __forceinline__ double kslot_sum(double v) {
 __device__ __forceinline__ float dot4(const f32x4& a, const f32x4& b) {
     return (a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3]);
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
-}
-
 // Two pieces of a row of the chunk states as eight k-slots.
 template <typename PV>
 __device__ __forceinline__ typename PV::Three three8(const f32x4& a, const f32x4& b) {
@@ -154,45 +148,46 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
     auto column = [&](int k) { return 64 * (k % pieces); };
 
     Stage<In, 64, kGradThreads> sx(a.xs.token, cols), sg(a.dv, cols);
-    f32x4 s4[4] = {}, r4[4] = {};   // the wave's rows of S and R: row m, columns 16 k + 4 g ..
+    f32x4 s4[4], r4[4];   // the wave's rows of S and R: row m, columns 16 k + 4 g ..
     auto fetch = [&](int k) {
         const int h = head(k), v0 = column(k);
         sx.load(static_cast<const In*>(a.x) + b * a.xs.batch + h * a.xs.head + t0 * a.xs.token + v0, a.xs.token, cols, n);
         sg.load(static_cast<const In*>(a.grad_out) + ((b * a.H + h) * a.T + t0) * a.dv + v0, a.dv, cols, n);
     };
-    auto fetch_states = [&](int k) {
-        if (16 * nt >= dk) return;
-        const long at = (((b * a.H + head(k)) * a.nc + chunk) * dk + 16 * nt) * a.dv + column(k);
-        const int lo = (m * a.dv + 4 * g) * 4;
+    // 16 rows of a state [dk][dv] from a wave's first on; zeros where there are none and
+    // past the columns, by the loads' bounds: a branch around a load waits for it
+    auto state_rows = [&](const float* p, bool there, f32x4 (&to)[4]) {
+        const int at = 16 * nt * a.dv;
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p + at), (short)0,
+                                                          there && 16 * nt < dk ? 16 * a.dv * 4 : 0, 0x00020000);
+        const uint32_t lo = (lane_again() % 16 * a.dv + 4 * (lane_again() / 16)) * 4;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {   // dv = 16, 32: zeros where nothing is
-            if (cols <= 16 * q) continue;
-            s4[q] = load4(lane_at(a.S + at + 16 * q, lo));
-            r4[q] = load4(lane_at(a.R + at + 16 * q, lo));
-        }
+        for (int q = 0; q < 4; ++q)
+            to[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, lo + (16 * q < cols ? 64u * q : 1u << 31), 0, 0));
+    };
+    auto fetch_states = [&](int k) {
+        const long at = ((b * a.H + head(k)) * a.nc + chunk) * dk * a.dv + column(k);
+        state_rows(a.S + at, true, s4);
+        state_rows(a.R + at, true, r4);
     };
     // what the states take from their segments' starts, whose rows are read here (they
     // stay in the caches) while the pairs are formed
     const int seg[2] = {chunk / a.seg_chunks, (a.nc - 1 - chunk) / a.seg_chunks};
     auto fetch_starts = [&](int k, f32x4 (&start)[2][4]) {
-        if (16 * nt >= dk) return;
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-            if (seg[side] == 0) continue;
             const long bh = (long)side * a.BH + b * a.H + head(k);
-            const float* from = a.seg_start + ((bh * a.nseg + seg[side] - 1) * dk + 16 * nt) * a.dv + column(k);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (16 * q < cols) start[side][q] = load4(lane_at(from + 16 * q, (m * a.dv + 4 * g) * 4));
+            state_rows(a.seg_start + (bh * a.nseg + seg[side] - 1) * dk * a.dv + column(k), seg[side] != 0, start[side]);
         }
     };
     auto add_starts = [&](int k, const f32x4 (&start)[2][4]) {
-        const float* by = a.chunk_decay + (b * a.H + head(k)) * a.nc + chunk;
-        const float ds = by[0], dr = by[a.BH * a.nc];
+        const long at = (b * a.H + head(k)) * a.nc + chunk;
+        const float ds = seg[0] ? shared_load(a.chunk_decay, at) : 0.0f;
+        const float dr = seg[1] ? shared_load(a.chunk_decay, a.BH * a.nc + at) : 0.0f;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (seg[0] != 0) s4[q] += ds * start[0][q];
-            if (seg[1] != 0) r4[q] += dr * start[1][q];
+            s4[q] += ds * start[0][q];
+            r4[q] += dr * start[1][q];
         }
     };
     float raw = 0.f;   // wave 7: the raw step sizes, and the next head's
@@ -203,7 +198,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
     auto scalars = [&](int h) {
         if (h >= h_last) return;
         raw = raw_step(a, next_raw, step_bias(a, h));
-        chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw, a.softplus) : 0.f, a.A[h]);
+        chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw, a.softplus) : 0.f, shared_load(a.A, h));
         fetch_raw(h + 1);
     };
     f32x4 cb[2], zsum[2] = {}, dc[TT] = {}, db[TT] = {};
@@ -256,9 +251,9 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         sx.store(X);
         sg.store(G);
         __syncthreads();
+        f32x4 start[2][4];
+        fetch_starts(k, start);   // loads come back in order: before the next rows, which come from further away
         if (k + 1 < all) fetch(k + 1);
-        f32x4 start[2][4] = {};
-        fetch_starts(k, start);
         // the pairs
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -334,8 +329,8 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             if (first == 0) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) S.r.put(16 * nt + m, g, q, r3);
-                carry = wave_sum(carry);
-                if (lane == 0) S.carry[nt] = carry;
+                carry = prefix_sum(carry);
+                if (lane == 63) S.carry[nt] = carry;
             }
         } else if (first == 0) {
             // dk = 16: zeros for the rows that are not there
@@ -362,7 +357,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             mma(o, G.col(vt, 1, m, g), {S.p.row(2 * half, 1, m, g), S.p.row(2 * half + 1, 1, m, g)});
             mma(o, G.col(vt, 0, m, g), {S.p.row(2 * half, 0, m, g), S.p.row(2 * half + 1, 0, m, g)});
             mfma_done(o);
-            const float skip = a.D ? a.D[h] : 0.0f;
+            const float skip = a.D ? shared_load(a.D, h) : 0.0f;
             In* gx = static_cast<In*>(ga.grad_x) + b * ga.gxs.batch + h * ga.gxs.head + t0 * ga.gxs.token + v0 + 16 * vt + 4 * g;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -375,8 +370,9 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             double row = 0.0, col = 0.0, rdt = 0.0, wrt = 0.0, cr = 0.0;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (q <= bi) row += S.row[q][lane];
-                if (q >= bi) col += S.col[q][lane];
+                const double r = S.row[q][lane], c = S.col[q][lane];
+                row += q <= bi ? r : 0.0;
+                col += q >= bi ? c : 0.0;
             }
 #pragma unroll
             for (int q = 0; q < N / 16; ++q) {
@@ -395,7 +391,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             if ((k + 1) % pieces == 0) {
                 double draw = 0.0, dA = 0.0;
                 if (lane < n) {
-                    const double dstep = direct + (double)a.A[h] * da;
+                    const double dstep = direct + (double)shared_load(a.A, h) * da;
                     draw = a.softplus ? dstep / (1.0 + (double)expf(-raw)) : dstep;
                     dA = step * da;
                 }
@@ -404,10 +400,10 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
                     if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, (float)draw);
                     else static_cast<float*>(ga.grad_dt)[o] = (float)draw;
                 }
-                dA = wave_sum(dA);
-                dskip = wave_sum(dskip);
-                draw = wave_sum(draw);
-                if (lane < 3) ga.sums[((long)h * 3 + lane) * a.B * a.nc + b * a.nc + chunk] = lane == 0 ? dA : lane == 1 ? dskip : draw;
+                const double sums[3] = {prefix_sum(dA), prefix_sum(dskip), prefix_sum(draw)};
+                if (lane == 63)
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) ga.sums[((long)h * 3 + q) * a.B * a.nc + b * a.nc + chunk] = sums[q];
                 direct = da = dskip = 0.0;
                 if (buffers == 2) scalars(h + 1);
             }
