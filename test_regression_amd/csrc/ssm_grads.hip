@@ -61,6 +61,14 @@ template <int N> struct StatePlane<float, N> {
     }
 };
 
+// What the tokens' decays and step sizes take from the pairs and states of a piece.
+template <int N>
+struct TokenSums {
+    double row[10][16], col[10][16];    // by tile: sums of E over j and of L o (C B^T) o M over i, without the diagonal
+    float diag[kSC], dx[kSC];           // L o (C B^T) o M on the diagonal, M there
+    float rd[N / 16][kSC], wr[N / 16][kSC];   // by 16 rows of dk
+    double carry[N / 16];
+};
 template <int N, typename In>
 struct GradLds {
     Plane<In, N> b, c;
@@ -68,10 +76,7 @@ struct GradLds {
     Square<In> p;           // rows: the pairs' earlier token
     StatePlane<In, N> r;
     Scalars s[kGradBuffers<N, In>];     // of this head and the next
-    double row[4][kSC], col[4][kSC];    // sums of E over j and of L o (C B^T) o M over i, by the other's block, without the diagonal
-    float diag[kSC], dx[kSC];           // L o (C B^T) o M on the diagonal, M there
-    float rd[N / 16][kSC], wr[N / 16][kSC];   // by 16 rows of dk
-    double carry[N / 16];
+    TokenSums<N> sums[kGradBuffers<N, In>];   // of this piece and the one before
 };
 
 template <typename In>
@@ -113,11 +118,11 @@ __device__ __forceinline__ typename PV::Three three8(const f32x4& a, const f32x4
     return PV::three(f);
 }
 
-// Eight waves.  The pairs' ten tiles go round; a wave takes 16 rows of dk and N / 32
-// tiles of tokens for dB and dC, and leaves the rows of R in LDS; then it takes 16
-// columns of dv and two tiles of tokens for dX, while wave 7 sums up the tokens' decays
-// and forms the next head's scalars.  The next piece's rows and states are on their way
-// from the middle of a piece to the middle of the next.
+// Eight waves.  The pairs' ten tiles go round the first seven, while wave 7 sums up the
+// tokens' decays of the piece before and forms the next head's scalars; a wave takes 16
+// rows of dk and N / 32 tiles of tokens for dB and dC, and leaves the rows of R in LDS;
+// then it takes 16 columns of dv and two tiles of tokens for dX.  The next piece's rows
+// and states are on their way from the middle of a piece to the middle of the next.
 template <int N, typename In>
 __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga) {
     typedef Plane<In, N> PN;
@@ -190,17 +195,20 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             r4[q] += dr * start[1][q];
         }
     };
-    float raw = 0.f;   // wave 7: the raw step sizes, and the next head's
+    // wave 7: the raw step sizes of the head whose sums are taken and of the next one, and
+    // those on their way
+    float raw = 0.f, raw_ahead = 0.f;
     uint32_t next_raw = 0u;
     auto fetch_raw = [&](int h) {
         if (h < h_last && lane < n) next_raw = step_bits(a, b, h, t0 + lane);
     };
     auto scalars = [&](int h) {
         if (h >= h_last) return;
-        raw = raw_step(a, next_raw, step_bias(a, h));
-        chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw, a.softplus) : 0.f, shared_load(a.A, h));
+        raw_ahead = raw_step(a, next_raw, step_bias(a, h));
+        chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw_ahead, a.softplus) : 0.f, shared_load(a.A, h));
         fetch_raw(h + 1);
     };
+    auto tile_of = [&](int q) { return wave < 7 ? wave + 7 * q : 10; };   // of ten
     f32x4 cb[2], zsum[2] = {}, dc[TT] = {}, db[TT] = {};
     if (n > 0) {
         fetch(0);
@@ -215,6 +223,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         if (wave == 7) {
             fetch_raw(h_first);
             scalars(h_first);
+            raw = raw_ahead;
         }
         // what is above the pairs, where products read it: six tiles
         if (wave < 6) {
@@ -225,7 +234,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         // C B^T: rows of tokens 16 i + 4 g + r, columns 16 j + m
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int k = min(wave + 8 * q, 9), i = tile_i(k), j = tile_j(k);
+            const int k = min(tile_of(q), 9), i = tile_i(k), j = tile_j(k);
             mma<true>(cb[q], S.c.row(i, 0, m, g), S.b.row(j, 0, m, g));
 #pragma unroll
             for (int e = 1; e < N / 32; ++e) mma(cb[q], S.c.row(i, e, m, g), S.b.row(j, e, m, g));
@@ -243,21 +252,72 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         if (threadIdx.x < 3) ga.sums[((long)h * 3 + threadIdx.x) * a.B * a.nc + b * a.nc + chunk] = 0.0;
     }
     double direct = 0.0, da = 0.0, dskip = 0.0;   // wave 7: of token t's step size and log decay, of skip
+    auto token_sums = [&](int k) {
+        const int h = head(k), bi = lane / 16, at = lane % 16;
+        const TokenSums<N>& U = S.sums[k % buffers];
+        const Scalars& sl = S.s[h % buffers];
+        double row = 0.0, col = 0.0, rdt = 0.0, wrt = 0.0, cr = 0.0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = min(q, bi), j = max(q, bi);
+            const double r = U.row[bi * (bi + 1) / 2 + i][at], c = U.col[j * (j + 1) / 2 + bi][at];
+            row += q <= bi ? r : 0.0;
+            col += q >= bi ? c : 0.0;
+        }
+#pragma unroll
+        for (int q = 0; q < N / 16; ++q) {
+            if (16 * q >= dk) continue;
+            rdt += U.rd[q][lane];
+            wrt += U.wr[q][lane];
+            cr += U.carry[q];
+        }
+        const float step = sl.step[lane];
+        direct += col + U.diag[lane] + wrt;
+        dskip += lane < n ? U.dx[lane] : 0.f;
+        // before: of the tokens before t; after: of t and those that follow
+        const double own = step * (col + wrt) - row, before = prefix_sum(own) - own;
+        const double upto = prefix_sum(rdt), after = __shfl(upto, 63, 64) - upto + rdt;
+        da += before + after + (double)sl.decay * cr;
+        if ((k + 1) % pieces == 0) {
+            double draw = 0.0, dA = 0.0;
+            if (lane < n) {
+                const double dstep = direct + (double)shared_load(a.A, h) * da;
+                draw = a.softplus ? dstep / (1.0 + (double)expf(-raw)) : dstep;
+                dA = step * da;
+            }
+            if (lane < rows) {
+                const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + lane) * ga.gdts.token;
+                if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, (float)draw);
+                else static_cast<float*>(ga.grad_dt)[o] = (float)draw;
+            }
+            const double sums[3] = {prefix_sum(dA), prefix_sum(dskip), prefix_sum(draw)};
+            if (lane == 63)
+#pragma unroll
+                for (int q = 0; q < 3; ++q) ga.sums[((long)h * 3 + q) * a.B * a.nc + b * a.nc + chunk] = sums[q];
+            direct = da = dskip = 0.0;
+            raw = raw_ahead;
+        }
+    };
     for (int k = 0; k < (n > 0 ? all : 0); ++k) {
         const int h = head(k), v0 = column(k);
         Plane<In, 64>& X = S.x[k % buffers];
         Plane<In, 64>& G = S.g[k % buffers];
         const Scalars& sl = S.s[h % buffers];
+        TokenSums<N>& U = S.sums[k % buffers];
         sx.store(X);
         sg.store(G);
         __syncthreads();
         f32x4 start[2][4];
         fetch_starts(k, start);   // loads come back in order: before the next rows, which come from further away
         if (k + 1 < all) fetch(k + 1);
+        if (buffers == 2 && wave == 7) {
+            if (k > 0) token_sums(k - 1);
+            if ((k + 1) % pieces == 0) scalars(h + 1);
+        }
         // the pairs
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const int lane = lane_again(), m = lane % 16, g = lane / 16, tile = wave + 8 * q;
+            const int lane = lane_again(), m = lane % 16, g = lane / 16, tile = tile_of(q);
             if (tile >= 10) continue;
             const int i = tile_i(tile), j = tile_j(tile), s = 16 * j + m;
             f32x4 M;
@@ -280,15 +340,15 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     if (s == 16 * i + 4 * g + r) {
-                        S.diag[s] = F[r];
-                        S.dx[s] = M[r];
+                        U.diag[s] = F[r];
+                        U.dx[s] = M[r];
                         F[r] = 0.f;
                     }
             }
             const double e[4] = {F[0] * D, F[1] * D, F[2] * D, F[3] * D};
             const double col = kslot_sum(((double)F[0] + F[1]) + ((double)F[2] + F[3])), row = row_sums(e, m);
-            if (g == 0) S.col[i][s] = col;
-            if (m < 4) S.row[j][16 * i + 4 * g + m] = row;
+            if (g == 0) U.col[tile][m] = col;
+            if (m < 4) U.row[tile][4 * g + m] = row;
         }
         // dC and dB of the states, transposed: rows of dk, columns of tokens
         if (16 * nt < dk) {
@@ -311,7 +371,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
                 const int s = 16 * (first + t) + m;
                 o[t] *= sl.in[s];
                 const float rd = kslot_sum(dot4(o[t], S.c.get4(s, 16 * nt + 4 * g)));
-                if (g == 0) S.rd[nt][s] = rd;
+                if (g == 0) U.rd[nt][s] = rd;
                 dc[t] += o[t];
                 x0[t] = X.row(first + t, 0, m, g);
                 x1[t] = X.row(first + t, 1, m, g);
@@ -323,14 +383,14 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
                 const int s = 16 * (first + t) + m;
                 o[t] *= sl.out[s];
                 const float wr = kslot_sum(dot4(o[t], S.b.get4(s, 16 * nt + 4 * g)));
-                if (g == 0) S.wr[nt][s] = wr;
+                if (g == 0) U.wr[nt][s] = wr;
                 db[t] += o[t] * sl.step[s];
             }
             if (first == 0) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) S.r.put(16 * nt + m, g, q, r3);
                 carry = prefix_sum(carry);
-                if (lane == 63) S.carry[nt] = carry;
+                if (lane == 63) U.carry[nt] = carry;
             }
         } else if (first == 0) {
             // dk = 16: zeros for the rows that are not there
@@ -365,60 +425,22 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
                 if (s < n) store4_el(gx + s * ga.gxs.token, o[j] * sl.step[s] + skip * G.get4(s, 16 * vt + 4 * g));
             }
         }
-        if (wave == 7) {
-            const int bi = lane / 16;
-            double row = 0.0, col = 0.0, rdt = 0.0, wrt = 0.0, cr = 0.0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const double r = S.row[q][lane], c = S.col[q][lane];
-                row += q <= bi ? r : 0.0;
-                col += q >= bi ? c : 0.0;
-            }
-#pragma unroll
-            for (int q = 0; q < N / 16; ++q) {
-                if (16 * q >= dk) continue;
-                rdt += S.rd[q][lane];
-                wrt += S.wr[q][lane];
-                cr += S.carry[q];
-            }
-            const float step = sl.step[lane];
-            direct += col + S.diag[lane] + wrt;
-            dskip += lane < n ? S.dx[lane] : 0.f;
-            // before: of the tokens before t; after: of t and those that follow
-            const double own = step * (col + wrt) - row, before = prefix_sum(own) - own;
-            const double upto = prefix_sum(rdt), after = __shfl(upto, 63, 64) - upto + rdt;
-            da += before + after + (double)sl.decay * cr;
-            if ((k + 1) % pieces == 0) {
-                double draw = 0.0, dA = 0.0;
-                if (lane < n) {
-                    const double dstep = direct + (double)shared_load(a.A, h) * da;
-                    draw = a.softplus ? dstep / (1.0 + (double)expf(-raw)) : dstep;
-                    dA = step * da;
-                }
-                if (lane < rows) {
-                    const long o = b * ga.gdts.batch + h * ga.gdts.head + (t0 + lane) * ga.gdts.token;
-                    if (a.dt_bf16) store1(static_cast<bf16_t*>(ga.grad_dt) + o, (float)draw);
-                    else static_cast<float*>(ga.grad_dt)[o] = (float)draw;
-                }
-                const double sums[3] = {prefix_sum(dA), prefix_sum(dskip), prefix_sum(draw)};
-                if (lane == 63)
-#pragma unroll
-                    for (int q = 0; q < 3; ++q) ga.sums[((long)h * 3 + q) * a.B * a.nc + b * a.nc + chunk] = sums[q];
-                direct = da = dskip = 0.0;
-                if (buffers == 2) scalars(h + 1);
-            }
-        }
         if (buffers == 1) {
+            if (wave == 7) token_sums(k);
             __syncthreads();
-            if (wave == 7 && (k + 1) % pieces == 0) scalars(h + 1);
+            if (wave == 7 && (k + 1) % pieces == 0) {
+                scalars(h + 1);
+                raw = raw_ahead;
+            }
         }
     }
+    if (buffers == 2 && wave == 7 && n > 0) token_sums(all - 1);
     // the pairs' dC and dB over the heads' sum of Z
     if (n > 0) {
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < 2; ++q)
-            if (wave + 8 * q < 10) S.p.put4(16 * tile_j(wave + 8 * q) + m, 16 * tile_i(wave + 8 * q) + 4 * g, zsum[q]);
+            if (tile_of(q) < 10) S.p.put4(16 * tile_j(tile_of(q)) + m, 16 * tile_i(tile_of(q)) + 4 * g, zsum[q]);
         __syncthreads();
     }
     if (16 * nt >= dk) return;
