@@ -75,7 +75,7 @@ struct GradLds {
     Plane<In, 64> x[kGradBuffers<N, In>], g[kGradBuffers<N, In>];
     Square<In> p;           // rows: the pairs' earlier token
     StatePlane<In, N> r;
-    Scalars s[kGradBuffers<N, In>];     // of this head and the next
+    Scalars s[2 * kGradBuffers<N, In> - 1];   // of this head, the one before and the next
     TokenSums<N> sums[kGradBuffers<N, In>];   // of this piece and the one before
 };
 
@@ -118,11 +118,11 @@ __device__ __forceinline__ typename PV::Three three8(const f32x4& a, const f32x4
     return PV::three(f);
 }
 
-// Eight waves.  The pairs' ten tiles go round the first seven, while wave 7 sums up the
-// tokens' decays of the piece before and forms the next head's scalars; a wave takes 16
-// rows of dk and N / 32 tiles of tokens for dB and dC, and leaves the rows of R in LDS;
-// then it takes 16 columns of dv and two tiles of tokens for dX.  The next piece's rows
-// and states are on their way from the middle of a piece to the middle of the next.
+// Eight waves.  The pairs' ten tiles go round the first six, while wave 7 sums up the
+// tokens' decays of the piece before and wave 6 forms the next head's scalars; a wave
+// takes 16 rows of dk and N / 32 tiles of tokens for dB and dC, and leaves the rows of R
+// in LDS; then it takes 16 columns of dv and two tiles of tokens for dX.  The next piece's
+// rows and states are on their way from the middle of a piece to the middle of the next.
 template <int N, typename In>
 __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga) {
     typedef Plane<In, N> PN;
@@ -195,20 +195,16 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             r4[q] += dr * start[1][q];
         }
     };
-    // wave 7: the raw step sizes of the head whose sums are taken and of the next one, and
-    // those on their way
-    float raw = 0.f, raw_ahead = 0.f;
-    uint32_t next_raw = 0u;
+    uint32_t next_raw = 0u;   // wave 6: the raw step sizes to come
     auto fetch_raw = [&](int h) {
         if (h < h_last && lane < n) next_raw = step_bits(a, b, h, t0 + lane);
     };
     auto scalars = [&](int h) {
         if (h >= h_last) return;
-        raw_ahead = raw_step(a, next_raw, step_bias(a, h));
-        chunk_scalars(S.s[h % buffers], lane < n ? step_of(raw_ahead, a.softplus) : 0.f, shared_load(a.A, h));
+        chunk_scalars(S.s[h % (2 * buffers - 1)], lane < n ? step_of(raw_step(a, next_raw, step_bias(a, h)), a.softplus) : 0.f, shared_load(a.A, h));
         fetch_raw(h + 1);
     };
-    auto tile_of = [&](int q) { return wave < 7 ? wave + 7 * q : 10; };   // of ten
+    auto tile_of = [&](int q) { return wave < 6 ? wave + 6 * q : 10; };   // of ten
     f32x4 cb[2], zsum[2] = {}, dc[TT] = {}, db[TT] = {};
     if (n > 0) {
         fetch(0);
@@ -220,10 +216,9 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             sb.store(S.b);
             sc.store(S.c);
         }
-        if (wave == 7) {
+        if (wave == 6) {
             fetch_raw(h_first);
             scalars(h_first);
-            raw = raw_ahead;
         }
         // what is above the pairs, where products read it: six tiles
         if (wave < 6) {
@@ -255,7 +250,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
     auto token_sums = [&](int k) {
         const int h = head(k), bi = lane / 16, at = lane % 16;
         const TokenSums<N>& U = S.sums[k % buffers];
-        const Scalars& sl = S.s[h % buffers];
+        const Scalars& sl = S.s[h % (2 * buffers - 1)];
         double row = 0.0, col = 0.0, rdt = 0.0, wrt = 0.0, cr = 0.0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -282,7 +277,8 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
             double draw = 0.0, dA = 0.0;
             if (lane < n) {
                 const double dstep = direct + (double)shared_load(a.A, h) * da;
-                draw = a.softplus ? dstep / (1.0 + (double)expf(-raw)) : dstep;
+                // the softplus' slope at a raw value is 1 - e^-step
+                draw = a.softplus ? dstep * -expm1f(-step) : dstep;
                 dA = step * da;
             }
             if (lane < rows) {
@@ -295,14 +291,13 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
 #pragma unroll
                 for (int q = 0; q < 3; ++q) ga.sums[((long)h * 3 + q) * a.B * a.nc + b * a.nc + chunk] = sums[q];
             direct = da = dskip = 0.0;
-            raw = raw_ahead;
         }
     };
     for (int k = 0; k < (n > 0 ? all : 0); ++k) {
         const int h = head(k), v0 = column(k);
         Plane<In, 64>& X = S.x[k % buffers];
         Plane<In, 64>& G = S.g[k % buffers];
-        const Scalars& sl = S.s[h % buffers];
+        const Scalars& sl = S.s[h % (2 * buffers - 1)];
         TokenSums<N>& U = S.sums[k % buffers];
         sx.store(X);
         sg.store(G);
@@ -310,10 +305,8 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         f32x4 start[2][4];
         fetch_starts(k, start);   // loads come back in order: before the next rows, which come from further away
         if (k + 1 < all) fetch(k + 1);
-        if (buffers == 2 && wave == 7) {
-            if (k > 0) token_sums(k - 1);
-            if ((k + 1) % pieces == 0) scalars(h + 1);
-        }
+        if (buffers == 2 && wave == 7 && k > 0) token_sums(k - 1);
+        if (buffers == 2 && wave == 6 && (k + 1) % pieces == 0) scalars(h + 1);
         // the pairs
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -428,10 +421,7 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
         if (buffers == 1) {
             if (wave == 7) token_sums(k);
             __syncthreads();
-            if (wave == 7 && (k + 1) % pieces == 0) {
-                scalars(h + 1);
-                raw = raw_ahead;
-            }
+            if (wave == 6 && (k + 1) % pieces == 0) scalars(h + 1);
         }
     }
     if (buffers == 2 && wave == 7 && n > 0) token_sums(all - 1);
