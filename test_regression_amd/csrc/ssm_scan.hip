@@ -3,8 +3,12 @@
 //
 // A workgroup takes up to 64 columns of one head's dv and goes over the chunks of its
 // part of the sequence; a wave keeps 16 columns of the state in accumulators.  Per
-// chunk the four waves form the 64 x 64 matrix L o (C B^T) diag(D) together, through
-// LDS, while the next chunk's rows are on their way.
+// chunk the four waves of ssm_out_kernel form the 64 x 64 matrix L o (C B^T) diag(D)
+// together, through LDS, while the next chunk's rows are on their way; two workgroups
+// share a CU.  16 heads of 16384 tokens, dk and dv 128, bfloat16, in 16 segments: 49 us
+// for the ends, 8 us to join them, 108 us for the outputs: 3.3 us a chunk and CU, of
+// which LDS works 41 %, the VALU 31 %, the matrix units 21 %: the chain from product to
+// product is what it waits for.
 #include <algorithm>
 
 #include "ssm_core.h"
@@ -439,7 +443,9 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
 // as far as they come from their segment, and the decay from the segment's start to
 // there, with which the gradients add the segments' starts; these states are [dk][dv],
 // a lane's rows v + 4 g + r and columns 16 i + m of dk.  Without STATES a lane holds rows
-// 16 i + 4 g + r of dk, column v + m.
+// 16 i + 4 g + r of dk, column v + m.  2 x 32 heads of 4096 tokens, dk 128, dv 64,
+// bfloat16, both directions: 90 us for 268 MB of states (3 TB/s); with the segments' ends
+// in a pass of their own before, 50 + 98 us.
 template <int N, typename In, bool STATES, bool BACK>
 __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, const SsmPlace& p) {
     const int dk = N > 32 ? N : a.dk;

@@ -7,7 +7,9 @@
 //
 // HBM-bound: 8 dk dv bytes of state a head against about 5 flops for each 8 bytes.
 // Lanes and rows as in the delta rule's step: eight lanes take a row (four at dk =
-// 16), 16-byte pieces interleaved over them, a wave one group of 8 or 16 rows.
+// 16), 16-byte pieces interleaved over them, a wave one group of 8 or 16 rows.  256
+// sequences of 32 heads, dk 128, dv 64: 82 us (6.5 TB/s of states, part of them from the
+// last-level cache where calls follow one another).
 #include "ssm_core.h"
 
 namespace mesa {
