@@ -1240,7 +1240,7 @@ mesa_status mesa_ssm_forward(const void* x, const int64_t* x_strides, const void
     a.nseg = nseg;
     a.seg_chunks = (int)((nc + nseg - 1) / nseg);
     a.seg_start = static_cast<float*>(workspace);
-    a.seg_decay = a.seg_start + (size_t)BH * (nseg - 1) * dv * dk;
+    a.seg_decay = a.seg_start + (size_t)BH * mesa::ssm_slots(nseg, 1) * dv * dk;
     const hipError_t e = timed_launch(MESA_KERNEL_SSM_SCAN, s, [&] { return mesa::launch_ssm_scan(a, s); });
     if (e != hipSuccess) return hip_fail(e, "state space scan kernel launch");
     return MESA_OK;

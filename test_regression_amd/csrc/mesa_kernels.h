@@ -200,7 +200,7 @@ struct SsmArgs {
     long BH; int B; int Hk; int H; int T; int dk; int dv; int nc; int bf16;
     void* out; float* final_state;     // the step: its state
     int nseg; int seg_chunks;          // segments of a sequence that are passed over at once, chunks of one
-    float* seg_start;                  // nseg > 1, workspace: ssm_slots states, segments' ends, then the next ones' starts
+    float* seg_start;                  // nseg > 1, workspace: ssm_slots states of a head, segments' ends that become the next ones' starts
     float* seg_decay;                  // one a state
     const void* grad_out; const float* grad_final; float* grad_state;   // backward
     // backward workspace [BH][nc][dk][dv]: states at the chunks' starts, gradients at their ends, both as they come
@@ -217,8 +217,8 @@ struct SsmGradArgs {
 };
 constexpr int kSsmGradGroups = 512;   // workgroups of the gradients, where splitting the heads gives more
 int ssm_segments(long BH, int nc, int dv, int sides);         // the number of segments; the backward has two sides
-// Segments' ends that are kept for a head: of all but the last, and for the gradients of both directions with it.
-constexpr int ssm_slots(int nseg, int sides) { return nseg == 1 ? 0 : sides == 1 ? nseg - 1 : 2 * nseg; }
+// States that a head's segments keep: their starts, for the gradients the ends of both directions.
+constexpr int ssm_slots(int nseg, int sides) { return nseg == 1 ? 0 : sides * nseg; }
 long ssm_segment_slots(long BH, int nc, int dv, int sides);   // the most BH ssm_slots of any smaller batch and length
 int ssm_grad_parts(long B, int Hk, int H, int nc);
 hipError_t launch_ssm_scan(const SsmArgs& a, hipStream_t s);

@@ -101,8 +101,8 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
 
     // the state's columns v + m, rows 16 i + 4 g + r
     f32x4 st[N / 16] = {};
-    const float* from = p.seg == 0 ? a.state0 ? a.state0 + p.bh * a.dv * dk : nullptr
-                                   : a.seg_start + (p.bh * (a.nseg - 1) + p.seg - 1) * a.dv * dk;
+    const float* from = a.nseg > 1 ? a.seg_start + (p.bh * a.nseg + p.seg) * a.dv * dk
+                                   : a.state0 ? a.state0 + p.bh * a.dv * dk : nullptr;
     if (from && mine)
 #pragma unroll
         for (int i = 0; i < N / 16; ++i)
@@ -313,8 +313,7 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
 
     // the state's columns v + m, rows 16 i + 4 g + r
     f32x4 st[N / 16] = {}, o[4];
-    const float* from = p.seg == 0 ? a.state0 ? a.state0 + p.bh * a.dv * dk : nullptr
-                                   : a.seg_start + (p.bh * (a.nseg - 1) + p.seg - 1) * a.dv * dk;
+    const float* from = a.state0 ? a.state0 + p.bh * a.dv * dk : nullptr;
     if (from && mine)
 #pragma unroll
         for (int i = 0; i < N / 16; ++i)
@@ -451,7 +450,7 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
     const int dk = N > 32 ? N : a.dk;
     typedef Plane<In, 64> PV;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16;
-    const int hk = p.h / (a.H / a.Hk), slots = STATES ? a.nseg : a.nseg - 1;
+    const int hk = p.h / (a.H / a.Hk);
     // chunks of the segment, counted from where the pass starts
     const int begin = p.seg * a.seg_chunks, end = min(a.nc, begin + a.seg_chunks), real = (p.valid + kSC - 1) / kSC;
     const bool mine = 16 * wave < p.cols;
@@ -462,7 +461,7 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
                         : static_cast<const In*>(a.x) + p.b * a.xs.batch + p.h * a.xs.head + p.v0;
     const long xt = BACK ? a.dv : a.xs.token;
     const float A = a.A[p.h];
-    const long slot = (BACK ? a.BH + p.bh : p.bh) * slots + p.seg;
+    const long slot = (BACK ? a.BH + p.bh : p.bh) * a.nseg + p.seg;
 
     f32x4 st[N / 16] = {};
     const float* from = p.seg == 0 ? (BACK ? a.grad_final : a.state0) : nullptr;
@@ -477,6 +476,12 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
                 for (int r = 0; r < 4; ++r) st[i][r] = from[(long)(v + 4 * g + r) * dk + 16 * i + m];
         }
     }
+    // the first segment's start, from where the outputs take it: the final state may
+    // take the given one's place while they are formed
+    if (!STATES && p.seg == 0 && mine)
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            if (16 * i < dk) store4(a.seg_start + (slot * a.dv + v + m) * dk + 16 * i + 4 * g, st[i]);
     Stage<In, N> sb(ks.token, dk);
     Stage<In, 64> sx(xt, p.cols);
     uint32_t raw = 0u;   // wave 3: the step sizes to come
@@ -539,7 +544,7 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
         return;
     }
     if (p.v0 == 0 && threadIdx.x == 0) a.seg_decay[slot] = exp2_small(total);
-    float* to = a.seg_start + slot * a.dv * dk;
+    float* to = a.seg_start + (slot + (STATES ? 0 : 1)) * a.dv * dk;   // the ends' next start
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
         if (16 * i >= dk) continue;
@@ -566,20 +571,20 @@ __global__ __launch_bounds__(256, 2) void ssm_states_kernel(SsmArgs a) {
 // place: start_{s+1} = decay_s start_s + end_s.  Of the gradients' second direction
 // (rows bh from `back` on) the last segment's end too, as the start state's gradient,
 // transposed.
-__global__ __launch_bounds__(256) void ssm_join_kernel(float* seg, const float* decay, long n, int dk, int dv, int slots, int starts,
-                                                       long back, float* grad_state) {
+__global__ __launch_bounds__(256) void ssm_join_kernel(float* ends, const float* decay, long n, int dk, int dv, int nseg, long back,
+                                                       float* grad_state) {
     const long i = (long)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
     const int per = dk * dv, at = (int)(i % per);
     const long bh = i / per;
-    float* p = seg + bh * slots * per + at;
+    float* p = ends + bh * nseg * per + at;
     float s = p[0];
-    for (int e = 1; e < starts; ++e) {
-        s = decay[bh * slots + e] * s + p[(long)e * per];
+    for (int e = 1; e < nseg - 1; ++e) {
+        s = decay[bh * nseg + e] * s + p[(long)e * per];
         p[(long)e * per] = s;
     }
     if (grad_state && bh >= back)
-        grad_state[(bh - back) * per + (long)(at % dv) * dk + at / dv] = decay[bh * slots + starts] * s + p[(long)starts * per];
+        grad_state[(bh - back) * per + (long)(at % dv) * dk + at / dv] = decay[bh * nseg + nseg - 1] * s + p[(nseg - 1L) * per];
 }
 
 // Workgroups from which on ssm_walk_kernel leaves too few CUs idle for segments to pay
@@ -614,20 +619,20 @@ static hipError_t scan_pass(const SsmArgs& a, SsmPass pass, hipStream_t s) {
     else scan_type<128>(a, pass, blocks, s);
     return hipGetLastError();
 }
-static hipError_t join(const SsmArgs& a, int sides, int slots, float* grad_state, hipStream_t s) {
+static hipError_t join(const SsmArgs& a, int sides, float* ends, float* grad_state, hipStream_t s) {
     const long n = sides * a.BH * a.dv * a.dk;
-    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.seg_start, a.seg_decay, n, a.dk, a.dv,
-                       slots, a.nseg - 1, a.BH, grad_state);
+    hipLaunchKernelGGL(ssm_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, ends, a.seg_decay, n, a.dk, a.dv, a.nseg,
+                       a.BH, grad_state);
     return hipGetLastError();
 }
 hipError_t launch_ssm_scan(const SsmArgs& a, hipStream_t s) {
     hipError_t e = a.nseg > 1 ? scan_pass(a, kEnds, s) : hipSuccess;
-    if (e == hipSuccess && a.nseg > 2) e = join(a, 1, a.nseg - 1, nullptr, s);
+    if (e == hipSuccess && a.nseg > 2) e = join(a, 1, a.seg_start + (long)a.dv * a.dk, nullptr, s);
     return e == hipSuccess ? scan_pass(a, kOut, s) : e;
 }
 hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s) {
     const hipError_t e = scan_pass(a, kStates, s);
-    return e == hipSuccess && (a.nseg > 2 || (a.nseg > 1 && a.grad_state)) ? join(a, 2, a.nseg, a.grad_state, s) : e;
+    return e == hipSuccess && (a.nseg > 2 || (a.nseg > 1 && a.grad_state)) ? join(a, 2, a.seg_start, a.grad_state, s) : e;
 }
 
 // Segments of a sequence that are passed over at once: twice as many while the
