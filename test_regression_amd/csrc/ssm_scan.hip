@@ -636,15 +636,18 @@ hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s) {
 }
 
 // Segments of a sequence that are passed over at once: twice as many while the
-// workgroups (of `sides` directions) stay below kSsmFill and a segment keeps
-// kSsmLeast chunks.  16 heads of 16384 tokens, dk and dv 128, bfloat16: 166 us in 16
-// segments (two workgroups a CU), 204 us in 8.
+// workgroups (of `sides` directions) stay below kSsmFill and a segment keeps kSsmLeast
+// chunks; for the outputs, which need the ends first, from kSsmShort chunks on.  16
+// heads of 16384 tokens, dk and dv 128, bfloat16: 166 us in 16 segments (two workgroups a
+// CU), 204 us in 8.  16 heads of 1024 tokens, dk 128, dv 64, bfloat16: 58 us in one segment,
+// 37 in four, 28 in eight, their gradients 59, 52 and 50 us; of 256 tokens 19 us in one,
+// 23 us in two.
 constexpr long kSsmFill = 512;
-constexpr int kSsmLeast = 8, kSsmMost = 32;
+constexpr int kSsmLeast = 2, kSsmShort = 8, kSsmMost = 32;
 int ssm_segments(long BH, int nc, int dv, int sides) {
     const long groups = BH * ((dv + 63) / 64) * sides;
     int n = 1;
-    if (sides == 1 && groups >= kSsmWalk && groups <= kSsmCUs) return n;
+    if (sides == 1 && ((groups >= kSsmWalk && groups <= kSsmCUs) || nc < kSsmShort)) return n;
     while (n < kSsmMost && groups * n < kSsmFill && nc >= 2 * kSsmLeast * n) n *= 2;
     return n;
 }
