@@ -19,13 +19,14 @@
 // from float32 parts.  dv goes by in pieces of 64 columns, in all of which the
 // formulas are sums.
 //
-// 2 x 32 heads of 4096 tokens that share b and c, dk 128, dv 64, bfloat16: 163 us (366
+// 2 x 32 heads of 4096 tokens that share b and c, dk 128, dv 64, bfloat16: 149 us (366
 // MB fetched, of which the states 268 MB), and 90 us for the states.  A head's chunk
 // takes 19,000 cycles of a workgroup that fills its CU: pairs 8,000, states 5,000 and
 // their wait 2,000, dX 3,000; the VALU issues 44 % of the time (float64 decays, three-part
-// splits), the matrix units 11 %.  With wave 7's sums after dX, where the others waited for
-// them, 182 us; with branches around the states' loads and the heads' scalars by vector
-// loads, behind which the wave waited, 209 us.
+// splits), the matrix units 11 %.  With twice the workgroups in two turns 162 us; so, and
+// with wave 7's sums after dX, where the others waited for them, 182 us; with branches
+// around the states' loads and the heads' scalars by vector loads, behind which the wave
+// waited, 209 us.
 #include <algorithm>
 
 #include "ssm_core.h"
