@@ -760,6 +760,10 @@ def mesa_causal_conv(x, w, bias=None, hist=None, *, silu=True, lens=None, out=No
     return (out, hist_out) if return_hist else out
 
 
+def mesa_causal_conv_backward_workspace_bytes(B, T, D, W) -> int:
+    return int(lib().mesa_causal_conv_backward_workspace_bytes(B, T, D, W))
+
+
 def mesa_causal_conv_backward(x, w, grad_y, bias=None, hist=None, *, silu=True, lens=None, grad_x=None, workspace=None,
                               stream=None):
     """Gradients of mesa_causal_conv from its inputs and grad_y [B,T,D].  Returns a
@@ -973,6 +977,10 @@ def mesa_qk_rotate(q, k, freqs, positions=None, wq=None, wk=None, *, norm=True, 
                                   out_q.data_ptr(), _at(out_k), _here(dev))
     _check(st, "mesa_qk_rotate")
     return out_q, out_k
+
+
+def mesa_qk_rotate_backward_workspace_bytes(d) -> int:
+    return int(lib().mesa_qk_rotate_backward_workspace_bytes(d))
 
 
 def mesa_qk_rotate_backward(q, k, grad_yq, grad_yk, freqs, positions=None, wq=None, wk=None, *, norm=True, eps=1e-6,

@@ -329,3 +329,64 @@ def test_kernels_are_counted():
     finally:
         mesa.profile_enable(False)
         mesa.profile_reset()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,lens", [(1100, (1100, 70, 0)), (130, (1, 64, 130))])
+def test_nothing_behind_a_length_is_read(T, lens, dtype):
+    """NaN behind the rows' lengths and in the workspaces: the results of clean rows, bit for bit."""
+    import torch
+    from test_regression_amd import mesa
+    say("case behind lengths", (T, lens, dtype))
+    B, Hk, H, dk, dv, W, code = 3, 1, 2, 64, 32, 3, 1 if dtype == "bf16" else 0
+    t, _ = ssm_inputs(23, B, Hk, H, T, dk, dv, dtype, lens=lens)
+    d = {n: None if x is None else x.cuda() for n, x in t.items()}
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    d["go"] = torch.randn(B, H, T, dv, device="cuda", generator=gen).to(d["x"].dtype)
+    d["rows"], d["dy"] = (torch.randn(B, T, 40, device="cuda", generator=gen).to(d["x"].dtype) for _ in range(2))
+    hist = torch.randn(B, W - 1, 40, device="cuda", generator=gen).to(d["x"].dtype)
+    w, gf = torch.randn(W, 40, device="cuda", generator=gen), torch.randn(B, H, dv, dk, device="cuda", generator=gen)
+
+    def calls(fill):
+        ws = lambda n: torch.full((max(n, 16),), fill, dtype=torch.uint8, device="cuda")  # noqa: E731
+        head = [d[n] for n in ("x", "b", "c", "dt", "A")]
+        o, S = mesa.mesa_ssm_forward(*head, d["D"], d["dt_bias"], d["state"], lens=d["lens"], return_final=True,
+                                     workspace=ws(mesa.mesa_ssm_workspace_bytes(B, H, T, dk, dv, code)))
+        g = mesa.mesa_ssm_backward(*head, d["go"], d["D"], d["dt_bias"], d["state"], lens=d["lens"], grad_final=gf,
+                                   workspace=ws(mesa.mesa_ssm_backward_workspace_bytes(B, Hk, H, T, dk, dv, code)))
+        y, h = mesa.mesa_causal_conv(d["rows"], w, None, hist, lens=d["lens"], return_hist=True)
+        gy = mesa.mesa_causal_conv_backward(d["rows"], w, d["dy"], None, hist, lens=d["lens"],
+                                            workspace=ws(mesa.mesa_causal_conv_backward_workspace_bytes(B, T, 40, W)))
+        torch.cuda.synchronize()
+        return [o, S, y, h, *[x for q in (g, gy) for x in q.values() if x is not None]]
+    ref = calls(0)
+    for b, n in enumerate(lens):
+        for name in ("x", "b", "c", "go"):
+            d[name][b, :, n:] = float("nan")
+        for name in ("rows", "dy"):
+            d[name][b, n:] = float("nan")
+        d["dt"][b, :, n:] = float("nan")
+    for i, (x, y) in enumerate(zip(calls(255), ref)):
+        assert torch.equal(x, y), i
+
+
+@pytest.mark.parametrize("B,Hk,H,T,dk,dv", [(1, 1, 3, 520, 32, 32), (1, 1, 2, 1290, 128, 64), (2, 1, 12, 700, 16, 16)])
+def test_segments_of_few_chunks(B, Hk, H, T, dk, dv):
+    """Short segments, the last of them with few chunks or none, both directions."""
+    import torch
+    from test_regression_amd import mesa
+    say("case short segments", (B, Hk, H, T, dk, dv))
+    t, f = ssm_inputs(31, B, Hk, H, T, dk, dv, "f32")
+    d = {n: None if x is None else x.cuda() for n, x in t.items()}
+    rng = np.random.default_rng(2)
+    go, gof = store(rng.standard_normal((B, H, T, dv)), "f32")
+    gf, gff = store(rng.standard_normal((B, H, dv, dk)), "f32")
+    head = [d[n] for n in ("x", "b", "c", "dt", "A")]
+    o, S = mesa.mesa_ssm_forward(*head, d["D"], d["dt_bias"], d["state"], return_final=True)
+    g = mesa.mesa_ssm_backward(*head, go.cuda(), d["D"], d["dt_bias"], d["state"], grad_final=gf.cuda())
+    torch.cuda.synchronize()
+    ro, rS, rg, terms = ssm_ref(f, gof, gff)
+    near(o, ro)
+    near(S, rS)
+    for n, y in rg.items():
+        near(g[n], y, terms=terms.get(n, 0.0), what=n)
