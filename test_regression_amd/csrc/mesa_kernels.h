@@ -216,7 +216,7 @@ struct SsmGradArgs {
     double* sums;    // [H][3][B nc]
 };
 // Workgroups of the gradients, where splitting the heads gives more: one a CU (2 x 32 heads of 4096 tokens, dk 128, dv 64,
-// bfloat16: 149 us, with two in turn 162 us).
+// bfloat16: 151 us, with two in turn 162 us).
 constexpr int kSsmGradGroups = 256;
 int ssm_segments(long BH, int nc, int dv, int sides);         // the number of segments; the backward has two sides
 // States that a head's segments keep: their starts, for the gradients the ends of both directions.

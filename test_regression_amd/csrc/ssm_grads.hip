@@ -19,7 +19,7 @@
 // from float32 parts.  dv goes by in pieces of 64 columns, in all of which the
 // formulas are sums.
 //
-// 2 x 32 heads of 4096 tokens that share b and c, dk 128, dv 64, bfloat16: 149 us (366
+// 2 x 32 heads of 4096 tokens that share b and c, dk 128, dv 64, bfloat16: 151 us (366
 // MB fetched, of which the states 268 MB), and 90 us for the states.  A head's chunk
 // takes 19,000 cycles of a workgroup that fills its CU: pairs 8,000, states 5,000 and
 // their wait 2,000, dX 3,000; the VALU issues 44 % of the time (float64 decays, three-part
@@ -347,7 +347,8 @@ __global__ __launch_bounds__(kGradThreads) void ssm_grads_kernel(SsmGradArgs ga)
                         F[r] = 0.f;
                     }
             }
-            const double e[4] = {F[0] * D, F[1] * D, F[2] * D, F[3] * D};
+            // not rounded: pairs before a token are in both sums and have to leave nothing
+            const double d = D, e[4] = {F[0] * d, F[1] * d, F[2] * d, F[3] * d};
             const double col = kslot_sum(((double)F[0] + F[1]) + ((double)F[2] + F[3])), row = row_sums(e, m);
             if (g == 0) U.col[tile][m] = col;
             if (m < 4) U.row[tile][4 * g + m] = row;

@@ -390,3 +390,27 @@ def test_segments_of_few_chunks(B, Hk, H, T, dk, dv):
     near(S, rS)
     for n, y in rg.items():
         near(g[n], y, terms=terms.get(n, 0.0), what=n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pairs_before_a_token_leave_nothing(dtype):
+    """Outputs whose gradients end at token 20: later step sizes change nothing.  Their
+    gradients are differences of the same float64 products E_ij summed two ways, at most
+    64 64 additions of 2^-53 of the terms each: below 2^-40 of A times the sum of |E|."""
+    import torch
+    from test_regression_amd import mesa
+    say("case pairs before", dtype)
+    B, H, T, dk, dv, last = 2, 3, 64, 32, 64, 20
+    t, f = ssm_inputs(41, B, 1, H, T, dk, dv, dtype, start=False)
+    d = {n: None if x is None else x.cuda() for n, x in t.items()}
+    d["dt"] = d["dt"].float()
+    go, gof = store(np.random.default_rng(3).standard_normal((B, H, T, dv)), dtype)
+    go[:, :, last:] = 0
+    gof[:, :, last:] = 0
+    g = mesa.mesa_ssm_backward(d["x"], d["b"], d["c"], d["dt"], d["A"], go.cuda(), d["D"], d["dt_bias"])
+    torch.cuda.synchronize()
+    step = np.log1p(np.exp(f["dt"] + f["dt_bias"][:, None]))
+    pairs = np.abs(gof @ f["x"].transpose(0, 1, 3, 2)) * np.abs(f["c"] @ f["b"].transpose(0, 1, 3, 2)) * step[:, :, None]
+    most = np.tril(pairs).sum((2, 3)) * np.abs(f["A"])
+    late = np.abs(f64(g["grad_dt"])[:, :, last:]).max(-1)
+    assert (late <= 2.0 ** -40 * most).all(), (late / most).max()
