@@ -45,8 +45,8 @@ __device__ __forceinline__ void turn_cos_sin(double turns, float m, float* c, fl
     *s = m * (k & 2 ? -b : b);
 }
 
-// The cosines and sines of a lane's eight features at one position; features that
-// are not rotated get 1 and 0.
+// The cosines and sines of a lane's eight features at one position (1 and 0 where
+// turned() does not use them).
 template <bool INTER>
 struct Turns {
     static constexpr int n = INTER ? 4 : 8;
@@ -80,7 +80,8 @@ __device__ __forceinline__ f32x8 from_lane(const f32x8& x, int lane) {
     return r;
 }
 
-// y = the rotation of x (SIGN 1) or its transpose (-1), o the opposite features.
+// y = the rotation of x (SIGN 1) or its transpose (-1), o the opposite features; x
+// itself past the rotated ones.
 template <bool INTER, int SIGN>
 __device__ __forceinline__ f32x8 turned(const f32x8& x, const Turns<INTER>& r, int partner, int d0, int rot) {
     f32x8 y;
@@ -96,6 +97,9 @@ __device__ __forceinline__ f32x8 turned(const f32x8& x, const Turns<INTER>& r, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) y.v[e] = x.v[e] * r.c[e] + sign * o.v[e] * r.s[e];
     }
+    // not by a product with 0, which an infinity would turn into a NaN
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y.v[e] = d0 < rot ? y.v[e] : x.v[e];
     return y;
 }
 
