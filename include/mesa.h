@@ -634,7 +634,8 @@ mesa_status mesa_rotary_frequencies(int rot, double base, int scaling, double fa
  *   rot       a multiple of 16, 16 <= rot <= d
  *   positions [B, T] int64 (or [T], positions_stride 0), batch stride
  *             positions_stride; NULL: token t is at position0 + t.  Angles are
- *             formed in float64: positions up to 2^40 keep their place in the turn
+ *             formed as pairs of float64 values: float32's accuracy at
+ *             positions up to 2^50 to either side (of frequencies up to 1)
  *   wq, wk    [d]             float32 weights of the norm, or NULL for 1
  *   yq, yk    [B, Hq, T, d], [B, Hk, T, d]  dtype
  * d in {16, 32, 64, 128, 256}; eps > 0.  A row of zeros gives zeros.  Squares are

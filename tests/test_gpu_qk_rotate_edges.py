@@ -1,13 +1,22 @@
-"""The rotation of queries and keys at its edges: features beyond the rotated ones, which
-stay what they are."""
+"""The rotation of queries and keys at its edges: positions up to 2^50, and features
+beyond the rotated ones, which stay what they are.
+
+Bounds, relative L2, as in tests/test_gpu_qk_rotate.py: 32 roundings of 2^-24, at any
+of them.  The turn count p f / 2 pi is a product of a whole number
+and two rounded ones; carried as a pair of float64 values it is off by 2^-100 of
+itself, and by 2^-53 of what is left of a turn.  The reference's angles are exact
+rationals: the frequencies are float64 numbers, 2 pi is taken to 60 digits."""
 import sys
+from fractions import Fraction
 
 import numpy as np
 import pytest
 
-from tests.ssm_helpers import store
+from tests.ssm_helpers import near, store
 
 pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+TWO_PI = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -20,6 +29,39 @@ def _need_gpu():
 def say(*a):
     print(*a, flush=True)
     sys.stdout.flush()
+
+
+def exact_angles(freqs, pos):
+    """p f less whole turns, [T, pairs]: reduced exactly, then rounded to float64."""
+    return np.array([[float((Fraction(int(p)) * Fraction(float(f))) % TWO_PI) for f in freqs] for p in pos])
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("base", [0, 1 << 27, 1 << 33, -(1 << 36), 1 << 40, -(1 << 40), 1 << 49, 100000 - (1 << 50)])
+def test_far_positions(base, inter):
+    import torch
+    from test_regression_amd import mesa
+    say("case far", base, inter)
+    d = 64
+    rng = np.random.default_rng(3)
+    x, xf = store(rng.standard_normal((1, 2, 6, d)), "f32")
+    pos = base + np.array([0, 1, 5, 1000, 4097, 99991])
+    freqs, _ = mesa.mesa_rotary_frequencies(d)
+    y, _ = mesa.mesa_qk_rotate(x.cuda(), None, freqs, torch.from_numpy(pos[None]).cuda(), norm=False, interleaved=inter)
+    counted, _ = mesa.mesa_qk_rotate(x.cuda()[:, :, :2].contiguous(), None, freqs, norm=False, interleaved=inter, position0=base)
+    back = mesa.mesa_qk_rotate_backward(x.cuda(), None, y, None, freqs, torch.from_numpy(pos[None]).cuda(), norm=False,
+                                        interleaved=inter)["grad_q"]
+    torch.cuda.synchronize()
+    ang = exact_angles(freqs.cpu().numpy(), pos)
+    cos, sin = np.cos(ang), np.sin(ang)
+    a, b = (slice(0, d, 2), slice(1, d, 2)) if inter else (slice(0, d // 2), slice(d // 2, d))
+    ref = np.empty_like(xf)
+    ref[..., a], ref[..., b] = xf[..., a] * cos - xf[..., b] * sin, xf[..., b] * cos + xf[..., a] * sin
+    # token by token, so that one position's error does not vanish in the others'
+    for t in range(6):
+        near(y[:, :, t], ref[:, :, t], 32 * U, what=(base, t))
+    assert torch.equal(counted, y[:, :, :2])
+    near(back, xf, 64 * U)   # the rotation and its transpose
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
