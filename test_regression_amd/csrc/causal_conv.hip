@@ -112,9 +112,12 @@ __global__ __launch_bounds__(256) void causal_conv_kernel(ConvArgs a) {
     }
 }
 
-// A workgroup takes 32 pieces of eight channels and eight runs of tokens of one
+// A workgroup takes 64 pieces of four channels and eight runs of tokens of one
 // batch row, so that the weights' gradients are summed in LDS over the runs and
-// written once a workgroup: partial[part][W + 1][D].
+// written once a workgroup: partial[part][W + 1][D].  A thread adds its run's tokens in
+// float32, kConvMost at most, so that a sum's error does not grow with the length; the
+// parts are joined in float64.
+constexpr int kConvMost = 256;
 constexpr int kConvPieces = 64, kConvRuns = 8, kConvThreads = kConvPieces * kConvRuns, kConvColumns = kConvPieces * kConvChannels;
 template <int W, bool WHOLE, typename In>
 __global__ __launch_bounds__(kConvThreads) void causal_conv_bwd_kernel(ConvBwdArgs a) {
@@ -234,17 +237,17 @@ __global__ __launch_bounds__(kConvThreads) void causal_conv_bwd_kernel(ConvBwdAr
 // workgroup, eight runs of parts side by side.
 __global__ __launch_bounds__(256) void conv_sums_kernel(const float* partial, long parts, int W, int D, float* grad_w,
                                                         float* grad_bias) {
-    __shared__ float red[8][32];
+    __shared__ double red[8][32];
     const long col = (long)blockIdx.x * 32 + threadIdx.x % 32, cols = (long)(W + 1) * D;
     const int slot = threadIdx.x / 32;
-    red[slot][threadIdx.x % 32] = col < cols ? strided_sum(partial + col, slot, parts, 8, cols) : 0.f;
+    red[slot][threadIdx.x % 32] = col < cols ? strided_sum(partial + col, slot, parts, 8, cols) : 0.0;
     __syncthreads();
     if (slot != 0 || col >= cols) return;
-    float s = 0.f;
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-    if (col < (long)W * D) grad_w[col] = s;
-    else if (grad_bias) grad_bias[col - (long)W * D] = s;
+    if (col < (long)W * D) grad_w[col] = (float)s;
+    else if (grad_bias) grad_bias[col - (long)W * D] = (float)s;
 }
 
 template <int W, typename In>
@@ -261,13 +264,14 @@ static void conv_dtype(const ConvArgs& a, unsigned blocks, hipStream_t s) {
 // Tokens a thread.  Workgroups that one more round over the card would be needed for
 // cost as much as a full round, and the rows around a run are read again: of the runs
 // that make one to six rounds the one with the fewest rows to go over, if a run of
-// `side` threads over T tokens makes `blocks` workgroups and `slots` of them fit.
-static int conv_run(int T, double blocks, int slots, int side, int W) {
+// `side` threads over T tokens makes `blocks` workgroups and `slots` of them fit; no run
+// of more than `most`.
+static int conv_run(int T, double blocks, int slots, int side, int W, int most) {
     int best = 1;
     double least = 0.0;
     for (int k = 1; k <= 6; ++k) {
         const long splits = std::max(1L, (long)(k * slots / blocks));
-        const int run = std::max<long>(std::min(T, kConvLeast), (T + splits * side - 1) / (splits * side));
+        const int run = (int)std::min<long>(most, std::max<long>(std::min(T, kConvLeast), (T + splits * side - 1) / (splits * side)));
         if (run < 1) return 1;   // no tokens
         const double groups = (T + (long)run * side - 1) / ((long)run * side) * blocks;
         const double rows = (double)(long)((groups + slots - 1) / slots) * (run + 2 * (W - 1));
@@ -281,7 +285,7 @@ static int conv_run(int T, double blocks, int slots, int side, int W) {
 
 hipError_t launch_causal_conv(ConvArgs a, hipStream_t s) {
     const long pieces = (a.D + kConvChannels - 1) / kConvChannels;
-    a.run = conv_run(a.T, (double)a.B * pieces / 256, 256 * (a.bf16 && a.D % kConvChannels == 0 ? 7 : 5), 1, a.W);
+    a.run = conv_run(a.T, (double)a.B * pieces / 256, 256 * (a.bf16 && a.D % kConvChannels == 0 ? 7 : 5), 1, a.W, std::max(a.T, 1));
     a.segs = std::max(1, (a.T + a.run - 1) / a.run);   // without a token the history still moves on
     const unsigned blocks = (unsigned)(((long)a.B * a.segs * pieces + 255) / 256);
     switch (a.W) {
@@ -309,7 +313,7 @@ long conv_bwd_parts(long B, int T) { return B * ((T + (long)kConvLeast * kConvRu
 
 hipError_t launch_causal_conv_bwd(ConvBwdArgs a, hipStream_t s) {
     const long groups = (a.f.D + kConvColumns - 1) / kConvColumns;
-    a.f.run = conv_run(a.f.T, (double)a.f.B * groups, 256 * 2, kConvRuns, a.f.W);
+    a.f.run = conv_run(a.f.T, (double)a.f.B * groups, 256 * 2, kConvRuns, a.f.W, kConvMost);
     a.f.segs = (int)((a.f.T + (long)a.f.run * kConvRuns - 1) / ((long)a.f.run * kConvRuns));
     const long parts = (long)a.f.B * a.f.segs;
     const unsigned blocks = (unsigned)(parts * groups);

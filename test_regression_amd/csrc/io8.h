@@ -185,15 +185,15 @@ template <> struct Held8<float> {
 };
 
 // p[i pitch] summed over i = first, first + step, .. below n, in that order, eight
-// loads on their way at a time.
-__device__ __forceinline__ float strided_sum(const float* p, long first, long n, long step, long pitch) {
-    float s = 0.f;
+// loads on their way at a time: eight in float32, and these in float64, so that the
+// error does not grow with n.
+__device__ __forceinline__ double strided_sum(const float* p, long first, long n, long step, long pitch) {
+    double s = 0.0;
     for (long i = first; i < n; i += 8 * step) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = i + e * step < n ? p[(i + e * step) * pitch] : 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += v[e];
+        s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
     }
     return s;
 }

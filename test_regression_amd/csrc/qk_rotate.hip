@@ -238,16 +238,16 @@ __global__ __launch_bounds__(256) void qk_rotate_bwd_kernel(RotateBwdArgs g) {
 // grad_wq and grad_wk over the workgroups' parts: eight columns a workgroup, 32 runs of
 // parts side by side.
 __global__ __launch_bounds__(256) void rotate_sums_kernel(const float* partial, long parts, int d, float* gq, float* gk) {
-    __shared__ float red[32][8];
+    __shared__ double red[32][8];
     const int col = blockIdx.x * 8 + threadIdx.x % 8, slot = threadIdx.x / 8;
     red[slot][threadIdx.x % 8] = strided_sum(partial + col, slot, parts, 32, 2L * d);
     __syncthreads();
     if (slot != 0) return;
-    float s = 0.f;
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
     float* to = col < d ? gq : gk;
-    if (to) to[col % d] = s;
+    if (to) to[col % d] = (float)s;
 }
 
 // Rows of a token side by side: as few as still fill the card (a lane's cosines
