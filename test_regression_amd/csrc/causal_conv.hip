@@ -22,11 +22,24 @@
 
 namespace mesa {
 
-__device__ __forceinline__ float conv_sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 __device__ __forceinline__ float conv_sigmoid_exact(float z) { return 1.0f / (1.0f + expf(-z)); }
-// bf16 outputs take the fast exponential (off by |z| 2^-24, little beside their rounding).
+// Outputs in bfloat16 take the fast exponential (off by |z| 2^-24, little beside their
+// rounding).
 template <typename In>
-__device__ __forceinline__ float conv_act(float z) { return sizeof(In) == 2 ? conv_sigmoid(z) : conv_sigmoid_exact(z); }
+__device__ __forceinline__ float conv_act(float z) {
+    return sizeof(In) == 2 ? __builtin_amdgcn_rcpf(1.0f + __expf(-z)) : conv_sigmoid_exact(z);
+}
+// The weights' gradients are float32 for bfloat16 rows too: the power's rounding is taken
+// off again to first order (z below -88 as -88, where float32 ends).  64 x 8192 tokens, 1024
+// channels: 658 us without it, 680 us with it, 710 us with expf.
+template <typename In>
+__device__ __forceinline__ float conv_act_bwd(float z) {
+    if constexpr (sizeof(In) == 4) return conv_sigmoid_exact(z);
+    constexpr float log2e = 1.442695041f, log2e_rest = 1.925963e-8f, ln2 = 0.6931471806f;
+    const float x = fmaxf(z, -88.0f), power = x * -log2e, e = __builtin_amdgcn_exp2f(power);
+    const float rest = fmaf(x, -log2e_rest, fmaf(x, -log2e, -power));
+    return __builtin_amdgcn_rcpf(1.0f + fmaf(e, rest * ln2, e));
+}
 
 __device__ __forceinline__ int conv_length(const int32_t* lens, long b, int T) {
     return lens ? min(max(lens[b], 0), T) : T;
@@ -179,7 +192,7 @@ __global__ __launch_bounds__(kConvThreads) void causal_conv_bwd_kernel(ConvBwdAr
                         float z = bias[e] + w[0][e] * in[i][e];
 #pragma unroll
                         for (int j = 1; j < W; ++j) z += w[j][e] * last[j - 1][e];
-                        const float s = a.f.silu ? conv_act<In>(z) : 1.0f;
+                        const float s = a.f.silu ? conv_act_bwd<In>(z) : 1.0f;
                         cur[e] = a.f.silu ? g[i][e] * s * (1.0f + z * (1.0f - s)) : g[i][e];
                     }
                 if (at < end)

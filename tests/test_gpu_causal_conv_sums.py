@@ -1,5 +1,6 @@
-"""The weights' gradients of the causal convolution as sums: long batches, and
-lengths on both sides of a thread's run and of a workgroup's eight.
+"""The weights' gradients of the causal convolution as sums: long batches, lengths on
+both sides of a thread's run and of a workgroup's eight, and slopes of far negative
+values.
 
 Bounds, relative to the sizes of the terms.  A thread adds at most 256 tokens in
 float32, a workgroup the eight runs; workgroups are joined by eight in float32 and these
@@ -93,3 +94,26 @@ def test_lengths_around_the_runs(T, W, dtype):
         near(r["grad_x"], rg["grad_x"], out + 112 * U, what="grad_x")
         for n in ("grad_w", "grad_bias"):
             near(r[n], rg[n], sums(T), terms[n], what=n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("z", [-81.875, -65.625, -12.0, 2.0])
+def test_slopes_of_far_values(z, dtype):
+    """Float32 gradients of the weights take the exponential to its own rounding, of
+    bfloat16 rows too.  z = bias + x is exact here, so a term is met with the exponential
+    (2), a sum, a reciprocal (2), the slope's three operations (in which 1 - s is off by two
+    roundings of 1 where s is near it, times z), the product, and 4 + 8 additions: below
+    24 roundings."""
+    import torch
+    from test_regression_amd import mesa
+    say("case conv far values", z, dtype)
+    x, xf = store(np.full((1, 4, 4), 0.5), dtype)
+    dy, dyf = store(np.ones((1, 4, 4)), dtype)
+    w, wf = store(np.ones((1, 4)), "f32")
+    bias, bf = store(np.full(4, z - 0.5), "f32")
+    r = mesa.mesa_causal_conv_backward(x.cuda(), w.cuda(), dy.cuda(), bias.cuda())
+    torch.cuda.synchronize()
+    _, _, rg, _ = conv_ref(xf, wf, bf, dy=dyf)
+    for n in ("grad_w", "grad_bias"):
+        got = r[n].double().cpu().numpy()
+        assert np.abs(got - rg[n]).max() <= 24 * U * np.abs(rg[n]).max(), (n, (got - rg[n]).max() / np.abs(rg[n]).max() / U)
