@@ -105,8 +105,9 @@ __device__ __forceinline__ void settle(F8& x) {
 // the small parts first, -2e-10 with the large one first and below 3e-11 with the small
 // parts in an accumulator of their own; a gradient that sums a sequence's terms of
 // mixed sign shows the first two (grad_A of 2x32x4096: 4e-6, 1.7e-6 and 6e-7).  So
-// what feeds states and gradients is taken apart (mma_pair), and added to the state
-// outside.  The steps are written with the accumulator
+// what the gradients sum is taken apart (mma_pair); what the forward's states take keeps
+// one accumulator, whose bias is far below a float32 rounding of the state.  Both are
+// added to the state outside.  The steps are written with the accumulator
 // tied to its destination (delta_core.h says why and what has to stand around them).
 template <typename T> inline constexpr int parts_of = 1;
 template <> inline constexpr int parts_of<B2> = 2;
@@ -149,46 +150,27 @@ __device__ __forceinline__ void mma(f32x4 (&C)[N], const A& a, const B (&b)[N]) 
             else mma_step<false>(C[i], a, b[i], s);
         }
 }
-// C[i] = a0 b0[i] + a1 b1[i] (or a0[i] b0 + a1[i] b1), ready for use; EXACT: the largest
-// parts and the others in accumulators of their own.
-template <int N, typename Step>
-__device__ __forceinline__ void mma_apart(f32x4 (&C)[N], int steps, Step step) {
-    f32x4 low[N];
-#pragma unroll
-    for (int s = 0; s < 2 * steps; ++s)      // step s / 2 of operand pair s % 2
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (s < 2) step(C[i], i, s, s == 0);
-            else step(low[i], i, s, s == 2);
-        }
-    mfma_done(C, low);
-#pragma unroll
-    for (int i = 0; i < N; ++i) C[i] += low[i];
-}
-template <bool EXACT = true, int N, typename A, typename B>
+// C[i] = a0 b0[i] + a1 b1[i], ready for use, of parts: the largest and the others in
+// accumulators of their own.
+template <int N, typename A, typename B>
 __device__ __forceinline__ void mma_pair(f32x4 (&C)[N], const A& a0, const B (&b0)[N], const A& a1, const B (&b1)[N]) {
-    if constexpr (!EXACT || std::is_same_v<A, F8>) {
+    if constexpr (std::is_same_v<A, F8>) {
         mma<true>(C, a0, b0);
         mma(C, a1, b1);
         mfma_done(C);
     } else {
-        mma_apart(C, mma_steps<A, B>, [&](f32x4& c, int i, int s, bool first) {
-            if (first) mma_step<true>(c, s % 2 ? a1 : a0, s % 2 ? b1[i] : b0[i], s / 2);
-            else mma_step<false>(c, s % 2 ? a1 : a0, s % 2 ? b1[i] : b0[i], s / 2);
-        });
-    }
-}
-template <bool EXACT = true, int N, typename A, typename B>
-__device__ __forceinline__ void mma_pair(f32x4 (&C)[N], const A (&a0)[N], const B& b0, const A (&a1)[N], const B& b1) {
-    if constexpr (!EXACT || std::is_same_v<A, F8>) {
-        mma<true>(C, a0, b0);
-        mma(C, a1, b1);
-        mfma_done(C);
-    } else {
-        mma_apart(C, mma_steps<A, B>, [&](f32x4& c, int i, int s, bool first) {
-            if (first) mma_step<true>(c, s % 2 ? a1[i] : a0[i], s % 2 ? b1 : b0, s / 2);
-            else mma_step<false>(c, s % 2 ? a1[i] : a0[i], s % 2 ? b1 : b0, s / 2);
-        });
+        f32x4 low[N];
+#pragma unroll
+        for (int s = 0; s < 2 * mma_steps<A, B>; ++s)   // step s / 2 of operand pair s % 2
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                f32x4& c = s < 2 ? C[i] : low[i];
+                if (s == 0 || s == 2) mma_step<true>(c, a0, b0[i], s / 2);
+                else mma_step<false>(c, s % 2 ? a1 : a0, s % 2 ? b1[i] : b0[i], s / 2);
+            }
+        mfma_done(C, low);
+#pragma unroll
+        for (int i = 0; i < N; ++i) C[i] += low[i];
     }
 }
 template <bool FIRST = false, typename A, typename B>

@@ -59,9 +59,10 @@ __device__ __forceinline__ typename PV::Three weighted(const typename PV::One& x
     return PV::three(f);
 }
 
-// st = decay st + the rows' columns (transposed) times w, four tiles at a time.  EXACT
-// keeps the parts' sums apart, for the gradients; one sum saves 32 additions a chunk.
-template <int N, bool FLIP, bool EXACT, typename PN, typename W>
+// st = decay st + the rows' columns (transposed) times w, four tiles at a time.
+// STATES, for the gradients: the states' columns lie along the lanes' rows, and the
+// parts' sums are kept apart; one sum saves 32 additions a chunk.
+template <int N, bool STATES, typename PN, typename W>
 __device__ __forceinline__ void add_outer(f32x4 (&st)[N / 16], float decay, const PN& rows, const W& w0, const W& w1, int m, int g) {
     constexpr int H = N / 16 < 4 ? N / 16 : 4;
 #pragma unroll
@@ -73,8 +74,13 @@ __device__ __forceinline__ void add_outer(f32x4 (&st)[N / 16], float decay, cons
             k1[i] = rows.col(h + i, 1, m, g);
         }
         f32x4 u[H];
-        if constexpr (FLIP) mma_pair<EXACT>(u, w0, k0, w1, k1);
-        else mma_pair<EXACT>(u, k0, w0, k1, w1);
+        if constexpr (STATES) {
+            mma_pair(u, w0, k0, w1, k1);
+        } else {
+            mma<true>(u, k0, w0);
+            mma(u, k1, w1);
+            mfma_done(u);
+        }
 #pragma unroll
         for (int i = 0; i < H; ++i) st[h + i] = st[h + i] * decay + u[i];
     }
@@ -221,7 +227,7 @@ __global__ __launch_bounds__(256, sizeof(In) == 2 ? 2 : 1) void ssm_out_kernel(S
             }
             // S' = e^{l_63} S + B^T diag(e^{l_63 - l} D) X
             const auto w0 = weighted<PV>(x0, sl.write, 0, g), w1 = weighted<PV>(x1, sl.write, 1, g);
-            add_outer<N, false, false>(st, sl.decay, S.b, w0, w1, m, g);
+            add_outer<N, false>(st, sl.decay, S.b, w0, w1, m, g);
         }
         __syncthreads();
     }
@@ -297,12 +303,10 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
     __shared__ WalkLds<N, In> lds[2];
     __shared__ Scalars scal[4];   // of the chunk passed over, the one prepared, the one after
     const int dk = N > 32 ? N : a.dk;
-    const SsmPlace p = ssm_place(a, xcd_order(), a.nseg);
+    const SsmPlace p = ssm_place(a, xcd_order(), 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, m = lane % 16, g = lane / 16;
     const int hk = p.h / (a.H / a.Hk);
-    const long first = (long)p.seg * a.seg_chunks * kSC;
-    const long last = min((long)a.T, first + (long)a.seg_chunks * kSC);   // the segment's tokens
-    const int chunks = first < p.valid ? (int)((min((long)p.valid, last) - first + kSC - 1) / kSC) : 0;
+    const int chunks = (int)(((long)p.valid + kSC - 1) / kSC);
     const bool carries = wave < 4, mine = carries && 16 * wave < p.cols;
     const int v = p.v0 + 16 * (wave % 4);   // the wave's columns of dv
     const In* xr = static_cast<const In*>(a.x) + p.b * a.xs.batch + p.h * a.xs.head + p.v0;
@@ -322,10 +326,10 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
     Stage<In, N> sb(a.bs.token, dk), sc(a.cs.token, dk);
     Stage<In, 64> sx(a.xs.token, p.cols);
     uint32_t raw = 0u;   // wave 7: the step sizes to come
-    auto tokens = [&](int c) { return (int)min((long)kSC, p.valid - first - (long)c * kSC); };
+    auto tokens = [&](int c) { return (int)min((long)kSC, p.valid - (long)c * kSC); };
     auto fetch = [&](int c) {
         if (c >= chunks) return;
-        const long t0 = first + (long)c * kSC;
+        const long t0 = (long)c * kSC;
         const int n = tokens(c);
         sb.load(br + t0 * a.bs.token, a.bs.token, dk, n);
         sc.load(cr + t0 * a.cs.token, a.cs.token, dk, n);
@@ -353,9 +357,9 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
         mma(o[2], x1, S.m.row(2, 1, m, g));
         mma(o[3], x1, S.m.row(3, 1, m, g));
         mfma_done(o);
-        const long t0 = first + (long)c * kSC;
+        const long t0 = (long)c * kSC;
         In* to = out + t0 * a.dv;
-        const int n = tokens(c), rows = (int)min((long)kSC, last - t0);
+        const int n = tokens(c), rows = (int)min((long)kSC, a.T - t0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 16 * i + m;
@@ -367,7 +371,7 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
         }
         // S' = e^{l_63} S + B^T diag(e^{l_63 - l} D) X
         const auto w0 = weighted<PV>(x0, sl.write, 0, g), w1 = weighted<PV>(x1, sl.write, 1, g);
-        add_outer<N, false, false>(st, sl.decay, S.b, w0, w1, m, g);
+        add_outer<N, false>(st, sl.decay, S.b, w0, w1, m, g);
     };
     // waves 4 to 6 take the tiles below the diagonal of one column block and one
     // diagonal tile, wave 7 the last one and the scalars of the chunk after
@@ -385,7 +389,7 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
         if (c < chunks) chunk_scalars(scal[c & 3], lane < tokens(c) ? step_of(raw_step(a, raw, bias), a.softplus) : 0.0f, A);
     };
     auto fetch_raw = [&](int c) {
-        if (c < chunks && lane < tokens(c)) raw = step_bits(a, p.b, p.h, first + (long)c * kSC + lane);
+        if (c < chunks && lane < tokens(c)) raw = step_bits(a, p.b, p.h, (long)c * kSC + lane);
     };
     if (!carries) {
         fetch(0);
@@ -426,9 +430,9 @@ __global__ __launch_bounds__(512) void ssm_walk_kernel(SsmArgs a) {
     }
     if (!mine) return;
     // rows past the length (whole chunks of them)
-    for (long t = first + (long)chunks * kSC + lane / 4; t < last; t += 16)
+    for (long t = (long)chunks * kSC + lane / 4; t < a.T; t += 16)
         store4(out + t * a.dv + 4 * (lane % 4), f32x4{0.f, 0.f, 0.f, 0.f});
-    if (a.final_state && p.seg == a.nseg - 1)
+    if (a.final_state)
 #pragma unroll
         for (int i = 0; i < N / 16; ++i)
             if (16 * i < dk) store4(a.final_state + (p.bh * a.dv + v + m) * dk + 16 * i + 4 * g, st[i]);
@@ -529,7 +533,7 @@ __device__ __forceinline__ void ssm_carry(const SsmArgs& a, CarryLds<N, In>& S, 
         if (mine) {
             const auto w0 = weighted<PV>(S.x.col(wave, 0, m, g), BACK ? sl.in : sl.write, 0, g);
             const auto w1 = weighted<PV>(S.x.col(wave, 1, m, g), BACK ? sl.in : sl.write, 1, g);
-            add_outer<N, STATES, STATES>(st, sl.decay, S.b, w0, w1, m, g);
+            add_outer<N, STATES>(st, sl.decay, S.b, w0, w1, m, g);
         }
         __syncthreads();
     }
