@@ -205,33 +205,49 @@ __global__ __launch_bounds__(256) void qk_rotate_kernel(RotateArgs a) {
     rotate_heads<true, d, INTER, In>(a, r, partner, slot, d0, b, t);
 }
 
+// The weights' gradients of a lane's features are added in float32 over kRotateAdd tokens
+// and these in float64, in the lane's own places in LDS, so that a sum's error does not
+// grow with the tokens.
+constexpr int kRotateAdd = 16;
 template <int d, bool INTER, typename In>
 __global__ __launch_bounds__(256) void qk_rotate_bwd_kernel(RotateBwdArgs g) {
     constexpr int L = d / 8, rows = 256 / L;
-    __shared__ float red[2][rows][d + 4];
+    __shared__ double red[2][rows][d + 2];
     const RotateArgs& a = g.f;
     const int lane = threadIdx.x % L, row = threadIdx.x / L, d0 = 8 * lane;
     const int slot = row % a.slots;
     const int partner = partner_lane(threadIdx.x % 64, d0, a.rot);
     f32x8 dw[2] = {};
+    bool first = true;
+    auto put = [&] {
+        if (!g.partial) return;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) red[k][row][d0 + e] = (first ? 0.0 : red[k][row][d0 + e]) + dw[k].v[e];
+        dw[0] = dw[1] = f32x8{};
+        first = false;
+    };
     const long step = rows / a.slots, all = (long)a.B * a.T;
+    int held = 0;
     for (long at = (long)blockIdx.x * step + row / a.slots; at < all; at += (long)gridDim.x * step) {
         const long b = at / a.T, t = at - b * a.T;
         Turns<INTER> r;
         r.at(a, b, t, d0);
         rotate_heads_bwd<false, d, INTER, In>(g, r, partner, slot, d0, b, t, dw[0]);
         rotate_heads_bwd<true, d, INTER, In>(g, r, partner, slot, d0, b, t, dw[1]);
+        if (++held == kRotateAdd) {
+            put();
+            held = 0;
+        }
     }
     if (!g.partial) return;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) red[k][row][d0 + e] = dw[k].v[e];
+    put();
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * d; c += 256) {
-        float s = 0.f;
+        double s = 0.0;
         for (int i = 0; i < rows; ++i) s += red[c / d][i][c % d];
-        g.partial[(long)blockIdx.x * 2 * d + c] = s;
+        g.partial[(long)blockIdx.x * 2 * d + c] = (float)s;
     }
 }
 

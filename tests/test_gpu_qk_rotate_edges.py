@@ -89,3 +89,25 @@ def test_features_past_the_rotation_stay(d, rot, inter, dtype):
         want = torch.cat([clean[..., :rot], x[..., rot:]], -1)
         nan = want.isnan()
         assert torch.equal(got.isnan(), nan) and torch.equal(got[~nan], want[~nan])
+
+
+def test_weight_gradients_of_many_tokens():
+    """Equal terms of which a float32 sum of 256 loses just under half a last place with
+    every addition from 128 on: 2^25 tokens of one head at position 0, where the rotation
+    is the identity, with rows of ones, whose norm is exactly one.  A lane adds 16 terms in
+    float32, workgroups and lanes are joined in float64 but for batches of eight: below 32
+    roundings of 2^-24."""
+    import torch
+    from test_regression_amd import mesa
+    say("case many tokens")
+    T, d = 1 << 25, 16
+    term = 1 + 0.49 * 2.0 ** -16 + 2.0 ** -23
+    term = float(np.float32(term))
+    x = torch.ones((1, 1, 1, d), device="cuda").expand(1, 1, T, d)
+    dy = torch.full((1, 1, T, d), term, device="cuda")
+    freqs, _ = mesa.mesa_rotary_frequencies(16)
+    pos = torch.zeros(T, dtype=torch.int64, device="cuda")
+    r = mesa.mesa_qk_rotate_backward(x, None, dy, None, freqs, pos, torch.ones(d, device="cuda"), eps=2.0 ** -40)
+    torch.cuda.synchronize()
+    got = r["grad_wq"].double().cpu().numpy()
+    assert np.abs(got - T * term).max() <= 32 * U * T * term, (got - T * term) / (T * term) / U
