@@ -1265,8 +1265,8 @@ static SsmBwdLayout ssm_bwd_layout(int B, int H, int T, int dk, int dv, size_t s
 size_t mesa_ssm_backward_workspace_bytes(int B, int Hk, int H, int T, int dk, int dv, int dtype) {
     if (B <= 0 || Hk <= 0 || H <= 0 || H % Hk != 0 || T <= 0 || dk <= 0 || dv <= 0 || !dtype_ok(dtype)) return 0;
     // enough for every smaller batch and shorter sequence too: those may split the heads further, but
-    // into at most kSsmGradGroups workgroups (of a part, row, group and chunk) where there is more than one part
-    const size_t parts = H > Hk ? std::min((size_t)mesa::kSsmGradGroups, (size_t)B * H * ssm_chunks(T)) : 0;
+    // into at most kSsmGradMost workgroups (of a part, row, group and chunk) where there is more than one part
+    const size_t parts = H > Hk ? std::min((size_t)mesa::kSsmGradMost, (size_t)B * H * ssm_chunks(T)) : 0;
     return ssm_bwd_layout(B, H, T, dk, dv, mesa::ssm_segment_slots((long)B * H, (int)ssm_chunks(T), dv, 2), parts).total;
 }
 

@@ -215,9 +215,11 @@ struct SsmGradArgs {
     float* part;     // parts > 1: [parts][B Hk][2][T][dk], dC and dB
     double* sums;    // [H][3][B nc]
 };
-// Workgroups of the gradients, where splitting the heads gives more: one a CU (2 x 32 heads of 4096 tokens, dk 128, dv 64,
-// bfloat16: 151 us, with two in turn 162 us).
-constexpr int kSsmGradGroups = 256;
+// The gradients' workgroups go over the card in turns of kSsmGradCUs; splitting the heads gives at most kSsmGradMost.
+// 2 x 32 heads of 4096 tokens, dk 128, dv 64, bfloat16, the gradient kernel: 151 us in one turn of 16 heads, 162 us in
+// two of eight.  Whole calls of 3 and 5 such rows: 372 and 615 us in 3 and 5 turns of eight heads, 394 and 718 us
+// unsplit in one and two of 32.
+constexpr long kSsmGradCUs = 256, kSsmGradMost = 1280;
 int ssm_segments(long BH, int nc, int dv, int sides);         // the number of segments; the backward has two sides
 // States that a head's segments keep: their starts, for the gradients the ends of both directions.
 constexpr int ssm_slots(int nseg, int sides) { return nseg == 1 ? 0 : sides * nseg; }

@@ -514,10 +514,20 @@ static void grads_go(const SsmGradArgs& a, unsigned blocks, hipStream_t s) {
     else hipLaunchKernelGGL((ssm_grads_kernel<N, float>), dim3(blocks), dim3(kGradThreads), 0, s, a);
 }
 
-// Workgroups that share the heads of one b and c: as many as fill the card.
+// Workgroups that share the heads of one b and c.  A CU takes one at a time: the fewest
+// turns over the card times a turn's heads, a turn's start and end (b and c staged, their
+// products, the parts) counted as one and a half heads (as measured at kSsmGradCUs).
 int ssm_grad_parts(long B, int Hk, int H, int nc) {
-    const long groups = B * Hk * nc;
-    return (int)std::min<long>(H / Hk, std::max(1L, kSsmGradGroups / std::max(groups, 1L)));
+    const long groups = B * Hk * nc, rep = H / Hk, most = std::min(rep, std::max(1L, kSsmGradMost / groups));
+    long best = 1, least = 0;
+    for (long n = 1; n <= most; ++n) {
+        const long turns = (groups * n + kSsmGradCUs - 1) / kSsmGradCUs, cost = turns * (2 * ((rep + n - 1) / n) + 3);
+        if (n == 1 || cost < least) {
+            best = n;
+            least = cost;
+        }
+    }
+    return (int)best;
 }
 
 hipError_t launch_ssm_grads(const SsmGradArgs& a, hipStream_t s) {

@@ -157,6 +157,21 @@ def test_several_heads_a_workgroup(size, dtype):
         run(t, lens, dtype, H)
 
 
+# chunks that do not divide the card: parts of two to eight heads in several turns
+TURNS = [(64, 1, 32, 130, 16, 16), (107, 1, 8, 130, 32, 32), (20, 4, 24, 200, 64, 16)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("size", TURNS)
+def test_parts_in_several_turns(size, dtype):
+    B, Hk, H, T, dk, dv = size
+    say("case turns", size, dtype)
+    rng = np.random.default_rng(B)
+    lens = [int(rng.integers(0, T + 1)) for _ in range(B)]
+    t, _ = ssm_inputs(B + H, B, Hk, H, T, dk, dv, dtype, True, lens)
+    run(t, lens, dtype, H)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("size", [(1, 1, 2, 1100, 32, 16), (1, 2, 2, 2111, 64, 128), (3, 1, 1, 1537, 128, 64), (1, 1, 3, 700, 128, 128)])
 def test_gradients_of_segments_that_see_one_another(size, dtype):
