@@ -101,9 +101,10 @@ def test_lengths_around_the_runs(T, W, dtype):
 def test_slopes_of_far_values(z, dtype):
     """Float32 gradients of the weights take the exponential to its own rounding, of
     bfloat16 rows too.  z = bias + x is exact here, so a term is met with the exponential
-    (2), a sum, a reciprocal (2), the slope's three operations (in which 1 - s is off by two
-    roundings of 1 where s is near it, times z), the product, and 4 + 8 additions: below
-    24 roundings."""
+    (1 of its own, and what ln 2 in float32 leaves of its power: 2^-28 of z, 5 at most), a
+    sum, a reciprocal (2), the slope's three operations (in which 1 - s is off by two
+    roundings of 1 where s is near it, times z), the product, and 3 + 8 additions: 24
+    roundings."""
     import torch
     from test_regression_amd import mesa
     say("case conv far values", z, dtype)
