@@ -1402,6 +1402,9 @@ mesa_status mesa_rotary_frequencies(int rot, double base, int scaling, double fa
     return MESA_OK;
 }
 
+static View positions_view(const int64_t* p, int64_t stride, int B, int T) {
+    return {p, {(long)stride, 0, 1}, B, 1, T, 1, 8, "positions"};
+}
 static mesa_status rotate_checks(const void* q, const void* k, int dtype, const double* freqs, int rot, float amplitude,
                                  const int64_t* positions, int64_t positions_stride, const float* wq, const float* wk, int norm,
                                  float eps, int B, int Hq, int Hk, int T, int d) {
@@ -1438,7 +1441,7 @@ mesa_status mesa_qk_rotate(const void* q, const int64_t* q_strides, const void* 
     const View vq = strided(q, q_strides, B, Hq, T, d, dtype, "q"), vk = strided(k, k_strides, B, Hk, T, d, dtype, "k");
     st = check_views({plain(yq, bytes_of(dtype, (double)B * Hq * T * d), "yq"), plain(Hk ? yk : nullptr, bytes_of(dtype, (double)B * Hk * T * d), "yk")},
                      {vq, vk, plain(freqs, (size_t)rot * 4, "freqs"), plain(wq, (size_t)d * 4, "wq"), plain(wk, (size_t)d * 4, "wk"),
-                      plain(positions, T > 0 ? ((size_t)positions_stride * (B - 1) + T) * 8 : 0, "positions")});
+                      positions_view(positions, positions_stride, B, T)});
     if (st != MESA_OK) return st;
     if (T == 0) return MESA_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -1477,7 +1480,7 @@ mesa_status mesa_qk_rotate_backward(const void* q, const int64_t* q_strides, con
     const size_t db = (size_t)d * 4;
     st = check_views({gq, gk, plain(grad_wq, db, "grad_wq"), plain(grad_wk, db, "grad_wk"), plain(workspace, need, "workspace")},
                      {vq, vk, plain(freqs, (size_t)rot * 4, "freqs"), plain(wq, db, "wq"), plain(wk, db, "wk"),
-                      plain(positions, T > 0 ? ((size_t)positions_stride * (B - 1) + T) * 8 : 0, "positions"),
+                      positions_view(positions, positions_stride, B, T),
                       plain(grad_yq, bytes_of(dtype, (double)B * Hq * T * d), "grad_yq"),
                       plain(Hk ? grad_yk : nullptr, bytes_of(dtype, (double)B * Hk * T * d), "grad_yk")});
     if (st != MESA_OK) return st;
