@@ -545,11 +545,13 @@ mesa_status mesa_causal_conv_backward(const void *x, const int64_t *x_strides, i
  *                               none is needed), which never decreases with B, H
  *                               or T
  * dk and dv in {16, 32, 64, 128}, T >= 0, token strides of x, b and c below 2^23.
- * Sums and states are float32, prefix sums of the decays float64.  Rows stored as bfloat16 enter the products exactly; what
- * is formed in float32 enters as two bfloat16 parts where only bfloat16 outputs
- * follow (2^-18 of a term) and as three (2^-27) where the state does.  Values are
- * taken as finite: a NaN or infinity reaches its chunk of 64 tokens and what
- * follows in its head, other heads never (of b and c: of the heads that share them).
+ * Sums and states are float32, prefix sums of the decays float64.  Rows stored as
+ * bfloat16 enter the products exactly; what is formed in float32 enters as two
+ * bfloat16 parts where only bfloat16 outputs follow (2^-18 of a term, below their
+ * rounding unless terms cancel by more than about 2^9) and as three (2^-27) where the
+ * state does.  Values are taken as finite: a NaN or infinity reaches its chunk of 64
+ * tokens and what follows in its head, other heads never (of b and c: of the heads
+ * that share them).
  */
 size_t mesa_ssm_workspace_bytes(int B, int H, int T, int dk, int dv, int dtype);
 mesa_status mesa_ssm_forward(const void *x, const int64_t *x_strides, const void *b, const int64_t *b_strides,

@@ -13,7 +13,7 @@
 // the next ones on their way; eight channels a thread left half as many waves and no
 // registers to load ahead with.  Sums are float32; outputs are rounded once.  8 x 4096
 // tokens, 2304 channels, W 4, bfloat16: 64 us (4.7 TB/s), with eight channels 83 us;
-// the gradients 94 us (4.8 TB/s) and 5 us for the parts' sums, with eight channels 204
+// the gradients 97 us (4.7 TB/s) and 4 us for the parts' sums, with eight channels 204
 // and 10 us, with four and no loads ahead 129 us.
 #include <algorithm>
 
@@ -276,7 +276,9 @@ static void conv_dtype(const ConvArgs& a, unsigned blocks, hipStream_t s) {
 // cost as much as a full round, and the rows around a run are read again: of the runs
 // that make one to six rounds the one with the fewest rows to go over, if a run of
 // `side` threads over T tokens makes `blocks` workgroups and `slots` of them fit; no run
-// of more than `most`.
+// of more than `most`.  The slots are those of W = 4 (seven workgroups a CU in bfloat16,
+// five otherwise); narrower windows fit up to eight, and their own counts gain 2.5 % at
+// 64 x 8192 x 1024 in bfloat16 and lose 4 % at 8 x 4096 x 2304 in float32.
 static int conv_run(int T, double blocks, int slots, int side, int W, int most) {
     int best = 1;
     double least = 0.0;

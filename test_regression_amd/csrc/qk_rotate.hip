@@ -19,7 +19,7 @@
 // features; a lane forms the cosines and sines of its features once a token and
 // uses them for all heads that it takes of the token.  16 + 4 heads of 8 x 4096
 // tokens, d 128, bfloat16: 56-70 us forward (4.8-6.0 TB/s; the next head's row on its way,
-// without it 74 us), 81-86 us backward (5.9 TB/s) and 4 us for the weights' sums.
+// without it 74 us), 82-87 us backward (5.9 TB/s) and 4 us for the weights' sums.
 #include <algorithm>
 
 #include "io8.h"

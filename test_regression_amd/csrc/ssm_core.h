@@ -257,8 +257,9 @@ template <int W> struct Plane<float, W> {
     static __device__ __forceinline__ F8 three(float (&v)[8]) { return two(v); }
 };
 
-// A 64 x 64 matrix formed in float32 (in two parts for bfloat16 rows), lower block
-// triangle, row r's columns as k-slots.
+// A 64 x 64 matrix formed in float32, lower block triangle, row r's columns as k-slots.
+// For bfloat16 rows in two parts: what its products give is stored as bfloat16, and 2^-18
+// of a term shows there only where terms cancel by more than about 2^9.
 template <typename In> struct Square;
 template <> struct Square<bf16_t> {
     Plane<bf16_t, 64> p[2];

@@ -19,11 +19,13 @@
 // from float32 parts.  dv goes by in pieces of 64 columns, in all of which the
 // formulas are sums.
 //
-// 2 x 32 heads of 4096 tokens that share b and c, dk 128, dv 64, bfloat16: 151 us (366
+// 2 x 32 heads of 4096 tokens that share b and c, dk 128, dv 64, bfloat16: 151 us (354
 // MB fetched, of which the states 268 MB), and 90 us for the states.  A head's chunk
 // takes 19,000 cycles of a workgroup that fills its CU: pairs 8,000, states 5,000 and
-// their wait 2,000, dX 3,000; the VALU issues 44 % of the time (float64 decays, three-part
-// splits), the matrix units 11 %.  With twice the workgroups in two turns 162 us; so, and
+// their wait 2,000, dX 3,000; the VALU issues 47 % of the time (float64 decays, three-part
+// splits), the matrix units 11 %.  Strides and addresses do not fit the scalar registers:
+// the compiler keeps 178 to 225 of them in lanes of vector registers, and at dk 128 in
+// float32 21 vector registers in scratch.  With twice the workgroups in two turns 162 us; so, and
 // with wave 7's sums after dX, where the others waited for them, 182 us; with branches
 // around the states' loads and the heads' scalars by vector loads, behind which the wave
 // waited, 209 us.
@@ -38,7 +40,9 @@ constexpr int kGradThreads = 512;
 // while those of this one are read: all but the widest float32 rows, which fill the LDS.
 template <int N, typename In> constexpr int kGradBuffers = sizeof(In) == 4 && N == 128 ? 1 : 2;
 
-// A state's rows of dk by 64 columns of dv: two parts, or float32.
+// A state's rows of dk by 64 columns of dv, float32, or for bfloat16 rows the first two
+// of its parts: only dX takes it from here, which is stored as bfloat16 (2^-18 of a term
+// beside 2^-8 of the sum), and at dk 128 a third plane would not fit the LDS.
 template <typename In, int N> struct StatePlane;
 template <int N> struct StatePlane<bf16_t, N> {
     static constexpr int pitch = Plane<bf16_t, 64>::pitch;

@@ -591,8 +591,13 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(float* ends, const float*
         grad_state[(bh - back) * per + (long)(at % dv) * dk + at / dv] = decay[bh * nseg + nseg - 1] * s + p[(nseg - 1L) * per];
 }
 
-// Workgroups from which on ssm_walk_kernel leaves too few CUs idle for segments to pay
-// (measured per chunk and CU: 3.7 us against 3.3 us and 1.05 us for the ends).
+// Workgroups from which on whole sequences leave too few CUs idle for segments to pay
+// (measured per chunk and CU, dk 128, dv 64, bfloat16: 3.7 us in ssm_walk_kernel against
+// 3.3 us and 1.05 us for the ends).  256 heads of 4096 tokens, whole and in two segments,
+// in us, dk / dv: bfloat16 128/64 217 and 259, 64/64 181 and 198, 16/16 126 and 129; float32
+// 64/64 322 and 388, 16/16 189 and 199, and 128/64, where it is ssm_out_kernel with one
+// workgroup a CU both times, 688 and 826.  Of 216 heads narrow bfloat16 ones would gain
+// from segments (16/16: 126 and 114), the others not (128/64: 217 and 271).
 constexpr long kSsmCUs = 256, kSsmWalk = 216;
 enum SsmPass { kOut, kEnds, kStates };
 template <int N, typename In>
@@ -645,7 +650,8 @@ hipError_t launch_ssm_states(const SsmArgs& a, hipStream_t s) {
 // heads of 16384 tokens, dk and dv 128, bfloat16: 166 us in 16 segments (two workgroups a
 // CU), 204 us in 8.  16 heads of 1024 tokens, dk 128, dv 64, bfloat16: 58 us in one segment,
 // 37 in four, 28 in eight, their gradients 59, 52 and 50 us; of 256 tokens 19 us in one,
-// 23 us in two.
+// 23 us in two.  Of float32 rows with dk 128 one workgroup fits a CU: 64 heads of 4096
+// tokens 242 us in eight segments, 250 in four; 16 heads 94 in 32, 81 in 16.
 constexpr long kSsmFill = 512;
 constexpr int kSsmLeast = 2, kSsmShort = 8, kSsmMost = 32;
 int ssm_segments(long BH, int nc, int dv, int sides) {
