@@ -637,7 +637,8 @@ mesa_status mesa_rotary_frequencies(int rot, double base, int scaling, double fa
  *   positions [B, T] int64 (or [T], positions_stride 0), batch stride
  *             positions_stride; NULL: token t is at position0 + t.  Angles are
  *             formed as pairs of float64 values: float32's accuracy at
- *             positions up to 2^50 to either side (of frequencies up to 1)
+ *             positions up to 2^50 to either side (of frequencies up to 1);
+ *             farther ones turn by some angle
  *   wq, wk    [d]             float32 weights of the norm, or NULL for 1
  *   yq, yk    [B, Hq, T, d], [B, Hk, T, d]  dtype
  * d in {16, 32, 64, 128, 256}; eps > 0.  A row of zeros gives zeros.  Squares are

@@ -45,7 +45,8 @@ __device__ __forceinline__ float rest_of_quarters(double p, double f, int* k) {
     const double all = p * one, rest = fma(p, one_rest, fma(p, one, -all));
     const double sum = all + ones;
     *k = (int)__builtin_bit_cast(uint64_t, sum) & 3;
-    return (float)(((all - (sum - ones)) + rest) * 1.5707963267948966);
+    // positions past those that have an angle left get some turn, nothing larger
+    return __builtin_amdgcn_fmed3f((float)(((all - (sum - ones)) + rest) * 1.5707963267948966), -1.6f, 1.6f);
 }
 // cos and sin of the angle p f, times m.
 __device__ __forceinline__ void turn_cos_sin(double p, double f, float m, float* c, float* s) {

@@ -111,3 +111,21 @@ def test_weight_gradients_of_many_tokens():
     torch.cuda.synchronize()
     got = r["grad_wq"].double().cpu().numpy()
     assert np.abs(got - T * term).max() <= 32 * U * T * term, (got - T * term) / (T * term) / U
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_positions_without_an_angle(inter):
+    """Positions that float64 does not hold, such as a padded batch may leave, turn by some
+    angle: rows stay finite and keep their size to the polynomials' error at pi / 2."""
+    import torch
+    from test_regression_amd import mesa
+    say("case no angle", inter)
+    ends = torch.tensor([-(1 << 63), (1 << 63) - 1, 1 << 62, -(1 << 55) + 12345, (1 << 52) + 1, -(1 << 51) - 3], device="cuda")
+    x = torch.randn((1, 2, 6, 64), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    freqs, _ = mesa.mesa_rotary_frequencies(64)
+    y, _ = mesa.mesa_qk_rotate(x, None, freqs, ends, norm=False, interleaved=inter)
+    g = mesa.mesa_qk_rotate_backward(x, None, x, None, freqs, ends, norm=False, interleaved=inter)["grad_q"]
+    torch.cuda.synchronize()
+    for r in (y, g):
+        # cos^2 + sin^2 of the polynomials at 1.6 is off by 1.6^11 / 11! and 1.6^12 / 12! of about one: below 2^-16
+        assert bool(((r.norm(dim=-1) / x.norm(dim=-1) - 1).abs() <= 2.0 ** -16).all())
