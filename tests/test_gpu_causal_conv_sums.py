@@ -118,3 +118,20 @@ def test_slopes_of_far_values(z, dtype):
     for n in ("grad_w", "grad_bias"):
         got = r[n].double().cpu().numpy()
         assert np.abs(got - rg[n]).max() <= 24 * U * np.abs(rg[n]).max(), (n, (got - rg[n]).max() / np.abs(rg[n]).max() / U)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_slopes_at_the_ends_of_the_range(dtype):
+    """Slopes of values up to float32's largest are exactly 0 and 1."""
+    import torch
+    from test_regression_amd import mesa
+    say("case conv range", dtype)
+    x, xf = store(np.array([3.3e38, -3.3e38, 2.0e38, -2.0e38, 1e30, -1e30, 500.0, -500.0]).reshape(1, 1, 8), dtype)
+    one, _ = store(np.ones((1, 1, 8)), dtype)
+    r = mesa.mesa_causal_conv_backward(x.cuda(), torch.ones((1, 8), device="cuda"), one.cuda())
+    y = mesa.mesa_causal_conv(x.cuda(), torch.ones((1, 8), device="cuda"))
+    torch.cuda.synchronize()
+    on = xf > 0
+    assert np.array_equal(y.double().cpu().numpy(), np.where(on, xf, 0.0))
+    assert np.array_equal(r["grad_x"].double().cpu().numpy(), np.where(on, 1.0, 0.0))
+    assert np.array_equal(r["grad_w"].double().cpu().numpy()[0], np.where(on, xf, 0.0)[0, 0])
