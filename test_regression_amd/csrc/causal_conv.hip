@@ -13,7 +13,7 @@
 // the next ones on their way; eight channels a thread left half as many waves and no
 // registers to load ahead with.  Sums are float32; outputs are rounded once.  8 x 4096
 // tokens, 2304 channels, W 4, bfloat16: 64 us (4.7 TB/s), with eight channels 83 us;
-// the gradients 97 us (4.7 TB/s) and 4 us for the parts' sums, with eight channels 204
+// the gradients 97-100 us (4.6 TB/s) and 4 us for the parts' sums, with eight channels 204
 // and 10 us, with four and no loads ahead 129 us.
 #include <algorithm>
 
